@@ -49,13 +49,31 @@ extern "C" {
 #endif
 
 /* Element types.  PKV_FP8_E4M3 is the OCP 8-bit "e4m3fn" format (bias 7, no
- * infinities, S.1111.111 = NaN, largest finite 448); it is a KV storage type
- * only. */
+ * infinities, S.1111.111 = NaN, largest finite 448) and PKV_FP4_E2M1 the
+ * block-scaled 4-bit cache described next; both are KV storage types only.
+ *
+ * PKV_FP4_E2M1: every 16 consecutive dims of a row share one e4m3 scale, and
+ * every element is an e2m1 code (bit 3 the sign, magnitudes 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6), so an element takes 4.5 bits; its value is
+ *     code * scale * kv_scale      (kv_scale: one fp32 factor per cache).
+ * A (physical block, kv head) tile is one run of block_size * (head_dim / 2 +
+ * head_dim / 16) bytes, tiles in the order [num_blocks][num_kv_heads]:
+ *     codes   [head_dim / 32][block_size][16 bytes]: 32 dims of a row in 16
+ *             bytes, dim 2i of them in the low nibble of byte i, 2i + 1 in the
+ *             high one (the rows of 32 dims lie side by side, so eight of them
+ *             are one 128-byte line)
+ *     scales  [block_size][head_dim / 16], one byte each
+ * Writing x[16] (in fp32): scale = e4m3(max |x| / (6 * kv_scale)), then
+ * code = e2m1(x / (scale * kv_scale)); products and quotients are IEEE fp32,
+ * e4m3() and e2m1() round to nearest even and saturate (448, 6).  A scale that
+ * rounds to 0 gives 16 zero codes; a NaN among the 16 gives a NaN scale (all
+ * 16 read back as NaN); an infinity saturates. */
 typedef enum pkv_dtype {
     PKV_F32 = 0,
     PKV_F16 = 1,
     PKV_BF16 = 2,
-    PKV_FP8_E4M3 = 3
+    PKV_FP8_E4M3 = 3,
+    PKV_FP4_E2M1 = 4
 } pkv_dtype;
 
 typedef enum pkv_status {
@@ -74,6 +92,7 @@ typedef enum pkv_status {
 #define PKV_DEV_BAD_SLOT       0x4u  /* slot >= num_blocks * block_size: token skipped */
 #define PKV_DEV_BAD_PAIR       0x8u  /* copy pair id outside [0, num_blocks): pair skipped */
 #define PKV_DEV_WAIT_TIMEOUT   0x10u /* a pipeline wait exceeded its bound: kernel returned */
+#define PKV_DEV_BAD_POSITION   0x20u /* position outside [0, max_position): token skipped */
 
 /* Symbols of the C ABI are the only ones the library exports. */
 #if defined(__GNUC__)
@@ -108,7 +127,8 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num
  * in one pass with the running-max rescale of §7's pseudocode, splitting long
  * contexts into chunks whose partial states are merged by the same rescale).
  * A sequence with context_len 0 gets an all-zero output.
- * With kv_dtype PKV_FP8_E4M3 every K/V element is decode(code) * kv_scale.
+ * With kv_dtype PKV_FP8_E4M3 every K/V element is decode(code) * kv_scale, with
+ * PKV_FP4_E2M1 it is code * scale * kv_scale (the 4-bit format above).
  *
  *   query         [num_seqs][num_q_heads][head_dim], q_dtype, 16-byte aligned
  *   k_cache,
@@ -124,8 +144,9 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num
  *                 flagged PKV_DEV_BAD_CONTEXT.
  *   scale         logit scale (1/sqrt(head_dim) for standard attention)
  *   q_dtype       PKV_F32 / PKV_F16 / PKV_BF16; out has the same type
- *   kv_dtype      q_dtype or PKV_FP8_E4M3
- *   kv_scale      dequantisation scale for FP8 KV (> 0, finite; pass 1 otherwise)
+ *   kv_dtype      q_dtype, PKV_FP8_E4M3 or PKV_FP4_E2M1
+ *   kv_scale      dequantisation scale for FP8 and 4-bit KV (> 0, finite; pass 1
+ *                 otherwise)
  *   workspace     device buffer of >= pkv_decode_workspace_bytes(...) bytes,
  *                 256-byte aligned; calls sharing a workspace must be ordered
  *                 on one stream
@@ -154,7 +175,8 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  * once for the whole group, and each member's remaining tokens separately;
  * the two parts are merged per (sequence, query head).  Grouping applies when
  * q and K/V are 16-bit or FP8 with 16-bit q (head_dim 128 for FP8) and a kv
- * head has at most 8 query heads; otherwise this is the plain decode.  The
+ * head has at most 8 query heads; otherwise (a 4-bit cache among them) this is
+ * the plain decode.  The
  * rounding differs from the plain call's (the summation is split
  * differently), within the same tolerances.
  */
@@ -252,14 +274,17 @@ PKV_API pkv_status pkv_paged_tree_attention(
  *   k_cache[block][h][row][:] = key[t][h][:]   (same for value / v_cache).
  * Same element type: a bit copy.  kv_dtype PKV_FP8_E4M3: each element becomes
  * e4m3(x / kv_scale), the quotient taken in fp32 with IEEE rounding, then
- * rounded to nearest-even with saturation to +-448 (NaN stays NaN).
+ * rounded to nearest-even with saturation to +-448 (NaN stays NaN).  kv_dtype
+ * PKV_FP4_E2M1: every 16 elements of a row become one scale and 16 codes, as
+ * the format above says.
  *
  *   key, value    [num_tokens][num_kv_heads][head_dim], src_dtype, contiguous,
  *                 16-byte aligned
  *   slot_mapping  int64 [num_tokens]; negative = padding, skipped; slots at or
  *                 beyond num_blocks * block_size are skipped and flagged
  *                 PKV_DEV_BAD_SLOT.  Two tokens with the same slot race.
- *   src_dtype     PKV_F32 / PKV_F16 / PKV_BF16;  kv_dtype: src_dtype or FP8
+ *   src_dtype     PKV_F32 / PKV_F16 / PKV_BF16;  kv_dtype: src_dtype, FP8 or
+ *                 PKV_FP4_E2M1
  * One launch on `stream` (none when num_tokens == 0).
  */
 PKV_API pkv_status pkv_reshape_and_cache(const void* key, const void* value, void* k_cache,
@@ -267,6 +292,95 @@ PKV_API pkv_status pkv_reshape_and_cache(const void* key, const void* value, voi
                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                  pkv_dtype src_dtype, pkv_dtype kv_dtype, float kv_scale,
                                  pkv_stream_t stream);
+
+/*
+ * Reading the cache back: the inverse of pkv_reshape_and_cache for runs of a
+ * sequence's tokens, for paths that want contiguous rows (an export, a kernel
+ * that does not take the cache's type).
+ *
+ * Row r with row_start[s] <= r < row_start[s + 1] of the outputs is token
+ * token_start[s] + r - row_start[s] of sequence s, found through block_tables:
+ *   key_out[r][h][:] = the row's stored values (times kv_scale for FP8 and 4-bit
+ *   caches: code * scale exactly, then one fp32 product), rounded once to
+ *   out_dtype; value_out likewise.
+ * Rows outside every sequence's range (below row_start[0], or at and beyond
+ * row_start[num_seqs]) are left as they were.
+ *
+ *   block_tables  int32 [num_seqs][max_blocks_per_seq]
+ *   row_start     int32 [num_seqs + 1], non-decreasing, at most total_rows
+ *   token_start   int32 [num_seqs], or NULL for 0: first token of each run
+ *   out_dtype     kv_dtype for 16- and 32-bit caches (a bit copy); PKV_F32,
+ *                 PKV_F16 or PKV_BF16 for FP8 and 4-bit caches
+ *   key_out, value_out [total_rows][num_kv_heads][head_dim], 16-byte aligned
+ * A token outside the table's capacity is flagged PKV_DEV_BAD_CONTEXT, a block
+ * id outside the pool PKV_DEV_BAD_BLOCK_ID; their rows are left as they were.
+ * One launch on `stream` (none when num_seqs or total_rows is 0).
+ */
+PKV_API pkv_status pkv_gather_cache(const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* row_start,
+                                    const int32_t* token_start, int num_seqs, int total_rows,
+                                    int num_kv_heads, int head_dim, int block_size,
+                                    int num_blocks, int max_blocks_per_seq, pkv_dtype kv_dtype,
+                                    float kv_scale, pkv_dtype out_dtype, void* key_out,
+                                    void* value_out, pkv_stream_t stream);
+
+/*
+ * Per-head RMS norm of queries and keys with the rotary position embedding, in
+ * one pass (one launch) over both.  For every token t and head row x[head_dim]:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (y = x where weight is NULL)
+ *   the first rot_dim dims of y are rotated by the token's angles
+ *   a_0 .. a_(rot_dim/2 - 1): pair (y_i, y_j) becomes
+ *       (y_i cos a - y_j sin a, y_j cos a + y_i sin a),
+ *   pair p being dims (p, p + rot_dim / 2), or (2p, 2p + 1) with `interleaved`;
+ *   dims from rot_dim on stay y.
+ * All of it in fp32, rounded once to `dtype`.
+ *
+ *   query, key    [num_tokens][heads][head_dim], heads contiguous, tokens
+ *                 *_stride elements apart (views of a fused projection's rows)
+ *   q_weight,
+ *   k_weight      [head_dim] of weight_dtype, 16-byte aligned; either may be NULL
+ *                 (rotation without the norm)
+ *   weight_dtype  dtype or PKV_F32
+ *   cos_sin       float [max_position][rot_dim]: rot_dim / 2 cosines, then sines
+ *   positions     int64 [num_tokens]; one outside [0, max_position) is flagged
+ *                 PKV_DEV_BAD_POSITION and its token skipped (nothing written)
+ *   q_out, k_out  as query and key, with strides of their own; each may be its
+ *                 input (in place), and must not overlap it otherwise
+ * Supported: head_dim in {64, 128}; rot_dim a multiple of 16 up to head_dim;
+ * dtype PKV_F32 / PKV_F16 / PKV_BF16.  Pointers and strides in bytes are multiples
+ * of 16.  One launch on `stream` (none when num_tokens == 0).
+ */
+PKV_API pkv_status pkv_qk_norm_rope(const void* query, int64_t query_stride, const void* key,
+                                    int64_t key_stride, const void* q_weight,
+                                    const void* k_weight, pkv_dtype weight_dtype, float eps,
+                                    const float* cos_sin, int max_position, int rot_dim,
+                                    int interleaved, const int64_t* positions, int num_tokens,
+                                    int num_q_heads, int num_kv_heads, int head_dim,
+                                    pkv_dtype dtype, void* q_out, int64_t q_out_stride,
+                                    void* k_out, int64_t k_out_stride, pkv_stream_t stream);
+
+/*
+ * pkv_qk_norm_rope whose keys, with their token's values, go straight into the
+ * paged cache: the same bits as pkv_qk_norm_rope followed by
+ * pkv_reshape_and_cache of its k_out (the keys are rounded to `dtype` first),
+ * in one launch.
+ *
+ *   value         [num_tokens][num_kv_heads][head_dim], value_stride apart
+ *   k_cache, v_cache, slot_mapping, block_size, num_blocks, kv_dtype, kv_scale
+ *                 as in pkv_reshape_and_cache (kv_dtype: dtype, FP8 or 4-bit).
+ *                 A negative slot's key and value are not written (its query
+ *                 is); nor are those of a slot beyond the pool, which is flagged
+ *                 PKV_DEV_BAD_SLOT.  A token with a bad position writes nothing.
+ *   the other arguments as in pkv_qk_norm_rope.
+ */
+PKV_API pkv_status pkv_qk_norm_rope_and_cache(
+    const void* query, int64_t query_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, const void* q_weight, const void* k_weight,
+    pkv_dtype weight_dtype, float eps, const float* cos_sin, int max_position, int rot_dim,
+    int interleaved, const int64_t* positions, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, pkv_dtype dtype, void* q_out, int64_t q_out_stride,
+    void* k_cache, void* v_cache, const int64_t* slot_mapping, int block_size, int num_blocks,
+    pkv_dtype kv_dtype, float kv_scale, pkv_stream_t stream);
 
 /*
  * Batched copy-on-write ("...Mathematical Foundations" §5 step 4, §7 kernel 3):

@@ -8,6 +8,7 @@ cannot be loaded the calls raise.
 Functions carry the C names:
   pkv_decode_workspace_bytes, pkv_paged_decode_attention,
   pkv_paged_decode_attention_prefix, pkv_paged_decode_attention_noalloc, pkv_reshape_and_cache, pkv_copy_blocks,
+  pkv_gather_cache, pkv_qk_norm_rope, pkv_qk_norm_rope_and_cache,
   pkv_get_device_status, pkv_status_string, pkv_version,
 and the host block manager pkv_bm_* (wrapped by ``BlockManager``).
 """
@@ -23,14 +24,22 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpagedkv.so")
 
-PKV_F32, PKV_F16, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2, 3
+PKV_F32, PKV_F16, PKV_BF16, PKV_FP8_E4M3, PKV_FP4_E2M1 = range(5)
 (PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA,
  PKV_ERR_OUT_OF_BLOCKS) = range(6)
-DEV_BAD_BLOCK_ID, DEV_BAD_CONTEXT, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_WAIT_TIMEOUT = (
-    0x1, 0x2, 0x4, 0x8, 0x10)
+(DEV_BAD_BLOCK_ID, DEV_BAD_CONTEXT, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_WAIT_TIMEOUT,
+ DEV_BAD_POSITION) = (0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
 
 # ctypes signatures of every exported symbol
+_P, _I, _L, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _SIGNATURES = {
+    "pkv_gather_cache": (ctypes.c_int, [_P] * 5 + [_I] * 8 + [_F, _I, _P, _P, _P]),
+    "pkv_qk_norm_rope": (
+        ctypes.c_int, [_P, _L, _P, _L, _P, _P, _I, _F, _P, _I, _I, _I, _P] + [_I] * 5 +
+        [_P, _L, _P, _L, _P]),
+    "pkv_qk_norm_rope_and_cache": (
+        ctypes.c_int, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _F, _P, _I, _I, _I, _P] + [_I] * 5 +
+        [_P, _L, _P, _P, _P, _I, _I, _I, _F, _P]),
     "pkv_decode_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6 + [ctypes.c_int]),
     "pkv_paged_decode_attention": (
         ctypes.c_int,
@@ -136,7 +145,8 @@ def _check(fn: str, status: int) -> None:
 
 _TORCH_CODES = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16,
                 torch.float8_e4m3fn: PKV_FP8_E4M3, torch.uint8: PKV_FP8_E4M3}
-_NAME_CODES = {"f32": PKV_F32, "f16": PKV_F16, "bf16": PKV_BF16, "e4m3": PKV_FP8_E4M3}
+_NAME_CODES = {"f32": PKV_F32, "f16": PKV_F16, "bf16": PKV_BF16, "e4m3": PKV_FP8_E4M3,
+               "e2m1": PKV_FP4_E2M1}
 
 
 def dtype_code(x) -> int:
@@ -147,6 +157,24 @@ def dtype_code(x) -> int:
     if isinstance(x, str):
         return _NAME_CODES[x]
     return int(x)
+
+
+def fp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int) -> tuple:
+    """Shape of a uint8 tensor that holds a 4-bit (PKV_FP4_E2M1) cache.  Its last two
+    dims are one (block, kv head) tile, whose bytes include/pagedkv.h lays out."""
+    return (num_blocks, num_kv_heads, block_size, head_dim // 2 + head_dim // 16)
+
+
+_FP4_ROW_BYTES = {36: 64, 72: 128}   # bytes of a row of a 4-bit cache -> head_dim
+
+
+def _cache_type(cache: torch.Tensor) -> tuple:
+    """(element type code, head_dim) of a cache [NB, Hkv, B, row].  A uint8 cache is FP8
+    unless its rows are 36 or 72 bytes: then it holds 4-bit codes and their scales."""
+    row = cache.shape[3]
+    if cache.dtype == torch.uint8 and row in _FP4_ROW_BYTES:
+        return PKV_FP4_E2M1, _FP4_ROW_BYTES[row]
+    return _TORCH_CODES[cache.dtype], row
 
 
 def _stream_ptr(stream) -> int:
@@ -173,15 +201,18 @@ def _decode_args(query, k_cache, v_cache, block_tables, context_lens, max_contex
                  kv_scale, workspace, out, stream, prefix):
     """Checks and marshals a decode call: (C function name, argument tuple, out, workspace)."""
     S, Hq, d = query.shape
-    NB, Hkv, B, d2 = k_cache.shape
-    if d2 != d or tuple(v_cache.shape) != tuple(k_cache.shape):
+    NB, Hkv, B, _ = k_cache.shape
+    kc, d2 = _cache_type(k_cache)
+    if d2 != d or v_cache.shape != k_cache.shape:
         raise ValueError("cache shapes must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    if kc == PKV_FP4_E2M1 and v_cache.dtype != k_cache.dtype:
+        raise ValueError("a 4-bit v_cache must be uint8 as the k_cache")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise ValueError("block_tables and context_lens must be int32")
     for t, n in ((query, "query"), (k_cache, "k_cache"), (v_cache, "v_cache"),
                  (block_tables, "block_tables"), (context_lens, "context_lens")):
         _cuda(t, n)
-    qc, kc = dtype_code(query), dtype_code(k_cache)
+    qc = dtype_code(query)
     need = pkv_decode_workspace_bytes(S, Hq, Hkv, d, B, max_context_len, kc)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=query.device)
@@ -206,7 +237,7 @@ def pkv_paged_decode_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cac
     """out[s, h] = softmax(scale * q[s, h] . K_s^T) V_s over context_lens[s] tokens.
 
     query [S, Hq, d]; k_cache / v_cache [NB, Hkv, B, d] (float8_e4m3fn or uint8
-    for FP8); block_tables int32 [S, max_blocks]; context_lens int32 [S].
+    for FP8; uint8 of fp4_cache_shape for 4 bits); block_tables int32 [S, max_blocks]; context_lens int32 [S].
     ``workspace`` (uint8, >= pkv_decode_workspace_bytes) is allocated if None.
     ``prefix=True`` calls pkv_paged_decode_attention_prefix (shared prompts
     read once per group of sequences).
@@ -346,6 +377,10 @@ def pkv_paged_decode_attention_noalloc(query: torch.Tensor, k_cache: torch.Tenso
     """
     S, Hq, d = query.shape
     NB, Hkv, B, _ = k_cache.shape
+    kc, d2 = _cache_type(k_cache)
+    if kc == PKV_FP4_E2M1 and (d2 != d or v_cache.shape != k_cache.shape or
+                               v_cache.dtype != k_cache.dtype):
+        raise ValueError("4-bit caches must have fp4_cache_shape(...) of query's head_dim")
     for t, n in ((query, "query"), (k_cache, "k_cache"), (v_cache, "v_cache"),
                  (block_tables, "block_tables"), (context_lens, "context_lens")):
         _cuda(t, n)
@@ -355,7 +390,7 @@ def pkv_paged_decode_attention_noalloc(query: torch.Tensor, k_cache: torch.Tenso
     st = load().pkv_paged_decode_attention_noalloc(
         query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), S, Hq, Hkv, d, B, NB, block_tables.shape[1],
-        int(max_context_len), float(scale), dtype_code(query), dtype_code(k_cache),
+        int(max_context_len), float(scale), dtype_code(query), kc,
         float(kv_scale), out.data_ptr(), _stream_ptr(stream))
     _check("pkv_paged_decode_attention_noalloc", st)
     return out
@@ -363,7 +398,11 @@ def pkv_paged_decode_attention_noalloc(query: torch.Tensor, k_cache: torch.Tenso
 
 def _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream):
     T, Hkv, d = key.shape
-    NB, Hkv2, B, d2 = k_cache.shape
+    NB, Hkv2, B, _ = k_cache.shape
+    kc, d2 = _cache_type(k_cache)
+    if kc == PKV_FP4_E2M1 and (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or
+                               value.dtype != key.dtype):
+        raise ValueError("key and value, and the two 4-bit caches, must have one shape and type")
     if (Hkv2, d2) != (Hkv, d) or tuple(value.shape) != tuple(key.shape):
         raise ValueError("key/value [T, Hkv, d] do not match the cache [NB, Hkv, B, d]")
     if slot_mapping.dtype != torch.int64:
@@ -372,14 +411,15 @@ def _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream):
                  (slot_mapping, "slot_mapping")):
         _cuda(t, n)
     return (key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            slot_mapping.data_ptr(), T, Hkv, d, B, NB, dtype_code(key), dtype_code(k_cache),
+            slot_mapping.data_ptr(), T, Hkv, d, B, NB, dtype_code(key), kc,
             float(kv_scale), _stream_ptr(stream))
 
 
 def pkv_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
                           v_cache: torch.Tensor, slot_mapping: torch.Tensor,
                           kv_scale: float = 1.0, stream=None) -> None:
-    """k_cache[slot // B, h, slot % B] = key[t, h] (e4m3(x / kv_scale) for FP8 caches)."""
+    """k_cache[slot // B, h, slot % B] = key[t, h] (e4m3(x / kv_scale) for FP8 caches; codes
+    and scales for 4-bit caches, uint8 of fp4_cache_shape)."""
     args = _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream)
     _check("pkv_reshape_and_cache", load().pkv_reshape_and_cache(*args))
 
@@ -390,6 +430,154 @@ def prepare_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, kv_sca
     return PreparedCall("pkv_reshape_and_cache",
                         _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale,
                                       stream), (key, value, k_cache, v_cache, slot_mapping))
+
+
+def pkv_gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     row_start: torch.Tensor, total_rows: int, out_dtype: torch.dtype,
+                     kv_scale: float = 1.0, token_start: torch.Tensor | None = None,
+                     key_out: torch.Tensor | None = None, value_out: torch.Tensor | None = None,
+                     stream=None) -> tuple:
+    """Read cached tokens back: (key, value) [total_rows, Hkv, d] of ``out_dtype``.
+
+    Rows row_start[s] .. row_start[s + 1] - 1 (int32 [S + 1]) are the tokens of sequence s
+    from token_start[s] (int32 [S]; 0 if None) on, found through block_tables int32
+    [S, max_blocks].  16- and 32-bit caches are copied (``out_dtype`` is theirs); FP8 and
+    4-bit ones become values in any of float32, float16 and bfloat16.  Rows outside every
+    sequence's range are left as they were (in outputs allocated here: uninitialised).
+    """
+    NB, Hkv, B, _ = k_cache.shape
+    kc, d = _cache_type(k_cache)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and type")
+    if block_tables.dtype != torch.int32 or row_start.dtype != torch.int32 or \
+            (token_start is not None and token_start.dtype != torch.int32):
+        raise ValueError("block_tables, row_start and token_start must be int32")
+    S, max_blocks = block_tables.shape
+    if row_start.shape != (S + 1,) or (token_start is not None and token_start.shape != (S,)):
+        raise ValueError("row_start must have num_seqs + 1 entries, token_start num_seqs")
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_tables, "block_tables"),
+                 (row_start, "row_start")):
+        _cuda(t, n)
+    if token_start is not None:
+        _cuda(token_start, "token_start")
+    shape = (int(total_rows), Hkv, d)
+    if key_out is None:
+        key_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    if value_out is None:
+        value_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    for t, n in ((key_out, "key_out"), (value_out, "value_out")):
+        _cuda(t, n)
+        if t.shape != shape or t.dtype != out_dtype:
+            raise ValueError(f"{n} must be {list(shape)} of {out_dtype}")
+    st = load().pkv_gather_cache(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), row_start.data_ptr(),
+        None if token_start is None else token_start.data_ptr(), S, shape[0], Hkv, d, B, NB,
+        max_blocks, kc, float(kv_scale), _TORCH_CODES[out_dtype], key_out.data_ptr(),
+        value_out.data_ptr(), _stream_ptr(stream))
+    _check("pkv_gather_cache", st)
+    return key_out, value_out
+
+
+# ---------------------------------------------------------- norm + rotary --
+
+def _head_rows(t: torch.Tensor, name: str) -> int:
+    """The token stride of a CUDA tensor [T, heads, d] whose tokens' heads are contiguous."""
+    _, h, d = t.shape
+    s = t.stride()
+    if not t.is_cuda or (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name} must be a CUDA tensor [T, heads, d], heads contiguous")
+    return s[0] if t.shape[0] > 1 else h * d
+
+
+def _norm_rope_args(query, key, cos_sin, positions, q_weight, k_weight, eps, interleaved, q_out,
+                    value=None):
+    """Checks shared by the two entry points: (arguments up to dtype, in two parts around
+    value's, query's outputs)."""
+    T, Hq, d = query.shape
+    Hkv = key.shape[1]
+    if key.shape != (T, Hkv, d) or key.dtype != query.dtype:
+        raise ValueError("query [T, Hq, d] and key [T, Hkv, d] must agree in T, d and type")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+    if positions.dtype != torch.int64 or positions.shape != (T,):
+        raise ValueError("positions must be int64 [T]")
+    _cuda(cos_sin, "cos_sin")
+    _cuda(positions, "positions")
+    wc = PKV_F32
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _cuda(w, n)
+            if w.shape != (d,):
+                raise ValueError(f"{n} must be [head_dim]")
+            wc = _TORCH_CODES[w.dtype]
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one type")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=query.dtype, device=query.device)
+    elif q_out.shape != query.shape or q_out.dtype != query.dtype:
+        raise ValueError("q_out must have query's shape and type")
+    head = [query.data_ptr(), _head_rows(query, "query"), key.data_ptr(), _head_rows(key, "key")]
+    if value is not None:
+        if value.shape != key.shape or value.dtype != key.dtype:
+            raise ValueError("value must have key's shape and type")
+        head += [value.data_ptr(), _head_rows(value, "value")]
+    head += [None if q_weight is None else q_weight.data_ptr(),
+             None if k_weight is None else k_weight.data_ptr(), wc, float(eps),
+             cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+             positions.data_ptr(), T, Hq, Hkv, d, _TORCH_CODES[query.dtype], q_out.data_ptr(),
+             _head_rows(q_out, "q_out")]
+    return head, q_out
+
+
+def pkv_qk_norm_rope(query: torch.Tensor, key: torch.Tensor, cos_sin: torch.Tensor,
+                     positions: torch.Tensor, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out: torch.Tensor | None = None,
+                     k_out: torch.Tensor | None = None, stream=None) -> tuple:
+    """Per-head RMS norm (where a weight is given) and rotary embedding: (q_out, k_out).
+
+    query [T, Hq, d] and key [T, Hkv, d] may be views of one projection's rows (heads
+    contiguous, any token stride that is a multiple of 16 bytes); weights [d] of their type
+    or float32; cos_sin float32 [max_position, rot_dim] holds each position's cosines, then
+    sines; positions int64 [T].  ``interleaved`` rotates dims (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2).  q_out / k_out may be query / key themselves (in place).
+    """
+    head, q_out = _norm_rope_args(query, key, cos_sin, positions, q_weight, k_weight, eps,
+                                  interleaved, q_out)
+    if k_out is None:
+        k_out = torch.empty(key.shape, dtype=key.dtype, device=key.device)
+    elif k_out.shape != key.shape or k_out.dtype != key.dtype:
+        raise ValueError("k_out must have key's shape and type")
+    _check("pkv_qk_norm_rope", load().pkv_qk_norm_rope(
+        *head, k_out.data_ptr(), _head_rows(k_out, "k_out"), _stream_ptr(stream)))
+    return q_out, k_out
+
+
+def pkv_qk_norm_rope_and_cache(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                               cos_sin: torch.Tensor, positions: torch.Tensor,
+                               k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               slot_mapping: torch.Tensor, q_weight: torch.Tensor | None = None,
+                               k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                               interleaved: bool = False, kv_scale: float = 1.0,
+                               q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pkv_qk_norm_rope whose keys, with ``value`` [T, Hkv, d], go into the paged cache at
+    slot_mapping (int64 [T], negative: not written); returns q_out.  The cache, of any type,
+    holds the same bits as after pkv_qk_norm_rope and pkv_reshape_and_cache of its keys."""
+    NB, Hkv, B, _ = k_cache.shape
+    kc, d = _cache_type(k_cache)
+    if (Hkv, d) != tuple(key.shape[1:]) or v_cache.shape != k_cache.shape or \
+            v_cache.dtype != k_cache.dtype:
+        raise ValueError("key [T, Hkv, d] does not match the caches [NB, Hkv, B, d]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (key.shape[0],):
+        raise ValueError("slot_mapping must be int64 [T]")
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (slot_mapping, "slot_mapping")):
+        _cuda(t, n)
+    head, q_out = _norm_rope_args(query, key, cos_sin, positions, q_weight, k_weight, eps,
+                                  interleaved, q_out, value)
+    _check("pkv_qk_norm_rope_and_cache", load().pkv_qk_norm_rope_and_cache(
+        *head, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), B, NB, kc,
+        float(kv_scale), _stream_ptr(stream)))
+    return q_out
 
 
 def validate_pairs(pairs: np.ndarray, num_blocks: int) -> None:
@@ -405,7 +593,8 @@ def validate_pairs(pairs: np.ndarray, num_blocks: int) -> None:
 
 
 def _copy_args(k_cache, v_cache, src_dst_pairs, stream):
-    NB, Hkv, B, d = k_cache.shape
+    NB, Hkv, B, _ = k_cache.shape
+    kc, d = _cache_type(k_cache)
     _cuda(k_cache, "k_cache")
     _cuda(v_cache, "v_cache")
     if isinstance(src_dst_pairs, torch.Tensor) and src_dst_pairs.is_cuda:
@@ -418,7 +607,7 @@ def _copy_args(k_cache, v_cache, src_dst_pairs, stream):
         raise ValueError("src_dst_pairs must be int32")
     n = pairs.numel() // 2
     return (k_cache.data_ptr(), v_cache.data_ptr(), pairs.data_ptr() if n else None, n, Hkv, d,
-            B, NB, dtype_code(k_cache), _stream_ptr(stream)), pairs
+            B, NB, kc, _stream_ptr(stream)), pairs
 
 
 def pkv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs,
@@ -447,9 +636,10 @@ def pkv_swap_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tenso
     (``tensor.pin_memory()``).  Host pairs are validated and staged in a pinned
     buffer; a CUDA or pinned tensor is used as is.
     """
-    NBs, Hkv, B, d = src_k.shape
+    NBs, Hkv, B, row = src_k.shape
+    kc, d = _cache_type(src_k)
     NBd = dst_k.shape[0]
-    if tuple(dst_k.shape[1:]) != (Hkv, B, d) or src_v.shape != src_k.shape or \
+    if tuple(dst_k.shape[1:]) != (Hkv, B, row) or src_v.shape != src_k.shape or \
             dst_v.shape != dst_k.shape:
         raise ValueError("pools must be [blocks, kv heads, B, d] with matching rows")
     for t, n in ((src_k, "src_k"), (src_v, "src_v"), (dst_k, "dst_k"), (dst_v, "dst_v")):
@@ -469,7 +659,7 @@ def pkv_swap_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tenso
     n = pairs.numel() // 2
     st = load().pkv_swap_blocks(src_k.data_ptr(), src_v.data_ptr(), NBs, dst_k.data_ptr(),
                                 dst_v.data_ptr(), NBd, pairs.data_ptr() if n else None, n, Hkv,
-                                d, B, dtype_code(src_k), _stream_ptr(stream))
+                                d, B, kc, _stream_ptr(stream))
     _check("pkv_swap_blocks", st)
     if not (isinstance(src_dst_pairs, torch.Tensor)) and n:
         # the launch reads the staged pairs asynchronously: keep them alive until it ran

@@ -6,8 +6,11 @@
 #include <math.h>
 
 #include "cache_ops.cuh"
+#include "cache_row.cuh"
+#include "decode_fp4.cuh"
 #include "decode_launch.cuh"
 #include "mq_attention.cuh"
+#include "norm_rope.cuh"
 
 // Per-device status word written by the kernels (bit-or of PKV_DEV_*).
 __device__ unsigned int g_pkv_status = 0u;
@@ -43,15 +46,11 @@ cudaError_t device_info(DeviceInfo** out) {
     return cudaSuccess;
 }
 
-int dtype_bytes(pkv_dtype t) {
-    switch (t) {
-    case PKV_F32: return 4;
-    case PKV_F16: return 2;
-    case PKV_BF16: return 2;
-    case PKV_FP8_E4M3: return 1;
-    default: return 0;
-    }
-}
+// Whether t is one of the header's element types.
+bool known(pkv_dtype t) { return cache_row_bytes(t, 64) != 0; }
+
+// Storage types that any query type reads.
+bool quantised(pkv_dtype t) { return t == PKV_FP8_E4M3 || t == PKV_FP4_E2M1; }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -120,7 +119,7 @@ extern "C" {
 
 size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                   int block_size, int max_context_len, pkv_dtype kv_dtype) {
-    if (dtype_bytes(kv_dtype) == 0) return 0;
+    if (!known(kv_dtype)) return 0;
     Plan p;
     if (make_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                   &p) != PKV_OK)
@@ -142,9 +141,9 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     if (num_seqs < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
         return PKV_ERR_INVALID_ARG;
     if (q_dtype != PKV_F32 && q_dtype != PKV_F16 && q_dtype != PKV_BF16)
-        return dtype_bytes(q_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
-    if (kv_dtype != q_dtype && kv_dtype != PKV_FP8_E4M3)
-        return dtype_bytes(kv_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
+        return known(q_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
+    if (kv_dtype != q_dtype && !quantised(kv_dtype))
+        return known(kv_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
     if (!isfinite(scale) || !isfinite(kv_scale) || !(kv_scale > 0.f)) return PKV_ERR_INVALID_ARG;
     Plan plan;
     pkv_status st = make_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -166,6 +165,28 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     if (err != cudaSuccess) return PKV_ERR_CUDA;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (kv_dtype == PKV_FP4_E2M1) {
+        DecodeFp4Params f{};
+        f.q = query;
+        f.k_cache = k_cache;
+        f.v_cache = v_cache;
+        f.block_tables = block_tables;
+        f.context_lens = context_lens;
+        f.out = out;
+        f.status = dev->status;
+        f.num_seqs = num_seqs;
+        f.num_q_heads = num_q_heads;
+        f.num_kv_heads = num_kv_heads;
+        f.group = plan.group;
+        f.head_dim = head_dim;
+        f.block_size = block_size;
+        f.num_blocks = num_blocks;
+        f.max_blocks = max_blocks_per_seq;
+        f.max_context_len = max_context_len;
+        f.qk_scale_log2 = scale * 1.4426950408889634f * kv_scale;
+        f.out_scale = kv_scale;
+        return cuda_status(launch_decode_fp4(f, q_dtype, reinterpret_cast<cudaStream_t>(stream)));
+    }
     DecodeParams p{};
     p.q = query;
     p.k_cache = k_cache;
@@ -265,12 +286,12 @@ pkv_status pkv_reshape_and_cache(const void* key, const void* value, void* k_cac
                                  pkv_stream_t stream) {
     if (num_tokens < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
     if (src_dtype != PKV_F32 && src_dtype != PKV_F16 && src_dtype != PKV_BF16)
-        return dtype_bytes(src_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
-    if (kv_dtype != src_dtype && kv_dtype != PKV_FP8_E4M3)
-        return dtype_bytes(kv_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
+        return known(src_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
+    if (kv_dtype != src_dtype && !quantised(kv_dtype))
+        return known(kv_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
-    const bool quant = kv_dtype == PKV_FP8_E4M3;
+    const bool quant = quantised(kv_dtype);
     if (quant && (!isfinite(kv_scale) || !(kv_scale > 0.f))) return PKV_ERR_INVALID_ARG;
     if (num_tokens == 0) return PKV_OK;
     if (!key || !value || !k_cache || !v_cache || !slot_mapping) return PKV_ERR_INVALID_ARG;
@@ -281,15 +302,172 @@ pkv_status pkv_reshape_and_cache(const void* key, const void* value, void* k_cac
     if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     ReshapeParams p{key, value, k_cache, v_cache, slot_mapping, dev->status, num_tokens,
                     num_kv_heads, head_dim, block_size, num_blocks, kv_scale};
+    if (kv_dtype == PKV_FP4_E2M1)
+        return cuda_status(launch_reshape_and_cache_fp4(p, src_dtype, dev->num_sms,
+                                                        reinterpret_cast<cudaStream_t>(stream)));
     return cuda_status(launch_reshape_and_cache(p, src_dtype, quant, dev->num_sms,
                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_gather_cache(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                            const int32_t* row_start, const int32_t* token_start, int num_seqs,
+                            int total_rows, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, int max_blocks_per_seq, pkv_dtype kv_dtype,
+                            float kv_scale, pkv_dtype out_dtype, void* key_out, void* value_out,
+                            pkv_stream_t stream) {
+    if (num_seqs < 0 || total_rows < 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (!known(kv_dtype) || !known(out_dtype)) return PKV_ERR_INVALID_ARG;
+    if (quantised(out_dtype) || (!quantised(kv_dtype) && out_dtype != kv_dtype))
+        return PKV_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
+    if (!isfinite(kv_scale) || !(kv_scale > 0.f)) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_rows == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !row_start || !key_out || !value_out)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
+        !aligned(row_start, 4) || !aligned(token_start, 4) || !aligned(key_out, 16) ||
+        !aligned(value_out, 16))
+        return PKV_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    GatherParams p{k_cache, v_cache, block_tables, row_start, token_start, key_out, value_out,
+                   dev->status, num_seqs, total_rows, num_kv_heads, head_dim, block_size,
+                   num_blocks, max_blocks_per_seq, kv_scale};
+    return cuda_status(launch_gather_cache(p, kv_dtype, out_dtype,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the two norm + rotary entry points; fills the common fields of p.
+pkv_status norm_rope_args(NormRopeParams* p, const void* query, int64_t query_stride,
+                          const void* key, int64_t key_stride, const void* q_weight,
+                          const void* k_weight, pkv_dtype weight_dtype, float eps,
+                          const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                          const int64_t* positions, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, pkv_dtype dtype, void* q_out,
+                          int64_t q_out_stride) {
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_position <= 0 ||
+        rot_dim <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (!known(dtype) || !known(weight_dtype)) return PKV_ERR_INVALID_ARG;
+    if (quantised(dtype) || (weight_dtype != dtype && weight_dtype != PKV_F32))
+        return PKV_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (rot_dim % 16 != 0 || rot_dim > head_dim) return PKV_ERR_UNSUPPORTED;
+    if (!isfinite(eps) || eps < 0.f) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    const int64_t unit = 16 / cache_row_bytes(dtype, 1);       // elements of 16 bytes
+    const int64_t qrow = (int64_t)num_q_heads * head_dim, krow = (int64_t)num_kv_heads * head_dim;
+    if (query_stride < qrow || key_stride < krow || q_out_stride < qrow ||
+        query_stride % unit || key_stride % unit || q_out_stride % unit)
+        return PKV_ERR_INVALID_ARG;
+    if (!query || !key || !cos_sin || !positions || !q_out) return PKV_ERR_INVALID_ARG;
+    if (!aligned(query, 16) || !aligned(key, 16) || !aligned(q_weight, 16) ||
+        !aligned(k_weight, 16) || !aligned(cos_sin, 16) || !aligned(positions, 8) ||
+        !aligned(q_out, 16))
+        return PKV_ERR_INVALID_ARG;
+    p->q = query;
+    p->k = key;
+    p->q_weight = q_weight;
+    p->k_weight = k_weight;
+    p->cos_sin = cos_sin;
+    p->positions = positions;
+    p->q_out = q_out;
+    p->q_stride = query_stride;
+    p->k_stride = key_stride;
+    p->q_out_stride = q_out_stride;
+    p->num_tokens = num_tokens;
+    p->num_q_heads = num_q_heads;
+    p->num_kv_heads = num_kv_heads;
+    p->head_dim = head_dim;
+    p->max_position = max_position;
+    p->rot_dim = rot_dim;
+    p->interleaved = interleaved;
+    p->weight_f32 = weight_dtype == PKV_F32;
+    p->eps = eps;
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_qk_norm_rope(const void* query, int64_t query_stride, const void* key,
+                            int64_t key_stride, const void* q_weight, const void* k_weight,
+                            pkv_dtype weight_dtype, float eps, const float* cos_sin,
+                            int max_position, int rot_dim, int interleaved,
+                            const int64_t* positions, int num_tokens, int num_q_heads,
+                            int num_kv_heads, int head_dim, pkv_dtype dtype, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                            pkv_stream_t stream) {
+    NormRopeParams p{};
+    const pkv_status st = norm_rope_args(&p, query, query_stride, key, key_stride, q_weight,
+                                         k_weight, weight_dtype, eps, cos_sin, max_position,
+                                         rot_dim, interleaved, positions, num_tokens, num_q_heads,
+                                         num_kv_heads, head_dim, dtype, q_out, q_out_stride);
+    if (st != PKV_OK || num_tokens == 0) return st;
+    if (!k_out || !aligned(k_out, 16) || k_out_stride < (int64_t)num_kv_heads * head_dim ||
+        k_out_stride % (16 / cache_row_bytes(dtype, 1)))
+        return PKV_ERR_INVALID_ARG;
+    p.k_out = k_out;
+    p.k_out_stride = k_out_stride;
+    DeviceInfo* dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    p.status = dev->status;
+    return cuda_status(launch_qk_norm_rope(p, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_qk_norm_rope_and_cache(
+    const void* query, int64_t query_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, const void* q_weight, const void* k_weight,
+    pkv_dtype weight_dtype, float eps, const float* cos_sin, int max_position, int rot_dim,
+    int interleaved, const int64_t* positions, int num_tokens, int num_q_heads, int num_kv_heads,
+    int head_dim, pkv_dtype dtype, void* q_out, int64_t q_out_stride, void* k_cache,
+    void* v_cache, const int64_t* slot_mapping, int block_size, int num_blocks,
+    pkv_dtype kv_dtype, float kv_scale, pkv_stream_t stream) {
+    NormRopeParams p{};
+    if (num_blocks <= 0 || !known(kv_dtype)) return PKV_ERR_INVALID_ARG;
+    const pkv_status st = norm_rope_args(&p, query, query_stride, key, key_stride, q_weight,
+                                         k_weight, weight_dtype, eps, cos_sin, max_position,
+                                         rot_dim, interleaved, positions, num_tokens, num_q_heads,
+                                         num_kv_heads, head_dim, dtype, q_out, q_out_stride);
+    if (st != PKV_OK) return st;
+    if (kv_dtype != dtype && !quantised(kv_dtype)) return PKV_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
+    if (quantised(kv_dtype) && (!isfinite(kv_scale) || !(kv_scale > 0.f)))
+        return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    if (!value || !k_cache || !v_cache || !slot_mapping) return PKV_ERR_INVALID_ARG;
+    if (!aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(slot_mapping, 8) || value_stride < (int64_t)num_kv_heads * head_dim ||
+        value_stride % (16 / cache_row_bytes(dtype, 1)))
+        return PKV_ERR_INVALID_ARG;
+    p.v = value;
+    p.v_stride = value_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slot_mapping = slot_mapping;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.kv_scale = kv_scale;
+    DeviceInfo* dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    p.status = dev->status;
+    return cuda_status(launch_qk_norm_rope_and_cache(p, dtype, kv_dtype,
+                                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src_dst_pairs,
                            int num_pairs, int num_kv_heads, int head_dim, int block_size,
                            int num_blocks, pkv_dtype kv_dtype, pkv_stream_t stream) {
     if (num_pairs < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
-    if (dtype_bytes(kv_dtype) == 0) return PKV_ERR_INVALID_ARG;
+    if (!known(kv_dtype)) return PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
@@ -300,7 +478,7 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src_dst_
     DeviceInfo* dev = nullptr;
     if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     CopyParams p{k_cache, v_cache, k_cache, v_cache, src_dst_pairs, dev->status,
-                 (int64_t)num_kv_heads * block_size * head_dim * dtype_bytes(kv_dtype),
+                 (int64_t)num_kv_heads * block_size * cache_row_bytes(kv_dtype, head_dim),
                  num_blocks, num_blocks};
     return cuda_status(launch_copy_blocks(p, num_pairs, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -312,7 +490,7 @@ pkv_status pkv_swap_blocks(const void* src_k, const void* src_v, int src_num_blo
                            pkv_stream_t stream) {
     if (num_pairs < 0 || num_kv_heads <= 0 || src_num_blocks <= 0 || dst_num_blocks <= 0)
         return PKV_ERR_INVALID_ARG;
-    if (dtype_bytes(kv_dtype) == 0) return PKV_ERR_INVALID_ARG;
+    if (!known(kv_dtype)) return PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
     if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
@@ -343,7 +521,7 @@ pkv_status pkv_swap_blocks(const void* src_k, const void* src_v, int src_num_blo
     }
     CopyParams p{mapped[0], mapped[1], mapped[2], mapped[3],
                  static_cast<const int32_t*>(mapped[4]), dev->status,
-                 (int64_t)num_kv_heads * block_size * head_dim * dtype_bytes(kv_dtype),
+                 (int64_t)num_kv_heads * block_size * cache_row_bytes(kv_dtype, head_dim),
                  src_num_blocks, dst_num_blocks};
     return cuda_status(launch_copy_blocks(p, num_pairs, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -403,7 +581,7 @@ pkv_status multi_query_attention(
         num_q_heads % num_kv_heads != 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 ||
         max_context_len < 0)
         return PKV_ERR_INVALID_ARG;
-    if (!dtype_bytes(q_dtype) || !dtype_bytes(kv_dtype)) return PKV_ERR_INVALID_ARG;
+    if (!known(q_dtype) || !known(kv_dtype)) return PKV_ERR_INVALID_ARG;
     if (!isfinite(scale) || !isfinite(kv_scale) || !(kv_scale > 0.f)) return PKV_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads;
     if ((q_dtype != PKV_F16 && q_dtype != PKV_BF16) || kv_dtype != q_dtype || head_dim != 128 ||

@@ -12,16 +12,9 @@
 // All are pure data movement: one thread moves one 16-byte chunk per
 // iteration with vector loads/stores, in a grid-stride loop.
 #include "cache_ops.cuh"
+#include "cache_row.cuh"
 
 namespace pkv {
-
-// Two fp32 values -> two e4m3 codes (round to nearest even, saturate to
-// +-448, NaN -> NaN), packed little-endian: `lo` lands in the lower byte.
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 template <typename ST>
 __device__ __forceinline__ void load16_as_float(const uint8_t* src, float* f);
@@ -100,6 +93,44 @@ __global__ void __launch_bounds__(256) reshape_and_cache_kernel(ReshapeParams p)
     }
 }
 
+// Into the 4-bit cache: one lane = eight dims of one (token, kv head) row, K and V; a pair
+// of lanes shares a 16-dim group's scale.  Whole warps run each iteration together (the
+// group's maximum is exchanged by a shuffle).
+template <typename ST>
+__global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(ReshapeParams p) {
+    pdl_launch_dependents();   // the decode launched next may start its launch now
+    const int lanes = p.head_dim / 8;                  // lanes of a row
+    const int64_t total = (int64_t)p.num_tokens * p.num_kv_heads * lanes;
+    const int64_t pool_slots = (int64_t)p.num_blocks * p.block_size;
+    const int64_t tile_bytes = (int64_t)p.block_size * (p.head_dim / 2 + p.head_dim / 16);
+    const int lane = threadIdx.x & 31;
+    for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + (threadIdx.x - lane); i0 < total;
+         i0 += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t idx = i0 + lane;
+        const bool in = idx < total;
+        const int j = (int)(idx % lanes);
+        const int64_t th = idx / lanes;
+        const int h = (int)(th % p.num_kv_heads);
+        const int64_t t = th / p.num_kv_heads;
+        const int64_t slot = in ? p.slot_mapping[t] : -1;
+        if (slot >= pool_slots && j == 0 && h == 0) set_status(p.status, PKV_DEV_BAD_SLOT);
+        const bool live = slot >= 0 && slot < pool_slots;
+        float k[8] = {0.f}, v[8] = {0.f};
+        if (live) {
+            const int64_t src = (th * p.head_dim + 8 * j) * ST::bytes;
+            load8<ST>(static_cast<const uint8_t*>(p.key) + src, k);
+            load8<ST>(static_cast<const uint8_t*>(p.value) + src, v);
+        }
+        const int64_t blk = live ? slot / p.block_size : 0;
+        const int row = live ? (int)(slot % p.block_size) : 0;
+        const int64_t tile = (blk * p.num_kv_heads + h) * tile_bytes;
+        CacheRow<E2M1>::store(static_cast<uint8_t*>(p.k_cache) + tile, p.block_size, p.head_dim,
+                              row, j, k, p.kv_scale, live);
+        CacheRow<E2M1>::store(static_cast<uint8_t*>(p.v_cache) + tile, p.block_size, p.head_dim,
+                              row, j, v, p.kv_scale, live);
+    }
+}
+
 // grid = (pairs, slices of a block, 2 caches); one 16-byte chunk per thread-iteration.
 // Block pairs[i][0] of the source pool -> block pairs[i][1] of the destination.
 __global__ void __launch_bounds__(256) copy_blocks_kernel(CopyParams p) {
@@ -143,6 +174,20 @@ cudaError_t launch_reshape_and_cache(const ReshapeParams& p, pkv_dtype src, bool
         break;
     default:
         return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src, int num_sms,
+                                         cudaStream_t stream) {
+    const int64_t total = (int64_t)p.num_tokens * p.num_kv_heads * (p.head_dim / 8);
+    const int64_t want = (total + 255) / 256, cap = (int64_t)num_sms * 8;
+    const int grid = (int)(want < cap ? want : cap);
+    switch (src) {
+    case PKV_F32: reshape_and_cache_fp4_kernel<F32><<<grid, 256, 0, stream>>>(p); break;
+    case PKV_F16: reshape_and_cache_fp4_kernel<F16><<<grid, 256, 0, stream>>>(p); break;
+    case PKV_BF16: reshape_and_cache_fp4_kernel<BF16><<<grid, 256, 0, stream>>>(p); break;
+    default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
 }

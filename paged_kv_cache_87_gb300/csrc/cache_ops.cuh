@@ -23,13 +23,32 @@ struct CopyParams {
     void* dst_v;
     const int32_t* pairs;
     unsigned* status;
-    int64_t block_bytes;   // num_kv_heads * block_size * head_dim * element bytes
+    int64_t block_bytes;   // num_kv_heads * block_size * bytes of a row
     int src_num_blocks, dst_num_blocks;
 };
 
 cudaError_t launch_reshape_and_cache(const ReshapeParams& p, pkv_dtype src, bool quant,
                                      int num_sms, cudaStream_t stream);
+cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src, int num_sms,
+                                         cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyParams& p, int num_pairs, cudaStream_t stream);
+
+// Reading the cache back into contiguous rows (gather.cu).
+struct GatherParams {
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* row_start;
+    const int32_t* token_start;   // may be null: 0
+    void* key_out;
+    void* value_out;
+    unsigned* status;
+    int num_seqs, total_rows, num_kv_heads, head_dim, block_size, num_blocks, max_blocks;
+    float kv_scale;
+};
+
+cudaError_t launch_gather_cache(const GatherParams& p, pkv_dtype kv, pkv_dtype out,
+                                cudaStream_t stream);
 
 // A kernel whose pipeline wait can never complete: it flags PKV_DEV_WAIT_TIMEOUT in
 // `status` once the wait's bound has passed, and returns.

@@ -36,6 +36,7 @@
 
 #include <type_traits>
 
+#include "cache_row.cuh"
 #include "decode.cuh"
 
 namespace pkv {
@@ -140,13 +141,6 @@ struct MmaCfg {
     static_assert(!FP8 || HD == 128, "FP8 rows must be 128 bytes");
     static_assert(std::is_same<QT, F16>::value || std::is_same<QT, BF16>::value, "q type");
 };
-
-// Two e4m3 codes (low byte first) -> f16x2 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
-    __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two_codes),
-                                               __NV_E4M3);
-    return *reinterpret_cast<uint32_t*>(&h);
-}
 
 // Two 16-bit q values (low first) as the mma operand type MT.
 template <typename QT, typename MT>
