@@ -64,6 +64,11 @@ struct Plan {
         off_units, off_expect, off_pm, off_pl, off_pacc, total;
 };
 
+struct Fp4Plan {
+    int group, nsub, workers;
+    size_t off_ml, total;
+};
+
 // Chunk length: at least 512 tokens, a multiple of 64 (every stage size and
 // block size divides it), long enough that a sequence has at most
 // kMaxMergeChunks chunks, and at most kMaxItemBlocks blocks.
@@ -108,6 +113,25 @@ pkv_status make_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Plan* p
     return PKV_OK;
 }
 
+// Workspace of the decode over a 4-bit cache: two partial states (m, l, acc of up to 8 heads) of
+// every worker.  The same argument checks as make_plan.
+pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4Plan* pl) {
+    if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_ctx < 0) return PKV_ERR_INVALID_ARG;
+    if (HD != 64 && HD != 128) return PKV_ERR_UNSUPPORTED;
+    if (B != 8 && B != 16 && B != 32) return PKV_ERR_UNSUPPORTED;
+    pl->group = Hq / Hkv;
+    pl->nsub = (pl->group + kFp4Heads - 1) / kFp4Heads;
+    const int64_t tiles = ((int64_t)max_ctx + kFp4Tile - 1) / kFp4Tile;
+    if ((int64_t)Hkv * pl->nsub > INT32_MAX || (int64_t)S * Hkv * pl->nsub > INT32_MAX ||
+        (int64_t)S * Hkv * pl->nsub * tiles > INT32_MAX - (1 << 24))
+        return PKV_ERR_UNSUPPORTED;                       // tiles are counted in 32 bits
+    pl->workers = (int)fp4_max_workers(S, Hkv, pl->nsub, max_ctx);
+    const size_t states = (size_t)pl->workers * 2 * kFp4Heads;
+    pl->off_ml = round_up(states * HD * 4, 256);
+    pl->total = round_up(pl->off_ml + states * 8, 256);
+    return PKV_OK;
+}
+
 pkv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
 }  // namespace
@@ -120,6 +144,11 @@ extern "C" {
 size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                   int block_size, int max_context_len, pkv_dtype kv_dtype) {
     if (!known(kv_dtype)) return 0;
+    if (kv_dtype == PKV_FP4_E2M1) {
+        Fp4Plan f;
+        return make_fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                             max_context_len, &f) == PKV_OK ? f.total : 0;
+    }
     Plan p;
     if (make_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                   &p) != PKV_OK)
@@ -145,9 +174,13 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     if (kv_dtype != q_dtype && !quantised(kv_dtype))
         return known(kv_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
     if (!isfinite(scale) || !isfinite(kv_scale) || !(kv_scale > 0.f)) return PKV_ERR_INVALID_ARG;
-    Plan plan;
-    pkv_status st = make_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                              max_context_len, &plan);
+    const bool fp4 = kv_dtype == PKV_FP4_E2M1;
+    Plan plan{};
+    Fp4Plan fplan{};
+    const pkv_status st = fp4 ? make_fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                              block_size, max_context_len, &fplan)
+                              : make_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                          block_size, max_context_len, &plan);
     if (st != PKV_OK) return st;
     if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size)
         return PKV_ERR_INVALID_ARG;
@@ -157,7 +190,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     if (!aligned(query, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.total)
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < (fp4 ? fplan.total : plan.total))
         return PKV_ERR_WORKSPACE;
 
     DeviceInfo* dev = nullptr;
@@ -165,7 +198,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     if (err != cudaSuccess) return PKV_ERR_CUDA;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (kv_dtype == PKV_FP4_E2M1) {
+    if (fp4) {
         DecodeFp4Params f{};
         f.q = query;
         f.k_cache = k_cache;
@@ -177,7 +210,11 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
         f.num_seqs = num_seqs;
         f.num_q_heads = num_q_heads;
         f.num_kv_heads = num_kv_heads;
-        f.group = plan.group;
+        f.group = fplan.group;
+        f.nsub = fplan.nsub;
+        f.max_workers = fplan.workers;
+        f.part_acc = reinterpret_cast<float*>(ws);
+        f.part_ml = reinterpret_cast<float*>(ws + fplan.off_ml);
         f.head_dim = head_dim;
         f.block_size = block_size;
         f.num_blocks = num_blocks;

@@ -1,92 +1,715 @@
 // decode_fp4.cu -- single-query decode attention over the 4-bit paged cache.
 //
 // o = sum_t softmax_t(scale q.k_t) v_t with k, v = code * scale * kv_scale; kv_scale is folded
-// into the logit scale and the output.  One CTA per (sequence, query head): its four warps take
-// every fourth token, a lane d / 32 dims of it, with a running max and sum each, and merge at the
-// end.
+// into the logit scale and the output.
+//
+// Products.  code * scale has at most 2 + 4 significant bits and lies in [2^-10, 2688]: it is
+// exact in fp16, so a widening convert and one packed multiply make tensor-core operands of
+// the stored bytes without a rounding (mma.sync m16n8k16, fp32 accumulation):
+//   S^T[16 tokens x 8 heads] = K[16 x d] . Q^T        O^T[d x 8] += V^T[d x 16] . P^T[16 x 8]
+// Queries of any type become fp16 exactly enough: each head's row is scaled by a power of two
+// that puts its largest magnitude in [2^14, 2^15) (undone in the logit scale), so a 16-bit row
+// keeps every bit down to 2^-39 of its largest value.  fp32 queries take two such terms (22
+// bits).  Weights enter the second product as fp16 in [0, 2^15] (the running maximum is moved
+// when a logit passes it by 2^8; weights are taken 2^7 above it, so that a weight 2^-32 of the
+// largest still counts), two terms of them for fp32; the denominator sums them in fp32 before
+// that rounding.
+//
+// Layout.  32 dims of a row are 16 bytes, eight rows of them one 128-byte line: ldmatrix reads
+// them free of bank conflicts with no swizzle, and one bulk copy moves a (block, kv head) tile
+// with its scales.  A lane's 4-byte word of K holds dims 8c .. 8c + 7 of row g: its four bytes
+// are four operand pairs, the reduction index being permuted for K and q alike.  A transposed
+// word of V holds dims 4g .. 4g + 3 of tokens 2c and 2c + 1: five bit operations pair the
+// tokens' nibbles in bytes.
+//
+// Split.  Every (sequence, kv head, 8 query heads) unit is cut into 64-token tiles, and the
+// flattened tiles are dealt in equal runs to one CTA each ("worker"), all resident at once.
+// Every CTA derives the plan by itself from context_lens (a block-wide scan), so no planning
+// kernel runs first.  A CTA is a producer warp filling a ring of tiles and four consumer warps,
+// 16 tokens of every tile each, whose states meet in shared memory at the end of a unit.  Units
+// inside one run are written straight to `out`; a worker leaves at most two partial states
+// (its first and its last unit), and merge_fp4_kernel joins those of each cut unit in order.
 #include "decode_fp4.cuh"
 
 #include "cache_row.cuh"
 
 namespace pkv {
+namespace {
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What is left of (lo, hi) after pack_f16's rounding, as fp16 again.
+__device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+    return pack_f16(lo - v.x, hi - v.y);
+}
+
+constexpr int kSlack = 8;    // log2 headroom before the running maximum moves
+constexpr int kLift = 7;     // weights are 2^(x - m + kLift): at most 2^15 in fp16
+constexpr int kConsumers = 4;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kMergeThreads = 512;
 
 template <typename QT, int HD>
-__global__ void __launch_bounds__(128) decode_fp4_kernel(DecodeFp4Params p) {
-    constexpr int LPR = HD / 8, TPW = 32 / LPR, GROUPS = 4 * TPW;   // lanes a token, tokens a warp
-    __shared__ float s_acc[GROUPS][HD], s_m[GROUPS], s_l[GROUPS];
-    const int s = blockIdx.x / p.num_q_heads, qh = blockIdx.x % p.num_q_heads;
-    const int kvh = qh / p.group, B = p.block_size;
-    const int lane = threadIdx.x & 31, j = lane % LPR;
-    const int grp = (threadIdx.x >> 5) * TPW + lane / LPR;
-    const int cap = min(p.max_context_len, p.max_blocks * B);
-    int ctx = p.context_lens[s];
-    if (ctx < 0 || ctx > cap) {
-        if (threadIdx.x == 0) set_status(p.status, PKV_DEV_BAD_CONTEXT);
-        ctx = ctx < 0 ? 0 : cap;
-    }
-    float q[8], acc[8] = {0.f}, m = -INFINITY, l = 0.f;
-    const int64_t row0 = ((int64_t)s * p.num_q_heads + qh) * HD;
+struct Cfg {
+    static constexpr int ROWB = HD / 2 + HD / 16;
+    static constexpr int KV_BYTES = kFp4Tile * ROWB;
+    static constexpr int Q_BYTES = kFp4Heads * HD * QT::bytes;
+    static constexpr int STAGE_BYTES = (2 * KV_BYTES + Q_BYTES + 127) / 128 * 128;
+    static constexpr int NSTAGE = 3;
+    static constexpr int NCHUNK = HD / 32;
+    static constexpr int NP = std::is_same<QT, F32>::value ? 2 : 1;   // terms of q and p
+    static constexpr int HS = HD + 1;                  // exchange stride of a head: few conflicts
+    static constexpr int XBUF = kConsumers * kFp4Heads * (HS + 2);    // acc, then m, l
+    static constexpr size_t OFF_META = (size_t)NSTAGE * STAGE_BYTES;
+    static constexpr size_t OFF_BARS = OFF_META + NSTAGE * 32;
+    static constexpr size_t OFF_X = OFF_BARS + 2 * NSTAGE * 8;
+    static constexpr size_t SMEM = OFF_X + XBUF * 4;
+    static constexpr int CTAS = NP == 1 ? 4 : 3;       // resident, by registers
+};
+
+struct TileMeta {
+    int flags, n;            // kFirst.., valid tokens of the tile
+    int s, kvh, qsub, nh;
+    int slot;                // partial slot of the worker, or -1: the whole unit is here
+    int pad;
+};
+constexpr int kFirst = 1, kLast = 2, kDone = 4;
+
+__device__ __forceinline__ int tiles_of(const DecodeFp4Params& p, int s) {
+    const int cap = min(p.max_context_len, p.max_blocks * p.block_size);
+    const int c = p.context_lens[s];
+    return c <= 0 ? 0 : (min(c, cap) + kFp4Tile - 1) / kFp4Tile;
+}
+
+// Block-wide scan of the sequences' tile counts: pref[i] = tiles of the sequences before
+// thread i's run of ceil(S / threads), pref[threads] = all.  Syncs the block.
+template <int THREADS>
+__device__ __forceinline__ void scan_tiles(const DecodeFp4Params& p, int* pref, int* wsum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = (p.num_seqs + THREADS - 1) / THREADS;
+    int n = 0;
+    for (int s = tid * run; s < min(p.num_seqs, (tid + 1) * run); ++s) n += tiles_of(p, s);
+    int x = n;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = load_as_float<QT>(p.q, row0 + 8 * j + i) * p.qk_scale_log2;
-    const int64_t tile_bytes = (int64_t)B * cache_row_bytes_of<E2M1>(HD);
-    for (int t0 = 0; t0 < ctx; t0 += GROUPS) {
-        const int t = t0 + grp;
-        const bool live = t < ctx;
-        float k[8] = {0.f}, v[8] = {0.f};
-        if (live) {
-            int blk = p.block_tables[(int64_t)s * p.max_blocks + t / B];
-            if (blk < 0 || blk >= p.num_blocks) {
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) before += w < warp ? wsum[w] : 0;
+    pref[tid + 1] = before + x;
+    if (tid == 0) pref[0] = 0;
+    __syncthreads();
+}
+
+// Place of flattened tile `pos` (below the total): its sequence, that sequence's tiles, and the
+// position of the sequence's first tile.
+template <int THREADS>
+__device__ __forceinline__ void locate(const DecodeFp4Params& p, const int* pref, int upi, int pos,
+                                       int* seq, int* tiles, int* base) {
+    int lo = 0, hi = THREADS - 1;
+    while (lo < hi) {                       // the last run starting at or before pos
+        const int mid = (lo + hi + 1) >> 1;
+        if (pref[mid] * upi <= pos) lo = mid;
+        else hi = mid - 1;
+    }
+    const int run = (p.num_seqs + THREADS - 1) / THREADS;
+    int s = lo * run, b = pref[lo] * upi, n = tiles_of(p, s);
+    while (b + n * upi <= pos) {
+        b += n * upi;
+        n = tiles_of(p, ++s);
+    }
+    *seq = s;
+    *tiles = n;
+    *base = b;
+}
+
+__device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total) {
+    return max(kFp4MinQuota, (total + p.workers - 1) / p.workers);
+}
+
+// Where the producer is: tile `tile` of unit `u` of sequence s (n tiles, ctx tokens).
+struct Cursor {
+    int s, u, tile, n, ctx;
+};
+
+// A run of at most 64 blocks of one unit.
+struct Window {
+    int valid, s, u, t0, t1;     // tokens [t0, t1)
+    int first, last, slot;
+};
+
+__device__ __forceinline__ Window next_window(const DecodeFp4Params& p, int upi, int a, int end,
+                                              int& pos, Cursor& c) {
+    Window w{};
+    if (pos >= end) return w;
+    while (c.tile == c.n) {                       // the next unit with tiles
+        c.tile = 0;
+        if (++c.u == upi || c.n == 0) {
+            c.u = 0;
+            ++c.s;
+            c.n = tiles_of(p, c.s);
+            c.ctx = min(p.context_lens[c.s], min(p.max_context_len, p.max_blocks * p.block_size));
+        }
+    }
+    const int wt = min(min(p.block_size, c.n - c.tile), end - pos);   // <= 64 blocks
+    const int ustart = pos - c.tile, uend = ustart + c.n;
+    w.valid = 1;
+    w.s = c.s;
+    w.u = c.u;
+    w.t0 = c.tile * kFp4Tile;
+    w.t1 = min((c.tile + wt) * kFp4Tile, c.ctx);
+    w.first = c.tile == 0 || pos == a;
+    w.last = pos + wt == end || c.tile + wt == c.n;
+    w.slot = ustart < a ? 0 : (uend > end ? 1 : -1);
+    c.tile += wt;
+    pos += wt;
+    return w;
+}
+
+template <typename QT, int HD>
+__global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
+    decode_fp4_kernel(DecodeFp4Params p) {
+    using C = Cfg<QT, HD>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_pref[kThreads + 1], s_wsum[kThreads / 32];
+    TileMeta* metas = reinterpret_cast<TileMeta*>(smem + C::OFF_META);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+    uint64_t* empty = full + C::NSTAGE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NSTAGE; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kConsumers);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();                // the kernel before (the cache write) has completed
+    pdl_launch_dependents();   // the merge kernel may plan beside this one
+    scan_tiles<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
+    const int B = p.block_size, upi = p.num_kv_heads * p.nsub;
+    const int tile_bytes = B * C::ROWB;
+    const int total = s_pref[kThreads] * upi, q = quota_of(p, total);
+    const int a = min(blockIdx.x * q, total), end = min(a + q, total);
+
+    if (warp == kConsumers) {
+        // ======================= producer warp =======================
+        const uint64_t policy = l2_evict_first_policy();
+        int stage = 0, pos = a;
+        uint32_t phase = 0;
+        Cursor cur{};
+        if (a < end) {
+            int base;
+            locate<kThreads>(p, s_pref, upi, a, &cur.s, &cur.n, &base);
+            cur.u = (a - base) / cur.n;
+            cur.tile = (a - base) % cur.n;
+            cur.ctx = min(p.context_lens[cur.s], min(p.max_context_len, p.max_blocks * B));
+        }
+        Window win = next_window(p, upi, a, end, pos, cur);
+        int e0 = 0, e1 = 0;
+        auto entries = [&](const Window& w, int& x0, int& x1) {
+            const int32_t* row = p.block_tables + (int64_t)w.s * p.max_blocks;
+            const int j0 = w.t0 / B, nb = (w.t1 + B - 1) / B - j0;
+            x0 = lane < nb ? row[j0 + lane] : 0;
+            x1 = lane + 32 < nb ? row[j0 + lane + 32] : 0;
+        };
+        if (win.valid) entries(win, e0, e1);
+        while (win.valid) {
+            const bool bad0 = e0 < 0 || e0 >= p.num_blocks, bad1 = e1 < 0 || e1 >= p.num_blocks;
+            if (bad0 || bad1) {
                 set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
-                blk = 0;
+                if (bad0) e0 = 0;
+                if (bad1) e1 = 0;
             }
-            const int64_t tile = ((int64_t)blk * p.num_kv_heads + kvh) * tile_bytes;
-            CacheRow<E2M1>::load(static_cast<const uint8_t*>(p.k_cache) + tile, B, HD, t % B, j, k);
-            CacheRow<E2M1>::load(static_cast<const uint8_t*>(p.v_cache) + tile, B, HD, t % B, j, v);
+            const int kvh = win.u / p.nsub, qsub = win.u % p.nsub;
+            const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
+            Window nxt{};
+            int n0 = 0, n1 = 0;
+            for (int ts = win.t0; ts < win.t1; ts += kFp4Tile) {
+                const int te = min(ts + kFp4Tile, win.t1);
+                const bool first = win.first && ts == win.t0;
+                if (!mbar_wait(&empty[stage], phase ^ 1u)) {
+                    set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
+                    return;
+                }
+                uint8_t* sb = smem + (size_t)stage * C::STAGE_BYTES;
+                const int nblk = (te - ts + B - 1) / B;
+                const uint32_t qbytes = first ? (uint32_t)(nh * HD * QT::bytes) : 0u;
+                if (lane == 0) {
+                    TileMeta m;
+                    m.flags = (first ? kFirst : 0) |
+                              (win.last && ts + kFp4Tile >= win.t1 ? kLast : 0);
+                    m.n = te - ts;
+                    m.s = win.s;
+                    m.kvh = kvh;
+                    m.qsub = qsub;
+                    m.nh = nh;
+                    m.slot = win.slot;
+                    m.pad = 0;
+                    metas[stage] = m;
+                    mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)(nblk * tile_bytes) + qbytes);
+                }
+                __syncwarp();
+                const int rel = (ts - win.t0) / B + lane;
+                const int pa = __shfl_sync(0xffffffffu, e0, rel & 31);
+                const int pb = __shfl_sync(0xffffffffu, e1, rel & 31);
+                if (lane < nblk) {
+                    const int64_t off =
+                        ((int64_t)(rel < 32 ? pa : pb) * p.num_kv_heads + kvh) * tile_bytes;
+                    bulk_g2s_hint(sb + lane * tile_bytes, static_cast<const uint8_t*>(p.k_cache) + off,
+                                  (uint32_t)tile_bytes, &full[stage], policy);
+                    bulk_g2s_hint(sb + C::KV_BYTES + lane * tile_bytes,
+                                  static_cast<const uint8_t*>(p.v_cache) + off,
+                                  (uint32_t)tile_bytes, &full[stage], policy);
+                }
+                if (qbytes && lane == 31) {
+                    const int64_t row = (int64_t)win.s * p.num_q_heads + kvh * p.group + qsub * kFp4Heads;
+                    bulk_g2s(sb + 2 * C::KV_BYTES,
+                             static_cast<const uint8_t*>(p.q) + row * HD * QT::bytes, qbytes,
+                             &full[stage]);
+                }
+                if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
+                if (ts == win.t0) {      // look ahead: the next window's entries load meanwhile
+                    nxt = next_window(p, upi, a, end, pos, cur);
+                    if (nxt.valid) entries(nxt, n0, n1);
+                }
+            }
+            win = nxt;
+            e0 = n0;
+            e1 = n1;
         }
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z = fmaf(q[i], k[i], z);
-#pragma unroll
-        for (int off = LPR / 2; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-        if (live) {
-            const float mn = fmaxf(m, z);
-            const float r = exp2f(m - mn), e = exp2f(z - mn);
-            l = l * r + e;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = acc[i] * r + e * v[i];
-            m = mn;
+        if (!mbar_wait(&empty[stage], phase ^ 1u)) {
+            set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
+            return;
+        }
+        if (lane == 0) {
+            metas[stage].flags = kDone;
+            mbar_arrive(&full[stage]);
+        }
+        return;
+    }
+
+    // ========================= consumer warps =========================
+    // sequences without context: zero rows (and lengths outside the bounds are flagged once)
+    {
+        const int cap = min(p.max_context_len, p.max_blocks * B), row = p.num_q_heads * HD;
+        for (int s = blockIdx.x * kConsumers + warp; s < p.num_seqs; s += gridDim.x * kConsumers) {
+            const int c = p.context_lens[s];
+            if (lane == 0 && (c < 0 || c > cap)) set_status(p.status, PKV_DEV_BAD_CONTEXT);
+            if (c <= 0 || cap == 0)
+                for (int i = lane; i < row; i += 32)
+                    store_from_float<QT>(p.out, (int64_t)s * row + i, 0.f);
         }
     }
+    const int g = lane >> 2, c = lane & 3;
+    // this lane's places in a stage: ldmatrix row (token 16 warp + 8 (mi & 1) + r of chunk
+    // mi >> 1), and the scale rows of tokens g, g + 8 (K) and 2c, 2c + 8 (V)
+    auto place = [&](int tok, int bytes) { return tok / B * tile_bytes + tok % B * bytes; };
+    const int mi = lane >> 3;
+    const uint32_t ld_off = place(16 * warp + 8 * (mi & 1) + (lane & 7), 16) + (mi >> 1) * B * 16;
+    const int sc0 = B * (HD / 2);
+    const uint32_t ks_a = sc0 + place(16 * warp + g, HD / 16), ks_b = sc0 + place(16 * warp + g + 8, HD / 16);
+    const uint32_t vs_a = sc0 + place(16 * warp + 2 * c, HD / 16), vs_b = sc0 + place(16 * warp + 2 * c + 8, HD / 16);
+    // byte picks: K scales of chunk pairs, each twice; V scales of tokens 2c (low) and 2c + 1
+    const uint32_t ksel = (c >> 1) ? 0x3311u : 0x2200u;
+    const uint32_t vsel = (g >> 2) ? 0x7351u : 0x6240u;
+
+    uint32_t qf[C::NP][C::NCHUNK][4];     // per chunk: two k-steps of (b0, b1)
+    float o[2 * C::NCHUNK][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, qs0 = 0.f, qs1 = 0.f;
+    int stage = 0;
+    uint32_t phase = 0;
+
+    while (true) {
+        if (!mbar_wait(&full[stage], phase)) {
+            set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
+            return;
+        }
+        const TileMeta meta = metas[stage];
+        if (meta.flags & kDone) return;
+        const uint8_t* sb = smem + (size_t)stage * C::STAGE_BYTES;
+        if (meta.flags & kFirst) {
+            // q row of head g: dims 32 ch + 8c .. + 7, scaled by a power of two into fp16
+            float x[C::NCHUNK][8];
+            float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_acc[grp][8 * j + i] = acc[i];
-    if (j == 0) {
-        s_m[grp] = m;
-        s_l[grp] = l;
+            for (int ch = 0; ch < C::NCHUNK; ++ch) {
+                if (g < meta.nh)
+                    load8<QT>(sb + 2 * C::KV_BYTES + (g * HD + 32 * ch + 8 * c) * QT::bytes, x[ch]);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[ch][i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = absmax_nan(x[ch][i], amax);
+            }
+            amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
+            amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 2), amax);
+            const int ex = (int)(__float_as_uint(amax) >> 23) - 127;     // floor(log2), or 128
+            const int e = ex == 128 ? 0 : min(14 - ex, 126);
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            const float qs = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+            qs0 = __shfl_sync(0xffffffffu, qs, 8 * c);
+            qs1 = __shfl_sync(0xffffffffu, qs, 8 * c + 4);
+#pragma unroll
+            for (int ch = 0; ch < C::NCHUNK; ++ch)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float lo = x[ch][2 * i] * up, hi = x[ch][2 * i + 1] * up;
+                    qf[0][ch][i] = pack_f16(lo, hi);
+                    if constexpr (C::NP == 2) qf[1][ch][i] = pack_f16_rest(lo, hi, qf[0][ch][i]);
+                }
+#pragma unroll
+            for (int mt = 0; mt < 2 * C::NCHUNK; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][i] = 0.f;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
+        }
+        const int nv = meta.n - 16 * warp;          // valid tokens of this warp's 16
+        if (nv > 0) {
+            // ---- S^T = K Q^T ----
+            float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            uint32_t ka[2], kb[2];                  // scale bytes of rows g, g + 8
+            if constexpr (HD == 128) {
+                const uint2 ra = *reinterpret_cast<const uint2*>(sb + ks_a);
+                const uint2 rb = *reinterpret_cast<const uint2*>(sb + ks_b);
+                ka[0] = ra.x; ka[1] = ra.y; kb[0] = rb.x; kb[1] = rb.y;
+            } else {
+                ka[0] = *reinterpret_cast<const uint32_t*>(sb + ks_a);
+                kb[0] = *reinterpret_cast<const uint32_t*>(sb + ks_b);
+                ka[1] = kb[1] = 0u;
+            }
+#pragma unroll
+            for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
+                uint32_t r[4];
+                ldsm4(smem_addr(sb) + ld_off + 2 * cp * B * 16, r);
+                const uint32_t da = __byte_perm(ka[cp], 0u, ksel), db = __byte_perm(kb[cp], 0u, ksel);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int ch = 2 * cp + k;
+                    const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                    const uint32_t fa = e4m3x2_to_f16x2(k ? da >> 16 : da & 0xffffu);
+                    const uint32_t fb = e4m3x2_to_f16x2(k ? db >> 16 : db & 0xffffu);
+                    const uint32_t a00 = hmul2(e2m1x2_to_f16x2<0>(wa), fa), a01 = hmul2(e2m1x2_to_f16x2<0>(wb), fb);
+                    const uint32_t a02 = hmul2(e2m1x2_to_f16x2<1>(wa), fa), a03 = hmul2(e2m1x2_to_f16x2<1>(wb), fb);
+                    const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
+                    const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
+#pragma unroll
+                    for (int t = 0; t < C::NP; ++t) {
+                        mma_f16(sa[0], a00, a01, a02, a03, qf[t][ch][0], qf[t][ch][1]);
+                        mma_f16(sa[1], a10, a11, a12, a13, qf[t][ch][2], qf[t][ch][3]);
+                    }
+                }
+            }
+            // ---- running softmax: tokens g (x0, x1) and g + 8 (x2, x3), heads 2c and 2c + 1 ----
+            float x0 = (sa[0][0] + sa[1][0]) * qs0, x1 = (sa[0][1] + sa[1][1]) * qs1;
+            float x2 = (sa[0][2] + sa[1][2]) * qs0, x3 = (sa[0][3] + sa[1][3]) * qs1;
+            if (nv < 16) {
+                if (g >= nv) x0 = x1 = -INFINITY;
+                if (g + 8 >= nv) x2 = x3 = -INFINITY;
+            }
+            float t0 = fmaxf(x0, x2), t1 = fmaxf(x1, x3);
+            if (__any_sync(0xffffffffu, t0 > m0 + kSlack || t1 > m1 + kSlack)) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
+                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+                }
+                const bool n0 = t0 > m0 + kSlack, n1 = t1 > m1 + kSlack;
+                const float r0 = n0 ? fast_exp2(m0 - t0) : 1.f, r1 = n1 ? fast_exp2(m1 - t1) : 1.f;
+                if (n0) m0 = t0;
+                if (n1) m1 = t1;
+                l0 *= r0;
+                l1 *= r1;
+#pragma unroll
+                for (int mt = 0; mt < 2 * C::NCHUNK; ++mt) {
+                    o[mt][0] *= r0;
+                    o[mt][1] *= r1;
+                    o[mt][2] *= r0;
+                    o[mt][3] *= r1;
+                }
+            }
+            const float p0 = fast_exp2(x0 - (m0 - kLift)), p1 = fast_exp2(x1 - (m1 - kLift));
+            const float p2 = fast_exp2(x2 - (m0 - kLift)), p3 = fast_exp2(x3 - (m1 - kLift));
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            uint32_t pb[C::NP][2];
+            {
+                const uint32_t u = pack_f16(p0, p1), v = pack_f16(p2, p3);
+                pb[0][0] = trans8x8(u);
+                pb[0][1] = trans8x8(v);
+                if constexpr (C::NP == 2) {
+                    pb[1][0] = trans8x8(pack_f16_rest(p0, p1, u));
+                    pb[1][1] = trans8x8(pack_f16_rest(p2, p3, v));
+                }
+            }
+            // ---- O^T += V^T P^T ----
+            const uint8_t* sv = sb + C::KV_BYTES;
+            uint32_t va[4], vb[4];      // scale bytes: tokens 2c (words 0, 1), 2c + 1 (2, 3); + 8
+            if constexpr (HD == 128) {
+                const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_a);
+                const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_b);
+                va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
+                vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
+            } else {
+                const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_a);
+                const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_b);
+                va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
+                va[1] = va[3] = vb[1] = vb[3] = 0u;
+            }
+            if (nv < 16) {   // rows past the context may hold anything: scale 0 (codes are finite)
+                if (2 * c >= nv) va[0] = va[1] = 0u;
+                if (2 * c + 1 >= nv) va[2] = va[3] = 0u;
+                if (2 * c + 8 >= nv) vb[0] = vb[1] = 0u;
+                if (2 * c + 9 >= nv) vb[2] = vb[3] = 0u;
+            }
+#pragma unroll
+            for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
+                uint32_t r[4];
+                ldsm4_trans(smem_addr(sv) + ld_off + 2 * cp * B * 16, r);
+                // bytes (2c, 2c + 1) of chunk 2cp's group, then of chunk 2cp + 1's
+                const uint32_t da = __byte_perm(va[cp], va[cp + 2], vsel);
+                const uint32_t db = __byte_perm(vb[cp], vb[cp + 2], vsel);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int ch = 2 * cp + k;
+                    const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                    const uint32_t fa = e4m3x2_to_f16x2(k ? da >> 16 : da & 0xffffu);
+                    const uint32_t fb = e4m3x2_to_f16x2(k ? db >> 16 : db & 0xffffu);
+                    // nibble pairs (token 2c low, 2c + 1 high): dims 0, 2 and 1, 3 of the four
+                    const uint32_t ea = (wa & 0x0f0fu) | ((wa >> 12) & 0xf0f0u);
+                    const uint32_t eb = (wb & 0x0f0fu) | ((wb >> 12) & 0xf0f0u);
+                    const uint32_t oa = ((wa >> 4) & 0x0f0fu) | ((wa >> 16) & 0xf0f0u);
+                    const uint32_t ob = ((wb >> 4) & 0x0f0fu) | ((wb >> 16) & 0xf0f0u);
+                    const uint32_t e0 = hmul2(e2m1x2_to_f16x2<0>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<1>(ea), fa);
+                    const uint32_t e2 = hmul2(e2m1x2_to_f16x2<0>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<1>(eb), fb);
+                    const uint32_t d0 = hmul2(e2m1x2_to_f16x2<0>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<1>(oa), fa);
+                    const uint32_t d2 = hmul2(e2m1x2_to_f16x2<0>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<1>(ob), fb);
+#pragma unroll
+                    for (int t = 0; t < C::NP; ++t) {
+                        mma_f16(o[2 * ch], e0, e1, e2, e3, pb[t][0], pb[t][1]);
+                        mma_f16(o[2 * ch + 1], d0, d1, d2, d3, pb[t][0], pb[t][1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
+        if (!(meta.flags & kLast)) continue;
+
+        // ---------------- end of the segment: the four warps' states meet ----------------
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+        }
+        float* xa = reinterpret_cast<float*>(smem + C::OFF_X);
+        float* xm = xa + kConsumers * kFp4Heads * C::HS;
+        float* xl = xm + kConsumers * kFp4Heads;
+        const int hw = warp * kFp4Heads + 2 * c;
+#pragma unroll
+        for (int mt = 0; mt < 2 * C::NCHUNK; ++mt) {
+            const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);      // o[.][2], o[.][3]: dim + 2
+            xa[hw * C::HS + dim] = o[mt][0];
+            xa[(hw + 1) * C::HS + dim] = o[mt][1];
+            xa[hw * C::HS + dim + 2] = o[mt][2];
+            xa[(hw + 1) * C::HS + dim + 2] = o[mt][3];
+        }
+        if (g == 0) {
+            xm[hw] = m0;
+            xm[hw + 1] = m1;
+            xl[hw] = l0;
+            xl[hw + 1] = l1;
+        }
+        named_bar_sync(1, kConsumers * 32);
+        const int h = threadIdx.x >> 4, part = threadIdx.x & 15;    // 16 threads a head
+        if (h < meta.nh) {
+            float M = -INFINITY, L = 0.f, f[kConsumers];
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) {
+                const float mw = xm[w * kFp4Heads + h];
+                f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+                L = fmaf(xl[w * kFp4Heads + h], f[w], L);
+            }
+            const int head = meta.kvh * p.group + meta.qsub * kFp4Heads + h;
+            const int64_t row = (int64_t)meta.s * p.num_q_heads + head;
+            const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.slot, 0)) * kFp4Heads + h;
+            const float inv = p.out_scale / L;
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+                const int dim = part + 16 * i;
+                float A = 0.f;
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w)
+                    A = fmaf(xa[(w * kFp4Heads + h) * C::HS + dim], f[w], A);
+                if (meta.slot < 0) store_from_float<QT>(p.out, row * HD + dim, A * inv);
+                else p.part_acc[pi * HD + dim] = A;
+            }
+            if (meta.slot >= 0 && part == 0) {
+                p.part_ml[2 * pi] = M;
+                p.part_ml[2 * pi + 1] = L;
+            }
+        }
+        named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
+    }
+}
+
+// CTA b looks at the boundary between workers b and b + 1: if it cuts a unit and is the first to
+// do so, the CTA joins the unit's partial states (worker order) and writes its heads.  Sixteen
+// warps share the heads: warp w takes head w % nh's pieces w / nh, w / nh + 16 / nh, ...
+template <typename QT, int HD>
+__global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Params p) {
+    constexpr int WARPS = kMergeThreads / 32, V = HD / 32;      // dims of a lane
+    __shared__ int s_pref[kMergeThreads + 1], s_wsum[WARPS];
+    __shared__ float s_acc[WARPS][HD], s_m[WARPS], s_l[WARPS];
+    scan_tiles<kMergeThreads>(p, s_pref, s_wsum);
+    const int upi = p.num_kv_heads * p.nsub;
+    const int total = s_pref[kMergeThreads] * upi, q = quota_of(p, total);
+    const int pos = (blockIdx.x + 1) * q;
+    pdl_wait();                // the partial states are written; also in CTAs without a boundary:
+    if (pos >= total) return;  // this grid must not end before the decode has
+    int s, n, base;
+    locate<kMergeThreads>(p, s_pref, upi, pos, &s, &n, &base);
+    const int u = (pos - base) / n, ustart = base + u * n, uend = ustart + n;
+    const int w0 = ustart / q, w1 = (uend - 1) / q;             // workers of the unit
+    if (ustart == pos || w0 != blockIdx.x) return;
+    const int kvh = u / p.nsub, qsub = u % p.nsub;
+    const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = warp % nh, step = WARPS / nh;
+    float M = -INFINITY, L = 0.f, A[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 0.f;
+    if (warp / nh < step)
+        for (int w = w0 + warp / nh; w <= w1; w += step) {
+            // a worker's slot 0 is the unit it starts inside of, slot 1 the one it ends inside of
+            const int64_t pi = ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * kFp4Heads + h;
+            const float m = __ldcg(p.part_ml + 2 * pi), l = __ldcg(p.part_ml + 2 * pi + 1);
+            float a[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) a[i] = __ldcg(p.part_acc + pi * HD + lane + 32 * i);
+            const float Mn = fmaxf(M, m);
+            const float fo = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+            const float fn = m == -INFINITY ? 0.f : fast_exp2(m - Mn);
+            L = L * fo + l * fn;
+#pragma unroll
+            for (int i = 0; i < V; ++i) A[i] = A[i] * fo + a[i] * fn;
+            M = Mn;
+        }
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_acc[warp][lane + 32 * i] = A[i];
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = L;
     }
     __syncthreads();
-    if (threadIdx.x < HD) {
-        float M = -INFINITY, L = 0.f, A = 0.f;
-        for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, s_m[g]);
-        for (int g = 0; g < GROUPS; ++g) {
-            const float f = s_m[g] == -INFINITY ? 0.f : exp2f(s_m[g] - M);
-            L = fmaf(s_l[g], f, L);
-            A = fmaf(s_acc[g][threadIdx.x], f, A);
-        }
-        store_from_float<QT>(p.out, row0 + threadIdx.x, ctx > 0 ? A / L * p.out_scale : 0.f);
+    if (warp >= nh) return;
+    M = -INFINITY;
+    for (int k = 0; k < step; ++k) M = fmaxf(M, s_m[h + k * nh]);
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 0.f;
+    for (int k = 0; k < step; ++k) {
+        const int w = h + k * nh;
+        const float f = s_m[w] == -INFINITY ? 0.f : fast_exp2(s_m[w] - M);
+        L = fmaf(s_l[w], f, L);
+#pragma unroll
+        for (int i = 0; i < V; ++i) A[i] = fmaf(s_acc[w][lane + 32 * i], f, A[i]);
     }
+    const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + qsub * kFp4Heads + h;
+    const float inv = p.out_scale / L;
+#pragma unroll
+    for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, row * HD + lane + 32 * i, A[i] * inv);
 }
 
-template <typename QT>
-cudaError_t launch(const DecodeFp4Params& p, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(p.num_seqs * p.num_q_heads);
-    if (p.head_dim == 128) decode_fp4_kernel<QT, 128><<<grid, 128, 0, stream>>>(p);
-    else decode_fp4_kernel<QT, 64><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+template <typename QT, int HD>
+cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
+    using C = Cfg<QT, HD>;
+    static int workers[64] = {0};          // CTAs the device holds at once
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    auto kernel = decode_fp4_kernel<QT, HD>;
+    if (workers[dev] == 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (err != cudaSuccess) return err;
+        int per_sm = 0, sms = 0;
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, C::SMEM);
+        if (err != cudaSuccess) return err;
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (err != cudaSuccess) return err;
+        const int w = (per_sm > 0 ? per_sm : 1) * sms;
+        workers[dev] = w < kFp4MaxWorkers ? w : kFp4MaxWorkers;
+    }
+    DecodeFp4Params p = p0;
+    p.workers = workers[dev];
+    const int grid = p.max_workers < p.workers ? p.max_workers : p.workers;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (err != cudaSuccess || grid == 1) return err;      // one worker cuts nothing
+    cfg.gridDim = dim3((unsigned)(grid - 1), 1, 1);
+    cfg.blockDim = dim3(kMergeThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD>, p);
 }
+
+}  // namespace
 
 cudaError_t launch_decode_fp4(const DecodeFp4Params& p, pkv_dtype q, cudaStream_t stream) {
-    if (q == PKV_F32) return launch<F32>(p, stream);
-    return q == PKV_F16 ? launch<F16>(p, stream) : launch<BF16>(p, stream);
+    if (q == PKV_F32) return p.head_dim == 128 ? launch<F32, 128>(p, stream) : launch<F32, 64>(p, stream);
+    if (q == PKV_F16) return p.head_dim == 128 ? launch<F16, 128>(p, stream) : launch<F16, 64>(p, stream);
+    return p.head_dim == 128 ? launch<BF16, 128>(p, stream) : launch<BF16, 64>(p, stream);
 }
 
 }  // namespace pkv
