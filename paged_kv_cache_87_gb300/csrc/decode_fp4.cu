@@ -72,14 +72,28 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The low (k = 0) or high half of an f16x2 in both halves (an operand modifier, not an operation).
+__device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 t = k ? __high2half2(h) : __low2half2(h);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// (a & mask) | (b & ~mask)
+__device__ __forceinline__ uint32_t bitselect(uint32_t a, uint32_t b, uint32_t mask) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(mask));
+    return r;
+}
+
 // What is left of (lo, hi) after pack_f16's rounding, as fp16 again.
 __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&packed));
     return pack_f16(lo - v.x, hi - v.y);
 }
 
-constexpr int kSlack = 8;    // log2 headroom before the running maximum moves
-constexpr int kLift = 7;     // weights are 2^(x - m + kLift): at most 2^15 in fp16
+constexpr float kSlack = 8.f;    // log2 headroom before the running maximum moves
+constexpr float kLift = 7.f;     // weights are 2^(x - m + kLift): at most 2^15 in fp16
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMergeThreads = 512;
@@ -348,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     const int sc0 = B * (HD / 2);
     const uint32_t ks_a = sc0 + place(16 * warp + g, HD / 16), ks_b = sc0 + place(16 * warp + g + 8, HD / 16);
     const uint32_t vs_a = sc0 + place(16 * warp + 2 * c, HD / 16), vs_b = sc0 + place(16 * warp + 2 * c + 8, HD / 16);
-    // byte picks: K scales of chunk pairs, each twice; V scales of tokens 2c (low) and 2c + 1
-    const uint32_t ksel = (c >> 1) ? 0x3311u : 0x2200u;
+    // byte picks: K scales of the chunks (dims 8c of each); V scales of tokens 2c, 2c + 1
+    const uint32_t ksel = (c >> 1) ? 0x7531u : 0x6420u;
     const uint32_t vsel = (g >> 2) ? 0x7351u : 0x6240u;
 
     uint32_t qf[C::NP][C::NCHUNK][4];     // per chunk: two k-steps of (b0, b1)
@@ -407,27 +421,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         if (nv > 0) {
             // ---- S^T = K Q^T ----
             float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            uint32_t ka[2], kb[2];                  // scale bytes of rows g, g + 8
+            uint32_t da, db;     // this lane's scale byte of every chunk, rows g and g + 8
             if constexpr (HD == 128) {
                 const uint2 ra = *reinterpret_cast<const uint2*>(sb + ks_a);
                 const uint2 rb = *reinterpret_cast<const uint2*>(sb + ks_b);
-                ka[0] = ra.x; ka[1] = ra.y; kb[0] = rb.x; kb[1] = rb.y;
+                da = __byte_perm(ra.x, ra.y, ksel);
+                db = __byte_perm(rb.x, rb.y, ksel);
             } else {
-                ka[0] = *reinterpret_cast<const uint32_t*>(sb + ks_a);
-                kb[0] = *reinterpret_cast<const uint32_t*>(sb + ks_b);
-                ka[1] = kb[1] = 0u;
+                da = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_a), 0u, ksel);
+                db = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_b), 0u, ksel);
             }
 #pragma unroll
             for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
                 uint32_t r[4];
                 ldsm4(smem_addr(sb) + ld_off + 2 * cp * B * 16, r);
-                const uint32_t da = __byte_perm(ka[cp], 0u, ksel), db = __byte_perm(kb[cp], 0u, ksel);
+                // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
+                const uint32_t pa = e4m3x2_to_f16x2(cp ? da >> 16 : da & 0xffffu);
+                const uint32_t pb = e4m3x2_to_f16x2(cp ? db >> 16 : db & 0xffffu);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int ch = 2 * cp + k;
                     const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
-                    const uint32_t fa = e4m3x2_to_f16x2(k ? da >> 16 : da & 0xffffu);
-                    const uint32_t fb = e4m3x2_to_f16x2(k ? db >> 16 : db & 0xffffu);
+                    const uint32_t fa = half_twice(pa, k), fb = half_twice(pb, k);
                     const uint32_t a00 = hmul2(e2m1x2_to_f16x2<0>(wa), fa), a01 = hmul2(e2m1x2_to_f16x2<0>(wb), fb);
                     const uint32_t a02 = hmul2(e2m1x2_to_f16x2<1>(wa), fa), a03 = hmul2(e2m1x2_to_f16x2<1>(wb), fb);
                     const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
@@ -439,15 +454,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     }
                 }
             }
-            // ---- running softmax: tokens g (x0, x1) and g + 8 (x2, x3), heads 2c and 2c + 1 ----
-            float x0 = (sa[0][0] + sa[1][0]) * qs0, x1 = (sa[0][1] + sa[1][1]) * qs1;
-            float x2 = (sa[0][2] + sa[1][2]) * qs0, x3 = (sa[0][3] + sa[1][3]) * qs1;
+            // ---- running softmax: tokens g (y0, y1) and g + 8 (y2, y3), heads 2c and 2c + 1;
+            // y = logit - (running max - kLift), log2 domain ----
+            const float z0 = sa[0][0] + sa[1][0], z1 = sa[0][1] + sa[1][1];
+            const float z2 = sa[0][2] + sa[1][2], z3 = sa[0][3] + sa[1][3];
+            float y0 = fmaf(z0, qs0, kLift - m0), y1 = fmaf(z1, qs1, kLift - m1);
+            float y2 = fmaf(z2, qs0, kLift - m0), y3 = fmaf(z3, qs1, kLift - m1);
             if (nv < 16) {
-                if (g >= nv) x0 = x1 = -INFINITY;
-                if (g + 8 >= nv) x2 = x3 = -INFINITY;
+                if (g >= nv) y0 = y1 = -INFINITY;
+                if (g + 8 >= nv) y2 = y3 = -INFINITY;
             }
-            float t0 = fmaxf(x0, x2), t1 = fmaxf(x1, x3);
-            if (__any_sync(0xffffffffu, t0 > m0 + kSlack || t1 > m1 + kSlack)) {
+            if (__any_sync(0xffffffffu, fmaxf(fmaxf(y0, y2), fmaxf(y1, y3)) > kSlack + kLift)) {
+                float t0 = fmaxf(g < nv ? z0 * qs0 : -INFINITY, g + 8 < nv ? z2 * qs0 : -INFINITY);
+                float t1 = fmaxf(g < nv ? z1 * qs1 : -INFINITY, g + 8 < nv ? z3 * qs1 : -INFINITY);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
@@ -466,9 +485,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     o[mt][2] *= r0;
                     o[mt][3] *= r1;
                 }
+                y0 = fmaf(z0, qs0, kLift - m0), y1 = fmaf(z1, qs1, kLift - m1);
+                y2 = fmaf(z2, qs0, kLift - m0), y3 = fmaf(z3, qs1, kLift - m1);
+                if (g >= nv) y0 = y1 = -INFINITY;
+                if (g + 8 >= nv) y2 = y3 = -INFINITY;
             }
-            const float p0 = fast_exp2(x0 - (m0 - kLift)), p1 = fast_exp2(x1 - (m1 - kLift));
-            const float p2 = fast_exp2(x2 - (m0 - kLift)), p3 = fast_exp2(x3 - (m1 - kLift));
+            const float p0 = fast_exp2(y0), p1 = fast_exp2(y1), p2 = fast_exp2(y2), p3 = fast_exp2(y3);
             l0 += p0 + p2;
             l1 += p1 + p3;
             uint32_t pb[C::NP][2];
@@ -514,15 +536,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
                     const uint32_t fa = e4m3x2_to_f16x2(k ? da >> 16 : da & 0xffffu);
                     const uint32_t fb = e4m3x2_to_f16x2(k ? db >> 16 : db & 0xffffu);
-                    // nibble pairs (token 2c low, 2c + 1 high): dims 0, 2 and 1, 3 of the four
-                    const uint32_t ea = (wa & 0x0f0fu) | ((wa >> 12) & 0xf0f0u);
-                    const uint32_t eb = (wb & 0x0f0fu) | ((wb >> 12) & 0xf0f0u);
-                    const uint32_t oa = ((wa >> 4) & 0x0f0fu) | ((wa >> 16) & 0xf0f0u);
-                    const uint32_t ob = ((wb >> 4) & 0x0f0fu) | ((wb >> 16) & 0xf0f0u);
-                    const uint32_t e0 = hmul2(e2m1x2_to_f16x2<0>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<1>(ea), fa);
-                    const uint32_t e2 = hmul2(e2m1x2_to_f16x2<0>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<1>(eb), fb);
-                    const uint32_t d0 = hmul2(e2m1x2_to_f16x2<0>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<1>(oa), fa);
-                    const uint32_t d2 = hmul2(e2m1x2_to_f16x2<0>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<1>(ob), fb);
+                    // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
+                    // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
+                    // room, the logic pipe that also converts has not).
+                    const uint32_t ea = bitselect(wa * p.two16, wa * p.two4, 0x0f0f0f0fu);
+                    const uint32_t eb = bitselect(wb * p.two16, wb * p.two4, 0x0f0f0f0fu);
+                    const uint32_t oa = bitselect(wa * p.two12, wa, 0x0f0f0f0fu);
+                    const uint32_t ob = bitselect(wb * p.two12, wb, 0x0f0f0f0fu);
+                    const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
+                    const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
+                    const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
+                    const uint32_t d2 = hmul2(e2m1x2_to_f16x2<2>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<3>(ob), fb);
 #pragma unroll
                     for (int t = 0; t < C::NP; ++t) {
                         mma_f16(o[2 * ch], e0, e1, e2, e3, pb[t][0], pb[t][1]);
@@ -685,6 +709,9 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     }
     DecodeFp4Params p = p0;
     p.workers = workers[dev];
+    p.two4 = 1u << 4;
+    p.two12 = 1u << 12;
+    p.two16 = 1u << 16;
     const int grid = p.max_workers < p.workers ? p.max_workers : p.workers;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -26,6 +26,7 @@ struct DecodeFp4Params {
     int max_workers;       // workers that can have work, by max_context_len
     float qk_scale_log2;   // scale * log2(e) * kv_scale
     float out_scale;       // kv_scale
+    uint32_t two4, two12, two16;   // 2^4, 2^12, 2^16: shifts as products (decode_fp4.cu)
 };
 
 // Workers that can have work over contexts up to max_ctx: bounds grid and workspace.
