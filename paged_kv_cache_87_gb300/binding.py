@@ -178,14 +178,22 @@ def _cache_type(cache: torch.Tensor) -> tuple:
 
 
 def _stream_ptr(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:   # the handle itself: building a Stream object costs 2.8 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream)
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     return t
+
+
+def _contiguous(*tensors) -> None:
+    for t in tensors:
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError(f"a contiguous CUDA tensor is needed, not {tuple(t.shape)} "
+                             f"strides {t.stride()} on {t.device}")
 
 
 # ------------------------------------------------------------------ calls --
@@ -445,88 +453,92 @@ def pkv_gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     4-bit ones become values in any of float32, float16 and bfloat16.  Rows outside every
     sequence's range are left as they were (in outputs allocated here: uninitialised).
     """
-    NB, Hkv, B, _ = k_cache.shape
+    NB, Hkv, B, _ = shape = k_cache.shape
     kc, d = _cache_type(k_cache)
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must have one shape and type")
-    if block_tables.dtype != torch.int32 or row_start.dtype != torch.int32 or \
-            (token_start is not None and token_start.dtype != torch.int32):
-        raise ValueError("block_tables, row_start and token_start must be int32")
     S, max_blocks = block_tables.shape
-    if row_start.shape != (S + 1,) or (token_start is not None and token_start.shape != (S,)):
-        raise ValueError("row_start must have num_seqs + 1 entries, token_start num_seqs")
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_tables, "block_tables"),
-                 (row_start, "row_start")):
-        _cuda(t, n)
+    if block_tables.dtype != torch.int32 or row_start.dtype != torch.int32 or \
+            row_start.shape != (S + 1,):
+        raise ValueError("block_tables must be int32 [S, max_blocks], row_start int32 [S + 1]")
+    _contiguous(k_cache, v_cache, block_tables, row_start)
+    first = None
     if token_start is not None:
-        _cuda(token_start, "token_start")
-    shape = (int(total_rows), Hkv, d)
+        if token_start.dtype != torch.int32 or token_start.shape != (S,):
+            raise ValueError("token_start must be int32 [S]")
+        _contiguous(token_start)
+        first = token_start.data_ptr()
+    rows = (total_rows, Hkv, d)
     if key_out is None:
-        key_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+        key_out = torch.empty(rows, dtype=out_dtype, device=k_cache.device)
+    elif key_out.shape != rows or key_out.dtype != out_dtype:
+        raise ValueError(f"key_out must be {list(rows)} of {out_dtype}")
+    else:
+        _contiguous(key_out)
     if value_out is None:
-        value_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
-    for t, n in ((key_out, "key_out"), (value_out, "value_out")):
-        _cuda(t, n)
-        if t.shape != shape or t.dtype != out_dtype:
-            raise ValueError(f"{n} must be {list(shape)} of {out_dtype}")
-    st = load().pkv_gather_cache(
+        value_out = torch.empty_like(key_out)
+    elif value_out.shape != rows or value_out.dtype != out_dtype:
+        raise ValueError(f"value_out must be {list(rows)} of {out_dtype}")
+    else:
+        _contiguous(value_out)
+    st = (_lib or load()).pkv_gather_cache(
         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), row_start.data_ptr(),
-        None if token_start is None else token_start.data_ptr(), S, shape[0], Hkv, d, B, NB,
-        max_blocks, kc, float(kv_scale), _TORCH_CODES[out_dtype], key_out.data_ptr(),
-        value_out.data_ptr(), _stream_ptr(stream))
-    _check("pkv_gather_cache", st)
+        first, S, total_rows, Hkv, d, B, NB, max_blocks, kc, kv_scale, _TORCH_CODES[out_dtype],
+        key_out.data_ptr(), value_out.data_ptr(), _stream_ptr(stream))
+    if st:
+        raise PagedKVError("pkv_gather_cache", st)
     return key_out, value_out
 
 
 # ---------------------------------------------------------- norm + rotary --
 
-def _head_rows(t: torch.Tensor, name: str) -> int:
+def _head_rows(t: torch.Tensor, d: int, heads: int) -> int:
     """The token stride of a CUDA tensor [T, heads, d] whose tokens' heads are contiguous."""
-    _, h, d = t.shape
-    s = t.stride()
-    if not t.is_cuda or (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-        raise ValueError(f"{name} must be a CUDA tensor [T, heads, d], heads contiguous")
-    return s[0] if t.shape[0] > 1 else h * d
+    s0, s1, s2 = t.stride()
+    if not t.is_cuda or s2 != 1 or (s1 != d and heads > 1):
+        raise ValueError("rows must be CUDA tensors [T, heads, d] with their heads contiguous")
+    return s0 if t.shape[0] > 1 else heads * d
 
 
-def _norm_rope_args(query, key, cos_sin, positions, q_weight, k_weight, eps, interleaved, q_out,
-                    value=None):
-    """Checks shared by the two entry points: (arguments up to dtype, in two parts around
-    value's, query's outputs)."""
+def _norm_rope_args(query, key, value, cos_sin, positions, q_weight, k_weight, eps, interleaved,
+                    q_out):
+    """Checks shared by the two entry points: (the C arguments up to q_out's stride, q_out).
+    ``value``: the C arguments of the values, [] without them."""
     T, Hq, d = query.shape
-    Hkv = key.shape[1]
-    if key.shape != (T, Hkv, d) or key.dtype != query.dtype:
+    Tk, Hkv, dk = key.shape
+    dtype = query.dtype
+    if Tk != T or dk != d or key.dtype != dtype:
         raise ValueError("query [T, Hq, d] and key [T, Hkv, d] must agree in T, d and type")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
     if positions.dtype != torch.int64 or positions.shape != (T,):
         raise ValueError("positions must be int64 [T]")
-    _cuda(cos_sin, "cos_sin")
-    _cuda(positions, "positions")
-    wc = PKV_F32
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _cuda(w, n)
-            if w.shape != (d,):
-                raise ValueError(f"{n} must be [head_dim]")
-            wc = _TORCH_CODES[w.dtype]
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must have one type")
+    _contiguous(cos_sin, positions)
+    wc, qw, kw = PKV_F32, None, None
+    if q_weight is not None:
+        qw, wc = q_weight.data_ptr(), _TORCH_CODES[q_weight.dtype]
+        if q_weight.shape != (d,):
+            raise ValueError("q_weight must be [head_dim]")
+        _contiguous(q_weight)
+    if k_weight is not None:
+        kw, wc = k_weight.data_ptr(), _TORCH_CODES[k_weight.dtype]
+        if k_weight.shape != (d,):
+            raise ValueError("k_weight must be [head_dim]")
+        if q_weight is not None and k_weight.dtype != q_weight.dtype:
+            raise ValueError("q_weight and k_weight must have one type")
+        _contiguous(k_weight)
+    q_stride, k_stride = _head_rows(query, d, Hq), _head_rows(key, d, Hkv)
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=query.dtype, device=query.device)
-    elif q_out.shape != query.shape or q_out.dtype != query.dtype:
+        q_out, out_stride = torch.empty((T, Hq, d), dtype=dtype, device=query.device), Hq * d
+    elif q_out.shape != query.shape or q_out.dtype != dtype:
         raise ValueError("q_out must have query's shape and type")
-    head = [query.data_ptr(), _head_rows(query, "query"), key.data_ptr(), _head_rows(key, "key")]
-    if value is not None:
-        if value.shape != key.shape or value.dtype != key.dtype:
-            raise ValueError("value must have key's shape and type")
-        head += [value.data_ptr(), _head_rows(value, "value")]
-    head += [None if q_weight is None else q_weight.data_ptr(),
-             None if k_weight is None else k_weight.data_ptr(), wc, float(eps),
-             cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-             positions.data_ptr(), T, Hq, Hkv, d, _TORCH_CODES[query.dtype], q_out.data_ptr(),
-             _head_rows(q_out, "q_out")]
-    return head, q_out
+    else:
+        out_stride = _head_rows(q_out, d, Hq)
+    max_position, rot_dim = cos_sin.shape
+    return (query.data_ptr(), q_stride, key.data_ptr(), k_stride, *value, qw, kw, wc, eps,
+            cos_sin.data_ptr(), max_position, rot_dim, 1 if interleaved else 0,
+            positions.data_ptr(), T, Hq, Hkv, d, _TORCH_CODES[dtype], q_out.data_ptr(),
+            out_stride), q_out
 
 
 def pkv_qk_norm_rope(query: torch.Tensor, key: torch.Tensor, cos_sin: torch.Tensor,
@@ -542,14 +554,18 @@ def pkv_qk_norm_rope(query: torch.Tensor, key: torch.Tensor, cos_sin: torch.Tens
     sines; positions int64 [T].  ``interleaved`` rotates dims (2i, 2i + 1) instead of
     (i, i + rot_dim / 2).  q_out / k_out may be query / key themselves (in place).
     """
-    head, q_out = _norm_rope_args(query, key, cos_sin, positions, q_weight, k_weight, eps,
+    args, q_out = _norm_rope_args(query, key, (), cos_sin, positions, q_weight, k_weight, eps,
                                   interleaved, q_out)
+    T, Hkv, d = shape = key.shape
     if k_out is None:
-        k_out = torch.empty(key.shape, dtype=key.dtype, device=key.device)
-    elif k_out.shape != key.shape or k_out.dtype != key.dtype:
+        k_out, k_stride = torch.empty(shape, dtype=key.dtype, device=key.device), Hkv * d
+    elif k_out.shape != shape or k_out.dtype != key.dtype:
         raise ValueError("k_out must have key's shape and type")
-    _check("pkv_qk_norm_rope", load().pkv_qk_norm_rope(
-        *head, k_out.data_ptr(), _head_rows(k_out, "k_out"), _stream_ptr(stream)))
+    else:
+        k_stride = _head_rows(k_out, d, Hkv)
+    st = (_lib or load()).pkv_qk_norm_rope(*args, k_out.data_ptr(), k_stride, _stream_ptr(stream))
+    if st:
+        raise PagedKVError("pkv_qk_norm_rope", st)
     return q_out, k_out
 
 
@@ -563,20 +579,23 @@ def pkv_qk_norm_rope_and_cache(query: torch.Tensor, key: torch.Tensor, value: to
     """pkv_qk_norm_rope whose keys, with ``value`` [T, Hkv, d], go into the paged cache at
     slot_mapping (int64 [T], negative: not written); returns q_out.  The cache, of any type,
     holds the same bits as after pkv_qk_norm_rope and pkv_reshape_and_cache of its keys."""
-    NB, Hkv, B, _ = k_cache.shape
+    NB, Hkv, B, _ = shape = k_cache.shape
     kc, d = _cache_type(k_cache)
-    if (Hkv, d) != tuple(key.shape[1:]) or v_cache.shape != k_cache.shape or \
-            v_cache.dtype != k_cache.dtype:
+    rows = key.shape
+    if rows[1] != Hkv or rows[2] != d or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("key [T, Hkv, d] does not match the caches [NB, Hkv, B, d]")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (key.shape[0],):
+    if value.shape != rows or value.dtype != key.dtype:
+        raise ValueError("value must have key's shape and type")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (rows[0],):
         raise ValueError("slot_mapping must be int64 [T]")
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (slot_mapping, "slot_mapping")):
-        _cuda(t, n)
-    head, q_out = _norm_rope_args(query, key, cos_sin, positions, q_weight, k_weight, eps,
-                                  interleaved, q_out, value)
-    _check("pkv_qk_norm_rope_and_cache", load().pkv_qk_norm_rope_and_cache(
-        *head, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), B, NB, kc,
-        float(kv_scale), _stream_ptr(stream)))
+    _contiguous(k_cache, v_cache, slot_mapping)
+    args, q_out = _norm_rope_args(query, key, (value.data_ptr(), _head_rows(value, d, Hkv)),
+                                  cos_sin, positions, q_weight, k_weight, eps, interleaved, q_out)
+    st = (_lib or load()).pkv_qk_norm_rope_and_cache(
+        *args, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), B, NB, kc,
+        kv_scale, _stream_ptr(stream))
+    if st:
+        raise PagedKVError("pkv_qk_norm_rope_and_cache", st)
     return q_out
 
 
