@@ -93,41 +93,53 @@ __global__ void __launch_bounds__(256) reshape_and_cache_kernel(ReshapeParams p)
     }
 }
 
-// Into the 4-bit cache: one lane = eight dims of one (token, kv head) row, K and V; a pair
-// of lanes shares a 16-dim group's scale.  Whole warps run each iteration together (the
-// group's maximum is exchanged by a shuffle).
-template <typename ST>
-__global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(ReshapeParams p) {
+// Into the 4-bit cache.  A lane holds eight dims of a (token, kv head) row; a pair of lanes
+// shares a 16-dim group's scale (a shuffle, so whole warps run together).  A warp takes
+// kWriteRows rows a lane group, K heads then V heads of one token, all loads in flight at once.
+constexpr int kWriteRows = 4;
+
+template <typename ST, int HD>
+__global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(ReshapeParams p, int warps,
+                                                                    int log_block) {
     pdl_launch_dependents();   // the decode launched next may start its launch now
-    const int lanes = p.head_dim / 8;                  // lanes of a row
-    const int64_t total = (int64_t)p.num_tokens * p.num_kv_heads * lanes;
-    const int64_t pool_slots = (int64_t)p.num_blocks * p.block_size;
-    const int64_t tile_bytes = (int64_t)p.block_size * (p.head_dim / 2 + p.head_dim / 16);
-    const int lane = threadIdx.x & 31;
-    for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + (threadIdx.x - lane); i0 < total;
-         i0 += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t idx = i0 + lane;
-        const bool in = idx < total;
-        const int j = (int)(idx % lanes);
-        const int64_t th = idx / lanes;
-        const int h = (int)(th % p.num_kv_heads);
-        const int64_t t = th / p.num_kv_heads;
-        const int64_t slot = in ? p.slot_mapping[t] : -1;
-        if (slot >= pool_slots && j == 0 && h == 0) set_status(p.status, PKV_DEV_BAD_SLOT);
-        const bool live = slot >= 0 && slot < pool_slots;
-        float k[8] = {0.f}, v[8] = {0.f};
-        if (live) {
-            const int64_t src = (th * p.head_dim + 8 * j) * ST::bytes;
-            load8<ST>(static_cast<const uint8_t*>(p.key) + src, k);
-            load8<ST>(static_cast<const uint8_t*>(p.value) + src, v);
+    constexpr int LPR = HD / 8, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, j = lane % LPR, rows = 2 * p.num_kv_heads;
+    const int tpc = max(1, (int)(blockDim.x / 32) / warps);         // tokens of the CTA
+    const int64_t t = (int64_t)blockIdx.x * tpc + (threadIdx.x >> 5) / warps;
+    if (t >= p.num_tokens) return;
+    const int64_t slot = p.slot_mapping[t];
+    const bool live = slot >= 0 && (slot >> log_block) < p.num_blocks;
+    for (int r0 = (threadIdx.x >> 5) % warps * (RPW * kWriteRows); r0 < rows;
+         r0 += blockDim.x / 32 * (RPW * kWriteRows)) {
+        float x[kWriteRows][8];
+#pragma unroll
+        for (int u = 0; u < kWriteRows; ++u) {
+            const int r = r0 + u * RPW + lane / LPR;
+            if (r < rows && live) {
+                const bool v = r >= p.num_kv_heads;
+                const int64_t row = t * p.num_kv_heads + (v ? r - p.num_kv_heads : r);
+                load8<ST>(static_cast<const uint8_t*>(v ? p.value : p.key) +
+                              (row * HD + 8 * j) * ST::bytes, x[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+            }
         }
-        const int64_t blk = live ? slot / p.block_size : 0;
-        const int row = live ? (int)(slot % p.block_size) : 0;
-        const int64_t tile = (blk * p.num_kv_heads + h) * tile_bytes;
-        CacheRow<E2M1>::store(static_cast<uint8_t*>(p.k_cache) + tile, p.block_size, p.head_dim,
-                              row, j, k, p.kv_scale, live);
-        CacheRow<E2M1>::store(static_cast<uint8_t*>(p.v_cache) + tile, p.block_size, p.head_dim,
-                              row, j, v, p.kv_scale, live);
+        if (!live) {
+            if (slot >= 0 && r0 == 0 && lane == 0) set_status(p.status, PKV_DEV_BAD_SLOT);
+            return;
+        }
+        const int64_t blk = slot >> log_block;
+        const int row = (int)(slot & ((1 << log_block) - 1));
+#pragma unroll
+        for (int u = 0; u < kWriteRows; ++u) {
+            const int r = r0 + u * RPW + lane / LPR;
+            const bool v = r >= p.num_kv_heads;
+            const int64_t tile = (blk * p.num_kv_heads + (v ? r - p.num_kv_heads : r)) *
+                                 (int64_t)(p.block_size * cache_row_bytes_of<E2M1>(HD));
+            CacheRow<E2M1>::store(static_cast<uint8_t*>(v ? p.v_cache : p.k_cache) + tile,
+                                  p.block_size, HD, row, j, x[u], p.kv_scale, r < rows);
+        }
     }
 }
 
@@ -178,18 +190,24 @@ cudaError_t launch_reshape_and_cache(const ReshapeParams& p, pkv_dtype src, bool
     return cudaGetLastError();
 }
 
-cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src, int num_sms,
-                                         cudaStream_t stream) {
-    const int64_t total = (int64_t)p.num_tokens * p.num_kv_heads * (p.head_dim / 8);
-    const int64_t want = (total + 255) / 256, cap = (int64_t)num_sms * 8;
-    const int grid = (int)(want < cap ? want : cap);
-    switch (src) {
-    case PKV_F32: reshape_and_cache_fp4_kernel<F32><<<grid, 256, 0, stream>>>(p); break;
-    case PKV_F16: reshape_and_cache_fp4_kernel<F16><<<grid, 256, 0, stream>>>(p); break;
-    case PKV_BF16: reshape_and_cache_fp4_kernel<BF16><<<grid, 256, 0, stream>>>(p); break;
-    default: return cudaErrorInvalidValue;
-    }
+template <typename ST>
+static cudaError_t launch_write_fp4(const ReshapeParams& p, cudaStream_t stream) {
+    const int per_warp = 256 / p.head_dim * kWriteRows;
+    const int need = (2 * p.num_kv_heads + per_warp - 1) / per_warp;   // warps of a token
+    const int warps = need < 8 ? need : 8, tpc = 8 / warps;
+    const int log_block = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
+    const unsigned grid = (unsigned)((p.num_tokens + tpc - 1) / tpc);
+    if (p.head_dim == 128)
+        reshape_and_cache_fp4_kernel<ST, 128><<<grid, 32 * warps * tpc, 0, stream>>>(p, warps, log_block);
+    else
+        reshape_and_cache_fp4_kernel<ST, 64><<<grid, 32 * warps * tpc, 0, stream>>>(p, warps, log_block);
     return cudaGetLastError();
+}
+
+cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src,
+                                         cudaStream_t stream) {
+    if (src == PKV_F32) return launch_write_fp4<F32>(p, stream);
+    return src == PKV_F16 ? launch_write_fp4<F16>(p, stream) : launch_write_fp4<BF16>(p, stream);
 }
 
 cudaError_t launch_copy_blocks(const CopyParams& p, int num_pairs, cudaStream_t stream) {

@@ -138,10 +138,34 @@ struct CacheRow {
                                                  const float (&f)[8], float, bool live) {
         if (live) store8<KT>(tile + ((int64_t)row * d + 8 * j) * KT::bytes, f);
     }
-    // the stored values, before kv_scale
-    __device__ __forceinline__ static void load(const uint8_t* tile, int B, int d, int row, int j,
-                                                float (&f)[8]) {
-        load8<KT>(tile + ((int64_t)row * d + 8 * j) * KT::bytes, f);
+    // a quarter of a row: dims 32c + 8w .. + 7 of every 32-dim chunk c, as stored
+    template <int HD>
+    struct Raw {
+        uint4 x[HD / 32 * (KT::bytes == 4 ? 2 : 1)];
+    };
+    template <int HD>
+    __device__ __forceinline__ static void fetch(const uint8_t* tile, int B, int row, int w,
+                                                 Raw<HD>& r) {
+        const uint4* s = reinterpret_cast<const uint4*>(tile + ((int64_t)row * HD + 8 * w) * KT::bytes);
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) {
+            if constexpr (KT::bytes == 4) {
+                r.x[2 * c] = s[8 * c];
+                r.x[2 * c + 1] = s[8 * c + 1];
+            } else {
+                r.x[c] = s[4 * c];
+            }
+        }
+    }
+    // chunk c's eight values, before kv_scale
+    template <int HD>
+    __device__ __forceinline__ static void values(const Raw<HD>& r, int c, int, float (&f)[8]) {
+        if constexpr (KT::bytes == 4) {
+            Chunk<KT>::to_float(r.x[2 * c], f);
+            Chunk<KT>::to_float(r.x[2 * c + 1], f + 4);
+        } else {
+            Chunk<KT>::to_float(r.x[c], f);
+        }
     }
 };
 
@@ -157,10 +181,20 @@ struct CacheRow<E4M3> {
                                __fdiv_rn(f[4 * i + 3], kv_scale)) << 16);
         if (live) *reinterpret_cast<uint2*>(tile + (int64_t)row * d + 8 * j) = make_uint2(w[0], w[1]);
     }
-    __device__ __forceinline__ static void load(const uint8_t* tile, int B, int d, int row, int j,
-                                                float (&f)[8]) {
-        const uint2 r = *reinterpret_cast<const uint2*>(tile + (int64_t)row * d + 8 * j);
-        const uint32_t w[2] = {r.x, r.y};
+    template <int HD>
+    struct Raw {
+        uint2 x[HD / 32];
+    };
+    template <int HD>
+    __device__ __forceinline__ static void fetch(const uint8_t* tile, int B, int row, int w,
+                                                 Raw<HD>& r) {
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c)
+            r.x[c] = *reinterpret_cast<const uint2*>(tile + (int64_t)row * HD + 32 * c + 8 * w);
+    }
+    template <int HD>
+    __device__ __forceinline__ static void values(const Raw<HD>& r, int c, int, float (&f)[8]) {
+        const uint32_t w[2] = {r.x[c].x, r.x[c].y};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t h = e4m3x2_to_f16x2((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
@@ -190,22 +224,57 @@ struct CacheRow<E2M1> {
         const float step = __low2float(*reinterpret_cast<const __half2*>(&sh)) * kv_scale;
         uint32_t w = 0u;
         if (step > 0.f) {   // not for a scale of 0 or NaN: zero codes
+            // x / step, correctly rounded, from the correctly rounded reciprocal y: q = x y,
+            // r = q step - x (exact in a fused multiply-add), q - r y (P. Markstein, IBM J. Res.
+            // Dev. 34, 1990); with r of this sign a zero keeps its own.  Three operations instead
+            // of a division each; where a term could leave the normal range (a saturated group,
+            // far scales) the division.
+            const float y = __frcp_rn(step);
+            if (step > 0x1p-100f && step < 0x1p100f && amax * y < 0x1p20f) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w |= cvt_e2m1x2(__fdiv_rn(f[2 * i], step), __fdiv_rn(f[2 * i + 1], step)) << (8 * i);
+                for (int i = 0; i < 4; ++i) {
+                    const float q0 = f[2 * i] * y, q1 = f[2 * i + 1] * y;
+                    w |= cvt_e2m1x2(fmaf(-fmaf(q0, step, -f[2 * i]), y, q0),
+                                    fmaf(-fmaf(q1, step, -f[2 * i + 1]), y, q1)) << (8 * i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w |= cvt_e2m1x2(__fdiv_rn(f[2 * i], step), __fdiv_rn(f[2 * i + 1], step)) << (8 * i);
+            }
         }
         if (live) {
             *reinterpret_cast<uint32_t*>(tile + code_at(B, row, j)) = w;
             if ((j & 1) == 0) tile[scale_at(B, d, row, j)] = (uint8_t)sc;
         }
     }
-    __device__ __forceinline__ static void load(const uint8_t* tile, int B, int d, int row, int j,
-                                                float (&f)[8]) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + code_at(B, row, j));
-        const uint32_t sh = e4m3x2_to_f16x2(tile[scale_at(B, d, row, j)]);
+    template <int HD>
+    struct Raw {
+        uint32_t w[HD / 32], scales[HD / 64];       // this lane's words, the row's scales
+    };
+    template <int HD>
+    __device__ __forceinline__ static void fetch(const uint8_t* tile, int B, int row, int w,
+                                                 Raw<HD>& r) {
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c)
+            r.w[c] = *reinterpret_cast<const uint32_t*>(tile + (c * B + row) * 16 + 4 * w);
+        const uint8_t* s = tile + B * (HD / 2) + row * (HD / 16);
+        if constexpr (HD == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(s);
+            r.scales[0] = v.x;
+            r.scales[1] = v.y;
+        } else {
+            r.scales[0] = *reinterpret_cast<const uint32_t*>(s);
+        }
+    }
+    template <int HD>
+    __device__ __forceinline__ static void values(const Raw<HD>& r, int c, int w, float (&f)[8]) {
+        const int byte = 2 * c + (w >> 1);
+        const uint32_t sh = e4m3x2_to_f16x2((r.scales[c >> 1] >> (8 * (byte & 3))) & 0xffu);
         const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-        const uint32_t h[4] = {e2m1x2_to_f16x2<0>(w), e2m1x2_to_f16x2<1>(w),
-                               e2m1x2_to_f16x2<2>(w), e2m1x2_to_f16x2<3>(w)};
+        const uint32_t x = r.w[c];
+        const uint32_t h[4] = {e2m1x2_to_f16x2<0>(x), e2m1x2_to_f16x2<1>(x),
+                               e2m1x2_to_f16x2<2>(x), e2m1x2_to_f16x2<3>(x)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));

@@ -61,12 +61,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_cache_kernel(GatherPara
         const int row = (int)(place % B);
         const int64_t tile = (place / B * p.num_kv_heads + h) * tile_bytes;
         const int64_t dst = ((int64_t)(r0 + i) * p.num_kv_heads + h) * HD * OT::bytes;
+        typename CacheRow<KT>::template Raw<HD> rk, rv;       // every load first
+        CacheRow<KT>::template fetch<HD>(kc + tile, B, row, w, rk);
+        CacheRow<KT>::template fetch<HD>(vc + tile, B, row, w, rv);
 #pragma unroll
         for (int c = 0; c < HD / 32; ++c) {
             const int j = 4 * c + w;
             float k[8], v[8];
-            CacheRow<KT>::load(kc + tile, B, HD, row, j, k);
-            CacheRow<KT>::load(vc + tile, B, HD, row, j, v);
+            CacheRow<KT>::template values<HD>(rk, c, w, k);
+            CacheRow<KT>::template values<HD>(rv, c, w, v);
             if constexpr (is_quantised<KT>()) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {

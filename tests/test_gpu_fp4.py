@@ -90,6 +90,41 @@ def test_write_edges_bit_exact():
         assert (got.cpu().numpy() == want).all() and torch.equal(got, other)
 
 
+@pytest.mark.parametrize("src,kv", [("f32", 0.37), ("bf16", 1.0), ("f32", 1e30), ("f16", 3e-36)])
+def test_write_rounds_true_quotients(src, kv):
+    """Four million codes against IEEE divisions: groups of every magnitude, values on and next
+    to the codes' borders for the group's own step."""
+    g = torch.Generator("cuda").manual_seed(3)
+    T, h, d, B = 4096, 8, 128, 16
+    x = torch.randn(T, h, d // 16, 16, generator=g, device="cuda")
+    x = x * 2.0 ** torch.randint(-6, 7, (T, h, d // 16, 1), generator=g, device="cuda") * min(kv, 1e28)
+    kvt = torch.tensor(kv, device="cuda")
+
+    def step_of(x):
+        s = (x.abs().amax(-1) / (6 * kvt)).clamp(max=448.0).to(torch.float8_e4m3fn)
+        return s, (s.float() * kvt).unsqueeze(-1)
+
+    x = x.to(DT[src]).float()
+    border = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    near = step_of(x)[1] * border * (1 + torch.randint(-2, 3, (T, h, d // 16, 7), generator=g, device="cuda") * 2.0 ** -23)
+    x[..., 4:11] = torch.minimum(near, x[..., :4].abs().amax(-1, keepdim=True)) * torch.sign(x[..., 4:11])
+    x = x.to(DT[src])
+    s, step = step_of(x.float())
+    q = torch.where(step > 0, x.float() / step, torch.zeros_like(step))
+    m = q.abs()
+    code = (m > .25).int() + (m >= .75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5)
+    code = torch.where(step > 0, code + 8 * torch.signbit(q), 0)
+    c = torch.zeros(fp4.cache_shape(T // B, h, B, d), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(c)
+    x = x.flatten(2)
+    binding.pkv_reshape_and_cache(x, x, c, v, torch.arange(T, device="cuda"), kv_scale=kv)
+    flat = c.view(T // B, h, -1)
+    body = flat[..., :B * d // 2].view(T // B, h, d // 32, B, 16).permute(0, 3, 1, 2, 4).reshape(T, h, d // 2)
+    assert torch.equal(torch.stack([body & 15, body >> 4], -1).flatten(-2).int(), code.flatten(2).int())
+    sc = flat[..., B * d // 2:].view(T // B, h, B, d // 16).transpose(1, 2).reshape(T, h, -1)
+    assert torch.equal(sc, s.view(torch.uint8)) and torch.equal(c, v)
+
+
 def test_write_flags_slots_outside_and_leaves_the_rest():
     h, d, B, nb = 2, 64, 16, 3
     x = torch.randn(4, h, d, device="cuda")
