@@ -340,7 +340,7 @@ pkv_status pkv_reshape_and_cache(const void* key, const void* value, void* k_cac
     ReshapeParams p{key, value, k_cache, v_cache, slot_mapping, dev->status, num_tokens,
                     num_kv_heads, head_dim, block_size, num_blocks, kv_scale};
     if (kv_dtype == PKV_FP4_E2M1)
-        return cuda_status(launch_reshape_and_cache_fp4(p, src_dtype,
+        return cuda_status(launch_reshape_and_cache_fp4(p, src_dtype, dev->num_sms,
                                                         reinterpret_cast<cudaStream_t>(stream)));
     return cuda_status(launch_reshape_and_cache(p, src_dtype, quant, dev->num_sms,
                                                 reinterpret_cast<cudaStream_t>(stream)));

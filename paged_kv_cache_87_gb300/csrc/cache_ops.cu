@@ -94,52 +94,68 @@ __global__ void __launch_bounds__(256) reshape_and_cache_kernel(ReshapeParams p)
 }
 
 // Into the 4-bit cache.  A lane holds eight dims of a (token, kv head) row; a pair of lanes
-// shares a 16-dim group's scale (a shuffle, so whole warps run together).  A warp takes
-// kWriteRows rows a lane group, K heads then V heads of one token, all loads in flight at once.
+// shares a 16-dim group's scale (a shuffle, so whole warps run together).  A warp keeps its piece
+// of a token -- kWriteRows rows a lane group of K or of V -- and walks the tokens with the next
+// token's rows and slot loading while it quantises this one's.
 constexpr int kWriteRows = 4;
+constexpr int kWriteThreads = 256;
+constexpr int kWriteCtas = 3;    // a SM's share of the grid: resident at its registers
 
 template <typename ST, int HD>
-__global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(ReshapeParams p, int warps,
-                                                                    int log_block) {
+__global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_fp4_kernel(ReshapeParams p,
+                                                                              int log_block) {
     pdl_launch_dependents();   // the decode launched next may start its launch now
-    constexpr int LPR = HD / 8, RPW = 32 / LPR;
-    const int lane = threadIdx.x & 31, j = lane % LPR, rows = 2 * p.num_kv_heads;
-    const int tpc = max(1, (int)(blockDim.x / 32) / warps);         // tokens of the CTA
-    const int64_t t = (int64_t)blockIdx.x * tpc + (threadIdx.x >> 5) / warps;
-    if (t >= p.num_tokens) return;
-    const int64_t slot = p.slot_mapping[t];
-    const bool live = slot >= 0 && (slot >> log_block) < p.num_blocks;
-    for (int r0 = (threadIdx.x >> 5) % warps * (RPW * kWriteRows); r0 < rows;
-         r0 += blockDim.x / 32 * (RPW * kWriteRows)) {
-        float x[kWriteRows][8];
+    constexpr int LPR = HD / 8, RPW = 32 / LPR, STEP = RPW * kWriteRows;
+    constexpr int TILE_ROW = cache_row_bytes_of<E2M1>(HD), N16 = ST::bytes / 2;
+    const int lane = threadIdx.x & 31, j = lane % LPR;
+    const int half = (p.num_kv_heads + STEP - 1) / STEP;         // pieces of K; as many of V
+    const int gw = blockIdx.x * (kWriteThreads / 32) + (threadIdx.x >> 5);
+    const int step = gridDim.x * (kWriteThreads / 32) / (2 * half);
+    int64_t t = gw / (2 * half);
+    if (t >= step || t >= p.num_tokens) return;
+    const int piece = gw % (2 * half);
+    const bool v = piece >= half;
+    const int h0 = (piece - (v ? half : 0)) * STEP + lane / LPR;
+    const uint8_t* src = static_cast<const uint8_t*>(v ? p.value : p.key) + (h0 * HD + 8 * j) * ST::bytes;
+    uint8_t* pool = static_cast<uint8_t*>(v ? p.v_cache : p.k_cache);
+    const int tile_bytes = p.block_size * TILE_ROW;
+    const int64_t src_step = (int64_t)p.num_kv_heads * HD * ST::bytes;
+    uint4 now[kWriteRows][N16], next[kWriteRows][N16];
+    auto fetch = [&](uint4 (&x)[kWriteRows][N16], int64_t at) {
+        const uint4* row = reinterpret_cast<const uint4*>(src + at * src_step);
 #pragma unroll
-        for (int u = 0; u < kWriteRows; ++u) {
-            const int r = r0 + u * RPW + lane / LPR;
-            if (r < rows && live) {
-                const bool v = r >= p.num_kv_heads;
-                const int64_t row = t * p.num_kv_heads + (v ? r - p.num_kv_heads : r);
-                load8<ST>(static_cast<const uint8_t*>(v ? p.value : p.key) +
-                              (row * HD + 8 * j) * ST::bytes, x[u]);
-            } else {
+        for (int u = 0; u < kWriteRows; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-            }
-        }
-        if (!live) {
-            if (slot >= 0 && r0 == 0 && lane == 0) set_status(p.status, PKV_DEV_BAD_SLOT);
-            return;
+            for (int i = 0; i < N16; ++i)
+                x[u][i] = h0 + u * RPW < p.num_kv_heads ? row[u * (RPW * HD * ST::bytes / 16) + i]
+                                                        : make_uint4(0u, 0u, 0u, 0u);
+    };
+    fetch(now, t);
+    int64_t slot = p.slot_mapping[t], slot_next = -1;
+    for (; t < p.num_tokens; t += step) {
+        if (t + step < p.num_tokens) {
+            fetch(next, t + step);
+            slot_next = p.slot_mapping[t + step];
         }
         const int64_t blk = slot >> log_block;
-        const int row = (int)(slot & ((1 << log_block) - 1));
+        if (slot >= 0 && blk < p.num_blocks) {                   // the whole warp: one token
+            const int row = (int)(slot & ((1 << log_block) - 1));
+            uint8_t* tile = pool + (blk * p.num_kv_heads + h0) * tile_bytes;
 #pragma unroll
-        for (int u = 0; u < kWriteRows; ++u) {
-            const int r = r0 + u * RPW + lane / LPR;
-            const bool v = r >= p.num_kv_heads;
-            const int64_t tile = (blk * p.num_kv_heads + (v ? r - p.num_kv_heads : r)) *
-                                 (int64_t)(p.block_size * cache_row_bytes_of<E2M1>(HD));
-            CacheRow<E2M1>::store(static_cast<uint8_t*>(v ? p.v_cache : p.k_cache) + tile,
-                                  p.block_size, HD, row, j, x[u], p.kv_scale, r < rows);
+            for (int u = 0; u < kWriteRows; ++u) {
+                float x[8];
+                load8<ST>(now[u], x);
+                CacheRow<E2M1>::store(tile + u * RPW * tile_bytes, p.block_size, HD, row, j, x,
+                                      p.kv_scale, h0 + u * RPW < p.num_kv_heads);
+            }
+        } else if (slot >= 0 && piece == 0 && lane == 0) {
+            set_status(p.status, PKV_DEV_BAD_SLOT);
         }
+        slot = slot_next;
+#pragma unroll
+        for (int u = 0; u < kWriteRows; ++u)
+#pragma unroll
+            for (int i = 0; i < N16; ++i) now[u][i] = next[u][i];
     }
 }
 
@@ -191,23 +207,25 @@ cudaError_t launch_reshape_and_cache(const ReshapeParams& p, pkv_dtype src, bool
 }
 
 template <typename ST>
-static cudaError_t launch_write_fp4(const ReshapeParams& p, cudaStream_t stream) {
-    const int per_warp = 256 / p.head_dim * kWriteRows;
-    const int need = (2 * p.num_kv_heads + per_warp - 1) / per_warp;   // warps of a token
-    const int warps = need < 8 ? need : 8, tpc = 8 / warps;
+static cudaError_t launch_write_fp4(const ReshapeParams& p, int num_sms, cudaStream_t stream) {
+    const int step = 256 / p.head_dim * kWriteRows;
+    const int64_t pieces = 2 * (int64_t)((p.num_kv_heads + step - 1) / step);
+    const int64_t least = (pieces + 7) / 8, need = (p.num_tokens * pieces + 7) / 8;
+    const int64_t full = (int64_t)num_sms * kWriteCtas, most = full > least ? full : least;
+    const unsigned grid = (unsigned)(need < most ? need : most);
     const int log_block = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
-    const unsigned grid = (unsigned)((p.num_tokens + tpc - 1) / tpc);
     if (p.head_dim == 128)
-        reshape_and_cache_fp4_kernel<ST, 128><<<grid, 32 * warps * tpc, 0, stream>>>(p, warps, log_block);
+        reshape_and_cache_fp4_kernel<ST, 128><<<grid, kWriteThreads, 0, stream>>>(p, log_block);
     else
-        reshape_and_cache_fp4_kernel<ST, 64><<<grid, 32 * warps * tpc, 0, stream>>>(p, warps, log_block);
+        reshape_and_cache_fp4_kernel<ST, 64><<<grid, kWriteThreads, 0, stream>>>(p, log_block);
     return cudaGetLastError();
 }
 
-cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src,
+cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src, int num_sms,
                                          cudaStream_t stream) {
-    if (src == PKV_F32) return launch_write_fp4<F32>(p, stream);
-    return src == PKV_F16 ? launch_write_fp4<F16>(p, stream) : launch_write_fp4<BF16>(p, stream);
+    if (src == PKV_F32) return launch_write_fp4<F32>(p, num_sms, stream);
+    return src == PKV_F16 ? launch_write_fp4<F16>(p, num_sms, stream)
+                          : launch_write_fp4<BF16>(p, num_sms, stream);
 }
 
 cudaError_t launch_copy_blocks(const CopyParams& p, int num_pairs, cudaStream_t stream) {

@@ -29,7 +29,7 @@ struct CopyParams {
 
 cudaError_t launch_reshape_and_cache(const ReshapeParams& p, pkv_dtype src, bool quant,
                                      int num_sms, cudaStream_t stream);
-cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src,
+cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src, int num_sms,
                                          cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyParams& p, int num_pairs, cudaStream_t stream);
 

@@ -66,9 +66,17 @@ __device__ __forceinline__ void load_weight4(const void* w, int f32, int at, flo
     else Four<ST>::to_float(Four<ST>::load(static_cast<const uint8_t*>(w) + at * ST::bytes), f);
 }
 
+// What a warp has loaded of one token: its rows as stored, their angles, the token's position and
+// slot.
+template <typename ST>
+struct TokenRows {
+    typename Four<ST>::raw a[kNormRows], b[kNormRows];
+    float4 c, s;
+    int64_t pos, slot;
+};
+
 template <typename ST, typename KT, int HD>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopeParams p, int warps,
-                                                                    int log_block) {
+__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopeParams p, int log_block) {
     pdl_launch_dependents();   // the attention launched next may start its launch now
     constexpr bool CACHE = !std::is_same<KT, NoCache>::value;
     constexpr int LPR = HD / 8, RPW = 32 / LPR, STEP = RPW * kNormRows;   // lanes a row, rows a warp
@@ -76,83 +84,126 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
     const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR;
     const int nq = (p.num_q_heads + STEP - 1) / STEP, nk = (p.num_kv_heads + STEP - 1) / STEP;
     const int pieces = nq + (CACHE ? 2 : 1) * nk;                // warps' work of a token
-    const int tpc = max(1, (int)(blockDim.x / 32) / warps);      // tokens of the CTA
-    const int64_t t = (int64_t)blockIdx.x * tpc + (threadIdx.x >> 5) / warps;
-    if (t >= p.num_tokens) return;
-    const int64_t pos = p.positions[t];
-    int64_t slot = -1;
-    if constexpr (CACHE) slot = p.slot_mapping[t];
-    const bool cached = slot >= 0 && (slot >> log_block) < p.num_blocks;
-    const int in_block = (int)(slot & ((1 << log_block) - 1));
-    const int64_t tile_bytes = (int64_t)p.block_size * [] {
+    const int gw = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
+    const int step = gridDim.x * (kNormThreads / 32) / pieces;   // tokens at work at once
+    int64_t t = gw / pieces;
+    if (t >= step || t >= p.num_tokens) return;
+    const int piece = gw % pieces;
+    const int kind = piece < nq ? 0 : piece < nq + nk ? 1 : 2;   // query, key, value heads
+    const int heads = kind == 0 ? p.num_q_heads : p.num_kv_heads;
+    const int h0 = (piece - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * STEP + sub;
+    const int tile_bytes = p.block_size * [] {
         if constexpr (CACHE) return cache_row_bytes_of<KT>(HD);
         else return 0;
     }();
-    const int64_t tile0 = (slot >> log_block) * p.num_kv_heads;  // of kv head 0; used if cached
-    // this lane's runs of four dims
-    const int half = p.rot_dim / 2;
-    const bool turned = 8 * j < p.rot_dim, split = turned && !p.interleaved;
-    const int da = split ? 4 * j : 8 * j, db = split ? half + 4 * j : 8 * j + 4;
+    // the tile of this lane's first row in the slot's block, and whether there is one
+    auto tile_of = [&](int64_t slot) {
+        return ((slot >> log_block) * p.num_kv_heads + h0) * (int64_t)tile_bytes;
+    };
+    auto cached = [&](int64_t slot) { return slot >= 0 && (slot >> log_block) < p.num_blocks; };
+    auto known = [&](int64_t pos) { return pos >= 0 && pos < p.max_position; };
 
-    for (int piece = (threadIdx.x >> 5) % warps; piece < pieces; piece += blockDim.x / 32) {
-        const int kind = piece < nq ? 0 : piece < nq + nk ? 1 : 2;       // query, key, value
-        const int heads = kind == 0 ? p.num_q_heads : p.num_kv_heads;
-        const int h0 = (piece - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * STEP + sub;
-        if constexpr (CACHE) {
-            if (kind == 2) {                                     // values: moved as they are
-                float x[kNormRows][8];
+    if constexpr (CACHE) {
+        if (kind == 2) {                                         // values: moved as they are
+            uint4 x[kNormRows][ST::bytes / 2];
+            auto fetch = [&](int64_t at) {
+                const uint8_t* src = static_cast<const uint8_t*>(p.v) +
+                                     (at * p.v_stride + h0 * HD + 8 * j) * ST::bytes;
 #pragma unroll
                 for (int u = 0; u < kNormRows; ++u)
-                    if (h0 + u * RPW < heads) {
-                        load8<ST>(static_cast<const uint8_t*>(p.v) +
-                                      (t * p.v_stride + (int64_t)(h0 + u * RPW) * HD + 8 * j) * ST::bytes, x[u]);
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-                    }
-                if (!cached || pos < 0 || pos >= p.max_position) continue;
+                    for (int i = 0; i < ST::bytes / 2; ++i)
+                        x[u][i] = h0 + u * RPW < heads
+                            ? reinterpret_cast<const uint4*>(src + u * RPW * HD * ST::bytes)[i]
+                            : make_uint4(0u, 0u, 0u, 0u);
+            };
+            for (; t < p.num_tokens; t += step) {
+                fetch(t);
+                const int64_t pos = p.positions[t], slot = p.slot_mapping[t];
+                if (!cached(slot) || !known(pos)) continue;
+                const int row = (int)(slot & ((1 << log_block) - 1));
+                uint8_t* tile = static_cast<uint8_t*>(p.v_cache) + tile_of(slot);
 #pragma unroll
                 for (int u = 0; u < kNormRows; ++u) {
                     const bool live = h0 + u * RPW < heads;
-                    CacheRow<KT>::store(static_cast<uint8_t*>(p.v_cache) +
-                                            (live ? (tile0 + h0 + u * RPW) * tile_bytes : 0),
-                                        p.block_size, HD, in_block, j, x[u], p.kv_scale, live);
+                    float f[8];
+                    load8<ST>(x[u], f);
+                    CacheRow<KT>::store(tile + u * RPW * tile_bytes, p.block_size, HD, row, j, f,
+                                        p.kv_scale, live);
                 }
-                continue;
             }
+            return;
         }
-        const uint8_t* src = static_cast<const uint8_t*>(kind == 0 ? p.q : p.k) +
-                             (t * (kind == 0 ? p.q_stride : p.k_stride) + (int64_t)h0 * HD) * ST::bytes;
-        typename R::raw ra[kNormRows], rb[kNormRows];
+    }
+
+    // this lane's runs of four dims, and its weights
+    const int half = p.rot_dim / 2;
+    const bool turned = 8 * j < p.rot_dim, split = turned && !p.interleaved;
+    const int da = split ? 4 * j : 8 * j, db = split ? half + 4 * j : 8 * j + 4;
+    const void* weight = kind == 0 ? p.q_weight : p.k_weight;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (weight != nullptr) {
+        load_weight4<ST>(weight, p.weight_f32, da, w);
+        load_weight4<ST>(weight, p.weight_f32, db, w + 4);
+    }
+    const int64_t stride = kind == 0 ? p.q_stride : p.k_stride;
+    const uint8_t* src = static_cast<const uint8_t*>(kind == 0 ? p.q : p.k) + (int64_t)h0 * HD * ST::bytes;
+    int64_t out_stride = p.q_out_stride;
+    uint8_t* out = static_cast<uint8_t*>(p.q_out) + (int64_t)h0 * HD * ST::bytes;
+    if constexpr (!CACHE)
+        if (kind == 1) {
+            out_stride = p.k_out_stride;
+            out = static_cast<uint8_t*>(p.k_out) + (int64_t)h0 * HD * ST::bytes;
+        }
+    auto fetch_rows = [&](TokenRows<ST>& r, int64_t at) {
+        const uint8_t* row = src + at * stride * ST::bytes;
 #pragma unroll
         for (int u = 0; u < kNormRows; ++u) {
-            ra[u] = rb[u] = typename R::raw{};
+            r.a[u] = r.b[u] = typename R::raw{};
             if (h0 + u * RPW < heads) {
-                ra[u] = R::load(src + (u * RPW * HD + da) * ST::bytes);
-                rb[u] = R::load(src + (u * RPW * HD + db) * ST::bytes);
+                r.a[u] = R::load(row + (u * RPW * HD + da) * ST::bytes);
+                r.b[u] = R::load(row + (u * RPW * HD + db) * ST::bytes);
             }
         }
-        const void* weight = kind == 0 ? p.q_weight : p.k_weight;
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        if (weight != nullptr) {
-            load_weight4<ST>(weight, p.weight_f32, da, w);
-            load_weight4<ST>(weight, p.weight_f32, db, w + 4);
+        r.slot = -1;
+        if constexpr (CACHE) r.slot = p.slot_mapping[at];
+    };
+    auto fetch_angles = [&](TokenRows<ST>& r) {
+        r.c = r.s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (turned && known(r.pos)) {
+            const float* cs = p.cos_sin + r.pos * p.rot_dim + 4 * j;
+            r.c = *reinterpret_cast<const float4*>(cs);
+            r.s = *reinterpret_cast<const float4*>(cs + half);
         }
-        if (pos < 0 || pos >= p.max_position) {                  // the whole warp: one token
+    };
+
+    // rows and angles load one token ahead, positions two
+    TokenRows<ST> now, next;
+    now.pos = p.positions[t];
+    int64_t pos_after = t + step < p.num_tokens ? p.positions[t + step] : 0;
+    fetch_rows(now, t);
+    fetch_angles(now);
+    for (; t < p.num_tokens; t += step) {
+        if (t + step < p.num_tokens) {
+            next.pos = pos_after;
+            fetch_rows(next, t + step);
+            fetch_angles(next);
+            if (t + 2 * step < p.num_tokens) pos_after = p.positions[t + 2 * step];
+        }
+        if (!known(now.pos)) {                                   // the whole warp: one token
             if (piece == 0 && lane == 0) set_status(p.status, PKV_DEV_BAD_POSITION);
-            return;
+            now = next;
+            continue;
         }
         // every output is x_i m_i + x_partner n_i: m = weight cosine, n = -+ partner's weight sine.
         // Half-split lanes pair dim i of the first run with dim i of the second; the others hold
         // pairs (2i, 2i + 1).
         float m[8], n[8];
-        const float* cs = p.cos_sin + pos * p.rot_dim;
+        const float c[4] = {now.c.x, now.c.y, now.c.z, now.c.w};
+        const float sn[4] = {now.s.x, now.s.y, now.s.z, now.s.w};
         if (split) {
-            float c[4], sn[4];
-            Four<F32>::to_float(Four<F32>::load(cs + 4 * j), c);
-            Four<F32>::to_float(Four<F32>::load(cs + half + 4 * j), sn);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 m[i] = w[i] * c[i];
@@ -161,9 +212,6 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
                 n[i + 4] = w[i] * sn[i];
             }
         } else if (turned) {
-            float c[4], sn[4];
-            Four<F32>::to_float(Four<F32>::load(cs + 4 * j), c);
-            Four<F32>::to_float(Four<F32>::load(cs + half + 4 * j), sn);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 m[2 * i] = w[2 * i] * c[i];
@@ -175,17 +223,18 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
 #pragma unroll
             for (int i = 0; i < 8; ++i) m[i] = w[i];
         }
-        uint8_t* dst = nullptr;
-        if (kind == 0)
-            dst = static_cast<uint8_t*>(p.q_out) + (t * p.q_out_stride + (int64_t)h0 * HD) * ST::bytes;
-        else if constexpr (!CACHE)
-            dst = static_cast<uint8_t*>(p.k_out) + (t * p.k_out_stride + (int64_t)h0 * HD) * ST::bytes;
+        const bool hit = cached(now.slot);
+        const int in_block = (int)(now.slot & ((1 << log_block) - 1));
+        uint8_t* dst = out + t * out_stride * ST::bytes;
+        uint8_t* tile = nullptr;
+        if constexpr (CACHE)
+            if (hit) tile = static_cast<uint8_t*>(p.k_cache) + tile_of(now.slot);
 #pragma unroll
         for (int u = 0; u < kNormRows; ++u) {
             const bool live = h0 + u * RPW < heads;
             float x[8], y[8];
-            R::to_float(ra[u], x);
-            R::to_float(rb[u], x + 4);
+            R::to_float(now.a[u], x);
+            R::to_float(now.b[u], x + 4);
             float rs = 1.f;
             if (weight != nullptr) {
                 float ss = 0.f;
@@ -212,9 +261,8 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
                     *reinterpret_cast<typename R::raw*>(dst + (u * RPW * HD + db) * ST::bytes) = ob;
                 }
             } else if constexpr (CACHE && !is_quantised<KT>()) {
-                if (live && cached) {
-                    uint8_t* to = static_cast<uint8_t*>(p.k_cache) + (tile0 + h0 + u * RPW) * tile_bytes +
-                                  (int64_t)in_block * HD * ST::bytes;
+                if (live && hit) {
+                    uint8_t* to = tile + u * RPW * tile_bytes + in_block * HD * ST::bytes;
                     *reinterpret_cast<typename R::raw*>(to + da * ST::bytes) = oa;
                     *reinterpret_cast<typename R::raw*>(to + db * ST::bytes) = ob;
                 }
@@ -237,28 +285,48 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
                 }
                 R::to_float(oa, y);
                 R::to_float(ob, y + 4);
-                CacheRow<KT>::store(static_cast<uint8_t*>(p.k_cache) +
-                                        (live && cached ? (tile0 + h0 + u * RPW) * tile_bytes : 0),
-                                    p.block_size, HD, in_block, j, y, p.kv_scale, live && cached);
+                CacheRow<KT>::store(tile + (hit ? u * RPW * tile_bytes : 0), p.block_size, HD,
+                                    in_block, j, y, p.kv_scale, live && hit);
             }
         }
         if constexpr (CACHE)
-            if (piece == 0 && lane == 0 && slot >= 0 && !cached) set_status(p.status, PKV_DEV_BAD_SLOT);
+            if (piece == 0 && lane == 0 && now.slot >= 0 && !hit) set_status(p.status, PKV_DEV_BAD_SLOT);
+        now = next;
     }
+}
+
+template <typename ST, typename KT, int HD>
+cudaError_t launch_norm_rope_d(const NormRopeParams& p, cudaStream_t stream) {
+    constexpr bool CACHE = !std::is_same<KT, NoCache>::value;
+    constexpr int STEP = 256 / HD * kNormRows, WARPS = kNormThreads / 32;
+    static int resident[64] = {0};                // CTAs the device holds at once
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    auto kernel = qk_norm_rope_kernel<ST, KT, HD>;
+    if (resident[dev] == 0) {
+        int per_sm = 0, sms = 0;
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kNormThreads, 0);
+        if (err != cudaSuccess) return err;
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (err != cudaSuccess) return err;
+        resident[dev] = (per_sm > 0 ? per_sm : 1) * sms;
+    }
+    const int64_t pieces = (p.num_q_heads + STEP - 1) / STEP +
+                           (CACHE ? 2 : 1) * ((p.num_kv_heads + STEP - 1) / STEP);
+    const int64_t least = (pieces + WARPS - 1) / WARPS;          // one token at work at least
+    const int64_t most = resident[dev] > least ? resident[dev] : least;
+    const int64_t need = (p.num_tokens * pieces + WARPS - 1) / WARPS;
+    const int log_block = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
+    kernel<<<(unsigned)(need < most ? need : most), kNormThreads, 0, stream>>>(p, log_block);
+    return cudaGetLastError();
 }
 
 template <typename ST, typename KT>
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
-    constexpr bool CACHE = !std::is_same<KT, NoCache>::value;
-    const int step = 256 / p.head_dim * kNormRows;            // rows of a warp
-    const int need = (p.num_q_heads + step - 1) / step +
-                     (CACHE ? 2 : 1) * ((p.num_kv_heads + step - 1) / step);   // warps of a token
-    const int most = kNormThreads / 32, warps = need < most ? need : most, tpc = most / warps;
-    const int log_block = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
-    const unsigned grid = (unsigned)((p.num_tokens + tpc - 1) / tpc), threads = 32u * warps * tpc;
-    if (p.head_dim == 128) qk_norm_rope_kernel<ST, KT, 128><<<grid, threads, 0, stream>>>(p, warps, log_block);
-    else qk_norm_rope_kernel<ST, KT, 64><<<grid, threads, 0, stream>>>(p, warps, log_block);
-    return cudaGetLastError();
+    return p.head_dim == 128 ? launch_norm_rope_d<ST, KT, 128>(p, stream)
+                             : launch_norm_rope_d<ST, KT, 64>(p, stream);
 }
 
 cudaError_t launch_qk_norm_rope(const NormRopeParams& p, pkv_dtype dtype, cudaStream_t stream) {
