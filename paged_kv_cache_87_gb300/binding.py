@@ -1,8 +1,9 @@
-"""ctypes binding of libpagedkv.so (C ABI: include/pagedkv.h).
+"""Python binding of libpagedkv.so (C ABI: include/pagedkv.h).
 
 Argument marshalling only: shapes, dtypes and the stream are read off torch
-tensors and passed as plain pointers and sizes; every step of the hot path
-runs in the library's CUDA kernels.  There is no CPU fallback: if the library
+tensors and passed as plain pointers and sizes -- for the calls of a serving
+step in the extension module _marshal (csrc/host/marshal.cc), for the rest
+through ctypes; every step of the hot path runs in the library's CUDA kernels.  There is no CPU fallback: if the library
 cannot be loaded the calls raise.
 
 Functions carry the C names:
@@ -110,6 +111,7 @@ _SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_calls = None   # the extension module
 
 
 class PagedKVError(RuntimeError):
@@ -132,6 +134,21 @@ def load(path: str = LIB_PATH):
                 f.restype, f.argtypes = res, args
             _lib = lib
         return _lib
+
+
+def _marshal():
+    """The extension module, loaded on first use (built with the library)."""
+    global _calls
+    if _calls is None:
+        load()
+        path = os.path.join(_PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m paged_kv_cache_87_gb300.build` (needs nvcc and g++)")
+        from . import _marshal as module
+        module.set_error(PagedKVError)
+        _calls = module
+    return _calls
 
 
 def status_text(status: int) -> str:
@@ -189,13 +206,6 @@ def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _contiguous(*tensors) -> None:
-    for t in tensors:
-        if not (t.is_cuda and t.is_contiguous()):
-            raise ValueError(f"a contiguous CUDA tensor is needed, not {tuple(t.shape)} "
-                             f"strides {t.stride()} on {t.device}")
-
-
 # ------------------------------------------------------------------ calls --
 
 def pkv_decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -203,37 +213,6 @@ def pkv_decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: in
     return int(load().pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                                  block_size, max_context_len,
                                                  dtype_code(kv_dtype)))
-
-
-def _decode_args(query, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
-                 kv_scale, workspace, out, stream, prefix):
-    """Checks and marshals a decode call: (C function name, argument tuple, out, workspace)."""
-    S, Hq, d = query.shape
-    NB, Hkv, B, _ = k_cache.shape
-    kc, d2 = _cache_type(k_cache)
-    if d2 != d or v_cache.shape != k_cache.shape:
-        raise ValueError("cache shapes must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    if kc == PKV_FP4_E2M1 and v_cache.dtype != k_cache.dtype:
-        raise ValueError("a 4-bit v_cache must be uint8 as the k_cache")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise ValueError("block_tables and context_lens must be int32")
-    for t, n in ((query, "query"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                 (block_tables, "block_tables"), (context_lens, "context_lens")):
-        _cuda(t, n)
-    qc = dtype_code(query)
-    need = pkv_decode_workspace_bytes(S, Hq, Hkv, d, B, max_context_len, kc)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=query.device)
-    if out is None:
-        out = torch.empty_like(query)
-    _cuda(out, "out")
-    _cuda(workspace, "workspace")
-    fn = "pkv_paged_decode_attention_prefix" if prefix else "pkv_paged_decode_attention"
-    args = (query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), S, Hq, Hkv, d, B, NB, block_tables.shape[1],
-            int(max_context_len), float(scale), qc, kc, float(kv_scale), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), out.data_ptr(), _stream_ptr(stream))
-    return fn, args, out, workspace
 
 
 def pkv_paged_decode_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -250,11 +229,9 @@ def pkv_paged_decode_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cac
     ``prefix=True`` calls pkv_paged_decode_attention_prefix (shared prompts
     read once per group of sequences).
     """
-    fn, args, out, _ = _decode_args(query, k_cache, v_cache, block_tables, context_lens,
-                                    max_context_len, scale, kv_scale, workspace, out, stream,
-                                    prefix)
-    _check(fn, getattr(load(), fn)(*args))
-    return out
+    return (_calls or _marshal()).decode(query, k_cache, v_cache, block_tables, context_lens,
+                                         max_context_len, scale, kv_scale, workspace, out,
+                                         stream, prefix, False)
 
 
 class PreparedCall:
@@ -281,9 +258,10 @@ def prepare_paged_decode_attention(query, k_cache, v_cache, block_tables, contex
                                    max_context_len, scale, kv_scale=1.0, workspace=None,
                                    out=None, stream=None, prefix=False) -> PreparedCall:
     """pkv_paged_decode_attention (or the prefix-aware entry) as a PreparedCall."""
-    fn, args, out, workspace = _decode_args(query, k_cache, v_cache, block_tables,
-                                            context_lens, max_context_len, scale, kv_scale,
-                                            workspace, out, stream, prefix)
+    args, workspace, out = _marshal().decode(query, k_cache, v_cache, block_tables, context_lens,
+                                             max_context_len, scale, kv_scale, workspace, out,
+                                             stream, prefix, True)
+    fn = "pkv_paged_decode_attention_prefix" if prefix else "pkv_paged_decode_attention"
     return PreparedCall(fn, args, (query, k_cache, v_cache, block_tables, context_lens,
                                    workspace, out))
 
@@ -404,40 +382,22 @@ def pkv_paged_decode_attention_noalloc(query: torch.Tensor, k_cache: torch.Tenso
     return out
 
 
-def _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream):
-    T, Hkv, d = key.shape
-    NB, Hkv2, B, _ = k_cache.shape
-    kc, d2 = _cache_type(k_cache)
-    if kc == PKV_FP4_E2M1 and (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or
-                               value.dtype != key.dtype):
-        raise ValueError("key and value, and the two 4-bit caches, must have one shape and type")
-    if (Hkv2, d2) != (Hkv, d) or tuple(value.shape) != tuple(key.shape):
-        raise ValueError("key/value [T, Hkv, d] do not match the cache [NB, Hkv, B, d]")
-    if slot_mapping.dtype != torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    for t, n in ((key, "key"), (value, "value"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                 (slot_mapping, "slot_mapping")):
-        _cuda(t, n)
-    return (key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            slot_mapping.data_ptr(), T, Hkv, d, B, NB, dtype_code(key), kc,
-            float(kv_scale), _stream_ptr(stream))
-
-
 def pkv_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
                           v_cache: torch.Tensor, slot_mapping: torch.Tensor,
                           kv_scale: float = 1.0, stream=None) -> None:
     """k_cache[slot // B, h, slot % B] = key[t, h] (e4m3(x / kv_scale) for FP8 caches; codes
     and scales for 4-bit caches, uint8 of fp4_cache_shape)."""
-    args = _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream)
-    _check("pkv_reshape_and_cache", load().pkv_reshape_and_cache(*args))
+    (_calls or _marshal()).write(key, value, k_cache, v_cache, slot_mapping, kv_scale,
+                                 stream, False)
 
 
 def prepare_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, kv_scale=1.0,
                               stream=None) -> PreparedCall:
     """pkv_reshape_and_cache as a PreparedCall."""
-    return PreparedCall("pkv_reshape_and_cache",
-                        _reshape_args(key, value, k_cache, v_cache, slot_mapping, kv_scale,
-                                      stream), (key, value, k_cache, v_cache, slot_mapping))
+    args = _marshal().write(key, value, k_cache, v_cache, slot_mapping, kv_scale,
+                            stream, True)
+    return PreparedCall("pkv_reshape_and_cache", args,
+                        (key, value, k_cache, v_cache, slot_mapping))
 
 
 def pkv_gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -453,93 +413,11 @@ def pkv_gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     4-bit ones become values in any of float32, float16 and bfloat16.  Rows outside every
     sequence's range are left as they were (in outputs allocated here: uninitialised).
     """
-    NB, Hkv, B, _ = shape = k_cache.shape
-    kc, d = _cache_type(k_cache)
-    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must have one shape and type")
-    S, max_blocks = block_tables.shape
-    if block_tables.dtype != torch.int32 or row_start.dtype != torch.int32 or \
-            row_start.shape != (S + 1,):
-        raise ValueError("block_tables must be int32 [S, max_blocks], row_start int32 [S + 1]")
-    _contiguous(k_cache, v_cache, block_tables, row_start)
-    first = None
-    if token_start is not None:
-        if token_start.dtype != torch.int32 or token_start.shape != (S,):
-            raise ValueError("token_start must be int32 [S]")
-        _contiguous(token_start)
-        first = token_start.data_ptr()
-    rows = (total_rows, Hkv, d)
-    if key_out is None:
-        key_out = torch.empty(rows, dtype=out_dtype, device=k_cache.device)
-    elif key_out.shape != rows or key_out.dtype != out_dtype:
-        raise ValueError(f"key_out must be {list(rows)} of {out_dtype}")
-    else:
-        _contiguous(key_out)
-    if value_out is None:
-        value_out = torch.empty_like(key_out)
-    elif value_out.shape != rows or value_out.dtype != out_dtype:
-        raise ValueError(f"value_out must be {list(rows)} of {out_dtype}")
-    else:
-        _contiguous(value_out)
-    st = (_lib or load()).pkv_gather_cache(
-        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), row_start.data_ptr(),
-        first, S, total_rows, Hkv, d, B, NB, max_blocks, kc, kv_scale, _TORCH_CODES[out_dtype],
-        key_out.data_ptr(), value_out.data_ptr(), _stream_ptr(stream))
-    if st:
-        raise PagedKVError("pkv_gather_cache", st)
-    return key_out, value_out
+    return (_calls or _marshal()).gather(k_cache, v_cache, block_tables, row_start, total_rows,
+                                         out_dtype, kv_scale, token_start, key_out, value_out, stream)
 
 
 # ---------------------------------------------------------- norm + rotary --
-
-def _head_rows(t: torch.Tensor, d: int, heads: int) -> int:
-    """The token stride of a CUDA tensor [T, heads, d] whose tokens' heads are contiguous."""
-    s0, s1, s2 = t.stride()
-    if not t.is_cuda or s2 != 1 or (s1 != d and heads > 1):
-        raise ValueError("rows must be CUDA tensors [T, heads, d] with their heads contiguous")
-    return s0 if t.shape[0] > 1 else heads * d
-
-
-def _norm_rope_args(query, key, value, cos_sin, positions, q_weight, k_weight, eps, interleaved,
-                    q_out):
-    """Checks shared by the two entry points: (the C arguments up to q_out's stride, q_out).
-    ``value``: the C arguments of the values, [] without them."""
-    T, Hq, d = query.shape
-    Tk, Hkv, dk = key.shape
-    dtype = query.dtype
-    if Tk != T or dk != d or key.dtype != dtype:
-        raise ValueError("query [T, Hq, d] and key [T, Hkv, d] must agree in T, d and type")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
-    if positions.dtype != torch.int64 or positions.shape != (T,):
-        raise ValueError("positions must be int64 [T]")
-    _contiguous(cos_sin, positions)
-    wc, qw, kw = PKV_F32, None, None
-    if q_weight is not None:
-        qw, wc = q_weight.data_ptr(), _TORCH_CODES[q_weight.dtype]
-        if q_weight.shape != (d,):
-            raise ValueError("q_weight must be [head_dim]")
-        _contiguous(q_weight)
-    if k_weight is not None:
-        kw, wc = k_weight.data_ptr(), _TORCH_CODES[k_weight.dtype]
-        if k_weight.shape != (d,):
-            raise ValueError("k_weight must be [head_dim]")
-        if q_weight is not None and k_weight.dtype != q_weight.dtype:
-            raise ValueError("q_weight and k_weight must have one type")
-        _contiguous(k_weight)
-    q_stride, k_stride = _head_rows(query, d, Hq), _head_rows(key, d, Hkv)
-    if q_out is None:
-        q_out, out_stride = torch.empty((T, Hq, d), dtype=dtype, device=query.device), Hq * d
-    elif q_out.shape != query.shape or q_out.dtype != dtype:
-        raise ValueError("q_out must have query's shape and type")
-    else:
-        out_stride = _head_rows(q_out, d, Hq)
-    max_position, rot_dim = cos_sin.shape
-    return (query.data_ptr(), q_stride, key.data_ptr(), k_stride, *value, qw, kw, wc, eps,
-            cos_sin.data_ptr(), max_position, rot_dim, 1 if interleaved else 0,
-            positions.data_ptr(), T, Hq, Hkv, d, _TORCH_CODES[dtype], q_out.data_ptr(),
-            out_stride), q_out
-
 
 def pkv_qk_norm_rope(query: torch.Tensor, key: torch.Tensor, cos_sin: torch.Tensor,
                      positions: torch.Tensor, q_weight: torch.Tensor | None = None,
@@ -554,19 +432,8 @@ def pkv_qk_norm_rope(query: torch.Tensor, key: torch.Tensor, cos_sin: torch.Tens
     sines; positions int64 [T].  ``interleaved`` rotates dims (2i, 2i + 1) instead of
     (i, i + rot_dim / 2).  q_out / k_out may be query / key themselves (in place).
     """
-    args, q_out = _norm_rope_args(query, key, (), cos_sin, positions, q_weight, k_weight, eps,
-                                  interleaved, q_out)
-    T, Hkv, d = shape = key.shape
-    if k_out is None:
-        k_out, k_stride = torch.empty(shape, dtype=key.dtype, device=key.device), Hkv * d
-    elif k_out.shape != shape or k_out.dtype != key.dtype:
-        raise ValueError("k_out must have key's shape and type")
-    else:
-        k_stride = _head_rows(k_out, d, Hkv)
-    st = (_lib or load()).pkv_qk_norm_rope(*args, k_out.data_ptr(), k_stride, _stream_ptr(stream))
-    if st:
-        raise PagedKVError("pkv_qk_norm_rope", st)
-    return q_out, k_out
+    return (_calls or _marshal()).norm_rope(query, key, cos_sin, positions, q_weight, k_weight,
+                                            eps, interleaved, q_out, k_out, stream)
 
 
 def pkv_qk_norm_rope_and_cache(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -579,24 +446,9 @@ def pkv_qk_norm_rope_and_cache(query: torch.Tensor, key: torch.Tensor, value: to
     """pkv_qk_norm_rope whose keys, with ``value`` [T, Hkv, d], go into the paged cache at
     slot_mapping (int64 [T], negative: not written); returns q_out.  The cache, of any type,
     holds the same bits as after pkv_qk_norm_rope and pkv_reshape_and_cache of its keys."""
-    NB, Hkv, B, _ = shape = k_cache.shape
-    kc, d = _cache_type(k_cache)
-    rows = key.shape
-    if rows[1] != Hkv or rows[2] != d or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("key [T, Hkv, d] does not match the caches [NB, Hkv, B, d]")
-    if value.shape != rows or value.dtype != key.dtype:
-        raise ValueError("value must have key's shape and type")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (rows[0],):
-        raise ValueError("slot_mapping must be int64 [T]")
-    _contiguous(k_cache, v_cache, slot_mapping)
-    args, q_out = _norm_rope_args(query, key, (value.data_ptr(), _head_rows(value, d, Hkv)),
-                                  cos_sin, positions, q_weight, k_weight, eps, interleaved, q_out)
-    st = (_lib or load()).pkv_qk_norm_rope_and_cache(
-        *args, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), B, NB, kc,
-        kv_scale, _stream_ptr(stream))
-    if st:
-        raise PagedKVError("pkv_qk_norm_rope_and_cache", st)
-    return q_out
+    return (_calls or _marshal()).norm_rope_write(
+        query, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, q_weight, k_weight,
+        eps, interleaved, kv_scale, q_out, stream)
 
 
 def validate_pairs(pairs: np.ndarray, num_blocks: int) -> None:

@@ -1,7 +1,9 @@
 """Build libpagedkv.so in-tree with nvcc for sm_103a.
 
 Each .cu file compiles to an object in parallel; the objects link into
-``paged_kv_cache_87_gb300/libpagedkv.so``.  The build is content-addressed: a
+``paged_kv_cache_87_gb300/libpagedkv.so``.  ``_marshal.so`` beside it is the
+binding's extension module (csrc/host/marshal.cc: torch tensors into calls of
+the library), compiled by g++ at the same time.  The build is content-addressed: a
 SHA-256 over every source and header, the compile and link flags and the
 output of ``nvcc --version`` is stored beside the objects, and the library is
 rebuilt whenever that digest changes (a modification time is never trusted).
@@ -13,6 +15,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -75,7 +79,77 @@ def up_to_date(extra_flags: list[str] | None = None) -> bool:
         return f.read().strip() == digest(extra_flags)
 
 
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "host", "marshal.cc")
+MARSHAL_STAMP = os.path.join(BUILD, "marshal.sha256")
+GXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall"]
+
+
+def _marshal_commands(obj: str, out: str) -> tuple[list[str], list[str]]:
+    """The compile and link commands of the extension module, for the torch that runs this."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    sysinc = [os.path.join(root, "include"),
+              os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    lib = os.path.join(root, "lib")
+    return (["g++", *GXX_FLAGS, abi, *[f"-I{i}" for i in inc],
+             *[x for i in sysinc for x in ("-isystem", i)], "-c", MARSHAL_SRC, "-o", obj],
+            ["g++", "-shared", "-o", out, obj, LIB, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+             "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"])
+
+
+def _marshal_digest() -> str:
+    import torch
+    h = hashlib.sha256()
+    for f in (MARSHAL_SRC, os.path.join(ROOT, "include", "pagedkv.h")):
+        with open(f, "rb") as fh:
+            h.update(fh.read() + b"\0")
+    h.update(repr((_marshal_commands("o", "so"), torch.__version__, sys.version)).encode())
+    return h.hexdigest()
+
+
+def marshal_up_to_date() -> bool:
+    if not os.path.exists(MARSHAL) or not os.path.exists(MARSHAL_STAMP):
+        return False
+    with open(MARSHAL_STAMP) as f:
+        return f.read().strip() == _marshal_digest()
+
+
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+    return r.stderr
+
+
+def build_marshal(compiled: str) -> None:
+    """Link the compiled extension module against libpagedkv.so, in place."""
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    _run(_marshal_commands(compiled, tmp)[1], "linking _marshal.so")
+    os.replace(tmp, MARSHAL)
+    with open(MARSHAL_STAMP + f".tmp{os.getpid()}", "w") as f:
+        f.write(_marshal_digest() + "\n")
+    os.replace(MARSHAL_STAMP + f".tmp{os.getpid()}", MARSHAL_STAMP)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Build what is out of date of the library and the extension module."""
+    os.makedirs(BUILD, exist_ok=True)
+    obj = os.path.join(BUILD, "marshal.o")
+    if not force and marshal_up_to_date():
+        return build_library(force, verbose, ptxas_info)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        compiling = ex.submit(_run, _marshal_commands(obj, "")[0], "g++ on marshal.cc")
+        lib = build_library(force, verbose, ptxas_info)
+        compiling.result()
+    build_marshal(obj)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     if not force and up_to_date(extra):
         return LIB
@@ -110,5 +184,4 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="-v" in sys.argv))
