@@ -121,10 +121,10 @@ pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4
     if (B != 8 && B != 16 && B != 32) return PKV_ERR_UNSUPPORTED;
     pl->group = Hq / Hkv;
     pl->nsub = (pl->group + kFp4Heads - 1) / kFp4Heads;
-    const int64_t tiles = ((int64_t)max_ctx + kFp4Tile - 1) / kFp4Tile;
+    const int64_t slots = ((int64_t)max_ctx + kFp4Tile - 1) / kFp4Tile + kFp4UnitCost;
     if ((int64_t)Hkv * pl->nsub > INT32_MAX || (int64_t)S * Hkv * pl->nsub > INT32_MAX ||
-        (int64_t)S * Hkv * pl->nsub * tiles > INT32_MAX - (1 << 24))
-        return PKV_ERR_UNSUPPORTED;                       // tiles are counted in 32 bits
+        (int64_t)S * Hkv * pl->nsub * slots > INT32_MAX - (1 << 24))
+        return PKV_ERR_UNSUPPORTED;                       // slots are counted in 32 bits
     pl->workers = (int)fp4_max_workers(S, Hkv, pl->nsub, max_ctx);
     const size_t states = (size_t)pl->workers * 2 * kFp4Heads;
     pl->off_ml = round_up(states * HD * 4, 256);
@@ -217,6 +217,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
         f.part_ml = reinterpret_cast<float*>(ws + fplan.off_ml);
         f.head_dim = head_dim;
         f.block_size = block_size;
+        f.log_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
         f.num_blocks = num_blocks;
         f.max_blocks = max_blocks_per_seq;
         f.max_context_len = max_context_len;

@@ -107,13 +107,18 @@ struct Cfg {
     static constexpr int NSTAGE = 3;
     static constexpr int NCHUNK = HD / 32;
     static constexpr int NP = std::is_same<QT, F32>::value ? 2 : 1;   // terms of q and p
-    static constexpr int HS = HD + 1;                  // exchange stride of a head: few conflicts
+    static constexpr int XD = HD / 2;                  // dims exchanged at a time
+    static constexpr int HS = XD + 1;                  // exchange stride of a head: few conflicts
     static constexpr int XBUF = kConsumers * kFp4Heads * (HS + 2);    // acc, then m, l
     static constexpr size_t OFF_META = (size_t)NSTAGE * STAGE_BYTES;
     static constexpr size_t OFF_BARS = OFF_META + NSTAGE * 32;
-    static constexpr size_t OFF_X = OFF_BARS + 2 * NSTAGE * 8;
+    static constexpr size_t OFF_QF = (OFF_BARS + 2 * NSTAGE * 8 + 15) / 16 * 16;
+    static constexpr size_t OFF_X = OFF_QF + NP * NCHUNK * 32 * 16;
     static constexpr size_t SMEM = OFF_X + XBUF * 4;
-    static constexpr int CTAS = NP == 1 ? 4 : 3;       // resident, by registers
+    // resident CTAs, by registers.  The queries' operands stay in shared memory (a 16-byte load a
+    // chunk): 187 -> 175 us on long documents against registers.  A fifth CTA (72 registers) spills
+    // and loses: 200 us.
+    static constexpr int CTAS = NP == 1 ? 4 : 3;
 };
 
 struct TileMeta {
@@ -124,41 +129,62 @@ struct TileMeta {
 };
 constexpr int kFirst = 1, kLast = 2, kDone = 4;
 
+// Tiles of a sequence's context, per unit.
 __device__ __forceinline__ int tiles_of(const DecodeFp4Params& p, int s) {
     const int cap = min(p.max_context_len, p.max_blocks * p.block_size);
     const int c = p.context_lens[s];
     return c <= 0 ? 0 : (min(c, cap) + kFp4Tile - 1) / kFp4Tile;
 }
 
-// Block-wide scan of the sequences' tile counts: pref[i] = tiles of the sequences before
-// thread i's run of ceil(S / threads), pref[threads] = all.  Syncs the block.
+// A unit's length in the plan, in slots: its tiles and, before them, kFp4UnitCost slots that
+// stand for what a unit costs besides (its queries, the warps' meeting at its end).
+__device__ __forceinline__ int slots_of(const DecodeFp4Params& p, int s) {
+    const int n = tiles_of(p, s);
+    return n ? n + kFp4UnitCost : 0;
+}
+
+// Block-wide scan of the sequences' slots: pref[i] = slots of the sequences before thread i's run
+// of ceil(S / threads), pref[threads] = all, pref[threads + 1] = the longest.  Syncs the block.
 template <int THREADS>
-__device__ __forceinline__ void scan_tiles(const DecodeFp4Params& p, int* pref, int* wsum) {
+__device__ __forceinline__ void scan_slots(const DecodeFp4Params& p, int* pref, int2* wsum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (p.num_seqs + THREADS - 1) / THREADS;
-    int n = 0;
-    for (int s = tid * run; s < min(p.num_seqs, (tid + 1) * run); ++s) n += tiles_of(p, s);
+    int n = 0, most = 0;
+    for (int s = tid * run; s < min(p.num_seqs, (tid + 1) * run); ++s) {
+        const int k = slots_of(p, s);
+        n += k;
+        most = max(most, k);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
     int x = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, off);
         if (lane >= off) x += y;
     }
-    if (lane == 31) wsum[warp] = x;
+    if (lane == 31) wsum[warp] = make_int2(x, most);
     __syncthreads();
     int before = 0;
+    most = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) before += w < warp ? wsum[w] : 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const int2 v = wsum[w];
+        before += w < warp ? v.x : 0;
+        most = max(most, v.y);
+    }
     pref[tid + 1] = before + x;
-    if (tid == 0) pref[0] = 0;
+    if (tid == 0) {
+        pref[0] = 0;
+        pref[THREADS + 1] = most;
+    }
     __syncthreads();
 }
 
-// Place of flattened tile `pos` (below the total): its sequence, that sequence's tiles, and the
-// position of the sequence's first tile.
+// Place of flattened slot `pos` (below the total): its sequence, that sequence's slots a unit, and
+// the position of the sequence's first slot.
 template <int THREADS>
 __device__ __forceinline__ void locate(const DecodeFp4Params& p, const int* pref, int upi, int pos,
-                                       int* seq, int* tiles, int* base) {
+                                       int* seq, int* slots, int* base) {
     int lo = 0, hi = THREADS - 1;
     while (lo < hi) {                       // the last run starting at or before pos
         const int mid = (lo + hi + 1) >> 1;
@@ -166,23 +192,26 @@ __device__ __forceinline__ void locate(const DecodeFp4Params& p, const int* pref
         else hi = mid - 1;
     }
     const int run = (p.num_seqs + THREADS - 1) / THREADS;
-    int s = lo * run, b = pref[lo] * upi, n = tiles_of(p, s);
+    int s = lo * run, b = pref[lo] * upi, n = slots_of(p, s);
     while (b + n * upi <= pos) {
         b += n * upi;
-        n = tiles_of(p, ++s);
+        n = slots_of(p, ++s);
     }
     *seq = s;
-    *tiles = n;
+    *slots = n;
     *base = b;
 }
 
-__device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total) {
-    return max(kFp4MinQuota, (total + p.workers - 1) / p.workers);
+// Slots of a worker: an equal share, not under the least that pays, and not so few that one unit
+// leaves more than kFp4MaxPieces partial states to join.
+__device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total, int longest) {
+    return max(max(kFp4MinQuota, (total + p.workers - 1) / p.workers),
+               (longest + kFp4MaxPieces - 1) / kFp4MaxPieces);
 }
 
-// Where the producer is: tile `tile` of unit `u` of sequence s (n tiles, ctx tokens).
+// Where the producer is: slot `at` of unit `u` of sequence s (n slots, ctx tokens).
 struct Cursor {
-    int s, u, tile, n, ctx;
+    int s, u, at, n, ctx;
 };
 
 // A run of at most 64 blocks of one unit.
@@ -195,26 +224,36 @@ __device__ __forceinline__ Window next_window(const DecodeFp4Params& p, int upi,
                                               int& pos, Cursor& c) {
     Window w{};
     if (pos >= end) return w;
-    while (c.tile == c.n) {                       // the next unit with tiles
-        c.tile = 0;
+    while (c.at == c.n) {                         // the next unit with tiles
+        c.at = 0;
         if (++c.u == upi || c.n == 0) {
             c.u = 0;
             ++c.s;
-            c.n = tiles_of(p, c.s);
+            c.n = slots_of(p, c.s);
             c.ctx = min(p.context_lens[c.s], min(p.max_context_len, p.max_blocks * p.block_size));
         }
     }
-    const int wt = min(min(p.block_size, c.n - c.tile), end - pos);   // <= 64 blocks
-    const int ustart = pos - c.tile, uend = ustart + c.n;
+    if (c.at < kFp4UnitCost) {
+        const int skip = kFp4UnitCost - c.at;
+        if (pos + skip >= end) {                  // the range ends before the unit's first tile
+            pos = end;
+            return w;
+        }
+        pos += skip;
+        c.at = kFp4UnitCost;
+    }
+    const int tile = c.at - kFp4UnitCost, tiles = c.n - kFp4UnitCost;
+    const int wt = min(min(p.block_size, tiles - tile), end - pos);   // <= 64 blocks
+    const int dstart = pos - tile, uend = dstart + tiles;
     w.valid = 1;
     w.s = c.s;
     w.u = c.u;
-    w.t0 = c.tile * kFp4Tile;
-    w.t1 = min((c.tile + wt) * kFp4Tile, c.ctx);
-    w.first = c.tile == 0 || pos == a;
-    w.last = pos + wt == end || c.tile + wt == c.n;
-    w.slot = ustart < a ? 0 : (uend > end ? 1 : -1);
-    c.tile += wt;
+    w.t0 = tile * kFp4Tile;
+    w.t1 = min((tile + wt) * kFp4Tile, c.ctx);
+    w.first = tile == 0 || dstart + tile == a;
+    w.last = pos + wt == end || tile + wt == tiles;
+    w.slot = dstart < a ? 0 : (uend > end ? 1 : -1);
+    c.at += wt;
     pos += wt;
     return w;
 }
@@ -224,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p) {
     using C = Cfg<QT, HD>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_pref[kThreads + 1], s_wsum[kThreads / 32];
+    __shared__ int s_pref[kThreads + 2];
+    __shared__ int2 s_wsum[kThreads / 32];
     TileMeta* metas = reinterpret_cast<TileMeta*>(smem + C::OFF_META);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     uint64_t* empty = full + C::NSTAGE;
@@ -238,10 +278,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     }
     pdl_wait();                // the kernel before (the cache write) has completed
     pdl_launch_dependents();   // the merge kernel may plan beside this one
-    scan_tiles<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
-    const int B = p.block_size, upi = p.num_kv_heads * p.nsub;
+    scan_slots<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
+    const int B = p.block_size, logB = p.log_block, upi = p.num_kv_heads * p.nsub;
     const int tile_bytes = B * C::ROWB;
-    const int total = s_pref[kThreads] * upi, q = quota_of(p, total);
+    const int total = s_pref[kThreads] * upi, q = quota_of(p, total, s_pref[kThreads + 1]);
     const int a = min(blockIdx.x * q, total), end = min(a + q, total);
 
     if (warp == kConsumers) {
@@ -254,14 +294,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             int base;
             locate<kThreads>(p, s_pref, upi, a, &cur.s, &cur.n, &base);
             cur.u = (a - base) / cur.n;
-            cur.tile = (a - base) % cur.n;
+            cur.at = (a - base) % cur.n;
             cur.ctx = min(p.context_lens[cur.s], min(p.max_context_len, p.max_blocks * B));
         }
         Window win = next_window(p, upi, a, end, pos, cur);
         int e0 = 0, e1 = 0;
         auto entries = [&](const Window& w, int& x0, int& x1) {
             const int32_t* row = p.block_tables + (int64_t)w.s * p.max_blocks;
-            const int j0 = w.t0 / B, nb = (w.t1 + B - 1) / B - j0;
+            const int j0 = w.t0 >> logB, nb = ((w.t1 + B - 1) >> logB) - j0;
             x0 = lane < nb ? row[j0 + lane] : 0;
             x1 = lane + 32 < nb ? row[j0 + lane + 32] : 0;
         };
@@ -285,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     return;
                 }
                 uint8_t* sb = smem + (size_t)stage * C::STAGE_BYTES;
-                const int nblk = (te - ts + B - 1) / B;
+                const int nblk = (te - ts + B - 1) >> logB;
                 const uint32_t qbytes = first ? (uint32_t)(nh * HD * QT::bytes) : 0u;
                 if (lane == 0) {
                     TileMeta m;
@@ -302,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)(nblk * tile_bytes) + qbytes);
                 }
                 __syncwarp();
-                const int rel = (ts - win.t0) / B + lane;
+                const int rel = ((ts - win.t0) >> logB) + lane;
                 const int pa = __shfl_sync(0xffffffffu, e0, rel & 31);
                 const int pb = __shfl_sync(0xffffffffu, e1, rel & 31);
                 if (lane < nblk) {
@@ -356,17 +396,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     const int g = lane >> 2, c = lane & 3;
     // this lane's places in a stage: ldmatrix row (token 16 warp + 8 (mi & 1) + r of chunk
     // mi >> 1), and the scale rows of tokens g, g + 8 (K) and 2c, 2c + 8 (V)
-    auto place = [&](int tok, int bytes) { return tok / B * tile_bytes + tok % B * bytes; };
+    auto place = [&](int tok, int bytes) { return (tok >> logB) * tile_bytes + (tok & (B - 1)) * bytes; };
     const int mi = lane >> 3;
+    const int two_chunks = 2 * B * 16;
     const uint32_t ld_off = place(16 * warp + 8 * (mi & 1) + (lane & 7), 16) + (mi >> 1) * B * 16;
     const int sc0 = B * (HD / 2);
-    const uint32_t ks_a = sc0 + place(16 * warp + g, HD / 16), ks_b = sc0 + place(16 * warp + g + 8, HD / 16);
-    const uint32_t vs_a = sc0 + place(16 * warp + 2 * c, HD / 16), vs_b = sc0 + place(16 * warp + 2 * c + 8, HD / 16);
+    const uint32_t ks_a = sc0 + place(16 * warp + g, HD / 16), vs_a = sc0 + place(16 * warp + 2 * c, HD / 16);
+    const int eight = B == 8 ? tile_bytes : 8 * (HD / 16);       // from a token's scales to token + 8's
     // byte picks: K scales of the chunks (dims 8c of each); V scales of tokens 2c, 2c + 1
     const uint32_t ksel = (c >> 1) ? 0x7531u : 0x6420u;
     const uint32_t vsel = (g >> 2) ? 0x7351u : 0x6240u;
 
-    uint32_t qf[C::NP][C::NCHUNK][4];     // per chunk: two k-steps of (b0, b1)
+    uint4* s_qf = reinterpret_cast<uint4*>(smem + C::OFF_QF);   // per chunk: two k-steps of (b0, b1)
     float o[2 * C::NCHUNK][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, qs0 = 0.f, qs1 = 0.f;
     int stage = 0;
@@ -381,18 +422,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         if (meta.flags & kDone) return;
         const uint8_t* sb = smem + (size_t)stage * C::STAGE_BYTES;
         if (meta.flags & kFirst) {
-            // q row of head g: dims 32 ch + 8c .. + 7, scaled by a power of two into fp16
-            float x[C::NCHUNK][8];
+            // q row of head g, scaled by a power of two into fp16; warp w forms the operands of
+            // chunks w, w + 4, ..: dims 32 ch + 8c .. + 7
+            const uint8_t* sq = sb + 2 * C::KV_BYTES + (g * HD + 8 * c) * QT::bytes;
             float amax = 0.f;
 #pragma unroll
             for (int ch = 0; ch < C::NCHUNK; ++ch) {
-                if (g < meta.nh)
-                    load8<QT>(sb + 2 * C::KV_BYTES + (g * HD + 32 * ch + 8 * c) * QT::bytes, x[ch]);
-                else
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (g < meta.nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[ch][i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = absmax_nan(x[ch][i], amax);
+                for (int i = 0; i < 8; ++i) amax = absmax_nan(x[i], amax);
             }
             amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
             amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 2), amax);
@@ -402,14 +441,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             const float qs = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
             qs0 = __shfl_sync(0xffffffffu, qs, 8 * c);
             qs1 = __shfl_sync(0xffffffffu, qs, 8 * c + 4);
-#pragma unroll
-            for (int ch = 0; ch < C::NCHUNK; ++ch)
+            for (int ch = warp; ch < C::NCHUNK; ch += kConsumers) {
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (g < meta.nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
+                uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float lo = x[ch][2 * i] * up, hi = x[ch][2 * i + 1] * up;
-                    qf[0][ch][i] = pack_f16(lo, hi);
-                    if constexpr (C::NP == 2) qf[1][ch][i] = pack_f16_rest(lo, hi, qf[0][ch][i]);
+                    const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
+                    hi[i] = pack_f16(x0, x1);
+                    lo[i] = C::NP == 2 ? pack_f16_rest(x0, x1, hi[i]) : 0u;
                 }
+                s_qf[ch * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if constexpr (C::NP == 2)
+                    s_qf[(C::NCHUNK + ch) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            // the operands are whole; the unit before is done with its own (it met at its end)
+            named_bar_sync(1, kConsumers * 32);
 #pragma unroll
             for (int mt = 0; mt < 2 * C::NCHUNK; ++mt)
 #pragma unroll
@@ -424,17 +471,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             uint32_t da, db;     // this lane's scale byte of every chunk, rows g and g + 8
             if constexpr (HD == 128) {
                 const uint2 ra = *reinterpret_cast<const uint2*>(sb + ks_a);
-                const uint2 rb = *reinterpret_cast<const uint2*>(sb + ks_b);
+                const uint2 rb = *reinterpret_cast<const uint2*>(sb + ks_a + eight);
                 da = __byte_perm(ra.x, ra.y, ksel);
                 db = __byte_perm(rb.x, rb.y, ksel);
             } else {
                 da = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_a), 0u, ksel);
-                db = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_b), 0u, ksel);
+                db = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_a + eight), 0u, ksel);
             }
 #pragma unroll
             for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
                 uint32_t r[4];
-                ldsm4(smem_addr(sb) + ld_off + 2 * cp * B * 16, r);
+                ldsm4(smem_addr(sb) + ld_off + cp * two_chunks, r);
                 // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
                 const uint32_t pa = e4m3x2_to_f16x2(cp ? da >> 16 : da & 0xffffu);
                 const uint32_t pb = e4m3x2_to_f16x2(cp ? db >> 16 : db & 0xffffu);
@@ -449,8 +496,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
 #pragma unroll
                     for (int t = 0; t < C::NP; ++t) {
-                        mma_f16(sa[0], a00, a01, a02, a03, qf[t][ch][0], qf[t][ch][1]);
-                        mma_f16(sa[1], a10, a11, a12, a13, qf[t][ch][2], qf[t][ch][3]);
+                        const uint4 qf = s_qf[(t * C::NCHUNK + ch) * 32 + lane];
+                        mma_f16(sa[0], a00, a01, a02, a03, qf.x, qf.y);
+                        mma_f16(sa[1], a10, a11, a12, a13, qf.z, qf.w);
                     }
                 }
             }
@@ -508,12 +556,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             uint32_t va[4], vb[4];      // scale bytes: tokens 2c (words 0, 1), 2c + 1 (2, 3); + 8
             if constexpr (HD == 128) {
                 const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_a);
-                const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_b);
+                const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_a + eight);
                 va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
                 vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
             } else {
                 const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_a);
-                const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_b);
+                const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_a + eight);
                 va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
                 va[1] = va[3] = vb[1] = vb[3] = 0u;
             }
@@ -526,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 #pragma unroll
             for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
                 uint32_t r[4];
-                ldsm4_trans(smem_addr(sv) + ld_off + 2 * cp * B * 16, r);
+                ldsm4_trans(smem_addr(sv) + ld_off + cp * two_chunks, r);
                 // bytes (2c, 2c + 1) of chunk 2cp's group, then of chunk 2cp + 1's
                 const uint32_t da = __byte_perm(va[cp], va[cp + 2], vsel);
                 const uint32_t db = __byte_perm(vb[cp], vb[cp + 2], vsel);
@@ -570,74 +618,84 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         float* xm = xa + kConsumers * kFp4Heads * C::HS;
         float* xl = xm + kConsumers * kFp4Heads;
         const int hw = warp * kFp4Heads + 2 * c;
-#pragma unroll
-        for (int mt = 0; mt < 2 * C::NCHUNK; ++mt) {
-            const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);      // o[.][2], o[.][3]: dim + 2
-            xa[hw * C::HS + dim] = o[mt][0];
-            xa[(hw + 1) * C::HS + dim] = o[mt][1];
-            xa[hw * C::HS + dim + 2] = o[mt][2];
-            xa[(hw + 1) * C::HS + dim + 2] = o[mt][3];
-        }
+        const int h = threadIdx.x >> 4, part = threadIdx.x & 15;    // 16 threads a head
+        const int64_t row = (int64_t)meta.s * p.num_q_heads + meta.kvh * p.group + meta.qsub * kFp4Heads + h;
+        const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.slot, 0)) * kFp4Heads + h;
         if (g == 0) {
             xm[hw] = m0;
             xm[hw + 1] = m1;
             xl[hw] = l0;
             xl[hw + 1] = l1;
         }
-        named_bar_sync(1, kConsumers * 32);
-        const int h = threadIdx.x >> 4, part = threadIdx.x & 15;    // 16 threads a head
-        if (h < meta.nh) {
-            float M = -INFINITY, L = 0.f, f[kConsumers];
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
+        for (int hf = 0; hf < 2; ++hf) {                            // half of the dims at a time
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) {
-                const float mw = xm[w * kFp4Heads + h];
-                f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-                L = fmaf(xl[w * kFp4Heads + h], f[w], L);
+            for (int mt = 0; mt < C::NCHUNK; ++mt) {
+                const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);  // [2], [3]: dim + 2
+                const float* v = o[hf * C::NCHUNK + mt];
+                if (2 * c < meta.nh) {
+                    xa[hw * C::HS + dim] = v[0];
+                    xa[hw * C::HS + dim + 2] = v[2];
+                }
+                if (2 * c + 1 < meta.nh) {
+                    xa[(hw + 1) * C::HS + dim] = v[1];
+                    xa[(hw + 1) * C::HS + dim + 2] = v[3];
+                }
             }
-            const int head = meta.kvh * p.group + meta.qsub * kFp4Heads + h;
-            const int64_t row = (int64_t)meta.s * p.num_q_heads + head;
-            const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.slot, 0)) * kFp4Heads + h;
-            const float inv = p.out_scale / L;
+            named_bar_sync(1, kConsumers * 32);
+            if (h < meta.nh) {
+                float M = -INFINITY, L = 0.f, f[kConsumers];
 #pragma unroll
-            for (int i = 0; i < HD / 16; ++i) {
-                const int dim = part + 16 * i;
-                float A = 0.f;
+                for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w)
-                    A = fmaf(xa[(w * kFp4Heads + h) * C::HS + dim], f[w], A);
-                if (meta.slot < 0) store_from_float<QT>(p.out, row * HD + dim, A * inv);
-                else p.part_acc[pi * HD + dim] = A;
+                for (int w = 0; w < kConsumers; ++w) {
+                    const float mw = xm[w * kFp4Heads + h];
+                    f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+                    L = fmaf(xl[w * kFp4Heads + h], f[w], L);
+                }
+                const float inv = p.out_scale / L;
+#pragma unroll
+                for (int i = 0; i < C::XD / 16; ++i) {
+                    const int dim = part + 16 * i;
+                    float A = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kConsumers; ++w)
+                        A = fmaf(xa[(w * kFp4Heads + h) * C::HS + dim], f[w], A);
+                    if (meta.slot < 0) store_from_float<QT>(p.out, row * HD + hf * C::XD + dim, A * inv);
+                    else p.part_acc[pi * HD + hf * C::XD + dim] = A;
+                }
+                if (meta.slot >= 0 && part == 0 && hf == 0) {
+                    p.part_ml[2 * pi] = M;
+                    p.part_ml[2 * pi + 1] = L;
+                }
             }
-            if (meta.slot >= 0 && part == 0) {
-                p.part_ml[2 * pi] = M;
-                p.part_ml[2 * pi + 1] = L;
-            }
+            named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
         }
-        named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
     }
 }
 
-// CTA b looks at the boundary between workers b and b + 1: if it cuts a unit and is the first to
-// do so, the CTA joins the unit's partial states (worker order) and writes its heads.  Sixteen
-// warps share the heads: warp w takes head w % nh's pieces w / nh, w / nh + 16 / nh, ...
+// CTA b looks at the boundary between workers b and b + 1: if it cuts a unit's tiles and is the
+// first to do so, the CTA joins the unit's partial states and writes its heads.  Sixteen warps
+// share the heads: warp w takes head w % nh's pieces w / nh, w / nh + 16 / nh, ..., four pieces'
+// loads in flight at once; the order of the sums is fixed.
 template <typename QT, int HD>
 __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Params p) {
-    constexpr int WARPS = kMergeThreads / 32, V = HD / 32;      // dims of a lane
-    __shared__ int s_pref[kMergeThreads + 1], s_wsum[WARPS];
+    constexpr int WARPS = kMergeThreads / 32, V = HD / 32, FLY = 4;   // dims of a lane
+    __shared__ int s_pref[kMergeThreads + 2];
+    __shared__ int2 s_wsum[WARPS];
     __shared__ float s_acc[WARPS][HD], s_m[WARPS], s_l[WARPS];
-    scan_tiles<kMergeThreads>(p, s_pref, s_wsum);
+    scan_slots<kMergeThreads>(p, s_pref, s_wsum);
     const int upi = p.num_kv_heads * p.nsub;
-    const int total = s_pref[kMergeThreads] * upi, q = quota_of(p, total);
+    const int total = s_pref[kMergeThreads] * upi;
+    const int q = quota_of(p, total, s_pref[kMergeThreads + 1]);
     const int pos = (blockIdx.x + 1) * q;
-    pdl_wait();                // the partial states are written; also in CTAs without a boundary:
-    if (pos >= total) return;  // this grid must not end before the decode has
-    int s, n, base;
-    locate<kMergeThreads>(p, s_pref, upi, pos, &s, &n, &base);
-    const int u = (pos - base) / n, ustart = base + u * n, uend = ustart + n;
-    const int w0 = ustart / q, w1 = (uend - 1) / q;             // workers of the unit
-    if (ustart == pos || w0 != blockIdx.x) return;
+    int s = 0, n = 1, base = 0;
+    if (pos < total) locate<kMergeThreads>(p, s_pref, upi, pos, &s, &n, &base);
+    pdl_wait();                // the partial states are written; also in CTAs without a unit:
+                               // this grid must not end before the decode has
+    const int u = (pos - base) / n, dstart = base + u * n + kFp4UnitCost, uend = base + (u + 1) * n;
+    const int w0 = dstart / q, w1 = (uend - 1) / q;             // workers of the unit's tiles
+    if (pos >= total || pos <= dstart || w0 != blockIdx.x) return;
     const int kvh = u / p.nsub, qsub = u % p.nsub;
     const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -646,19 +704,32 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Param
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = 0.f;
     if (warp / nh < step)
-        for (int w = w0 + warp / nh; w <= w1; w += step) {
-            // a worker's slot 0 is the unit it starts inside of, slot 1 the one it ends inside of
-            const int64_t pi = ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * kFp4Heads + h;
-            const float m = __ldcg(p.part_ml + 2 * pi), l = __ldcg(p.part_ml + 2 * pi + 1);
-            float a[V];
+        for (int w = w0 + warp / nh; w <= w1; w += FLY * step) {
+            float m[FLY], l[FLY], a[FLY][V], Mn = M;
 #pragma unroll
-            for (int i = 0; i < V; ++i) a[i] = __ldcg(p.part_acc + pi * HD + lane + 32 * i);
-            const float Mn = fmaxf(M, m);
+            for (int k = 0; k < FLY; ++k) {
+                // a worker's state 0 is the unit it starts inside of, 1 the one it ends inside of
+                const int wk = w + k * step;
+                const int64_t pi = ((int64_t)wk * 2 + (wk == w0 ? 1 : 0)) * kFp4Heads + h;
+                m[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi) : -INFINITY;
+                l[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi + 1) : 0.f;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    a[k][i] = wk <= w1 ? __ldcg(p.part_acc + pi * HD + lane + 32 * i) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < FLY; ++k) Mn = fmaxf(Mn, m[k]);
             const float fo = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-            const float fn = m == -INFINITY ? 0.f : fast_exp2(m - Mn);
-            L = L * fo + l * fn;
+            L *= fo;
 #pragma unroll
-            for (int i = 0; i < V; ++i) A[i] = A[i] * fo + a[i] * fn;
+            for (int i = 0; i < V; ++i) A[i] *= fo;
+#pragma unroll
+            for (int k = 0; k < FLY; ++k) {
+                const float f = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - Mn);
+                L = fmaf(l[k], f, L);
+#pragma unroll
+                for (int i = 0; i < V; ++i) A[i] = fmaf(a[k][i], f, A[i]);
+            }
             M = Mn;
         }
 #pragma unroll

@@ -6,7 +6,9 @@
 namespace pkv {
 
 constexpr int kFp4Tile = 64;          // tokens of a tile: the split's unit and a ring stage
-constexpr int kFp4MinQuota = 2;       // tiles a worker takes at least
+constexpr int kFp4UnitCost = 1;       // slots of a unit besides its tiles
+constexpr int kFp4MinQuota = 2;       // slots a worker takes at least
+constexpr int kFp4MaxPieces = 64;     // partial states that one unit leaves, about
 constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most
 constexpr int kFp4Heads = 8;          // query heads of a work unit
 
@@ -22,6 +24,7 @@ struct DecodeFp4Params {
     float* part_ml;        // [workers * 2][kFp4Heads][2]: running max (log2 domain) and sum
     int num_seqs, num_q_heads, num_kv_heads, group, nsub;
     int head_dim, block_size, num_blocks, max_blocks, max_context_len;
+    int log_block;         // block_size == 1 << log_block
     int workers;           // the split's denominator: every CTA the device holds
     int max_workers;       // workers that can have work, by max_context_len
     float qk_scale_log2;   // scale * log2(e) * kv_scale
@@ -31,9 +34,9 @@ struct DecodeFp4Params {
 
 // Workers that can have work over contexts up to max_ctx: bounds grid and workspace.
 inline int64_t fp4_max_workers(int num_seqs, int num_kv_heads, int nsub, int max_ctx) {
-    const int64_t tiles = (int64_t)num_seqs * num_kv_heads * nsub *
-                          ((max_ctx + kFp4Tile - 1) / kFp4Tile);
-    const int64_t w = (tiles + kFp4MinQuota - 1) / kFp4MinQuota;
+    const int64_t slots = (int64_t)num_seqs * num_kv_heads * nsub *
+                          (((int64_t)max_ctx + kFp4Tile - 1) / kFp4Tile + kFp4UnitCost);
+    const int64_t w = (slots + kFp4MinQuota - 1) / kFp4MinQuota;
     return w < 1 ? 1 : (w < kFp4MaxWorkers ? w : kFp4MaxWorkers);
 }
 
