@@ -184,6 +184,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     if (st != PKV_OK) return st;
     if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size)
         return PKV_ERR_INVALID_ARG;
+    if (fp4 && (int64_t)num_blocks * num_kv_heads * 2 > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
     if (!query || !k_cache || !v_cache || !block_tables || !context_lens || !out)
         return PKV_ERR_INVALID_ARG;

@@ -32,9 +32,21 @@
 #include "decode_fp4.cuh"
 
 #include "cache_row.cuh"
+#include "tmap.cuh"
 
 namespace pkv {
 namespace {
+
+// Four rows of a 2-D tensor by their indices into consecutive rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, int y0, int y1,
+                                            int y2, int y3, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
+        ::"r"(smem_addr(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y0), "r"(y1),
+        "r"(y2), "r"(y3), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -111,22 +123,16 @@ struct Cfg {
     static constexpr int HS = XD + 1;                  // exchange stride of a head: few conflicts
     static constexpr int XBUF = kConsumers * kFp4Heads * (HS + 2);    // acc, then m, l
     static constexpr size_t OFF_META = (size_t)NSTAGE * STAGE_BYTES;
-    static constexpr size_t OFF_BARS = OFF_META + NSTAGE * 32;
+    static constexpr size_t OFF_BARS = OFF_META + NSTAGE * 16;
     static constexpr size_t OFF_QF = (OFF_BARS + 2 * NSTAGE * 8 + 15) / 16 * 16;
     static constexpr size_t OFF_X = OFF_QF + NP * NCHUNK * 32 * 16;
-    static constexpr size_t SMEM = OFF_X + XBUF * 4;
+    static constexpr size_t SMEM = OFF_X + XBUF * 4 + 128;             // the base is rounded up
     // resident CTAs, by registers.  The queries' operands stay in shared memory (a 16-byte load a
     // chunk): 187 -> 175 us on long documents against registers.  A fifth CTA (72 registers) spills
     // and loses: 200 us.
     static constexpr int CTAS = NP == 1 ? 4 : 3;
 };
 
-struct TileMeta {
-    int flags, n;            // kFirst.., valid tokens of the tile
-    int s, kvh, qsub, nh;
-    int slot;                // partial slot of the worker, or -1: the whole unit is here
-    int pad;
-};
 constexpr int kFirst = 1, kLast = 2, kDone = 4;
 
 // Tiles of a sequence's context, per unit.
@@ -214,7 +220,7 @@ struct Cursor {
     int s, u, at, n, ctx;
 };
 
-// A run of at most 64 blocks of one unit.
+// A run of at most 32 pool rows (8 or 16 tokens each) of one unit.
 struct Window {
     int valid, s, u, t0, t1;     // tokens [t0, t1)
     int first, last, slot;
@@ -243,7 +249,7 @@ __device__ __forceinline__ Window next_window(const DecodeFp4Params& p, int upi,
         c.at = kFp4UnitCost;
     }
     const int tile = c.at - kFp4UnitCost, tiles = c.n - kFp4UnitCost;
-    const int wt = min(min(p.block_size, tiles - tile), end - pos);   // <= 64 blocks
+    const int wt = min(min(p.block_size == 8 ? 4 : 8, tiles - tile), end - pos);
     const int dstart = pos - tile, uend = dstart + tiles;
     w.valid = 1;
     w.s = c.s;
@@ -260,12 +266,15 @@ __device__ __forceinline__ Window next_window(const DecodeFp4Params& p, int upi,
 
 template <typename QT, int HD>
 __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
-    decode_fp4_kernel(DecodeFp4Params p) {
+    decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<QT, HD>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 127u);
     __shared__ int s_pref[kThreads + 2];
     __shared__ int2 s_wsum[kThreads / 32];
-    TileMeta* metas = reinterpret_cast<TileMeta*>(smem + C::OFF_META);
+    // of a tile: {flags | tokens << 8, sequence, unit, partial state or -1: the whole unit is here}
+    int4* metas = reinterpret_cast<int4*>(smem + C::OFF_META);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     uint64_t* empty = full + C::NSTAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -297,85 +306,77 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             cur.at = (a - base) % cur.n;
             cur.ctx = min(p.context_lens[cur.s], min(p.max_context_len, p.max_blocks * B));
         }
+        if (lane == 0) {
+            prefetch_tensormap(&map_k);
+            prefetch_tensormap(&map_v);
+        }
+        // a pool row is a whole tile of 8 or 16 tokens, or half of a tile of 32
+        const int log_rt = min(logB, 4), per_block = logB - log_rt;
         Window win = next_window(p, upi, a, end, pos, cur);
-        int e0 = 0, e1 = 0;
-        auto entries = [&](const Window& w, int& x0, int& x1) {
-            const int32_t* row = p.block_tables + (int64_t)w.s * p.max_blocks;
-            const int j0 = w.t0 >> logB, nb = ((w.t1 + B - 1) >> logB) - j0;
-            x0 = lane < nb ? row[j0 + lane] : 0;
-            x1 = lane + 32 < nb ? row[j0 + lane + 32] : 0;
-        };
-        if (win.valid) entries(win, e0, e1);
-        while (win.valid) {
-            const bool bad0 = e0 < 0 || e0 >= p.num_blocks, bad1 = e1 < 0 || e1 >= p.num_blocks;
-            if (bad0 || bad1) {
+        // a lane's pool row of the window (beyond the context's last block: that one's again)
+        auto pool_row = [&](const Window& w) {
+            const int j0 = w.t0 >> logB, blocks = ((w.t1 - 1) >> logB) - j0 + 1;
+            const int i = min(lane, (blocks << per_block) - 1);
+            int blk = p.block_tables[(int64_t)w.s * p.max_blocks + j0 + (i >> per_block)];
+            if (blk < 0 || blk >= p.num_blocks) {
                 set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
-                if (bad0) e0 = 0;
-                if (bad1) e1 = 0;
+                blk = 0;
             }
+            const int tile = blk * p.num_kv_heads + w.u / p.nsub;
+            return per_block ? 2 * tile + (i & 1) : tile;
+        };
+        int rows = win.valid ? pool_row(win) : 0;
+        while (win.valid) {
             const int kvh = win.u / p.nsub, qsub = win.u % p.nsub;
-            const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
+            const int qrow = win.s * p.num_q_heads + kvh * p.group + qsub * kFp4Heads;
+            const uint32_t qbytes = min(kFp4Heads, p.group - qsub * kFp4Heads) * (HD * QT::bytes);
             Window nxt{};
-            int n0 = 0, n1 = 0;
+            int nrows = 0;
             for (int ts = win.t0; ts < win.t1; ts += kFp4Tile) {
-                const int te = min(ts + kFp4Tile, win.t1);
                 const bool first = win.first && ts == win.t0;
+                const int flags = (first ? kFirst : 0) | (win.last && ts + kFp4Tile >= win.t1 ? kLast : 0);
+                const int r = (ts - win.t0) >> log_rt;
+                int y[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, rows, r + k);
+                if (log_rt == 3)
+#pragma unroll
+                    for (int k = 4; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, rows, r + k);
                 if (!mbar_wait(&empty[stage], phase ^ 1u)) {
                     set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
                     return;
                 }
-                uint8_t* sb = smem + (size_t)stage * C::STAGE_BYTES;
-                const int nblk = (te - ts + B - 1) >> logB;
-                const uint32_t qbytes = first ? (uint32_t)(nh * HD * QT::bytes) : 0u;
                 if (lane == 0) {
-                    TileMeta m;
-                    m.flags = (first ? kFirst : 0) |
-                              (win.last && ts + kFp4Tile >= win.t1 ? kLast : 0);
-                    m.n = te - ts;
-                    m.s = win.s;
-                    m.kvh = kvh;
-                    m.qsub = qsub;
-                    m.nh = nh;
-                    m.slot = win.slot;
-                    m.pad = 0;
-                    metas[stage] = m;
-                    mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)(nblk * tile_bytes) + qbytes);
+                    uint8_t* sb = smem + stage * C::STAGE_BYTES;
+                    metas[stage] = make_int4(flags | min(kFp4Tile, win.t1 - ts) << 8, win.s, win.u, win.slot);
+                    mbar_arrive_expect_tx(&full[stage], 2u * C::KV_BYTES + (first ? qbytes : 0u));
+                    tma_gather4(sb, &map_k, y[0], y[1], y[2], y[3], &full[stage], policy);
+                    tma_gather4(sb + C::KV_BYTES, &map_v, y[0], y[1], y[2], y[3], &full[stage], policy);
+                    if (log_rt == 3) {
+                        tma_gather4(sb + C::KV_BYTES / 2, &map_k, y[4], y[5], y[6], y[7], &full[stage], policy);
+                        tma_gather4(sb + C::KV_BYTES * 3 / 2, &map_v, y[4], y[5], y[6], y[7], &full[stage], policy);
+                    }
+                    if (first)
+                        bulk_g2s(sb + 2 * C::KV_BYTES,
+                                 static_cast<const uint8_t*>(p.q) + (int64_t)qrow * HD * QT::bytes,
+                                 qbytes, &full[stage]);
                 }
                 __syncwarp();
-                const int rel = ((ts - win.t0) >> logB) + lane;
-                const int pa = __shfl_sync(0xffffffffu, e0, rel & 31);
-                const int pb = __shfl_sync(0xffffffffu, e1, rel & 31);
-                if (lane < nblk) {
-                    const int64_t off =
-                        ((int64_t)(rel < 32 ? pa : pb) * p.num_kv_heads + kvh) * tile_bytes;
-                    bulk_g2s_hint(sb + lane * tile_bytes, static_cast<const uint8_t*>(p.k_cache) + off,
-                                  (uint32_t)tile_bytes, &full[stage], policy);
-                    bulk_g2s_hint(sb + C::KV_BYTES + lane * tile_bytes,
-                                  static_cast<const uint8_t*>(p.v_cache) + off,
-                                  (uint32_t)tile_bytes, &full[stage], policy);
-                }
-                if (qbytes && lane == 31) {
-                    const int64_t row = (int64_t)win.s * p.num_q_heads + kvh * p.group + qsub * kFp4Heads;
-                    bulk_g2s(sb + 2 * C::KV_BYTES,
-                             static_cast<const uint8_t*>(p.q) + row * HD * QT::bytes, qbytes,
-                             &full[stage]);
-                }
                 if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
                 if (ts == win.t0) {      // look ahead: the next window's entries load meanwhile
                     nxt = next_window(p, upi, a, end, pos, cur);
-                    if (nxt.valid) entries(nxt, n0, n1);
+                    if (nxt.valid) nrows = pool_row(nxt);
                 }
             }
             win = nxt;
-            e0 = n0;
-            e1 = n1;
+            rows = nrows;
         }
         if (!mbar_wait(&empty[stage], phase ^ 1u)) {
             set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
             return;
         }
         if (lane == 0) {
-            metas[stage].flags = kDone;
+            metas[stage].x = kDone;
             mbar_arrive(&full[stage]);
         }
         return;
@@ -418,10 +419,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
             return;
         }
-        const TileMeta meta = metas[stage];
-        if (meta.flags & kDone) return;
-        const uint8_t* sb = smem + (size_t)stage * C::STAGE_BYTES;
-        if (meta.flags & kFirst) {
+        const int4 meta = metas[stage];
+        if (meta.x & kDone) return;
+        const uint8_t* sb = smem + stage * C::STAGE_BYTES;
+        if (meta.x & kFirst) {
+            const int nh = min(kFp4Heads, p.group - meta.z % p.nsub * kFp4Heads);
             // q row of head g, scaled by a power of two into fp16; warp w forms the operands of
             // chunks w, w + 4, ..: dims 32 ch + 8c .. + 7
             const uint8_t* sq = sb + 2 * C::KV_BYTES + (g * HD + 8 * c) * QT::bytes;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 #pragma unroll
             for (int ch = 0; ch < C::NCHUNK; ++ch) {
                 float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (g < meta.nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
+                if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) amax = absmax_nan(x[i], amax);
             }
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             qs1 = __shfl_sync(0xffffffffu, qs, 8 * c + 4);
             for (int ch = warp; ch < C::NCHUNK; ch += kConsumers) {
                 float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (g < meta.nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
+                if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.f;
         }
-        const int nv = meta.n - 16 * warp;          // valid tokens of this warp's 16
+        const int nv = (meta.x >> 8) - 16 * warp;          // valid tokens of this warp's 16
         if (nv > 0) {
             // ---- S^T = K Q^T ----
             float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
         if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
-        if (!(meta.flags & kLast)) continue;
+        if (!(meta.x & kLast)) continue;
 
         // ---------------- end of the segment: the four warps' states meet ----------------
 #pragma unroll
@@ -614,13 +616,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             l0 += __shfl_xor_sync(0xffffffffu, l0, off);
             l1 += __shfl_xor_sync(0xffffffffu, l1, off);
         }
+        const int kvh = meta.z / p.nsub, qsub = meta.z % p.nsub;
+        const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
         float* xa = reinterpret_cast<float*>(smem + C::OFF_X);
         float* xm = xa + kConsumers * kFp4Heads * C::HS;
         float* xl = xm + kConsumers * kFp4Heads;
         const int hw = warp * kFp4Heads + 2 * c;
         const int h = threadIdx.x >> 4, part = threadIdx.x & 15;    // 16 threads a head
-        const int64_t row = (int64_t)meta.s * p.num_q_heads + meta.kvh * p.group + meta.qsub * kFp4Heads + h;
-        const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.slot, 0)) * kFp4Heads + h;
+        const int64_t row = (int64_t)meta.y * p.num_q_heads + kvh * p.group + qsub * kFp4Heads + h;
+        const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.w, 0)) * kFp4Heads + h;
         if (g == 0) {
             xm[hw] = m0;
             xm[hw + 1] = m1;
@@ -633,17 +637,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             for (int mt = 0; mt < C::NCHUNK; ++mt) {
                 const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);  // [2], [3]: dim + 2
                 const float* v = o[hf * C::NCHUNK + mt];
-                if (2 * c < meta.nh) {
+                if (2 * c < nh) {
                     xa[hw * C::HS + dim] = v[0];
                     xa[hw * C::HS + dim + 2] = v[2];
                 }
-                if (2 * c + 1 < meta.nh) {
+                if (2 * c + 1 < nh) {
                     xa[(hw + 1) * C::HS + dim] = v[1];
                     xa[(hw + 1) * C::HS + dim + 2] = v[3];
                 }
             }
             named_bar_sync(1, kConsumers * 32);
-            if (h < meta.nh) {
+            if (h < nh) {
                 float M = -INFINITY, L = 0.f, f[kConsumers];
 #pragma unroll
                 for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
@@ -661,10 +665,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 #pragma unroll
                     for (int w = 0; w < kConsumers; ++w)
                         A = fmaf(xa[(w * kFp4Heads + h) * C::HS + dim], f[w], A);
-                    if (meta.slot < 0) store_from_float<QT>(p.out, row * HD + hf * C::XD + dim, A * inv);
+                    if (meta.w < 0) store_from_float<QT>(p.out, row * HD + hf * C::XD + dim, A * inv);
                     else p.part_acc[pi * HD + hf * C::XD + dim] = A;
                 }
-                if (meta.slot >= 0 && part == 0 && hf == 0) {
+                if (meta.w >= 0 && part == 0 && hf == 0) {
                     p.part_ml[2 * pi] = M;
                     p.part_ml[2 * pi + 1] = L;
                 }
@@ -779,6 +783,13 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
         workers[dev] = w < kFp4MaxWorkers ? w : kFp4MaxWorkers;
     }
     DecodeFp4Params p = p0;
+    // pools as rows of 16 tokens of one kv head (8 in blocks of 8): what one gather moves four of
+    const int rt = p.block_size < 16 ? p.block_size : 16;
+    const long long pool_rows = (long long)p.num_blocks * p.num_kv_heads * (p.block_size / rt);
+    CUtensorMap map_k, map_v;
+    if (!encode_rows_map(&map_k, p.k_cache, rt * C::ROWB, pool_rows) ||
+        !encode_rows_map(&map_v, p.v_cache, rt * C::ROWB, pool_rows))
+        return cudaErrorInvalidValue;
     p.workers = workers[dev];
     p.two4 = 1u << 4;
     p.two12 = 1u << 12;
@@ -794,7 +805,7 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kernel, p);
+    err = cudaLaunchKernelEx(&cfg, kernel, p, map_k, map_v);
     if (err != cudaSuccess || grid == 1) return err;      // one worker cuts nothing
     cfg.gridDim = dim3((unsigned)(grid - 1), 1, 1);
     cfg.blockDim = dim3(kMergeThreads, 1, 1);

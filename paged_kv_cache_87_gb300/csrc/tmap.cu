@@ -67,6 +67,21 @@ bool encode_pool_map_grouped(CUtensorMap* map, const void* pool, long long rows,
            CUDA_SUCCESS;
 }
 
+bool encode_rows_map(CUtensorMap* map, const void* pool, int row_bytes, long long rows) {
+    EncodeTiled enc = encoder();
+    if (!enc || rows <= 0 || rows > 0x7fffffffLL || row_bytes % 16 != 0 || row_bytes > 2048)
+        return false;
+    // 8-byte elements, a box of one whole row; rows land one behind the other
+    const cuuint64_t dims[2] = {(cuuint64_t)(row_bytes / 8), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)(row_bytes / 8), 1};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(pool), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 bool encode_q_map(CUtensorMap* map, const void* q, long long total_q, int num_q_heads, int group) {
     EncodeTiled enc = encoder();
     if (!enc || total_q <= 0 || total_q > 0x7fffffffLL || num_q_heads <= 0 || group <= 0 ||

@@ -16,6 +16,10 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, int head_dim, int elem_
 // swizzled, so the 8-row groups of a half are 2 KB apart across blocks.
 bool encode_pool_map_grouped(CUtensorMap* map, const void* pool, long long rows, int box_rows);
 
+// `rows` rows of `row_bytes` bytes (a multiple of 16, at most 2,048), box = one row, no swizzle:
+// for gathers of rows by their indices.
+bool encode_rows_map(CUtensorMap* map, const void* pool, int row_bytes, long long rows);
+
 // The queries [total_q][num_q_heads][128] (16-bit) as (element, head, token): one box
 // of 64 elements x `group` heads x 128 / group tokens is one 128-byte half of the
 // 128 (query token, head of a kv head's group) rows of a multi-query row tile,
