@@ -130,7 +130,7 @@ struct Cfg {
     // resident CTAs, by registers.  The queries' operands stay in shared memory (a 16-byte load a
     // chunk): 187 -> 175 us on long documents against registers.  A fifth CTA (72 registers) spills
     // and loses: 200 us.
-    static constexpr int CTAS = NP == 1 ? 4 : 3;
+    static constexpr int CTAS = 3;
 };
 
 constexpr int kFirst = 1, kLast = 2, kDone = 4;
@@ -249,7 +249,7 @@ __device__ __forceinline__ Window next_window(const DecodeFp4Params& p, int upi,
         c.at = kFp4UnitCost;
     }
     const int tile = c.at - kFp4UnitCost, tiles = c.n - kFp4UnitCost;
-    const int wt = min(min(p.block_size == 8 ? 4 : 8, tiles - tile), end - pos);
+    const int wt = min(min(p.block_size == 8 ? 2 : 4, tiles - tile), end - pos);
     const int dstart = pos - tile, uend = dstart + tiles;
     w.valid = 1;
     w.s = c.s;
@@ -335,31 +335,31 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             for (int ts = win.t0; ts < win.t1; ts += kFp4Tile) {
                 const bool first = win.first && ts == win.t0;
                 const int flags = (first ? kFirst : 0) | (win.last && ts + kFp4Tile >= win.t1 ? kLast : 0);
-                const int r = (ts - win.t0) >> log_rt;
-                int y[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, rows, r + k);
-                if (log_rt == 3)
-#pragma unroll
-                    for (int k = 4; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, rows, r + k);
+                const int n = min(kFp4Tile, win.t1 - ts), r = (ts - win.t0) >> log_rt;
+                // 32 or 64 tokens a gather; those past the context's last block stay out
+                const int per = 4 << log_rt, gathers = (n + per - 1) / per;
                 if (!mbar_wait(&empty[stage], phase ^ 1u)) {
                     set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
                     return;
                 }
+                uint8_t* sb = smem + stage * C::STAGE_BYTES;
                 if (lane == 0) {
-                    uint8_t* sb = smem + stage * C::STAGE_BYTES;
-                    metas[stage] = make_int4(flags | min(kFp4Tile, win.t1 - ts) << 8, win.s, win.u, win.slot);
-                    mbar_arrive_expect_tx(&full[stage], 2u * C::KV_BYTES + (first ? qbytes : 0u));
-                    tma_gather4(sb, &map_k, y[0], y[1], y[2], y[3], &full[stage], policy);
-                    tma_gather4(sb + C::KV_BYTES, &map_v, y[0], y[1], y[2], y[3], &full[stage], policy);
-                    if (log_rt == 3) {
-                        tma_gather4(sb + C::KV_BYTES / 2, &map_k, y[4], y[5], y[6], y[7], &full[stage], policy);
-                        tma_gather4(sb + C::KV_BYTES * 3 / 2, &map_v, y[4], y[5], y[6], y[7], &full[stage], policy);
-                    }
+                    metas[stage] = make_int4(flags | n << 8, win.s, win.u, win.slot);
+                    mbar_arrive_expect_tx(&full[stage], 2u * C::ROWB * per * gathers + (first ? qbytes : 0u));
                     if (first)
                         bulk_g2s(sb + 2 * C::KV_BYTES,
                                  static_cast<const uint8_t*>(p.q) + (int64_t)qrow * HD * QT::bytes,
                                  qbytes, &full[stage]);
+                }
+                for (int k = 0; k < gathers; ++k) {
+                    int y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, rows, r + 4 * k + i);
+                    if (lane == 0) {
+                        tma_gather4(sb + k * (per * C::ROWB), &map_k, y[0], y[1], y[2], y[3], &full[stage], policy);
+                        tma_gather4(sb + C::KV_BYTES + k * (per * C::ROWB), &map_v, y[0], y[1], y[2], y[3],
+                                    &full[stage], policy);
+                    }
                 }
                 __syncwarp();
                 if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
@@ -394,8 +394,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     store_from_float<QT>(p.out, (int64_t)s * row + i, 0.f);
         }
     }
+    constexpr int SUB = kFp4Tile / 64, SUB_BYTES = 64 * C::ROWB;    // a warp's pieces of a tile
     const int g = lane >> 2, c = lane & 3;
-    // this lane's places in a stage: ldmatrix row (token 16 warp + 8 (mi & 1) + r of chunk
+    // this lane's places in a piece: ldmatrix row (token 16 warp + 8 (mi & 1) + r of chunk
     // mi >> 1), and the scale rows of tokens g, g + 8 (K) and 2c, 2c + 8 (V)
     auto place = [&](int tok, int bytes) { return (tok >> logB) * tile_bytes + (tok & (B - 1)) * bytes; };
     const int mi = lane >> 3;
@@ -466,57 +467,90 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.f;
         }
-        const int nv = (meta.x >> 8) - 16 * warp;          // valid tokens of this warp's 16
+        const int nv = (meta.x >> 8) - 16 * warp;   // tokens of the tile from this warp's first on
         if (nv > 0) {
+            // two pieces of 16 tokens, 64 apart: their valid tokens (negative: none)
+            const bool part = nv < 64 + 16;
             // ---- S^T = K Q^T ----
-            float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            uint32_t da, db;     // this lane's scale byte of every chunk, rows g and g + 8
-            if constexpr (HD == 128) {
-                const uint2 ra = *reinterpret_cast<const uint2*>(sb + ks_a);
-                const uint2 rb = *reinterpret_cast<const uint2*>(sb + ks_a + eight);
-                da = __byte_perm(ra.x, ra.y, ksel);
-                db = __byte_perm(rb.x, rb.y, ksel);
-            } else {
-                da = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_a), 0u, ksel);
-                db = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_a + eight), 0u, ksel);
+            float sa[SUB][2][4];
+            uint32_t da[SUB], db[SUB];     // this lane's scale byte of every chunk, rows g and g + 8
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sa[u][0][i] = sa[u][1][i] = 0.f;
+                const uint8_t* sc = sb + u * SUB_BYTES + ks_a;
+                if constexpr (HD == 128) {
+                    const uint2 ra = *reinterpret_cast<const uint2*>(sc);
+                    const uint2 rb = *reinterpret_cast<const uint2*>(sc + eight);
+                    da[u] = __byte_perm(ra.x, ra.y, ksel);
+                    db[u] = __byte_perm(rb.x, rb.y, ksel);
+                } else {
+                    da[u] = __byte_perm(*reinterpret_cast<const uint32_t*>(sc), 0u, ksel);
+                    db[u] = __byte_perm(*reinterpret_cast<const uint32_t*>(sc + eight), 0u, ksel);
+                }
             }
 #pragma unroll
             for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
-                uint32_t r[4];
-                ldsm4(smem_addr(sb) + ld_off + cp * two_chunks, r);
-                // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
-                const uint32_t pa = e4m3x2_to_f16x2(cp ? da >> 16 : da & 0xffffu);
-                const uint32_t pb = e4m3x2_to_f16x2(cp ? db >> 16 : db & 0xffffu);
+                uint4 qf[C::NP][2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int ch = 2 * cp + k;
-                    const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
-                    const uint32_t fa = half_twice(pa, k), fb = half_twice(pb, k);
-                    const uint32_t a00 = hmul2(e2m1x2_to_f16x2<0>(wa), fa), a01 = hmul2(e2m1x2_to_f16x2<0>(wb), fb);
-                    const uint32_t a02 = hmul2(e2m1x2_to_f16x2<1>(wa), fa), a03 = hmul2(e2m1x2_to_f16x2<1>(wb), fb);
-                    const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
-                    const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
+                for (int t = 0; t < C::NP; ++t)
 #pragma unroll
-                    for (int t = 0; t < C::NP; ++t) {
-                        const uint4 qf = s_qf[(t * C::NCHUNK + ch) * 32 + lane];
-                        mma_f16(sa[0], a00, a01, a02, a03, qf.x, qf.y);
-                        mma_f16(sa[1], a10, a11, a12, a13, qf.z, qf.w);
+                    for (int k = 0; k < 2; ++k) qf[t][k] = s_qf[(t * C::NCHUNK + 2 * cp + k) * 32 + lane];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t r[4];
+                    ldsm4(smem_addr(sb) + u * SUB_BYTES + ld_off + cp * two_chunks, r);
+                    // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
+                    const uint32_t pa = e4m3x2_to_f16x2(cp ? da[u] >> 16 : da[u] & 0xffffu);
+                    const uint32_t pb = e4m3x2_to_f16x2(cp ? db[u] >> 16 : db[u] & 0xffffu);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                        const uint32_t fa = half_twice(pa, k), fb = half_twice(pb, k);
+                        const uint32_t a00 = hmul2(e2m1x2_to_f16x2<0>(wa), fa), a01 = hmul2(e2m1x2_to_f16x2<0>(wb), fb);
+                        const uint32_t a02 = hmul2(e2m1x2_to_f16x2<1>(wa), fa), a03 = hmul2(e2m1x2_to_f16x2<1>(wb), fb);
+                        const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
+                        const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
+#pragma unroll
+                        for (int t = 0; t < C::NP; ++t) {
+                            mma_f16(sa[u][0], a00, a01, a02, a03, qf[t][k].x, qf[t][k].y);
+                            mma_f16(sa[u][1], a10, a11, a12, a13, qf[t][k].z, qf[t][k].w);
+                        }
                     }
                 }
             }
-            // ---- running softmax: tokens g (y0, y1) and g + 8 (y2, y3), heads 2c and 2c + 1;
-            // y = logit - (running max - kLift), log2 domain ----
-            const float z0 = sa[0][0] + sa[1][0], z1 = sa[0][1] + sa[1][1];
-            const float z2 = sa[0][2] + sa[1][2], z3 = sa[0][3] + sa[1][3];
-            float y0 = fmaf(z0, qs0, kLift - m0), y1 = fmaf(z1, qs1, kLift - m1);
-            float y2 = fmaf(z2, qs0, kLift - m0), y3 = fmaf(z3, qs1, kLift - m1);
-            if (nv < 16) {
-                if (g >= nv) y0 = y1 = -INFINITY;
-                if (g + 8 >= nv) y2 = y3 = -INFINITY;
-            }
-            if (__any_sync(0xffffffffu, fmaxf(fmaxf(y0, y2), fmaxf(y1, y3)) > kSlack + kLift)) {
-                float t0 = fmaxf(g < nv ? z0 * qs0 : -INFINITY, g + 8 < nv ? z2 * qs0 : -INFINITY);
-                float t1 = fmaxf(g < nv ? z1 * qs1 : -INFINITY, g + 8 < nv ? z3 * qs1 : -INFINITY);
+            // ---- running softmax: [0], [1] are tokens g, [2], [3] tokens g + 8, of heads 2c and
+            // 2c + 1; y = logit - (running max - kLift), log2 domain ----
+            float z[SUB][4], y[SUB][4];
+            auto exponents = [&] {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[u][i] = (i & 1) ? fmaf(z[u][i], qs1, kLift - m1) : fmaf(z[u][i], qs0, kLift - m0);
+                        if (part && g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
+                    }
+            };
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[u][i] = sa[u][0][i] + sa[u][1][i];
+            exponents();
+            float top = y[0][0];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, y[u][i]);
+            if (__any_sync(0xffffffffu, top > kSlack + kLift)) {
+                float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        if (g + i * 4 < nv - 64 * u) {
+                            t0 = fmaxf(t0, z[u][i] * qs0);
+                            t1 = fmaxf(t1, z[u][i + 1] * qs1);
+                        }
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
@@ -535,72 +569,75 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     o[mt][2] *= r0;
                     o[mt][3] *= r1;
                 }
-                y0 = fmaf(z0, qs0, kLift - m0), y1 = fmaf(z1, qs1, kLift - m1);
-                y2 = fmaf(z2, qs0, kLift - m0), y3 = fmaf(z3, qs1, kLift - m1);
-                if (g >= nv) y0 = y1 = -INFINITY;
-                if (g + 8 >= nv) y2 = y3 = -INFINITY;
+                exponents();
             }
-            const float p0 = fast_exp2(y0), p1 = fast_exp2(y1), p2 = fast_exp2(y2), p3 = fast_exp2(y3);
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            uint32_t pb[C::NP][2];
-            {
-                const uint32_t u = pack_f16(p0, p1), v = pack_f16(p2, p3);
-                pb[0][0] = trans8x8(u);
-                pb[0][1] = trans8x8(v);
+            uint32_t pb[SUB][C::NP][2];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                const float p0 = fast_exp2(y[u][0]), p1 = fast_exp2(y[u][1]);
+                const float p2 = fast_exp2(y[u][2]), p3 = fast_exp2(y[u][3]);
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                const uint32_t ua = pack_f16(p0, p1), ub = pack_f16(p2, p3);
+                pb[u][0][0] = trans8x8(ua);
+                pb[u][0][1] = trans8x8(ub);
                 if constexpr (C::NP == 2) {
-                    pb[1][0] = trans8x8(pack_f16_rest(p0, p1, u));
-                    pb[1][1] = trans8x8(pack_f16_rest(p2, p3, v));
+                    pb[u][1][0] = trans8x8(pack_f16_rest(p0, p1, ua));
+                    pb[u][1][1] = trans8x8(pack_f16_rest(p2, p3, ub));
                 }
             }
             // ---- O^T += V^T P^T ----
-            const uint8_t* sv = sb + C::KV_BYTES;
-            uint32_t va[4], vb[4];      // scale bytes: tokens 2c (words 0, 1), 2c + 1 (2, 3); + 8
-            if constexpr (HD == 128) {
-                const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_a);
-                const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_a + eight);
-                va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
-                vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
-            } else {
-                const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_a);
-                const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_a + eight);
-                va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
-                va[1] = va[3] = vb[1] = vb[3] = 0u;
-            }
-            if (nv < 16) {   // rows past the context may hold anything: scale 0 (codes are finite)
-                if (2 * c >= nv) va[0] = va[1] = 0u;
-                if (2 * c + 1 >= nv) va[2] = va[3] = 0u;
-                if (2 * c + 8 >= nv) vb[0] = vb[1] = 0u;
-                if (2 * c + 9 >= nv) vb[2] = vb[3] = 0u;
-            }
 #pragma unroll
-            for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
-                uint32_t r[4];
-                ldsm4_trans(smem_addr(sv) + ld_off + cp * two_chunks, r);
-                // bytes (2c, 2c + 1) of chunk 2cp's group, then of chunk 2cp + 1's
-                const uint32_t da = __byte_perm(va[cp], va[cp + 2], vsel);
-                const uint32_t db = __byte_perm(vb[cp], vb[cp + 2], vsel);
+            for (int u = 0; u < SUB; ++u) {
+                const uint8_t* sv = sb + C::KV_BYTES + u * SUB_BYTES;
+                uint32_t va[4], vb[4];      // scale bytes: tokens 2c (words 0, 1), 2c + 1 (2, 3); + 8
+                if constexpr (HD == 128) {
+                    const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_a);
+                    const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_a + eight);
+                    va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
+                    vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
+                } else {
+                    const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_a);
+                    const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_a + eight);
+                    va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
+                    va[1] = va[3] = vb[1] = vb[3] = 0u;
+                }
+                if (part) {   // rows past the context may hold anything: scale 0 (codes are finite)
+                    const int left = nv - 64 * u;
+                    if (2 * c >= left) va[0] = va[1] = 0u;
+                    if (2 * c + 1 >= left) va[2] = va[3] = 0u;
+                    if (2 * c + 8 >= left) vb[0] = vb[1] = 0u;
+                    if (2 * c + 9 >= left) vb[2] = vb[3] = 0u;
+                }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int ch = 2 * cp + k;
-                    const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
-                    const uint32_t fa = e4m3x2_to_f16x2(k ? da >> 16 : da & 0xffffu);
-                    const uint32_t fb = e4m3x2_to_f16x2(k ? db >> 16 : db & 0xffffu);
-                    // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
-                    // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
-                    // room, the logic pipe that also converts has not).
-                    const uint32_t ea = bitselect(wa * p.two16, wa * p.two4, 0x0f0f0f0fu);
-                    const uint32_t eb = bitselect(wb * p.two16, wb * p.two4, 0x0f0f0f0fu);
-                    const uint32_t oa = bitselect(wa * p.two12, wa, 0x0f0f0f0fu);
-                    const uint32_t ob = bitselect(wb * p.two12, wb, 0x0f0f0f0fu);
-                    const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
-                    const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
-                    const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
-                    const uint32_t d2 = hmul2(e2m1x2_to_f16x2<2>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<3>(ob), fb);
+                for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
+                    uint32_t r[4];
+                    ldsm4_trans(smem_addr(sv) + ld_off + cp * two_chunks, r);
+                    // bytes (2c, 2c + 1) of chunk 2cp's group, then of chunk 2cp + 1's
+                    const uint32_t ga = __byte_perm(va[cp], va[cp + 2], vsel);
+                    const uint32_t gb = __byte_perm(vb[cp], vb[cp + 2], vsel);
 #pragma unroll
-                    for (int t = 0; t < C::NP; ++t) {
-                        mma_f16(o[2 * ch], e0, e1, e2, e3, pb[t][0], pb[t][1]);
-                        mma_f16(o[2 * ch + 1], d0, d1, d2, d3, pb[t][0], pb[t][1]);
+                    for (int k = 0; k < 2; ++k) {
+                        const int ch = 2 * cp + k;
+                        const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                        const uint32_t fa = e4m3x2_to_f16x2(k ? ga >> 16 : ga & 0xffffu);
+                        const uint32_t fb = e4m3x2_to_f16x2(k ? gb >> 16 : gb & 0xffffu);
+                        // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
+                        // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
+                        // room, the logic pipe that also converts has not).
+                        const uint32_t ea = bitselect(wa * p.two16, wa * p.two4, 0x0f0f0f0fu);
+                        const uint32_t eb = bitselect(wb * p.two16, wb * p.two4, 0x0f0f0f0fu);
+                        const uint32_t oa = bitselect(wa * p.two12, wa, 0x0f0f0f0fu);
+                        const uint32_t ob = bitselect(wb * p.two12, wb, 0x0f0f0f0fu);
+                        const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
+                        const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
+                        const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
+                        const uint32_t d2 = hmul2(e2m1x2_to_f16x2<2>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<3>(ob), fb);
+#pragma unroll
+                        for (int t = 0; t < C::NP; ++t) {
+                            mma_f16(o[2 * ch], e0, e1, e2, e3, pb[u][t][0], pb[u][t][1]);
+                            mma_f16(o[2 * ch + 1], d0, d1, d2, d3, pb[u][t][0], pb[u][t][1]);
+                        }
                     }
                 }
             }

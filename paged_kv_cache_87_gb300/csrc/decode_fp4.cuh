@@ -5,7 +5,7 @@
 
 namespace pkv {
 
-constexpr int kFp4Tile = 64;          // tokens of a tile: the split's unit and a ring stage
+constexpr int kFp4Tile = 128;         // tokens of a tile: the split's unit and a ring stage
 constexpr int kFp4UnitCost = 1;       // slots of a unit besides its tiles
 constexpr int kFp4MinQuota = 2;       // slots a worker takes at least
 constexpr int kFp4MaxPieces = 64;     // partial states that one unit leaves, about
