@@ -125,12 +125,13 @@ struct Cfg {
     static constexpr size_t OFF_META = (size_t)NSTAGE * STAGE_BYTES;
     static constexpr size_t OFF_BARS = OFF_META + NSTAGE * 16;
     static constexpr size_t OFF_QF = (OFF_BARS + 2 * NSTAGE * 8 + 15) / 16 * 16;
-    static constexpr size_t OFF_X = OFF_QF + NP * NCHUNK * 32 * 16;
+    static constexpr size_t OFF_PLAN = OFF_QF + NP * NCHUNK * 32 * 16;  // 32 tiles: int4, int2, rows
+    static constexpr size_t OFF_X = OFF_PLAN + 32 * (16 + 8 + 16 * 4);
     static constexpr size_t SMEM = OFF_X + XBUF * 4 + 128;             // the base is rounded up
     // resident CTAs, by registers.  The queries' operands stay in shared memory (a 16-byte load a
     // chunk): 187 -> 175 us on long documents against registers.  A fifth CTA (72 registers) spills
     // and loses: 200 us.
-    static constexpr int CTAS = 3;
+    static constexpr int CTAS = HD == 128 ? 3 : 4;
 };
 
 constexpr int kFirst = 1, kLast = 2, kDone = 4;
@@ -215,55 +216,6 @@ __device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total, int
                (longest + kFp4MaxPieces - 1) / kFp4MaxPieces);
 }
 
-// Where the producer is: slot `at` of unit `u` of sequence s (n slots, ctx tokens).
-struct Cursor {
-    int s, u, at, n, ctx;
-};
-
-// A run of at most 32 pool rows (8 or 16 tokens each) of one unit.
-struct Window {
-    int valid, s, u, t0, t1;     // tokens [t0, t1)
-    int first, last, slot;
-};
-
-__device__ __forceinline__ Window next_window(const DecodeFp4Params& p, int upi, int a, int end,
-                                              int& pos, Cursor& c) {
-    Window w{};
-    if (pos >= end) return w;
-    while (c.at == c.n) {                         // the next unit with tiles
-        c.at = 0;
-        if (++c.u == upi || c.n == 0) {
-            c.u = 0;
-            ++c.s;
-            c.n = slots_of(p, c.s);
-            c.ctx = min(p.context_lens[c.s], min(p.max_context_len, p.max_blocks * p.block_size));
-        }
-    }
-    if (c.at < kFp4UnitCost) {
-        const int skip = kFp4UnitCost - c.at;
-        if (pos + skip >= end) {                  // the range ends before the unit's first tile
-            pos = end;
-            return w;
-        }
-        pos += skip;
-        c.at = kFp4UnitCost;
-    }
-    const int tile = c.at - kFp4UnitCost, tiles = c.n - kFp4UnitCost;
-    const int wt = min(min(p.block_size == 8 ? 2 : 4, tiles - tile), end - pos);
-    const int dstart = pos - tile, uend = dstart + tiles;
-    w.valid = 1;
-    w.s = c.s;
-    w.u = c.u;
-    w.t0 = tile * kFp4Tile;
-    w.t1 = min((tile + wt) * kFp4Tile, c.ctx);
-    w.first = tile == 0 || dstart + tile == a;
-    w.last = pos + wt == end || tile + wt == tiles;
-    w.slot = dstart < a ? 0 : (uend > end ? 1 : -1);
-    c.at += wt;
-    pos += wt;
-    return w;
-}
-
 template <typename QT, int HD>
 __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
@@ -295,81 +247,88 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 
     if (warp == kConsumers) {
         // ======================= producer warp =======================
+        // Plans 32 slots at a time, one a lane, then issues their tiles.
         const uint64_t policy = l2_evict_first_policy();
-        int stage = 0, pos = a;
+        int stage = 0;
         uint32_t phase = 0;
-        Cursor cur{};
-        if (a < end) {
-            int base;
-            locate<kThreads>(p, s_pref, upi, a, &cur.s, &cur.n, &base);
-            cur.u = (a - base) / cur.n;
-            cur.at = (a - base) % cur.n;
-            cur.ctx = min(p.context_lens[cur.s], min(p.max_context_len, p.max_blocks * B));
-        }
         if (lane == 0) {
             prefetch_tensormap(&map_k);
             prefetch_tensormap(&map_v);
         }
+        int4* plan = reinterpret_cast<int4*>(smem + C::OFF_PLAN);      // as metas; 0: no tile here
+        int2* plan_at = reinterpret_cast<int2*>(plan + 32);            // {tile of the unit, kv head}
+        int* plan_row = reinterpret_cast<int*>(plan_at + 32);          // [32][16] pool rows
         // a pool row is a whole tile of 8 or 16 tokens, or half of a tile of 32
-        const int log_rt = min(logB, 4), per_block = logB - log_rt;
-        Window win = next_window(p, upi, a, end, pos, cur);
-        // a lane's pool row of the window (beyond the context's last block: that one's again)
-        auto pool_row = [&](const Window& w) {
-            const int j0 = w.t0 >> logB, blocks = ((w.t1 - 1) >> logB) - j0 + 1;
-            const int i = min(lane, (blocks << per_block) - 1);
-            int blk = p.block_tables[(int64_t)w.s * p.max_blocks + j0 + (i >> per_block)];
-            if (blk < 0 || blk >= p.num_blocks) {
-                set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
-                blk = 0;
+        const int log_rt = min(logB, 4), per_block = logB - log_rt, log_rows = 7 - log_rt;
+        const int cap = min(p.max_context_len, p.max_blocks * B);
+        for (int pos0 = a; pos0 < end; pos0 += 32) {
+            const int pos = pos0 + lane;
+            int4 m = make_int4(0, 0, 0, 0);
+            if (pos < end) {
+                int s, n, base;
+                locate<kThreads>(p, s_pref, upi, pos, &s, &n, &base);
+                const int u = (pos - base) / n, at = (pos - base) % n, tile = at - kFp4UnitCost;
+                if (tile >= 0) {
+                    const int dstart = pos - tile, uend = pos - at + n;
+                    const int tokens = min(kFp4Tile, min(p.context_lens[s], cap) - tile * kFp4Tile);
+                    m = make_int4((tile == 0 || pos == a ? kFirst : 0) |
+                                      (at == n - 1 || pos == end - 1 ? kLast : 0) | tokens << 8,
+                                  s, u, dstart < a ? 0 : uend > end ? 1 : -1);
+                    plan_at[lane] = make_int2(tile, u / p.nsub);
+                }
             }
-            const int tile = blk * p.num_kv_heads + w.u / p.nsub;
-            return per_block ? 2 * tile + (i & 1) : tile;
-        };
-        int rows = win.valid ? pool_row(win) : 0;
-        while (win.valid) {
-            const int kvh = win.u / p.nsub, qsub = win.u % p.nsub;
-            const int qrow = win.s * p.num_q_heads + kvh * p.group + qsub * kFp4Heads;
-            const uint32_t qbytes = min(kFp4Heads, p.group - qsub * kFp4Heads) * (HD * QT::bytes);
-            Window nxt{};
-            int nrows = 0;
-            for (int ts = win.t0; ts < win.t1; ts += kFp4Tile) {
-                const bool first = win.first && ts == win.t0;
-                const int flags = (first ? kFirst : 0) | (win.last && ts + kFp4Tile >= win.t1 ? kLast : 0);
-                const int n = min(kFp4Tile, win.t1 - ts), r = (ts - win.t0) >> log_rt;
-                // 32 or 64 tokens a gather; those past the context's last block stay out
-                const int per = 4 << log_rt, gathers = (n + per - 1) / per;
+            plan[lane] = m;
+            const unsigned have = __ballot_sync(0xffffffffu, m.x != 0);   // and the plan is visible
+            // the tiles' pool rows, 8 or 16 each (beyond the context's last block: that one's again)
+#pragma unroll 4
+            for (int i = lane; i < 32 << log_rows; i += 32) {
+                const int l = i >> log_rows, r = i & ((1 << log_rows) - 1);
+                const int4 t = plan[l];
+                if (t.x == 0) continue;
+                const int2 w = plan_at[l];
+                const int blocks = ((t.x >> 8) + B - 1) >> logB, k = min(r, (blocks << per_block) - 1);
+                int blk = p.block_tables[(int64_t)t.y * p.max_blocks + ((w.x * kFp4Tile) >> logB) + (k >> per_block)];
+                if (blk < 0 || blk >= p.num_blocks) {
+                    set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
+                    blk = 0;
+                }
+                const int row = blk * p.num_kv_heads + w.y;
+                plan_row[l * 16 + r] = per_block ? 2 * row + (k & 1) : row;
+            }
+            __syncwarp();
+            for (unsigned left = have; left != 0; left &= left - 1) {
+                const int l = __ffs(left) - 1;
                 if (!mbar_wait(&empty[stage], phase ^ 1u)) {
                     set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
                     return;
                 }
-                uint8_t* sb = smem + stage * C::STAGE_BYTES;
                 if (lane == 0) {
-                    metas[stage] = make_int4(flags | n << 8, win.s, win.u, win.slot);
-                    mbar_arrive_expect_tx(&full[stage], 2u * C::ROWB * per * gathers + (first ? qbytes : 0u));
-                    if (first)
-                        bulk_g2s(sb + 2 * C::KV_BYTES,
-                                 static_cast<const uint8_t*>(p.q) + (int64_t)qrow * HD * QT::bytes,
-                                 qbytes, &full[stage]);
-                }
-                for (int k = 0; k < gathers; ++k) {
-                    int y[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, rows, r + 4 * k + i);
-                    if (lane == 0) {
-                        tma_gather4(sb + k * (per * C::ROWB), &map_k, y[0], y[1], y[2], y[3], &full[stage], policy);
-                        tma_gather4(sb + C::KV_BYTES + k * (per * C::ROWB), &map_v, y[0], y[1], y[2], y[3],
+                    const int4 t = plan[l];
+                    const int kvh = plan_at[l].y, qsub = t.z - kvh * p.nsub;
+                    uint8_t* sb = smem + stage * C::STAGE_BYTES;
+                    // 32 or 64 tokens a gather; those past the context's last block stay out
+                    const int per = 4 << log_rt, gathers = ((t.x >> 8) + per - 1) >> (log_rt + 2);
+                    uint32_t bytes = 2u * C::ROWB * per * gathers;
+                    const uint32_t qbytes = min(kFp4Heads, p.group - qsub * kFp4Heads) * (HD * QT::bytes);
+                    if (t.x & kFirst) bytes += qbytes;
+                    metas[stage] = t;
+                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    for (int k = 0; k < gathers; ++k) {
+                        const int4 y = *reinterpret_cast<const int4*>(plan_row + l * 16 + 4 * k);
+                        tma_gather4(sb + k * (per * C::ROWB), &map_k, y.x, y.y, y.z, y.w, &full[stage], policy);
+                        tma_gather4(sb + C::KV_BYTES + k * (per * C::ROWB), &map_v, y.x, y.y, y.z, y.w,
                                     &full[stage], policy);
                     }
+                    if (t.x & kFirst) {
+                        const int64_t row = (int64_t)t.y * p.num_q_heads + kvh * p.group + qsub * kFp4Heads;
+                        bulk_g2s(sb + 2 * C::KV_BYTES,
+                                 static_cast<const uint8_t*>(p.q) + row * HD * QT::bytes, qbytes,
+                                 &full[stage]);
+                    }
                 }
-                __syncwarp();
                 if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
-                if (ts == win.t0) {      // look ahead: the next window's entries load meanwhile
-                    nxt = next_window(p, upi, a, end, pos, cur);
-                    if (nxt.valid) nrows = pool_row(nxt);
-                }
             }
-            win = nxt;
-            rows = nrows;
+            __syncwarp();                 // the plan may be rewritten
         }
         if (!mbar_wait(&empty[stage], phase ^ 1u)) {
             set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
