@@ -119,7 +119,7 @@ struct Cfg {
     static constexpr int NSTAGE = 3;
     static constexpr int NCHUNK = HD / 32;
     static constexpr int NP = std::is_same<QT, F32>::value ? 2 : 1;   // terms of q and p
-    static constexpr int XD = HD / 2;                  // dims exchanged at a time
+    static constexpr int XD = 64;                      // dims exchanged at a time
     static constexpr int HS = XD + 1;                  // exchange stride of a head: few conflicts
     static constexpr int XBUF = kConsumers * kFp4Heads * (HS + 2);    // acc, then m, l
     static constexpr size_t OFF_META = (size_t)NSTAGE * STAGE_BYTES;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     store_from_float<QT>(p.out, (int64_t)s * row + i, 0.f);
         }
     }
-    constexpr int SUB = kFp4Tile / 64, SUB_BYTES = 64 * C::ROWB;    // a warp's pieces of a tile
+    constexpr int SUB_BYTES = 64 * C::ROWB;       // from a warp's first piece of a tile to its second
     const int g = lane >> 2, c = lane & 3;
     // this lane's places in a piece: ldmatrix row (token 16 warp + 8 (mi & 1) + r of chunk
     // mi >> 1), and the scale rows of tokens g, g + 8 (K) and 2c, 2c + 8 (V)
@@ -374,6 +374,182 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     int stage = 0;
     uint32_t phase = 0;
 
+    // One tile: SUB pieces of 16 tokens, 64 apart, nv tokens from the first of them on.
+    auto attend = [&](auto pieces, const uint8_t* sb, int nv) {
+        constexpr int SUB = decltype(pieces)::value;
+        const bool part = nv < 64 * SUB - 48;         // some of the tokens are not valid
+        // ---- S^T = K Q^T ----
+        float sa[SUB][2][4];
+        uint32_t da[SUB], db[SUB];     // this lane's scale byte of every chunk, rows g and g + 8
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sa[u][0][i] = sa[u][1][i] = 0.f;
+            const uint8_t* sc = sb + u * SUB_BYTES + ks_a;
+            if constexpr (HD == 128) {
+                const uint2 ra = *reinterpret_cast<const uint2*>(sc);
+                const uint2 rb = *reinterpret_cast<const uint2*>(sc + eight);
+                da[u] = __byte_perm(ra.x, ra.y, ksel);
+                db[u] = __byte_perm(rb.x, rb.y, ksel);
+            } else {
+                da[u] = __byte_perm(*reinterpret_cast<const uint32_t*>(sc), 0u, ksel);
+                db[u] = __byte_perm(*reinterpret_cast<const uint32_t*>(sc + eight), 0u, ksel);
+            }
+        }
+#pragma unroll
+        for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
+            uint4 qf[C::NP][2];
+#pragma unroll
+            for (int t = 0; t < C::NP; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) qf[t][k] = s_qf[(t * C::NCHUNK + 2 * cp + k) * 32 + lane];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t r[4];
+                ldsm4(smem_addr(sb) + u * SUB_BYTES + ld_off + cp * two_chunks, r);
+                // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
+                const uint32_t pa = e4m3x2_to_f16x2(cp ? da[u] >> 16 : da[u] & 0xffffu);
+                const uint32_t pb = e4m3x2_to_f16x2(cp ? db[u] >> 16 : db[u] & 0xffffu);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                    const uint32_t fa = half_twice(pa, k), fb = half_twice(pb, k);
+                    const uint32_t a00 = hmul2(e2m1x2_to_f16x2<0>(wa), fa), a01 = hmul2(e2m1x2_to_f16x2<0>(wb), fb);
+                    const uint32_t a02 = hmul2(e2m1x2_to_f16x2<1>(wa), fa), a03 = hmul2(e2m1x2_to_f16x2<1>(wb), fb);
+                    const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
+                    const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
+#pragma unroll
+                    for (int t = 0; t < C::NP; ++t) {
+                        mma_f16(sa[u][0], a00, a01, a02, a03, qf[t][k].x, qf[t][k].y);
+                        mma_f16(sa[u][1], a10, a11, a12, a13, qf[t][k].z, qf[t][k].w);
+                    }
+                }
+            }
+        }
+        // ---- running softmax: [0], [1] are tokens g, [2], [3] tokens g + 8, of heads 2c and
+        // 2c + 1; y = logit - (running max - kLift), log2 domain ----
+        float z[SUB][4], y[SUB][4];
+        auto exponents = [&] {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[u][i] = (i & 1) ? fmaf(z[u][i], qs1, kLift - m1) : fmaf(z[u][i], qs0, kLift - m0);
+                    if (part && g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
+                }
+        };
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[u][i] = sa[u][0][i] + sa[u][1][i];
+        exponents();
+        float top = y[0][0];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, y[u][i]);
+        if (__any_sync(0xffffffffu, top > kSlack + kLift)) {
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+                    if (g + i * 4 < nv - 64 * u) {
+                        t0 = fmaxf(t0, z[u][i] * qs0);
+                        t1 = fmaxf(t1, z[u][i + 1] * qs1);
+                    }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+            }
+            const bool n0 = t0 > m0 + kSlack, n1 = t1 > m1 + kSlack;
+            const float r0 = n0 ? fast_exp2(m0 - t0) : 1.f, r1 = n1 ? fast_exp2(m1 - t1) : 1.f;
+            if (n0) m0 = t0;
+            if (n1) m1 = t1;
+            l0 *= r0;
+            l1 *= r1;
+#pragma unroll
+            for (int mt = 0; mt < 2 * C::NCHUNK; ++mt) {
+                o[mt][0] *= r0;
+                o[mt][1] *= r1;
+                o[mt][2] *= r0;
+                o[mt][3] *= r1;
+            }
+            exponents();
+        }
+        uint32_t pb[SUB][C::NP][2];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            const float p0 = fast_exp2(y[u][0]), p1 = fast_exp2(y[u][1]);
+            const float p2 = fast_exp2(y[u][2]), p3 = fast_exp2(y[u][3]);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            const uint32_t ua = pack_f16(p0, p1), ub = pack_f16(p2, p3);
+            pb[u][0][0] = trans8x8(ua);
+            pb[u][0][1] = trans8x8(ub);
+            if constexpr (C::NP == 2) {
+                pb[u][1][0] = trans8x8(pack_f16_rest(p0, p1, ua));
+                pb[u][1][1] = trans8x8(pack_f16_rest(p2, p3, ub));
+            }
+        }
+        // ---- O^T += V^T P^T ----
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            const uint8_t* sv = sb + C::KV_BYTES + u * SUB_BYTES;
+            uint32_t va[4], vb[4];      // scale bytes: tokens 2c (words 0, 1), 2c + 1 (2, 3); + 8
+            if constexpr (HD == 128) {
+                const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_a);
+                const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_a + eight);
+                va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
+                vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
+            } else {
+                const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_a);
+                const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_a + eight);
+                va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
+                va[1] = va[3] = vb[1] = vb[3] = 0u;
+            }
+            if (part) {   // rows past the context may hold anything: scale 0 (codes are finite)
+                const int left = nv - 64 * u;
+                if (2 * c >= left) va[0] = va[1] = 0u;
+                if (2 * c + 1 >= left) va[2] = va[3] = 0u;
+                if (2 * c + 8 >= left) vb[0] = vb[1] = 0u;
+                if (2 * c + 9 >= left) vb[2] = vb[3] = 0u;
+            }
+#pragma unroll
+            for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
+                uint32_t r[4];
+                ldsm4_trans(smem_addr(sv) + ld_off + cp * two_chunks, r);
+                // bytes (2c, 2c + 1) of chunk 2cp's group, then of chunk 2cp + 1's
+                const uint32_t ga = __byte_perm(va[cp], va[cp + 2], vsel);
+                const uint32_t gb = __byte_perm(vb[cp], vb[cp + 2], vsel);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int ch = 2 * cp + k;
+                    const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                    const uint32_t fa = e4m3x2_to_f16x2(k ? ga >> 16 : ga & 0xffffu);
+                    const uint32_t fb = e4m3x2_to_f16x2(k ? gb >> 16 : gb & 0xffffu);
+                    // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
+                    // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
+                    // room, the logic pipe that also converts has not).
+                    const uint32_t ea = bitselect(wa * p.two16, wa * p.two4, 0x0f0f0f0fu);
+                    const uint32_t eb = bitselect(wb * p.two16, wb * p.two4, 0x0f0f0f0fu);
+                    const uint32_t oa = bitselect(wa * p.two12, wa, 0x0f0f0f0fu);
+                    const uint32_t ob = bitselect(wb * p.two12, wb, 0x0f0f0f0fu);
+                    const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
+                    const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
+                    const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
+                    const uint32_t d2 = hmul2(e2m1x2_to_f16x2<2>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<3>(ob), fb);
+#pragma unroll
+                    for (int t = 0; t < C::NP; ++t) {
+                        mma_f16(o[2 * ch], e0, e1, e2, e3, pb[u][t][0], pb[u][t][1]);
+                        mma_f16(o[2 * ch + 1], d0, d1, d2, d3, pb[u][t][0], pb[u][t][1]);
+                    }
+                }
+            }
+        }
+    };
+
     while (true) {
         if (!mbar_wait(&full[stage], phase)) {
             set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
@@ -384,25 +560,29 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         const uint8_t* sb = smem + stage * C::STAGE_BYTES;
         if (meta.x & kFirst) {
             const int nh = min(kFp4Heads, p.group - meta.z % p.nsub * kFp4Heads);
-            // q row of head g, scaled by a power of two into fp16; warp w forms the operands of
-            // chunks w, w + 4, ..: dims 32 ch + 8c .. + 7
+            // q row of head g, scaled by a power of two into fp16 (fp16 rows as they are); warp w
+            // forms the operands of chunks w, w + 4, ..: dims 32 ch + 8c .. + 7
             const uint8_t* sq = sb + 2 * C::KV_BYTES + (g * HD + 8 * c) * QT::bytes;
-            float amax = 0.f;
+            float up = 1.f;
+            qs0 = qs1 = p.qk_scale_log2;
+            if constexpr (!std::is_same<QT, F16>::value) {
+                float amax = 0.f;
 #pragma unroll
-            for (int ch = 0; ch < C::NCHUNK; ++ch) {
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
+                for (int ch = 0; ch < C::NCHUNK; ++ch) {
+                    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = absmax_nan(x[i], amax);
+                    for (int i = 0; i < 8; ++i) amax = absmax_nan(x[i], amax);
+                }
+                amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
+                amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 2), amax);
+                const int ex = (int)(__float_as_uint(amax) >> 23) - 127;     // floor(log2), or 128
+                const int e = ex == 128 ? 0 : min(14 - ex, 126);
+                up = __uint_as_float((uint32_t)(e + 127) << 23);
+                const float qs = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+                qs0 = __shfl_sync(0xffffffffu, qs, 8 * c);
+                qs1 = __shfl_sync(0xffffffffu, qs, 8 * c + 4);
             }
-            amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
-            amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 2), amax);
-            const int ex = (int)(__float_as_uint(amax) >> 23) - 127;     // floor(log2), or 128
-            const int e = ex == 128 ? 0 : min(14 - ex, 126);
-            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-            const float qs = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-            qs0 = __shfl_sync(0xffffffffu, qs, 8 * c);
-            qs1 = __shfl_sync(0xffffffffu, qs, 8 * c + 4);
             for (int ch = warp; ch < C::NCHUNK; ch += kConsumers) {
                 float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                 if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
@@ -427,180 +607,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             l0 = l1 = 0.f;
         }
         const int nv = (meta.x >> 8) - 16 * warp;   // tokens of the tile from this warp's first on
-        if (nv > 0) {
-            // two pieces of 16 tokens, 64 apart: their valid tokens (negative: none)
-            const bool part = nv < 64 + 16;
-            // ---- S^T = K Q^T ----
-            float sa[SUB][2][4];
-            uint32_t da[SUB], db[SUB];     // this lane's scale byte of every chunk, rows g and g + 8
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sa[u][0][i] = sa[u][1][i] = 0.f;
-                const uint8_t* sc = sb + u * SUB_BYTES + ks_a;
-                if constexpr (HD == 128) {
-                    const uint2 ra = *reinterpret_cast<const uint2*>(sc);
-                    const uint2 rb = *reinterpret_cast<const uint2*>(sc + eight);
-                    da[u] = __byte_perm(ra.x, ra.y, ksel);
-                    db[u] = __byte_perm(rb.x, rb.y, ksel);
-                } else {
-                    da[u] = __byte_perm(*reinterpret_cast<const uint32_t*>(sc), 0u, ksel);
-                    db[u] = __byte_perm(*reinterpret_cast<const uint32_t*>(sc + eight), 0u, ksel);
-                }
-            }
-#pragma unroll
-            for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
-                uint4 qf[C::NP][2];
-#pragma unroll
-                for (int t = 0; t < C::NP; ++t)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) qf[t][k] = s_qf[(t * C::NCHUNK + 2 * cp + k) * 32 + lane];
-#pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    uint32_t r[4];
-                    ldsm4(smem_addr(sb) + u * SUB_BYTES + ld_off + cp * two_chunks, r);
-                    // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
-                    const uint32_t pa = e4m3x2_to_f16x2(cp ? da[u] >> 16 : da[u] & 0xffffu);
-                    const uint32_t pb = e4m3x2_to_f16x2(cp ? db[u] >> 16 : db[u] & 0xffffu);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
-                        const uint32_t fa = half_twice(pa, k), fb = half_twice(pb, k);
-                        const uint32_t a00 = hmul2(e2m1x2_to_f16x2<0>(wa), fa), a01 = hmul2(e2m1x2_to_f16x2<0>(wb), fb);
-                        const uint32_t a02 = hmul2(e2m1x2_to_f16x2<1>(wa), fa), a03 = hmul2(e2m1x2_to_f16x2<1>(wb), fb);
-                        const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
-                        const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
-#pragma unroll
-                        for (int t = 0; t < C::NP; ++t) {
-                            mma_f16(sa[u][0], a00, a01, a02, a03, qf[t][k].x, qf[t][k].y);
-                            mma_f16(sa[u][1], a10, a11, a12, a13, qf[t][k].z, qf[t][k].w);
-                        }
-                    }
-                }
-            }
-            // ---- running softmax: [0], [1] are tokens g, [2], [3] tokens g + 8, of heads 2c and
-            // 2c + 1; y = logit - (running max - kLift), log2 domain ----
-            float z[SUB][4], y[SUB][4];
-            auto exponents = [&] {
-#pragma unroll
-                for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[u][i] = (i & 1) ? fmaf(z[u][i], qs1, kLift - m1) : fmaf(z[u][i], qs0, kLift - m0);
-                        if (part && g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
-                    }
-            };
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[u][i] = sa[u][0][i] + sa[u][1][i];
-            exponents();
-            float top = y[0][0];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, y[u][i]);
-            if (__any_sync(0xffffffffu, top > kSlack + kLift)) {
-                float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2)
-                        if (g + i * 4 < nv - 64 * u) {
-                            t0 = fmaxf(t0, z[u][i] * qs0);
-                            t1 = fmaxf(t1, z[u][i + 1] * qs1);
-                        }
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
-                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
-                }
-                const bool n0 = t0 > m0 + kSlack, n1 = t1 > m1 + kSlack;
-                const float r0 = n0 ? fast_exp2(m0 - t0) : 1.f, r1 = n1 ? fast_exp2(m1 - t1) : 1.f;
-                if (n0) m0 = t0;
-                if (n1) m1 = t1;
-                l0 *= r0;
-                l1 *= r1;
-#pragma unroll
-                for (int mt = 0; mt < 2 * C::NCHUNK; ++mt) {
-                    o[mt][0] *= r0;
-                    o[mt][1] *= r1;
-                    o[mt][2] *= r0;
-                    o[mt][3] *= r1;
-                }
-                exponents();
-            }
-            uint32_t pb[SUB][C::NP][2];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                const float p0 = fast_exp2(y[u][0]), p1 = fast_exp2(y[u][1]);
-                const float p2 = fast_exp2(y[u][2]), p3 = fast_exp2(y[u][3]);
-                l0 += p0 + p2;
-                l1 += p1 + p3;
-                const uint32_t ua = pack_f16(p0, p1), ub = pack_f16(p2, p3);
-                pb[u][0][0] = trans8x8(ua);
-                pb[u][0][1] = trans8x8(ub);
-                if constexpr (C::NP == 2) {
-                    pb[u][1][0] = trans8x8(pack_f16_rest(p0, p1, ua));
-                    pb[u][1][1] = trans8x8(pack_f16_rest(p2, p3, ub));
-                }
-            }
-            // ---- O^T += V^T P^T ----
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                const uint8_t* sv = sb + C::KV_BYTES + u * SUB_BYTES;
-                uint32_t va[4], vb[4];      // scale bytes: tokens 2c (words 0, 1), 2c + 1 (2, 3); + 8
-                if constexpr (HD == 128) {
-                    const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_a);
-                    const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_a + eight);
-                    va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
-                    vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
-                } else {
-                    const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_a);
-                    const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_a + eight);
-                    va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
-                    va[1] = va[3] = vb[1] = vb[3] = 0u;
-                }
-                if (part) {   // rows past the context may hold anything: scale 0 (codes are finite)
-                    const int left = nv - 64 * u;
-                    if (2 * c >= left) va[0] = va[1] = 0u;
-                    if (2 * c + 1 >= left) va[2] = va[3] = 0u;
-                    if (2 * c + 8 >= left) vb[0] = vb[1] = 0u;
-                    if (2 * c + 9 >= left) vb[2] = vb[3] = 0u;
-                }
-#pragma unroll
-                for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
-                    uint32_t r[4];
-                    ldsm4_trans(smem_addr(sv) + ld_off + cp * two_chunks, r);
-                    // bytes (2c, 2c + 1) of chunk 2cp's group, then of chunk 2cp + 1's
-                    const uint32_t ga = __byte_perm(va[cp], va[cp + 2], vsel);
-                    const uint32_t gb = __byte_perm(vb[cp], vb[cp + 2], vsel);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int ch = 2 * cp + k;
-                        const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
-                        const uint32_t fa = e4m3x2_to_f16x2(k ? ga >> 16 : ga & 0xffffu);
-                        const uint32_t fb = e4m3x2_to_f16x2(k ? gb >> 16 : gb & 0xffffu);
-                        // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
-                        // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
-                        // room, the logic pipe that also converts has not).
-                        const uint32_t ea = bitselect(wa * p.two16, wa * p.two4, 0x0f0f0f0fu);
-                        const uint32_t eb = bitselect(wb * p.two16, wb * p.two4, 0x0f0f0f0fu);
-                        const uint32_t oa = bitselect(wa * p.two12, wa, 0x0f0f0f0fu);
-                        const uint32_t ob = bitselect(wb * p.two12, wb, 0x0f0f0f0fu);
-                        const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
-                        const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
-                        const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
-                        const uint32_t d2 = hmul2(e2m1x2_to_f16x2<2>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<3>(ob), fb);
-#pragma unroll
-                        for (int t = 0; t < C::NP; ++t) {
-                            mma_f16(o[2 * ch], e0, e1, e2, e3, pb[u][t][0], pb[u][t][1]);
-                            mma_f16(o[2 * ch + 1], d0, d1, d2, d3, pb[u][t][0], pb[u][t][1]);
-                        }
-                    }
-                }
-            }
-        }
+        if (nv > 64) attend(std::integral_constant<int, 2>(), sb, nv);
+        else if (nv > 0) attend(std::integral_constant<int, 1>(), sb, nv);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
         if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
@@ -627,12 +635,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             xl[hw] = l0;
             xl[hw + 1] = l1;
         }
+        float f[kConsumers] = {0.f};                                // the warps' shares
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {                            // half of the dims at a time
+        for (int pass = 0; pass < HD / C::XD; ++pass) {             // 64 dims at a time
 #pragma unroll
-            for (int mt = 0; mt < C::NCHUNK; ++mt) {
+            for (int mt = 0; mt < C::XD / 16; ++mt) {
                 const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);  // [2], [3]: dim + 2
-                const float* v = o[hf * C::NCHUNK + mt];
+                const float* v = o[pass * (C::XD / 16) + mt];
                 if (2 * c < nh) {
                     xa[hw * C::HS + dim] = v[0];
                     xa[hw * C::HS + dim + 2] = v[2];
@@ -644,16 +653,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             }
             named_bar_sync(1, kConsumers * 32);
             if (h < nh) {
-                float M = -INFINITY, L = 0.f, f[kConsumers];
+                if (pass == 0) {
+                    float M = -INFINITY, L = 0.f;
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
+                    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
-                    const float mw = xm[w * kFp4Heads + h];
-                    f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-                    L = fmaf(xl[w * kFp4Heads + h], f[w], L);
+                    for (int w = 0; w < kConsumers; ++w) {
+                        const float mw = xm[w * kFp4Heads + h];
+                        f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+                        L = fmaf(xl[w * kFp4Heads + h], f[w], L);
+                    }
+                    if (meta.w < 0) {
+                        const float inv = p.out_scale / L;
+#pragma unroll
+                        for (int w = 0; w < kConsumers; ++w) f[w] *= inv;
+                    } else if (part == 0) {
+                        p.part_ml[2 * pi] = M;
+                        p.part_ml[2 * pi + 1] = L;
+                    }
                 }
-                const float inv = p.out_scale / L;
 #pragma unroll
                 for (int i = 0; i < C::XD / 16; ++i) {
                     const int dim = part + 16 * i;
@@ -661,12 +679,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 #pragma unroll
                     for (int w = 0; w < kConsumers; ++w)
                         A = fmaf(xa[(w * kFp4Heads + h) * C::HS + dim], f[w], A);
-                    if (meta.w < 0) store_from_float<QT>(p.out, row * HD + hf * C::XD + dim, A * inv);
-                    else p.part_acc[pi * HD + hf * C::XD + dim] = A;
-                }
-                if (meta.w >= 0 && part == 0 && hf == 0) {
-                    p.part_ml[2 * pi] = M;
-                    p.part_ml[2 * pi + 1] = L;
+                    if (meta.w < 0) store_from_float<QT>(p.out, row * HD + pass * C::XD + dim, A);
+                    else p.part_acc[pi * HD + pass * C::XD + dim] = A;
                 }
             }
             named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
