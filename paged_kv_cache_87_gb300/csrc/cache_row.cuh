@@ -54,6 +54,19 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// The same of the low (HALF = 0) or high half of a word of four codes.
+template <int HALF>
+__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t w) {
+    uint32_t r;
+    if constexpr (HALF == 0)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+            : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}"
+            : "=r"(r) : "r"(w));
+    return r;
+}
+
 // Two fp32 values -> two e2m1 codes (round to nearest even, saturate to +-6), `lo` in the
 // low nibble.
 __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {

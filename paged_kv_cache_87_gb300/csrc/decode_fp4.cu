@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     uint4* s_qf = reinterpret_cast<uint4*>(smem + C::OFF_QF);   // per chunk: two k-steps of (b0, b1)
     float o[2 * C::NCHUNK][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, qs0 = 0.f, qs1 = 0.f;
+    float lm0 = INFINITY, lm1 = INFINITY;               // kLift - m0, kLift - m1
     int stage = 0;
     uint32_t phase = 0;
 
@@ -408,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                 uint32_t r[4];
                 ldsm4(smem_addr(sb) + u * SUB_BYTES + ld_off + cp * two_chunks, r);
                 // scales of chunks 2cp (low half) and 2cp + 1, the multiply broadcasts a half
-                const uint32_t pa = e4m3x2_to_f16x2(cp ? da[u] >> 16 : da[u] & 0xffffu);
-                const uint32_t pb = e4m3x2_to_f16x2(cp ? db[u] >> 16 : db[u] & 0xffffu);
+                const uint32_t pa = cp ? e4m3x2_of<1>(da[u]) : e4m3x2_of<0>(da[u]);
+                const uint32_t pb = cp ? e4m3x2_of<1>(db[u]) : e4m3x2_of<0>(db[u]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
@@ -433,10 +434,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[u][i] = (i & 1) ? fmaf(z[u][i], qs1, kLift - m1) : fmaf(z[u][i], qs0, kLift - m0);
-                    if (part && g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
-                }
+                for (int i = 0; i < 4; ++i)
+                    y[u][i] = (i & 1) ? fmaf(z[u][i], qs1, lm1) : fmaf(z[u][i], qs0, lm0);
+            if (part)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
         };
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
@@ -467,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
             const float r0 = n0 ? fast_exp2(m0 - t0) : 1.f, r1 = n1 ? fast_exp2(m1 - t1) : 1.f;
             if (n0) m0 = t0;
             if (n1) m1 = t1;
+            lm0 = kLift - m0;
+            lm1 = kLift - m1;
             l0 *= r0;
             l1 *= r1;
 #pragma unroll
@@ -527,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                 for (int k = 0; k < 2; ++k) {
                     const int ch = 2 * cp + k;
                     const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
-                    const uint32_t fa = e4m3x2_to_f16x2(k ? ga >> 16 : ga & 0xffffu);
-                    const uint32_t fb = e4m3x2_to_f16x2(k ? gb >> 16 : gb & 0xffffu);
+                    const uint32_t fa = k ? e4m3x2_of<1>(ga) : e4m3x2_of<0>(ga);
+                    const uint32_t fb = k ? e4m3x2_of<1>(gb) : e4m3x2_of<0>(gb);
                     // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
                     // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
                     // room, the logic pipe that also converts has not).
@@ -604,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[mt][i] = 0.f;
             m0 = m1 = -INFINITY;
+            lm0 = lm1 = INFINITY;
             l0 = l1 = 0.f;
         }
         const int nv = (meta.x >> 8) - 16 * warp;   // tokens of the tile from this warp's first on

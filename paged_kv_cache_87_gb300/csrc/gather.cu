@@ -13,7 +13,7 @@
 
 namespace pkv {
 
-constexpr int kGatherRows = 32;
+constexpr int kGatherRows = 8;
 constexpr int kGatherThreads = 256;
 
 template <typename KT, typename OT, int HD>
