@@ -7,7 +7,7 @@ namespace pkv {
 
 constexpr int kFp4Tile = 128;         // tokens of a tile: the split's unit and a ring stage
 constexpr int kFp4UnitCost = 1;       // slots of a unit besides its tiles
-constexpr int kFp4MinQuota = 2;       // slots a worker takes at least
+constexpr int kFp4MinQuota = 1;       // slots a worker takes at least
 constexpr int kFp4MaxPieces = 64;     // partial states that one unit leaves, about
 constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most
 constexpr int kFp4Heads = 8;          // query heads of a work unit
