@@ -93,21 +93,21 @@ __global__ void __launch_bounds__(256) reshape_and_cache_kernel(ReshapeParams p)
     }
 }
 
-// Into the 4-bit cache.  A lane holds eight dims of a (token, kv head) row; a pair of lanes
-// shares a 16-dim group's scale (a shuffle, so whole warps run together).  A warp keeps its piece
-// of a token -- kWriteRows rows a lane group of K or of V -- and walks the tokens with the next
-// token's rows and slot loading while it quantises this one's.
-constexpr int kWriteRows = 4;
+// Into the 4-bit cache.  A lane holds 16 dims of a (token, kv head) row: one scale's group, so that
+// what a scale costs (a division, a reciprocal) is paid once.  A warp keeps its piece of a token --
+// kWriteRows rows a lane group of K or of V -- and walks the tokens with the next token's rows and
+// slot loading while it quantises this one's.
+constexpr int kWriteRows = 2;
 constexpr int kWriteThreads = 256;
-constexpr int kWriteCtas = 3;    // a SM's share of the grid: resident at its registers
+constexpr int kWriteCtas = 6;    // a SM's share of the grid: resident at its registers
 
 template <typename ST, int HD>
 __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_fp4_kernel(ReshapeParams p,
                                                                               int log_block) {
     pdl_launch_dependents();   // the decode launched next may start its launch now
-    constexpr int LPR = HD / 8, RPW = 32 / LPR, STEP = RPW * kWriteRows;
-    constexpr int TILE_ROW = cache_row_bytes_of<E2M1>(HD), N16 = ST::bytes / 2;
-    const int lane = threadIdx.x & 31, j = lane % LPR;
+    constexpr int LPR = HD / 16, RPW = 32 / LPR, STEP = RPW * kWriteRows;
+    constexpr int TILE_ROW = cache_row_bytes_of<E2M1>(HD), N16 = ST::bytes;   // 16-byte pieces
+    const int lane = threadIdx.x & 31, g = lane % LPR;
     const int half = (p.num_kv_heads + STEP - 1) / STEP;         // pieces of K; as many of V
     const int gw = blockIdx.x * (kWriteThreads / 32) + (threadIdx.x >> 5);
     const int step = gridDim.x * (kWriteThreads / 32) / (2 * half);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_fp4_kernel(Re
     const int piece = gw % (2 * half);
     const bool v = piece >= half;
     const int h0 = (piece - (v ? half : 0)) * STEP + lane / LPR;
-    const uint8_t* src = static_cast<const uint8_t*>(v ? p.value : p.key) + (h0 * HD + 8 * j) * ST::bytes;
+    const uint8_t* src = static_cast<const uint8_t*>(v ? p.value : p.key) + (h0 * HD + 16 * g) * ST::bytes;
     uint8_t* pool = static_cast<uint8_t*>(v ? p.v_cache : p.k_cache);
     const int tile_bytes = p.block_size * TILE_ROW;
     const int64_t src_step = (int64_t)p.num_kv_heads * HD * ST::bytes;
@@ -143,10 +143,12 @@ __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_fp4_kernel(Re
             uint8_t* tile = pool + (blk * p.num_kv_heads + h0) * tile_bytes;
 #pragma unroll
             for (int u = 0; u < kWriteRows; ++u) {
-                float x[8];
-                load8<ST>(now[u], x);
-                CacheRow<E2M1>::store(tile + u * RPW * tile_bytes, p.block_size, HD, row, j, x,
-                                      p.kv_scale, h0 + u * RPW < p.num_kv_heads);
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < N16; ++i) Chunk<ST>::to_float(now[u][i], x + i * (16 / N16));
+                if (h0 + u * RPW < p.num_kv_heads)
+                    CacheRow<E2M1>::store_group(tile + u * RPW * tile_bytes, p.block_size, HD, row, g,
+                                                x, p.kv_scale);
             }
         } else if (slot >= 0 && piece == 0 && lane == 0) {
             set_status(p.status, PKV_DEV_BAD_SLOT);
@@ -208,7 +210,7 @@ cudaError_t launch_reshape_and_cache(const ReshapeParams& p, pkv_dtype src, bool
 
 template <typename ST>
 static cudaError_t launch_write_fp4(const ReshapeParams& p, int num_sms, cudaStream_t stream) {
-    const int step = 256 / p.head_dim * kWriteRows;
+    const int step = 512 / p.head_dim * kWriteRows;
     const int64_t pieces = 2 * (int64_t)((p.num_kv_heads + step - 1) / step);
     const int64_t least = (pieces + 7) / 8, need = (p.num_tokens * pieces + 7) / 8;
     const int64_t full = (int64_t)num_sms * kWriteCtas, most = full > least ? full : least;

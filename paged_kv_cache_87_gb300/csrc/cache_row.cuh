@@ -67,14 +67,18 @@ __device__ __forceinline__ uint32_t e4m3x2_of(uint32_t w) {
     return r;
 }
 
-// Two fp32 values -> two e2m1 codes (round to nearest even, saturate to +-6), `lo` in the
-// low nibble.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+// Eight fp32 values -> e2m1 codes (round to nearest even, saturate to +-6), the first in the
+// lowest nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&q)[8]) {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-        "cvt.u32.u8 %0, t;\n\t}"
-        : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
     return r;
 }
 
@@ -226,40 +230,64 @@ struct CacheRow<E2M1> {
     __device__ __forceinline__ static int scale_at(int B, int d, int row, int j) {
         return B * (d / 2) + row * (d / 16) + (j >> 1);
     }
+    // The scale of a group whose largest magnitude is amax (NaN if it holds one): its e4m3 code,
+    // and what its codes' quotients need.
+    struct Scale {
+        uint32_t code;
+        float step, inverse;    // scale * kv_scale, and its correctly rounded reciprocal
+        bool near;              // every term of a quotient below stays in the normal range
+        __device__ __forceinline__ Scale(float amax, float kv_scale) {
+            code = cvt_e4m3x2(__fdiv_rn(amax, 6.0f * kv_scale), 0.f) & 0xffu;
+            const uint32_t h = e4m3x2_to_f16x2(code);
+            step = __low2float(*reinterpret_cast<const __half2*>(&h)) * kv_scale;
+            inverse = __frcp_rn(step);
+            near = step > 0x1p-100f && step < 0x1p100f && amax * inverse < 0x1p20f;
+        }
+    };
+    // Eight codes: e2m1(x / step), zeros for a scale of 0 or NaN.  x / step is correctly rounded,
+    // from the correctly rounded reciprocal y: q = x y, r = q step - x (exact in a fused
+    // multiply-add), q - r y (P. Markstein, IBM J. Res. Dev. 34, 1990); with r of this sign a zero
+    // keeps its own.  Three operations instead of a division each; where a term could leave the
+    // normal range (a saturated group, far scales) the division.
+    __device__ __forceinline__ static uint32_t codes8(const float* f, const Scale& s) {
+        float q[8];
+        if (s.near) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = f[i] * s.inverse;
+                q[i] = fmaf(-fmaf(t, s.step, -f[i]), s.inverse, t);
+            }
+        } else if (s.step > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(f[i], s.step);
+        } else {
+            return 0u;
+        }
+        return cvt_e2m1x8(q);
+    }
     __device__ __forceinline__ static void store(uint8_t* tile, int B, int d, int row, int j,
                                                  const float (&f)[8], float kv_scale, bool live) {
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = absmax_nan(f[i], amax);
         amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
-        const uint32_t sc = cvt_e4m3x2(__fdiv_rn(amax, 6.0f * kv_scale), 0.f) & 0xffu;
-        const uint32_t sh = e4m3x2_to_f16x2(sc);
-        const float step = __low2float(*reinterpret_cast<const __half2*>(&sh)) * kv_scale;
-        uint32_t w = 0u;
-        if (step > 0.f) {   // not for a scale of 0 or NaN: zero codes
-            // x / step, correctly rounded, from the correctly rounded reciprocal y: q = x y,
-            // r = q step - x (exact in a fused multiply-add), q - r y (P. Markstein, IBM J. Res.
-            // Dev. 34, 1990); with r of this sign a zero keeps its own.  Three operations instead
-            // of a division each; where a term could leave the normal range (a saturated group,
-            // far scales) the division.
-            const float y = __frcp_rn(step);
-            if (step > 0x1p-100f && step < 0x1p100f && amax * y < 0x1p20f) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float q0 = f[2 * i] * y, q1 = f[2 * i + 1] * y;
-                    w |= cvt_e2m1x2(fmaf(-fmaf(q0, step, -f[2 * i]), y, q0),
-                                    fmaf(-fmaf(q1, step, -f[2 * i + 1]), y, q1)) << (8 * i);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w |= cvt_e2m1x2(__fdiv_rn(f[2 * i], step), __fdiv_rn(f[2 * i + 1], step)) << (8 * i);
-            }
-        }
+        const Scale s(amax, kv_scale);
+        const uint32_t w = codes8(f, s);
         if (live) {
             *reinterpret_cast<uint32_t*>(tile + code_at(B, row, j)) = w;
-            if ((j & 1) == 0) tile[scale_at(B, d, row, j)] = (uint8_t)sc;
+            if ((j & 1) == 0) tile[scale_at(B, d, row, j)] = (uint8_t)s.code;
         }
+    }
+    // A whole group, dims 16g .. 16g + 15, by one lane: the same bytes.
+    __device__ __forceinline__ static void store_group(uint8_t* tile, int B, int d, int row, int g,
+                                                       const float (&f)[16], float kv_scale) {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = absmax_nan(f[i], amax);
+        const Scale s(amax, kv_scale);
+        *reinterpret_cast<uint2*>(tile + code_at(B, row, 2 * g)) =
+            make_uint2(codes8(f, s), codes8(f + 8, s));
+        tile[scale_at(B, d, row, 2 * g)] = (uint8_t)s.code;
     }
     template <int HD>
     struct Raw {

@@ -221,7 +221,10 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = w[i];
+            for (int i = 0; i < 8; ++i) {
+                m[i] = w[i];
+                n[i] = 0.f;
+            }
         }
         const bool hit = cached(now.slot);
         const int in_block = (int)(now.slot & ((1 << log_block) - 1));
@@ -244,16 +247,16 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
                 for (int off = LPR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
                 rs = rsqrtf(fmaf(ss, 1.f / HD, p.eps));
             }
-            if (split) {
+            // (a dim that is not rotated has n = 0, and its partner must not reach it as NaN)
+            if (!p.interleaved) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], m[i], __fmul_rn(x[(i + 4) % 8], n[i])) * rs;
-            } else if (turned) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], m[i], __fmul_rn(x[i ^ 1], n[i])) * rs;
+                for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(turned ? x[(i + 4) % 8] : 0.f, n[i]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = x[i] * m[i] * rs;
+                for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(turned ? x[i ^ 1] : 0.f, n[i]);
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], m[i], y[i]) * rs;
             typename R::raw oa = R::pack(y), ob = R::pack(y + 4);
             if (!CACHE || kind == 0) {
                 if (live) {
