@@ -65,7 +65,7 @@ struct Plan {
 };
 
 struct Fp4Plan {
-    int group, nsub, workers;
+    int group, nsub, unit_heads, workers;
     size_t off_ml, total;
 };
 
@@ -113,20 +113,21 @@ pkv_status make_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Plan* p
     return PKV_OK;
 }
 
-// Workspace of the decode over a 4-bit cache: two partial states (m, l, acc of up to 8 heads) of
-// every worker.  The same argument checks as make_plan.
+// Workspace of the decode over a 4-bit cache: two partial states (m, l, acc of a unit's
+// heads) of every worker.  The same argument checks as make_plan.
 pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4Plan* pl) {
     if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_ctx < 0) return PKV_ERR_INVALID_ARG;
     if (HD != 64 && HD != 128) return PKV_ERR_UNSUPPORTED;
     if (B != 8 && B != 16 && B != 32) return PKV_ERR_UNSUPPORTED;
     pl->group = Hq / Hkv;
-    pl->nsub = (pl->group + kFp4Heads - 1) / kFp4Heads;
+    pl->unit_heads = fp4_unit_heads(pl->group);
+    pl->nsub = (pl->group + pl->unit_heads - 1) / pl->unit_heads;
     const int64_t slots = ((int64_t)max_ctx + kFp4Tile - 1) / kFp4Tile + kFp4UnitCost;
     if ((int64_t)Hkv * pl->nsub > INT32_MAX || (int64_t)S * Hkv * pl->nsub > INT32_MAX ||
         (int64_t)S * Hkv * pl->nsub * slots > INT32_MAX - (1 << 24))
         return PKV_ERR_UNSUPPORTED;                       // slots are counted in 32 bits
-    pl->workers = (int)fp4_max_workers(S, Hkv, pl->nsub, max_ctx);
-    const size_t states = (size_t)pl->workers * 2 * kFp4Heads;
+    pl->workers = (int)fp4_max_workers(S, Hkv, pl->nsub, pl->unit_heads, max_ctx);
+    const size_t states = (size_t)pl->workers * 2 * pl->unit_heads;
     pl->off_ml = round_up(states * HD * 4, 256);
     pl->total = round_up(pl->off_ml + states * 8, 256);
     return PKV_OK;
@@ -213,6 +214,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
         f.num_kv_heads = num_kv_heads;
         f.group = fplan.group;
         f.nsub = fplan.nsub;
+        f.unit_heads = fplan.unit_heads;
         f.max_workers = fplan.workers;
         f.part_acc = reinterpret_cast<float*>(ws);
         f.part_ml = reinterpret_cast<float*>(ws + fplan.off_ml);
@@ -224,7 +226,10 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
         f.max_context_len = max_context_len;
         f.qk_scale_log2 = scale * 1.4426950408889634f * kv_scale;
         f.out_scale = kv_scale;
-        return cuda_status(launch_decode_fp4(f, q_dtype, reinterpret_cast<cudaStream_t>(stream)));
+        cudaStream_t fs = reinterpret_cast<cudaStream_t>(stream);
+        return cuda_status(q_dtype == PKV_F32   ? decode_fp4_f32(f, fs)
+                           : q_dtype == PKV_F16 ? decode_fp4_f16(f, fs)
+                                                : decode_fp4_bf16(f, fs));
     }
     DecodeParams p{};
     p.q = query;

@@ -9,8 +9,12 @@ constexpr int kFp4Tile = 128;         // tokens of a tile: the split's unit and 
 constexpr int kFp4UnitCost = 1;       // slots of a unit besides its tiles
 constexpr int kFp4MinQuota = 1;       // slots a worker takes at least
 constexpr int kFp4MaxPieces = 64;     // partial states that one unit leaves, about
-constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most
-constexpr int kFp4Heads = 8;          // query heads of a work unit
+constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most (half with units of 16 heads)
+
+// Query heads of a work unit: one kv head's group, in parts of 16 at most.  Groups of up to eight
+// take the kernel whose unit is eight (long documents: 161 us at eight heads a group; at sixteen,
+// XXX us in one unit against 307 in two).
+inline int fp4_unit_heads(int group) { return group > 8 ? 16 : 8; }
 
 struct DecodeFp4Params {
     const void* q;
@@ -20,9 +24,9 @@ struct DecodeFp4Params {
     const int32_t* context_lens;
     void* out;
     unsigned* status;
-    float* part_acc;       // [workers * 2][kFp4Heads][head_dim]
-    float* part_ml;        // [workers * 2][kFp4Heads][2]: running max (log2 domain) and sum
-    int num_seqs, num_q_heads, num_kv_heads, group, nsub;
+    float* part_acc;       // [workers * 2][unit_heads][head_dim]
+    float* part_ml;        // [workers * 2][unit_heads][2]: running max (log2 domain) and sum
+    int num_seqs, num_q_heads, num_kv_heads, group, nsub, unit_heads;
     int head_dim, block_size, num_blocks, max_blocks, max_context_len;
     int log_block;         // block_size == 1 << log_block
     int workers;           // the split's denominator: every CTA the device holds
@@ -33,13 +37,18 @@ struct DecodeFp4Params {
 };
 
 // Workers that can have work over contexts up to max_ctx: bounds grid and workspace.
-inline int64_t fp4_max_workers(int num_seqs, int num_kv_heads, int nsub, int max_ctx) {
+inline int64_t fp4_max_workers(int num_seqs, int num_kv_heads, int nsub, int unit_heads,
+                               int max_ctx) {
     const int64_t slots = (int64_t)num_seqs * num_kv_heads * nsub *
                           (((int64_t)max_ctx + kFp4Tile - 1) / kFp4Tile + kFp4UnitCost);
     const int64_t w = (slots + kFp4MinQuota - 1) / kFp4MinQuota;
-    return w < 1 ? 1 : (w < kFp4MaxWorkers ? w : kFp4MaxWorkers);
+    const int64_t most = kFp4MaxWorkers * 8 / unit_heads;
+    return w < 1 ? 1 : (w < most ? w : most);
 }
 
-cudaError_t launch_decode_fp4(const DecodeFp4Params& p, pkv_dtype q, cudaStream_t stream);
+// Defined in decode_fp4_f32.cu, decode_fp4_f16.cu and decode_fp4_bf16.cu.
+cudaError_t decode_fp4_f32(const DecodeFp4Params& p, cudaStream_t s);
+cudaError_t decode_fp4_f16(const DecodeFp4Params& p, cudaStream_t s);
+cudaError_t decode_fp4_bf16(const DecodeFp4Params& p, cudaStream_t s);
 
 }  // namespace pkv

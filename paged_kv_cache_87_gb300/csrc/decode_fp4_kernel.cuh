@@ -1,4 +1,4 @@
-// decode_fp4.cu -- single-query decode attention over the 4-bit paged cache.
+// decode_fp4_kernel.cuh -- single-query decode attention over the 4-bit paged cache.
 //
 // o = sum_t softmax_t(scale q.k_t) v_t with k, v = code * scale * kv_scale; kv_scale is folded
 // into the logit scale and the output.
@@ -29,6 +29,8 @@
 // 16 tokens of every tile each, whose states meet in shared memory at the end of a unit.  Units
 // inside one run are written straight to `out`; a worker leaves at most two partial states
 // (its first and its last unit), and merge_fp4_kernel joins those of each cut unit in order.
+#pragma once
+
 #include "decode_fp4.cuh"
 
 #include "cache_row.cuh"
@@ -110,28 +112,32 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMergeThreads = 512;
 
-template <typename QT, int HD>
+// NT: groups of eight query heads that a unit serves (each widened row of K and V serves them all)
+template <typename QT, int HD, int NT>
 struct Cfg {
+    static constexpr int HEADS = 8 * NT;
     static constexpr int ROWB = HD / 2 + HD / 16;
     static constexpr int KV_BYTES = kFp4Tile * ROWB;
-    static constexpr int Q_BYTES = kFp4Heads * HD * QT::bytes;
+    static constexpr int Q_BYTES = HEADS * HD * QT::bytes;
     static constexpr int STAGE_BYTES = (2 * KV_BYTES + Q_BYTES + 127) / 128 * 128;
     static constexpr int NSTAGE = 3;
     static constexpr int NCHUNK = HD / 32;
     static constexpr int NP = std::is_same<QT, F32>::value ? 2 : 1;   // terms of q and p
-    static constexpr int XD = 64;                      // dims exchanged at a time
+    static constexpr int XD = 64;                      // dims of eight heads exchanged at a time
     static constexpr int HS = XD + 1;                  // exchange stride of a head: few conflicts
-    static constexpr int XBUF = kConsumers * kFp4Heads * (HS + 2);    // acc, then m, l
+    static constexpr int XBUF = kConsumers * (8 * HS + 2 * HEADS);    // acc, then m, l
     static constexpr size_t OFF_META = (size_t)NSTAGE * STAGE_BYTES;
     static constexpr size_t OFF_BARS = OFF_META + NSTAGE * 16;
     static constexpr size_t OFF_QF = (OFF_BARS + 2 * NSTAGE * 8 + 15) / 16 * 16;
-    static constexpr size_t OFF_PLAN = OFF_QF + NP * NCHUNK * 32 * 16;  // 32 tiles: int4, int2, rows
+    static constexpr size_t OFF_PLAN = OFF_QF + NP * NT * NCHUNK * 32 * 16;  // 32 tiles: int4, int2, rows
     static constexpr size_t OFF_X = OFF_PLAN + 32 * (16 + 8 + 16 * 4);
     static constexpr size_t SMEM = OFF_X + XBUF * 4 + 128;             // the base is rounded up
     // resident CTAs, by registers.  The queries' operands stay in shared memory (a 16-byte load a
     // chunk): 187 -> 175 us on long documents against registers.  A fifth CTA (72 registers) spills
     // and loses: 200 us.
-    static constexpr int CTAS = HD == 128 ? 3 : 4;
+    static constexpr int CTAS = HD == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);
+    // pieces of 16 tokens a warp works on at once, by registers
+    static constexpr int PIECES = NT == 1 ? 2 : 1;
 };
 
 constexpr int kFirst = 1, kLast = 2, kDone = 4;
@@ -216,11 +222,12 @@ __device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total, int
                (longest + kFp4MaxPieces - 1) / kFp4MaxPieces);
 }
 
-template <typename QT, int HD>
-__global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
+template <typename QT, int HD, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
-    using C = Cfg<QT, HD>;
+    using C = Cfg<QT, HD, NT>;
+    constexpr int HEADS = C::HEADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 127u);
     __shared__ int s_pref[kThreads + 2];
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     // 32 or 64 tokens a gather; those past the context's last block stay out
                     const int per = 4 << log_rt, gathers = ((t.x >> 8) + per - 1) >> (log_rt + 2);
                     uint32_t bytes = 2u * C::ROWB * per * gathers;
-                    const uint32_t qbytes = min(kFp4Heads, p.group - qsub * kFp4Heads) * (HD * QT::bytes);
+                    const uint32_t qbytes = min(HEADS, p.group - qsub * HEADS) * (HD * QT::bytes);
                     if (t.x & kFirst) bytes += qbytes;
                     metas[stage] = t;
                     mbar_arrive_expect_tx(&full[stage], bytes);
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                                     &full[stage], policy);
                     }
                     if (t.x & kFirst) {
-                        const int64_t row = (int64_t)t.y * p.num_q_heads + kvh * p.group + qsub * kFp4Heads;
+                        const int64_t row = (int64_t)t.y * p.num_q_heads + kvh * p.group + qsub * HEADS;
                         bulk_g2s(sb + 2 * C::KV_BYTES,
                                  static_cast<const uint8_t*>(p.q) + row * HD * QT::bytes, qbytes,
                                  &full[stage]);
@@ -369,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
     const uint32_t vsel = (g >> 2) ? 0x7351u : 0x6240u;
 
     uint4* s_qf = reinterpret_cast<uint4*>(smem + C::OFF_QF);   // per chunk: two k-steps of (b0, b1)
-    float o[2 * C::NCHUNK][4];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, qs0 = 0.f, qs1 = 0.f;
-    float lm0 = INFINITY, lm1 = INFINITY;               // kLift - m0, kLift - m1
+    // running states of heads 8 nt + 2c ([0]) and 8 nt + 2c + 1 ([1])
+    float o[NT][2 * C::NCHUNK][4];
+    float m[NT][2], lift[NT][2], l[NT][2], qs[NT][2];   // lift: kLift - m
     int stage = 0;
     uint32_t phase = 0;
 
@@ -380,12 +387,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         constexpr int SUB = decltype(pieces)::value;
         const bool part = nv < 64 * SUB - 48;         // some of the tokens are not valid
         // ---- S^T = K Q^T ----
-        float sa[SUB][2][4];
+        float sa[SUB][NT][2][4];
         uint32_t da[SUB], db[SUB];     // this lane's scale byte of every chunk, rows g and g + 8
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sa[u][0][i] = sa[u][1][i] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sa[u][nt][0][i] = sa[u][nt][1][i] = 0.f;
             const uint8_t* sc = sb + u * SUB_BYTES + ks_a;
             if constexpr (HD == 128) {
                 const uint2 ra = *reinterpret_cast<const uint2*>(sc);
@@ -399,11 +408,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         }
 #pragma unroll
         for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
-            uint4 qf[C::NP][2];
+            uint4 qf[NT][C::NP][2];
 #pragma unroll
-            for (int t = 0; t < C::NP; ++t)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) qf[t][k] = s_qf[(t * C::NCHUNK + 2 * cp + k) * 32 + lane];
+                for (int t = 0; t < C::NP; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        qf[nt][t][k] = s_qf[((nt * C::NP + t) * C::NCHUNK + 2 * cp + k) * 32 + lane];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 uint32_t r[4];
@@ -420,84 +432,83 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     const uint32_t a10 = hmul2(e2m1x2_to_f16x2<2>(wa), fa), a11 = hmul2(e2m1x2_to_f16x2<2>(wb), fb);
                     const uint32_t a12 = hmul2(e2m1x2_to_f16x2<3>(wa), fa), a13 = hmul2(e2m1x2_to_f16x2<3>(wb), fb);
 #pragma unroll
-                    for (int t = 0; t < C::NP; ++t) {
-                        mma_f16(sa[u][0], a00, a01, a02, a03, qf[t][k].x, qf[t][k].y);
-                        mma_f16(sa[u][1], a10, a11, a12, a13, qf[t][k].z, qf[t][k].w);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int t = 0; t < C::NP; ++t) {
+                            mma_f16(sa[u][nt][0], a00, a01, a02, a03, qf[nt][t][k].x, qf[nt][t][k].y);
+                            mma_f16(sa[u][nt][1], a10, a11, a12, a13, qf[nt][t][k].z, qf[nt][t][k].w);
+                        }
                 }
             }
         }
-        // ---- running softmax: [0], [1] are tokens g, [2], [3] tokens g + 8, of heads 2c and
+        // ---- running softmax: elements 0, 1 are tokens g, 2, 3 tokens g + 8, of heads 2c and
         // 2c + 1; y = logit - (running max - kLift), log2 domain ----
-        float z[SUB][4], y[SUB][4];
-        auto exponents = [&] {
+        uint32_t pb[SUB][NT][C::NP][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float z[SUB][4], y[SUB][4];
+            auto exponents = [&] {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[u][i] = fmaf(z[u][i], qs[nt][i & 1], lift[nt][i & 1]);
+                if (part)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
+            };
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[u][i] = (i & 1) ? fmaf(z[u][i], qs1, lm1) : fmaf(z[u][i], qs0, lm0);
-            if (part)
+                for (int i = 0; i < 4; ++i) z[u][i] = sa[u][nt][0][i] + sa[u][nt][1][i];
+            exponents();
+            float top = y[0][0];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, y[u][i]);
+            if (__any_sync(0xffffffffu, top > kSlack + kLift)) {
+                float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
-        };
+                        if (g + (i & 2) * 4 < nv - 64 * u) t[i & 1] = fmaxf(t[i & 1], z[u][i] * qs[nt][i & 1]);
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+                for (int off = 4; off < 32; off <<= 1) {
+                    t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], off));
+                    t[1] = fmaxf(t[1], __shfl_xor_sync(0xffffffffu, t[1], off));
+                }
+                float r[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[u][i] = sa[u][0][i] + sa[u][1][i];
-        exponents();
-        float top = y[0][0];
+                for (int k = 0; k < 2; ++k) {
+                    const bool move = t[k] > m[nt][k] + kSlack;
+                    r[k] = move ? fast_exp2(m[nt][k] - t[k]) : 1.f;
+                    if (move) m[nt][k] = t[k];
+                    lift[nt][k] = kLift - m[nt][k];
+                    l[nt][k] *= r[k];
+                }
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+                for (int mt = 0; mt < 2 * C::NCHUNK; ++mt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, y[u][i]);
-        if (__any_sync(0xffffffffu, top > kSlack + kLift)) {
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2)
-                    if (g + i * 4 < nv - 64 * u) {
-                        t0 = fmaxf(t0, z[u][i] * qs0);
-                        t1 = fmaxf(t1, z[u][i + 1] * qs1);
-                    }
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+                    for (int i = 0; i < 4; ++i) o[nt][mt][i] *= r[i & 1];
+                exponents();
             }
-            const bool n0 = t0 > m0 + kSlack, n1 = t1 > m1 + kSlack;
-            const float r0 = n0 ? fast_exp2(m0 - t0) : 1.f, r1 = n1 ? fast_exp2(m1 - t1) : 1.f;
-            if (n0) m0 = t0;
-            if (n1) m1 = t1;
-            lm0 = kLift - m0;
-            lm1 = kLift - m1;
-            l0 *= r0;
-            l1 *= r1;
 #pragma unroll
-            for (int mt = 0; mt < 2 * C::NCHUNK; ++mt) {
-                o[mt][0] *= r0;
-                o[mt][1] *= r1;
-                o[mt][2] *= r0;
-                o[mt][3] *= r1;
-            }
-            exponents();
-        }
-        uint32_t pb[SUB][C::NP][2];
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-            const float p0 = fast_exp2(y[u][0]), p1 = fast_exp2(y[u][1]);
-            const float p2 = fast_exp2(y[u][2]), p3 = fast_exp2(y[u][3]);
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            const uint32_t ua = pack_f16(p0, p1), ub = pack_f16(p2, p3);
-            pb[u][0][0] = trans8x8(ua);
-            pb[u][0][1] = trans8x8(ub);
-            if constexpr (C::NP == 2) {
-                pb[u][1][0] = trans8x8(pack_f16_rest(p0, p1, ua));
-                pb[u][1][1] = trans8x8(pack_f16_rest(p2, p3, ub));
+            for (int u = 0; u < SUB; ++u) {
+                const float p0 = fast_exp2(y[u][0]), p1 = fast_exp2(y[u][1]);
+                const float p2 = fast_exp2(y[u][2]), p3 = fast_exp2(y[u][3]);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                const uint32_t ua = pack_f16(p0, p1), ub = pack_f16(p2, p3);
+                pb[u][nt][0][0] = trans8x8(ua);
+                pb[u][nt][0][1] = trans8x8(ub);
+                if constexpr (C::NP == 2) {
+                    pb[u][nt][1][0] = trans8x8(pack_f16_rest(p0, p1, ua));
+                    pb[u][nt][1][1] = trans8x8(pack_f16_rest(p2, p3, ub));
+                }
             }
         }
         // ---- O^T += V^T P^T ----
@@ -548,10 +559,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
                     const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
                     const uint32_t d2 = hmul2(e2m1x2_to_f16x2<2>(ob), fb), d3 = hmul2(e2m1x2_to_f16x2<3>(ob), fb);
 #pragma unroll
-                    for (int t = 0; t < C::NP; ++t) {
-                        mma_f16(o[2 * ch], e0, e1, e2, e3, pb[u][t][0], pb[u][t][1]);
-                        mma_f16(o[2 * ch + 1], d0, d1, d2, d3, pb[u][t][0], pb[u][t][1]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int t = 0; t < C::NP; ++t) {
+                            mma_f16(o[nt][2 * ch], e0, e1, e2, e3, pb[u][nt][t][0], pb[u][nt][t][1]);
+                            mma_f16(o[nt][2 * ch + 1], d0, d1, d2, d3, pb[u][nt][t][0], pb[u][nt][t][1]);
+                        }
                 }
             }
         }
@@ -566,132 +579,148 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
         if (meta.x & kDone) return;
         const uint8_t* sb = smem + stage * C::STAGE_BYTES;
         if (meta.x & kFirst) {
-            const int nh = min(kFp4Heads, p.group - meta.z % p.nsub * kFp4Heads);
-            // q row of head g, scaled by a power of two into fp16 (fp16 rows as they are); warp w
-            // forms the operands of chunks w, w + 4, ..: dims 32 ch + 8c .. + 7
-            const uint8_t* sq = sb + 2 * C::KV_BYTES + (g * HD + 8 * c) * QT::bytes;
-            float up = 1.f;
-            qs0 = qs1 = p.qk_scale_log2;
-            if constexpr (!std::is_same<QT, F16>::value) {
-                float amax = 0.f;
+            const int nh = min(HEADS, p.group - meta.z % p.nsub * HEADS);
+            // q row of head 8 nt + g, scaled by a power of two into fp16 (fp16 rows as they are);
+            // warp w forms the operands of chunks w, w + 4, ..: dims 32 ch + 8c .. + 7
 #pragma unroll
-                for (int ch = 0; ch < C::NCHUNK; ++ch) {
+            for (int nt = 0; nt < NT; ++nt) {
+                const bool live = 8 * nt + g < nh;
+                const uint8_t* sq = sb + 2 * C::KV_BYTES + ((8 * nt + g) * HD + 8 * c) * QT::bytes;
+                float up = 1.f;
+                qs[nt][0] = qs[nt][1] = p.qk_scale_log2;
+                if constexpr (!std::is_same<QT, F16>::value) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int ch = 0; ch < C::NCHUNK; ++ch) {
+                        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        if (live) load8<QT>(sq + 32 * ch * QT::bytes, x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) amax = absmax_nan(x[i], amax);
+                    }
+                    amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
+                    amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 2), amax);
+                    const int ex = (int)(__float_as_uint(amax) >> 23) - 127;     // floor(log2), or 128
+                    const int e = ex == 128 ? 0 : min(14 - ex, 126);
+                    up = __uint_as_float((uint32_t)(e + 127) << 23);
+                    const float back = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+                    qs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
+                    qs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+                }
+                for (int ch = warp; ch < C::NCHUNK; ch += kConsumers) {
                     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
+                    if (live) load8<QT>(sq + 32 * ch * QT::bytes, x);
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) amax = absmax_nan(x[i], amax);
+                    for (int i = 0; i < 4; ++i) {
+                        const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
+                        hi[i] = pack_f16(x0, x1);
+                        lo[i] = C::NP == 2 ? pack_f16_rest(x0, x1, hi[i]) : 0u;
+                    }
+                    uint4* to = s_qf + (nt * C::NP * C::NCHUNK + ch) * 32 + lane;
+                    to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (C::NP == 2) to[C::NCHUNK * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 1), amax);
-                amax = absmax_nan(__shfl_xor_sync(0xffffffffu, amax, 2), amax);
-                const int ex = (int)(__float_as_uint(amax) >> 23) - 127;     // floor(log2), or 128
-                const int e = ex == 128 ? 0 : min(14 - ex, 126);
-                up = __uint_as_float((uint32_t)(e + 127) << 23);
-                const float qs = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-                qs0 = __shfl_sync(0xffffffffu, qs, 8 * c);
-                qs1 = __shfl_sync(0xffffffffu, qs, 8 * c + 4);
-            }
-            for (int ch = warp; ch < C::NCHUNK; ch += kConsumers) {
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (g < nh) load8<QT>(sq + 32 * ch * QT::bytes, x);
-                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
-                    hi[i] = pack_f16(x0, x1);
-                    lo[i] = C::NP == 2 ? pack_f16_rest(x0, x1, hi[i]) : 0u;
+                for (int mt = 0; mt < 2 * C::NCHUNK; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    m[nt][k] = -INFINITY;
+                    lift[nt][k] = INFINITY;
+                    l[nt][k] = 0.f;
                 }
-                s_qf[ch * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if constexpr (C::NP == 2)
-                    s_qf[(C::NCHUNK + ch) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             // the operands are whole; the unit before is done with its own (it met at its end)
             named_bar_sync(1, kConsumers * 32);
-#pragma unroll
-            for (int mt = 0; mt < 2 * C::NCHUNK; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][i] = 0.f;
-            m0 = m1 = -INFINITY;
-            lm0 = lm1 = INFINITY;
-            l0 = l1 = 0.f;
         }
         const int nv = (meta.x >> 8) - 16 * warp;   // tokens of the tile from this warp's first on
-        if (nv > 64) attend(std::integral_constant<int, 2>(), sb, nv);
-        else if (nv > 0) attend(std::integral_constant<int, 1>(), sb, nv);
+        if constexpr (C::PIECES == 2) {
+            if (nv > 64) attend(std::integral_constant<int, 2>(), sb, nv);
+            else if (nv > 0) attend(std::integral_constant<int, 1>(), sb, nv);
+        } else {
+            for (int u = 0; u < 2; ++u)
+                if (nv > 64 * u) attend(std::integral_constant<int, 1>(), sb + u * SUB_BYTES, nv - 64 * u);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
         if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
         if (!(meta.x & kLast)) continue;
 
         // ---------------- end of the segment: the four warps' states meet ----------------
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-        }
         const int kvh = meta.z / p.nsub, qsub = meta.z % p.nsub;
-        const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
+        const int nh = min(HEADS, p.group - qsub * HEADS);
         float* xa = reinterpret_cast<float*>(smem + C::OFF_X);
-        float* xm = xa + kConsumers * kFp4Heads * C::HS;
-        float* xl = xm + kConsumers * kFp4Heads;
-        const int hw = warp * kFp4Heads + 2 * c;
-        const int h = threadIdx.x >> 4, part = threadIdx.x & 15;    // 16 threads a head
-        const int64_t row = (int64_t)meta.y * p.num_q_heads + kvh * p.group + qsub * kFp4Heads + h;
-        const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.w, 0)) * kFp4Heads + h;
-        if (g == 0) {
-            xm[hw] = m0;
-            xm[hw + 1] = m1;
-            xl[hw] = l0;
-            xl[hw + 1] = l1;
-        }
-        float f[kConsumers] = {0.f};                                // the warps' shares
+        float* xm = xa + kConsumers * 8 * C::HS;
+        float* xl = xm + kConsumers * HEADS;
+        const int part = threadIdx.x & 15;                          // 16 threads a head
 #pragma unroll
-        for (int pass = 0; pass < HD / C::XD; ++pass) {             // 64 dims at a time
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < C::XD / 16; ++mt) {
-                const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);  // [2], [3]: dim + 2
-                const float* v = o[pass * (C::XD / 16) + mt];
-                if (2 * c < nh) {
-                    xa[hw * C::HS + dim] = v[0];
-                    xa[hw * C::HS + dim + 2] = v[2];
-                }
-                if (2 * c + 1 < nh) {
-                    xa[(hw + 1) * C::HS + dim] = v[1];
-                    xa[(hw + 1) * C::HS + dim + 2] = v[3];
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], off);
+                if (g == 0) {
+                    xm[warp * HEADS + 8 * nt + 2 * c + k] = m[nt][k];
+                    xl[warp * HEADS + 8 * nt + 2 * c + k] = l[nt][k];
                 }
             }
-            named_bar_sync(1, kConsumers * 32);
-            if (h < nh) {
-                if (pass == 0) {
-                    float M = -INFINITY, L = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * kFp4Heads + h]);
+        for (int nt = 0; nt < NT; ++nt) {                           // eight heads at a time,
+            if (8 * nt >= nh) break;
+            const int h = 8 * nt + (threadIdx.x >> 4);
+            const int64_t row = (int64_t)meta.y * p.num_q_heads + kvh * p.group + qsub * HEADS + h;
+            const int64_t pi = ((int64_t)blockIdx.x * 2 + max(meta.w, 0)) * HEADS + h;
+            float f[kConsumers] = {0.f};                            // the warps' shares
 #pragma unroll
-                    for (int w = 0; w < kConsumers; ++w) {
-                        const float mw = xm[w * kFp4Heads + h];
-                        f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-                        L = fmaf(xl[w * kFp4Heads + h], f[w], L);
+            for (int pass = 0; pass < HD / C::XD; ++pass) {         // 64 dims at a time
+#pragma unroll
+                for (int mt = 0; mt < C::XD / 16; ++mt) {
+                    const int dim = 32 * (mt >> 1) + 4 * g + (mt & 1);  // [2], [3]: dim + 2
+                    const float* v = o[nt][pass * (C::XD / 16) + mt];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (8 * nt + 2 * c + k < nh) {
+                            float* to = xa + (warp * 8 + 2 * c + k) * C::HS + dim;
+                            to[0] = v[k];
+                            to[2] = v[2 + k];
+                        }
+                }
+                named_bar_sync(1, kConsumers * 32);
+                if (h < nh) {
+                    if (pass == 0) {
+                        float M = -INFINITY, L = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, xm[w * HEADS + h]);
+#pragma unroll
+                        for (int w = 0; w < kConsumers; ++w) {
+                            const float mw = xm[w * HEADS + h];
+                            f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+                            L = fmaf(xl[w * HEADS + h], f[w], L);
+                        }
+                        if (meta.w < 0) {
+                            const float inv = p.out_scale / L;
+#pragma unroll
+                            for (int w = 0; w < kConsumers; ++w) f[w] *= inv;
+                        } else if (part == 0) {
+                            p.part_ml[2 * pi] = M;
+                            p.part_ml[2 * pi + 1] = L;
+                        }
                     }
-                    if (meta.w < 0) {
-                        const float inv = p.out_scale / L;
 #pragma unroll
-                        for (int w = 0; w < kConsumers; ++w) f[w] *= inv;
-                    } else if (part == 0) {
-                        p.part_ml[2 * pi] = M;
-                        p.part_ml[2 * pi + 1] = L;
+                    for (int i = 0; i < C::XD / 16; ++i) {
+                        const int dim = part + 16 * i;
+                        float A = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kConsumers; ++w)
+                            A = fmaf(xa[(w * 8 + h - 8 * nt) * C::HS + dim], f[w], A);
+                        if (meta.w < 0) store_from_float<QT>(p.out, row * HD + pass * C::XD + dim, A);
+                        else p.part_acc[pi * HD + pass * C::XD + dim] = A;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < C::XD / 16; ++i) {
-                    const int dim = part + 16 * i;
-                    float A = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kConsumers; ++w)
-                        A = fmaf(xa[(w * kFp4Heads + h) * C::HS + dim], f[w], A);
-                    if (meta.w < 0) store_from_float<QT>(p.out, row * HD + pass * C::XD + dim, A);
-                    else p.part_acc[pi * HD + pass * C::XD + dim] = A;
-                }
+                named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
             }
-            named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
         }
     }
 }
@@ -700,9 +729,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD>::CTAS))
 // first to do so, the CTA joins the unit's partial states and writes its heads.  Sixteen warps
 // share the heads: warp w takes head w % nh's pieces w / nh, w / nh + 16 / nh, ..., four pieces'
 // loads in flight at once; the order of the sums is fixed.
-template <typename QT, int HD>
+template <typename QT, int HD, int NT>
 __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Params p) {
     constexpr int WARPS = kMergeThreads / 32, V = HD / 32, FLY = 4;   // dims of a lane
+    constexpr int HEADS = 8 * NT;
     __shared__ int s_pref[kMergeThreads + 2];
     __shared__ int2 s_wsum[WARPS];
     __shared__ float s_acc[WARPS][HD], s_m[WARPS], s_l[WARPS];
@@ -719,7 +749,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Param
     const int w0 = dstart / q, w1 = (uend - 1) / q;             // workers of the unit's tiles
     if (pos >= total || pos <= dstart || w0 != blockIdx.x) return;
     const int kvh = u / p.nsub, qsub = u % p.nsub;
-    const int nh = min(kFp4Heads, p.group - qsub * kFp4Heads);
+    const int nh = min(HEADS, p.group - qsub * HEADS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = warp % nh, step = WARPS / nh;
     float M = -INFINITY, L = 0.f, A[V];
@@ -732,7 +762,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Param
             for (int k = 0; k < FLY; ++k) {
                 // a worker's state 0 is the unit it starts inside of, 1 the one it ends inside of
                 const int wk = w + k * step;
-                const int64_t pi = ((int64_t)wk * 2 + (wk == w0 ? 1 : 0)) * kFp4Heads + h;
+                const int64_t pi = ((int64_t)wk * 2 + (wk == w0 ? 1 : 0)) * HEADS + h;
                 m[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi) : -INFINITY;
                 l[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi + 1) : 0.f;
 #pragma unroll
@@ -774,21 +804,21 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Param
 #pragma unroll
         for (int i = 0; i < V; ++i) A[i] = fmaf(s_acc[w][lane + 32 * i], f, A[i]);
     }
-    const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + qsub * kFp4Heads + h;
+    const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + qsub * HEADS + h;
     const float inv = p.out_scale / L;
 #pragma unroll
     for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, row * HD + lane + 32 * i, A[i] * inv);
 }
 
-template <typename QT, int HD>
+template <typename QT, int HD, int NT>
 cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
-    using C = Cfg<QT, HD>;
+    using C = Cfg<QT, HD, NT>;
     static int workers[64] = {0};          // CTAs the device holds at once
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = decode_fp4_kernel<QT, HD>;
+    auto kernel = decode_fp4_kernel<QT, HD, NT>;
     if (workers[dev] == 0) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
         if (err != cudaSuccess) return err;
@@ -798,7 +828,7 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (err != cudaSuccess) return err;
         const int w = (per_sm > 0 ? per_sm : 1) * sms;
-        workers[dev] = w < kFp4MaxWorkers ? w : kFp4MaxWorkers;
+        workers[dev] = w < kFp4MaxWorkers / NT ? w : kFp4MaxWorkers / NT;
     }
     DecodeFp4Params p = p0;
     // pools as rows of 16 tokens of one kv head (8 in blocks of 8): what one gather moves four of
@@ -828,15 +858,15 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)(grid - 1), 1, 1);
     cfg.blockDim = dim3(kMergeThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD>, p);
+    return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT>, p);
+}
+
+template <typename QT>
+cudaError_t launch_decode_fp4(const DecodeFp4Params& p, cudaStream_t stream) {
+    if (p.unit_heads == 16)
+        return p.head_dim == 128 ? launch<QT, 128, 2>(p, stream) : launch<QT, 64, 2>(p, stream);
+    return p.head_dim == 128 ? launch<QT, 128, 1>(p, stream) : launch<QT, 64, 1>(p, stream);
 }
 
 }  // namespace
-
-cudaError_t launch_decode_fp4(const DecodeFp4Params& p, pkv_dtype q, cudaStream_t stream) {
-    if (q == PKV_F32) return p.head_dim == 128 ? launch<F32, 128>(p, stream) : launch<F32, 64>(p, stream);
-    if (q == PKV_F16) return p.head_dim == 128 ? launch<F16, 128>(p, stream) : launch<F16, 64>(p, stream);
-    return p.head_dim == 128 ? launch<BF16, 128>(p, stream) : launch<BF16, 64>(p, stream);
-}
-
 }  // namespace pkv
