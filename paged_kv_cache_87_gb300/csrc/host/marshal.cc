@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/Dtype.h>
@@ -39,9 +40,15 @@ const at::Tensor& tensor(PyObject* o) {
     return THPVariable_Unpack(o);
 }
 
+// The library works on the current device (its pointers, its stream, its status word).
+void here(const at::Tensor& t) {
+    need(t.get_device() == c10::cuda::current_device(), "tensors must be on the current CUDA device");
+}
+
 const at::Tensor& contiguous(PyObject* o, const char* text) {
     const at::Tensor& t = tensor(o);
     need(t.is_cuda() && t.is_contiguous(), text);
+    here(t);
     return t;
 }
 
@@ -128,6 +135,7 @@ int64_t head_rows(const at::Tensor& t, int64_t heads, int64_t d) {
     const auto s = t.strides();
     need(t.is_cuda() && s[2] == 1 && (heads == 1 || s[1] == d),
          "rows must be CUDA tensors [T, heads, d] with their heads contiguous");
+    here(t);
     return t.size(0) > 1 ? s[0] : heads * d;
 }
 

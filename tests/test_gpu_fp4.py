@@ -335,6 +335,16 @@ def test_decode_split_contexts(dt, lens):
     check_decode(np.random.default_rng(len(lens)), lens, 8, 2, 128, 16, dt, 1.0)
 
 
+@pytest.mark.parametrize("bound", [4096, 100000])
+def test_decode_bound_far_above_the_lengths(bound):
+    check_decode(np.random.default_rng(5), [300, 0, 77, 2048], 8, 2, 128, 8, "bf16", 1.0, max_ctx=bound)
+
+
+def test_decode_nothing_cached():
+    check_decode(np.random.default_rng(5), [0] * 40, 8, 2, 128, 8, "bf16", 1.0, max_ctx=0)
+    check_decode(np.random.default_rng(5), [0] * 40, 8, 2, 64, 16, "f32", 1.0, max_ctx=500)
+
+
 def test_decode_many_sequences():
     rng = np.random.default_rng(4)
     check_decode(rng, rng.integers(0, 90, 1500).tolist(), 4, 2, 64, 8, "bf16", 1.0)
@@ -351,16 +361,143 @@ def test_decode_queries_and_scales_far_from_one(dt, q_mul, kv):
     check_decode(np.random.default_rng(7), [300, 65], 4, 2, 64, 16, dt, kv, q_mul=1.0)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.09])
+def test_decode_takes_any_finite_scale(scale):
+    """A scale of 0 weighs every token alike; a negative one turns the order around."""
+    rng = np.random.default_rng(14)
+    h, hq, d, B, lens = 2, 6, 64, 16, [70, 1, 200]
+    table, nb = tables_of(rng, lens, B)
+    ck, gk = cache_of(rng, nb, h, B, d, 1.0)
+    cv, gv = cache_of(rng, nb, h, B, d, 1.0)
+    q = (torch.randn(3, hq, d) / 8).half()
+    out = binding.pkv_paged_decode_attention(q.cuda(), gk, gv, torch.from_numpy(table).cuda(),
+                                             torch.tensor(lens, dtype=torch.int32, device="cuda"), 200, scale)
+    vk, vv = fp4.values(ck, d, 1.0), fp4.values(cv, d, 1.0)
+    for s, n in enumerate(lens):
+        rk, rv = (rows_of(x, table[s], n, B).transpose(1, 0, 2) for x in (vk, vv))
+        ref = fp4.attention(f64(q[s]), rk, rv, scale)
+        tol = decode_bound(f64(q[s]), rk, rv, abs(scale), "f16") * 1.01 + HALF["f16"] * np.abs(ref)
+        assert (np.abs(f64(out[s]) - ref) <= tol).all()
+
+
+def test_a_query_row_of_nan_or_infinity_stays_alone():
+    rng = np.random.default_rng(15)
+    h, d, B = 2, 128, 16
+    table, nb = tables_of(rng, [300, 17], B)
+    _, g = cache_of(rng, nb, h, B, d, 1.0)
+    args = (g, g, torch.from_numpy(table).cuda(), torch.tensor([300, 17], dtype=torch.int32, device="cuda"), 300, 0.05)
+    for dt in (torch.bfloat16, torch.float16, torch.float32):
+        q = torch.randn(2, 8, d, device="cuda").to(dt) / 32
+        ref = binding.pkv_paged_decode_attention(q, *args)
+        q[0, 1, 3], q[1, 6, 100] = float("nan"), float("inf")
+        got = binding.pkv_paged_decode_attention(q, *args)
+        assert torch.isnan(got[0, 1]).all() and torch.isnan(got[1, 6]).all()
+        keep = torch.ones(2, 8, dtype=torch.bool)
+        keep[0, 1] = keep[1, 6] = False
+        assert torch.equal(got[keep], ref[keep])
+
+
+def test_caches_beyond_32_bits():
+    """Blocks on either side of 2 and 4 GB of each cache: written, fused-written, copied, decoded
+    and read back."""
+    h, d, B = 8, 128, 16
+    tile = h * B * 72
+    nb = (1 << 32) // tile + 40
+    k = torch.empty(binding.fp4_cache_shape(nb, h, B, d), dtype=torch.uint8, device="cuda")
+    v = torch.empty_like(k)
+    lo, hi = (1 << 31) // tile, (1 << 32) // tile
+    blocks = [lo - 1, lo, lo + 1, hi - 1, hi, hi + 1, nb - 1, 0]
+    T = len(blocks) * B
+    slots = torch.tensor([b * B + r for b in blocks for r in range(B)], device="cuda")
+    key, val = (torch.randn(T, h, d, device="cuda").bfloat16() for _ in range(2))
+    binding.pkv_reshape_and_cache(key, val, k, v, slots)
+    # the same tokens in a small cache at blocks 0, 1, ..
+    sk = torch.empty(binding.fp4_cache_shape(len(blocks) + 1, h, B, d), dtype=torch.uint8, device="cuda")
+    sv = torch.empty_like(sk)
+    binding.pkv_reshape_and_cache(key, val, sk, sv, torch.arange(T, device="cuda"))
+    for i, b in enumerate(blocks):
+        assert torch.equal(k[b], sk[i]) and torch.equal(v[b], sv[i])
+    cs = torch.cat([torch.ones(4, 32), torch.zeros(4, 32)], 1).cuda()
+    pos = torch.zeros(T, dtype=torch.int64, device="cuda")
+    q = torch.randn(1, 16, d, device="cuda").bfloat16()
+    qq = q.expand(T, 16, d).contiguous()
+    for c in (k, v):
+        c[blocks[:3]] = 0
+    binding.pkv_qk_norm_rope_and_cache(qq, key, val, cs, pos, k, v, slots)      # no turn, no norm
+    for i, b in enumerate(blocks):
+        assert torch.equal(k[b], sk[i]) and torch.equal(v[b], sv[i])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    far, near = i32([blocks]), i32([list(range(len(blocks)))])
+    a = binding.pkv_paged_decode_attention(q, k, v, far, i32([T - 3]), T, 0.1)
+    b = binding.pkv_paged_decode_attention(q, sk, sv, near, i32([T - 3]), T, 0.1)
+    assert torch.equal(a, b)
+    a = binding.pkv_gather_cache(k, v, far, i32([0, T]), T, torch.bfloat16)
+    b = binding.pkv_gather_cache(sk, sv, near, i32([0, T]), T, torch.bfloat16)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    binding.pkv_copy_blocks(k, v, [[hi + 1, 5], [lo, nb - 2]])
+    assert torch.equal(k[5], sk[5]) and torch.equal(v[nb - 2], sv[1])
+    assert binding.pkv_get_device_status() == 0
+
+
+def test_prepared_calls_and_two_streams_at_once():
+    """The marshalled calls issue the same work; two decodes run beside each other, each with a
+    workspace of its own, one of them captured."""
+    rng = np.random.default_rng(16)
+    args, out = check_decode(rng, [900, 33, 2500], 8, 2, 128, 16, "bf16", 1.0)
+    other, out2 = check_decode(rng, [10, 0, 4000, 777], 16, 1, 64, 32, "f16", 0.5)
+    got = torch.empty_like(out)
+    call = binding.prepare_paged_decode_attention(*args, out=got)
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(got, out)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    need = binding.pkv_decode_workspace_bytes(4, 16, 1, 64, 32, 4000, "e2m1")
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    got2 = torch.empty_like(out2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.pkv_paged_decode_attention(*other, kv_scale=0.5, workspace=ws, out=got2)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got.zero_(), got2.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            graph.replay()
+        binding.pkv_paged_decode_attention(*args, out=got, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(got, out) and torch.equal(got2, out2)
+    # a prepared write, and the write on a stream of its own
+    T, h, d, B = 40, 2, 64, 8
+    key, val = (torch.randn(T, h, d, device="cuda").half() for _ in range(2))
+    slots = torch.randperm(48, device="cuda")[:T]
+    a, b, c, e = (torch.zeros(binding.fp4_cache_shape(6, h, B, d), dtype=torch.uint8, device="cuda") for _ in range(4))
+    binding.pkv_reshape_and_cache(key, val, a, b, slots)
+    call = binding.prepare_reshape_and_cache(key, val, c, e, slots)
+    call()
+    assert torch.equal(a, c) and torch.equal(b, e)
+    rows = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    table = torch.arange(6, dtype=torch.int32, device="cuda")[None]
+    ref = binding.pkv_gather_cache(a, b, table, rows, 40, torch.float32)
+    torch.cuda.synchronize()
+    again = binding.pkv_gather_cache(a, b, table, rows, 40, torch.float32, stream=s1)
+    torch.cuda.synchronize()
+    assert torch.equal(ref[0], again[0]) and torch.equal(ref[1], again[1])
+    assert binding.pkv_get_device_status() == 0
+
+
 def test_decode_prefix_entry_is_the_plain_decode():
     args, out = check_decode(np.random.default_rng(8), [100, 700], 8, 2, 128, 16, "bf16", 1.0)
     again = binding.pkv_paged_decode_attention(*args, prefix=True)
     assert torch.equal(out, again)
 
 
-def test_decode_noalloc_and_a_larger_bound_give_the_same_bits():
+def test_decode_noalloc_gives_the_same_bits():
     args, out = check_decode(np.random.default_rng(8), [100, 700, 0, 64], 8, 2, 128, 16, "bf16", 1.0)
     assert torch.equal(out, binding.pkv_paged_decode_attention_noalloc(*args))
-    assert torch.equal(out, binding.pkv_paged_decode_attention(*args))
+    # units of 16 heads and a full chip of workers: the static scratch still suffices
+    args, out = check_decode(np.random.default_rng(9), [3000, 40, 1500], 64, 4, 128, 8, "f32", 1.0)
+    assert torch.equal(out, binding.pkv_paged_decode_attention_noalloc(*args))
+    assert binding.pkv_decode_workspace_bytes(300, 128, 8, 128, 16, 131072, "e2m1") <= binding.NOALLOC_SCRATCH_BYTES
 
 
 def test_decode_is_deterministic_and_replays_in_a_graph():

@@ -227,5 +227,15 @@ def test_binding_refuses_before_any_call(lib):
         binding.pkv_gather_cache(f4, f4, i32(3, 4), i32(3), 5, torch.float16)
     with pytest.raises(ValueError):
         binding.pkv_gather_cache(f4, f4[:, :1], i32(3, 4), i32(4), 5, torch.float16)
+    with pytest.raises(ValueError):                        # a negative number of rows
+        binding.pkv_gather_cache(f4, f4, i32(3, 4), i32(4), -1, torch.float16)
+    with pytest.raises(TypeError):
+        binding.pkv_gather_cache(f4, f4, None, i32(4), 5, torch.float16)
+    with pytest.raises(KeyError):                          # a type that the library does not know
+        binding.pkv_qk_norm_rope(q.double(), k.double(), cs, pos)
+    with pytest.raises(ValueError):                        # too few slots
+        binding.pkv_reshape_and_cache(k, k, kc, kc, slots[:2])
+    with pytest.raises(ValueError):                        # a row of tables for each query
+        binding.pkv_paged_decode_attention(z(3, 4, 64, dtype=torch.bfloat16), kc, kc, i32(2, 4), i32(3), 64, 0.1)
     with pytest.raises(ValueError):                        # queries of another head_dim
         binding.pkv_paged_decode_attention(z(1, 2, 64), f4, f4, i32(1, 4), i32(1), 64, 0.1)
