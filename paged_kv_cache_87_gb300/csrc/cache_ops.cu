@@ -105,6 +105,7 @@ template <typename ST, int HD>
 __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_fp4_kernel(ReshapeParams p,
                                                                               int log_block) {
     pdl_launch_dependents();   // the decode launched next may start its launch now
+    pdl_wait();
     constexpr int LPR = HD / 16, RPW = 32 / LPR, STEP = RPW * kWriteRows;
     constexpr int TILE_ROW = cache_row_bytes_of<E2M1>(HD), N16 = ST::bytes;   // 16-byte pieces
     const int lane = threadIdx.x & 31, g = lane % LPR;
@@ -216,11 +217,9 @@ static cudaError_t launch_write_fp4(const ReshapeParams& p, int num_sms, cudaStr
     const int64_t full = (int64_t)num_sms * kWriteCtas, most = full > least ? full : least;
     const unsigned grid = (unsigned)(need < most ? need : most);
     const int log_block = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
-    if (p.head_dim == 128)
-        reshape_and_cache_fp4_kernel<ST, 128><<<grid, kWriteThreads, 0, stream>>>(p, log_block);
-    else
-        reshape_and_cache_fp4_kernel<ST, 64><<<grid, kWriteThreads, 0, stream>>>(p, log_block);
-    return cudaGetLastError();
+    return launch_overlapped(p.head_dim == 128 ? reshape_and_cache_fp4_kernel<ST, 128>
+                                               : reshape_and_cache_fp4_kernel<ST, 64>,
+                             grid, kWriteThreads, stream, p, log_block);
 }
 
 cudaError_t launch_reshape_and_cache_fp4(const ReshapeParams& p, pkv_dtype src, int num_sms,

@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Param
     __shared__ int s_pref[kMergeThreads + 2];
     __shared__ int2 s_wsum[WARPS];
     __shared__ float s_acc[WARPS][HD], s_m[WARPS], s_l[WARPS];
+    pdl_launch_dependents();   // the kernel after waits for this one, and this one for the decode
     scan_slots<kMergeThreads>(p, s_pref, s_wsum);
     const int upi = p.num_kv_heads * p.nsub;
     const int total = s_pref[kMergeThreads] * upi;

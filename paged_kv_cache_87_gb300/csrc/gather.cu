@@ -19,6 +19,7 @@ constexpr int kGatherThreads = 256;
 template <typename KT, typename OT, int HD>
 __global__ void __launch_bounds__(kGatherThreads) gather_cache_kernel(GatherParams p) {
     pdl_launch_dependents();
+    pdl_wait();
     __shared__ int64_t s_place[kGatherRows];   // block * block_size + row in it, or -1
     const int r0 = blockIdx.x * kGatherRows;
     const int n = min(kGatherRows, p.total_rows - r0);
@@ -86,9 +87,9 @@ __global__ void __launch_bounds__(kGatherThreads) gather_cache_kernel(GatherPara
 template <typename KT, typename OT>
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
     const int grid = (p.total_rows + kGatherRows - 1) / kGatherRows;
-    if (p.head_dim == 128) gather_cache_kernel<KT, OT, 128><<<grid, kGatherThreads, 0, stream>>>(p);
-    else gather_cache_kernel<KT, OT, 64><<<grid, kGatherThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(p.head_dim == 128 ? gather_cache_kernel<KT, OT, 128>
+                                               : gather_cache_kernel<KT, OT, 64>,
+                             (unsigned)grid, kGatherThreads, stream, p);
 }
 
 cudaError_t launch_gather_cache(const GatherParams& p, pkv_dtype kv, pkv_dtype out,

@@ -15,6 +15,7 @@
 // same bits as after the two separate calls.
 #include "norm_rope.cuh"
 
+#include "cache_ops.cuh"
 #include "cache_row.cuh"
 
 namespace pkv {
@@ -78,6 +79,7 @@ struct TokenRows {
 template <typename ST, typename KT, int HD>
 __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopeParams p, int log_block) {
     pdl_launch_dependents();   // the attention launched next may start its launch now
+    pdl_wait();
     constexpr bool CACHE = !std::is_same<KT, NoCache>::value;
     constexpr int LPR = HD / 8, RPW = 32 / LPR, STEP = RPW * kNormRows;   // lanes a row, rows a warp
     using R = Four<ST>;
@@ -322,8 +324,8 @@ cudaError_t launch_norm_rope_d(const NormRopeParams& p, cudaStream_t stream) {
     const int64_t most = resident[dev] > least ? resident[dev] : least;
     const int64_t need = (p.num_tokens * pieces + WARPS - 1) / WARPS;
     const int log_block = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
-    kernel<<<(unsigned)(need < most ? need : most), kNormThreads, 0, stream>>>(p, log_block);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, (unsigned)(need < most ? need : most), kNormThreads, stream, p,
+                             log_block);
 }
 
 template <typename ST, typename KT>
