@@ -6,14 +6,18 @@
 namespace pkv {
 
 constexpr int kFp4Tile = 128;         // tokens of a tile: the split's unit and a ring stage
-constexpr int kFp4UnitCost = 1;       // slots of a unit besides its tiles
-constexpr int kFp4MinQuota = 1;       // slots a worker takes at least
-constexpr int kFp4MaxPieces = 64;     // partial states that one unit leaves, about
+// Slots of a unit besides its tiles (0: a serving batch took 144 us instead of 116; 2: the same).
+constexpr int kFp4UnitCost = 1;
+// Slots a worker takes at least (one context of 600 tokens: 8.0 us with 1, 8.7 with 2).
+constexpr int kFp4MinQuota = 1;
+// Partial states that one unit leaves, about (one context of 100,000 tokens and one kv head: 95 us
+// without a bound, 22 with 64 or 128, 29 with 32).
+constexpr int kFp4MaxPieces = 64;
 constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most (half with units of 16 heads)
 
 // Query heads of a work unit: one kv head's group, in parts of 16 at most.  Groups of up to eight
-// take the kernel whose unit is eight (long documents: 161 us at eight heads a group; at sixteen,
-// XXX us in one unit against 307 in two).
+// take the kernel whose unit is eight (long documents: 160 us at eight heads a group; at sixteen,
+// 233 us in one unit against 307 in two).
 inline int fp4_unit_heads(int group) { return group > 8 ? 16 : 8; }
 
 struct DecodeFp4Params {
@@ -33,7 +37,7 @@ struct DecodeFp4Params {
     int max_workers;       // workers that can have work, by max_context_len
     float qk_scale_log2;   // scale * log2(e) * kv_scale
     float out_scale;       // kv_scale
-    uint32_t two4, two12, two16;   // 2^4, 2^12, 2^16: shifts as products (decode_fp4.cu)
+    uint32_t two4, two12, two16;   // 2^4, 2^12, 2^16: shifts as products
 };
 
 // Workers that can have work over contexts up to max_ctx: bounds grid and workspace.

@@ -16,19 +16,36 @@
 // that rounding.
 //
 // Layout.  32 dims of a row are 16 bytes, eight rows of them one 128-byte line: ldmatrix reads
-// them free of bank conflicts with no swizzle, and one bulk copy moves a (block, kv head) tile
-// with its scales.  A lane's 4-byte word of K holds dims 8c .. 8c + 7 of row g: its four bytes
+// them free of bank conflicts with no swizzle, and one gather moves 32 or 64 tokens of K or V, codes
+// and scales.  A lane's 4-byte word of K holds dims 8c .. 8c + 7 of row g: its four bytes
 // are four operand pairs, the reduction index being permuted for K and q alike.  A transposed
-// word of V holds dims 4g .. 4g + 3 of tokens 2c and 2c + 1: five bit operations pair the
-// tokens' nibbles in bytes.
+// word of V holds dims 4g .. 4g + 3 of tokens 2c and 2c + 1: three products (as shifts) and two bit
+// selections pair the tokens' nibbles in bytes.  (Leaving the pairs of dims as they are and giving
+// each of the two a product with zeros in the weights saves those and costs eight more mma: 163 us
+// against 160 on long documents, 252 against 233 with sixteen heads.)
 //
-// Split.  Every (sequence, kv head, 8 query heads) unit is cut into 64-token tiles, and the
+// Split.  Every (sequence, kv head, 8 or 16 query heads) unit is cut into 128-token tiles, and the
 // flattened tiles are dealt in equal runs to one CTA each ("worker"), all resident at once.
 // Every CTA derives the plan by itself from context_lens (a block-wide scan), so no planning
-// kernel runs first.  A CTA is a producer warp filling a ring of tiles and four consumer warps,
-// 16 tokens of every tile each, whose states meet in shared memory at the end of a unit.  Units
-// inside one run are written straight to `out`; a worker leaves at most two partial states
-// (its first and its last unit), and merge_fp4_kernel joins those of each cut unit in order.
+// kernel runs first.  A CTA is a producer warp, which plans 32 tiles at a time, one a lane, and
+// fills a ring of them, and four consumer warps, 2 x 16 tokens of every tile each, whose states
+// meet in shared memory at the end of a unit.  Units inside one run are written straight to `out`; a
+// worker leaves at most two partial states (its first and its last unit), and merge_fp4_kernel
+// joins those of each cut unit in order.
+//
+// What bounds it.  The consumers' issue slots, not HBM: 292 instructions for 16 tokens of K and V at
+// head_dim 128 (128 of them the converts and multiplies), issued at 2.35 a clock an SM.  Without the
+// arithmetic the same kernel streams at 0.97 of the copy rate.  Measured (device time, GB300):
+//   long documents (8 x 32k - 131k tokens, 64 / 8 heads, d 128, blocks of 32): 160 us, 5.39 TB/s,
+//     0.79 of the measured copy rate; a first, CUDA-core kernel 14,124 us
+//   serving batch (256 x 64 - 8k, 32 / 8 heads, d 128, blocks of 16): 109 us, 4.62 TB/s, 0.68
+//   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 31.8 us, 1.91 TB/s, 0.28: the units are
+//     short, and one costs 0.8 of a tile besides its tiles
+//   one context of 600 tokens: 8.3 us, latency
+// Tried and not kept: four warps loading their own tokens by 16-byte asynchronous copies, without
+// a producer (237 us on long documents); operands of q in registers (187 against 175 us); a fifth
+// CTA a SM at 72 registers (200 against 175 us); one piece of 16 tokens a warp at a time (174
+// against 163 us); halves of the loops rolled up (168 - 172 against 160 us).
 #pragma once
 
 #include "decode_fp4.cuh"
@@ -132,9 +149,7 @@ struct Cfg {
     static constexpr size_t OFF_PLAN = OFF_QF + NP * NT * NCHUNK * 32 * 16;  // 32 tiles: int4, int2, rows
     static constexpr size_t OFF_X = OFF_PLAN + 32 * (16 + 8 + 16 * 4);
     static constexpr size_t SMEM = OFF_X + XBUF * 4 + 128;             // the base is rounded up
-    // resident CTAs, by registers.  The queries' operands stay in shared memory (a 16-byte load a
-    // chunk): 187 -> 175 us on long documents against registers.  A fifth CTA (72 registers) spills
-    // and loses: 200 us.
+    // resident CTAs, by registers
     static constexpr int CTAS = HD == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);
     // pieces of 16 tokens a warp works on at once, by registers
     static constexpr int PIECES = NT == 1 ? 2 : 1;

@@ -3,14 +3,18 @@
 //
 // For a head row x: y = x / sqrt(mean(x^2) + eps) * w, then every pair (y_i, y_j) of the first
 // rot_dim dims is rotated by its angle.  One read and one write of every row: bound by HBM at
-// prompt sizes, by the launch at a decode step's.
+// prompt sizes, by the launch at a decode step's.  Measured with the cache write, bf16, 32 / 8 heads,
+// d 128: 16,384 tokens 68 us (6.0 TB/s, 0.89 of the measured copy rate), 64 tokens 2.9 us; alone, f16,
+// 40 / 40 heads, d 64, 3,001 tokens 12.8 us (0.71).
 //
 // A lane holds eight dims of a row (d / 8 lanes a row) as two runs of four: the halves of four
 // pairs, so that the rotation stays in the lane (half-split: dims 4j .. and rot_dim / 2 + 4j ..;
 // adjacent pairs and dims beyond rot_dim: eight in a row).  The sum of squares is a shuffle
 // reduction over the row's lanes.  A warp takes kNormRows rows a lane group of one kind (query,
 // key or value heads) of one token: weight times cosine and sine are formed once for them all,
-// and their loads are in flight together.  Everything is fp32 until the one rounding at the end;
+// and their loads are in flight together.  The grid is what the device holds at once, and a warp
+// walks the tokens with the next one's rows loading (a CTA a token took 101 us on the prompts).
+// Everything is fp32 until the one rounding at the end;
 // with the cache write the keys are rounded to their own type first, so that the cache holds the
 // same bits as after the two separate calls.
 #include "norm_rope.cuh"
