@@ -66,7 +66,7 @@ struct Plan {
 
 struct Fp4Plan {
     int group, nsub, unit_heads, workers;
-    size_t off_ml, total;
+    size_t off_ml, off_cuts, total;
 };
 
 // Chunk length: at least 512 tokens, a multiple of 64 (every stage size and
@@ -129,7 +129,8 @@ pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4
     pl->workers = (int)fp4_max_workers(S, Hkv, pl->nsub, pl->unit_heads, max_ctx);
     const size_t states = (size_t)pl->workers * 2 * pl->unit_heads;
     pl->off_ml = round_up(states * HD * 4, 256);
-    pl->total = round_up(pl->off_ml + states * 8, 256);
+    pl->off_cuts = round_up(pl->off_ml + states * 8, 256);
+    pl->total = round_up(pl->off_cuts + (size_t)pl->workers * 16, 256);
     return PKV_OK;
 }
 
@@ -218,6 +219,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
         f.max_workers = fplan.workers;
         f.part_acc = reinterpret_cast<float*>(ws);
         f.part_ml = reinterpret_cast<float*>(ws + fplan.off_ml);
+        f.cuts = reinterpret_cast<int4*>(ws + fplan.off_cuts);
         f.head_dim = head_dim;
         f.block_size = block_size;
         f.log_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;

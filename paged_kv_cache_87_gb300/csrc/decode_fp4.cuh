@@ -30,6 +30,8 @@ struct DecodeFp4Params {
     unsigned* status;
     float* part_acc;       // [workers * 2][unit_heads][head_dim]
     float* part_ml;        // [workers * 2][unit_heads][2]: running max (log2 domain) and sum
+    int4* cuts;            // [workers]: {1, sequence, unit, its last worker} of a unit it began and
+                           // left unfinished, or {0}
     int num_seqs, num_q_heads, num_kv_heads, group, nsub, unit_heads;
     int head_dim, block_size, num_blocks, max_blocks, max_context_len;
     int log_block;         // block_size == 1 << log_block

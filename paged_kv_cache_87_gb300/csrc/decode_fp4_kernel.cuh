@@ -34,12 +34,13 @@
 // joins those of each cut unit in order.
 //
 // What bounds it.  The consumers' issue slots, not HBM: 292 instructions for 16 tokens of K and V at
-// head_dim 128 (128 of them the converts and multiplies), issued at 2.35 a clock an SM.  Without the
+// head_dim 128 (128 of them the converts and multiplies), issued at 2.35 a clock an SM; and 3 - 4 us
+// that the joining of the cut units takes after the last of them.  Without the
 // arithmetic the same kernel streams at 0.97 of the copy rate.  Measured (device time, GB300):
-//   long documents (8 x 32k - 131k tokens, 64 / 8 heads, d 128, blocks of 32): 160 us, 5.39 TB/s,
-//     0.79 of the measured copy rate; a first, CUDA-core kernel 14,124 us
-//   serving batch (256 x 64 - 8k, 32 / 8 heads, d 128, blocks of 16): 109 us, 4.62 TB/s, 0.68
-//   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 31.8 us, 1.91 TB/s, 0.28: the units are
+//   long documents (8 x 32k - 131k tokens, 64 / 8 heads, d 128, blocks of 32): 158 us, 5.46 TB/s,
+//     0.81 of the measured copy rate; a first, CUDA-core kernel 14,124 us
+//   serving batch (256 x 64 - 8k, 32 / 8 heads, d 128, blocks of 16): 107 us, 4.71 TB/s, 0.69
+//   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 28.0 us, 2.17 TB/s, 0.32: the units are
 //     short, and one costs 0.8 of a tile besides its tiles
 //   one context of 600 tokens: 8.3 us, latency
 // Tried and not kept: four warps loading their own tokens by 16-byte asynchronous copies, without
@@ -127,7 +128,6 @@ constexpr float kSlack = 8.f;    // log2 headroom before the running maximum mov
 constexpr float kLift = 7.f;     // weights are 2^(x - m + kLift): at most 2^15 in fp16
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kMergeThreads = 512;
 
 // NT: groups of eight query heads that a unit serves (each widened row of K and V serves them all)
 template <typename QT, int HD, int NT>
@@ -283,15 +283,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         // a pool row is a whole tile of 8 or 16 tokens, or half of a tile of 32
         const int log_rt = min(logB, 4), per_block = logB - log_rt, log_rows = 7 - log_rt;
         const int cap = min(p.max_context_len, p.max_blocks * B);
+        if (lane == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        __syncwarp();
         for (int pos0 = a; pos0 < end; pos0 += 32) {
             const int pos = pos0 + lane;
             int4 m = make_int4(0, 0, 0, 0);
+            int uend_of = 0;
             if (pos < end) {
                 int s, n, base;
                 locate<kThreads>(p, s_pref, upi, pos, &s, &n, &base);
                 const int u = (pos - base) / n, at = (pos - base) % n, tile = at - kFp4UnitCost;
                 if (tile >= 0) {
                     const int dstart = pos - tile, uend = pos - at + n;
+                    uend_of = uend;
                     const int tokens = min(kFp4Tile, min(p.context_lens[s], cap) - tile * kFp4Tile);
                     m = make_int4((tile == 0 || pos == a ? kFirst : 0) |
                                       (at == n - 1 || pos == end - 1 ? kLast : 0) | tokens << 8,
@@ -300,6 +304,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 }
             }
             plan[lane] = m;
+            if (pos == end - 1 && m.x != 0 && m.w == 1)   // begun here, goes on in the next worker
+                p.cuts[blockIdx.x] = make_int4(1, m.y, m.z, (uend_of - 1) / q);
             const unsigned have = __ballot_sync(0xffffffffu, m.x != 0);   // and the plan is visible
             // the tiles' pool rows, 8 or 16 each (beyond the context's last block: that one's again)
 #pragma unroll 4
@@ -740,90 +746,86 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     }
 }
 
-// CTA b looks at the boundary between workers b and b + 1: if it cuts a unit's tiles and is the
-// first to do so, the CTA joins the unit's partial states and writes its heads.  Sixteen warps
-// share the heads: warp w takes head w % nh's pieces w / nh, w / nh + 16 / nh, ..., four pieces'
-// loads in flight at once; the order of the sums is fixed.
-template <typename QT, int HD, int NT>
-__global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(DecodeFp4Params p) {
-    constexpr int WARPS = kMergeThreads / 32, V = HD / 32, FLY = 4;   // dims of a lane
+// CTA b joins the partial states of the unit that worker b began and left unfinished, if it did
+// (its record in `cuts`): those of workers b, b + 1, .., in that order, and writes the unit's heads.
+// The warps share the heads: warp w takes head w % nh's pieces w / nh, w / nh + warps / nh, ..., four
+// pieces' loads in flight at once (heads beyond the warps come after).  A plan of its own in
+// every CTA instead of the record cost 4 us a call.
+template <typename QT, int HD, int NT, int THREADS>
+__global__ void __launch_bounds__(THREADS) merge_fp4_kernel(DecodeFp4Params p) {
+    constexpr int WARPS = THREADS / 32, V = HD / 32, FLY = 4;   // dims of a lane
     constexpr int HEADS = 8 * NT;
-    __shared__ int s_pref[kMergeThreads + 2];
-    __shared__ int2 s_wsum[WARPS];
     __shared__ float s_acc[WARPS][HD], s_m[WARPS], s_l[WARPS];
     pdl_launch_dependents();   // the kernel after waits for this one, and this one for the decode
-    scan_slots<kMergeThreads>(p, s_pref, s_wsum);
-    const int upi = p.num_kv_heads * p.nsub;
-    const int total = s_pref[kMergeThreads] * upi;
-    const int q = quota_of(p, total, s_pref[kMergeThreads + 1]);
-    const int pos = (blockIdx.x + 1) * q;
-    int s = 0, n = 1, base = 0;
-    if (pos < total) locate<kMergeThreads>(p, s_pref, upi, pos, &s, &n, &base);
-    pdl_wait();                // the partial states are written; also in CTAs without a unit:
-                               // this grid must not end before the decode has
-    const int u = (pos - base) / n, dstart = base + u * n + kFp4UnitCost, uend = base + (u + 1) * n;
-    const int w0 = dstart / q, w1 = (uend - 1) / q;             // workers of the unit's tiles
-    if (pos >= total || pos <= dstart || w0 != blockIdx.x) return;
+    pdl_wait();
+    const int4 cut = __ldcg(p.cuts + blockIdx.x);
+    if (cut.x == 0) return;
+    const int s = cut.y, u = cut.z, w0 = blockIdx.x, w1 = cut.w;
     const int kvh = u / p.nsub, qsub = u % p.nsub;
-    const int nh = min(HEADS, p.group - qsub * HEADS);
+    const int heads = min(HEADS, p.group - qsub * HEADS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = warp % nh, step = WARPS / nh;
-    float M = -INFINITY, L = 0.f, A[V];
+    for (int h0 = 0; h0 < heads; h0 += WARPS) {
+        const int nh = min(WARPS, heads - h0);
+        const int h = h0 + warp % nh, step = WARPS / nh;
+        float M = -INFINITY, L = 0.f, A[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 0.f;
-    if (warp / nh < step)
-        for (int w = w0 + warp / nh; w <= w1; w += FLY * step) {
-            float m[FLY], l[FLY], a[FLY][V], Mn = M;
+        for (int i = 0; i < V; ++i) A[i] = 0.f;
+        if (warp / nh < step)
+            for (int w = w0 + warp / nh; w <= w1; w += FLY * step) {
+                float m[FLY], l[FLY], a[FLY][V], Mn = M;
 #pragma unroll
-            for (int k = 0; k < FLY; ++k) {
-                // a worker's state 0 is the unit it starts inside of, 1 the one it ends inside of
-                const int wk = w + k * step;
-                const int64_t pi = ((int64_t)wk * 2 + (wk == w0 ? 1 : 0)) * HEADS + h;
-                m[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi) : -INFINITY;
-                l[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi + 1) : 0.f;
+                for (int k = 0; k < FLY; ++k) {
+                    // a worker's state 0 is the unit it starts inside of, 1 the one it ends inside of
+                    const int wk = w + k * step;
+                    const int64_t pi = ((int64_t)wk * 2 + (wk == w0 ? 1 : 0)) * HEADS + h;
+                    m[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi) : -INFINITY;
+                    l[k] = wk <= w1 ? __ldcg(p.part_ml + 2 * pi + 1) : 0.f;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    a[k][i] = wk <= w1 ? __ldcg(p.part_acc + pi * HD + lane + 32 * i) : 0.f;
+                    for (int i = 0; i < V; ++i)
+                        a[k][i] = wk <= w1 ? __ldcg(p.part_acc + pi * HD + lane + 32 * i) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < FLY; ++k) Mn = fmaxf(Mn, m[k]);
+                const float fo = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+                L *= fo;
+#pragma unroll
+                for (int i = 0; i < V; ++i) A[i] *= fo;
+#pragma unroll
+                for (int k = 0; k < FLY; ++k) {
+                    const float f = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - Mn);
+                    L = fmaf(l[k], f, L);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) A[i] = fmaf(a[k][i], f, A[i]);
+                }
+                M = Mn;
             }
 #pragma unroll
-            for (int k = 0; k < FLY; ++k) Mn = fmaxf(Mn, m[k]);
-            const float fo = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-            L *= fo;
-#pragma unroll
-            for (int i = 0; i < V; ++i) A[i] *= fo;
-#pragma unroll
-            for (int k = 0; k < FLY; ++k) {
-                const float f = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - Mn);
-                L = fmaf(l[k], f, L);
-#pragma unroll
-                for (int i = 0; i < V; ++i) A[i] = fmaf(a[k][i], f, A[i]);
-            }
-            M = Mn;
+        for (int i = 0; i < V; ++i) s_acc[warp][lane + 32 * i] = A[i];
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = L;
         }
+        __syncthreads();
+        if (warp < nh) {
+            M = -INFINITY;
+            for (int k = 0; k < step; ++k) M = fmaxf(M, s_m[warp + k * nh]);
+            L = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_acc[warp][lane + 32 * i] = A[i];
-    if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = L;
+            for (int i = 0; i < V; ++i) A[i] = 0.f;
+            for (int k = 0; k < step; ++k) {
+                const int w = warp + k * nh;
+                const float f = s_m[w] == -INFINITY ? 0.f : fast_exp2(s_m[w] - M);
+                L = fmaf(s_l[w], f, L);
+#pragma unroll
+                for (int i = 0; i < V; ++i) A[i] = fmaf(s_acc[w][lane + 32 * i], f, A[i]);
+            }
+            const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + qsub * HEADS + h;
+            const float inv = p.out_scale / L;
+#pragma unroll
+            for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, row * HD + lane + 32 * i, A[i] * inv);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (warp >= nh) return;
-    M = -INFINITY;
-    for (int k = 0; k < step; ++k) M = fmaxf(M, s_m[h + k * nh]);
-    L = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 0.f;
-    for (int k = 0; k < step; ++k) {
-        const int w = h + k * nh;
-        const float f = s_m[w] == -INFINITY ? 0.f : fast_exp2(s_m[w] - M);
-        L = fmaf(s_l[w], f, L);
-#pragma unroll
-        for (int i = 0; i < V; ++i) A[i] = fmaf(s_acc[w][lane + 32 * i], f, A[i]);
-    }
-    const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + qsub * HEADS + h;
-    const float inv = p.out_scale / L;
-#pragma unroll
-    for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, row * HD + lane + 32 * i, A[i] * inv);
 }
 
 template <typename QT, int HD, int NT>
@@ -872,9 +874,16 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     err = cudaLaunchKernelEx(&cfg, kernel, p, map_k, map_v);
     if (err != cudaSuccess || grid == 1) return err;      // one worker cuts nothing
     cfg.gridDim = dim3((unsigned)(grid - 1), 1, 1);
-    cfg.blockDim = dim3(kMergeThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT>, p);
+    // eight warps join a unit's few states; where few units share the chip, and each leaves eight
+    // states or more, sixteen do (one context of 100,000 tokens and one kv head: 22 us against 31;
+    // a serving batch: 107.5 us with sixteen, 106.9 with eight)
+    if ((int64_t)p.num_seqs * p.num_kv_heads * p.nsub * 8 <= grid) {
+        cfg.blockDim = dim3(512, 1, 1);
+        return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT, 512>, p);
+    }
+    cfg.blockDim = dim3(256, 1, 1);
+    return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT, 256>, p);
 }
 
 template <typename QT>
