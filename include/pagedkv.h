@@ -10,7 +10,11 @@
  *   - pkv_reshape_and_cache: §7 kernel 1 (write each new token's key and
  *     value straight into its physical block slot);
  *   - pkv_copy_blocks: §5 Parallel Sampling step 4 and §7 kernel 3 (all
- *     copy-on-write block copies of a step in one launch).
+ *     copy-on-write block copies of a step in one launch);
+ * and beside them what a serving step needs around the cache: several queries
+ * a sequence, the norm and rotary embedding of queries and keys with their
+ * write, reading the cache back, moving blocks to host memory and a 4-bit
+ * cache type.
  *
  * Conventions shared by every call
  *   Memory:  every pointer argument except `host_code` is a DEVICE pointer
@@ -86,7 +90,8 @@ typedef enum pkv_status {
 } pkv_status;
 
 /* Bits of the device status word (see pkv_get_device_status). */
-#define PKV_DEV_BAD_BLOCK_ID   0x1u  /* table entry outside [0, num_blocks): block skipped */
+#define PKV_DEV_BAD_BLOCK_ID   0x1u  /* table entry outside [0, num_blocks): not followed (attention
+                                        reads block 0 instead: such a sequence's rows are of no use) */
 #define PKV_DEV_BAD_CONTEXT    0x2u  /* context_len < 0 or above max_context_len or
                                         max_blocks_per_seq * block_size: clamped */
 #define PKV_DEV_BAD_SLOT       0x4u  /* slot >= num_blocks * block_size: token skipped */
@@ -108,8 +113,9 @@ typedef struct CUstream_st* pkv_stream_t;
  * Bytes of device workspace pkv_paged_decode_attention needs for these sizes.
  * The workspace holds the per-call work list, one arrival counter per
  * (sequence, kv head group) and the split-KV partial states (m, l, acc[d]) of
- * every chunk of every (sequence, query head).  It need not be zeroed.
- * Returns 0 for unsupported or invalid sizes.
+ * every chunk of every (sequence, query head); for a 4-bit cache two partial
+ * states and a record of every CTA, 9 MB at most whatever the lengths.  It need
+ * not be zeroed.  Returns 0 for unsupported or invalid sizes.
  */
 PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                   int head_dim, int block_size, int max_context_len,
@@ -152,8 +158,12 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num
  *                 on one stream
  *   out           [num_seqs][num_q_heads][head_dim], q_dtype, 16-byte aligned
  * Supported: head_dim in {64, 128}; block_size in {8, 16, 32}; any
- * num_q_heads that is a multiple of num_kv_heads.
- * Two launches on `stream`: a one-CTA planning kernel and the decode kernel.
+ * num_q_heads that is a multiple of num_kv_heads.  A 4-bit cache with 2^30 or
+ * more (block, kv head) tiles, or work of 2^31 or more (sequence, kv head,
+ * 128-token) pieces by max_context_len, returns PKV_ERR_UNSUPPORTED.
+ * Two launches on `stream`: a one-CTA planning kernel and the decode kernel;
+ * over a 4-bit cache the decode kernel, which plans by itself, and one that
+ * joins the contexts it has split.
  */
 PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_cache, const void* v_cache,
                                       const int32_t* block_tables, const int32_t* context_lens,

@@ -33,7 +33,8 @@ struct DecodeFp4Params {
     int4* cuts;            // [workers]: {1, sequence, unit, its last worker} of a unit it began and
                            // left unfinished, or {0}
     int num_seqs, num_q_heads, num_kv_heads, group, nsub, unit_heads;
-    int head_dim, block_size, num_blocks, max_blocks, max_context_len;
+    int head_dim, block_size, num_blocks, max_blocks;
+    int max_context_len;   // at most max_blocks * block_size
     int log_block;         // block_size == 1 << log_block
     int workers;           // the split's denominator: every CTA the device holds
     int max_workers;       // workers that can have work, by max_context_len

@@ -159,9 +159,8 @@ constexpr int kFirst = 1, kLast = 2, kDone = 4;
 
 // Tiles of a sequence's context, per unit.
 __device__ __forceinline__ int tiles_of(const DecodeFp4Params& p, int s) {
-    const int cap = min(p.max_context_len, p.max_blocks * p.block_size);
     const int c = p.context_lens[s];
-    return c <= 0 ? 0 : (min(c, cap) + kFp4Tile - 1) / kFp4Tile;
+    return c <= 0 ? 0 : (min(c, p.max_context_len) + kFp4Tile - 1) / kFp4Tile;
 }
 
 // A unit's length in the plan, in slots: its tiles and, before them, kFp4UnitCost slots that
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         int* plan_row = reinterpret_cast<int*>(plan_at + 32);          // [32][16] pool rows
         // a pool row is a whole tile of 8 or 16 tokens, or half of a tile of 32
         const int log_rt = min(logB, 4), per_block = logB - log_rt, log_rows = 7 - log_rt;
-        const int cap = min(p.max_context_len, p.max_blocks * B);
+        const int cap = p.max_context_len;
         if (lane == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
         __syncwarp();
         for (int pos0 = a; pos0 < end; pos0 += 32) {
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 const int2 w = plan_at[l];
                 const int blocks = ((t.x >> 8) + B - 1) >> logB, k = min(r, (blocks << per_block) - 1);
                 int blk = p.block_tables[(int64_t)t.y * p.max_blocks + ((w.x * kFp4Tile) >> logB) + (k >> per_block)];
-                if (blk < 0 || blk >= p.num_blocks) {
+                if (blk < 0 || blk >= p.num_blocks) {   // block 0 in its place, as every decode here
                     set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
                     blk = 0;
                 }
@@ -372,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     // ========================= consumer warps =========================
     // sequences without context: zero rows (and lengths outside the bounds are flagged once)
     {
-        const int cap = min(p.max_context_len, p.max_blocks * B), row = p.num_q_heads * HD;
+        const int cap = p.max_context_len;
+        const int64_t row = (int64_t)p.num_q_heads * HD;
         for (int s = blockIdx.x * kConsumers + warp; s < p.num_seqs; s += gridDim.x * kConsumers) {
             const int c = p.context_lens[s];
             if (lane == 0 && (c < 0 || c > cap)) set_status(p.status, PKV_DEV_BAD_CONTEXT);
             if (c <= 0 || cap == 0)
-                for (int i = lane; i < row; i += 32)
-                    store_from_float<QT>(p.out, (int64_t)s * row + i, 0.f);
+                for (int64_t i = lane; i < row; i += 32) store_from_float<QT>(p.out, s * row + i, 0.f);
         }
     }
     constexpr int SUB_BYTES = 64 * C::ROWB;       // from a warp's first piece of a tile to its second

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_cache_kernel(GatherPara
 
 template <typename KT, typename OT>
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
-    const int grid = (p.total_rows + kGatherRows - 1) / kGatherRows;
+    const int64_t grid = ((int64_t)p.total_rows + kGatherRows - 1) / kGatherRows;
     return launch_overlapped(p.head_dim == 128 ? gather_cache_kernel<KT, OT, 128>
                                                : gather_cache_kernel<KT, OT, 64>,
                              (unsigned)grid, kGatherThreads, stream, p);

@@ -8,7 +8,9 @@
 // Arguments are positional (binding.py has the signatures and their documentation).  A wrong
 // tensor raises ValueError, an element type that the library does not know KeyError, and a
 // pkv_status that is not PKV_OK the class that set_error() was given, with (function, status).
-// No C++ exception leaves: torch's become their Python classes.
+// No C++ exception leaves: torch's become their Python classes.  The interpreter's lock is let go
+// while memory is taken and while the library is called: a full launch queue waits for the device,
+// and what the device waits for may be a callback that needs the lock.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -58,14 +60,20 @@ double number(PyObject* o) {
     return v;
 }
 
-long long integer(PyObject* o) {
-    const long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) throw Refused{};
-    return v;
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v != 0;
 }
 
+// int(o), within 32 bits
 int int32(PyObject* o, const char* text) {
-    const long long v = integer(o);
+    PyObject* i = PyNumber_Long(o);
+    if (!i) throw Refused{};
+    int over = 0;
+    long long v = PyLong_AsLongLongAndOverflow(i, &over);
+    Py_DECREF(i);
+    if (over) v = INT64_MAX;
     need(v >= INT32_MIN && v <= INT32_MAX, text);
     return (int)v;
 }
@@ -126,6 +134,32 @@ pkv_stream_t stream_of(PyObject* o) {
     return reinterpret_cast<pkv_stream_t>(v);
 }
 
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// Calls f without the interpreter's lock; its status is checked with it.
+template <typename F>
+void call(const char* fn, F f) {
+    pkv_status st;
+    {
+        Unlocked u;
+        st = f();
+    }
+    check(fn, st);
+}
+
+// A new tensor for a call on `stream`: its memory, taken on the current stream, is not used
+// again before `stream` has done what it holds when the tensor is dropped.
+at::Tensor fresh(at::IntArrayRef shape, const at::TensorOptions& options, pkv_stream_t stream) {
+    Unlocked u;
+    at::Tensor t = at::empty(shape, options);
+    if (stream != c10::cuda::getCurrentCUDAStream().stream() && t.numel() != 0)
+        t.record_stream(c10::cuda::getStreamFromExternal(stream, t.get_device()).unwrap());
+    return t;
+}
+
 void count(Py_ssize_t got, Py_ssize_t want) {
     if (got != want) refuse(PyExc_TypeError, "wrong number of arguments");
 }
@@ -169,42 +203,45 @@ PKV_ENTRY(decode) {
     need(bt.scalar_type() == at::kInt && cl.scalar_type() == at::kInt,
          "block_tables and context_lens must be int32");
     for (int i = 0; i < 5; ++i) contiguous(a[i], plain);
-    const int S = size32(q.size(0)), Hq = size32(q.size(1));
+    const int S = size32(q.size(0)), Hq = size32(q.size(1)), width = size32(bt.size(1));
     need(bt.size(0) >= S && cl.numel() >= S, "block_tables and context_lens must have a row a query");
     const int max_ctx = int32(a[5], "max_context_len does not fit in 32 bits");
     const float scale = (float)number(a[6]), kv_scale = (float)number(a[7]);
+    const pkv_stream_t stream = stream_of(a[10]);
     at::Tensor ws, out;
     if (a[8] == Py_None) {
         const size_t bytes = pkv_decode_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, c.type);
-        ws = at::empty({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte));
+        ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
     } else {
         ws = contiguous(a[8], "workspace must be a contiguous CUDA tensor");
     }
     if (a[9] == Py_None) {
-        out = at::empty(q.sizes(), q.options());
+        out = fresh(q.sizes(), q.options(), stream);
     } else {
         out = contiguous(a[9], "out must be a contiguous CUDA tensor");
-        need(out.numel() == q.numel() && out.scalar_type() == q.scalar_type(),
+        need(out.numel() >= q.numel() && out.scalar_type() == q.scalar_type(),
              "out must have query's size and type");
     }
-    const bool prefix = PyObject_IsTrue(a[11]);
+    const bool prefix = truth(a[11]);
     const pkv_dtype qt = code_of(q.scalar_type());
     const size_t ws_bytes = (size_t)ws.numel() * ws.element_size();
-    if (PyObject_IsTrue(a[12]))
+    if (truth(a[12]))
         return Py_BuildValue(
             "((KKKKKiiiiiiiidiidKnKK)NN)", (unsigned long long)q.data_ptr(),
             (unsigned long long)k.data_ptr(), (unsigned long long)v.data_ptr(),
             (unsigned long long)bt.data_ptr(), (unsigned long long)cl.data_ptr(), S, Hq, c.heads,
-            c.d, c.block, c.blocks, (int)bt.size(1), max_ctx, (double)scale, (int)qt, (int)c.type,
+            c.d, c.block, c.blocks, width, max_ctx, (double)scale, (int)qt, (int)c.type,
             (double)kv_scale, (unsigned long long)ws.data_ptr(), (Py_ssize_t)ws_bytes,
-            (unsigned long long)out.data_ptr(), (unsigned long long)stream_of(a[10]),
+            (unsigned long long)out.data_ptr(), (unsigned long long)stream,
             THPVariable_Wrap(ws), THPVariable_Wrap(out));
     auto* fn = prefix ? pkv_paged_decode_attention_prefix : pkv_paged_decode_attention;
-    check(prefix ? "pkv_paged_decode_attention_prefix" : "pkv_paged_decode_attention",
-          fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const int32_t*>(bt.data_ptr()),
-             static_cast<const int32_t*>(cl.data_ptr()), S, Hq, c.heads, c.d, c.block, c.blocks,
-             size32(bt.size(1)), max_ctx, scale, qt, c.type, kv_scale, ws.data_ptr(), ws_bytes,
-             out.data_ptr(), stream_of(a[10])));
+    call(prefix ? "pkv_paged_decode_attention_prefix" : "pkv_paged_decode_attention", [&] {
+        return fn(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                  static_cast<const int32_t*>(bt.data_ptr()),
+                  static_cast<const int32_t*>(cl.data_ptr()), S, Hq, c.heads, c.d, c.block,
+                  c.blocks, width, max_ctx, scale, qt, c.type, kv_scale, ws.data_ptr(), ws_bytes,
+                  out.data_ptr(), stream);
+    });
     return THPVariable_Wrap(std::move(out));
 }
 
@@ -231,16 +268,18 @@ PKV_ENTRY(write) {
     const int T = size32(key.size(0));
     const float kv_scale = (float)number(a[5]);
     const pkv_dtype st = code_of(key.scalar_type());
-    if (PyObject_IsTrue(a[7]))
+    const pkv_stream_t stream = stream_of(a[6]);
+    if (truth(a[7]))
         return Py_BuildValue("(KKKKKiiiiiiidK)", (unsigned long long)key.data_ptr(),
                              (unsigned long long)value.data_ptr(), (unsigned long long)k.data_ptr(),
                              (unsigned long long)v.data_ptr(), (unsigned long long)slots.data_ptr(),
                              T, c.heads, c.d, c.block, c.blocks, (int)st, (int)c.type,
-                             (double)kv_scale, (unsigned long long)stream_of(a[6]));
-    check("pkv_reshape_and_cache",
-          pkv_reshape_and_cache(key.data_ptr(), value.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                static_cast<const int64_t*>(slots.data_ptr()), T, c.heads, c.d,
-                                c.block, c.blocks, st, c.type, kv_scale, stream_of(a[6])));
+                             (double)kv_scale, (unsigned long long)stream);
+    call("pkv_reshape_and_cache", [&] {
+        return pkv_reshape_and_cache(key.data_ptr(), value.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                     static_cast<const int64_t*>(slots.data_ptr()), T, c.heads, c.d,
+                                     c.block, c.blocks, st, c.type, kv_scale, stream);
+    });
     Py_RETURN_NONE;
 }
 
@@ -268,23 +307,28 @@ PKV_ENTRY(gather) {
     need(rows >= 0, "total_rows must not be negative");
     need(THPDtype_Check(a[5]), "out_dtype must be a torch.dtype");
     const at::ScalarType type = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
+    const pkv_dtype out_type = code_of(type);
     const int64_t shape[3] = {rows, c.heads, c.d};
+    const int S = size32(bt.size(0)), width = size32(bt.size(1));
+    const float kv_scale = (float)number(a[6]);
+    const pkv_stream_t stream = stream_of(a[10]);
     at::Tensor out[2];
     for (int i = 0; i < 2; ++i) {
         if (a[8 + i] == Py_None) {
-            out[i] = at::empty(shape, k.options().dtype(type));
+            out[i] = fresh(shape, k.options().dtype(type), stream);
         } else {
             out[i] = contiguous(a[8 + i], "key_out and value_out must be contiguous CUDA tensors");
             need(out[i].sizes() == at::IntArrayRef(shape, 3) && out[i].scalar_type() == type,
                  "key_out and value_out must be [total_rows, Hkv, d] of out_dtype");
         }
     }
-    check("pkv_gather_cache",
-          pkv_gather_cache(k.data_ptr(), v.data_ptr(), static_cast<const int32_t*>(bt.data_ptr()),
-                           static_cast<const int32_t*>(rs.data_ptr()), first, size32(bt.size(0)),
-                           rows, c.heads, c.d, c.block, c.blocks, size32(bt.size(1)), c.type,
-                           (float)number(a[6]), code_of(type), out[0].data_ptr(),
-                           out[1].data_ptr(), stream_of(a[10])));
+    call("pkv_gather_cache", [&] {
+        return pkv_gather_cache(k.data_ptr(), v.data_ptr(),
+                                static_cast<const int32_t*>(bt.data_ptr()),
+                                static_cast<const int32_t*>(rs.data_ptr()), first, S, rows, c.heads,
+                                c.d, c.block, c.blocks, width, c.type, kv_scale, out_type,
+                                out[0].data_ptr(), out[1].data_ptr(), stream);
+    });
     return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(out[0])), THPVariable_Wrap(std::move(out[1])));
 }
 
@@ -294,12 +338,14 @@ struct NormRope {
     at::Tensor q_out;
     const void *qw = nullptr, *kw = nullptr;
     pkv_dtype type, weight_type = PKV_F32;
-    int T, Hq, Hkv, d;
+    int T, Hq, Hkv, d, positions_known, rot_dim;
     int64_t q_stride, k_stride, out_stride;
     float eps;
+    bool interleaved;
+    pkv_stream_t stream;
 
     NormRope(PyObject* query, PyObject* key, PyObject* cos_sin, PyObject* positions, PyObject* q_w,
-             PyObject* k_w, PyObject* eps_, PyObject* out) {
+             PyObject* k_w, PyObject* eps_, PyObject* interleaved_, PyObject* out, PyObject* stream_) {
         q = &tensor(query);
         k = &tensor(key);
         need(q->dim() == 3 && k->dim() == 3 && q->size(0) == k->size(0) &&
@@ -313,6 +359,8 @@ struct NormRope {
         cs = &contiguous(cos_sin, "cos_sin must be a contiguous CUDA tensor");
         need(cs->dim() == 2 && cs->scalar_type() == at::kFloat,
              "cos_sin must be float32 [max_position, rot_dim]");
+        positions_known = size32(cs->size(0));
+        rot_dim = size32(cs->size(1));
         pos = &contiguous(positions, "positions must be a contiguous CUDA tensor");
         need(pos->dim() == 1 && pos->size(0) == T && pos->scalar_type() == at::kLong,
              "positions must be int64 [T]");
@@ -330,12 +378,14 @@ struct NormRope {
         q_stride = head_rows(*q, Hq, d);
         k_stride = head_rows(*k, Hkv, d);
         eps = (float)number(eps_);
+        interleaved = truth(interleaved_);
+        stream = stream_of(stream_);
         rows_out(out, *q, Hq, &q_out, &out_stride);
     }
 
     void rows_out(PyObject* given, const at::Tensor& like, int64_t heads, at::Tensor* to, int64_t* stride) {
         if (given == Py_None) {
-            *to = at::empty(like.sizes(), like.options());
+            *to = fresh(like.sizes(), like.options(), stream);
             *stride = heads * d;
         } else {
             *to = tensor(given);
@@ -350,17 +400,18 @@ struct NormRope {
 //           stream): (q_out, k_out)
 PKV_ENTRY(norm_rope) {
     count(n, 11);
-    NormRope r(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[8]);
+    NormRope r(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[10]);
     at::Tensor k_out;
     int64_t k_out_stride;
     r.rows_out(a[9], *r.k, r.Hkv, &k_out, &k_out_stride);
-    check("pkv_qk_norm_rope",
-          pkv_qk_norm_rope(r.q->data_ptr(), r.q_stride, r.k->data_ptr(), r.k_stride, r.qw, r.kw,
-                           r.weight_type, r.eps, static_cast<const float*>(r.cs->data_ptr()),
-                           size32(r.cs->size(0)), size32(r.cs->size(1)), PyObject_IsTrue(a[7]),
-                           static_cast<const int64_t*>(r.pos->data_ptr()), r.T, r.Hq, r.Hkv, r.d,
-                           r.type, r.q_out.data_ptr(), r.out_stride, k_out.data_ptr(),
-                           k_out_stride, stream_of(a[10])));
+    call("pkv_qk_norm_rope", [&] {
+        return pkv_qk_norm_rope(r.q->data_ptr(), r.q_stride, r.k->data_ptr(), r.k_stride, r.qw, r.kw,
+                                r.weight_type, r.eps, static_cast<const float*>(r.cs->data_ptr()),
+                                r.positions_known, r.rot_dim, r.interleaved,
+                                static_cast<const int64_t*>(r.pos->data_ptr()), r.T, r.Hq, r.Hkv,
+                                r.d, r.type, r.q_out.data_ptr(), r.out_stride, k_out.data_ptr(),
+                                k_out_stride, r.stream);
+    });
     return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(r.q_out)), THPVariable_Wrap(std::move(k_out)));
 }
 
@@ -380,17 +431,19 @@ PKV_ENTRY(norm_rope_write) {
          "slot_mapping must be int64 [T]");
     for (int i = 5; i < 8; ++i)
         contiguous(a[i], "caches and slot_mapping must be contiguous CUDA tensors");
-    NormRope r(a[0], a[1], a[3], a[4], a[8], a[9], a[10], a[13]);
-    check("pkv_qk_norm_rope_and_cache",
-          pkv_qk_norm_rope_and_cache(
-              r.q->data_ptr(), r.q_stride, r.k->data_ptr(), r.k_stride, value.data_ptr(),
-              head_rows(value, r.Hkv, r.d), r.qw, r.kw, r.weight_type, r.eps,
-              static_cast<const float*>(r.cs->data_ptr()), size32(r.cs->size(0)),
-              size32(r.cs->size(1)), PyObject_IsTrue(a[11]),
-              static_cast<const int64_t*>(r.pos->data_ptr()), r.T, r.Hq, r.Hkv, r.d, r.type,
-              r.q_out.data_ptr(), r.out_stride, k.data_ptr(), v.data_ptr(),
-              static_cast<const int64_t*>(slots.data_ptr()), c.block, c.blocks, c.type,
-              (float)number(a[12]), stream_of(a[14])));
+    NormRope r(a[0], a[1], a[3], a[4], a[8], a[9], a[10], a[11], a[13], a[14]);
+    const int64_t v_stride = head_rows(value, r.Hkv, r.d);
+    const float kv_scale = (float)number(a[12]);
+    call("pkv_qk_norm_rope_and_cache", [&] {
+        return pkv_qk_norm_rope_and_cache(
+            r.q->data_ptr(), r.q_stride, r.k->data_ptr(), r.k_stride, value.data_ptr(), v_stride,
+            r.qw, r.kw, r.weight_type, r.eps, static_cast<const float*>(r.cs->data_ptr()),
+            r.positions_known, r.rot_dim, r.interleaved,
+            static_cast<const int64_t*>(r.pos->data_ptr()), r.T, r.Hq, r.Hkv, r.d, r.type,
+            r.q_out.data_ptr(), r.out_stride, k.data_ptr(), v.data_ptr(),
+            static_cast<const int64_t*>(slots.data_ptr()), c.block, c.blocks, c.type, kv_scale,
+            r.stream);
+    });
     return THPVariable_Wrap(std::move(r.q_out));
 }
 

@@ -638,3 +638,46 @@ def test_chunked_prefill_over_a_4_bit_context():
         tol = decode_bound(f64(q[i]), k64[:, :m], v64[:, :m], d ** -0.5, "f16") + HALF["f16"] * np.abs(ref)
         assert (np.abs(f64(out[i]) - ref) <= tol).all()
     assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("kt", ["e2m1", "bf16"])
+def test_workspace_of_a_call_on_a_busy_stream_is_not_reused_before_it_ran(kt):
+    """A call allocates its workspace on the current stream and drops it; where it was asked to run
+    on another one, the memory stays taken until that stream is through."""
+    rng = np.random.default_rng(31)
+    args, out = check_decode(rng, [900, 2500], 8, 2, 128, 16, "bf16", 1.0)
+    if kt == "bf16":
+        pool = torch.randn(args[1].shape[0], 2, 16, 128, device="cuda").bfloat16()
+        args = (args[0], pool, pool, *args[3:])
+        out = binding.pkv_paged_decode_attention(*args)
+    need = binding.pkv_decode_workspace_bytes(2, 8, 2, 128, 16, 2500, kt)
+    got, side = torch.zeros_like(out), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def held():
+        s = torch.cuda.memory_stats()
+        return s["active_bytes.all.current"] - s["allocated_bytes.all.current"]
+
+    before = held()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)                  # some 20 ms
+    binding.pkv_paged_decode_attention(*args, out=got, stream=side)
+    assert held() - before >= need
+    trash = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and len(trash) == 8
+
+
+def test_decode_takes_a_larger_output_and_a_length_as_a_float():
+    rng = np.random.default_rng(32)
+    args, out = check_decode(rng, [70, 5], 4, 2, 64, 8, "f16", 1.0)
+    big = torch.full((3, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    binding.pkv_paged_decode_attention(*args[:5], float(args[5]), args[6], out=big)
+    assert torch.equal(big[:2], out) and (big[2] == 7).all()
+    with pytest.raises(ValueError):
+        binding.pkv_paged_decode_attention(*args, out=big[:1])
+    with pytest.raises(ValueError):
+        binding.pkv_paged_decode_attention(*args, out=big[:2].float())
+    with pytest.raises(ValueError):
+        binding.pkv_paged_decode_attention(*args[:5], 1 << 40, args[6])
+    assert binding.pkv_get_device_status() == 0
