@@ -40,7 +40,7 @@ struct DecodeFp4Params {
     int max_workers;       // workers that can have work, by max_context_len
     float qk_scale_log2;   // scale * log2(e) * kv_scale
     float out_scale;       // kv_scale
-    uint32_t two4, two12, two16;   // 2^4, 2^12, 2^16: shifts as products
+    uint32_t even, odd, minus;     // 2^4 + 2^16, 1 + 2^12, -1: shifts as products
 };
 
 // Workers that can have work over contexts up to max_ctx: bounds grid and workspace.

@@ -10,19 +10,20 @@
 // Queries of any type become fp16 exactly enough: each head's row is scaled by a power of two
 // that puts its largest magnitude in [2^14, 2^15) (undone in the logit scale), so a 16-bit row
 // keeps every bit down to 2^-39 of its largest value.  fp32 queries take two such terms (22
-// bits).  Weights enter the second product as fp16 in [0, 2^15] (the running maximum is moved
-// when a logit passes it by 2^8; weights are taken 2^7 above it, so that a weight 2^-32 of the
-// largest still counts), two terms of them for fp32; the denominator sums them in fp32 before
+// bits).  Weights enter the second product as fp16 in [0, 2^15] (they are taken 2^7 above the running
+// maximum, which is moved when the sum of a lane's two or four passes 2^15, so that a weight 2^-31 of
+// the largest still counts), two terms of them for fp32; the denominator sums them in fp32 before
 // that rounding.
 //
 // Layout.  32 dims of a row are 16 bytes, eight rows of them one 128-byte line: ldmatrix reads
 // them free of bank conflicts with no swizzle, and one gather moves 32 or 64 tokens of K or V, codes
 // and scales.  A lane's 4-byte word of K holds dims 8c .. 8c + 7 of row g: its four bytes
 // are four operand pairs, the reduction index being permuted for K and q alike.  A transposed
-// word of V holds dims 4g .. 4g + 3 of tokens 2c and 2c + 1: three products (as shifts) and two bit
-// selections pair the tokens' nibbles in bytes.  (Leaving the pairs of dims as they are and giving
-// each of the two a product with zeros in the weights saves those and costs eight more mma: 163 us
-// against 160 on long documents, 252 against 233 with sixteen heads.)
+// word of V holds dims 4g .. 4g + 3 of tokens 2c and 2c + 1: a mask and three products (as shifts)
+// pair the tokens' nibbles in bytes.  (Leaving the pairs of dims as they are and giving each of the
+// two a product with zeros in the weights saves those and costs eight more mma: 163 us against 160 on
+// long documents, 252 against 233 with sixteen heads; pairing after the conversion, by byte
+// permutations: 165 against 158.)
 //
 // Split.  Every (sequence, kv head, 8 or 16 query heads) unit is cut into 128-token tiles, and the
 // flattened tiles are dealt in equal runs to one CTA each ("worker"), all resident at once.
@@ -111,21 +112,15 @@ __device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// (a & mask) | (b & ~mask)
-__device__ __forceinline__ uint32_t bitselect(uint32_t a, uint32_t b, uint32_t mask) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(mask));
-    return r;
-}
-
 // What is left of (lo, hi) after pack_f16's rounding, as fp16 again.
 __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&packed));
     return pack_f16(lo - v.x, hi - v.y);
 }
 
-constexpr float kSlack = 8.f;    // log2 headroom before the running maximum moves
-constexpr float kLift = 7.f;     // weights are 2^(x - m + kLift): at most 2^15 in fp16
+constexpr float kLift = 7.f;     // weights are 2^(x - m + kLift)
+constexpr float kMost = 32768.f; // what a lane's weights of a head may sum to before its maximum moves
+constexpr float kSlack = 5.5f;   // then one of the four at least is past this (log2; 15 - 2 - kLift > 5.5)
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 
@@ -407,14 +402,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         constexpr int SUB = decltype(pieces)::value;
         const bool part = nv < 64 * SUB - 48;         // some of the tokens are not valid
         // ---- S^T = K Q^T ----
-        float sa[SUB][NT][2][4];
+        float sa[SUB][NT][4];
         uint32_t da[SUB], db[SUB];     // this lane's scale byte of every chunk, rows g and g + 8
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sa[u][nt][0][i] = sa[u][nt][1][i] = 0.f;
+                for (int i = 0; i < 4; ++i) sa[u][nt][i] = 0.f;
             const uint8_t* sc = sb + u * SUB_BYTES + ks_a;
             if constexpr (HD == 128) {
                 const uint2 ra = *reinterpret_cast<const uint2*>(sc);
@@ -455,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int t = 0; t < C::NP; ++t) {
-                            mma_f16(sa[u][nt][0], a00, a01, a02, a03, qf[nt][t][k].x, qf[nt][t][k].y);
-                            mma_f16(sa[u][nt][1], a10, a11, a12, a13, qf[nt][t][k].z, qf[nt][t][k].w);
+                            mma_f16(sa[u][nt], a00, a01, a02, a03, qf[nt][t][k].x, qf[nt][t][k].y);
+                            mma_f16(sa[u][nt], a10, a11, a12, a13, qf[nt][t][k].z, qf[nt][t][k].w);
                         }
                 }
             }
@@ -466,36 +461,35 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         uint32_t pb[SUB][NT][C::NP][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float z[SUB][4], y[SUB][4];
-            auto exponents = [&] {
+            float y[SUB][4], w[SUB][4], sum[2];
+            auto weights = [&] {
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[u][i] = fmaf(z[u][i], qs[nt][i & 1], lift[nt][i & 1]);
+                    for (int i = 0; i < 4; ++i) y[u][i] = fmaf(sa[u][nt][i], qs[nt][i & 1], lift[nt][i & 1]);
                 if (part)
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
+                sum[0] = sum[1] = 0.f;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[u][i] = fast_exp2(y[u][i]);
+                    sum[0] = u ? sum[0] + (w[u][0] + w[u][2]) : w[u][0] + w[u][2];
+                    sum[1] = u ? sum[1] + (w[u][1] + w[u][3]) : w[u][1] + w[u][3];
+                }
             };
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[u][i] = sa[u][nt][0][i] + sa[u][nt][1][i];
-            exponents();
-            float top = y[0][0];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, y[u][i]);
-            if (__any_sync(0xffffffffu, top > kSlack + kLift)) {
+            weights();
+            if (__any_sync(0xffffffffu, fmaxf(sum[0], sum[1]) > kMost)) {
                 float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (g + (i & 2) * 4 < nv - 64 * u) t[i & 1] = fmaxf(t[i & 1], z[u][i] * qs[nt][i & 1]);
+                        if (g + (i & 2) * 4 < nv - 64 * u) t[i & 1] = fmaxf(t[i & 1], sa[u][nt][i] * qs[nt][i & 1]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], off));
@@ -514,20 +508,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 for (int mt = 0; mt < 2 * C::NCHUNK; ++mt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[nt][mt][i] *= r[i & 1];
-                exponents();
+                weights();
             }
+            l[nt][0] += sum[0];
+            l[nt][1] += sum[1];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                const float p0 = fast_exp2(y[u][0]), p1 = fast_exp2(y[u][1]);
-                const float p2 = fast_exp2(y[u][2]), p3 = fast_exp2(y[u][3]);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                const uint32_t ua = pack_f16(p0, p1), ub = pack_f16(p2, p3);
+                const uint32_t ua = pack_f16(w[u][0], w[u][1]), ub = pack_f16(w[u][2], w[u][3]);
                 pb[u][nt][0][0] = trans8x8(ua);
                 pb[u][nt][0][1] = trans8x8(ub);
                 if constexpr (C::NP == 2) {
-                    pb[u][nt][1][0] = trans8x8(pack_f16_rest(p0, p1, ua));
-                    pb[u][nt][1][1] = trans8x8(pack_f16_rest(p2, p3, ub));
+                    pb[u][nt][1][0] = trans8x8(pack_f16_rest(w[u][0], w[u][1], ua));
+                    pb[u][nt][1][1] = trans8x8(pack_f16_rest(w[u][2], w[u][3], ub));
                 }
             }
         }
@@ -568,12 +560,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                     const uint32_t fa = k ? e4m3x2_of<1>(ga) : e4m3x2_of<0>(ga);
                     const uint32_t fb = k ? e4m3x2_of<1>(gb) : e4m3x2_of<0>(gb);
                     // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3: dims 0, 2 and
-                    // dims 1, 3 of the four.  The shifts are products (the multiplier's pipe has
-                    // room, the logic pipe that also converts has not).
-                    const uint32_t ea = bitselect(wa * p.two16, wa * p.two4, 0x0f0f0f0fu);
-                    const uint32_t eb = bitselect(wb * p.two16, wb * p.two4, 0x0f0f0f0fu);
-                    const uint32_t oa = bitselect(wa * p.two12, wa, 0x0f0f0f0fu);
-                    const uint32_t ob = bitselect(wb * p.two12, wb, 0x0f0f0f0fu);
+                    // dims 1, 3 of the four.  Every nibble has its place in the product of the even
+                    // (or odd) ones with two shifts at once (the multiplier's pipe has room, the
+                    // logic pipe that also converts has not).
+                    const uint32_t la = wa & 0x0f0f0f0fu, lb = wb & 0x0f0f0f0fu;
+                    const uint32_t ea = la * p.even, eb = lb * p.even;
+                    const uint32_t oa = (la * p.minus + wa) * p.odd, ob = (lb * p.minus + wb) * p.odd;
                     const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
                     const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
                     const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);
@@ -856,9 +848,9 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
         !encode_rows_map(&map_v, p.v_cache, rt * C::ROWB, pool_rows))
         return cudaErrorInvalidValue;
     p.workers = workers[dev];
-    p.two4 = 1u << 4;
-    p.two12 = 1u << 12;
-    p.two16 = 1u << 16;
+    p.even = 0x10010u;
+    p.odd = 0x1001u;
+    p.minus = ~0u;
     const int grid = p.max_workers < p.workers ? p.max_workers : p.workers;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
