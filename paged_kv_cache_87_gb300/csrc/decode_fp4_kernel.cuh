@@ -565,7 +565,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                     // logic pipe that also converts has not).
                     const uint32_t la = wa & 0x0f0f0f0fu, lb = wb & 0x0f0f0f0fu;
                     const uint32_t ea = la * p.even, eb = lb * p.even;
-                    const uint32_t oa = (la * p.minus + wa) * p.odd, ob = (lb * p.minus + wb) * p.odd;
+                    // (the odd nibbles by a mask: long documents 152 instead of 151 us; with sixteen
+                    // heads 227 instead of 231)
+                    const uint32_t ma = NT == 1 ? la * p.minus + wa : wa & 0xf0f0f0f0u;
+                    const uint32_t mb = NT == 1 ? lb * p.minus + wb : wb & 0xf0f0f0f0u;
+                    const uint32_t oa = ma * p.odd, ob = mb * p.odd;
                     const uint32_t e0 = hmul2(e2m1x2_to_f16x2<2>(ea), fa), e1 = hmul2(e2m1x2_to_f16x2<3>(ea), fa);
                     const uint32_t e2 = hmul2(e2m1x2_to_f16x2<2>(eb), fb), e3 = hmul2(e2m1x2_to_f16x2<3>(eb), fb);
                     const uint32_t d0 = hmul2(e2m1x2_to_f16x2<2>(oa), fa), d1 = hmul2(e2m1x2_to_f16x2<3>(oa), fa);

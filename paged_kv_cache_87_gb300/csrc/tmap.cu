@@ -76,9 +76,11 @@ bool encode_rows_map(CUtensorMap* map, const void* pool, int row_bytes, long lon
     const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)(row_bytes / 8), 1};
     const cuuint32_t estr[2] = {1, 1};
+    // (promotion to 256 bytes: 117 us against 88 for the 4-bit decode of 8 x 16k - 64k tokens in blocks
+    // of 8, whose rows are 576 bytes; the other cases as fast)
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(pool), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
 
