@@ -153,11 +153,23 @@ void call(const char* fn, F f) {
 // A new tensor for a call on `stream`: its memory, taken on the current stream, is not used
 // again before `stream` has done what it holds when the tensor is dropped.
 at::Tensor fresh(at::IntArrayRef shape, const at::TensorOptions& options, pkv_stream_t stream) {
-    Unlocked u;
     at::Tensor t = at::empty(shape, options);
     if (stream != c10::cuda::getCurrentCUDAStream().stream() && t.numel() != 0)
         t.record_stream(c10::cuda::getStreamFromExternal(stream, t.get_device()).unwrap());
     return t;
+}
+
+// Two new tensors [rows, heads, d], one behind the other in one allocation (a second one is a
+// quarter of what such a call costs the host: norm of one token 5.2 us with two, 4.0 with one).
+void fresh_pair(int64_t rows, int64_t heads0, int64_t heads1, int64_t d, const at::TensorOptions& options,
+                pkv_stream_t stream, at::Tensor* first, at::Tensor* second) {
+    *first = fresh({rows * (heads0 + heads1) * d}, options, stream);
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(first->storage()), first->key_set(),
+                                                     first->dtype());
+    impl->set_storage_offset(rows * heads0 * d);
+    impl->set_sizes_contiguous({rows, heads1, d});
+    *second = at::Tensor(std::move(impl));
+    first->unsafeGetTensorImpl()->set_sizes_contiguous({rows, heads0, d});
 }
 
 void count(Py_ssize_t got, Py_ssize_t want) {
@@ -209,23 +221,26 @@ PKV_ENTRY(decode) {
     const float scale = (float)number(a[6]), kv_scale = (float)number(a[7]);
     const pkv_stream_t stream = stream_of(a[10]);
     at::Tensor ws, out;
-    if (a[8] == Py_None) {
-        const size_t bytes = pkv_decode_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, c.type);
-        ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
-    } else {
-        ws = contiguous(a[8], "workspace must be a contiguous CUDA tensor");
-    }
-    if (a[9] == Py_None) {
-        out = fresh(q.sizes(), q.options(), stream);
-    } else {
+    if (a[8] != Py_None) ws = contiguous(a[8], "workspace must be a contiguous CUDA tensor");
+    if (a[9] != Py_None) {
         out = contiguous(a[9], "out must be a contiguous CUDA tensor");
         need(out.numel() >= q.numel() && out.scalar_type() == q.scalar_type(),
              "out must have query's size and type");
     }
     const bool prefix = truth(a[11]);
     const pkv_dtype qt = code_of(q.scalar_type());
-    const size_t ws_bytes = (size_t)ws.numel() * ws.element_size();
-    if (truth(a[12]))
+    const bool prepare = truth(a[12]);
+    size_t ws_bytes = 0;
+    auto take = [&] {
+        if (!ws.defined()) {
+            const size_t bytes = pkv_decode_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, c.type);
+            ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
+        }
+        if (!out.defined()) out = fresh(q.sizes(), q.options(), stream);
+        ws_bytes = (size_t)ws.numel() * ws.element_size();
+    };
+    if (prepare) {
+        take();
         return Py_BuildValue(
             "((KKKKKiiiiiiiidiidKnKK)NN)", (unsigned long long)q.data_ptr(),
             (unsigned long long)k.data_ptr(), (unsigned long long)v.data_ptr(),
@@ -234,8 +249,10 @@ PKV_ENTRY(decode) {
             (double)kv_scale, (unsigned long long)ws.data_ptr(), (Py_ssize_t)ws_bytes,
             (unsigned long long)out.data_ptr(), (unsigned long long)stream,
             THPVariable_Wrap(ws), THPVariable_Wrap(out));
+    }
     auto* fn = prefix ? pkv_paged_decode_attention_prefix : pkv_paged_decode_attention;
     call(prefix ? "pkv_paged_decode_attention_prefix" : "pkv_paged_decode_attention", [&] {
+        take();
         return fn(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                   static_cast<const int32_t*>(bt.data_ptr()),
                   static_cast<const int32_t*>(cl.data_ptr()), S, Hq, c.heads, c.d, c.block,
@@ -313,16 +330,17 @@ PKV_ENTRY(gather) {
     const float kv_scale = (float)number(a[6]);
     const pkv_stream_t stream = stream_of(a[10]);
     at::Tensor out[2];
-    for (int i = 0; i < 2; ++i) {
-        if (a[8 + i] == Py_None) {
-            out[i] = fresh(shape, k.options().dtype(type), stream);
-        } else {
+    for (int i = 0; i < 2; ++i)
+        if (a[8 + i] != Py_None) {
             out[i] = contiguous(a[8 + i], "key_out and value_out must be contiguous CUDA tensors");
             need(out[i].sizes() == at::IntArrayRef(shape, 3) && out[i].scalar_type() == type,
                  "key_out and value_out must be [total_rows, Hkv, d] of out_dtype");
         }
-    }
     call("pkv_gather_cache", [&] {
+        if (!out[0].defined() && !out[1].defined())
+            fresh_pair(rows, c.heads, c.heads, c.d, k.options().dtype(type), stream, &out[0], &out[1]);
+        for (at::Tensor& t : out)
+            if (!t.defined()) t = fresh(shape, k.options().dtype(type), stream);
         return pkv_gather_cache(k.data_ptr(), v.data_ptr(),
                                 static_cast<const int32_t*>(bt.data_ptr()),
                                 static_cast<const int32_t*>(rs.data_ptr()), first, S, rows, c.heads,
@@ -383,11 +401,10 @@ struct NormRope {
         rows_out(out, *q, Hq, &q_out, &out_stride);
     }
 
+    // What was given as an output, checked; nothing yet where none was.
     void rows_out(PyObject* given, const at::Tensor& like, int64_t heads, at::Tensor* to, int64_t* stride) {
-        if (given == Py_None) {
-            *to = fresh(like.sizes(), like.options(), stream);
-            *stride = heads * d;
-        } else {
+        *stride = heads * d;
+        if (given != Py_None) {
             *to = tensor(given);
             need(to->sizes() == like.sizes() && to->scalar_type() == like.scalar_type(),
                  "q_out and k_out must have query's and key's shape and type");
@@ -405,6 +422,10 @@ PKV_ENTRY(norm_rope) {
     int64_t k_out_stride;
     r.rows_out(a[9], *r.k, r.Hkv, &k_out, &k_out_stride);
     call("pkv_qk_norm_rope", [&] {
+        if (!r.q_out.defined() && !k_out.defined())
+            fresh_pair(r.T, r.Hq, r.Hkv, r.d, r.q->options(), r.stream, &r.q_out, &k_out);
+        if (!r.q_out.defined()) r.q_out = fresh(r.q->sizes(), r.q->options(), r.stream);
+        if (!k_out.defined()) k_out = fresh(r.k->sizes(), r.k->options(), r.stream);
         return pkv_qk_norm_rope(r.q->data_ptr(), r.q_stride, r.k->data_ptr(), r.k_stride, r.qw, r.kw,
                                 r.weight_type, r.eps, static_cast<const float*>(r.cs->data_ptr()),
                                 r.positions_known, r.rot_dim, r.interleaved,
@@ -435,6 +456,7 @@ PKV_ENTRY(norm_rope_write) {
     const int64_t v_stride = head_rows(value, r.Hkv, r.d);
     const float kv_scale = (float)number(a[12]);
     call("pkv_qk_norm_rope_and_cache", [&] {
+        if (!r.q_out.defined()) r.q_out = fresh(r.q->sizes(), r.q->options(), r.stream);
         return pkv_qk_norm_rope_and_cache(
             r.q->data_ptr(), r.q_stride, r.k->data_ptr(), r.k_stride, value.data_ptr(), v_stride,
             r.qw, r.kw, r.weight_type, r.eps, static_cast<const float*>(r.cs->data_ptr()),
