@@ -3,7 +3,7 @@
 // The checks of shapes, types and strides, the outputs' and the workspace's allocation and the
 // call itself, in one extension function each.  They were Python: on the host of a GB300 an
 // attribute of a tensor costs 0.1 us there and a call 15 - 25 us in all, five times what the
-// kernels of a decode step take; here a call is 5 us, most of it the launch.
+// kernels of a decode step take; here a call is 2 - 3.5 us, most of it the launch.
 //
 // Arguments are positional (binding.py has the signatures and their documentation).  A wrong
 // tensor raises ValueError, an element type that the library does not know KeyError, and a
@@ -13,7 +13,7 @@
 // and what the device waits for may be a callback that needs the lock.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -42,9 +42,12 @@ const at::Tensor& tensor(PyObject* o) {
     return THPVariable_Unpack(o);
 }
 
+thread_local int g_device = -1;   // the current device, once an entry has asked for it
+
 // The library works on the current device (its pointers, its stream, its status word).
 void here(const at::Tensor& t) {
-    need(t.get_device() == c10::cuda::current_device(), "tensors must be on the current CUDA device");
+    if (g_device < 0) g_device = c10::cuda::current_device();
+    need(t.get_device() == g_device, "tensors must be on the current CUDA device");
 }
 
 const at::Tensor& contiguous(PyObject* o, const char* text) {
@@ -150,17 +153,28 @@ void call(const char* fn, F f) {
     check(fn, st);
 }
 
-// A new tensor for a call on `stream`: its memory, taken on the current stream, is not used
-// again before `stream` has done what it holds when the tensor is dropped.
+// A new tensor for a call on `stream`, on the current device: its memory, taken from torch's
+// allocator on the current stream, is not used again before `stream` has done what it holds when
+// the tensor is dropped.  (Through at::empty, with its dispatch, a norm of one token took 4.1 us
+// instead of 3.5.)
 at::Tensor fresh(at::IntArrayRef shape, const at::TensorOptions& options, pkv_stream_t stream) {
-    at::Tensor t = at::empty(shape, options);
+    int64_t n = 1;
+    for (int64_t v : shape) n *= v;
+    const caffe2::TypeMeta type = options.dtype();
+    const size_t bytes = (size_t)n * type.itemsize();
+    c10::Allocator* pool = c10::cuda::CUDACachingAllocator::get();
+    at::Tensor t(c10::make_intrusive<c10::TensorImpl>(
+        c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                           pool->allocate(bytes), pool, true)),
+        c10::DispatchKeySet(c10::DispatchKey::CUDA), type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
     if (stream != c10::cuda::getCurrentCUDAStream().stream() && t.numel() != 0)
         t.record_stream(c10::cuda::getStreamFromExternal(stream, t.get_device()).unwrap());
     return t;
 }
 
 // Two new tensors [rows, heads, d], one behind the other in one allocation (a second one is a
-// quarter of what such a call costs the host: norm of one token 5.2 us with two, 4.0 with one).
+// fifth of what such a call costs the host: norm of one token 5.2 us with two, 4.2 with one).
 void fresh_pair(int64_t rows, int64_t heads0, int64_t heads1, int64_t d, const at::TensorOptions& options,
                 pkv_stream_t stream, at::Tensor* first, at::Tensor* second) {
     *first = fresh({rows * (heads0 + heads1) * d}, options, stream);
@@ -185,16 +199,24 @@ int64_t head_rows(const at::Tensor& t, int64_t heads, int64_t d) {
     return t.size(0) > 1 ? s[0] : heads * d;
 }
 
+// The exception being handled, as a Python one.
+PyObject* translated() {
+    HANDLE_TH_ERRORS
+    throw;
+    END_HANDLE_TH_ERRORS
+}
+
 #define PKV_ENTRY(name)                                                       \
     PyObject* name##_body(PyObject* const* a, Py_ssize_t n);                  \
     PyObject* name(PyObject*, PyObject* const* a, Py_ssize_t n) {             \
-        HANDLE_TH_ERRORS                                                      \
+        g_device = -1;                                                        \
         try {                                                                 \
             return name##_body(a, n);                                         \
         } catch (const Refused&) {                                            \
             return nullptr;                                                   \
+        } catch (...) {                                                       \
+            return translated();                                              \
         }                                                                     \
-        END_HANDLE_TH_ERRORS                                                  \
     }                                                                         \
     PyObject* name##_body(PyObject* const* a, Py_ssize_t n)
 

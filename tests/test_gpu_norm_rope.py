@@ -176,3 +176,33 @@ def test_another_stream_and_a_captured_step():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref) and torch.equal(kc, rk) and torch.equal(vc, rv)
+
+
+def test_outputs_are_ordinary_tensors():
+    """Outputs that a call allocates: contiguous, apart from each other, of any mode, and gone when dropped."""
+    q = torch.randn(5, 4, 64, device="cuda", dtype=torch.bfloat16)
+    k = torch.randn(5, 2, 64, device="cuda", dtype=torch.bfloat16)
+    cs = torch.randn(9, 32, device="cuda")
+    pos = torch.arange(5, device="cuda")
+    qo, ko = binding.pkv_qk_norm_rope(q, k, cs, pos)
+    assert qo.shape == q.shape and ko.shape == k.shape and qo.is_contiguous() and ko.is_contiguous()
+    assert qo.device == q.device and qo.dtype == q.dtype and not qo.requires_grad
+    keep = qo.clone()
+    ko.fill_(7)
+    assert torch.equal(qo, keep) and (ko == 7).all() and ko._version == 1 and qo._version == 0
+    loss = (qo.float().requires_grad_() * 2).sum()
+    loss.backward()
+    again = ko.resize_(3, 2, 64).reshape(-1).tolist()
+    assert again == [7.0] * 384 and torch.equal(qo, keep)
+    with torch.inference_mode():
+        a, b = binding.pkv_qk_norm_rope(q, k, cs, pos)
+        assert a.is_inference() and b.is_inference() and torch.equal(a, qo)
+    assert not qo.is_inference() and not ko.is_inference()
+    e, f = binding.pkv_qk_norm_rope(q[:0], k[:0], cs, pos[:0])
+    assert e.shape == (0, 4, 64) and f.shape == (0, 2, 64)
+    torch.cuda.synchronize()
+    del qo, ko, a, b, e, f, keep, loss
+    before = torch.cuda.memory_allocated()
+    for _ in range(50):
+        binding.pkv_qk_norm_rope(q, k, cs, pos)
+    assert torch.cuda.memory_allocated() == before
