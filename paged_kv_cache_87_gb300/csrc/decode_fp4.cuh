@@ -6,7 +6,7 @@
 namespace pkv {
 
 constexpr int kFp4Tile = 128;         // tokens of a tile: the split's unit and a ring stage
-// Slots of a unit besides its tiles (0: a serving batch took 144 us instead of 116; 2: the same).
+// Slots of a unit besides its tiles (a serving batch takes 141 us with 0, 103.5 with 1, 104.6 with 2).
 constexpr int kFp4UnitCost = 1;
 // Slots a worker takes at least (one context of 600 tokens: 8.0 us with 1, 8.7 with 2).
 constexpr int kFp4MinQuota = 1;
@@ -16,8 +16,8 @@ constexpr int kFp4MaxPieces = 64;
 constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most (half with units of 16 heads)
 
 // Query heads of a work unit: one kv head's group, in parts of 16 at most.  Groups of up to eight
-// take the kernel whose unit is eight (long documents: 160 us at eight heads a group; at sixteen,
-// 233 us in one unit against 307 in two).
+// take the kernel whose unit is eight (long documents: 151 us at eight heads a group; at sixteen,
+// 228 us in one unit, and 233 against 307 in two when that was chosen).
 inline int fp4_unit_heads(int group) { return group > 8 ? 16 : 8; }
 
 struct DecodeFp4Params {

@@ -34,20 +34,22 @@
 // worker leaves at most two partial states (its first and its last unit), and merge_fp4_kernel
 // joins those of each cut unit in order.
 //
-// What bounds it.  The consumers' issue slots, not HBM: 292 instructions for 16 tokens of K and V at
-// head_dim 128 (128 of them the converts and multiplies), issued at 2.35 a clock an SM; and 3 - 4 us
+// What bounds it.  The consumers' instructions, not HBM: 275 for 16 tokens of K and V at head_dim 128
+// (128 of them the converts and multiplies), issued at 2.4 a clock an SM; and 3 - 4 us
 // that the joining of the cut units takes after the last of them.  Without the
 // arithmetic the same kernel streams at 0.97 of the copy rate.  Measured (device time, GB300):
-//   long documents (8 x 32k - 131k tokens, 64 / 8 heads, d 128, blocks of 32): 158 us, 5.46 TB/s,
-//     0.81 of the measured copy rate; a first, CUDA-core kernel 14,124 us
-//   serving batch (256 x 64 - 8k, 32 / 8 heads, d 128, blocks of 16): 107 us, 4.71 TB/s, 0.69
-//   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 28.0 us, 2.17 TB/s, 0.32: the units are
+//   long documents (8 x 32k - 131k tokens, 64 / 8 heads, d 128, blocks of 32): 151 us, 5.70 TB/s,
+//     0.84 of the measured copy rate; a first, CUDA-core kernel 14,124 us
+//   serving batch (256 x 64 - 8k, 32 / 8 heads, d 128, blocks of 16): 104 us, 4.86 TB/s, 0.72
+//   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 26.6 us, 2.29 TB/s, 0.34: the units are
 //     short, and one costs 0.8 of a tile besides its tiles
-//   one context of 600 tokens: 8.3 us, latency
-// Tried and not kept: four warps loading their own tokens by 16-byte asynchronous copies, without
-// a producer (237 us on long documents); operands of q in registers (187 against 175 us); a fifth
-// CTA a SM at 72 registers (200 against 175 us); one piece of 16 tokens a warp at a time (174
-// against 163 us); halves of the loops rolled up (168 - 172 against 160 us).
+//   one context of 600 tokens: 8.1 us, latency
+// Tried and not kept (each against the step of its time): four warps loading their own tokens by
+// 16-byte asynchronous copies, without a producer (237 against 160 us on long documents); no producer,
+// the last warp through with a stage filling it again (186 against 158); operands of q in registers
+// (187 against 175); a fifth CTA a SM at 72 registers (200 against 175); one piece of 16 tokens a warp
+// at a time (167 against 158; with four CTAs 164); two stages (164 against 158); halves of the loops
+// rolled up (168 - 172 against 160).
 #pragma once
 
 #include "decode_fp4.cuh"
