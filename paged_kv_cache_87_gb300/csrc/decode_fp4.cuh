@@ -20,6 +20,14 @@ constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most (half with 
 // 228 us in one unit, and 233 against 307 in two when that was chosen).
 inline int fp4_unit_heads(int group) { return group > 8 ? 16 : 8; }
 
+// Few short contexts: a cluster of eight CTAs takes a unit and joins it by itself, where every unit's
+// cluster is resident at once and no CTA has more than kFp4ClusterTiles tiles.  One sequence, 32 / 8
+// heads, d 128 (us, clusters against equal runs and a joining kernel): 600 tokens 6.3 against 8.1, 2,048
+// 7.0 against 9.4, 8,192 11.5 against 11.8 (and 12.2 against 14.6 with 64 / 4 heads, d 64); six sequences
+// of 8,192: 18.2 against 20.0; seven of 4,096, whose 56 clusters would take two rounds: 21 against 17.
+constexpr int kFp4Cluster = 8;
+constexpr int kFp4ClusterTiles = 8;
+
 struct DecodeFp4Params {
     const void* q;
     const void* k_cache;

@@ -32,7 +32,8 @@
 // fills a ring of them, and four consumer warps, 2 x 16 tokens of every tile each, whose states
 // meet in shared memory at the end of a unit.  Units inside one run are written straight to `out`; a
 // worker leaves at most two partial states (its first and its last unit), and merge_fp4_kernel
-// joins those of each cut unit in order.
+// joins those of each cut unit in order.  Few short contexts take a cluster a unit instead, whose
+// CTAs join their states themselves.
 //
 // What bounds it.  The consumers' instructions, not HBM: 275 for 16 tokens of K and V at head_dim 128
 // (128 of them the converts and multiplies), issued at 2.4 a clock an SM; and 3 - 4 us
@@ -43,7 +44,7 @@
 //   serving batch (256 x 64 - 8k, 32 / 8 heads, d 128, blocks of 16): 104 us, 4.86 TB/s, 0.72
 //   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 26.6 us, 2.29 TB/s, 0.34: the units are
 //     short, and one costs 0.8 of a tile besides its tiles
-//   one context of 600 tokens: 8.1 us, latency
+//   one context of 600 tokens: 6.3 us, latency (8.1 in equal runs with a joining kernel)
 // Tried and not kept (each against the step of its time): four warps loading their own tokens by
 // 16-byte asynchronous copies, without a producer (237 against 160 us on long documents); no producer,
 // the last warp through with a stage filling it again (186 against 158); operands of q in registers
@@ -114,6 +115,19 @@ __device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A float of this CTA's shared memory, in CTA `rank` of the cluster.
+__device__ __forceinline__ float load_from(const float* mine, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // What is left of (lo, hi) after pack_f16's rounding, as fp16 again.
 __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&packed));
@@ -146,6 +160,7 @@ struct Cfg {
     static constexpr size_t OFF_PLAN = OFF_QF + NP * NT * NCHUNK * 32 * 16;  // 32 tiles: int4, int2, rows
     static constexpr size_t OFF_X = OFF_PLAN + 32 * (16 + 8 + 16 * 4);
     static constexpr size_t SMEM = OFF_X + XBUF * 4 + 128;             // the base is rounded up
+    static_assert(HEADS * (HD + 2) * 4 <= STAGE_BYTES, "a stage holds a CTA's state");
     // resident CTAs, by registers
     static constexpr int CTAS = HD == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);
     // pieces of 16 tokens a warp works on at once, by registers
@@ -233,7 +248,9 @@ __device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total, int
                (longest + kFp4MaxPieces - 1) / kFp4MaxPieces);
 }
 
-template <typename QT, int HD, int NT>
+// CLUSTER: a cluster of kFp4Cluster CTAs takes one unit, a run of its tiles each, and joins its own
+// states through distributed shared memory.
+template <typename QT, int HD, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
@@ -257,13 +274,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     }
     pdl_wait();                // the kernel before (the cache write) has completed
     pdl_launch_dependents();   // the merge kernel may plan beside this one
-    scan_slots<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
     const int B = p.block_size, logB = p.log_block, upi = p.num_kv_heads * p.nsub;
     const int tile_bytes = B * C::ROWB;
-    const int total = s_pref[kThreads] * upi, q = quota_of(p, total, s_pref[kThreads + 1]);
-    const int a = min(blockIdx.x * q, total), end = min(a + q, total);
+    int a, end, q = 1;          // this CTA's slots (CLUSTER: tiles of its unit), the slots of each CTA
+    const int my_unit = blockIdx.x / kFp4Cluster, rank = blockIdx.x % kFp4Cluster;
+    if constexpr (CLUSTER) {
+        const int n = tiles_of(p, my_unit / upi);
+        a = n * rank / kFp4Cluster;
+        end = n * (rank + 1) / kFp4Cluster;
+        __syncthreads();                           // the barriers are visible
+    } else {
+        scan_slots<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
+        const int total = s_pref[kThreads] * upi;
+        q = quota_of(p, total, s_pref[kThreads + 1]);
+        a = min(blockIdx.x * q, total);
+        end = min(a + q, total);
+    }
 
-    if (warp == kConsumers) {
+    auto produce = [&] {
         // ======================= producer warp =======================
         // Plans 32 slots at a time, one a lane, then issues their tiles.
         const uint64_t policy = l2_evict_first_policy();
@@ -279,13 +307,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         // a pool row is a whole tile of 8 or 16 tokens, or half of a tile of 32
         const int log_rt = min(logB, 4), per_block = logB - log_rt, log_rows = 7 - log_rt;
         const int cap = p.max_context_len;
-        if (lane == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (!CLUSTER && lane == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
         __syncwarp();
         for (int pos0 = a; pos0 < end; pos0 += 32) {
             const int pos = pos0 + lane;
             int4 m = make_int4(0, 0, 0, 0);
             int uend_of = 0;
-            if (pos < end) {
+            if (CLUSTER && pos < end) {
+                const int s = my_unit / upi, u = my_unit % upi;
+                m = make_int4((pos == a ? kFirst : 0) | (pos == end - 1 ? kLast : 0) |
+                                  min(kFp4Tile, min(p.context_lens[s], cap) - pos * kFp4Tile) << 8, s, u, 0);
+                plan_at[lane] = make_int2(pos, u / p.nsub);
+            }
+            if (!CLUSTER && pos < end) {
                 int s, n, base;
                 locate<kThreads>(p, s_pref, upi, pos, &s, &n, &base);
                 const int u = (pos - base) / n, at = (pos - base) % n, tile = at - kFp4UnitCost;
@@ -300,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 }
             }
             plan[lane] = m;
-            if (pos == end - 1 && m.x != 0 && m.w == 1)   // begun here, goes on in the next worker
+            if (!CLUSTER && pos == end - 1 && m.x != 0 && m.w == 1)   // begun here, goes on in the next worker
                 p.cuts[blockIdx.x] = make_int4(1, m.y, m.z, (uend_of - 1) / q);
             const unsigned have = __ballot_sync(0xffffffffu, m.x != 0);   // and the plan is visible
             // the tiles' pool rows, 8 or 16 each (beyond the context's last block: that one's again)
@@ -362,6 +396,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
             metas[stage].x = kDone;
             mbar_arrive(&full[stage]);
         }
+    };
+    if (warp == kConsumers) {
+        produce();
+        if constexpr (CLUSTER) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
         return;
     }
 
@@ -373,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         for (int s = blockIdx.x * kConsumers + warp; s < p.num_seqs; s += gridDim.x * kConsumers) {
             const int c = p.context_lens[s];
             if (lane == 0 && (c < 0 || c > cap)) set_status(p.status, PKV_DEV_BAD_CONTEXT);
-            if (c <= 0 || cap == 0)
+            if (c <= 0 || cap == 0)              // (with CLUSTER, a unit's CTAs find nothing to join)
                 for (int64_t i = lane; i < row; i += 32) store_from_float<QT>(p.out, s * row + i, 0.f);
         }
     }
@@ -588,13 +630,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         }
     };
 
+    // CLUSTER: this CTA's state, [HEADS][HD] and (m, l) of the heads, in the ring's first stage (all of
+    // the CTA's tiles have been read when it is written)
+    float* mine = reinterpret_cast<float*>(smem);
+    float* mine_ml = mine + HEADS * HD;
+    if (CLUSTER && a == end && threadIdx.x < HEADS) {
+        mine_ml[2 * threadIdx.x] = -INFINITY;
+        mine_ml[2 * threadIdx.x + 1] = 0.f;
+    }
     while (true) {
         if (!mbar_wait(&full[stage], phase)) {
             set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
-            return;
+            break;
         }
         const int4 meta = metas[stage];
-        if (meta.x & kDone) return;
+        if (meta.x & kDone) break;
         const uint8_t* sb = smem + stage * C::STAGE_BYTES;
         if (meta.x & kFirst) {
             const int nh = min(HEADS, p.group - meta.z % p.nsub * HEADS);
@@ -717,7 +767,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                             f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
                             L = fmaf(xl[w * HEADS + h], f[w], L);
                         }
-                        if (meta.w < 0) {
+                        if (CLUSTER) {
+                            if (part == 0) {
+                                mine_ml[2 * h] = M;
+                                mine_ml[2 * h + 1] = L;
+                            }
+                        } else if (meta.w < 0) {
                             const float inv = p.out_scale / L;
 #pragma unroll
                             for (int w = 0; w < kConsumers; ++w) f[w] *= inv;
@@ -733,13 +788,43 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
 #pragma unroll
                         for (int w = 0; w < kConsumers; ++w)
                             A = fmaf(xa[(w * 8 + h - 8 * nt) * C::HS + dim], f[w], A);
-                        if (meta.w < 0) store_from_float<QT>(p.out, row * HD + pass * C::XD + dim, A);
+                        if (CLUSTER) mine[h * HD + pass * C::XD + dim] = A;
+                        else if (meta.w < 0) store_from_float<QT>(p.out, row * HD + pass * C::XD + dim, A);
                         else p.part_acc[pi * HD + pass * C::XD + dim] = A;
                     }
                 }
                 named_bar_sync(1, kConsumers * 32);     // the exchange buffer is free again
             }
         }
+    }
+    if constexpr (CLUSTER) {
+        __syncwarp();
+        cluster_sync();
+        // head `rank` of the unit (and every kFp4Cluster-th from there), a dim a thread
+        const int s = my_unit / upi, u = my_unit % upi, kvh = u / p.nsub, h0 = u % p.nsub * HEADS;
+        const int nh = min(HEADS, p.group - h0), dim = threadIdx.x;
+        if (p.context_lens[s] > 0 && p.max_context_len > 0 && dim < HD)
+            for (int h = rank; h < nh; h += kFp4Cluster) {
+                float m[kFp4Cluster], A[kFp4Cluster], M = -INFINITY, L = 0.f, sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < kFp4Cluster; ++k) {
+                    m[k] = load_from(mine_ml + 2 * h, k);
+                    A[k] = load_from(mine + h * HD + dim, k);
+                    M = fmaxf(M, m[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kFp4Cluster; ++k) {
+                    const float l = load_from(mine_ml + 2 * h + 1, k);
+                    if (m[k] == -INFINITY && l == 0.f) continue;     // no tiles there
+                    const float f = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - M);
+                    L = fmaf(l, f, L);
+                    sum = fmaf(A[k], f, sum);
+                }
+                const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + h0 + h;
+                store_from_float<QT>(p.out, row * HD + dim, sum * (p.out_scale / L));
+            }
+        __syncwarp();
+        cluster_sync();                 // what the others read stays until they have
     }
 }
 
@@ -825,7 +910,7 @@ __global__ void __launch_bounds__(THREADS) merge_fp4_kernel(DecodeFp4Params p) {
     }
 }
 
-template <typename QT, int HD, int NT>
+template <typename QT, int HD, int NT, bool CLUSTER>
 cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     using C = Cfg<QT, HD, NT>;
     static int workers[64] = {0};          // CTAs the device holds at once
@@ -833,7 +918,7 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = decode_fp4_kernel<QT, HD, NT>;
+    auto kernel = decode_fp4_kernel<QT, HD, NT, CLUSTER>;
     if (workers[dev] == 0) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
         if (err != cudaSuccess) return err;
@@ -857,8 +942,12 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     p.even = 0x10010u;
     p.odd = 0x1001u;
     p.minus = ~0u;
-    const int grid = p.max_workers < p.workers ? p.max_workers : p.workers;
-    cudaLaunchAttribute pdl[1];
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
+    const int grid = CLUSTER ? (int)units * kFp4Cluster : p.max_workers < p.workers ? p.max_workers : p.workers;
+    cudaLaunchAttribute pdl[2];
+    pdl[1].id = cudaLaunchAttributeClusterDimension;
+    pdl[1].val.clusterDim.x = kFp4Cluster;
+    pdl[1].val.clusterDim.y = pdl[1].val.clusterDim.z = 1;
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
@@ -867,15 +956,16 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
     err = cudaLaunchKernelEx(&cfg, kernel, p, map_k, map_v);
-    if (err != cudaSuccess || grid == 1) return err;      // one worker cuts nothing
+    if (err != cudaSuccess || CLUSTER || grid == 1) return err;      // one worker cuts nothing
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3((unsigned)(grid - 1), 1, 1);
     cfg.dynamicSmemBytes = 0;
     // eight warps join a unit's few states; where few units share the chip, and each leaves eight
     // states or more, sixteen do (one context of 100,000 tokens and one kv head: 22 us against 31;
     // a serving batch: 107.5 us with sixteen, 106.9 with eight)
-    if ((int64_t)p.num_seqs * p.num_kv_heads * p.nsub * 8 <= grid) {
+    if (units * 8 <= grid) {
         cfg.blockDim = dim3(512, 1, 1);
         return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT, 512>, p);
     }
@@ -883,11 +973,54 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT, 256>, p);
 }
 
+// Clusters that the device holds at once.
+template <typename QT, int HD, int NT>
+cudaError_t resident_clusters(int* most) {
+    using C = Cfg<QT, HD, NT>;
+    static int clusters[64] = {0};         // and one, once asked for
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (clusters[dev] == 0) {
+        auto kernel = decode_fp4_kernel<QT, HD, NT, true>;
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (err != cudaSuccess) return err;
+        cudaLaunchAttribute dim[1];
+        dim[0].id = cudaLaunchAttributeClusterDimension;
+        dim[0].val.clusterDim.x = kFp4Cluster;
+        dim[0].val.clusterDim.y = dim[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kFp4Cluster, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.attrs = dim;
+        cfg.numAttrs = 1;
+        int n = 0;
+        err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (err != cudaSuccess) return err;
+        clusters[dev] = n + 1;
+    }
+    *most = clusters[dev] - 1;
+    return cudaSuccess;
+}
+
+template <typename QT, int HD, int NT>
+cudaError_t launch_units(const DecodeFp4Params& p, cudaStream_t stream) {
+    if (p.max_context_len <= kFp4Cluster * kFp4ClusterTiles * kFp4Tile) {
+        int most = 0;
+        const cudaError_t err = resident_clusters<QT, HD, NT>(&most);
+        if (err != cudaSuccess) return err;
+        if ((int64_t)p.num_seqs * p.num_kv_heads * p.nsub <= most) return launch<QT, HD, NT, true>(p, stream);
+    }
+    return launch<QT, HD, NT, false>(p, stream);
+}
+
 template <typename QT>
 cudaError_t launch_decode_fp4(const DecodeFp4Params& p, cudaStream_t stream) {
     if (p.unit_heads == 16)
-        return p.head_dim == 128 ? launch<QT, 128, 2>(p, stream) : launch<QT, 64, 2>(p, stream);
-    return p.head_dim == 128 ? launch<QT, 128, 1>(p, stream) : launch<QT, 64, 1>(p, stream);
+        return p.head_dim == 128 ? launch_units<QT, 128, 2>(p, stream) : launch_units<QT, 64, 2>(p, stream);
+    return p.head_dim == 128 ? launch_units<QT, 128, 1>(p, stream) : launch_units<QT, 64, 1>(p, stream);
 }
 
 }  // namespace

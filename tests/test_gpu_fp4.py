@@ -329,6 +329,15 @@ def test_decode_lengths(hq, h, d, B, dt, kv):
                  [0, 1, B - 1, B, B + 1, 63, 64, 65, 0, 127, 130, 517, 2], hq, h, d, B, dt, kv)
 
 
+@pytest.mark.parametrize("max_ctx", [None, 8192, 8193])
+@pytest.mark.parametrize("hq,h,d,B,dt", [(8, 1, 128, 16, "bf16"), (4, 4, 64, 8, "f16"), (12, 1, 128, 32, "f32"),
+                                         (40, 2, 64, 32, "bf16"), (7, 1, 64, 16, "f32"), (32, 2, 128, 8, "f16")])
+def test_decode_few_sequences_either_way(hq, h, d, B, dt, max_ctx):
+    """Up to 8,192 tokens a cluster takes a unit; a higher bound of the lengths deals equal runs."""
+    lens = [0, 1, 127, 129, 1025, 700]
+    check_decode(np.random.default_rng(hq + d + B), lens, hq, h, d, B, dt, 1.0, max_ctx=max_ctx)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("lens", [[5000], [3000, 1, 4097], [1]])
 def test_decode_split_contexts(dt, lens):
