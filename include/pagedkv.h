@@ -163,8 +163,8 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num
  * 128-token) pieces by max_context_len, returns PKV_ERR_UNSUPPORTED.
  * Two launches on `stream`: a one-CTA planning kernel and the decode kernel;
  * over a 4-bit cache the decode kernel, which plans by itself, and, unless
- * max_context_len is at most 8,192 and the sequences are few, one that joins the
- * contexts it has split.
+ * the contexts are few and short (by num_seqs and max_context_len, up to 8,192),
+ * one that joins the contexts it has split.
  */
 PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_cache, const void* v_cache,
                                       const int32_t* block_tables, const int32_t* context_lens,

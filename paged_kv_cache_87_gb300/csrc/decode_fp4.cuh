@@ -20,13 +20,16 @@ constexpr int kFp4MaxWorkers = 1024;  // CTAs of the decode, at most (half with 
 // 228 us in one unit, and 233 against 307 in two when that was chosen).
 inline int fp4_unit_heads(int group) { return group > 8 ? 16 : 8; }
 
-// Few short contexts: a cluster of eight CTAs takes a unit and joins it by itself, where every unit's
-// cluster is resident at once and no CTA has more than kFp4ClusterTiles tiles.  One sequence, 32 / 8
-// heads, d 128 (us, clusters against equal runs and a joining kernel): 600 tokens 6.3 against 8.1, 2,048
-// 7.0 against 9.4, 8,192 11.5 against 11.8 (and 12.2 against 14.6 with 64 / 4 heads, d 64); six sequences
-// of 8,192: 18.2 against 20.0; seven of 4,096, whose 56 clusters would take two rounds: 21 against 17.
-constexpr int kFp4Cluster = 8;
-constexpr int kFp4ClusterTiles = 8;
+// Few short contexts: a cluster of up to eight CTAs takes a unit and joins it by itself -- the largest
+// size, not above the tiles, with which every unit's cluster is resident at once, if no CTA has more than
+// kFp4ClusterTiles tiles then (eight, in clusters of eight; what a longer run of one CTA costs outweighs the
+// joining kernel).  Measured (us, clusters against equal runs and a joining kernel), 32 / 8 heads, d 128:
+// one sequence of 100 tokens 5.0 against 6.7, 600 6.3 against 8.1, 2,000 7.2 against 9.4, 8,192 11.5 against
+// 11.8; 14 sequences of 100 5.5 against 7.9, 600 9.1 against 11.2, 1 - 1,000 8.7 against 9.4.  Without the
+// bound on tiles, 20 sequences of 1 - 2,000: 15.4 against 10.9; without that on residence, 7 of 4,096: 21
+// against 17.
+constexpr int kFp4Cluster = 8;        // CTAs of a cluster, at most (a power of two)
+constexpr int kFp4ClusterTiles = 4;
 
 struct DecodeFp4Params {
     const void* q;
@@ -46,6 +49,7 @@ struct DecodeFp4Params {
     int log_block;         // block_size == 1 << log_block
     int workers;           // the split's denominator: every CTA the device holds
     int max_workers;       // workers that can have work, by max_context_len
+    int log_cluster;       // of the CTAs of a unit's cluster
     float qk_scale_log2;   // scale * log2(e) * kv_scale
     float out_scale;       // kv_scale
     uint32_t even, odd, minus;     // 2^4 + 2^16, 1 + 2^12, -1: shifts as products

@@ -119,13 +119,21 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A float of this CTA's shared memory, in CTA `rank` of the cluster.
-__device__ __forceinline__ float load_from(const float* mine, int rank) {
+// Two or four floats of this CTA's shared memory, in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t place_in(const float* mine, int rank) {
     uint32_t at;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(mine)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
+    return at;
+}
+__device__ __forceinline__ void load_from(const float* mine, int rank, float& a, float& b) {
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(place_in(mine, rank)) : "memory");
+}
+__device__ __forceinline__ void load_from(const float* mine, int rank, float (&v)[2]) {
+    load_from(mine, rank, v[0], v[1]);
+}
+__device__ __forceinline__ void load_from(const float* mine, int rank, float (&v)[4]) {
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(place_in(mine, rank)) : "memory");
 }
 
 // What is left of (lo, hi) after pack_f16's rounding, as fp16 again.
@@ -248,8 +256,8 @@ __device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total, int
                (longest + kFp4MaxPieces - 1) / kFp4MaxPieces);
 }
 
-// CLUSTER: a cluster of kFp4Cluster CTAs takes one unit, a run of its tiles each, and joins its own
-// states through distributed shared memory.
+// CLUSTER: a cluster of 1 << p.log_cluster CTAs takes one unit, a run of its tiles each, and joins its
+// own states through distributed shared memory (a lone CTA writes its unit straight to `out`).
 template <typename QT, int HD, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
@@ -277,11 +285,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     const int B = p.block_size, logB = p.log_block, upi = p.num_kv_heads * p.nsub;
     const int tile_bytes = B * C::ROWB;
     int a, end, q = 1;          // this CTA's slots (CLUSTER: tiles of its unit), the slots of each CTA
-    const int my_unit = blockIdx.x / kFp4Cluster, rank = blockIdx.x % kFp4Cluster;
+    const int my_unit = blockIdx.x >> p.log_cluster, rank = blockIdx.x & ((1 << p.log_cluster) - 1);
     if constexpr (CLUSTER) {
         const int n = tiles_of(p, my_unit / upi);
-        a = n * rank / kFp4Cluster;
-        end = n * (rank + 1) / kFp4Cluster;
+        a = n * rank >> p.log_cluster;
+        end = n * (rank + 1) >> p.log_cluster;
         __syncthreads();                           // the barriers are visible
     } else {
         scan_slots<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
@@ -316,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
             if (CLUSTER && pos < end) {
                 const int s = my_unit / upi, u = my_unit % upi;
                 m = make_int4((pos == a ? kFirst : 0) | (pos == end - 1 ? kLast : 0) |
-                                  min(kFp4Tile, min(p.context_lens[s], cap) - pos * kFp4Tile) << 8, s, u, 0);
+                                  min(kFp4Tile, min(p.context_lens[s], cap) - pos * kFp4Tile) << 8,
+                              s, u, p.log_cluster ? 0 : -1);
                 plan_at[lane] = make_int2(pos, u / p.nsub);
             }
             if (!CLUSTER && pos < end) {
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     };
     if (warp == kConsumers) {
         produce();
-        if constexpr (CLUSTER) {
+        if (CLUSTER && p.log_cluster) {
             __syncwarp();
             cluster_sync();
             cluster_sync();
@@ -767,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                             f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
                             L = fmaf(xl[w * HEADS + h], f[w], L);
                         }
-                        if (CLUSTER) {
+                        if (CLUSTER && meta.w >= 0) {
                             if (part == 0) {
                                 mine_ml[2 * h] = M;
                                 mine_ml[2 * h + 1] = L;
@@ -788,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
 #pragma unroll
                         for (int w = 0; w < kConsumers; ++w)
                             A = fmaf(xa[(w * 8 + h - 8 * nt) * C::HS + dim], f[w], A);
-                        if (CLUSTER) mine[h * HD + pass * C::XD + dim] = A;
+                        if (CLUSTER && meta.w >= 0) mine[h * HD + pass * C::XD + dim] = A;
                         else if (meta.w < 0) store_from_float<QT>(p.out, row * HD + pass * C::XD + dim, A);
                         else p.part_acc[pi * HD + pass * C::XD + dim] = A;
                     }
@@ -797,31 +806,35 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
             }
         }
     }
-    if constexpr (CLUSTER) {
+    if (CLUSTER && p.log_cluster) {
         __syncwarp();
         cluster_sync();
-        // head `rank` of the unit (and every kFp4Cluster-th from there), a dim a thread
+        // a head a warp, HD / 32 dims a lane: heads `rank`, rank + cluster, .. of the unit
         const int s = my_unit / upi, u = my_unit % upi, kvh = u / p.nsub, h0 = u % p.nsub * HEADS;
-        const int nh = min(HEADS, p.group - h0), dim = threadIdx.x;
-        if (p.context_lens[s] > 0 && p.max_context_len > 0 && dim < HD)
-            for (int h = rank; h < nh; h += kFp4Cluster) {
-                float m[kFp4Cluster], A[kFp4Cluster], M = -INFINITY, L = 0.f, sum = 0.f;
+        const int nh = min(HEADS, p.group - h0), last = (1 << p.log_cluster) - 1;
+        constexpr int V = HD / 32;
+        if (p.context_lens[s] > 0 && p.max_context_len > 0)
+            for (int h = rank + (warp << p.log_cluster); h < nh; h += kConsumers << p.log_cluster) {
+                float m[kFp4Cluster], l[kFp4Cluster], A[kFp4Cluster][V], M = -INFINITY, L = 0.f, sum[V] = {0.f};
 #pragma unroll
-                for (int k = 0; k < kFp4Cluster; ++k) {
-                    m[k] = load_from(mine_ml + 2 * h, k);
-                    A[k] = load_from(mine + h * HD + dim, k);
-                    M = fmaxf(M, m[k]);
+                for (int k = 0; k < kFp4Cluster; ++k) {              // every load in flight at once
+                    load_from(mine_ml + 2 * h, min(k, last), m[k], l[k]);
+                    load_from(mine + h * HD + V * lane, min(k, last), A[k]);
                 }
 #pragma unroll
+                for (int k = 0; k < kFp4Cluster; ++k) M = fmaxf(M, m[k]);
+#pragma unroll
                 for (int k = 0; k < kFp4Cluster; ++k) {
-                    const float l = load_from(mine_ml + 2 * h + 1, k);
-                    if (m[k] == -INFINITY && l == 0.f) continue;     // no tiles there
+                    if (k > last || (m[k] == -INFINITY && l[k] == 0.f)) continue;   // no tiles there
                     const float f = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - M);
-                    L = fmaf(l, f, L);
-                    sum = fmaf(A[k], f, sum);
+                    L = fmaf(l[k], f, L);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] = fmaf(A[k][i], f, sum[i]);
                 }
                 const int64_t row = (int64_t)s * p.num_q_heads + kvh * p.group + h0 + h;
-                store_from_float<QT>(p.out, row * HD + dim, sum * (p.out_scale / L));
+                const float inv = p.out_scale / L;
+#pragma unroll
+                for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, row * HD + V * lane + i, sum[i] * inv);
             }
         __syncwarp();
         cluster_sync();                 // what the others read stays until they have
@@ -943,10 +956,10 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     p.odd = 0x1001u;
     p.minus = ~0u;
     const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
-    const int grid = CLUSTER ? (int)units * kFp4Cluster : p.max_workers < p.workers ? p.max_workers : p.workers;
+    const int grid = CLUSTER ? (int)units << p.log_cluster : p.max_workers < p.workers ? p.max_workers : p.workers;
     cudaLaunchAttribute pdl[2];
     pdl[1].id = cudaLaunchAttributeClusterDimension;
-    pdl[1].val.clusterDim.x = kFp4Cluster;
+    pdl[1].val.clusterDim.x = CLUSTER ? 1 << p.log_cluster : 1;
     pdl[1].val.clusterDim.y = pdl[1].val.clusterDim.z = 1;
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -973,11 +986,12 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, HD, NT, 256>, p);
 }
 
-// Clusters that the device holds at once.
+// Clusters of 1 << log_size CTAs that the device holds at once.
 template <typename QT, int HD, int NT>
-cudaError_t resident_clusters(int* most) {
+cudaError_t resident_clusters(int log_size, int* most) {
     using C = Cfg<QT, HD, NT>;
-    static int clusters[64] = {0};         // and one, once asked for
+    static int known[4][64] = {{0}};       // and one, once asked for
+    int* clusters = known[log_size];
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -988,10 +1002,10 @@ cudaError_t resident_clusters(int* most) {
         if (err != cudaSuccess) return err;
         cudaLaunchAttribute dim[1];
         dim[0].id = cudaLaunchAttributeClusterDimension;
-        dim[0].val.clusterDim.x = kFp4Cluster;
+        dim[0].val.clusterDim.x = 1 << log_size;
         dim[0].val.clusterDim.y = dim[0].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kFp4Cluster, 1, 1);
+        cfg.gridDim = dim3(1 << log_size, 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = C::SMEM;
         cfg.attrs = dim;
@@ -1007,11 +1021,17 @@ cudaError_t resident_clusters(int* most) {
 
 template <typename QT, int HD, int NT>
 cudaError_t launch_units(const DecodeFp4Params& p, cudaStream_t stream) {
-    if (p.max_context_len <= kFp4Cluster * kFp4ClusterTiles * kFp4Tile) {
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
+    const int64_t tiles = ((int64_t)p.max_context_len + kFp4Tile - 1) / kFp4Tile;
+    for (int log_size = tiles > 4 ? 3 : tiles > 2 ? 2 : tiles > 1; log_size >= 0; --log_size) {
+        if (tiles > (log_size == 3 ? 8 : kFp4ClusterTiles) << log_size || units > kFp4MaxWorkers) continue;
         int most = 0;
-        const cudaError_t err = resident_clusters<QT, HD, NT>(&most);
+        const cudaError_t err = resident_clusters<QT, HD, NT>(log_size, &most);
         if (err != cudaSuccess) return err;
-        if ((int64_t)p.num_seqs * p.num_kv_heads * p.nsub <= most) return launch<QT, HD, NT, true>(p, stream);
+        if (units > most) continue;
+        DecodeFp4Params of_clusters = p;
+        of_clusters.log_cluster = log_size;
+        return launch<QT, HD, NT, true>(of_clusters, stream);
     }
     return launch<QT, HD, NT, false>(p, stream);
 }

@@ -329,13 +329,31 @@ def test_decode_lengths(hq, h, d, B, dt, kv):
                  [0, 1, B - 1, B, B + 1, 63, 64, 65, 0, 127, 130, 517, 2], hq, h, d, B, dt, kv)
 
 
-@pytest.mark.parametrize("max_ctx", [None, 8192, 8193])
-@pytest.mark.parametrize("hq,h,d,B,dt", [(8, 1, 128, 16, "bf16"), (4, 4, 64, 8, "f16"), (12, 1, 128, 32, "f32"),
-                                         (40, 2, 64, 32, "bf16"), (7, 1, 64, 16, "f32"), (32, 2, 128, 8, "f16")])
+FEW = [(8, 1, 128, 16, "bf16"), (4, 4, 64, 8, "f16"), (12, 1, 128, 32, "f32"), (40, 2, 64, 32, "bf16"),
+       (7, 1, 64, 16, "f32"), (32, 2, 128, 8, "f16")]
+
+
+@pytest.mark.parametrize("lens", [[128, 0, 1, 77], [256, 129, 0, 5], [0, 512, 257, 128], [0, 1, 127, 129, 1025, 700]])
+@pytest.mark.parametrize("hq,h,d,B,dt", FEW)
+def test_decode_clusters_of_every_size(hq, h, d, B, dt, lens):
+    """One, two, four and eight CTAs a unit, with units that leave some of them nothing."""
+    check_decode(np.random.default_rng(hq + d + B + len(lens)), lens, hq, h, d, B, dt, 1.0)
+
+
+@pytest.mark.parametrize("max_ctx", [8192, 8193])
+@pytest.mark.parametrize("hq,h,d,B,dt", FEW)
 def test_decode_few_sequences_either_way(hq, h, d, B, dt, max_ctx):
-    """Up to 8,192 tokens a cluster takes a unit; a higher bound of the lengths deals equal runs."""
-    lens = [0, 1, 127, 129, 1025, 700]
-    check_decode(np.random.default_rng(hq + d + B), lens, hq, h, d, B, dt, 1.0, max_ctx=max_ctx)
+    """A bound of the lengths up to 8,192 keeps the clusters, a higher one deals equal runs."""
+    check_decode(np.random.default_rng(hq + d + B), [0, 1, 127, 129, 1025, 700], hq, h, d, B, dt, 1.0, max_ctx=max_ctx)
+
+
+@pytest.mark.parametrize("S,h,most", [(60, 1, 2048), (28, 4, 1024), (56, 8, 512), (56, 8, 513), (240, 8, 128)])
+def test_decode_units_near_what_is_resident(S, h, most):
+    """Cluster sizes by the number of units, up to four tiles a CTA, and the equal runs beyond."""
+    rng = np.random.default_rng(S + h)
+    lens = rng.integers(0, most + 1, S)
+    lens[S // 2] = most
+    check_decode(rng, lens.tolist(), 4 * h, h, 64, 16, "bf16", 1.0)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
