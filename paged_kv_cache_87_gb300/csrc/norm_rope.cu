@@ -4,8 +4,8 @@
 // For a head row x: y = x / sqrt(mean(x^2) + eps) * w, then every pair (y_i, y_j) of the first
 // rot_dim dims is rotated by its angle.  One read and one write of every row: bound by HBM at
 // prompt sizes, by the launch at a decode step's.  Measured with the cache write, bf16, 32 / 8 heads,
-// d 128: 16,384 tokens 68 us (6.0 TB/s, 0.89 of the measured copy rate), 64 tokens 2.9 us; alone, f16,
-// 40 / 40 heads, d 64, 3,001 tokens 12.8 us (0.71).
+// d 128: 16,384 tokens 67 us (6.1 TB/s, 0.90 of the measured copy rate), 64 tokens 2.8 us; alone, f16,
+// 40 / 40 heads, d 64, 3,001 tokens 12.7 us (0.72).
 //
 // A lane holds eight dims of a row (d / 8 lanes a row) as two runs of four: the halves of four
 // pairs, so that the rotation stays in the lane (half-split: dims 4j .. and rot_dim / 2 + 4j ..;
@@ -24,7 +24,7 @@
 
 namespace pkv {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128;   // (256: 68.5 us on the prompts against 67.2, one token 2.5 against 2.3)
 constexpr int kNormRows = 4;     // rows a lane works on at once: their loads are in flight together
 
 // What the kernel does with keys: NoCache writes k_out, a cache type writes the pool.
