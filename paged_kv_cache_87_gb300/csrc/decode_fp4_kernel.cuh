@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         fence_mbar_init();
     }
     pdl_wait();                // the kernel before (the cache write) has completed
-    pdl_launch_dependents();   // the merge kernel may plan beside this one
+    pdl_launch_dependents();   // the joining kernel may start its launch beside this one
     const int B = p.block_size, logB = p.log_block, upi = p.num_kv_heads * p.nsub;
     const int tile_bytes = B * C::ROWB;
     int a, end, q = 1;          // this CTA's slots (CLUSTER: tiles of its unit), the slots of each CTA
@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
             plan[lane] = m;
             if (!CLUSTER && pos == end - 1 && m.x != 0 && m.w == 1)   // begun here, goes on in the next worker
                 p.cuts[blockIdx.x] = make_int4(1, m.y, m.z, (uend_of - 1) / q);
-            const unsigned have = __ballot_sync(0xffffffffu, m.x != 0);   // and the plan is visible
+            const unsigned have = __ballot_sync(0xffffffffu, m.x != 0);
+            __syncwarp();                 // the plan is visible to every lane (a vote orders no memory)
             // the tiles' pool rows, 8 or 16 each (beyond the context's last block: that one's again)
 #pragma unroll 4
             for (int i = lane; i < 32 << log_rows; i += 32) {

@@ -1,0 +1,74 @@
+"""Decode over the 4-bit cache where a CTA plans many tiles and contexts are cut into many
+pieces: tables draw their blocks from a small pool, references are fp64 on the GPU."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4
+from paged_kv_cache_87_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+# half a step of rounding, relative to the value
+HALF = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def pool_of(rng, nb, h, B, d):
+    """A cache of quantised normal rows on the GPU, and its values in fp64."""
+    c = np.zeros(fp4.cache_shape(nb, h, B, d), np.uint8)
+    fp4.write((rng.standard_normal((nb * B, h, d)) * 32).astype(np.float32), c, np.arange(nb * B), 1.0)
+    return torch.from_numpy(c).cuda(), torch.from_numpy(fp4.values(c, d, 1.0)).cuda()
+
+
+def rows_of(vals, table, n):
+    """[h, n, d] rows of a sequence's first n tokens from pool values [nb, h, B, d]."""
+    h, B, d = vals.shape[1:]
+    x = vals[table[:-(-n // B)].long()]                    # [blocks, h, B, d]
+    return x.transpose(0, 1).reshape(h, -1, d)[:, :n]
+
+
+def check(got, q, kv, vv, table, lens, scale, dt):
+    """Every output against fp64.  Weights have half a step of 2^-11 (2^-22 in two terms, for fp32
+    queries) in numerator and denominator; logits are fp32 sums of d terms, off by (d + 8) 2^-24
+    of the largest sum |q k| scale, which moves a weight (against the maximum) by twice that, its
+    exponential 2^-21 more; a worker sums 16 tokens at a time in each of four warps and its own and
+    up to 65 others' states are joined: (n / 64 + 100) 2^-24 of sum p |v|, twice; weights far below
+    the largest are off by 2^-32 of it; one rounding of the result."""
+    h = kv.shape[1]
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert (got[s] == 0).all()
+            continue
+        k, v = rows_of(kv, table[s], n), rows_of(vv, table[s], n)
+        x = q[s].double().view(h, -1, q.shape[2])
+        z = torch.einsum("hgd,hnd->hgn", x, k) * scale
+        p = torch.softmax(z, -1)
+        ref = torch.einsum("hgn,hnd->hgd", p, v)
+        size = torch.einsum("hgn,hnd->hgd", p, v.abs())
+        logit = (torch.einsum("hgd,hnd->hgn", x.abs(), k.abs()).amax(-1) * abs(scale))[..., None]
+        rel = 2 * (2.0 ** -22 if dt == "f32" else 2.0 ** -11) + 4 * (q.shape[2] + 8) * 2.0 ** -24 * logit + \
+            2.0 ** -19 + 2 * (n / 64 + 100) * 2.0 ** -24
+        far = 2.0 ** -32 * v.abs().sum(1)[:, None]
+        tol = (rel * size + far) * (1 + HALF[dt]) + HALF[dt] * ref.abs() + 1e-30
+        err = (got[s].double().view_as(ref) - ref).abs()
+        assert (err <= tol).all(), (s, n, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("hq,h,d,B,dt", [(16, 8, 64, 16, "bf16"), (16, 8, 128, 8, "f16"), (40, 4, 64, 32, "f32")])
+def test_decode_plans_of_several_rounds_repeat_their_bits(hq, h, d, B, dt):
+    """More units than a CTA plans at once (32 slots, one a lane), three rounds and more each."""
+    rng = np.random.default_rng(hq + d)
+    S, nb = 3000, 64
+    lens = rng.integers(0, 260, S)
+    table = torch.from_numpy(rng.integers(0, nb, (S, -(-260 // B))).astype(np.int32)).cuda()
+    (gk, kv), (gv, vv) = (pool_of(rng, nb, h, B, d) for _ in range(2))
+    q = (torch.from_numpy(rng.standard_normal((S, hq, d))) / 32).to(DT[dt]).cuda()
+    args = (q, gk, gv, table, torch.from_numpy(lens.astype(np.int32)).cuda(), 260, 1 / math.sqrt(d))
+    out = binding.pkv_paged_decode_attention(*args)
+    check(out, q, kv, vv, table, lens.tolist(), 1 / math.sqrt(d), dt)
+    for _ in range(20):
+        assert torch.equal(out, binding.pkv_paged_decode_attention(*args))
+    assert binding.pkv_get_device_status() == 0
