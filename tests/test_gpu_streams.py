@@ -1,0 +1,86 @@
+"""Calls that take memory for another stream than the current one: it is neither memory that the
+current stream's queued work still uses, nor given out again while that stream reads the result."""
+import pytest
+import torch
+
+from paged_kv_cache_87_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 40_000_000          # cycles: some 20 ms
+
+
+def step():
+    """Inputs of every call that allocates, long ready on the device, and the calls by name: each
+    takes a stream and gives a list of its outputs."""
+    g = torch.Generator("cuda").manual_seed(1)
+    T, hq, h, d, B, nb = 512, 8, 2, 128, 16, 40
+    kc, vc = (torch.zeros(binding.fp4_cache_shape(nb, h, B, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    q, k, v = (torch.randn(T, n, d, generator=g, device="cuda").bfloat16() for n in (hq, h, h))
+    slots = torch.randperm(nb * B, generator=g, device="cuda")[:T]
+    cs = torch.cat([torch.ones(T, 64), torch.zeros(T, 64)], 1).cuda()
+    pos = torch.arange(T, device="cuda")
+    binding.pkv_reshape_and_cache(k, v, kc, vc, slots)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None].expand(T, nb).contiguous()
+    lens = i32([600] * T)
+    rows = i32([0, T])
+    calls = {
+        "decode": lambda s: [binding.pkv_paged_decode_attention(q, kc, vc, table, lens, 640, 0.1, stream=s)],
+        "gather": lambda s: binding.pkv_gather_cache(kc, vc, table[:1], rows, T, torch.bfloat16, stream=s),
+        "norm": lambda s: binding.pkv_qk_norm_rope(q, k, cs, pos, stream=s),
+        "norm and write": lambda s: [binding.pkv_qk_norm_rope_and_cache(q, k, v, cs, pos, kc, vc, slots, stream=s)],
+    }
+    return calls
+
+
+def drop_while_read(tensor):
+    """Queues a long delay and then a reader of `tensor` on the current stream: what it reads."""
+    seen = torch.empty_like(tensor)
+    torch.cuda._sleep(BUSY)
+    seen.copy_(tensor)
+    return seen
+
+
+@pytest.mark.parametrize("name", ["decode", "gather", "norm", "norm and write"])
+def test_a_call_on_another_stream_leaves_what_the_current_one_still_reads(name):
+    call = step()[name]
+    ref = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = {t.untyped_storage().nbytes() for t in call(None)}
+    need = binding.pkv_decode_workspace_bytes(512, 8, 2, 128, 16, 640, "e2m1")
+    for size in sorted(sizes) + [need]:            # a block that would fit the output, or the workspace
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        x = torch.full((size,), 17, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        seen = drop_while_read(x)
+        del x
+        out = call(side)
+        torch.cuda.synchronize()
+        assert (seen == 17).all()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["decode", "gather", "norm", "norm and write"])
+def test_an_output_dropped_while_the_current_stream_reads_it_is_not_written_again(name):
+    call = step()[name]
+    ref = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    seen = [drop_while_read(t) for t in out]
+    del out
+    trash = []
+    with torch.cuda.stream(side):
+        for t in ref:
+            trash += [torch.full_like(t, 9.0) for _ in range(4)]
+    again = call(side)
+    torch.cuda.synchronize()
+    assert len(trash) == 4 * len(ref)
+    assert all(torch.equal(a, b) for a, b in zip(seen, ref))
+    assert all(torch.equal(a, b) for a, b in zip(again, ref))
+    assert binding.pkv_get_device_status() == 0
