@@ -206,6 +206,28 @@ def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
+def _fresh(like: torch.Tensor, stream, nbytes: int | None = None) -> torch.Tensor:
+    """A new tensor like `like` (or of `nbytes` bytes) for a call on `stream`.  Where that is not
+    the current stream, the memory comes from what torch's allocator keeps for `stream` -- a block
+    that the current stream has dropped may still have its work in flight -- and is held until the
+    current stream, where the caller reads it, is through as well."""
+    shape, dtype = (like.shape, like.dtype) if nbytes is None else ((nbytes,), torch.uint8)
+    now = torch.cuda.current_stream()
+    if stream is None or int(stream.cuda_stream) == now.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(now)
+    return t
+
+
+def _torch_stream(stream) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream.cuda_stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
 # ------------------------------------------------------------------ calls --
 
 def pkv_decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -327,9 +349,9 @@ def _multi_query(name, query, k_cache, v_cache, block_tables, context_lens, quer
         _cuda(t, n)
     need = pkv_multi_query_workspace_bytes(S)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=query.device)
+        workspace = _fresh(query, stream, max(need, 256))
     if out is None:
-        out = torch.empty_like(query)
+        out = _fresh(query, stream)
     _cuda(out, "out")
     _cuda(workspace, "workspace")
     head = [query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
@@ -371,7 +393,7 @@ def pkv_paged_decode_attention_noalloc(query: torch.Tensor, k_cache: torch.Tenso
                  (block_tables, "block_tables"), (context_lens, "context_lens")):
         _cuda(t, n)
     if out is None:
-        out = torch.empty_like(query)
+        out = _fresh(query, stream)
     _cuda(out, "out")
     st = load().pkv_paged_decode_attention_noalloc(
         query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),

@@ -7,6 +7,7 @@ from paged_kv_cache_87_gb300 import binding
 
 pytestmark = pytest.mark.gpu
 
+CALLS = ["decode", "gather", "norm", "norm and write", "multi-query", "draft trees", "without a workspace"]
 BUSY = 40_000_000          # cycles: some 20 ms
 
 
@@ -21,15 +22,24 @@ def step():
     cs = torch.cat([torch.ones(T, 64), torch.zeros(T, 64)], 1).cuda()
     pos = torch.arange(T, device="cuda")
     binding.pkv_reshape_and_cache(k, v, kc, vc, slots)
+    k16, v16 = (torch.randn(nb, h, B, d, generator=g, device="cuda").bfloat16() for _ in range(2))
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
     table = torch.arange(nb, dtype=torch.int32, device="cuda")[None].expand(T, nb).contiguous()
     lens = i32([600] * T)
     rows = i32([0, T])
+    chain = i32(list(range(0, T + 1, 8)))
+    tree = torch.full((T,), 1, dtype=torch.int64, device="cuda")
     calls = {
         "decode": lambda s: [binding.pkv_paged_decode_attention(q, kc, vc, table, lens, 640, 0.1, stream=s)],
         "gather": lambda s: binding.pkv_gather_cache(kc, vc, table[:1], rows, T, torch.bfloat16, stream=s),
         "norm": lambda s: binding.pkv_qk_norm_rope(q, k, cs, pos, stream=s),
         "norm and write": lambda s: [binding.pkv_qk_norm_rope_and_cache(q, k, v, cs, pos, kc, vc, slots, stream=s)],
+        "multi-query": lambda s: [binding.pkv_paged_multi_query_attention(
+            q, k16, v16, table[:T // 8], lens[:T // 8], chain, 640, 0.1, stream=s)],
+        "draft trees": lambda s: [binding.pkv_paged_tree_attention(
+            q, k16, v16, table[:T // 8], lens[:T // 8], chain, tree, 640, 0.1, stream=s)],
+        "without a workspace": lambda s: [binding.pkv_paged_decode_attention_noalloc(
+            q[:32], k16, v16, table[:32], lens[:32], 640, 0.1, stream=s)],
     }
     return calls
 
@@ -42,15 +52,16 @@ def drop_while_read(tensor):
     return seen
 
 
-@pytest.mark.parametrize("name", ["decode", "gather", "norm", "norm and write"])
+@pytest.mark.parametrize("name", CALLS)
 def test_a_call_on_another_stream_leaves_what_the_current_one_still_reads(name):
     call = step()[name]
     ref = [t.clone() for t in call(None)]
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     sizes = {t.untyped_storage().nbytes() for t in call(None)}
-    need = binding.pkv_decode_workspace_bytes(512, 8, 2, 128, 16, 640, "e2m1")
-    for size in sorted(sizes) + [need]:            # a block that would fit the output, or the workspace
+    need = [binding.pkv_decode_workspace_bytes(512, 8, 2, 128, 16, 640, "e2m1"),
+            binding.pkv_multi_query_workspace_bytes(64)]
+    for size in sorted(sizes) + need:            # a block that would fit the output, or the workspace
         torch.cuda.synchronize()
         torch.cuda.empty_cache()
         x = torch.full((size,), 17, dtype=torch.uint8, device="cuda")
@@ -64,7 +75,7 @@ def test_a_call_on_another_stream_leaves_what_the_current_one_still_reads(name):
     assert binding.pkv_get_device_status() == 0
 
 
-@pytest.mark.parametrize("name", ["decode", "gather", "norm", "norm and write"])
+@pytest.mark.parametrize("name", CALLS)
 def test_an_output_dropped_while_the_current_stream_reads_it_is_not_written_again(name):
     call = step()[name]
     ref = [t.clone() for t in call(None)]
