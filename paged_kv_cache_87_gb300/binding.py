@@ -496,6 +496,8 @@ def _copy_args(k_cache, v_cache, src_dst_pairs, stream):
         host = np.ascontiguousarray(np.asarray(src_dst_pairs, dtype=np.int32).reshape(-1, 2))
         validate_pairs(host, NB)
         pairs = torch.from_numpy(host).to(k_cache.device)
+        if stream is not None:     # dropped before the call's stream has read it
+            pairs.record_stream(_torch_stream(stream))
     if pairs.dtype != torch.int32:
         raise ValueError("src_dst_pairs must be int32")
     n = pairs.numel() // 2

@@ -95,3 +95,20 @@ def test_an_output_dropped_while_the_current_stream_reads_it_is_not_written_agai
     assert all(torch.equal(a, b) for a, b in zip(seen, ref))
     assert all(torch.equal(a, b) for a, b in zip(again, ref))
     assert binding.pkv_get_device_status() == 0
+
+
+def test_block_pairs_from_the_host_outlive_the_call():
+    """Pairs that a call stages for itself stay until its stream has read them."""
+    nb, h, B, d = 64, 2, 16, 128
+    k, v = (torch.randn(nb, h, B, d, device="cuda").half() for _ in range(2))
+    pairs = [[i, 32 + i] for i in range(32)]
+    other = torch.tensor([[i, 63 - i] for i in range(32)], dtype=torch.int32)
+    want = [torch.cat([x[:32], x[:32]]) for x in (k, v)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    binding.pkv_copy_blocks(k, v, pairs, stream=side)
+    trash = [other.cuda() for _ in range(16)]
+    torch.cuda.synchronize()
+    assert len(trash) == 16 and torch.equal(k, want[0]) and torch.equal(v, want[1])
