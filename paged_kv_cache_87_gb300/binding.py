@@ -556,7 +556,7 @@ def pkv_swap_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tenso
                                 dst_v.data_ptr(), NBd, pairs.data_ptr() if n else None, n, Hkv,
                                 d, B, kc, _stream_ptr(stream))
     _check("pkv_swap_blocks", st)
-    if not (isinstance(src_dst_pairs, torch.Tensor)) and n:
+    if pairs is not src_dst_pairs and n:
         # the launch reads the staged pairs asynchronously: keep them alive until it ran
         (stream or torch.cuda.current_stream()).synchronize()
 

@@ -1,5 +1,6 @@
 """Calls that take memory for another stream than the current one: it is neither memory that the
 current stream's queued work still uses, nor given out again while that stream reads the result."""
+import numpy as np
 import pytest
 import torch
 
@@ -112,3 +113,26 @@ def test_block_pairs_from_the_host_outlive_the_call():
     trash = [other.cuda() for _ in range(16)]
     torch.cuda.synchronize()
     assert len(trash) == 16 and torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+@pytest.mark.parametrize("kind", ["list", "array", "tensor"])
+def test_swap_pairs_from_the_host_outlive_the_call(kind):
+    """The pinned buffer that a swap stages its pairs in, whatever they came as."""
+    nb, h, B, d = 64, 2, 16, 128
+    k, v = (torch.randn(nb, h, B, d, device="cuda").half() for _ in range(2))
+    hk, hv = (torch.zeros(nb, h, B, d, dtype=torch.float16).pin_memory() for _ in range(2))
+    pairs = [[i, 63 - i] for i in range(32)]
+    other = torch.tensor([[63 - i, i] for i in range(32)], dtype=torch.int32)
+    given = {"list": pairs, "array": np.array(pairs), "tensor": torch.tensor(pairs)}[kind]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    binding.pkv_swap_blocks(k, v, hk, hv, given, stream=side)
+    trash = [other.clone().pin_memory() for _ in range(16)]
+    torch.cuda.synchronize()
+    want = torch.zeros(2, nb, h, B, d, dtype=torch.float16)
+    for a, b in pairs:
+        want[0, b], want[1, b] = k[a].cpu(), v[a].cpu()
+    assert len(trash) == 16 and torch.equal(hk, want[0]) and torch.equal(hv, want[1])
+    assert binding.pkv_get_device_status() == 0
