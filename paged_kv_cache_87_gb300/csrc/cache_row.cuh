@@ -147,42 +147,41 @@ __device__ __forceinline__ void store8(void* dst, const float (&f)[8]) {
 }
 
 // One row of a cache of type KT: dims 8j .. 8j + 7 of row `row` of the (block, kv head)
-// tile at `tile` (B rows, d dims).  store() is called by all 32 lanes of a warp together,
-// lanes 2i and 2i + 1 holding the two halves of one 16-dim group; only `live` lanes write.
+// tile at `tile` (B rows, d dims).  Of the quantised types, store() is called by all 32 lanes of a
+// warp together, lanes 2i and 2i + 1 holding the two halves of one 16-dim group; only `live` lanes
+// write; values() are chunk c's eight values, before kv_scale.
+// A cache of the rows' own type takes them as they are stored: put() and copy() move bits, which
+// a way through fp32 would not (a 16-bit NaN comes back from it without its sign and payload).
 template <typename KT>
 struct CacheRow {
-    __device__ __forceinline__ static void store(uint8_t* tile, int B, int d, int row, int j,
-                                                 const float (&f)[8], float, bool live) {
-        if (live) store8<KT>(tile + ((int64_t)row * d + 8 * j) * KT::bytes, f);
+    static constexpr int N16 = KT::bytes / 2;      // 16-byte pieces of eight dims
+    __device__ __forceinline__ static void put(uint8_t* tile, int d, int row, int j, const uint4 (&x)[N16]) {
+        uint4* to = reinterpret_cast<uint4*>(tile + ((int64_t)row * d + 8 * j) * KT::bytes);
+#pragma unroll
+        for (int i = 0; i < N16; ++i) to[i] = x[i];
     }
     // a quarter of a row: dims 32c + 8w .. + 7 of every 32-dim chunk c, as stored
     template <int HD>
     struct Raw {
-        uint4 x[HD / 32 * (KT::bytes == 4 ? 2 : 1)];
+        uint4 x[HD / 32 * N16];
     };
     template <int HD>
     __device__ __forceinline__ static void fetch(const uint8_t* tile, int B, int row, int w,
                                                  Raw<HD>& r) {
         const uint4* s = reinterpret_cast<const uint4*>(tile + ((int64_t)row * HD + 8 * w) * KT::bytes);
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-            if constexpr (KT::bytes == 4) {
-                r.x[2 * c] = s[8 * c];
-                r.x[2 * c + 1] = s[8 * c + 1];
-            } else {
-                r.x[c] = s[4 * c];
-            }
-        }
+        for (int c = 0; c < HD / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < N16; ++i) r.x[N16 * c + i] = s[4 * N16 * c + i];
     }
-    // chunk c's eight values, before kv_scale
+    // the quarter into a row of the same type
     template <int HD>
-    __device__ __forceinline__ static void values(const Raw<HD>& r, int c, int, float (&f)[8]) {
-        if constexpr (KT::bytes == 4) {
-            Chunk<KT>::to_float(r.x[2 * c], f);
-            Chunk<KT>::to_float(r.x[2 * c + 1], f + 4);
-        } else {
-            Chunk<KT>::to_float(r.x[c], f);
-        }
+    __device__ __forceinline__ static void copy(const Raw<HD>& r, int w, uint8_t* row) {
+        uint4* to = reinterpret_cast<uint4*>(row + 8 * w * KT::bytes);
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < N16; ++i) to[4 * N16 * c + i] = r.x[N16 * c + i];
     }
 };
 

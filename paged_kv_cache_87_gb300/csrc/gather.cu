@@ -68,21 +68,26 @@ __global__ void __launch_bounds__(kGatherThreads) gather_cache_kernel(GatherPara
         typename CacheRow<KT>::template Raw<HD> rk, rv;       // every load first
         CacheRow<KT>::template fetch<HD>(kc + tile, B, row, w, rk);
         CacheRow<KT>::template fetch<HD>(vc + tile, B, row, w, rv);
+        uint8_t* ko = static_cast<uint8_t*>(p.key_out) + dst;
+        uint8_t* vo = static_cast<uint8_t*>(p.value_out) + dst;
+        if constexpr (!is_quantised<KT>()) {
+            CacheRow<KT>::template copy<HD>(rk, w, ko);
+            CacheRow<KT>::template copy<HD>(rv, w, vo);
+        } else {
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-            const int j = 4 * c + w;
-            float k[8], v[8];
-            CacheRow<KT>::template values<HD>(rk, c, w, k);
-            CacheRow<KT>::template values<HD>(rv, c, w, v);
-            if constexpr (is_quantised<KT>()) {
+            for (int c = 0; c < HD / 32; ++c) {
+                const int j = 4 * c + w;
+                float k[8], v[8];
+                CacheRow<KT>::template values<HD>(rk, c, w, k);
+                CacheRow<KT>::template values<HD>(rv, c, w, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     k[e] *= p.kv_scale;
                     v[e] *= p.kv_scale;
                 }
+                store8<OT>(ko + j * 8 * OT::bytes, k);
+                store8<OT>(vo + j * 8 * OT::bytes, v);
             }
-            store8<OT>(static_cast<uint8_t*>(p.key_out) + dst + (int64_t)j * 8 * OT::bytes, k);
-            store8<OT>(static_cast<uint8_t*>(p.value_out) + dst + (int64_t)j * 8 * OT::bytes, v);
         }
     }
 }

@@ -132,10 +132,14 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(NormRopePara
 #pragma unroll
                 for (int u = 0; u < kNormRows; ++u) {
                     const bool live = h0 + u * RPW < heads;
-                    float f[8];
-                    load8<ST>(x[u], f);
-                    CacheRow<KT>::store(tile + u * RPW * tile_bytes, p.block_size, HD, row, j, f,
-                                        p.kv_scale, live);
+                    uint8_t* to = tile + u * RPW * tile_bytes;
+                    if constexpr (is_quantised<KT>()) {
+                        float f[8];
+                        load8<ST>(x[u], f);
+                        CacheRow<KT>::store(to, p.block_size, HD, row, j, f, p.kv_scale, live);
+                    } else if (live) {
+                        CacheRow<KT>::put(to, HD, row, j, x[u]);
+                    }
                 }
             }
             return;
