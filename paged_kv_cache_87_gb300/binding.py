@@ -194,6 +194,11 @@ def _cache_type(cache: torch.Tensor) -> tuple:
     return _TORCH_CODES[cache.dtype], row
 
 
+def _one_type(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    if _TORCH_CODES.get(v_cache.dtype) != _TORCH_CODES[k_cache.dtype]:
+        raise ValueError("k_cache and v_cache must have one element type")
+
+
 def _stream_ptr(stream) -> int:
     if stream is None:   # the handle itself: building a Stream object costs 2.8 us a call
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -338,6 +343,7 @@ def _multi_query(name, query, k_cache, v_cache, block_tables, context_lens, quer
     S = int(context_lens.shape[0])
     if d2 != d or tuple(v_cache.shape) != tuple(k_cache.shape):
         raise ValueError("cache shapes must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    _one_type(k_cache, v_cache)
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or \
             query_start.dtype != torch.int32:
         raise ValueError("block_tables, context_lens and query_start must be int32")
@@ -389,6 +395,7 @@ def pkv_paged_decode_attention_noalloc(query: torch.Tensor, k_cache: torch.Tenso
     if kc == PKV_FP4_E2M1 and (d2 != d or v_cache.shape != k_cache.shape or
                                v_cache.dtype != k_cache.dtype):
         raise ValueError("4-bit caches must have fp4_cache_shape(...) of query's head_dim")
+    _one_type(k_cache, v_cache)
     for t, n in ((query, "query"), (k_cache, "k_cache"), (v_cache, "v_cache"),
                  (block_tables, "block_tables"), (context_lens, "context_lens")):
         _cuda(t, n)

@@ -98,6 +98,12 @@ pkv_dtype code_of(at::ScalarType t) {
     }
 }
 
+// Whether two tensors hold the same element type (FP8 comes as float8_e4m3fn or as uint8).
+bool one_type(const at::Tensor& a, const at::Tensor& b) {
+    auto fp8 = [](at::ScalarType t) { return t == at::kFloat8_e4m3fn || t == at::kByte; };
+    return a.scalar_type() == b.scalar_type() || (fp8(a.scalar_type()) && fp8(b.scalar_type()));
+}
+
 // A cache [NB, Hkv, B, row]: uint8 rows of 36 or 72 bytes are 4-bit codes with their scales.
 struct Cache {
     int blocks, heads, block, d;
@@ -240,10 +246,10 @@ PKV_ENTRY(decode) {
                      &cl = tensor(a[4]);
     need(q.dim() == 3 && bt.dim() == 2, "query must be [S, Hq, d], block_tables [S, max_blocks]");
     const Cache c = cache_of(k);
-    need(c.d == q.size(2) && v.sizes() == k.sizes() && v.element_size() == k.element_size(),
+    need(c.d == q.size(2) && v.sizes() == k.sizes(),
          "cache shapes must be [num_blocks, num_kv_heads, block_size, head_dim]");
-    need(c.type != PKV_FP4_E2M1 || v.scalar_type() == k.scalar_type(),
-         "a 4-bit v_cache must be uint8 as the k_cache");
+    need(one_type(k, v) && (c.type != PKV_FP4_E2M1 || v.scalar_type() == k.scalar_type()),
+         "k_cache and v_cache must have one element type");
     need(bt.scalar_type() == at::kInt && cl.scalar_type() == at::kInt,
          "block_tables and context_lens must be int32");
     for (int i = 0; i < 5; ++i) contiguous(a[i], plain);
@@ -302,14 +308,15 @@ PKV_ENTRY(write) {
                      &v = tensor(a[3]), &slots = tensor(a[4]);
     need(key.dim() == 3, "key must be [T, Hkv, d]");
     const Cache c = cache_of(k);
-    need(key.size(1) == c.heads && key.size(2) == c.d && value.sizes() == key.sizes() &&
-             value.element_size() == key.element_size(),
+    need(key.size(1) == c.heads && key.size(2) == c.d && value.sizes() == key.sizes(),
          "key/value [T, Hkv, d] do not match the cache [NB, Hkv, B, d]");
-    need(v.sizes() == k.sizes() && v.element_size() == k.element_size(),
-         "k_cache and v_cache must have one shape and type");
-    need(c.type != PKV_FP4_E2M1 ||
-             (v.scalar_type() == k.scalar_type() && value.scalar_type() == key.scalar_type()),
-         "key and value, and the two 4-bit caches, must have one type");
+    need(v.sizes() == k.sizes(), "k_cache and v_cache must have one shape");
+    // rows that are copied may be of two types, each of its own cache's
+    const bool copied = key.scalar_type() == k.scalar_type() && value.scalar_type() == v.scalar_type() &&
+                        value.element_size() == key.element_size();
+    need(copied || (one_type(k, v) && value.scalar_type() == key.scalar_type() &&
+                    (c.type != PKV_FP4_E2M1 || v.scalar_type() == k.scalar_type())),
+         "key and value, and the two caches, must have one element type");
     need(slots.scalar_type() == at::kLong && slots.numel() >= key.size(0),
          "slot_mapping must be int64 [T]");
     for (int i = 0; i < 5; ++i)
