@@ -72,3 +72,84 @@ def test_decode_plans_of_several_rounds_repeat_their_bits(hq, h, d, B, dt):
     for _ in range(20):
         assert torch.equal(out, binding.pkv_paged_decode_attention(*args))
     assert binding.pkv_get_device_status() == 0
+
+
+LONG = [  # hq, h, d, B, dt, lens: one context in some 60 pieces (joined by sixteen warps), units of
+          # sixteen heads, and more units than a CTA each, cut where runs end (joined by eight warps)
+    (8, 1, 64, 32, "bf16", [100000]), (4, 1, 128, 16, "f32", [100000, 0, 3]),
+    (16, 1, 128, 16, "f16", [20000, 0, 9000, 1, 40]), (12, 1, 64, 8, "f32", [9000, 20000]),
+    (20, 1, 128, 32, "bf16", [70000]), (16, 8, 64, 16, "bf16", "many"), (64, 4, 128, 16, "f16", "many"),
+    (24, 8, 128, 8, "f32", "many")]
+
+
+def lens_of(lens, rng):
+    if lens != "many":
+        return lens
+    x = np.exp(rng.uniform(0, math.log(9500), 60)).astype(int)
+    x[3], x[17], x[40] = 9500, 0, 8193
+    return x.tolist()
+
+
+@pytest.mark.parametrize("hq,h,d,B,dt,lens", LONG)
+def test_decode_joins_contexts_cut_into_many_pieces(hq, h, d, B, dt, lens):
+    """Equal runs and the joining kernel, eagerly and replayed over a workspace of any contents."""
+    rng = np.random.default_rng(hq + h + d)
+    lens = lens_of(lens, rng)
+    S, nb, most = len(lens), 97, max(lens)
+    assert most > 8192                                     # (bounds up to that may take clusters)
+    table = torch.from_numpy(rng.integers(0, nb, (S, -(-most // B))).astype(np.int32)).cuda()
+    (gk, kv), (gv, vv) = (pool_of(rng, nb, h, B, d) for _ in range(2))
+    q = (torch.from_numpy(rng.standard_normal((S, hq, d))) / 32).to(DT[dt]).cuda()
+    args = (q, gk, gv, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), most, 1 / math.sqrt(d))
+    out = binding.pkv_paged_decode_attention(*args)
+    check(out, q, kv, vv, table, lens, 1 / math.sqrt(d), dt)
+    ws = torch.empty(binding.pkv_decode_workspace_bytes(S, hq, h, d, B, most, "e2m1"), dtype=torch.uint8, device="cuda")
+    got = torch.empty_like(out)
+    binding.pkv_paged_decode_attention(*args, workspace=ws, out=got)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.pkv_paged_decode_attention(*args, workspace=ws, out=got)
+    for fill in (0, 255, 127):
+        ws.fill_(fill), got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+    assert torch.equal(binding.pkv_paged_decode_attention_noalloc(*args), out)
+    # other lengths in the same buffers, replayed: other cuts
+    other = lens[1:] + [most // 2]
+    args[4].copy_(torch.tensor(other, dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    check(got, q, kv, vv, table, other, 1 / math.sqrt(d), dt)
+    assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("hq,h,d,B,dt,lens", LONG + [(8, 2, 128, 16, "bf16", [8000, 0, 700, 129])])
+def test_decode_counts_every_tile_once(hq, h, d, B, dt, lens):
+    """A scale of 0 weighs every token alike, and a tile's values are 6 in one dim: an output is 6
+    times the share of the tokens marked so.  Weights are one power of two and sums whole multiples
+    of it below 2^24: exact; the quotient and the product round by 2^-24 each, then the result."""
+    rng = np.random.default_rng(hq + d)
+    lens = lens_of(lens, rng)
+    S, most = len(lens), max(lens)
+    gk, _ = pool_of(rng, d, h, B, d)
+    x = np.zeros((d, B, h, d), np.float32)
+    x[np.arange(d), :, :, np.arange(d)] = 6.0              # block j: dim j
+    c = np.zeros(fp4.cache_shape(d, h, B, d), np.uint8)
+    fp4.write(x.reshape(d * B, h, d), c, np.arange(d * B), 1.0)
+    marks = rng.integers(0, d, (S, -(-most // 128)))
+    table = np.repeat(marks, 128 // B, 1)[:, :-(-most // B)].astype(np.int32)
+    q = torch.randn(S, hq, d, device="cuda").to(DT[dt])
+    out = binding.pkv_paged_decode_attention(
+        q, gk, torch.from_numpy(c).cuda(), torch.from_numpy(np.ascontiguousarray(table)).cuda(),
+        torch.tensor(lens, dtype=torch.int32, device="cuda"), most, 0.0).double().cpu().numpy()
+    assert binding.pkv_get_device_status() == 0
+    for s, n in enumerate(lens):
+        tiles = -(-n // 128)
+        tokens = np.minimum(128, n - 128 * np.arange(tiles))
+        want = 6.0 * np.bincount(marks[s, :tiles], weights=tokens, minlength=d) / max(n, 1)
+        tol = want * (HALF[dt] + 2.0 ** -22)
+        if dt == "f16":
+            tol = tol + 2.0 ** -25                         # half a step of its smallest values
+        assert (np.abs(out[s] - want) <= tol).all(), (s, n)
