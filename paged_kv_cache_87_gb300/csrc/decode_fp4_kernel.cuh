@@ -179,8 +179,8 @@ constexpr int kFirst = 1, kLast = 2, kDone = 4;
 
 // Tiles of a sequence's context, per unit.
 __device__ __forceinline__ int tiles_of(const DecodeFp4Params& p, int s) {
-    const int c = p.context_lens[s];
-    return c <= 0 ? 0 : (min(c, p.max_context_len) + kFp4Tile - 1) / kFp4Tile;
+    const int n = min(p.context_lens[s], p.max_context_len);
+    return n <= 0 ? 0 : (n - 1) / kFp4Tile + 1;          // (n + 127 would pass 31 bits)
 }
 
 // A unit's length in the plan, in slots: its tiles and, before them, kFp4UnitCost slots that

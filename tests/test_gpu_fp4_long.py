@@ -153,3 +153,26 @@ def test_decode_counts_every_tile_once(hq, h, d, B, dt, lens):
         if dt == "f16":
             tol = tol + 2.0 ** -25                         # half a step of its smallest values
         assert (np.abs(out[s] - want) <= tol).all(), (s, n)
+
+
+def test_decode_of_a_context_of_all_31_bits():
+    """2^31 - 1 tokens, and 127 fewer, over a table that repeats 64 blocks marked with a dim each.
+    Every weight is alike; a warp's sums are whole and below 2^24, and some 70 of them are added:
+    128 2^-24 at most; 127 tokens more or less are 2^-18 of an output; then the result's rounding."""
+    n, d, B = (1 << 31) - 1, 64, 32
+    x = np.zeros((d, B, 1, d), np.float32)
+    x[np.arange(d), :, :, np.arange(d)] = 6.0
+    c = np.zeros(fp4.cache_shape(d, 1, B, d), np.uint8)
+    fp4.write(x.reshape(d * B, 1, d), c, np.arange(d * B), 1.0)
+    cache = torch.from_numpy(c).cuda()
+    g = torch.Generator("cuda").manual_seed(4)
+    table = torch.randint(0, d, (1, 1 << 26), generator=g, dtype=torch.int32, device="cuda")
+    want = 6.0 * B * torch.bincount(table[0], minlength=d).double()
+    want[table[0, -1]] -= 6.0
+    want /= n
+    q = torch.randn(1, 8, d, device="cuda").bfloat16()
+    for length in (n, n - 127):
+        out = binding.pkv_paged_decode_attention(q, cache, cache, table, torch.tensor([length], dtype=torch.int32, device="cuda"),
+                                                 n, 0.0)
+        assert binding.pkv_get_device_status() == 0
+        assert ((out[0].double() - want).abs() <= want * (2.0 ** -8 + 128 * 2.0 ** -24 + 2.0 ** -17)).all()
