@@ -12,8 +12,9 @@
 // keeps every bit down to 2^-39 of its largest value.  fp32 queries take two such terms (22
 // bits).  Weights enter the second product as fp16 in [0, 2^15] (they are taken 2^7 above the running
 // maximum, which is moved when the sum of a lane's two or four passes 2^15, so that a weight 2^-31 of
-// the largest still counts), two terms of them for fp32; the denominator sums them in fp32 before
-// that rounding.
+// the largest still counts), for fp32 queries as two terms of them in [0, 60000] (2^13 above, down to
+// 2^-37); the denominator sums them in fp32 before that rounding, and what is smaller still counts
+// there alone: n tokens lose at most n 2^-32 of an output (n 2^-38).
 //
 // Layout.  32 dims of a row are 16 bytes, eight rows of them one 128-byte line: ldmatrix reads
 // them free of bank conflicts with no swizzle, and one gather moves 32 or 64 tokens of K or V, codes
@@ -142,9 +143,18 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t p
     return pack_f16(lo - v.x, hi - v.y);
 }
 
-constexpr float kLift = 7.f;     // weights are 2^(x - m + kLift)
-constexpr float kMost = 32768.f; // what a lane's weights of a head may sum to before its maximum moves
-constexpr float kSlack = 5.5f;   // then one of the four at least is past this (log2; 15 - 2 - kLift > 5.5)
+// Weights are 2^(x - m + kLift) with the running maximum m, which moves to a larger logit where a
+// lane's weights of a head sum to more than kMost: one of the two or four is kSlack (log2) past m
+// then, and below kMost no weight leaves fp16.  fp32 queries keep more of what is far below the
+// largest weight (down to 2^-38 of it instead of 2^-32) and move the maximum more often.
+template <typename QT>
+struct Weight {
+    static constexpr float kLift = 7.f, kMost = 32768.f, kSlack = 5.5f;   // 2^(15 - 2 - 7) > 2^5.5
+};
+template <>
+struct Weight<F32> {
+    static constexpr float kLift = 13.f, kMost = 60000.f, kSlack = 0.8f;  // 60000 / 4 > 2^(13 + 0.8)
+};
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 
@@ -263,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<QT, HD, NT>;
+    constexpr float kLift = Weight<QT>::kLift, kMost = Weight<QT>::kMost, kSlack = Weight<QT>::kSlack;
     constexpr int HEADS = C::HEADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 127u);
