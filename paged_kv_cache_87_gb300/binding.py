@@ -137,15 +137,20 @@ def load(path: str = LIB_PATH):
 
 
 def _marshal():
-    """The extension module, loaded on first use (built with the library)."""
+    """The extension module, loaded on first use (built with the library, for one torch)."""
     global _calls
     if _calls is None:
         load()
         path = os.path.join(_PKG, "_marshal.so")
+        build = "build it with `python -m paged_kv_cache_87_gb300.build` (needs nvcc, g++ and Python's headers)"
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
-                               "`python -m paged_kv_cache_87_gb300.build` (needs nvcc and g++)")
-        from . import _marshal as module
+            raise RuntimeError(f"{path} is missing: {build}")
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError(f"{path} does not fit this torch ({torch.__version__}) or Python: {build}") from e
+        if module.TORCH != torch.__version__:
+            raise RuntimeError(f"{path} was built for torch {module.TORCH}, this is {torch.__version__}: {build}")
         module.set_error(PagedKVError)
         _calls = module
     return _calls

@@ -95,7 +95,8 @@ def _marshal_commands(obj: str, out: str) -> tuple[list[str], list[str]]:
               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
     lib = os.path.join(root, "lib")
-    return (["g++", *GXX_FLAGS, abi, *[f"-I{i}" for i in inc],
+    built_for = f'-DPKV_TORCH="{torch.__version__}"'
+    return (["g++", *GXX_FLAGS, abi, built_for, *[f"-I{i}" for i in inc],
              *[x for i in sysinc for x in ("-isystem", i)], "-c", MARSHAL_SRC, "-o", obj],
             ["g++", "-shared", "-o", out, obj, LIB, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
              "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"])

@@ -523,4 +523,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__marshal() {
+    PyObject* m = PyModule_Create(&g_module);
+    // the torch it was compiled for: binding.py asks, for no interface of torch's C++ stays the same
+    if (m && PyModule_AddStringConstant(m, "TORCH", PKV_TORCH) < 0) Py_CLEAR(m);
+    return m;
+}
