@@ -262,8 +262,9 @@ PKV_ENTRY(decode) {
     if (a[8] != Py_None) ws = contiguous(a[8], "workspace must be a contiguous CUDA tensor");
     if (a[9] != Py_None) {
         out = contiguous(a[9], "out must be a contiguous CUDA tensor");
-        need(out.numel() >= q.numel() && out.scalar_type() == q.scalar_type(),
-             "out must have query's size and type");
+        need(out.nbytes() >= q.nbytes() && (out.scalar_type() == q.scalar_type() ||
+                                            c10::isIntegralType(out.scalar_type(), false)),
+             "out must have query's size and type, or be that many bytes in integers");
     }
     const bool prefix = truth(a[11]);
     const pkv_dtype qt = code_of(q.scalar_type());
@@ -310,7 +311,8 @@ PKV_ENTRY(write) {
     const Cache c = cache_of(k);
     need(key.size(1) == c.heads && key.size(2) == c.d && value.sizes() == key.sizes(),
          "key/value [T, Hkv, d] do not match the cache [NB, Hkv, B, d]");
-    need(v.sizes() == k.sizes(), "k_cache and v_cache must have one shape");
+    need(v.dim() == 4 && v.size(0) >= k.size(0) && v.sizes().slice(1) == k.sizes().slice(1),
+         "k_cache and v_cache must have one shape (v_cache may have more blocks)");
     // rows that are copied may be of two types, each of its own cache's
     const bool copied = key.scalar_type() == k.scalar_type() && value.scalar_type() == v.scalar_type() &&
                         value.element_size() == key.element_size();

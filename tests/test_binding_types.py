@@ -82,3 +82,41 @@ def test_fp8_caches_come_as_either_type():
         assert torch.equal(binding.pkv_paged_decode_attention(q, a, b, table, lens, 32, 0.1), ref)
         assert torch.equal(binding.pkv_paged_decode_attention_noalloc(q, a, b, table, lens, 32, 0.1), ref)
     assert binding.pkv_get_device_status() == 0
+
+
+def test_a_v_cache_that_is_smaller_or_of_another_shape_is_refused():
+    rows, slots = z(T, H, D), torch.arange(T)
+    k = z(NB, H, B, D)
+    for v in (k[:4], z(NB, H, 2 * B, D), z(NB, 2 * H, B, D), z(NB * H, B, D), z(NB, H, B, 2 * D)):
+        with pytest.raises(ValueError, match="v_cache"):
+            binding.pkv_reshape_and_cache(rows, rows, k, v, slots)
+
+
+@pytest.mark.gpu
+def test_calls_that_were_always_taken_are_taken():
+    """An output given as bytes or integers, larger or not; a v_cache with more blocks than the
+    k_cache holds."""
+    g = torch.Generator("cuda").manual_seed(0)
+    q = torch.randn(T, HQ, 128, generator=g, device="cuda").bfloat16()
+    key, value = (torch.randn(4 * B, H, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = z(4, H, B, 128, dt=BF16, dev="cuda"), z(9, H, B, 128, dt=BF16, dev="cuda")
+    same = z(4, H, B, 128, dt=BF16, dev="cuda")
+    slots = torch.arange(4 * B, device="cuda")
+    binding.pkv_reshape_and_cache(key, value, k, v, slots)
+    binding.pkv_reshape_and_cache(key, value, k, same, slots)
+    assert torch.equal(v[:4], same) and not v[4:].any()
+    binding.prepare_reshape_and_cache(key, value, k, v, slots)()
+    assert torch.equal(v[:4], same)
+    table = torch.arange(4, dtype=torch.int32, device="cuda").expand(T, 4).contiguous()
+    lens = torch.tensor([64, 1, 33], dtype=torch.int32, device="cuda")
+    args = (q, k, same, table, lens, 64, 0.1)
+    ref = binding.pkv_paged_decode_attention(*args)
+    for dt, n in ((U8, 2 * q.numel()), (U8, 2 * q.numel() + 64), (torch.int16, q.numel()), (torch.int64, q.numel() // 4)):
+        out = z(n, dt=dt, dev="cuda")
+        assert binding.pkv_paged_decode_attention(*args, out=out) is out
+        assert torch.equal(out.view(U8)[:2 * q.numel()], ref.view(U8).flatten())
+        assert not out.view(U8)[2 * q.numel():].any()
+    for out in (z(2 * q.numel() - 1, dt=U8, dev="cuda"), z(q.numel(), dt=F16, dev="cuda"), z(q.numel(), dev="cuda")):
+        with pytest.raises(ValueError, match="out must have"):
+            binding.pkv_paged_decode_attention(*args, out=out)
+    assert binding.pkv_get_device_status() == 0
