@@ -97,11 +97,16 @@ __global__ void __launch_bounds__(256) reshape_and_cache_kernel(ReshapeParams p)
 // what a scale costs (a division, a reciprocal) is paid once.  A warp keeps its piece of a token --
 // kWriteRows rows a lane group of K or of V -- and walks the tokens with the next token's rows and
 // slot loading while it quantises this one's.  Bound by the arithmetic (173 instructions for a lane's
-// 16 elements, 64 % of the issue slots) close to HBM: 32,768 tokens of 8 heads, d 128, bf16 in 34 us
-// (5.1 TB/s); a lane of eight dims and an IEEE division each took 70 us.
+// 16 elements, 64 % of the issue slots): 32,768 tokens of 8 heads, d 128, bf16 in 34 us (5.1 TB/s) where
+// HBM alone would take 25, with slots that fill block by block; in no order at all, 53 us.  (A lane of
+// eight dims and an IEEE division each took 70 us.)
 constexpr int kWriteRows = 2;
 constexpr int kWriteThreads = 256;
-constexpr int kWriteCtas = 6;    // a SM's share of the grid: resident at its registers
+// A SM's share of the grid: twice what is resident (three CTAs at 77 registers; two of fp32 rows, at
+// 100).  Measured, 8 heads of 128: 32,768 tokens in bf16 34.0 us against 36.6 with three a SM, in fp32
+// 49.7 against 51.3 with two; smaller chunks are better off with three (9,000 tokens 9.6 us against 10.4,
+// 2,000 tokens 4.2 against 4.7), heads of 64 nearly the same (19.2 against 19.7).
+constexpr int kWriteCtas = 6;
 
 template <typename ST, int HD>
 __global__ void __launch_bounds__(kWriteThreads) reshape_and_cache_fp4_kernel(ReshapeParams p,
