@@ -164,7 +164,17 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int num
  * Two launches on `stream`: a one-CTA planning kernel and the decode kernel;
  * over a 4-bit cache the decode kernel, which plans by itself, and, unless
  * the contexts are few and short (by num_seqs and max_context_len, up to 8,192),
- * one that joins the contexts it has split.
+ * one that joins the contexts it has split.  That choice is made on the host, by
+ * the bound alone: one context of 600 tokens takes 6.3 us under a bound of 600
+ * and 8.6 under one of 131,072, which a step captured for any length passes.
+ * Rounding: logits, maxima, sums and partial states are fp32.  Over a 4-bit cache
+ * the softmax weights of 16-bit queries enter the product with V as fp16, lifted
+ * above the running maximum so that 2^-32 of the largest is what is lost (n tokens
+ * at that level: n 2^-32 of an output), and the denominator sums them unrounded;
+ * against fp64 an fp16 output is off by 2.3e-4 to 2.7e-4 (root mean square,
+ * relative) where fp32 weights give 2.0e-4 to 2.3e-4, a bf16 one by 1.6e-3 either
+ * way.  fp32 queries and their weights are taken as two fp16 terms (22 bits, down
+ * to 2^-38 of the largest weight).
  */
 PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_cache, const void* v_cache,
                                       const int32_t* block_tables, const int32_t* context_lens,
@@ -374,7 +384,9 @@ PKV_API pkv_status pkv_qk_norm_rope(const void* query, int64_t query_stride, con
  * pkv_qk_norm_rope whose keys, with their token's values, go straight into the
  * paged cache: the same bits as pkv_qk_norm_rope followed by
  * pkv_reshape_and_cache of its k_out (the keys are rounded to `dtype` first),
- * in one launch.
+ * in one launch.  Into FP8 and 4-bit caches that is the faster way for a step's
+ * tokens; for a prompt of some 1,000 tokens or more the two calls are (16,384
+ * tokens, 32 / 8 heads of 128: 72 us against 121 in 4 bits, 80 against 131 in FP8).
  *
  *   value         [num_tokens][num_kv_heads][head_dim], value_stride apart
  *   k_cache, v_cache, slot_mapping, block_size, num_blocks, kv_dtype, kv_scale

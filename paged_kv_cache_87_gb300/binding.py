@@ -2,9 +2,13 @@
 
 Argument marshalling only: shapes, dtypes and the stream are read off torch
 tensors and passed as plain pointers and sizes -- for the calls of a serving
-step in the extension module _marshal (csrc/host/marshal.cc), for the rest
-through ctypes; every step of the hot path runs in the library's CUDA kernels.  There is no CPU fallback: if the library
-cannot be loaded the calls raise.
+step in the extension module _marshal (csrc/host/marshal.cc, compiled for the torch that is
+installed), for the rest through ctypes; every step of the hot path runs in the library's CUDA
+kernels.  There is no CPU fallback: if the library or the module cannot be loaded the calls raise.
+
+Calls run on the current device, where their tensors have to be (the extension module refuses
+others), and on its current stream or the one given.  What a call allocates for a stream other
+than the current one is that stream's memory, held until the current stream is through too.
 
 Functions carry the C names:
   pkv_decode_workspace_bytes, pkv_paged_decode_attention,
@@ -258,6 +262,7 @@ def pkv_paged_decode_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cac
     query [S, Hq, d]; k_cache / v_cache [NB, Hkv, B, d] (float8_e4m3fn or uint8
     for FP8; uint8 of fp4_cache_shape for 4 bits); block_tables int32 [S, max_blocks]; context_lens int32 [S].
     ``workspace`` (uint8, >= pkv_decode_workspace_bytes) is allocated if None.
+    ``out`` has query's type, or is as many bytes in integers (larger ones are filled in part).
     ``prefix=True`` calls pkv_paged_decode_attention_prefix (shared prompts
     read once per group of sequences).
     """
@@ -420,7 +425,8 @@ def pkv_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch
                           v_cache: torch.Tensor, slot_mapping: torch.Tensor,
                           kv_scale: float = 1.0, stream=None) -> None:
     """k_cache[slot // B, h, slot % B] = key[t, h] (e4m3(x / kv_scale) for FP8 caches; codes
-    and scales for 4-bit caches, uint8 of fp4_cache_shape)."""
+    and scales for 4-bit caches, uint8 of fp4_cache_shape).  key and value have one element type,
+    and the two caches one; rows that are copied may have two, each its own cache's."""
     (_calls or _marshal()).write(key, value, k_cache, v_cache, slot_mapping, kv_scale,
                                  stream, False)
 
@@ -446,6 +452,7 @@ def pkv_gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     [S, max_blocks].  16- and 32-bit caches are copied (``out_dtype`` is theirs); FP8 and
     4-bit ones become values in any of float32, float16 and bfloat16.  Rows outside every
     sequence's range are left as they were (in outputs allocated here: uninitialised).
+    Two outputs allocated here share one storage: either keeps the memory of both.
     """
     return (_calls or _marshal()).gather(k_cache, v_cache, block_tables, row_start, total_rows,
                                          out_dtype, kv_scale, token_start, key_out, value_out, stream)
@@ -465,6 +472,7 @@ def pkv_qk_norm_rope(query: torch.Tensor, key: torch.Tensor, cos_sin: torch.Tens
     or float32; cos_sin float32 [max_position, rot_dim] holds each position's cosines, then
     sines; positions int64 [T].  ``interleaved`` rotates dims (2i, 2i + 1) instead of
     (i, i + rot_dim / 2).  q_out / k_out may be query / key themselves (in place).
+    Two outputs allocated here share one storage: either keeps the memory of both.
     """
     return (_calls or _marshal()).norm_rope(query, key, cos_sin, positions, q_weight, k_weight,
                                             eps, interleaved, q_out, k_out, stream)
@@ -479,7 +487,8 @@ def pkv_qk_norm_rope_and_cache(query: torch.Tensor, key: torch.Tensor, value: to
                                q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """pkv_qk_norm_rope whose keys, with ``value`` [T, Hkv, d], go into the paged cache at
     slot_mapping (int64 [T], negative: not written); returns q_out.  The cache, of any type,
-    holds the same bits as after pkv_qk_norm_rope and pkv_reshape_and_cache of its keys."""
+    holds the same bits as after pkv_qk_norm_rope and pkv_reshape_and_cache of its keys.  (Into
+    FP8 and 4 bits, those two are faster for prompts: 16,384 tokens 72 us against 121.)"""
     return (_calls or _marshal()).norm_rope_write(
         query, key, value, cos_sin, positions, k_cache, v_cache, slot_mapping, q_weight, k_weight,
         eps, interleaved, kv_scale, q_out, stream)

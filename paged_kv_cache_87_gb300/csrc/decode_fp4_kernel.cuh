@@ -46,6 +46,8 @@
 //   ragged (67 x 1 - 4k, 20 / 20 heads, d 64, blocks of 8): 26.6 us, 2.29 TB/s, 0.34: the units are
 //     short, and one costs 0.8 of a tile besides its tiles
 //   one context of 600 tokens: 6.3 us, latency (8.1 in equal runs with a joining kernel)
+//   sixteen query heads a kv head (long documents of 842 MB): 223 us, 0.56; fp32 queries over them: 204 us,
+//     0.61: twice the products for the same rows
 // Tried and not kept (each against the step of its time): four warps loading their own tokens by
 // 16-byte asynchronous copies, without a producer (237 against 160 us on long documents); no producer,
 // the last warp through with a stage filling it again (186 against 158); operands of q in registers

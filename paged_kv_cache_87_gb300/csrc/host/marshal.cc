@@ -3,7 +3,8 @@
 // The checks of shapes, types and strides, the outputs' and the workspace's allocation and the
 // call itself, in one extension function each.  They were Python: on the host of a GB300 an
 // attribute of a tensor costs 0.1 us there and a call 15 - 25 us in all, five times what the
-// kernels of a decode step take; here a call is 2 - 3.5 us, most of it the launch.
+// kernels of a decode step take; here the host's part is 2 - 3.5 us a call in a loop of nothing else
+// (a program that looks its tensors up between the calls: 4 - 6 us), most of it the launch.
 //
 // Arguments are positional (binding.py has the signatures and their documentation).  A wrong
 // tensor raises ValueError, an element type that the library does not know KeyError, and a
@@ -164,7 +165,8 @@ void call(const char* fn, F f) {
 // allocator keeps for `stream`: a block that the current stream has dropped may still have that
 // stream's work in flight, which `stream` does not wait for.  It is not given out again before
 // `stream`, and the current stream, where the caller reads it, have done what they hold when it is
-// dropped.  (Through at::empty, with its dispatch, a norm of one token took 4.1 us instead of 3.5.)
+// dropped.  (Through at::empty, with its dispatch, a norm of one token took the host 4.1 us
+// in such a loop instead of 3.5.)
 at::Tensor fresh(at::IntArrayRef shape, const at::TensorOptions& options, pkv_stream_t stream) {
     int64_t n = 1;
     for (int64_t v : shape) n *= v;
@@ -189,8 +191,9 @@ at::Tensor fresh(at::IntArrayRef shape, const at::TensorOptions& options, pkv_st
     return t;
 }
 
-// Two new tensors [rows, heads, d], one behind the other in one allocation (a second one is a
-// fifth of what such a call costs the host: norm of one token 5.2 us with two, 4.2 with one).
+// Two new tensors [rows, heads, d], one behind the other in one allocation, which they share: either
+// keeps the memory of both (a second one is a fifth of what such a call costs the host: norm of one
+// token 5.2 us with two, 4.2 with one).
 void fresh_pair(int64_t rows, int64_t heads0, int64_t heads1, int64_t d, const at::TensorOptions& options,
                 pkv_stream_t stream, at::Tensor* first, at::Tensor* second) {
     *first = fresh({rows * (heads0 + heads1) * d}, options, stream);

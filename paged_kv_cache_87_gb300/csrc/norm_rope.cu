@@ -3,9 +3,14 @@
 //
 // For a head row x: y = x / sqrt(mean(x^2) + eps) * w, then every pair (y_i, y_j) of the first
 // rot_dim dims is rotated by its angle.  One read and one write of every row: bound by HBM at
-// prompt sizes, by the launch at a decode step's.  Measured with the cache write, bf16, 32 / 8 heads,
-// d 128: 16,384 tokens 67 us (6.1 TB/s, 0.90 of the measured copy rate), 64 tokens 2.8 us; alone, f16,
-// 40 / 40 heads, d 64, 3,001 tokens 12.7 us (0.72).
+// prompt sizes, by the launch at a decode step's.  Measured with the write into a cache of the rows'
+// own type, bf16, 32 / 8 heads, d 128: 16,384 tokens 67 us (6.1 TB/s, 0.90 of the measured copy rate),
+// 64 tokens 2.8 us; alone, f16, 40 / 40 heads, d 64, 3,001 tokens 12.7 us (0.72).
+// Into a quantised cache the same takes 121 us in 4 bits (3.0 TB/s, 0.44) and 131 us in FP8 (0.43), 64
+// tokens 3.9 and 4.2: the query pieces are no other work, so what is beyond 67 us is the key and value
+// pieces', which a third of the warps do while the rest are through.  The two calls one after the other,
+// whose write gives every warp such a piece, take 72 and 80 us (64 tokens 4.2 and 5.3; 1,000 tokens in
+// 4 bits 9.5 against this call's 11.2).
 //
 // A lane holds eight dims of a row (d / 8 lanes a row) as two runs of four: the halves of four
 // pairs, so that the rotation stays in the lane (half-split: dims 4j .. and rot_dim / 2 + 4j ..;
