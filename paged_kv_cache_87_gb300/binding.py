@@ -226,12 +226,11 @@ def _fresh(like: torch.Tensor, stream, nbytes: int | None = None) -> torch.Tenso
     that the current stream has dropped may still have its work in flight -- and is held until the
     current stream, where the caller reads it, is through as well."""
     shape, dtype = (like.shape, like.dtype) if nbytes is None else ((nbytes,), torch.uint8)
-    now = torch.cuda.current_stream()
-    if stream is None or int(stream.cuda_stream) == now.cuda_stream:
+    if stream is None or int(stream.cuda_stream) == _stream_ptr(None):
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(_torch_stream(stream)):
         t = torch.empty(shape, dtype=dtype, device=like.device)
-    t.record_stream(now)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 

@@ -136,3 +136,50 @@ def test_swap_pairs_from_the_host_outlive_the_call(kind):
         want[0, b], want[1, b] = k[a].cpu(), v[a].cpu()
     assert len(trash) == 16 and torch.equal(hk, want[0]) and torch.equal(hv, want[1])
     assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_default_stream_asked_for_under_another_one(name):
+    """The other way round: work is current on a side stream, the call goes to the default one."""
+    call = step()[name]
+    ref = [t.clone() for t in call(None)]
+    side, default = torch.cuda.Stream(), torch.cuda.default_stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        x = [torch.full((t.untyped_storage().nbytes(),), 17, dtype=torch.uint8, device="cuda") for t in ref]
+        torch.cuda.synchronize()
+        seen = [drop_while_read(t) for t in x]
+        del x
+        out = call(default)
+        assert torch.cuda.current_stream() == side
+    torch.cuda.synchronize()
+    assert all((t == 17).all() for t in seen)
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_on_a_stream_that_joins_a_capture(name):
+    """Captured on a side stream of the graph's own, with memory of the graph's pool; two graphs."""
+    call = step()[name]
+    ref = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            side.wait_stream(torch.cuda.current_stream())
+            outs.append(call(side))
+            torch.cuda.current_stream().wait_stream(side)
+        graphs.append(graph)
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, ref))
+    assert binding.pkv_get_device_status() == 0
