@@ -186,6 +186,39 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
                                       pkv_stream_t stream);
 
 /*
+ * Decode under a sliding window, with the first tokens of the context kept in sight
+ * (attention sinks): pkv_paged_decode_attention over what is left of each context.
+ *
+ * The query of sequence s is the token at position n - 1 of its context of n =
+ * context_lens[s] tokens; with low = max(0, n - window) it attends to the tokens
+ * t >= low and to t < num_sinks:
+ *     out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) * v_t  over those t.
+ * Table entries of blocks that hold no such token are never read: a caller gives
+ * those blocks back and leaves what it likes in the table.  Cache rows that are
+ * not seen may hold anything (NaN), as may those past the context.
+ *
+ *   window     tokens, the query's own among them; at least 1 (INT_MAX: all)
+ *   num_sinks  tokens, at least 0
+ *   workspace  >= pkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned: of
+ *              the size that contexts of the window and the sinks need, however
+ *              long max_context_len is
+ *   the other arguments, types and errors as in pkv_paged_decode_attention (16-bit
+ *   queries over pools of 2^31 rows or more return PKV_ERR_UNSUPPORTED).
+ * Launches and rounding are those of pkv_paged_decode_attention.
+ */
+PKV_API size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                                 int head_dim, int block_size,
+                                                 int max_context_len, int window,
+                                                 int num_sinks, pkv_dtype kv_dtype);
+
+PKV_API pkv_status pkv_paged_decode_attention_window(
+    const void* query, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len, int window,
+    int num_sinks, float scale, pkv_dtype q_dtype, pkv_dtype kv_dtype, float kv_scale,
+    void* workspace, size_t workspace_bytes, void* out, pkv_stream_t stream);
+
+/*
  * Prefix-aware decode: the same result as pkv_paged_decode_attention (same
  * arguments, workspace size and errors), for batches in which sequences
  * share the physical blocks of a common prompt ("...Mathematical

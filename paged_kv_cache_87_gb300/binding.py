@@ -12,7 +12,8 @@ than the current one is that stream's memory, held until the current stream is t
 
 Functions carry the C names:
   pkv_decode_workspace_bytes, pkv_paged_decode_attention,
-  pkv_paged_decode_attention_prefix, pkv_paged_decode_attention_noalloc, pkv_reshape_and_cache, pkv_copy_blocks,
+  pkv_paged_decode_attention_prefix, pkv_paged_decode_attention_noalloc,
+  pkv_paged_decode_attention_window, pkv_reshape_and_cache, pkv_copy_blocks,
   pkv_gather_cache, pkv_qk_norm_rope, pkv_qk_norm_rope_and_cache,
   pkv_get_device_status, pkv_status_string, pkv_version,
 and the host block manager pkv_bm_* (wrapped by ``BlockManager``).
@@ -58,6 +59,9 @@ _SIGNATURES = {
                                                      ctypes.c_float, ctypes.c_void_p,
                                                      ctypes.c_size_t, ctypes.c_void_p,
                                                      ctypes.c_void_p]),
+    "pkv_decode_window_workspace_bytes": (ctypes.c_size_t, [_I] * 9),
+    "pkv_paged_decode_attention_window": (
+        ctypes.c_int, [_P] * 5 + [_I] * 10 + [_F, _I, _I, _F, _P, ctypes.c_size_t, _P, _P]),
     "pkv_multi_query_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int]),
     "pkv_paged_multi_query_attention": (
         ctypes.c_int,
@@ -268,6 +272,30 @@ def pkv_paged_decode_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cac
     return (_calls or _marshal()).decode(query, k_cache, v_cache, block_tables, context_lens,
                                          max_context_len, scale, kv_scale, workspace, out,
                                          stream, prefix, False)
+
+
+def pkv_decode_window_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                      head_dim: int, block_size: int, max_context_len: int,
+                                      window: int, sinks: int, kv_dtype) -> int:
+    return int(load().pkv_decode_window_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                        block_size, max_context_len, window, sinks,
+                                                        dtype_code(kv_dtype)))
+
+
+def pkv_paged_decode_attention_window(query: torch.Tensor, k_cache: torch.Tensor,
+                                      v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                      context_lens: torch.Tensor, max_context_len: int,
+                                      scale: float, window: int, sinks: int = 0,
+                                      kv_scale: float = 1.0,
+                                      workspace: torch.Tensor | None = None,
+                                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pkv_paged_decode_attention of queries that see only the last ``window`` tokens of their
+    context (their own among them) and its first ``sinks``.  Table entries of blocks that hold
+    none of these are never read: such blocks may have been given back.  ``workspace`` is of
+    pkv_decode_window_workspace_bytes; the other arguments are those of the plain call."""
+    return (_calls or _marshal()).decode_window(query, k_cache, v_cache, block_tables, context_lens,
+                                                max_context_len, scale, kv_scale, workspace, out,
+                                                stream, False, False, window, sinks)
 
 
 class PreparedCall:

@@ -168,7 +168,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
                        int num_blocks, int max_blocks_per_seq, int max_context_len, float scale,
                        pkv_dtype q_dtype, pkv_dtype kv_dtype, float kv_scale, void* workspace,
                        size_t workspace_bytes, void* out, pkv_stream_t stream,
-                       int allow_groups) {
+                       int allow_groups, int window = 0, int sinks = 0) {
     if (num_seqs < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
         return PKV_ERR_INVALID_ARG;
     if (q_dtype != PKV_F32 && q_dtype != PKV_F16 && q_dtype != PKV_BF16)
@@ -179,10 +179,12 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     const bool fp4 = kv_dtype == PKV_FP4_E2M1;
     Plan plan{};
     Fp4Plan fplan{};
+    // under a window the kernels walk virtual contexts: those bound the plan
+    const int max_seen = window ? window_most(max_context_len, window, sinks, block_size) : max_context_len;
     const pkv_status st = fp4 ? make_fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                              block_size, max_context_len, &fplan)
+                                              block_size, max_seen, &fplan)
                               : make_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                          block_size, max_context_len, &plan);
+                                          block_size, max_seen, &plan);
     if (st != PKV_OK) return st;
     if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size)
         return PKV_ERR_INVALID_ARG;
@@ -226,9 +228,16 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
         f.num_blocks = num_blocks;
         f.max_blocks = max_blocks_per_seq;
         f.max_context_len = max_context_len;
+        f.window = window;
+        f.sinks = sinks;
+        f.max_seen = max_seen;
         f.qk_scale_log2 = scale * 1.4426950408889634f * kv_scale;
         f.out_scale = kv_scale;
         cudaStream_t fs = reinterpret_cast<cudaStream_t>(stream);
+        if (window)
+            return cuda_status(q_dtype == PKV_F32   ? decode_fp4_window_f32(f, fs)
+                               : q_dtype == PKV_F16 ? decode_fp4_window_f16(f, fs)
+                                                    : decode_fp4_window_bf16(f, fs));
         return cuda_status(q_dtype == PKV_F32   ? decode_fp4_f32(f, fs)
                            : q_dtype == PKV_F16 ? decode_fp4_f16(f, fs)
                                                 : decode_fp4_bf16(f, fs));
@@ -266,6 +275,10 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.max_context_len = max_context_len;
+    p.window = window;
+    p.sinks = sinks;
+    p.max_seen = max_seen;
+    p.log_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.chunk_tokens = plan.chunk_tokens;
     p.max_chunks = plan.max_chunks;
     p.part_stride = plan.part_stride;
@@ -280,13 +293,19 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     const bool mma = (q_dtype == PKV_F16 || q_dtype == PKV_BF16) &&
                      (kv_dtype == q_dtype || (kv_dtype == PKV_FP8_E4M3 && head_dim == 128)) &&
                      (int64_t)num_blocks * num_kv_heads * block_size <= 0x7fffffffLL;
+    if (window && !mma && q_dtype != PKV_F32 && !(kv_dtype == PKV_FP8_E4M3 && head_dim == 64))
+        return PKV_ERR_UNSUPPORTED;          // 2^31 rows or more
     const int hpi = mma ? kMmaHeadsPerItem : plan.hpi;
     p.nsub = (plan.group + hpi - 1) / hpi;   // never above plan.nsub: the workspace fits
     // CUDA-core path with every context within one chunk: no split, no merge, so the
     // decode kernel takes its work items straight from the sequence index (one launch)
-    p.self_plan = !mma && max_context_len <= plan.chunk_tokens;
+    p.self_plan = !mma && max_seen <= plan.chunk_tokens;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (window)
+        return cuda_status(q_dtype == PKV_F32   ? decode_window_f32(p, kv_dtype, hpi, s)
+                           : q_dtype == PKV_F16 ? decode_window_f16(p, kv_dtype, hpi, s)
+                                                : decode_window_bf16(p, kv_dtype, hpi, s));
     switch (q_dtype) {
     case PKV_F32: err = decode_dispatch_f32(p, kv_dtype, hpi, s); break;
     case PKV_F16: err = decode_dispatch_f16(p, kv_dtype, hpi, s); break;
@@ -323,6 +342,32 @@ pkv_status pkv_paged_decode_attention_prefix(
                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                        max_blocks_per_seq, max_context_len, scale, q_dtype, kv_dtype, kv_scale,
                        workspace, workspace_bytes, out, stream, 1);
+}
+
+size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int block_size, int max_context_len,
+                                         int window, int num_sinks, pkv_dtype kv_dtype) {
+    if (window < 1 || num_sinks < 0 || max_context_len < 0 ||
+        (block_size != 8 && block_size != 16 && block_size != 32))
+        return 0;
+    return pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                      window_most(max_context_len, window, num_sinks, block_size),
+                                      kv_dtype);
+}
+
+pkv_status pkv_paged_decode_attention_window(
+    const void* query, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len, int window,
+    int num_sinks, float scale, pkv_dtype q_dtype, pkv_dtype kv_dtype, float kv_scale,
+    void* workspace, size_t workspace_bytes, void* out, pkv_stream_t stream) {
+    if (window < 1 || num_sinks < 0) return PKV_ERR_INVALID_ARG;
+    if (block_size != 8 && block_size != 16 && block_size != 32)
+        return block_size <= 0 ? PKV_ERR_INVALID_ARG : PKV_ERR_UNSUPPORTED;
+    return decode_impl(query, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                       max_blocks_per_seq, max_context_len, scale, q_dtype, kv_dtype, kv_scale,
+                       workspace, workspace_bytes, out, stream, 0, window, num_sinks);
 }
 
 pkv_status pkv_reshape_and_cache(const void* key, const void* value, void* k_cache,

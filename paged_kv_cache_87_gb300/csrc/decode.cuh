@@ -33,6 +33,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "window_span.cuh"
 
 namespace pkv {
 
@@ -86,6 +87,10 @@ struct DecodeParams {
                           // its split units are merged by a separate merge kernel
     int self_plan;        // CUDA-core path, every context within one chunk: no planning
                           // kernel; work item w is (sequence w / units, unit w % units)
+    int window, sinks;    // sliding window and first tokens that stay visible (0: no window); the
+                          // planner and the kernels walk the virtual contexts of window_span.cuh
+    int max_seen;         // tokens of a virtual context, at most (max_context_len without a window)
+    int log_block;        // block_size == 1 << log_block
     float qk_scale_log2;  // scale * log2(e) (* kv_scale for FP8)
     float out_scale;      // kv_scale for FP8, else 1
 };
@@ -113,6 +118,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(DecodeParams p) {
                 set_status(p.status, PKV_DEV_BAD_CONTEXT);
                 ctx = ctx < 0 ? 0 : cap;
             }
+            if (p.window) ctx = window_span(ctx, p.window, p.sinks, p.log_block).tokens;
             p.ws.ctx_eff[s] = ctx;
             n = (ctx + C - 1) / C;
         }
@@ -190,7 +196,8 @@ struct StageMeta {
     int ts, te;                 // logical tokens [ts, te) held by this stage
     int flags;                  // kFirst | kLast | kDone
     int expect, segoff;         // private unit: partial states merged, first private one
-    int pad[5];
+    int hide_lo, hide_hi;       // under a window: hidden tokens [hide_lo, hide_hi)
+    int pad[3];
 };
 constexpr int kFirst = 1, kLast = 2, kDone = 4, kGroup = 8;
 
@@ -309,7 +316,8 @@ __device__ __forceinline__ void finish_item(const DecodeParams& p, const StageMe
     named_bar_sync(1, NT);   // scratch and misc are reused by the next item
 }
 
-template <typename QT, typename KT, int HD, int HPI>
+// WIN: contexts under a sliding window (p.window, p.sinks).
+template <typename QT, typename KT, int HD, int HPI, bool WIN = false>
 __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
     decode_simt_kernel(DecodeParams p) {
     using Cfg = SimtCfg<QT, KT, HD, HPI>;
@@ -353,13 +361,16 @@ __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
             const int it = (int)(w / units_per_item), rem = (int)(w % units_per_item);
             const int kvh = rem / p.nsub, qsub = rem % p.nsub;
             int s, chunk, ctx, e0, e1;
+            WindowSpan span{};
             if (p.self_plan) {
                 // one chunk per sequence: the table's first entries load beside the length
                 s = it;
                 chunk = 0;
-                const int32_t* trow = p.block_tables + (int64_t)s * p.max_blocks;
-                e0 = lane < p.max_blocks ? trow[lane] : 0;
-                e1 = lane + 32 < p.max_blocks ? trow[lane + 32] : 0;
+                if constexpr (!WIN) {
+                    const int32_t* trow = p.block_tables + (int64_t)s * p.max_blocks;
+                    e0 = lane < p.max_blocks ? trow[lane] : 0;
+                    e1 = lane + 32 < p.max_blocks ? trow[lane + 32] : 0;
+                }
                 ctx = p.context_lens[s];
                 const int cap = min(p.max_context_len, p.max_blocks * B);
                 if (ctx < 0 || ctx > cap) {
@@ -381,10 +392,21 @@ __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
                 chunk = sc.y;
                 ctx = p.ws.ctx_eff[s];
             }
+            if constexpr (WIN) {
+                int raw = p.context_lens[s];
+                const int cap = min(p.max_context_len, p.max_blocks * B);
+                raw = raw < 0 ? 0 : (raw > cap ? cap : raw);
+                span = window_span(raw, p.window, p.sinks, p.log_block);
+                ctx = span.tokens;
+            }
             const int nchunks = (ctx + C - 1) / C;
             const int t0 = chunk * C, t1 = min(t0 + C, ctx);
             const int jb0 = t0 / B, nb = (t1 + B - 1) / B - jb0;
-            if (!p.self_plan) {
+            if constexpr (WIN) {
+                const int32_t* trow = p.block_tables + (int64_t)s * p.max_blocks;
+                e0 = lane < nb ? trow[window_entry(span, jb0 + lane)] : 0;
+                e1 = lane + 32 < nb ? trow[window_entry(span, jb0 + lane + 32)] : 0;
+            } else if (!p.self_plan) {
                 const int32_t* trow = p.block_tables + (int64_t)s * p.max_blocks;
                 e0 = lane < nb ? trow[jb0 + lane] : 0;
                 e1 = lane + 32 < nb ? trow[jb0 + lane + 32] : 0;
@@ -412,6 +434,7 @@ __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
                     StageMeta& m = metas[stage];
                     m.s = s; m.kvh = kvh; m.qsub = qsub; m.nh = nh;
                     m.chunk = chunk; m.nchunks = nchunks; m.ts = ts; m.te = te;
+                    if constexpr (WIN) { m.hide_lo = span.hide_lo; m.hide_hi = span.hide_hi; }
                     m.flags = (st == 0 ? kFirst : 0) | (st == nstages - 1 ? kLast : 0);
                     mbar_arrive_expect_tx(&full[stage],
                                           2u * (uint32_t)(te - ts) * Cfg::ROWB + qbytes);
@@ -499,6 +522,9 @@ __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
         }
 
         const int ntok = meta.te - meta.ts;
+        auto seen = [&](int tl) {        // whether the stage's token tl counts
+            return tl < ntok && (!WIN || meta.ts + tl < meta.hide_lo || meta.ts + tl >= meta.hide_hi);
+        };
         float sc[TPG][HPI];
 #pragma unroll
         for (int i = 0; i < TPG; ++i) {
@@ -536,7 +562,7 @@ __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
             float v = -INFINITY;
 #pragma unroll
             for (int i = 0; i < TPG; ++i)
-                if (i * NG + gid < ntok) v = fmaxf(v, sc[i][h]);
+                if (seen(i * NG + gid)) v = fmaxf(v, sc[i][h]);
             smax[h] = v;
             need |= v > m[h] + kRescaleSlack;
         }
@@ -555,7 +581,7 @@ __global__ void __launch_bounds__(SimtCfg<QT, KT, HD, HPI>::THREADS, 2)
 #pragma unroll
         for (int i = 0; i < TPG; ++i) {
             const int tl = i * NG + gid;
-            if (tl < ntok) {
+            if (seen(tl)) {
                 float pr[HPI];
 #pragma unroll
                 for (int h = 0; h < HPI; ++h) {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "window_span.cuh"
 
 namespace pkv {
 
@@ -46,6 +47,8 @@ struct DecodeFp4Params {
     int num_seqs, num_q_heads, num_kv_heads, group, nsub, unit_heads;
     int head_dim, block_size, num_blocks, max_blocks;
     int max_context_len;   // at most max_blocks * block_size
+    int window, sinks;     // sliding window and first tokens that stay visible (0: no window)
+    int max_seen;          // tokens of a virtual context (window_span.cuh), at most; else max_context_len
     int log_block;         // block_size == 1 << log_block
     int workers;           // the split's denominator: every CTA the device holds
     int max_workers;       // workers that can have work, by max_context_len
@@ -69,5 +72,10 @@ inline int64_t fp4_max_workers(int num_seqs, int num_kv_heads, int nsub, int uni
 cudaError_t decode_fp4_f32(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_f16(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_bf16(const DecodeFp4Params& p, cudaStream_t s);
+
+// The same under a sliding window (decode_fp4_window_*.cu).
+cudaError_t decode_fp4_window_f32(const DecodeFp4Params& p, cudaStream_t s);
+cudaError_t decode_fp4_window_f16(const DecodeFp4Params& p, cudaStream_t s);
+cudaError_t decode_fp4_window_bf16(const DecodeFp4Params& p, cudaStream_t s);
 
 }  // namespace pkv

@@ -189,28 +189,50 @@ struct Cfg {
 
 constexpr int kFirst = 1, kLast = 2, kDone = 4;
 
-// Tiles of a sequence's context, per unit.
-__device__ __forceinline__ int tiles_of(const DecodeFp4Params& p, int s) {
+// Tokens of a tile, from the first word of its record.
+template <bool WIN>
+__device__ __forceinline__ int tile_tokens(int x) { return WIN ? x >> 8 & 255 : x >> 8; }
+
+// The hidden tokens of a tile of sequence s, in the bits of that word: [first, end).
+__device__ __forceinline__ int hidden_of(const DecodeFp4Params& p, int s, int tile) {
+    const WindowSpan w = window_span(min(p.context_lens[s], p.max_context_len), p.window, p.sinks, p.log_block);
+    const int lo = min(max(w.hide_lo - tile * kFp4Tile, 0), kFp4Tile);
+    const int hi = min(max(w.hide_hi - tile * kFp4Tile, 0), kFp4Tile);
+    return (int)((uint32_t)lo << 16 | (uint32_t)hi << 24);
+}
+
+// Tokens of a sequence's context that are walked: under a window (WIN) its virtual context's.
+template <bool WIN>
+__device__ __forceinline__ int tokens_of(const DecodeFp4Params& p, int s) {
     const int n = min(p.context_lens[s], p.max_context_len);
+    if constexpr (WIN) return n <= 0 ? 0 : window_span(n, p.window, p.sinks, p.log_block).tokens;
+    return n;
+}
+
+// Tiles of a sequence's context, per unit.
+template <bool WIN>
+__device__ __forceinline__ int tiles_of(const DecodeFp4Params& p, int s) {
+    const int n = tokens_of<WIN>(p, s);
     return n <= 0 ? 0 : (n - 1) / kFp4Tile + 1;          // (n + 127 would pass 31 bits)
 }
 
 // A unit's length in the plan, in slots: its tiles and, before them, kFp4UnitCost slots that
 // stand for what a unit costs besides (its queries, the warps' meeting at its end).
+template <bool WIN>
 __device__ __forceinline__ int slots_of(const DecodeFp4Params& p, int s) {
-    const int n = tiles_of(p, s);
+    const int n = tiles_of<WIN>(p, s);
     return n ? n + kFp4UnitCost : 0;
 }
 
 // Block-wide scan of the sequences' slots: pref[i] = slots of the sequences before thread i's run
 // of ceil(S / threads), pref[threads] = all, pref[threads + 1] = the longest.  Syncs the block.
-template <int THREADS>
+template <int THREADS, bool WIN>
 __device__ __forceinline__ void scan_slots(const DecodeFp4Params& p, int* pref, int2* wsum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (p.num_seqs + THREADS - 1) / THREADS;
     int n = 0, most = 0;
     for (int s = tid * run; s < min(p.num_seqs, (tid + 1) * run); ++s) {
-        const int k = slots_of(p, s);
+        const int k = slots_of<WIN>(p, s);
         n += k;
         most = max(most, k);
     }
@@ -241,7 +263,7 @@ __device__ __forceinline__ void scan_slots(const DecodeFp4Params& p, int* pref, 
 
 // Place of flattened slot `pos` (below the total): its sequence, that sequence's slots a unit, and
 // the position of the sequence's first slot.
-template <int THREADS>
+template <int THREADS, bool WIN>
 __device__ __forceinline__ void locate(const DecodeFp4Params& p, const int* pref, int upi, int pos,
                                        int* seq, int* slots, int* base) {
     int lo = 0, hi = THREADS - 1;
@@ -251,10 +273,10 @@ __device__ __forceinline__ void locate(const DecodeFp4Params& p, const int* pref
         else hi = mid - 1;
     }
     const int run = (p.num_seqs + THREADS - 1) / THREADS;
-    int s = lo * run, b = pref[lo] * upi, n = slots_of(p, s);
+    int s = lo * run, b = pref[lo] * upi, n = slots_of<WIN>(p, s);
     while (b + n * upi <= pos) {
         b += n * upi;
-        n = slots_of(p, ++s);
+        n = slots_of<WIN>(p, ++s);
     }
     *seq = s;
     *slots = n;
@@ -270,7 +292,9 @@ __device__ __forceinline__ int quota_of(const DecodeFp4Params& p, int total, int
 
 // CLUSTER: a cluster of 1 << p.log_cluster CTAs takes one unit, a run of its tiles each, and joins its
 // own states through distributed shared memory (a lone CTA writes its unit straight to `out`).
-template <typename QT, int HD, int NT, bool CLUSTER>
+// WIN: contexts under a sliding window: the tiles are those of the virtual contexts of window_span.cuh,
+// and the hidden tokens in them are masked like those past the context.
+template <typename QT, int HD, int NT, bool CLUSTER, bool WIN>
 __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     decode_fp4_kernel(DecodeFp4Params p, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
@@ -281,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 127u);
     __shared__ int s_pref[kThreads + 2];
     __shared__ int2 s_wsum[kThreads / 32];
-    // of a tile: {flags | tokens << 8, sequence, unit, partial state or -1: the whole unit is here}
+    // of a tile: {flags | tokens << 8 (WIN: | hidden tokens' first << 16, end << 24), sequence, unit, partial state or -1: the whole unit is here}
     int4* metas = reinterpret_cast<int4*>(smem + C::OFF_META);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     uint64_t* empty = full + C::NSTAGE;
@@ -300,12 +324,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     int a, end, q = 1;          // this CTA's slots (CLUSTER: tiles of its unit), the slots of each CTA
     const int my_unit = blockIdx.x >> p.log_cluster, rank = blockIdx.x & ((1 << p.log_cluster) - 1);
     if constexpr (CLUSTER) {
-        const int n = tiles_of(p, my_unit / upi);
+        const int n = tiles_of<WIN>(p, my_unit / upi);
         a = n * rank >> p.log_cluster;
         end = n * (rank + 1) >> p.log_cluster;
         __syncthreads();                           // the barriers are visible
     } else {
-        scan_slots<kThreads>(p, s_pref, s_wsum);   // and the barriers are visible
+        scan_slots<kThreads, WIN>(p, s_pref, s_wsum);   // and the barriers are visible
         const int total = s_pref[kThreads] * upi;
         q = quota_of(p, total, s_pref[kThreads + 1]);
         a = min(blockIdx.x * q, total);
@@ -327,7 +351,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
         int* plan_row = reinterpret_cast<int*>(plan_at + 32);          // [32][16] pool rows
         // a pool row is a whole tile of 8 or 16 tokens, or half of a tile of 32
         const int log_rt = min(logB, 4), per_block = logB - log_rt, log_rows = 7 - log_rt;
-        const int cap = p.max_context_len;
         if (!CLUSTER && lane == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
         __syncwarp();
         for (int pos0 = a; pos0 < end; pos0 += 32) {
@@ -337,20 +360,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
             if (CLUSTER && pos < end) {
                 const int s = my_unit / upi, u = my_unit % upi;
                 m = make_int4((pos == a ? kFirst : 0) | (pos == end - 1 ? kLast : 0) |
-                                  min(kFp4Tile, min(p.context_lens[s], cap) - pos * kFp4Tile) << 8,
+                                  min(kFp4Tile, tokens_of<WIN>(p, s) - pos * kFp4Tile) << 8 |
+                                  (WIN ? hidden_of(p, s, pos) : 0),
                               s, u, p.log_cluster ? 0 : -1);
                 plan_at[lane] = make_int2(pos, u / p.nsub);
             }
             if (!CLUSTER && pos < end) {
                 int s, n, base;
-                locate<kThreads>(p, s_pref, upi, pos, &s, &n, &base);
+                locate<kThreads, WIN>(p, s_pref, upi, pos, &s, &n, &base);
                 const int u = (pos - base) / n, at = (pos - base) % n, tile = at - kFp4UnitCost;
                 if (tile >= 0) {
                     const int dstart = pos - tile, uend = pos - at + n;
                     uend_of = uend;
-                    const int tokens = min(kFp4Tile, min(p.context_lens[s], cap) - tile * kFp4Tile);
+                    const int tokens = min(kFp4Tile, tokens_of<WIN>(p, s) - tile * kFp4Tile);
                     m = make_int4((tile == 0 || pos == a ? kFirst : 0) |
-                                      (at == n - 1 || pos == end - 1 ? kLast : 0) | tokens << 8,
+                                      (at == n - 1 || pos == end - 1 ? kLast : 0) | tokens << 8 |
+                                      (WIN ? hidden_of(p, s, tile) : 0),
                                   s, u, dstart < a ? 0 : uend > end ? 1 : -1);
                     plan_at[lane] = make_int2(tile, u / p.nsub);
                 }
@@ -367,8 +392,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 const int4 t = plan[l];
                 if (t.x == 0) continue;
                 const int2 w = plan_at[l];
-                const int blocks = ((t.x >> 8) + B - 1) >> logB, k = min(r, (blocks << per_block) - 1);
-                int blk = p.block_tables[(int64_t)t.y * p.max_blocks + ((w.x * kFp4Tile) >> logB) + (k >> per_block)];
+                const int blocks = (tile_tokens<WIN>(t.x) + B - 1) >> logB, k = min(r, (blocks << per_block) - 1);
+                int at = ((w.x * kFp4Tile) >> logB) + (k >> per_block);
+                if constexpr (WIN)
+                    at = window_entry(window_span(min(p.context_lens[t.y], p.max_context_len), p.window, p.sinks,
+                                                  logB), at);
+                int blk = p.block_tables[(int64_t)t.y * p.max_blocks + at];
                 if (blk < 0 || blk >= p.num_blocks) {   // block 0 in its place, as every decode here
                     set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
                     blk = 0;
@@ -388,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                     const int kvh = plan_at[l].y, qsub = t.z - kvh * p.nsub;
                     uint8_t* sb = smem + stage * C::STAGE_BYTES;
                     // 32 or 64 tokens a gather; those past the context's last block stay out
-                    const int per = 4 << log_rt, gathers = ((t.x >> 8) + per - 1) >> (log_rt + 2);
+                    const int per = 4 << log_rt, gathers = (tile_tokens<WIN>(t.x) + per - 1) >> (log_rt + 2);
                     uint32_t bytes = 2u * C::ROWB * per * gathers;
                     const uint32_t qbytes = min(HEADS, p.group - qsub * HEADS) * (HD * QT::bytes);
                     if (t.x & kFirst) bytes += qbytes;
@@ -464,10 +493,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
     int stage = 0;
     uint32_t phase = 0;
 
-    // One tile: SUB pieces of 16 tokens, 64 apart, nv tokens from the first of them on.
-    auto attend = [&](auto pieces, const uint8_t* sb, int nv) {
+    // One tile: SUB pieces of 16 tokens, 64 apart, nv tokens from the first of them on, of which
+    // (WIN) [ha, hb) are hidden.
+    auto attend = [&](auto pieces, const uint8_t* sb, int nv, int ha, int hb) {
         constexpr int SUB = decltype(pieces)::value;
-        const bool part = nv < 64 * SUB - 48;         // some of the tokens are not valid
+        // some of the tokens are not valid
+        const bool part = nv < 64 * SUB - 48 || (WIN && ha < hb && hb > 0 && ha < 64 * SUB - 48);
+        auto valid = [&](int t) { return t < nv && (!WIN || t < ha || t >= hb); };
         // ---- S^T = K Q^T ----
         float sa[SUB][NT][4];
         uint32_t da[SUB], db[SUB];     // this lane's scale byte of every chunk, rows g and g + 8
@@ -539,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                     for (int u = 0; u < SUB; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (g + (i & 2) * 4 >= nv - 64 * u) y[u][i] = -INFINITY;
+                            if (!valid(g + (i & 2) * 4 + 64 * u)) y[u][i] = -INFINITY;
                 sum[0] = sum[1] = 0.f;
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
@@ -556,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (g + (i & 2) * 4 < nv - 64 * u) t[i & 1] = fmaxf(t[i & 1], sa[u][nt][i] * qs[nt][i & 1]);
+                        if (valid(g + (i & 2) * 4 + 64 * u)) t[i & 1] = fmaxf(t[i & 1], sa[u][nt][i] * qs[nt][i & 1]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], off));
@@ -607,11 +639,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
                 va[1] = va[3] = vb[1] = vb[3] = 0u;
             }
             if (part) {   // rows past the context may hold anything: scale 0 (codes are finite)
-                const int left = nv - 64 * u;
-                if (2 * c >= left) va[0] = va[1] = 0u;
-                if (2 * c + 1 >= left) va[2] = va[3] = 0u;
-                if (2 * c + 8 >= left) vb[0] = vb[1] = 0u;
-                if (2 * c + 9 >= left) vb[2] = vb[3] = 0u;
+                if (!valid(64 * u + 2 * c)) va[0] = va[1] = 0u;
+                if (!valid(64 * u + 2 * c + 1)) va[2] = va[3] = 0u;
+                if (!valid(64 * u + 2 * c + 8)) vb[0] = vb[1] = 0u;
+                if (!valid(64 * u + 2 * c + 9)) vb[2] = vb[3] = 0u;
             }
 #pragma unroll
             for (int cp = 0; cp < C::NCHUNK / 2; ++cp) {
@@ -725,13 +756,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<QT, HD, NT>::CTAS))
             // the operands are whole; the unit before is done with its own (it met at its end)
             named_bar_sync(1, kConsumers * 32);
         }
-        const int nv = (meta.x >> 8) - 16 * warp;   // tokens of the tile from this warp's first on
+        const int nv = tile_tokens<WIN>(meta.x) - 16 * warp;   // tokens of the tile from this warp's first on
+        const int ha = WIN ? (meta.x >> 16 & 255) - 16 * warp : 0;
+        const int hb = WIN ? (int)((uint32_t)meta.x >> 24) - 16 * warp : 0;
         if constexpr (C::PIECES == 2) {
-            if (nv > 64) attend(std::integral_constant<int, 2>(), sb, nv);
-            else if (nv > 0) attend(std::integral_constant<int, 1>(), sb, nv);
+            if (nv > 64) attend(std::integral_constant<int, 2>(), sb, nv, ha, hb);
+            else if (nv > 0) attend(std::integral_constant<int, 1>(), sb, nv, ha, hb);
         } else {
             for (int u = 0; u < 2; ++u)
-                if (nv > 64 * u) attend(std::integral_constant<int, 1>(), sb + u * SUB_BYTES, nv - 64 * u);
+                if (nv > 64 * u)
+                    attend(std::integral_constant<int, 1>(), sb + u * SUB_BYTES, nv - 64 * u, ha - 64 * u, hb - 64 * u);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
@@ -937,7 +971,7 @@ __global__ void __launch_bounds__(THREADS) merge_fp4_kernel(DecodeFp4Params p) {
     }
 }
 
-template <typename QT, int HD, int NT, bool CLUSTER>
+template <typename QT, int HD, int NT, bool CLUSTER, bool WIN>
 cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     using C = Cfg<QT, HD, NT>;
     static int workers[64] = {0};          // CTAs the device holds at once
@@ -945,7 +979,7 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = decode_fp4_kernel<QT, HD, NT, CLUSTER>;
+    auto kernel = decode_fp4_kernel<QT, HD, NT, CLUSTER, WIN>;
     if (workers[dev] == 0) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
         if (err != cudaSuccess) return err;
@@ -1001,7 +1035,7 @@ cudaError_t launch(const DecodeFp4Params& p0, cudaStream_t stream) {
 }
 
 // Clusters of 1 << log_size CTAs that the device holds at once.
-template <typename QT, int HD, int NT>
+template <typename QT, int HD, int NT, bool WIN>
 cudaError_t resident_clusters(int log_size, int* most) {
     using C = Cfg<QT, HD, NT>;
     static int known[4][64] = {{0}};       // and one, once asked for
@@ -1011,7 +1045,7 @@ cudaError_t resident_clusters(int log_size, int* most) {
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (clusters[dev] == 0) {
-        auto kernel = decode_fp4_kernel<QT, HD, NT, true>;
+        auto kernel = decode_fp4_kernel<QT, HD, NT, true, WIN>;
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
         if (err != cudaSuccess) return err;
         cudaLaunchAttribute dim[1];
@@ -1033,28 +1067,28 @@ cudaError_t resident_clusters(int log_size, int* most) {
     return cudaSuccess;
 }
 
-template <typename QT, int HD, int NT>
+template <typename QT, int HD, int NT, bool WIN>
 cudaError_t launch_units(const DecodeFp4Params& p, cudaStream_t stream) {
     const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
-    const int64_t tiles = ((int64_t)p.max_context_len + kFp4Tile - 1) / kFp4Tile;
+    const int64_t tiles = ((int64_t)p.max_seen + kFp4Tile - 1) / kFp4Tile;
     for (int log_size = tiles > 4 ? 3 : tiles > 2 ? 2 : tiles > 1; log_size >= 0; --log_size) {
         if (tiles > (log_size == 3 ? 8 : kFp4ClusterTiles) << log_size || units > kFp4MaxWorkers) continue;
         int most = 0;
-        const cudaError_t err = resident_clusters<QT, HD, NT>(log_size, &most);
+        const cudaError_t err = resident_clusters<QT, HD, NT, WIN>(log_size, &most);
         if (err != cudaSuccess) return err;
         if (units > most) continue;
         DecodeFp4Params of_clusters = p;
         of_clusters.log_cluster = log_size;
-        return launch<QT, HD, NT, true>(of_clusters, stream);
+        return launch<QT, HD, NT, true, WIN>(of_clusters, stream);
     }
-    return launch<QT, HD, NT, false>(p, stream);
+    return launch<QT, HD, NT, false, WIN>(p, stream);
 }
 
-template <typename QT>
+template <typename QT, bool WIN = false>
 cudaError_t launch_decode_fp4(const DecodeFp4Params& p, cudaStream_t stream) {
     if (p.unit_heads == 16)
-        return p.head_dim == 128 ? launch_units<QT, 128, 2>(p, stream) : launch_units<QT, 64, 2>(p, stream);
-    return p.head_dim == 128 ? launch_units<QT, 128, 1>(p, stream) : launch_units<QT, 64, 1>(p, stream);
+        return p.head_dim == 128 ? launch_units<QT, 128, 2, WIN>(p, stream) : launch_units<QT, 64, 2, WIN>(p, stream);
+    return p.head_dim == 128 ? launch_units<QT, 128, 1, WIN>(p, stream) : launch_units<QT, 64, 1, WIN>(p, stream);
 }
 
 }  // namespace

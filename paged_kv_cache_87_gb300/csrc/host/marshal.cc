@@ -242,8 +242,8 @@ PyObject* translated() {
 // decode(query, k_cache, v_cache, block_tables, context_lens, max_context_len, scale, kv_scale,
 //        workspace, out, stream, prefix, prepare): out; with `prepare` nothing is launched and the
 // result is (the C call's arguments, workspace, out).
-PKV_ENTRY(decode) {
-    count(n, 13);
+// With a window (decode_window) two arguments more follow: window, sinks.
+PyObject* decode_call(PyObject* const* a, bool windowed) {
     const char* plain = "query, caches, tables and lengths must be contiguous CUDA tensors";
     const at::Tensor &q = tensor(a[0]), &k = tensor(a[1]), &v = tensor(a[2]), &bt = tensor(a[3]),
                      &cl = tensor(a[4]);
@@ -270,12 +270,17 @@ PKV_ENTRY(decode) {
              "out must have query's size and type, or be that many bytes in integers");
     }
     const bool prefix = truth(a[11]);
+    const int window = windowed ? int32(a[13], "window does not fit in 32 bits") : 0;
+    const int sinks = windowed ? int32(a[14], "sinks does not fit in 32 bits") : 0;
     const pkv_dtype qt = code_of(q.scalar_type());
     const bool prepare = truth(a[12]);
     size_t ws_bytes = 0;
     auto take = [&] {
         if (!ws.defined()) {
-            const size_t bytes = pkv_decode_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, c.type);
+            const size_t bytes =
+                windowed ? pkv_decode_window_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, window,
+                                                             sinks, c.type)
+                         : pkv_decode_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, c.type);
             ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
         }
         if (!out.defined()) out = fresh(q.sizes(), q.options(), stream);
@@ -292,6 +297,17 @@ PKV_ENTRY(decode) {
             (unsigned long long)out.data_ptr(), (unsigned long long)stream,
             THPVariable_Wrap(ws), THPVariable_Wrap(out));
     }
+    if (windowed) {
+        call("pkv_paged_decode_attention_window", [&] {
+            take();
+            return pkv_paged_decode_attention_window(
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const int32_t*>(bt.data_ptr()),
+                static_cast<const int32_t*>(cl.data_ptr()), S, Hq, c.heads, c.d, c.block, c.blocks, width,
+                max_ctx, window, sinks, scale, qt, c.type, kv_scale, ws.data_ptr(), ws_bytes,
+                out.data_ptr(), stream);
+        });
+        return THPVariable_Wrap(std::move(out));
+    }
     auto* fn = prefix ? pkv_paged_decode_attention_prefix : pkv_paged_decode_attention;
     call(prefix ? "pkv_paged_decode_attention_prefix" : "pkv_paged_decode_attention", [&] {
         take();
@@ -302,6 +318,18 @@ PKV_ENTRY(decode) {
                   out.data_ptr(), stream);
     });
     return THPVariable_Wrap(std::move(out));
+}
+
+PKV_ENTRY(decode) {
+    count(n, 13);
+    return decode_call(a, false);
+}
+
+// decode_window(the arguments of decode, window, sinks): out (nothing is prepared)
+PKV_ENTRY(decode_window) {
+    count(n, 15);
+    need(!truth(a[12]) && !truth(a[11]), "a windowed decode has neither a prefix form nor a prepared one");
+    return decode_call(a, true);
 }
 
 // write(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream, prepare): None, or the C
@@ -520,7 +548,7 @@ PyObject* set_error(PyObject*, PyObject* type) {
 }
 
 #define PKV_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {PKV_FAST(decode), PKV_FAST(write), PKV_FAST(gather), PKV_FAST(norm_rope),
+PyMethodDef g_methods[] = {PKV_FAST(decode), PKV_FAST(decode_window), PKV_FAST(write), PKV_FAST(gather), PKV_FAST(norm_rope),
                            PKV_FAST(norm_rope_write), {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods,
