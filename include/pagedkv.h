@@ -320,6 +320,54 @@ PKV_API pkv_status pkv_paged_tree_attention(
     pkv_stream_t stream);
 
 /*
+ * Attention of a chunk of new tokens over a paged cache of any 16-bit, FP8 or 4-bit type: a
+ * prompt, a part of one, a chain of draft tokens or a mixed step (single tokens among them), with
+ * or without a sliding window and sinks.
+ *
+ * Sequence s owns query rows query_start[s] .. query_start[s + 1] - 1 (n_s rows), the last n_s of
+ * its context_lens[s] cached tokens.  Row i of them is the token at position p = context_lens[s]
+ * - n_s + i, and for each query head h
+ *   out[row][h] = sum_t softmax_t(scale * q[row][h] . k_t) v_t
+ * over the tokens t <= p with t > p - window or t < num_sinks.  Table entries of blocks that none
+ * of a sequence's rows sees are never read, and cache rows that none sees may hold anything.
+ *
+ *   query        [total_q][num_q_heads][head_dim], q_dtype, 16-byte aligned
+ *   query_start  int32 [num_seqs + 1], query_start[0] = 0, non-decreasing,
+ *                query_start[num_seqs] = total_q
+ *   context_lens int32 [num_seqs], n_s <= context_lens[s] <= max_context_len; a sequence that
+ *                breaks this is skipped (its rows are left as they were) and flagged
+ *                PKV_DEV_BAD_CONTEXT
+ *   window       tokens, a row's own among them; at least 1 (INT_MAX: causal attention alone)
+ *   num_sinks    tokens, at least 0
+ *   scale        finite and > 0
+ *   q_dtype      PKV_F16 or PKV_BF16;  kv_dtype: q_dtype, PKV_FP8_E4M3 or PKV_FP4_E2M1
+ *   workspace    >= pkv_chunk_workspace_bytes(...) bytes, 256-byte aligned (need not be zeroed;
+ *                calls that share one must be ordered)
+ *   out          [total_q][num_q_heads][head_dim], q_dtype, 16-byte aligned
+ *   the other arguments as in pkv_paged_decode_attention.
+ * Supported: head_dim in {64, 128}; block_size in {8, 16, 32}; up to 128 query heads a kv head;
+ * max_context_len up to 2^30; pools of fewer than 2^31 rows (num_blocks * num_kv_heads *
+ * block_size); others return PKV_ERR_UNSUPPORTED.
+ * Rounding: logits, maxima, sums, accumulators and partial states are fp32.  Operands are the
+ * cache's 16-bit type; over FP8 and 4 bits they are f16, which the cached values are exactly, and
+ * bf16 queries are scaled into f16 by a power of two per row (a value keeps its bits down to 2^-29
+ * of the row's largest).  Softmax weights enter the product with V in the operands' type (f16:
+ * 2^-32 of the largest is what is lost), the denominator sums them unrounded.
+ * Three launches: a planner, the attention, and the joining of what the planner split over several
+ * SMs (few or long items); results are the same bits on every call.
+ */
+PKV_API size_t pkv_chunk_workspace_bytes(int num_seqs, int total_q, int num_q_heads,
+                                         int num_kv_heads, int head_dim, int max_context_len);
+
+PKV_API pkv_status pkv_paged_chunk_attention(
+    const void* query, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, int num_seqs, int total_q,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+    int max_blocks_per_seq, int max_context_len, int window, int num_sinks, float scale,
+    pkv_dtype q_dtype, pkv_dtype kv_dtype, float kv_scale, void* workspace,
+    size_t workspace_bytes, void* out, pkv_stream_t stream);
+
+/*
  * Write new tokens' keys and values into their cache slots
  * ("...Mathematical Foundations" §7 kernel 1; §4 Allocation Lifecycle step 2).
  *

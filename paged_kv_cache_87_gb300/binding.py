@@ -13,7 +13,7 @@ than the current one is that stream's memory, held until the current stream is t
 Functions carry the C names:
   pkv_decode_workspace_bytes, pkv_paged_decode_attention,
   pkv_paged_decode_attention_prefix, pkv_paged_decode_attention_noalloc,
-  pkv_paged_decode_attention_window, pkv_reshape_and_cache, pkv_copy_blocks,
+  pkv_paged_decode_attention_window, pkv_paged_chunk_attention, pkv_reshape_and_cache, pkv_copy_blocks,
   pkv_gather_cache, pkv_qk_norm_rope, pkv_qk_norm_rope_and_cache,
   pkv_get_device_status, pkv_status_string, pkv_version,
 and the host block manager pkv_bm_* (wrapped by ``BlockManager``).
@@ -62,6 +62,9 @@ _SIGNATURES = {
     "pkv_decode_window_workspace_bytes": (ctypes.c_size_t, [_I] * 9),
     "pkv_paged_decode_attention_window": (
         ctypes.c_int, [_P] * 5 + [_I] * 10 + [_F, _I, _I, _F, _P, ctypes.c_size_t, _P, _P]),
+    "pkv_chunk_workspace_bytes": (ctypes.c_size_t, [_I] * 6),
+    "pkv_paged_chunk_attention": (
+        ctypes.c_int, [_P] * 6 + [_I] * 11 + [_F, _I, _I, _F, _P, ctypes.c_size_t, _P, _P]),
     "pkv_multi_query_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int]),
     "pkv_paged_multi_query_attention": (
         ctypes.c_int,
@@ -408,6 +411,33 @@ def _multi_query(name, query, k_cache, v_cache, block_tables, context_lens, quer
         workspace.numel() * workspace.element_size(), out.data_ptr(), _stream_ptr(stream))
     _check(name, st)
     return out
+
+
+def pkv_chunk_workspace_bytes(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int,
+                              head_dim: int, max_context_len: int) -> int:
+    return int(load().pkv_chunk_workspace_bytes(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim,
+                                                max_context_len))
+
+
+def pkv_paged_chunk_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor,
+                              query_start: torch.Tensor, max_context_len: int, scale: float,
+                              window: int | None = None, sinks: int = 0, kv_scale: float = 1.0,
+                              workspace: torch.Tensor | None = None,
+                              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's new tokens over its cache of 16 bits, FP8 or 4 bits.
+
+    query [total_q, Hq, d] (float16 or bfloat16); rows query_start[s] .. query_start[s + 1] - 1
+    (int32 [S + 1]) are the last of sequence s's context_lens[s] cached tokens.  The token at
+    position p sees the tokens t <= p, under a ``window`` those with t > p - window and t < sinks;
+    table entries of blocks that no row of a sequence sees are never read.  Caches as in
+    pkv_paged_decode_attention, head_dim 64 or 128, up to 128 query heads a kv head.
+    ``workspace`` (uint8, >= pkv_chunk_workspace_bytes) is allocated if None; rows behind the last
+    sequence are left as they were (in an ``out`` allocated here: uninitialised).
+    """
+    return (_calls or _marshal()).chunk(query, k_cache, v_cache, block_tables, context_lens, query_start,
+                                        max_context_len, scale, window, sinks, kv_scale, workspace, out,
+                                        stream)
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20   # PKV_NOALLOC_SCRATCH_BYTES

@@ -7,6 +7,7 @@
 
 #include "cache_ops.cuh"
 #include "cache_row.cuh"
+#include "chunk_attention.cuh"
 #include "decode_fp4.cuh"
 #include "decode_launch.cuh"
 #include "mq_attention.cuh"
@@ -131,6 +132,34 @@ pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4
     pl->off_ml = round_up(states * HD * 4, 256);
     pl->off_cuts = round_up(pl->off_ml + states * 8, 256);
     pl->total = round_up(pl->off_cuts + (size_t)pl->workers * 16, 256);
+    return PKV_OK;
+}
+
+// Workspace of the chunk attention.  Pieces: every item, and one more where a CTA's run ends inside
+// of one; partial states: two a CTA, of at most as many CTAs as the steps of the longest possible
+// launch keep busy.
+pkv_status make_chunk_plan(int S, int total_q, int Hq, int Hkv, int HD, int max_ctx, ChunkPlan* pl) {
+    if (S < 0 || total_q < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_ctx < 0) return PKV_ERR_INVALID_ARG;
+    if (HD != 64 && HD != 128) return PKV_ERR_UNSUPPORTED;
+    const int G = Hq / Hkv;
+    if (G > kChunkTile || max_ctx > 1 << 30) return PKV_ERR_UNSUPPORTED;
+    const int qpt = kChunkTile / G;
+    const int64_t pairs = (int64_t)total_q / (2 * qpt) + S;
+    pl->items = pairs * Hkv;
+    if (pl->items > INT32_MAX - kChunkMaxCtas) return PKV_ERR_UNSUPPORTED;
+    pl->part_rows = total_q > qpt ? kChunkRows : kChunkTile;
+    const int64_t steps = pl->items * (((int64_t)max_ctx + kChunkTile - 1) / kChunkTile + 2);
+    const int64_t ctas = (steps + kChunkMinRun - 1) / kChunkMinRun;
+    pl->slots = 2 * (int)(ctas < kChunkMaxCtas ? ctas : kChunkMaxCtas);
+    size_t off = round_up((size_t)S * 4, 256);
+    pl->off_prefix = off;  off = round_up(off + ((size_t)S + 1) * 4, 256);
+    pl->off_pieces = off;  off = round_up(off + (size_t)(pl->items + kChunkMaxCtas) * sizeof(ChunkPiece), 256);
+    pl->off_cuts = off;    off = round_up(off + kChunkMaxCtas * sizeof(ChunkCut), 256);
+    pl->off_first = off;   off = round_up(off + (kChunkMaxCtas + 1) * 4, 256);
+    pl->off_head = off;    off += 256;
+    pl->off_acc = off;     off += (size_t)pl->slots * pl->part_rows * HD * 4;
+    pl->off_ml = off;      off += (size_t)pl->slots * pl->part_rows * 8;
+    pl->total = off;
     return PKV_OK;
 }
 
@@ -342,6 +371,94 @@ pkv_status pkv_paged_decode_attention_prefix(
                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                        max_blocks_per_seq, max_context_len, scale, q_dtype, kv_dtype, kv_scale,
                        workspace, workspace_bytes, out, stream, 1);
+}
+
+size_t pkv_chunk_workspace_bytes(int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
+                                 int head_dim, int max_context_len) {
+    ChunkPlan pl;
+    return make_chunk_plan(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, max_context_len, &pl) == PKV_OK
+               ? pl.total : 0;
+}
+
+pkv_status pkv_paged_chunk_attention(
+    const void* query, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, int num_seqs, int total_q,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+    int max_blocks_per_seq, int max_context_len, int window, int num_sinks, float scale,
+    pkv_dtype q_dtype, pkv_dtype kv_dtype, float kv_scale, void* workspace,
+    size_t workspace_bytes, void* out, pkv_stream_t stream) {
+    if (window < 1 || num_sinks < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || block_size <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (!known(q_dtype) || !known(kv_dtype)) return PKV_ERR_INVALID_ARG;
+    if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (kv_dtype != q_dtype && !quantised(kv_dtype)) return PKV_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
+    if (!isfinite(scale) || !(scale > 0.f) || !isfinite(kv_scale) || !(kv_scale > 0.f))
+        return PKV_ERR_INVALID_ARG;
+    ChunkPlan pl;
+    const pkv_status st = make_chunk_plan(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim,
+                                          max_context_len, &pl);
+    if (st != PKV_OK) return st;
+    if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)num_blocks * num_kv_heads * block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_q == 0) return PKV_OK;
+    if (!query || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(query, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4))
+        return PKV_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < pl.total) return PKV_ERR_WORKSPACE;
+    DeviceInfo* dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    ChunkParams p{};
+    p.q = query;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.out = out;
+    p.seq_order = reinterpret_cast<int*>(ws);
+    p.pair_prefix = reinterpret_cast<int*>(ws + pl.off_prefix);
+    p.pieces = reinterpret_cast<ChunkPiece*>(ws + pl.off_pieces);
+    p.cuts = reinterpret_cast<ChunkCut*>(ws + pl.off_cuts);
+    p.first = reinterpret_cast<int*>(ws + pl.off_first);
+    p.head = reinterpret_cast<int*>(ws + pl.off_head);
+    p.part_acc = reinterpret_cast<float*>(ws + pl.off_acc);
+    p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+    p.status = dev->status;
+    p.num_seqs = num_seqs;
+    p.total_q = total_q;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.qpt = kChunkTile / p.group;
+    p.block_size = block_size;
+    p.log_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    // what reaches past every context is as good as the longest one (and keeps sums in 32 bits)
+    p.window = window < max_context_len ? window : max_context_len > 0 ? max_context_len : 1;
+    p.sinks = num_sinks < max_context_len ? num_sinks : max_context_len;
+    p.num_ctas = dev->num_sms < kChunkMaxCtas ? dev->num_sms : kChunkMaxCtas;
+    if (p.num_ctas > pl.slots / 2) p.num_ctas = pl.slots / 2;
+    p.part_rows = pl.part_rows;
+    p.max_pairs = (int)(pl.items / num_kv_heads);
+    const float kv = quantised(kv_dtype) ? kv_scale : 1.f;
+    p.qk_scale_log2 = scale * 1.4426950408889634f * kv;
+    p.out_scale = kv;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = q_dtype == PKV_BF16;
+    switch (kv_dtype) {
+    case PKV_FP8_E4M3:
+        return cuda_status(bf16 ? chunk_bf16_fp8(p, head_dim, s) : chunk_f16_fp8(p, head_dim, s));
+    case PKV_FP4_E2M1:
+        return cuda_status(bf16 ? chunk_bf16_fp4(p, head_dim, s) : chunk_f16_fp4(p, head_dim, s));
+    default:
+        return cuda_status(bf16 ? chunk_bf16_16(p, head_dim, s) : chunk_f16_16(p, head_dim, s));
+    }
 }
 
 size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,

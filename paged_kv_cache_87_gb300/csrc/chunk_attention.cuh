@@ -1,0 +1,93 @@
+// chunk_attention.cuh -- parameters and launcher of the attention of a chunk of new tokens over a
+// paged cache of 16 bits, FP8 or 4 bits, causal or under a sliding window with sinks.
+#pragma once
+
+#include "common.cuh"
+
+namespace pkv {
+
+constexpr int kChunkTile = 128;       // rows of a row tile; tokens of a K/V tile ("step")
+constexpr int kChunkRows = 256;       // (token, head of the group) rows of an item, at most
+constexpr int kChunkMaxCtas = 160;    // persistent CTAs, at most (one an SM)
+// Steps that a CTA of a split launch takes at least.
+constexpr int kChunkMinRun = 4;
+// What splitting costs, in steps of every CTA: two partial states written, the joining kernel.
+constexpr int kChunkSplitCost = 8;
+
+// A run of an item's steps, as the planner lists them.
+struct __align__(16) ChunkPiece {
+    int s, kvh, pair;                 // sequence, kv head, pair of row tiles
+    int j0, j1;                       // its steps
+    int slot;                         // partial state it writes, or -1: the whole item is here
+    int pad[2];
+};
+
+// An item that several CTAs share: what the joining kernel needs.
+struct __align__(16) ChunkCut {
+    int s, kvh, pair;                 // s < 0: none
+    int last;                         // the CTA with its last steps (the first is the entry's own)
+};
+
+struct ChunkParams {
+    const void* q;                    // [total_q, Hq, d]
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;      // [S, max_blocks]
+    const int32_t* context_lens;      // [S]: tokens in the cache, the new ones included
+    const int32_t* query_start;       // [S + 1]
+    void* out;                        // [total_q, Hq, d]
+    int* seq_order;                   // workspace [S]: the sequence planned k-th
+    int* pair_prefix;                 // workspace [S + 1]: pairs of row tiles before it
+    ChunkPiece* pieces;               // workspace [max_pieces]
+    ChunkCut* cuts;                   // workspace [kChunkMaxCtas]
+    int* first;                       // workspace [kChunkMaxCtas + 1]: a CTA's first piece (split)
+    int* head;                        // workspace: {pieces, split, next piece}
+    float* part_acc;                  // workspace [slots][part_rows][d]
+    float2* part_ml;                  // workspace [slots][part_rows]: running max (log2), sum
+    unsigned* status;
+    int num_seqs, total_q, num_q_heads, num_kv_heads, group, qpt;
+    int block_size, log_block, num_blocks, max_blocks, max_context_len;
+    int window, sinks;                // window >= max_context_len: none
+    int max_pairs;                    // pairs of row tiles that the workspace has room for
+    int num_ctas, part_rows;
+    float qk_scale_log2;              // scale * log2(e) * kv_scale
+    float out_scale;                  // kv_scale of FP8 and 4 bits, else 1
+};
+
+// Sizes of a call's workspace.
+struct ChunkPlan {
+    int64_t items;                    // at most
+    int slots, part_rows;
+    size_t off_prefix, off_pieces, off_cuts, off_first, off_head, off_acc, off_ml, total;
+};
+
+// What a tile pair sees of its context, and so its steps: tiles [0, sink_tiles), then from tile
+// `first` to the one of its last token.  (Tokens below `low` that are no sinks are seen by no row.)
+struct ChunkSpan {
+    int low, sink_tiles, first, steps;
+};
+
+__host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end, int window, int sinks) {
+    ChunkSpan w;
+    const int low = p_first - window;                  // the last token that the first row does not see
+    w.low = low < 0 ? 0 : low + 1;
+    const int kept = sinks < w.low ? sinks : w.low;
+    w.sink_tiles = (kept + kChunkTile - 1) / kChunkTile;
+    w.first = w.low / kChunkTile;
+    if (w.first < w.sink_tiles) w.first = w.sink_tiles;
+    w.steps = w.sink_tiles + (kv_end - 1) / kChunkTile + 1 - w.first;
+    return w;
+}
+
+// Defined in chunk_plan.cu.
+cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
+
+// Planner, attention and joining kernel; each defined in the .cu file of its name.
+cudaError_t chunk_f16_16(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t chunk_f16_fp8(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t chunk_f16_fp4(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t chunk_bf16_16(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t chunk_bf16_fp8(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t chunk_bf16_fp4(const ChunkParams& p, int head_dim, cudaStream_t s);
+
+}  // namespace pkv

@@ -332,6 +332,53 @@ PKV_ENTRY(decode_window) {
     return decode_call(a, true);
 }
 
+// chunk(query, k_cache, v_cache, block_tables, context_lens, query_start, max_context_len, scale, window,
+//       sinks, kv_scale, workspace, out, stream): out
+PKV_ENTRY(chunk) {
+    count(n, 14);
+    const at::Tensor &q = tensor(a[0]), &k = tensor(a[1]), &v = tensor(a[2]), &bt = tensor(a[3]),
+                     &cl = tensor(a[4]), &qs = tensor(a[5]);
+    need(q.dim() == 3 && bt.dim() == 2 && cl.dim() == 1 && qs.dim() == 1,
+         "query must be [total_q, Hq, d], block_tables [S, max_blocks], context_lens [S], query_start [S + 1]");
+    const Cache c = cache_of(k);
+    need(c.d == q.size(2) && v.sizes() == k.sizes(),
+         "cache shapes must be [num_blocks, num_kv_heads, block_size, head_dim]");
+    need(one_type(k, v) && (c.type != PKV_FP4_E2M1 || v.scalar_type() == k.scalar_type()),
+         "k_cache and v_cache must have one element type");
+    need(bt.scalar_type() == at::kInt && cl.scalar_type() == at::kInt && qs.scalar_type() == at::kInt,
+         "block_tables, context_lens and query_start must be int32");
+    for (int i = 0; i < 6; ++i)
+        contiguous(a[i], "query, caches, tables, lengths and query_start must be contiguous CUDA tensors");
+    const int S = size32(cl.size(0)), T = size32(q.size(0)), Hq = size32(q.size(1)), width = size32(bt.size(1));
+    need(bt.size(0) == S && qs.size(0) == (int64_t)S + 1,
+         "block_tables must have a row and query_start an entry a sequence, and one more");
+    const int max_ctx = int32(a[6], "max_context_len does not fit in 32 bits");
+    const float scale = (float)number(a[7]), kv_scale = (float)number(a[10]);
+    const int window = a[8] == Py_None ? INT32_MAX : int32(a[8], "window does not fit in 32 bits");
+    const int sinks = int32(a[9], "sinks does not fit in 32 bits");
+    const pkv_stream_t stream = stream_of(a[13]);
+    at::Tensor ws, out;
+    if (a[11] != Py_None) ws = contiguous(a[11], "workspace must be a contiguous CUDA tensor");
+    if (a[12] != Py_None) {
+        out = contiguous(a[12], "out must be a contiguous CUDA tensor");
+        need(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type(), "out must have query's shape and type");
+    }
+    const pkv_dtype qt = code_of(q.scalar_type());
+    call("pkv_paged_chunk_attention", [&] {
+        if (!ws.defined()) {
+            const size_t bytes = pkv_chunk_workspace_bytes(S, T, Hq, c.heads, c.d, max_ctx);
+            ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
+        }
+        if (!out.defined()) out = fresh(q.sizes(), q.options(), stream);
+        return pkv_paged_chunk_attention(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const int32_t*>(bt.data_ptr()),
+            static_cast<const int32_t*>(cl.data_ptr()), static_cast<const int32_t*>(qs.data_ptr()), S, T, Hq,
+            c.heads, c.d, c.block, c.blocks, width, max_ctx, window, sinks, scale, qt, c.type, kv_scale,
+            ws.data_ptr(), (size_t)ws.numel() * ws.element_size(), out.data_ptr(), stream);
+    });
+    return THPVariable_Wrap(std::move(out));
+}
+
 // write(key, value, k_cache, v_cache, slot_mapping, kv_scale, stream, prepare): None, or the C
 // call's arguments.
 PKV_ENTRY(write) {
@@ -548,7 +595,7 @@ PyObject* set_error(PyObject*, PyObject* type) {
 }
 
 #define PKV_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {PKV_FAST(decode), PKV_FAST(decode_window), PKV_FAST(write), PKV_FAST(gather), PKV_FAST(norm_rope),
+PyMethodDef g_methods[] = {PKV_FAST(decode), PKV_FAST(decode_window), PKV_FAST(chunk), PKV_FAST(write), PKV_FAST(gather), PKV_FAST(norm_rope),
                            PKV_FAST(norm_rope_write), {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods,

@@ -102,4 +102,18 @@ bool encode_q_map(CUtensorMap* map, const void* q, long long total_q, int num_q_
            CUDA_SUCCESS;
 }
 
+bool encode_chunk_q_map(CUtensorMap* map, const void* q, long long total_q, int num_q_heads, int group,
+                        int tokens, int head_dim) {
+    EncodeTiled enc = encoder();
+    if (!enc || total_q <= 0 || total_q > 0x7fffffffLL || group <= 0 || tokens <= 0 || group * tokens > 128)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_q_heads * head_dim * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pkv

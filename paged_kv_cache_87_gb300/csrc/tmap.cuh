@@ -26,4 +26,9 @@ bool encode_rows_map(CUtensorMap* map, const void* pool, int row_bytes, long lon
 // landing as [row][128 B], 128-byte swizzled.  False if it cannot be encoded.
 bool encode_q_map(CUtensorMap* map, const void* q, long long total_q, int num_q_heads, int group);
 
+// The same for the chunk attention: head_dim 64 or 128, and a box of `group` heads x `tokens` query
+// tokens (group * tokens rows of at most 128).
+bool encode_chunk_q_map(CUtensorMap* map, const void* q, long long total_q, int num_q_heads, int group,
+                        int tokens, int head_dim);
+
 }  // namespace pkv

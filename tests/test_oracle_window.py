@@ -85,3 +85,36 @@ def test_virtual_contexts(B, tmp_path):
     o = (ctypes.c_int * 5)()
     lib.span(100, big, big, log, o)
     assert list(o) == [100, 0, 0, 0, 0] and lib.most(big, big, big, B) == big
+
+
+def test_chunk_spans(tmp_path):
+    """chunk_span() of the planner, compiled for the host: its tiles hold every token that a row sees,
+    each in order, and no tile that none sees."""
+    import ctypes
+    import os
+    import re
+    import subprocess
+    import paged_kv_cache_87_gb300 as pkg
+    text = open(os.path.join(os.path.dirname(pkg.__file__), "csrc", "chunk_attention.cuh")).read()
+    body = re.search(r"struct ChunkSpan \{.*?\n\};", text, re.S).group(0) + "\n" + \
+        re.search(r"__host__ __device__ __forceinline__ ChunkSpan chunk_span.*?\n\}\n", text, re.S).group(0)
+    c = tmp_path / "span.cpp"
+    c.write_text('#define __host__\n#define __device__\n#define __forceinline__ inline\n'
+                 'constexpr int kChunkTile = 128;\n' + body +
+                 'extern "C" void span(int p, int e, int w, int s, int* o) { ChunkSpan x = chunk_span(p, e, w, s);\n'
+                 'o[0] = x.low; o[1] = x.sink_tiles; o[2] = x.first; o[3] = x.steps; }\n')
+    so = str(tmp_path / "span.so")
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", so, str(c)], check=True)
+    lib = ctypes.CDLL(so)
+    rng = np.random.default_rng(0)
+    for _ in range(600):
+        n = int(rng.integers(1, 2000))
+        m = int(rng.integers(1, min(n, 300) + 1))
+        w, s = int(rng.integers(1, 700)), int(rng.integers(0, 400))
+        o = (ctypes.c_int * 4)()
+        lib.span(n - m, n, w, s, o)
+        low, sink_tiles, first, steps = o
+        tiles = [j if j < sink_tiles else first + j - sink_tiles for j in range(steps)]
+        seen = np.flatnonzero(window.seen(n, m, w, s).any(0))
+        assert tiles == sorted(set((seen // 128).tolist())), (n, m, w, s)
+        assert set(seen.tolist()) == {t for t in range(n) if t < s or t >= low}
