@@ -151,8 +151,7 @@ pkv_status make_chunk_plan(int S, int total_q, int Hq, int Hkv, int HD, int max_
     const int64_t steps = pl->items * (((int64_t)max_ctx + kChunkTile - 1) / kChunkTile + 2);
     const int64_t ctas = (steps + kChunkMinRun - 1) / kChunkMinRun;
     pl->slots = 2 * (int)(ctas < kChunkMaxCtas ? ctas : kChunkMaxCtas);
-    size_t off = round_up((size_t)S * 4, 256);
-    pl->off_prefix = off;  off = round_up(off + ((size_t)S + 1) * 4, 256);
+    size_t off = round_up(((size_t)S + 1) * 4, 256);
     pl->off_pieces = off;  off = round_up(off + (size_t)(pl->items + kChunkMaxCtas) * sizeof(ChunkPiece), 256);
     pl->off_cuts = off;    off = round_up(off + kChunkMaxCtas * sizeof(ChunkCut), 256);
     pl->off_first = off;   off = round_up(off + (kChunkMaxCtas + 1) * 4, 256);
@@ -419,8 +418,7 @@ pkv_status pkv_paged_chunk_attention(
     p.context_lens = context_lens;
     p.query_start = query_start;
     p.out = out;
-    p.seq_order = reinterpret_cast<int*>(ws);
-    p.pair_prefix = reinterpret_cast<int*>(ws + pl.off_prefix);
+    p.pair_prefix = reinterpret_cast<int*>(ws);
     p.pieces = reinterpret_cast<ChunkPiece*>(ws + pl.off_pieces);
     p.cuts = reinterpret_cast<ChunkCut*>(ws + pl.off_cuts);
     p.first = reinterpret_cast<int*>(ws + pl.off_first);

@@ -36,8 +36,7 @@ struct ChunkParams {
     const int32_t* context_lens;      // [S]: tokens in the cache, the new ones included
     const int32_t* query_start;       // [S + 1]
     void* out;                        // [total_q, Hq, d]
-    int* seq_order;                   // workspace [S]: the sequence planned k-th
-    int* pair_prefix;                 // workspace [S + 1]: pairs of row tiles before it
+    int* pair_prefix;                 // workspace [S + 1]: pairs of row tiles before a sequence (many sequences)
     ChunkPiece* pieces;               // workspace [max_pieces]
     ChunkCut* cuts;                   // workspace [kChunkMaxCtas]
     int* first;                       // workspace [kChunkMaxCtas + 1]: a CTA's first piece (split)
@@ -58,7 +57,7 @@ struct ChunkParams {
 struct ChunkPlan {
     int64_t items;                    // at most
     int slots, part_rows;
-    size_t off_prefix, off_pieces, off_cuts, off_first, off_head, off_acc, off_ml, total;
+    size_t off_pieces, off_cuts, off_first, off_head, off_acc, off_ml, total;
 };
 
 // What a tile pair sees of its context, and so its steps: tiles [0, sink_tiles), then from tile

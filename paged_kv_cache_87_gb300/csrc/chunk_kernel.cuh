@@ -319,97 +319,131 @@ __device__ __forceinline__ uint32_t operand_at(int r, int c) {
                       (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <typename C, int HD>
-__device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* to, int logB, int tid, bool clean,
-                                           const TileRows& rows) {
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// One raw entry at shared address `raw` into the operand tile at `to`; CLEAN: rows of V that no row
+// of the item sees become zeros.  All loads of a thread go out before its first store: a warp is
+// alone on its scheduler but for two softmax warps, so what hides latency is its own instructions
+// (with a load behind every store an entry took 1,700 cycles).
+template <typename C, int HD, bool CLEAN>
+__device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t to, int logB, int tid, const TileRows& rows) {
     const int B = 1 << logB;
     if constexpr (C::FP4) {
         // a thread a row: its 16 bytes of each 32 dims, its scales; eight lanes read 128 bytes and
         // write eight different 16-byte columns
         const int rr = tid & (B - 1);
-        const uint8_t* blk = raw + (tid >> logB) * (B * C::RAW_ROW);
+        const uint32_t blk = raw + (tid >> logB) * (B * C::RAW_ROW);
+        uint4 w[HD / 32];
         uint32_t sc[HD / 64];
-        if constexpr (HD == 128) {
-            const uint2 s = *reinterpret_cast<const uint2*>(blk + B * (HD / 2) + rr * (HD / 16));
-            sc[0] = s.x;
-            sc[1] = s.y;
-        } else {
-            sc[0] = *reinterpret_cast<const uint32_t*>(blk + B * (HD / 2) + rr * (HD / 16));
+#pragma unroll
+        for (int ch = 0; ch < HD / 32; ++ch) w[ch] = lds128(blk + (ch * B + rr) * 16);
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc[i]) : "r"(blk + B * (HD / 2) + rr * (HD / 16) + 4 * i) : "memory");
+        // a scale of zero makes a row's values zeros (codes are finite)
+        if (CLEAN && rows.hidden(tid)) {
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i) sc[i] = 0u;
         }
-        const bool zero = clean && rows.hidden(tid);
+        const uint32_t row = to + (tid >> 3) * C::GROUP_BYTES + (tid & 7) * 128, x7 = (tid & 7) << 4;
 #pragma unroll
         for (int ch = 0; ch < HD / 32; ++ch) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(blk + (ch * B + rr) * 16);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
             const uint32_t pair = (ch & 1) ? e4m3x2_of<1>(sc[ch >> 1]) : e4m3x2_of<0>(sc[ch >> 1]);
             const __half2 two = *reinterpret_cast<const __half2*>(&pair);
-            const __half2 s0 = __low2half2(two), s1 = __high2half2(two);
+            const uint32_t word[4] = {w[ch].x, w[ch].y, w[ch].z, w[ch].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half2 s = i < 2 ? s0 : s1;
-                uint32_t x[4] = {e2m1x2_to_f16x2<0>(w[i]), e2m1x2_to_f16x2<1>(w[i]), e2m1x2_to_f16x2<2>(w[i]),
-                                 e2m1x2_to_f16x2<3>(w[i])};
+                const __half2 s = i < 2 ? __low2half2(two) : __high2half2(two);
+                uint32_t x[4] = {e2m1x2_to_f16x2<0>(word[i]), e2m1x2_to_f16x2<1>(word[i]),
+                                 e2m1x2_to_f16x2<2>(word[i]), e2m1x2_to_f16x2<3>(word[i])};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x[e]), s);
-                    x[e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&v);
+                    x[e] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                *reinterpret_cast<uint4*>(to + operand_at<C>(tid, 4 * ch + i)) = make_uint4(x[0], x[1], x[2], x[3]);
+                const int c = 4 * ch + i;
+                sts128(row + (c >> 3) * C::GROUP_HALF + (((c & 7) << 4) ^ x7), x[0], x[1], x[2], x[3]);
             }
         }
     } else {
-        // a thread 16 codes: eight lanes read 128 bytes; of a row's two halves one writes its odd
-        // column first, so that eight lanes write eight different columns
-        constexpr int PER = HD / 16;
+        // a thread 16 codes at a time: eight lanes read 128 bytes; of a row's two halves one writes
+        // its odd column first, so that eight lanes write eight different columns
+        constexpr int PER = HD / 16, UNITS = kT * PER / 128, STEP = 128 / PER;   // rows from unit to unit
+        uint4 w[UNITS];
 #pragma unroll
-        for (int u = 0; u < kT * PER / 128; ++u) {
-            const int at = u * 128 + tid, r = at / PER, c = at % PER;
-            const uint4 w4 = *reinterpret_cast<const uint4*>(raw + at * 16);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            const bool zero = clean && rows.hidden(r);
+        for (int u = 0; u < UNITS; ++u) w[u] = lds128(raw + (u * 128 + tid) * 16);
+        const int r0 = tid / PER, c = tid % PER;
+        const bool odd = HD == 128 && c >= 4;
+        // STEP is a multiple of 8: rows r0 + u STEP have the same place in their groups
+        const uint32_t at = to + (r0 >> 3) * C::GROUP_BYTES + (r0 & 7) * 128 + (c >> 2) * C::GROUP_HALF;
+        const uint32_t lo = ((2 * c + odd) & 7) << 4, hi = ((2 * c + !odd) & 7) << 4, x7 = (r0 & 7) << 4;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
             uint32_t x[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[2 * i] = zero ? 0u : e4m3x2_of<0>(w[i]);
-                x[2 * i + 1] = zero ? 0u : e4m3x2_of<1>(w[i]);
+                x[2 * i] = e4m3x2_of<0>(word[i]);
+                x[2 * i + 1] = e4m3x2_of<1>(word[i]);
             }
-            const bool odd = HD == 128 && c >= 4;
-            const uint4 lo = make_uint4(x[0], x[1], x[2], x[3]), hi = make_uint4(x[4], x[5], x[6], x[7]);
-            *reinterpret_cast<uint4*>(to + operand_at<C>(r, 2 * c + odd)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(to + operand_at<C>(r, 2 * c + !odd)) = odd ? lo : hi;
+            if (CLEAN && rows.hidden(r0 + u * STEP)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = 0u;
+            }
+            const uint32_t to_u = at + u * (STEP >> 3) * C::GROUP_BYTES;
+            sts128(to_u + (lo ^ x7), odd ? x[4] : x[0], odd ? x[5] : x[1], odd ? x[6] : x[2], odd ? x[7] : x[3]);
+            sts128(to_u + (hi ^ x7), odd ? x[0] : x[4], odd ? x[1] : x[5], odd ? x[2] : x[6], odd ? x[3] : x[7]);
         }
     }
 }
 
-// Row r of a Q tile (bf16) to f16 in place, times 2^e; returns e (2^60 at most, so that the logit
-// scale that undoes it stays a normal number; rows below 2^-46 lose what is 2^-24 under 2^-60).
+// Row r of a Q tile (bf16) at shared address `tile` to f16 in place, times 2^e; returns e (2^60 at
+// most, so that the logit scale that undoes it stays a normal number; rows below 2^-46 lose what is
+// 2^-24 under 2^-60).
 template <typename C, int HD>
-__device__ __forceinline__ int scale_q_row(uint8_t* tile, int r) {
-    float amax = 0.f;
-    auto chunk = [&](int c) {
-        return reinterpret_cast<uint4*>(tile + (c >> 3) * C::HALF_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-    };
-#pragma unroll 4
-    for (int c = 0; c < HD / 8; ++c) {
-        float x[8];
-        Chunk<BF16>::to_float(*chunk(c), x);
+__device__ __forceinline__ int scale_q_row(uint32_t tile, int r) {
+    const uint32_t row = tile + r * 128, x7 = (r & 7) << 4;
+    auto at = [&](int c) { return row + (c >> 3) * C::HALF_BYTES + (((c & 7) << 4) ^ x7); };
+    uint32_t top = 0u;                 // the largest magnitudes of even and of odd dims
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int c0 = 0; c0 < HD / 8; c0 += 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = lds128(at(c0 + c));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            top = __vmaxu2(top, w[c].x & 0x7fff7fffu);
+            top = __vmaxu2(top, w[c].y & 0x7fff7fffu);
+            top = __vmaxu2(top, w[c].z & 0x7fff7fffu);
+            top = __vmaxu2(top, w[c].w & 0x7fff7fffu);
+        }
     }
-    const int ex = (int)(__float_as_uint(amax) >> 23) - 127;          // floor(log2); 128: infinite
+    const int ex = (int)(max(top >> 16, top & 0xffffu) >> 7) - 127;    // floor(log2); 128: not finite
     const int e = ex == 128 ? 0 : min(14 - ex, 60);
     const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll 4
-    for (int c = 0; c < HD / 8; ++c) {
-        float x[8];
-        Chunk<BF16>::to_float(*chunk(c), x);
-        uint32_t y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(x[2 * i] * up, x[2 * i + 1] * up);
-            y[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int c0 = 0; c0 < HD / 8; c0 += 4) {
+        uint4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = lds128(at(c0 + c));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 h = __floats2half2_rn(__uint_as_float(x[i] << 16) * up,
+                                                    __uint_as_float(x[i] & 0xffff0000u) * up);
+                x[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            sts128(at(c0 + c), x[0], x[1], x[2], x[3]);
         }
-        *chunk(c) = make_uint4(y[0], y[1], y[2], y[3]);
     }
     return e;
 }
@@ -418,6 +452,7 @@ template <typename C, int HD>
 __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* smem, const ChunkBars<C>& b,
                                               const ChunkSlot* items, volatile int* abort_flag) {
     const int tid = threadIdx.x - 384, lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(smem);
     uint32_t g = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -431,8 +466,9 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
                 ok = false;
                 break;
             }
-            widen_tile<C, HD>(smem + C::OFF_RAW + rs * C::RAW_BYTES, smem + C::OFF_RING + st * C::TILE_BYTES,
-                              p.log_block, tid, (i & 1) && rows.any(), rows);
+            const uint32_t raw = base + C::OFF_RAW + rs * C::RAW_BYTES, to = base + C::OFF_RING + st * C::TILE_BYTES;
+            if ((i & 1) && rows.any()) widen_tile<C, HD, true>(raw, to, p.log_block, tid, rows);
+            else widen_tile<C, HD, false>(raw, to, p.log_block, tid, rows);
             fence_proxy_async_smem();                    // the MMAs, and the copies that reuse the raw bytes
             __syncwarp();
             if (lane == 0) {
@@ -446,7 +482,7 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
                 }
                 int8_t* back = reinterpret_cast<int8_t*>(smem + C::OFF_BACK) + (k & 1) * 256;
                 for (int X = 0; X < (it.qn_b > 0 ? 2 : 1); ++X)
-                    back[X * kT + tid] = (int8_t)scale_q_row<C, HD>(smem + C::OFF_Q + X * C::TILE_BYTES, tid);
+                    back[X * kT + tid] = (int8_t)scale_q_row<C, HD>(base + C::OFF_Q + X * C::TILE_BYTES, tid);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.q_full[k & 1]);
