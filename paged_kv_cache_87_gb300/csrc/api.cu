@@ -422,7 +422,7 @@ pkv_status pkv_paged_chunk_attention(
     p.pieces = reinterpret_cast<ChunkPiece*>(ws + pl.off_pieces);
     p.cuts = reinterpret_cast<ChunkCut*>(ws + pl.off_cuts);
     p.first = reinterpret_cast<int*>(ws + pl.off_first);
-    p.head = reinterpret_cast<int*>(ws + pl.off_head);
+    p.head = reinterpret_cast<ChunkHead*>(ws + pl.off_head);
     p.part_acc = reinterpret_cast<float*>(ws + pl.off_acc);
     p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
     p.status = dev->status;
@@ -444,6 +444,7 @@ pkv_status pkv_paged_chunk_attention(
     if (p.num_ctas > pl.slots / 2) p.num_ctas = pl.slots / 2;
     p.part_rows = pl.part_rows;
     p.max_pairs = (int)(pl.items / num_kv_heads);
+    p.max_cuts = (int)(pl.items < p.num_ctas ? pl.items : p.num_ctas);
     const float kv = quantised(kv_dtype) ? kv_scale : 1.f;
     p.qk_scale_log2 = scale * 1.4426950408889634f * kv;
     p.out_scale = kv;

@@ -14,18 +14,31 @@ constexpr int kChunkMinRun = 4;
 // What splitting costs, in steps of every CTA: two partial states written, the joining kernel.
 constexpr int kChunkSplitCost = 8;
 
-// A run of an item's steps, as the planner lists them.
+// A run of an item's steps, as the planner lists them: CTA c's first one is entry c, what else it
+// takes (`first`, or the counter) lies behind entry num_ctas - 1.
 struct __align__(16) ChunkPiece {
     int s, kvh, pair;                 // sequence, kv head, pair of row tiles
     int j0, j1;                       // its steps
     int slot;                         // partial state it writes, or -1: the whole item is here
-    int pad[2];
+    int q_begin, n, ctx;              // the sequence's first row, its rows, its tokens in the cache
+    int pad[3];
 };
 
 // An item that several CTAs share: what the joining kernel needs.
 struct __align__(16) ChunkCut {
-    int s, kvh, pair;                 // s < 0: none
-    int last;                         // the CTA with its last steps (the first is the entry's own)
+    int kvh, pair, q_begin, n;
+    int c0, c1;                       // the CTAs with its first and its last steps
+    int pad[2];
+};
+
+// What the planner leaves besides.
+struct __align__(16) ChunkHead {
+    int begun;                        // CTAs that have a first piece
+    int end;                          // end of the list (whole items: of those behind the first ones)
+    int split;                        // a CTA's other pieces are `first`'s, not the counter's
+    int next;                         // the counter
+    int cuts;
+    int pad[3];
 };
 
 struct ChunkParams {
@@ -39,8 +52,8 @@ struct ChunkParams {
     int* pair_prefix;                 // workspace [S + 1]: pairs of row tiles before a sequence (many sequences)
     ChunkPiece* pieces;               // workspace [max_pieces]
     ChunkCut* cuts;                   // workspace [kChunkMaxCtas]
-    int* first;                       // workspace [kChunkMaxCtas + 1]: a CTA's first piece (split)
-    int* head;                        // workspace: {pieces, split, next piece}
+    int* first;                       // workspace [kChunkMaxCtas + 1]: a CTA's second piece (split)
+    ChunkHead* head;                  // workspace
     float* part_acc;                  // workspace [slots][part_rows][d]
     float2* part_ml;                  // workspace [slots][part_rows]: running max (log2), sum
     unsigned* status;
@@ -49,6 +62,7 @@ struct ChunkParams {
     int window, sinks;                // window >= max_context_len: none
     int max_pairs;                    // pairs of row tiles that the workspace has room for
     int num_ctas, part_rows;
+    int max_cuts;                     // items that can be cut, by the sizes
     float qk_scale_log2;              // scale * log2(e) * kv_scale
     float out_scale;                  // kv_scale of FP8 and 4 bits, else 1
 };

@@ -119,8 +119,8 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const Chun
     ChunkItem it;
     it.s = x.s;
     it.kvh = x.kvh;
-    it.q_begin = p.query_start[x.s];
-    const int n = p.query_start[x.s + 1] - it.q_begin, ctx = p.context_lens[x.s];
+    it.q_begin = x.q_begin;
+    const int n = x.n, ctx = x.ctx;
     const int q0 = x.pair * 2 * p.qpt;
     it.q_row = it.q_begin + q0;
     it.p0 = ctx - n + q0;
@@ -204,12 +204,11 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
     const uint64_t policy = l2_evict_last_policy();      // other items read K/V again
     const uint64_t q_policy = l2_evict_first_policy();   // a query row is read once
     const int B = p.block_size, logB = p.log_block, per_tile = kT >> logB;
-    const int total = p.head[0], split = p.head[1];
-    int next = 0, end = 0;
-    if (split) {
-        next = p.first[blockIdx.x];
-        end = p.first[blockIdx.x + 1];
-    }
+    // one round of loads to the CTA's first piece
+    const ChunkPiece piece0 = p.pieces[blockIdx.x];
+    const ChunkHead head = *p.head;
+    int next = p.first[blockIdx.x];
+    const int end = head.split ? p.first[blockIdx.x + 1] : head.end;
     uint64_t* ring_full = C::WIDE ? b.raw_full : b.full;
     uint64_t* ring_empty = C::WIDE ? b.raw_empty : b.empty;
     constexpr int RING = C::WIDE ? C::RAWS : C::STAGES;
@@ -222,13 +221,17 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
                 set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
                 *abort_flag = 1;
             } else if (!*abort_flag) {
-                idx = split ? next++ : atomicAdd(p.head + 2, 1);
-                if (idx >= (split ? end : total)) idx = -1;
+                if (k == 0) {
+                    idx = blockIdx.x < head.begun ? (int)blockIdx.x : -1;
+                } else {
+                    idx = head.split ? next++ : atomicAdd(&p.head->next, 1);
+                    if (idx >= end) idx = -1;
+                }
             }
         }
         idx = __shfl_sync(0xffffffffu, idx, 0);
         ChunkItem it{};
-        if (idx >= 0) it = chunk_item(p, p.pieces[idx]);
+        if (idx >= 0) it = chunk_item(p, k == 0 ? piece0 : p.pieces[idx]);
         if (lane == 0) {
             items[slot].it = it;
             items[slot].idx = idx;
@@ -309,6 +312,13 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
         }
         if (!ok) break;
     }
+}
+
+// Bits 0 .. n - 1 (none below 1, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    uint32_t x;
+    asm("shl.b32 %0, 1, %1;" : "=r"(x) : "r"(max(n, 0)));     // 0 from 32 on
+    return x - 1u;
 }
 
 // ---- the widening warps (128 threads): raw entries into operands, and bf16 Q into f16 ----
@@ -699,9 +709,18 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
                 tc5::ld_32x32b_x64(colS + 64u, sv[1]);
                 tc5::wait_ld();
                 if (masked) {
+                    // 32 columns' bits at a time (comparing each column with the three bounds became
+                    // branches: 10,000 cycles a tile instead of 2,000)
 #pragma unroll
-                    for (int c = 0; c < kT; ++c)
-                        if (c > lim || (c <= low && c >= kept)) sv[c >> 6][c & 63] = __float_as_uint(-INFINITY);
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t seen = bits_below(lim + 1 - 32 * w) &
+                                              (~bits_below(low + 1 - 32 * w) | bits_below(kept - 32 * w));
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            uint32_t& x = sv[w >> 1][32 * (w & 1) + c];
+                            x = (seen >> c & 1u) ? x : __float_as_uint(-INFINITY);
+                        }
+                    }
                 }
                 float pmx[4];
 #pragma unroll
@@ -828,18 +847,16 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
     named_bar_sync(1, C::THREADS);
 }
 
-// Joins the items that lie in several CTAs' runs: entry blockIdx.x is the item that CTA blockIdx.x
-// began and left unfinished, if it did; the states of CTAs c, c + 1, .. in that order, a warp a row,
-// HD / 32 dims a lane, four states' loads in flight.
+// Joins the items that lie in several CTAs' runs, entry blockIdx.x of the planner's list: the states
+// of CTAs c0, c0 + 1, .. in that order, a warp a row, HD / 32 dims a lane, eight states' loads in flight.
 template <typename QT, int HD>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int V = HD / 32, FLY = 4;
-    const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x));
-    if (raw.x < 0) return;
-    const int s = raw.x, kvh = raw.y, pair = raw.z, c0 = blockIdx.x, c1 = raw.w;
-    const int q_begin = p.query_start[s], n = p.query_start[s + 1] - q_begin, q0 = pair * 2 * p.qpt;
+    constexpr int V = HD / 32, FLY = 8;
+    const ChunkCut cut = p.cuts[blockIdx.x];
+    if ((int)blockIdx.x >= p.head->cuts) return;
+    const int kvh = cut.kvh, c0 = cut.c0, c1 = cut.c1, q_begin = cut.q_begin, n = cut.n, q0 = cut.pair * 2 * p.qpt;
     const int lane = threadIdx.x & 31, warps = gridDim.y * 8;
     for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < 2 * kT; row += warps) {
         const int X = row >> 7, r = row & (kT - 1), tok = q0 + X * p.qpt + r / p.group;
@@ -931,9 +948,9 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, kernel, p, tk, tv, tq);
     if (err != cudaSuccess) return err;
-    // eight warps a CTA, a row each at a time: enough CTAs an item that a warp has eight rows at most
-    const int rows = p.part_rows;
-    cfg.gridDim = dim3((unsigned)p.num_ctas, (unsigned)((rows + 63) / 64), 1);
+    // eight warps a CTA, a row each at a time; about 1,200 CTAs at most, as many as are resident
+    const int most = p.part_rows / 8, want = 1200 / p.max_cuts;
+    cfg.gridDim = dim3((unsigned)p.max_cuts, (unsigned)(want < 4 ? 4 : want < most ? want : most), 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, chunk_join_kernel<QT, HD>, p);

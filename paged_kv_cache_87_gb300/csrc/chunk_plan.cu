@@ -47,25 +47,25 @@ struct Seq {
 
 // Steps of the g-th pair of row tiles in planned order (of a sequence the later, longer pairs first).
 struct Pair {
-    int s, pair, steps;
+    Seq q;
+    int pair, steps;
 };
 
 __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     pdl_launch_dependents();
-    __shared__ int wsum[3][32];
+    __shared__ int wsum[2][32];
     __shared__ int s_ctx[kSeqs];
     __shared__ Seq s_seq[kSeqs];
     __shared__ int s_prefix[kSeqs + 1];
-    __shared__ int s_most;
+    __shared__ int s_most, s_cuts;
     __shared__ unsigned long long s_total;
     const int tid = threadIdx.x, S = p.num_seqs;
     const bool small = S <= kSeqs;
     if (tid == 0) {
-        s_most = 0;
+        s_most = s_cuts = 0;
         s_total = 0;
     }
     pdl_wait();
-    for (int c = tid; c < kChunkMaxCtas; c += kThreads) p.cuts[c].s = -1;
     const int64_t cap = min((int64_t)p.max_context_len, (int64_t)p.max_blocks * p.block_size);
     // pairs of a sequence; one that breaks the contract has none
     auto pairs_of = [&](int q0, int q1, int ctx) {
@@ -133,31 +133,27 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
             if (prefix[mid] <= g) lo = mid;
             else hi = mid - 1;
         }
-        Seq q;
-        if (small) {
-            q = s_seq[lo];
-        } else {
-            q.s = lo;
-            q.q0 = p.query_start[lo];
-            q.n = p.query_start[lo + 1] - q.q0;
-            q.ctx = p.context_lens[lo];
-        }
         Pair r;
-        r.s = q.s;
+        if (small) {
+            r.q = s_seq[lo];
+        } else {
+            r.q.s = lo;
+            r.q.q0 = p.query_start[lo];
+            r.q.n = p.query_start[lo + 1] - r.q.q0;
+            r.q.ctx = p.context_lens[lo];
+        }
         r.pair = prefix[lo + 1] - 1 - g;
-        const int a = r.pair * 2 * p.qpt, b = min(q.n, a + 2 * p.qpt);
-        r.steps = chunk_span(q.ctx - q.n + a, q.ctx - q.n + b, p.window, p.sinks).steps;
+        const int a = r.pair * 2 * p.qpt, b = min(r.q.n, a + 2 * p.qpt), before = r.q.ctx - r.q.n;
+        r.steps = chunk_span(before + a, before + b, p.window, p.sinks).steps;
         return r;
     };
     // all steps, and the longest item's
     int64_t steps = 0;
     int most = 0;
-    Pair first{0, 0, 0};                    // this thread's first pair: it is needed again below
     for (int g = tid; g < pairs; g += kThreads) {
-        const Pair r = pair_at(g);
-        if (g == tid) first = r;
-        steps += r.steps;
-        most = max(most, r.steps);
+        const int n = pair_at(g).steps;
+        steps += n;
+        most = max(most, n);
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, off);
@@ -174,53 +170,48 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     const int64_t whole = max((int64_t)most, (items + p.num_ctas - 1) / p.num_ctas * total / max(items, (int64_t)1));
     const bool split = whole > q64 + kChunkSplitCost && total <= INT32_MAX - (1 << 20);
     const uint32_t q = (uint32_t)q64;
-    // the pieces, in the flattened order
-    int at_steps = 0, at_pieces = 0;
-    for (int base = 0; base < pairs; base += kThreads) {
-        const int g = base + tid;
-        Pair r{0, 0, 0};
-        if (g < pairs) r = base == 0 ? first : pair_at(g);
-        int all_steps = 0, all_pieces;
-        const int pos0 = split ? at_steps + block_scan(r.steps * p.num_kv_heads, wsum[1], &all_steps) : 0;
-        int mine = 0;
-        if (g < pairs) {
-            if (split)
-                for (int h = 0; h < p.num_kv_heads; ++h) {
-                    const uint32_t a = pos0 + h * r.steps;
-                    mine += (a + r.steps - 1) / q - a / q + 1;
-                }
-            else
-                mine = p.num_kv_heads;
+    // the pieces, in the flattened order, an item a thread
+    const int nitems = (int)items, used = split ? (int)((total + q - 1) / q) : min(nitems, p.num_ctas);
+    int at_steps = 0, extras = 0;
+    for (int base = 0; base < nitems; base += kThreads) {
+        const int i = base + tid, h = i % p.num_kv_heads;
+        Pair r{};
+        if (i < nitems) r = pair_at(i / p.num_kv_heads);
+        ChunkPiece x{r.q.s, h, r.pair, 0, r.steps, -1, r.q.q0, r.q.n, r.q.ctx, {0, 0, 0}};
+        if (!split) {
+            if (i < nitems) p.pieces[i] = x;
+            continue;
         }
-        int i = at_pieces + block_scan(mine, wsum[2], &all_pieces);
-        if (g < pairs)
-            for (int h = 0; h < p.num_kv_heads; ++h) {
-                ChunkPiece x{r.s, h, r.pair, 0, r.steps, -1, {0, 0}};
-                if (!split) {
-                    p.pieces[i++] = x;
-                    continue;
-                }
-                const uint32_t a = pos0 + h * r.steps, c0 = a / q, c1 = (a + r.steps - 1) / q;
-                for (uint32_t c = c0; c <= c1; ++c) {
-                    x.j0 = c == c0 ? 0 : (int)(c * q - a);
-                    x.j1 = c == c1 ? r.steps : (int)((c + 1) * q - a);
-                    x.slot = c0 == c1 ? -1 : (int)(2 * c + (c == c0));
-                    if (a + x.j0 == c * q) p.first[c] = i;
-                    p.pieces[i++] = x;
-                }
-                if (c0 != c1) p.cuts[c0] = ChunkCut{r.s, h, r.pair, (int)c1};
+        int all_steps, all_extras;
+        const uint32_t a = at_steps + block_scan(r.steps, wsum[0], &all_steps), b = a + r.steps;
+        const uint32_t c0 = a / q, c1 = i < nitems ? (b - 1) / q : 0;
+        const bool extra = i < nitems && a != c0 * q;        // its first piece is not its CTA's first
+        int e = extras + block_scan(extra, wsum[1], &all_extras);
+        if (i < nitems) {
+            if (extra) {
+                x.j1 = min(r.steps, (int)((c0 + 1) * q - a));
+                x.slot = c0 == c1 ? -1 : (int)(2 * c0 + 1);
+                p.pieces[p.num_ctas + e++] = x;
             }
+            for (uint32_t c = c0 + extra; c <= c1; ++c) {
+                x.j0 = (int)(c * q - a);
+                x.j1 = min(r.steps, (int)((c + 1) * q - a));
+                x.slot = c0 == c1 ? -1 : (int)(2 * c + (c == c0));
+                p.pieces[c] = x;
+                p.first[c] = p.num_ctas + e;
+            }
+            if (c0 != c1)                                    // (in any order: each is an item of its own)
+                p.cuts[atomicAdd(&s_cuts, 1)] = ChunkCut{h, r.pair, r.q.q0, r.q.n, (int)c0, (int)c1, {0, 0}};
+        }
         at_steps += all_steps;
-        at_pieces += all_pieces;
+        extras += all_extras;
         __syncthreads();
     }
-    for (int64_t c = tid; c <= p.num_ctas; c += kThreads)      // CTAs without work
-        if (!split || c * q >= total) p.first[c] = at_pieces;
-    if (tid == 0) {
-        p.head[0] = at_pieces;
-        p.head[1] = split;
-        p.head[2] = 0;
-    }
+    for (int c = tid; c <= p.num_ctas; c += kThreads)        // where CTAs without work would begin
+        if (c >= used) p.first[c] = p.num_ctas + extras;
+    __syncthreads();
+    if (tid == 0)
+        *p.head = ChunkHead{used, split ? p.num_ctas + extras : nitems, split, p.num_ctas, s_cuts, {0, 0, 0}};
 }
 
 }  // namespace
