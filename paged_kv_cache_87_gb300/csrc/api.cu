@@ -144,10 +144,13 @@ pkv_status make_chunk_plan(int S, int total_q, int Hq, int Hkv, int HD, int max_
     const int G = Hq / Hkv;
     if (G > kChunkTile || max_ctx > 1 << 30) return PKV_ERR_UNSUPPORTED;
     const int qpt = kChunkTile / G;
-    const int64_t pairs = (int64_t)total_q / (2 * qpt) + S;
+    // items of one row tile where sequences have 128 rows or fewer on average, else of two (16 x 512
+    // tokens over up to 8,192 in FP8, 32 / 8 heads: 247 us in two)
+    pl->item_tokens = total_q <= (int64_t)S * qpt ? qpt : 2 * qpt;
+    const int64_t pairs = (int64_t)total_q / pl->item_tokens + S;
     pl->items = pairs * Hkv;
     if (pl->items > INT32_MAX - kChunkMaxCtas) return PKV_ERR_UNSUPPORTED;
-    pl->part_rows = total_q > qpt ? kChunkRows : kChunkTile;
+    pl->part_rows = pl->item_tokens > qpt && total_q > qpt ? kChunkRows : kChunkTile;
     const int64_t steps = pl->items * (((int64_t)max_ctx + kChunkTile - 1) / kChunkTile + 2);
     const int64_t ctas = (steps + kChunkMinRun - 1) / kChunkMinRun;
     pl->slots = 2 * (int)(ctas < kChunkMaxCtas ? ctas : kChunkMaxCtas);
@@ -443,6 +446,7 @@ pkv_status pkv_paged_chunk_attention(
     p.num_ctas = dev->num_sms < kChunkMaxCtas ? dev->num_sms : kChunkMaxCtas;
     if (p.num_ctas > pl.slots / 2) p.num_ctas = pl.slots / 2;
     p.part_rows = pl.part_rows;
+    p.item_tokens = pl.item_tokens;
     p.max_pairs = (int)(pl.items / num_kv_heads);
     p.max_cuts = (int)(pl.items < p.num_ctas ? pl.items : p.num_ctas);
     const float kv = quantised(kv_dtype) ? kv_scale : 1.f;

@@ -58,6 +58,7 @@ struct ChunkParams {
     float2* part_ml;                  // workspace [slots][part_rows]: running max (log2), sum
     unsigned* status;
     int num_seqs, total_q, num_q_heads, num_kv_heads, group, qpt;
+    int item_tokens;                  // of an item: qpt (one row tile, NARROW) or 2 qpt
     int block_size, log_block, num_blocks, max_blocks, max_context_len;
     int window, sinks;                // window >= max_context_len: none
     int max_pairs;                    // pairs of row tiles that the workspace has room for
@@ -70,7 +71,7 @@ struct ChunkParams {
 // Sizes of a call's workspace.
 struct ChunkPlan {
     int64_t items;                    // at most
-    int slots, part_rows;
+    int slots, part_rows, item_tokens;
     size_t off_pieces, off_cuts, off_first, off_head, off_acc, off_ml, total;
 };
 

@@ -41,7 +41,10 @@ namespace {
 constexpr int kT = kChunkTile;
 constexpr float kSlack = 8.0f;         // log2-domain headroom before the running max moves
 
-template <typename QT, typename KT, int HD>
+// NARROW: items of one row tile; its steps go to tiles A and B in turn (both hold the same rows), whose
+// states the rows' threads add up at the end.  For launches with few rows a sequence: two softmaxes
+// and two runs of products overlap where a lone tile's would follow each other.
+template <typename QT, typename KT, int HD, bool NARROW>
 struct ChunkCfg {
     static constexpr bool WIDE = !std::is_same<QT, KT>::value;      // raw bytes to be widened
     static constexpr bool FP4 = std::is_same<KT, E2M1>::value;
@@ -54,7 +57,8 @@ struct ChunkCfg {
     static constexpr int GROUP_BYTES = HALVES * GROUP_HALF;
     static constexpr int RAW_ROW = FP4 ? HD / 2 + HD / 16 : HD;      // bytes of a cached row
     static constexpr int RAW_BYTES = kT * RAW_ROW;
-    static constexpr int STAGES = HD == 64 ? 6 : WIDE ? (FP4 ? 4 : 3) : 5;
+    static constexpr int QTILES = NARROW ? 1 : 2;
+    static constexpr int STAGES = HD == 64 ? 6 : (WIDE ? (FP4 ? 4 : 3) : 5) + NARROW;
     static constexpr int RAWS = WIDE ? (HD == 64 ? 6 : FP4 ? 3 : 4) : 0;
     static constexpr int WARPS = WIDE ? 16 : 12;
     static constexpr int THREADS = 32 * WARPS;
@@ -63,14 +67,15 @@ struct ChunkCfg {
     static constexpr float LIFT = std::is_same<MT, F16>::value ? 7.f : 0.f;
     static constexpr int ITEM_READERS = 10 + (WIDE ? 4 : 0);
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = 2 * TILE_BYTES;
+    static constexpr int OFF_RING = QTILES * TILE_BYTES;
     static constexpr int OFF_RAW = OFF_RING + STAGES * TILE_BYTES;
     static constexpr int OFF_BARS = OFF_RAW + RAWS * RAW_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * RAWS + 16;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * RAWS + 17;
     static constexpr int OFF_MISC = OFF_BARS + NUM_BARS * 8;         // TMEM address, abort flag
     static constexpr int OFF_ITEMS = (OFF_MISC + 8 + 15) / 16 * 16;
     static constexpr int OFF_BACK = OFF_ITEMS + 2 * 80;              // [2][256] powers of two of Q's rows
-    static constexpr int SMEM = OFF_BACK + (SCALE_Q ? 2 * 256 : 0) + 1024;
+    static constexpr int OFF_ML = OFF_BACK + (SCALE_Q ? 2 * 256 : 0);  // [128] (m, l) of tile B's rows
+    static constexpr int SMEM = OFF_ML + (NARROW ? kT * 8 : 0) + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
     static_assert(ROW_REGS * 256 + AUX_REGS * (THREADS - 256) <= 65536 / THREADS / 8 * 8 * THREADS,
                   "the register split fits the launch's registers");
@@ -84,7 +89,7 @@ struct ChunkItem {
     int s, kvh, q_row, q_begin;    // q_row: the first query row (token) of tile A in `query`
     int p0;                        // its position
     int qn_a, qn_b;                // tokens of tiles A and B (B may have none)
-    int T_a, T_b, T;               // steps of A, of B, of the piece
+    int T_a, T_b, T;               // steps of A, of B, of the piece (NARROW: 0, 2, .. are A's, 1, 3, .. B's)
     int j0, sink_tiles, first;     // step j of the piece is tile j0 + j, or first + j0 + j - sink_tiles
     int low, kv_end;               // tokens that some row sees: [0, sinks) and [low, kv_end)
     int slot;
@@ -115,17 +120,18 @@ __device__ __forceinline__ TileRows rows_of_tile(const ChunkItem& it, int sinks,
     return r;
 }
 
+template <bool NARROW>
 __device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const ChunkPiece& x) {
     ChunkItem it;
     it.s = x.s;
     it.kvh = x.kvh;
     it.q_begin = x.q_begin;
     const int n = x.n, ctx = x.ctx;
-    const int q0 = x.pair * 2 * p.qpt;
+    const int q0 = x.pair * (NARROW ? 1 : 2) * p.qpt;
     it.q_row = it.q_begin + q0;
     it.p0 = ctx - n + q0;
     it.qn_a = min(p.qpt, n - q0);
-    it.qn_b = max(0, min(p.qpt, n - q0 - p.qpt));
+    it.qn_b = NARROW ? 0 : max(0, min(p.qpt, n - q0 - p.qpt));
     it.kv_end = it.p0 + it.qn_a + it.qn_b;
     const ChunkSpan w = chunk_span(it.p0, it.kv_end, p.window, p.sinks);
     it.low = w.low;
@@ -133,12 +139,17 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const Chun
     it.first = w.first;
     it.j0 = x.j0;
     it.T = x.j1 - x.j0;
+    it.slot = x.slot;
+    if (NARROW) {
+        it.T_a = (it.T + 1) / 2;
+        it.T_b = it.T / 2;
+        return it;
+    }
     // steps of tile A alone: its last token lies in an earlier tile, perhaps
     const int steps_a = w.sink_tiles + (it.p0 + it.qn_a - 1) / kT + 1 - w.first;
     it.T_a = max(0, min(steps_a - x.j0, it.T));
     it.T_b = it.qn_b > 0 ? it.T : 0;
     if (it.qn_b == 0) it.T_a = it.T;
-    it.slot = x.slot;
     return it;
 }
 
@@ -169,6 +180,7 @@ struct ChunkBars {
     uint64_t *o_free;              // [2] O_X read by the epilogue (128 arrivals)
     uint64_t *item_full, *item_empty;   // [2]
     uint64_t* fin;                 // every MMA of the CTA completed
+    uint64_t* ml;                  // NARROW: tile B's (m, l) of a piece are there (128 arrivals)
     __device__ __forceinline__ explicit ChunkBars(uint8_t* smem) {
         full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
         empty = full + C::STAGES;
@@ -184,11 +196,12 @@ struct ChunkBars {
         item_full = o_free + 2;
         item_empty = item_full + 2;
         fin = item_empty + 2;
+        ml = fin + 1;
     }
 };
 
 // ---- the producer warp: pieces; per step the entries K_j, V_j ----
-template <typename C, int HD>
+template <typename C, int HD, bool NARROW>
 __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUtensorMap* tmK,
                                                const CUtensorMap* tmV, const CUtensorMap* tmQ,
                                                uint8_t* smem, const ChunkBars<C>& b, ChunkSlot* items,
@@ -231,7 +244,7 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
         }
         idx = __shfl_sync(0xffffffffu, idx, 0);
         ChunkItem it{};
-        if (idx >= 0) it = chunk_item(p, k == 0 ? piece0 : p.pieces[idx]);
+        if (idx >= 0) it = chunk_item<NARROW>(p, k == 0 ? piece0 : p.pieces[idx]);
         if (lane == 0) {
             items[slot].it = it;
             items[slot].idx = idx;
@@ -506,7 +519,7 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
 }
 
 // ---- the MMA issuer (one thread) ----
-template <typename C, int HD>
+template <typename C, int HD, bool NARROW>
 __device__ __forceinline__ void chunk_mma(const ChunkParams& p, uint8_t* smem, uint32_t tmem,
                                           const ChunkBars<C>& b, const ChunkSlot* items,
                                           volatile int* abort_flag) {
@@ -518,7 +531,7 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, uint8_t* smem, u
     const uint32_t q_lo0 = tc5::desc_lo_sw128(aQ, 16), r_lo0 = tc5::desc_lo_sw128(aR, 16),
                    v_lo0 = tc5::desc_lo_sw128(aR, C::GROUP_HALF);
     auto issue_s = [&](int X, int st) {
-        const uint32_t qx = q_lo0 + (uint32_t)(X * (C::TILE_BYTES >> 4));
+        const uint32_t qx = q_lo0 + (uint32_t)((NARROW ? 0 : X) * (C::TILE_BYTES >> 4));
         const uint32_t kx = r_lo0 + (uint32_t)(st * (C::TILE_BYTES >> 4));
         const uint32_t d = tmem + kColS + (uint32_t)(X * kT);
 #pragma unroll
@@ -550,6 +563,35 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, uint8_t* smem, u
         if (idx < 0 || *abort_flag) break;
         if (!wait_bar(&b.q_full[k & 1], (k >> 1) & 1) || !wait_entry(rbase)) { ok = false; break; }
         tc5::fence_after_sync();
+        if constexpr (NARROW) {
+            // S_A(0), S_B(1), then PV_X(j), S_X(j + 2) of X = j & 1; one tile reads an entry
+            auto score = [&](int j) {
+                const uint32_t gk = rbase + 2u * j;
+                if (!wait_entry(gk)) return false;
+                tc5::fence_after_sync();
+                issue_s(j & 1, (int)(gk % C::STAGES));
+                tc5::commit(&b.empty[gk % C::STAGES]);
+                if (j == it.T - 1) tc5::commit(b.q_free);
+                return true;
+            };
+            ok = score(0) && (it.T < 2 || score(1));
+            if (ok && k > 0 && (!wait_bar(&b.o_free[0], (k - 1) & 1) || !wait_bar(&b.o_free[1], (k - 1) & 1)))
+                ok = false;
+            for (int j = 0; j < it.T && ok; ++j) {
+                const uint32_t gv = rbase + 2u * j + 1u;
+                if (!wait_entry(gv) || !wait_bar(&b.p_full[j & 1], ((j & 1) ? np_b++ : np_a++) & 1)) {
+                    ok = false;
+                    break;
+                }
+                issue_pv(j & 1, (int)(gv % C::STAGES), j > 1);
+                tc5::commit(&b.empty[gv % C::STAGES]);
+                if (j + 2 < it.T) ok = score(j + 2);
+            }
+            if (!ok) break;
+            tc5::commit(b.drain);
+            rbase += 2u * (uint32_t)it.T;
+            continue;
+        }
         const int st0 = (int)(rbase % C::STAGES);
         if (it.T_a > 0) issue_s(0, st0);
         if (it.T_b > 0) issue_s(1, st0);
@@ -593,11 +635,11 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, uint8_t* smem, u
     }
 }
 
-template <typename QT, typename KT, int HD>
-__global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_attention_kernel(
+template <typename QT, typename KT, int HD, bool NARROW>
+__global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) chunk_attention_kernel(
     ChunkParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
     const __grid_constant__ CUtensorMap tmQ) {
-    using C = ChunkCfg<QT, KT, HD>;
+    using C = ChunkCfg<QT, KT, HD, NARROW>;
     using MT = typename C::MT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -628,6 +670,7 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
         mbar_init(b.q_free, 1);
         mbar_init(b.drain, 1);
         mbar_init(b.fin, 1);
+        mbar_init(b.ml, kT);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -642,9 +685,9 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
     if (warp >= 8) {
         tc5::setmaxnreg_dec<C::AUX_REGS>();
         if (warp == 8) {
-            chunk_producer<C, HD>(p, &tmK, &tmV, &tmQ, smem, b, items, abort_flag);
+            chunk_producer<C, HD, NARROW>(p, &tmK, &tmV, &tmQ, smem, b, items, abort_flag);
         } else if (warp == 9) {
-            if (lane == 0) chunk_mma<C, HD>(p, smem, tmem, b, items, abort_flag);
+            if (lane == 0) chunk_mma<C, HD, NARROW>(p, smem, tmem, b, items, abort_flag);
             __syncwarp();
         } else if (warp == 10) {
             // a piece's Q rows into L2 when it is published, before the Q buffer frees
@@ -675,7 +718,7 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t colS = tmem + lane_base + kColS + (uint32_t)(X * kT),
                        colO = tmem + lane_base + kColO + (uint32_t)(X * kT);
-        const int G = p.group, qi = X * p.qpt + r / G;      // the row's token of the item
+        const int G = p.group, qi = (NARROW ? 0 : X * p.qpt) + r / G;   // the row's token of the item
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         bool ok = true;
         uint32_t rbase = 0, ns = 0;
@@ -683,7 +726,7 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
         int idx = take_item(items, b.item_full, b.item_empty, 0, it, abort_flag, p.status);
         for (int k = 0; idx >= 0 && ok; ++k) {
             const int Tx = X ? it.T_b : it.T_a;
-            const bool row_valid = r < (X ? it.qn_b : it.qn_a) * G;
+            const bool row_valid = r < (X && !NARROW ? it.qn_b : it.qn_a) * G;
             const int pos = it.p0 + qi;                     // sees t <= pos, t > pos - window or t < sinks
             float qk = p.qk_scale_log2;
             if constexpr (C::SCALE_Q) {
@@ -691,7 +734,7 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
                 if (Tx > 0) {
                     ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&b.q_full[k & 1], (k >> 1) & 1));
                     if (!ok) break;
-                    const int e = reinterpret_cast<const int8_t*>(smem + C::OFF_BACK)[(k & 1) * 256 + X * kT + r];
+                    const int e = reinterpret_cast<const int8_t*>(smem + C::OFF_BACK)[(k & 1) * 256 + (NARROW ? 0 : X * kT) + r];
                     qk *= __uint_as_float((uint32_t)(127 - e) << 23);
                 }
             }
@@ -700,7 +743,8 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
                 const bool got = !*abort_flag && mbar_wait(&b.s_full[X], ns++ & 1);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc5::fence_after_sync();
-                const int t0 = tile_of(it, j) * kT;
+                const int step = NARROW ? 2 * j + X : j;
+                const int t0 = tile_of(it, step) * kT;
                 // columns c <= lim, and of these c > low or c < kept, are seen
                 const int lim = pos - t0, low = pos - p.window - t0, kept = p.sinks - t0;
                 const bool masked = !__all_sync(0xffffffffu, lim >= kT - 1 && (low < 0 || kept >= kT));
@@ -771,8 +815,8 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
                 if constexpr (!C::WIDE) {
                     // the row tile whose P.V reads a V tile first zeroes what no row sees of it
                     const TileRows rows = rows_of_tile(it, p.sinks, t0);
-                    if (rows.any() && (X == 0 || j >= it.T_a)) {
-                        const uint32_t gv = rbase + 2u * j + 1u;
+                    if (rows.any() && (NARROW || X == 0 || j >= it.T_a)) {
+                        const uint32_t gv = rbase + 2u * step + 1u;
                         if (!__all_sync(0xffffffffu, mbar_wait(&b.full[gv % C::STAGES], (gv / C::STAGES) & 1))) {
                             ok = false;
                             break;
@@ -798,10 +842,43 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD>::THREADS), 1) chunk_atte
             ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(b.drain, k & 1));
             if (!ok) break;
             tc5::fence_after_sync();
+            if (NARROW && X == 1) {
+                // tile A's threads add this state to theirs (O_B lies in the same lanes)
+                reinterpret_cast<float2*>(smem + C::OFF_ML)[r] = make_float2(m_run, l_run);
+                tc5::fence_before_sync();
+                mbar_arrive(b.ml);
+                it = nx;
+                continue;
+            }
             uint32_t ov[HD / 32][32];
 #pragma unroll
             for (int c4 = 0; c4 < HD / 32; ++c4) tc5::ld_32x32b_x32(colO + (uint32_t)(c4 * 32), ov[c4]);
             tc5::wait_ld();
+            if constexpr (NARROW) {
+                ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(b.ml, k & 1));
+                if (!ok) break;
+                tc5::fence_after_sync();
+                const float2 other = reinterpret_cast<const float2*>(smem + C::OFF_ML)[r];
+                if (it.T_b > 0) {
+                    const float M = fmaxf(m_run, other.x);
+                    const float fa = m_run == -INFINITY ? 0.f : fast_exp2(m_run - M);
+                    const float fb = other.x == -INFINITY ? 0.f : fast_exp2(other.x - M);
+                    // (l is not 0 where its tile holds NaN but no finite score)
+                    l_run = M == -INFINITY ? l_run + other.y : fmaf(l_run, fa, other.y * fb);
+                    m_run = M;
+#pragma unroll
+                    for (int c4 = 0; c4 < HD / 32; ++c4) {
+                        uint32_t o[32];
+                        tc5::ld_32x32b_x32(colO + (uint32_t)(kT + c4 * 32), o);
+                        tc5::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            ov[c4][e] = __float_as_uint(fmaf(__uint_as_float(ov[c4][e]), fa, __uint_as_float(o[e]) * fb));
+                    }
+                }
+                tc5::fence_before_sync();
+                mbar_arrive(&b.o_free[1]);
+            }
             tc5::fence_before_sync();
             mbar_arrive(&b.o_free[X]);
             if (row_valid && it.slot >= 0) {
@@ -856,9 +933,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
     constexpr int V = HD / 32, FLY = 8;
     const ChunkCut cut = p.cuts[blockIdx.x];
     if ((int)blockIdx.x >= p.head->cuts) return;
-    const int kvh = cut.kvh, c0 = cut.c0, c1 = cut.c1, q_begin = cut.q_begin, n = cut.n, q0 = cut.pair * 2 * p.qpt;
+    const int kvh = cut.kvh, c0 = cut.c0, c1 = cut.c1, q_begin = cut.q_begin, n = cut.n, q0 = cut.pair * p.item_tokens;
     const int lane = threadIdx.x & 31, warps = gridDim.y * 8;
-    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < 2 * kT; row += warps) {
+    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < p.part_rows; row += warps) {
         const int X = row >> 7, r = row & (kT - 1), tok = q0 + X * p.qpt + r / p.group;
         if (r >= p.qpt * p.group || tok >= n) continue;
         float M = -INFINITY, L = 0.f, A[V];
@@ -910,15 +987,15 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
     }
 }
 
-template <typename QT, typename KT, int HD>
+template <typename QT, typename KT, int HD, bool NARROW>
 cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
-    using C = ChunkCfg<QT, KT, HD>;
+    using C = ChunkCfg<QT, KT, HD, NARROW>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = chunk_attention_kernel<QT, KT, HD>;
+    auto kernel = chunk_attention_kernel<QT, KT, HD, NARROW>;
     if (!attr_set[dev]) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (err != cudaSuccess) return err;
@@ -956,9 +1033,15 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, chunk_join_kernel<QT, HD>, p);
 }
 
+template <typename QT, typename KT, int HD>
+cudaError_t launch_chunk_rows(const ChunkParams& p, cudaStream_t stream) {
+    return p.item_tokens == p.qpt ? launch_chunk_typed<QT, KT, HD, true>(p, stream)
+                                  : launch_chunk_typed<QT, KT, HD, false>(p, stream);
+}
+
 template <typename QT, typename KT>
 cudaError_t launch_chunk_kv(const ChunkParams& p, int head_dim, cudaStream_t stream) {
-    return head_dim == 128 ? launch_chunk_typed<QT, KT, 128>(p, stream) : launch_chunk_typed<QT, KT, 64>(p, stream);
+    return head_dim == 128 ? launch_chunk_rows<QT, KT, 128>(p, stream) : launch_chunk_rows<QT, KT, 64>(p, stream);
 }
 
 }  // namespace

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     auto pairs_of = [&](int q0, int q1, int ctx) {
         const int64_t n = (int64_t)q1 - q0;
         if (n >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= n && ctx <= cap)
-            return (int)(((uint32_t)n + 2 * p.qpt - 1) / (uint32_t)(2 * p.qpt));
+            return (int)(((uint32_t)n + p.item_tokens - 1) / (uint32_t)(p.item_tokens));
         set_status(p.status, PKV_DEV_BAD_CONTEXT);
         return 0;
     };
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
             s_seq[rank] = me;
         }
         __syncthreads();
-        const int pairs = tid < S ? (s_seq[tid].n + 2 * p.qpt - 1) / (2 * p.qpt) : 0;
+        const int pairs = tid < S ? (s_seq[tid].n + p.item_tokens - 1) / (p.item_tokens) : 0;
         int all;
         s_prefix[tid] = block_scan(pairs, wsum[0], &all);
         carry = all;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
             r.q.ctx = p.context_lens[lo];
         }
         r.pair = prefix[lo + 1] - 1 - g;
-        const int a = r.pair * 2 * p.qpt, b = min(r.q.n, a + 2 * p.qpt), before = r.q.ctx - r.q.n;
+        const int a = r.pair * p.item_tokens, b = min(r.q.n, a + p.item_tokens), before = r.q.ctx - r.q.n;
         r.steps = chunk_span(before + a, before + b, p.window, p.sinks).steps;
         return r;
     };

@@ -89,6 +89,25 @@ def test_whole_items_from_the_counter(kv_type):
     run(rng, lens, new, 8, 4, 64, 16, "bf16", kv_type, 40, 2)
 
 
+@pytest.mark.parametrize("q_type,kv_type", [("bf16", "bf16"), ("f16", "fp4")])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (150, 3)])
+def test_whole_items_of_two_tiles_from_the_counter(q_type, kv_type, window, sinks):
+    rng = np.random.default_rng(40)
+    S = 30
+    lens = rng.integers(100, 600, S).tolist()
+    new = [int(rng.integers(60, min(n, 200))) for n in lens]
+    run(rng, lens, new, 16, 4, 64, 16, q_type, kv_type, window, sinks)
+
+
+@pytest.mark.parametrize("q_type,kv_type", TYPES)
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 9])
+def test_few_rows_of_every_number_of_steps(q_type, kv_type, steps):
+    """Items of one row tile, whose steps the two halves of a CTA take in turn."""
+    rng = np.random.default_rng(steps)
+    S = 170                                            # more items than CTAs: none is cut
+    run(rng, [128 * steps - int(rng.integers(0, 100)) for _ in range(S)], [2] * S, 2, 1, 64, 16, q_type, kv_type)
+
+
 def test_many_sequences():
     """More sequences than the planner ranks, empty ones among them."""
     rng = np.random.default_rng(5)
