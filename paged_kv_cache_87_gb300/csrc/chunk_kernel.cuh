@@ -62,8 +62,8 @@ struct ChunkCfg {
     static constexpr int RAWS = WIDE ? (HD == 64 ? 6 : FP4 ? 3 : 4) : 0;
     static constexpr int WARPS = WIDE ? 16 : 12;
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int ROW_REGS = WIDE ? 200 : 216;
-    static constexpr int AUX_REGS = WIDE ? 56 : 72;
+    static constexpr int ROW_REGS = WIDE ? 184 : 216;
+    static constexpr int AUX_REGS = 72;
     static constexpr float LIFT = std::is_same<MT, F16>::value ? 7.f : 0.f;
     static constexpr int ITEM_READERS = 10 + (WIDE ? 4 : 0);
     static constexpr int OFF_Q = 0;
