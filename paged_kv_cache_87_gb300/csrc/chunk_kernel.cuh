@@ -351,36 +351,36 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// One raw entry at shared address `raw` into the operand tile at `to`; CLEAN: rows of V that no row
-// of the item sees become zeros.  All loads of a thread go out before its first store: a warp is
-// alone on its scheduler but for two softmax warps, so what hides latency is its own instructions
-// (with a load behind every store an entry took 1,700 cycles).
-template <typename C, int HD, bool CLEAN>
-__device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t to, int logB, int tid, const TileRows& rows) {
-    const int B = 1 << logB;
+// One raw entry at shared address `raw` into the operand tile at `to`, by 128 threads, in a rolled
+// loop whose next loads are in flight.  Its code is short on purpose: a sub-partition runs a widening
+// warp beside two softmax warps, and what does not fit its instruction cache beside them costs more
+// than the loop (unrolled whole: drafts over FP8 125 us; in two copies, for rows to be zeroed and
+// not: 153; with a load behind every store: 157).
+template <typename C, int HD>
+__device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t to, int logB, int tid) {
     if constexpr (C::FP4) {
-        // a thread a row: its 16 bytes of each 32 dims, its scales; eight lanes read 128 bytes and
-        // write eight different 16-byte columns
-        const int rr = tid & (B - 1);
-        const uint32_t blk = raw + (tid >> logB) * (B * C::RAW_ROW);
-        uint4 w[HD / 32];
-        uint32_t sc[HD / 64];
-#pragma unroll
-        for (int ch = 0; ch < HD / 32; ++ch) w[ch] = lds128(blk + (ch * B + rr) * 16);
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i)
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc[i]) : "r"(blk + B * (HD / 2) + rr * (HD / 16) + 4 * i) : "memory");
-        // a scale of zero makes a row's values zeros (codes are finite)
-        if (CLEAN && rows.hidden(tid)) {
-#pragma unroll
-            for (int i = 0; i < HD / 64; ++i) sc[i] = 0u;
-        }
-        const uint32_t row = to + (tid >> 3) * C::GROUP_BYTES + (tid & 7) * 128, x7 = (tid & 7) << 4;
-#pragma unroll
-        for (int ch = 0; ch < HD / 32; ++ch) {
-            const uint32_t pair = (ch & 1) ? e4m3x2_of<1>(sc[ch >> 1]) : e4m3x2_of<0>(sc[ch >> 1]);
+        // a thread a row: its 16 bytes of each 32 dims and the two scales of these; eight lanes read
+        // 128 bytes and write eight different 16-byte columns
+        const int B = 1 << logB, rr = tid & (B - 1);
+        uint32_t at = raw + (tid >> logB) * (B * C::RAW_ROW) + rr * 16;
+        uint32_t sc_at = raw + (tid >> logB) * (B * C::RAW_ROW) + B * (HD / 2) + rr * (HD / 16);
+        uint32_t row = to + (tid >> 3) * C::GROUP_BYTES + (tid & 7) * 128, col = (tid & 7) << 4;
+        uint4 w = lds128(at);
+        uint16_t sc;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc) : "r"(sc_at) : "memory");
+#pragma unroll 1
+        for (int ch = 0;;) {
+            uint4 w_next = w;
+            uint16_t sc_next = sc;
+            if (ch + 1 < HD / 32) {
+                at += B * 16;
+                sc_at += 2;
+                w_next = lds128(at);
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc_next) : "r"(sc_at) : "memory");
+            }
+            const uint32_t pair = e4m3x2_of<0>(sc);
             const __half2 two = *reinterpret_cast<const __half2*>(&pair);
-            const uint32_t word[4] = {w[ch].x, w[ch].y, w[ch].z, w[ch].w};
+            const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const __half2 s = i < 2 ? __low2half2(two) : __high2half2(two);
@@ -391,38 +391,45 @@ __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t to, int logB, 
                     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x[e]), s);
                     x[e] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                const int c = 4 * ch + i;
-                sts128(row + (c >> 3) * C::GROUP_HALF + (((c & 7) << 4) ^ x7), x[0], x[1], x[2], x[3]);
+                sts128(row + (col ^ (i << 4)), x[0], x[1], x[2], x[3]);
             }
+            if (++ch == HD / 32) break;
+            col ^= 64;                                   // four columns on, in the slice's other half
+            if (!(ch & 1)) row += C::GROUP_HALF;
+            w = w_next;
+            sc = sc_next;
         }
     } else {
         // a thread 16 codes at a time: eight lanes read 128 bytes; of a row's two halves one writes
         // its odd column first, so that eight lanes write eight different columns
-        constexpr int PER = HD / 16, UNITS = kT * PER / 128, STEP = 128 / PER;   // rows from unit to unit
-        uint4 w[UNITS];
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) w[u] = lds128(raw + (u * 128 + tid) * 16);
-        const int r0 = tid / PER, c = tid % PER;
+        constexpr int PER = HD / 16, UNITS = kT * PER / 128;
+        const int r0 = tid / PER, c = tid % PER;         // (the next unit's row is a multiple of 8 on)
         const bool odd = HD == 128 && c >= 4;
-        // STEP is a multiple of 8: rows r0 + u STEP have the same place in their groups
-        const uint32_t at = to + (r0 >> 3) * C::GROUP_BYTES + (r0 & 7) * 128 + (c >> 2) * C::GROUP_HALF;
-        const uint32_t lo = ((2 * c + odd) & 7) << 4, hi = ((2 * c + !odd) & 7) << 4, x7 = (r0 & 7) << 4;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-            const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-            uint32_t x[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = e4m3x2_of<0>(word[i]);
-                x[2 * i + 1] = e4m3x2_of<1>(word[i]);
+        uint32_t at = raw + tid * 16;
+        uint32_t out = to + (r0 >> 3) * C::GROUP_BYTES + (r0 & 7) * 128 + (c >> 2) * C::GROUP_HALF;
+        const uint32_t x7 = (r0 & 7) << 4;
+        const uint32_t first = (((2 * c + odd) & 7) << 4) ^ x7, second = (((2 * c + !odd) & 7) << 4) ^ x7;
+        uint4 w[2] = {lds128(at), lds128(at + 2048)};
+#pragma unroll 1
+        for (int u = 0;;) {
+            uint4 next[2] = {w[0], w[1]};
+            u += 2;
+            if (u < UNITS) {
+                at += 4096;
+                next[0] = lds128(at);
+                next[1] = lds128(at + 2048);
             }
-            if (CLEAN && rows.hidden(r0 + u * STEP)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0u;
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t a0 = odd ? w[i].z : w[i].x, a1 = odd ? w[i].w : w[i].y;
+                const uint32_t b0 = odd ? w[i].x : w[i].z, b1 = odd ? w[i].y : w[i].w;
+                sts128(out + first, e4m3x2_of<0>(a0), e4m3x2_of<1>(a0), e4m3x2_of<0>(a1), e4m3x2_of<1>(a1));
+                sts128(out + second, e4m3x2_of<0>(b0), e4m3x2_of<1>(b0), e4m3x2_of<0>(b1), e4m3x2_of<1>(b1));
+                out += 4096;                             // 128 / PER rows on: HD 128 and 64 alike
             }
-            const uint32_t to_u = at + u * (STEP >> 3) * C::GROUP_BYTES;
-            sts128(to_u + (lo ^ x7), odd ? x[4] : x[0], odd ? x[5] : x[1], odd ? x[6] : x[2], odd ? x[7] : x[3]);
-            sts128(to_u + (hi ^ x7), odd ? x[0] : x[4], odd ? x[1] : x[5], odd ? x[2] : x[6], odd ? x[3] : x[7]);
+            if (u >= UNITS) break;
+            w[0] = next[0];
+            w[1] = next[1];
         }
     }
 }
@@ -435,13 +442,13 @@ __device__ __forceinline__ int scale_q_row(uint32_t tile, int r) {
     const uint32_t row = tile + r * 128, x7 = (r & 7) << 4;
     auto at = [&](int c) { return row + (c >> 3) * C::HALF_BYTES + (((c & 7) << 4) ^ x7); };
     uint32_t top = 0u;                 // the largest magnitudes of even and of odd dims
+#pragma unroll 1
+    for (int c0 = 0; c0 < HD / 8; c0 += 4) {
+        uint4 w[4];
 #pragma unroll
-    for (int c0 = 0; c0 < HD / 8; c0 += 8) {
-        uint4 w[8];
+        for (int c = 0; c < 4; ++c) w[c] = lds128(at(c0 + c));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = lds128(at(c0 + c));
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
             top = __vmaxu2(top, w[c].x & 0x7fff7fffu);
             top = __vmaxu2(top, w[c].y & 0x7fff7fffu);
             top = __vmaxu2(top, w[c].z & 0x7fff7fffu);
@@ -451,13 +458,13 @@ __device__ __forceinline__ int scale_q_row(uint32_t tile, int r) {
     const int ex = (int)(max(top >> 16, top & 0xffffu) >> 7) - 127;    // floor(log2); 128: not finite
     const int e = ex == 128 ? 0 : min(14 - ex, 60);
     const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll 1
+    for (int c0 = 0; c0 < HD / 8; c0 += 2) {
+        uint4 w[2];
 #pragma unroll
-    for (int c0 = 0; c0 < HD / 8; c0 += 4) {
-        uint4 w[4];
+        for (int c = 0; c < 2; ++c) w[c] = lds128(at(c0 + c));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = lds128(at(c0 + c));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
             uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -476,34 +483,46 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
                                               const ChunkSlot* items, volatile int* abort_flag) {
     const int tid = threadIdx.x - 384, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
-    uint32_t g = 0;
+    int st = 0, rs = 0;                                  // an entry's places, and their phases
+    uint32_t st_phase = 0, rs_phase = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
         ChunkItem it{};
         const int idx = take_item(items, b.item_full, b.item_empty, k, it, abort_flag, p.status);
         if (idx < 0 || *abort_flag) break;
-        for (int i = 0; i < 2 * it.T; ++i, ++g) {
-            const int rs = (int)(g % C::RAWS), st = (int)(g % C::STAGES);
-            const TileRows rows = rows_of_tile(it, p.sinks, tile_of(it, i >> 1) * kT);
-            if (!mbar_wait(&b.raw_full[rs], (g / C::RAWS) & 1) || !mbar_wait(&b.empty[st], ((g / C::STAGES) & 1) ^ 1u)) {
+#pragma unroll 1
+        for (int i = 0; i < 2 * it.T; ++i) {
+            if (!mbar_wait(&b.raw_full[rs], rs_phase) || !mbar_wait(&b.empty[st], st_phase ^ 1u)) {
                 ok = false;
                 break;
             }
-            const uint32_t raw = base + C::OFF_RAW + rs * C::RAW_BYTES, to = base + C::OFF_RING + st * C::TILE_BYTES;
-            if ((i & 1) && rows.any()) widen_tile<C, HD, true>(raw, to, p.log_block, tid, rows);
-            else widen_tile<C, HD, false>(raw, to, p.log_block, tid, rows);
+            const uint32_t to = base + C::OFF_RING + st * C::TILE_BYTES;
+            widen_tile<C, HD>(base + C::OFF_RAW + rs * C::RAW_BYTES, to, p.log_block, tid);
+            if (i & 1) {
+                // rows of V that no row of the item sees become zeros
+                const TileRows rows = rows_of_tile(it, p.sinks, tile_of(it, i >> 1) * kT);
+                if (rows.any()) {
+                    named_bar_sync(2, 128);              // every row has been written
+                    if (rows.hidden(tid))
+#pragma unroll 1
+                        for (int c = 0; c < HD / 8; ++c) sts128(to + operand_at<C>(tid, c), 0u, 0u, 0u, 0u);
+                }
+            }
             fence_proxy_async_smem();                    // the MMAs, and the copies that reuse the raw bytes
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&b.full[st]);
                 mbar_arrive(&b.raw_empty[rs]);
             }
+            if (++st == C::STAGES) { st = 0; st_phase ^= 1u; }
+            if (++rs == C::RAWS) { rs = 0; rs_phase ^= 1u; }
             if (C::SCALE_Q && i == 0) {
                 if (!mbar_wait(b.q_raw, k & 1)) {
                     ok = false;
                     break;
                 }
                 int8_t* back = reinterpret_cast<int8_t*>(smem + C::OFF_BACK) + (k & 1) * 256;
+#pragma unroll 1
                 for (int X = 0; X < (it.qn_b > 0 ? 2 : 1); ++X)
                     back[X * kT + tid] = (int8_t)scale_q_row<C, HD>(base + C::OFF_Q + X * C::TILE_BYTES, tid);
                 fence_proxy_async_smem();
