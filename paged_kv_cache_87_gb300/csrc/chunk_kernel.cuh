@@ -797,7 +797,7 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) ch
                 const bool resc = j > 0 && m_new != m_run;
                 if (__any_sync(0xffffffffu, resc)) {
                     const float f = resc ? fast_exp2(m_run - m_new) : 1.f;
-#pragma unroll
+#pragma unroll 1
                     for (int c4 = 0; c4 < HD / 32; ++c4) {
                         uint32_t o[32];
                         tc5::ld_32x32b_x32(colO + (uint32_t)(c4 * 32), o);
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) ch
                         }
                         if (rows.hidden(r)) {
                             uint8_t* vrow = smem + C::OFF_RING + (gv % C::STAGES) * C::TILE_BYTES;
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < HD / 8; ++c)
                                 *reinterpret_cast<uint4*>(vrow + operand_at<C>(r, c)) = make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -869,69 +869,71 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) ch
                 it = nx;
                 continue;
             }
-            uint32_t ov[HD / 32][32];
-#pragma unroll
-            for (int c4 = 0; c4 < HD / 32; ++c4) tc5::ld_32x32b_x32(colO + (uint32_t)(c4 * 32), ov[c4]);
-            tc5::wait_ld();
+            float fa = 1.f, fb = 0.f;                     // NARROW: the shares of the two states
             if constexpr (NARROW) {
                 ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(b.ml, k & 1));
                 if (!ok) break;
                 tc5::fence_after_sync();
-                const float2 other = reinterpret_cast<const float2*>(smem + C::OFF_ML)[r];
                 if (it.T_b > 0) {
+                    const float2 other = reinterpret_cast<const float2*>(smem + C::OFF_ML)[r];
                     const float M = fmaxf(m_run, other.x);
-                    const float fa = m_run == -INFINITY ? 0.f : fast_exp2(m_run - M);
-                    const float fb = other.x == -INFINITY ? 0.f : fast_exp2(other.x - M);
+                    fa = m_run == -INFINITY ? 0.f : fast_exp2(m_run - M);
+                    fb = other.x == -INFINITY ? 0.f : fast_exp2(other.x - M);
                     // (l is not 0 where its tile holds NaN but no finite score)
                     l_run = M == -INFINITY ? l_run + other.y : fmaf(l_run, fa, other.y * fb);
                     m_run = M;
-#pragma unroll
-                    for (int c4 = 0; c4 < HD / 32; ++c4) {
-                        uint32_t o[32];
-                        tc5::ld_32x32b_x32(colO + (uint32_t)(kT + c4 * 32), o);
-                        tc5::wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            ov[c4][e] = __float_as_uint(fmaf(__uint_as_float(ov[c4][e]), fa, __uint_as_float(o[e]) * fb));
-                    }
                 }
-                tc5::fence_before_sync();
-                mbar_arrive(&b.o_free[1]);
             }
-            tc5::fence_before_sync();
-            mbar_arrive(&b.o_free[X]);
-            if (row_valid && it.slot >= 0) {
-                const int64_t row = (int64_t)it.slot * p.part_rows + X * kT + r;
-                p.part_ml[row] = make_float2(m_run, l_run);
-                if (Tx > 0) {
-                    float* dst = p.part_acc + row * HD;      // 32-byte aligned
-#pragma unroll
-                    for (int c4 = 0; c4 < HD / 32; ++c4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) st_global_v8(dst + c4 * 32 + 8 * e, ov[c4] + 8 * e);
-                }
-            } else if (row_valid) {
+            const bool whole = it.slot < 0;
+            if (whole) {
                 const float inv = l_run != 0.f ? p.out_scale / l_run : 0.f;
-                uint16_t* dst0 = static_cast<uint16_t*>(p.out) +
-                                 ((int64_t)(it.q_row + qi) * p.num_q_heads + it.kvh * G + r % G) * HD;
+                fa *= inv;
+                fb *= inv;
+            }
+            const int64_t part = (int64_t)it.slot * p.part_rows + X * kT + r;
+            uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                            ((int64_t)(it.q_row + qi) * p.num_q_heads + it.kvh * G + r % G) * HD;
+            // 32 columns at a time, in a rolled loop (code that runs once an item should not drive the
+            // softmax's out of the instruction cache)
+#pragma unroll 1
+            for (int c4 = 0; c4 < HD / 32; ++c4) {
+                uint32_t o[32];
+                tc5::ld_32x32b_x32(colO + (uint32_t)(c4 * 32), o);
+                tc5::wait_ld();
+                if (!NARROW || it.T_b == 0) {
 #pragma unroll
-                for (int c4 = 0; c4 < HD / 32; ++c4) {
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fa);
+                } else {
+                    uint32_t o2[32];
+                    tc5::ld_32x32b_x32(colO + (uint32_t)(kT + c4 * 32), o2);
+                    tc5::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), fa, __uint_as_float(o2[e]) * fb));
+                }
+                if (!row_valid) continue;
+                if (whole) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        ov[c4][e] = pack2_bits<QT>(__uint_as_float(ov[c4][2 * e]) * inv,
-                                                   __uint_as_float(ov[c4][2 * e + 1]) * inv);
-                    uint16_t* dst = dst0 + c4 * 32;
+                        o[e] = pack2_bits<QT>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
                     if (out32) {
-                        st_global_v8(dst, ov[c4]);
-                        st_global_v8(dst + 16, ov[c4] + 8);
+                        st_global_v8(dst + c4 * 32, o);
+                        st_global_v8(dst + c4 * 32 + 16, o + 8);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4*>(dst)[e] = make_uint4(ov[c4][4 * e], ov[c4][4 * e + 1],
-                                                                          ov[c4][4 * e + 2], ov[c4][4 * e + 3]);
+                            reinterpret_cast<uint4*>(dst + c4 * 32)[e] =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
+                } else if (Tx > 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st_global_v8(p.part_acc + part * HD + c4 * 32 + 8 * e, o + 8 * e);
                 }
             }
+            if (row_valid && !whole) p.part_ml[part] = make_float2(m_run, l_run);
+            tc5::fence_before_sync();
+            mbar_arrive(&b.o_free[X]);
+            if (NARROW) mbar_arrive(&b.o_free[1]);
             it = nx;
         }
         if (!ok) {
