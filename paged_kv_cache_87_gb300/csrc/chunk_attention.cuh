@@ -75,21 +75,27 @@ struct ChunkPlan {
     size_t off_pieces, off_cuts, off_first, off_head, off_acc, off_ml, total;
 };
 
-// What a tile pair sees of its context, and so its steps: tiles [0, sink_tiles), then from tile
-// `first` to the one of its last token.  (Tokens below `low` that are no sinks are seen by no row.)
+// What an item sees of its context, and so its steps.  Blocks that none of its rows sees are left out:
+// it walks a virtual context, the blocks of the sinks and then, `skip` tokens on, those from the
+// window's first one.  Positions count in that context: they keep their order and their distances
+// within the window, and its tokens below `low` that are no sinks are seen by no row.  (With the
+// sinks' tokens in a tile of their own a window of 1,024 takes 10.5 steps an item instead of 9.)
 struct ChunkSpan {
-    int low, sink_tiles, first, steps;
+    int skip, sink_blocks, low, kv_end, steps;
 };
 
-__host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end, int window, int sinks) {
+__host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end, int window, int sinks,
+                                                         int log_block) {
     ChunkSpan w;
-    const int low = p_first - window;                  // the last token that the first row does not see
-    w.low = low < 0 ? 0 : low + 1;
-    const int kept = sinks < w.low ? sinks : w.low;
-    w.sink_tiles = (kept + kChunkTile - 1) / kChunkTile;
-    w.first = w.low / kChunkTile;
-    if (w.first < w.sink_tiles) w.first = w.sink_tiles;
-    w.steps = w.sink_tiles + (kv_end - 1) / kChunkTile + 1 - w.first;
+    const int past = p_first - window;                 // the last token that the first row does not see
+    const int low = past < 0 ? 0 : past + 1;
+    const int kept = sinks < low ? sinks : low;
+    w.sink_blocks = kept <= 0 ? 0 : ((kept - 1) >> log_block) + 1;
+    const int first = low >> log_block;
+    w.skip = first > w.sink_blocks ? (first - w.sink_blocks) << log_block : 0;
+    w.low = low - w.skip;
+    w.kv_end = kv_end - w.skip;
+    w.steps = (w.kv_end - 1) / kChunkTile + 1;
     return w;
 }
 

@@ -5,8 +5,8 @@
 // Organisation.  A row is a (new token, query head of the kv head's group) pair; an item is a
 // sequence, a kv head and two tiles of 128 rows (TMEM lanes), which share every K/V tile of 128
 // tokens.  S = Q K^T (M 128, N 128, fp32 in TMEM), a thread a row for the softmax, P over S's
-// columns as 16-bit pairs, O += P V (M 128, N d).  The steps of an item are the tiles that its rows
-// see: those of the sinks, then the window's; what is between is neither staged nor looked up.  A
+// columns as 16-bit pairs, O += P V (M 128, N d).  The steps of an item are the tiles of its
+// virtual context: the sinks' blocks, then the window's; what is between is neither staged nor looked up.  A
 // persistent CTA an SM takes pieces (runs of steps of an item) as the planner dealt them; the ring,
 // the MMAs and the softmax run on from one piece into the next.
 //
@@ -87,10 +87,11 @@ constexpr uint32_t kColS = 0, kColO = 256;           // S_X at 128 X (P_X over i
 // ---- a piece of work, as the CTA's warps see it ----
 struct ChunkItem {
     int s, kvh, q_row, q_begin;    // q_row: the first query row (token) of tile A in `query`
-    int p0;                        // its position
+    int p0;                        // its position (in the virtual context, as `low` and `kv_end`)
     int qn_a, qn_b;                // tokens of tiles A and B (B may have none)
     int T_a, T_b, T;               // steps of A, of B, of the piece (NARROW: 0, 2, .. are A's, 1, 3, .. B's)
-    int j0, sink_tiles, first;     // step j of the piece is tile j0 + j, or first + j0 + j - sink_tiles
+    int j0;                        // step j of the piece is tile j0 + j
+    int sink_blocks, skip;         // blocks from sink_blocks on are found `skip` tokens on
     int low, kv_end;               // tokens that some row sees: [0, sinks) and [low, kv_end)
     int slot;
 };
@@ -102,8 +103,7 @@ struct __align__(16) ChunkSlot {
 static_assert(sizeof(ChunkSlot) == 80, "two slots fill 160 bytes");
 
 __device__ __forceinline__ int tile_of(const ChunkItem& it, int j) {
-    const int jj = it.j0 + j;
-    return jj < it.sink_tiles ? jj : it.first + jj - it.sink_tiles;
+    return it.j0 + j;
 }
 
 // What of a tile some row sees: rows [0, a) and [b, e); the rest of V is zeroed.
@@ -132,11 +132,12 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const Chun
     it.p0 = ctx - n + q0;
     it.qn_a = min(p.qpt, n - q0);
     it.qn_b = NARROW ? 0 : max(0, min(p.qpt, n - q0 - p.qpt));
-    it.kv_end = it.p0 + it.qn_a + it.qn_b;
-    const ChunkSpan w = chunk_span(it.p0, it.kv_end, p.window, p.sinks);
+    const ChunkSpan w = chunk_span(it.p0, it.p0 + it.qn_a + it.qn_b, p.window, p.sinks, p.log_block);
     it.low = w.low;
-    it.sink_tiles = w.sink_tiles;
-    it.first = w.first;
+    it.kv_end = w.kv_end;
+    it.sink_blocks = w.sink_blocks;
+    it.skip = w.skip;
+    it.p0 -= w.skip;
     it.j0 = x.j0;
     it.T = x.j1 - x.j0;
     it.slot = x.slot;
@@ -146,7 +147,7 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const Chun
         return it;
     }
     // steps of tile A alone: its last token lies in an earlier tile, perhaps
-    const int steps_a = w.sink_tiles + (it.p0 + it.qn_a - 1) / kT + 1 - w.first;
+    const int steps_a = (it.p0 + it.qn_a - 1) / kT + 1;
     it.T_a = max(0, min(steps_a - x.j0, it.T));
     it.T_b = it.qn_b > 0 ? it.T : 0;
     if (it.qn_b == 0) it.T_a = it.T;
@@ -259,7 +260,8 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
             const TileRows r = rows_of_tile(it, p.sinks, t0);
             const bool in = j < it.T && lane < per_tile && r0 < r.e && (r0 < r.a || r0 + B > r.b);
             need = __ballot_sync(0xffffffffu, in);
-            return in ? trow[(t0 >> logB) + lane] : 0;
+            const int blk = (t0 >> logB) + lane;
+            return in ? trow[blk < it.sink_blocks ? blk : blk + (it.skip >> logB)] : 0;
         };
         unsigned need, need_next = 0;
         int cur = entry(0, need), nxt = 0;
@@ -778,10 +780,12 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) ch
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t seen = bits_below(lim + 1 - 32 * w) &
                                               (~bits_below(low + 1 - 32 * w) | bits_below(kept - 32 * w));
+                        if (__any_sync(0xffffffffu, seen != ~0u)) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            uint32_t& x = sv[w >> 1][32 * (w & 1) + c];
-                            x = (seen >> c & 1u) ? x : __float_as_uint(-INFINITY);
+                            for (int c = 0; c < 32; ++c) {
+                                uint32_t& x = sv[w >> 1][32 * (w & 1) + c];
+                                x = (seen >> c & 1u) ? x : __float_as_uint(-INFINITY);
+                            }
                         }
                     }
                 }

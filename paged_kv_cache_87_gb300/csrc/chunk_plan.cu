@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
         }
         r.pair = prefix[lo + 1] - 1 - g;
         const int a = r.pair * p.item_tokens, b = min(r.q.n, a + p.item_tokens), before = r.q.ctx - r.q.n;
-        r.steps = chunk_span(before + a, before + b, p.window, p.sinks).steps;
+        r.steps = chunk_span(before + a, before + b, p.window, p.sinks, p.log_block).steps;
         return r;
     };
     // all steps, and the longest item's

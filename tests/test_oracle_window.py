@@ -88,8 +88,8 @@ def test_virtual_contexts(B, tmp_path):
 
 
 def test_chunk_spans(tmp_path):
-    """chunk_span() of the planner, compiled for the host: its tiles hold every token that a row sees,
-    each in order, and no tile that none sees."""
+    """chunk_span() of the planner, compiled for the host: its blocks are those that hold a token that
+    a row sees, in order, and what it hides of them is what no row sees."""
     import ctypes
     import os
     import re
@@ -101,20 +101,30 @@ def test_chunk_spans(tmp_path):
     c = tmp_path / "span.cpp"
     c.write_text('#define __host__\n#define __device__\n#define __forceinline__ inline\n'
                  'constexpr int kChunkTile = 128;\n' + body +
-                 'extern "C" void span(int p, int e, int w, int s, int* o) { ChunkSpan x = chunk_span(p, e, w, s);\n'
-                 'o[0] = x.low; o[1] = x.sink_tiles; o[2] = x.first; o[3] = x.steps; }\n')
+                 'extern "C" void span(int p, int e, int w, int s, int b, int* o) {\n'
+                 'ChunkSpan x = chunk_span(p, e, w, s, b);\n'
+                 'o[0] = x.skip; o[1] = x.sink_blocks; o[2] = x.low; o[3] = x.kv_end; o[4] = x.steps; }\n')
     so = str(tmp_path / "span.so")
     subprocess.run(["g++", "-shared", "-fPIC", "-o", so, str(c)], check=True)
     lib = ctypes.CDLL(so)
     rng = np.random.default_rng(0)
-    for _ in range(600):
+    for _ in range(900):
+        log = int(rng.integers(3, 6))
+        B = 1 << log
         n = int(rng.integers(1, 2000))
         m = int(rng.integers(1, min(n, 300) + 1))
         w, s = int(rng.integers(1, 700)), int(rng.integers(0, 400))
-        o = (ctypes.c_int * 4)()
-        lib.span(n - m, n, w, s, o)
-        low, sink_tiles, first, steps = o
-        tiles = [j if j < sink_tiles else first + j - sink_tiles for j in range(steps)]
-        seen = np.flatnonzero(window.seen(n, m, w, s).any(0))
-        assert tiles == sorted(set((seen // 128).tolist())), (n, m, w, s)
-        assert set(seen.tolist()) == {t for t in range(n) if t < s or t >= low}
+        o = (ctypes.c_int * 5)()
+        lib.span(n - m, n, w, s, log, o)
+        skip, sink_blocks, low, kv_end, steps = o
+        assert skip % B == 0 and steps == -(-kv_end // 128)
+        seen = window.seen(n, m, w, s)
+        blocks = [j if j < sink_blocks else j + skip // B for j in range(-(-kv_end // B))]
+        assert blocks == sorted(set((np.flatnonzero(seen.any(0)) // B).tolist())), (n, m, w, s)
+        # every row, in the virtual context: the mask that the kernel forms from its position there
+        v = np.arange(kv_end)
+        t = np.array([blocks[x // B] * B + x % B for x in v])
+        pos = np.arange(n - m, n)[:, None] - skip
+        mine = (v <= pos) & ((v > pos - w) | (v < s))
+        assert (mine == seen[:, t]).all()
+        assert (((v < s) | (v >= low)) == seen[:, t].any(0)).all()
