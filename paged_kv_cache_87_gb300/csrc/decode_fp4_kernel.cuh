@@ -59,6 +59,7 @@
 #include "decode_fp4.cuh"
 
 #include "cache_row.cuh"
+#include "cluster.cuh"
 #include "tmap.cuh"
 
 namespace pkv {
@@ -116,27 +117,6 @@ __device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
     const __half2 h = *reinterpret_cast<const __half2*>(&x);
     const __half2 t = k ? __high2half2(h) : __low2half2(h);
     return *reinterpret_cast<const uint32_t*>(&t);
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Two or four floats of this CTA's shared memory, in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t place_in(const float* mine, int rank) {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(mine)), "r"(rank));
-    return at;
-}
-__device__ __forceinline__ void load_from(const float* mine, int rank, float& a, float& b) {
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(place_in(mine, rank)) : "memory");
-}
-__device__ __forceinline__ void load_from(const float* mine, int rank, float (&v)[2]) {
-    load_from(mine, rank, v[0], v[1]);
-}
-__device__ __forceinline__ void load_from(const float* mine, int rank, float (&v)[4]) {
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(place_in(mine, rank)) : "memory");
 }
 
 // What is left of (lo, hi) after pack_f16's rounding, as fp16 again.

@@ -65,7 +65,7 @@ cudaError_t launch_decode_simt(const DecodeParams& p, cudaStream_t stream) {
 // The prefix-aware entry point groups sequences that share leading blocks
 // (up to 16 query heads per shared unit) when a kv head has at most 8 query
 // heads: the NT = 2 kernel.  Otherwise NT = 1.
-template <typename QT, typename KT, int HD, int NT, bool WIN = false>
+template <typename QT, typename KT, int HD, int NT>
 cudaError_t launch_decode_mma_nt(const DecodeParams& p, cudaStream_t stream) {
     using Cfg = MmaCfg<QT, KT, HD, NT>;
     static OccCache occ;
@@ -73,7 +73,7 @@ cudaError_t launch_decode_mma_nt(const DecodeParams& p, cudaStream_t stream) {
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = decode_mma_kernel<QT, KT, HD, NT, WIN>;
+    auto kernel = decode_mma_kernel<QT, KT, HD, NT>;
     if (occ.ctas[dev] == 0) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)Cfg::SMEM);
@@ -162,27 +162,6 @@ cudaError_t dispatch_decode_kv(const DecodeParams& p, int hpi, cudaStream_t stre
     if (hpi == 1) return launch_decode_simt<QT, KT, 64, 1>(p, stream);
     if (hpi == 2) return launch_decode_simt<QT, KT, 64, 2>(p, stream);
     return launch_decode_simt<QT, KT, 64, 4>(p, stream);
-}
-
-// Contexts under a sliding window (p.window): the same kernels over virtual contexts.  16-bit
-// queries take the tensor cores wherever a stage's rows are 128 bytes or more, so the CUDA-core
-// kernel is left with fp32 queries and FP8 rows of 64 dims.
-template <typename QT, typename KT, int HD>
-cudaError_t dispatch_window_hd(const DecodeParams& p, int hpi, cudaStream_t stream) {
-    constexpr bool kFp8 = std::is_same<KT, E4M3>::value;
-    if constexpr (!std::is_same<QT, F32>::value && !(kFp8 && HD == 64)) {
-        return launch_decode_mma_nt<QT, KT, HD, 1, true>(p, stream);
-    } else {
-        if (hpi == 1) return launch_decode_simt<QT, KT, HD, 1, true>(p, stream);
-        if (hpi == 2) return launch_decode_simt<QT, KT, HD, 2, true>(p, stream);
-        return launch_decode_simt<QT, KT, HD, 4, true>(p, stream);
-    }
-}
-
-template <typename QT, typename KT>
-cudaError_t dispatch_window_kv(const DecodeParams& p, int hpi, cudaStream_t stream) {
-    return p.head_dim == 128 ? dispatch_window_hd<QT, KT, 128>(p, hpi, stream)
-                             : dispatch_window_hd<QT, KT, 64>(p, hpi, stream);
 }
 
 // Defined in decode_window_f32.cu / decode_window_f16.cu / decode_window_bf16.cu.

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(1024) plan_split_kernel(DecodeParams p) {
     for (int base = 0; base < p.num_seqs; base += blockDim.x) {
         const int s = base + tid;
         const bool valid = s < p.num_seqs;
-        int ctx = 0, raw = 0;      // tokens walked; tokens of the context (more under a window)
+        int ctx = 0;
         // entries this sequence's row has in common with its predecessor's (written by
         // prefix_common_kernel); it loads beside the context length
         const int common = can_group && valid ? __ldcg(p.ws.common + s) : 0;
@@ -288,8 +288,6 @@ __global__ void __launch_bounds__(1024) plan_split_kernel(DecodeParams p) {
                 set_status(p.status, PKV_DEV_BAD_CONTEXT);
                 ctx = ctx < 0 ? 0 : cap;
             }
-            raw = ctx;
-            if (p.window) ctx = window_span(ctx, p.window, p.sinks, p.log_block).tokens;
             p.ws.ctx_eff[s] = ctx;
         }
         s_ctx[tid] = ctx;
@@ -379,7 +377,7 @@ __global__ void __launch_bounds__(1024) plan_split_kernel(DecodeParams p) {
         const int my_gst = leader >= 0 ? s_sh[lp] / kTileTokens : 0;
         if (valid) {
             const int r = r0 + (members >= 2);
-            p.ws.rec[r] = make_int4(s, start, ctx, p.window ? raw : my_gbase);
+            p.ws.rec[r] = make_int4(s, start, ctx, my_gbase);
             p.ws.rec_prefix[r] = pbase;
             if (r < kPlanSmemRecords) s_rp[r] = pbase;
             p.ws.seq_info[s] = make_int4(priv_tiles, pbase, my_gbase, my_gst);
@@ -570,10 +568,8 @@ struct RecCursor {
     int group, id, start, end;  // kind, sequence / leader, token range [start, end)
     int members;                // sequences served
     int gbase;                  // private record: first tile of its group's record, or -1
-    int ctx;                    // under a window: tokens of the whole context
 };
 
-template <bool WIN>
 __device__ __forceinline__ void rec_set(RecCursor& rc, int lo, int hi, int4 e) {
     rc.lo = lo;
     rc.hi = hi;
@@ -582,27 +578,24 @@ __device__ __forceinline__ void rec_set(RecCursor& rc, int lo, int hi, int4 e) {
     rc.start = e.y;
     rc.end = e.z;
     rc.members = rc.group ? e.w : 1;
-    rc.gbase = rc.group || WIN ? -1 : e.w;
-    rc.ctx = e.w;
+    rc.gbase = rc.group ? -1 : e.w;
 }
 
-template <bool WIN>
 __device__ __forceinline__ void rec_load(const DecodeParams& p, RecCursor& rc) {
-    rec_set<WIN>(rc, __ldcg(&p.ws.rec_prefix[rc.r]), __ldcg(&p.ws.rec_prefix[rc.r + 1]),
+    rec_set(rc, __ldcg(&p.ws.rec_prefix[rc.r]), __ldcg(&p.ws.rec_prefix[rc.r + 1]),
             __ldcg(&p.ws.rec[rc.r]));
 }
 
 // The window starting at flattened tile `pos` of a worker whose range is
 // [a, end); `rc` advances in place to the record holding `pos` (global loads
 // only when the record changes).
-template <bool WIN>
 __device__ __forceinline__ Window make_window(const DecodeParams& p, int worker, int a, int end,
                                               int q, int pos, RecCursor& rc) {
     Window w{};
     if (pos >= end) return w;
     while (rc.hi <= pos) {
         ++rc.r;
-        rec_load<WIN>(p, rc);
+        rec_load(p, rc);
     }
     const int tiles = (rc.end - rc.start + kTileTokens - 1) / kTileTokens;
     const int rel = pos - rc.lo;
@@ -655,10 +648,7 @@ __device__ __forceinline__ void slot_head(const DecodeParams& p, int group, int 
 
 // --------------------------------------------------------------------- kernel --
 
-// WIN: contexts under a sliding window (p.window, p.sinks; NT = 1): the records hold virtual
-// contexts, blocks of the table are found through window_entry, and the hidden tokens, at most
-// two blocks' ends, are masked like those past the context.
-template <typename QT, typename KT, int HD, int NT, bool WIN = false>
+template <typename QT, typename KT, int HD, int NT>
 __global__ void __launch_bounds__(32 * (NT + 1), 4) decode_mma_kernel(DecodeParams p,
                                                         const __grid_constant__ CUtensorMap tmK,
                                                         const __grid_constant__ CUtensorMap tmV) {
@@ -709,19 +699,16 @@ __global__ void __launch_bounds__(32 * (NT + 1), 4) decode_mma_kernel(DecodePara
             const int4 wf = __ldcg(&p.ws.worker_first[2 * blockIdx.x]);
             const int4 e = __ldcg(&p.ws.worker_first[2 * blockIdx.x + 1]);
             rc.r = wf.x;
-            rec_set<WIN>(rc, wf.y, wf.z, e);
+            rec_set(rc, wf.y, wf.z, e);
         }
-        WindowSpan span{}, nspan{};
-        auto entry = [&](const WindowSpan& w, int j) { return WIN ? window_entry(w, j) : j; };
-        Window win = make_window<WIN>(p, blockIdx.x, a, end, q, a, rc);
+        Window win = make_window(p, blockIdx.x, a, end, q, a, rc);
         int pos = a;
         int e0 = 0, e1 = 0;
         if (win.valid) {
             const int32_t* trow = p.block_tables + (int64_t)win.s * p.max_blocks;
             const int jb0 = win.t0 / B, nb = (win.t1 + B - 1) / B - jb0;
-            if constexpr (WIN) span = window_span(rc.ctx, p.window, p.sinks, p.log_block);
-            e0 = lane < nb ? trow[entry(span, jb0 + lane)] : 0;
-            e1 = lane + 32 < nb ? trow[entry(span, jb0 + lane + 32)] : 0;
+            e0 = lane < nb ? trow[jb0 + lane] : 0;
+            e1 = lane + 32 < nb ? trow[jb0 + lane + 32] : 0;
         }
         while (win.valid && ok) {
             const int wtiles = (win.t1 - win.t0 + kTileTokens - 1) / kTileTokens;
@@ -751,7 +738,6 @@ __global__ void __launch_bounds__(32 * (NT + 1), 4) decode_mma_kernel(DecodePara
                     m.s = win.s; m.kvh = win.kvh; m.qsub = win.qsub; m.nh = win.nh;
                     m.chunk = win.seg; m.nchunks = win.members; m.ts = ts; m.te = te;
                     m.expect = win.expect; m.segoff = win.segoff;
-                    if constexpr (WIN) { m.hide_lo = span.hide_lo; m.hide_hi = span.hide_hi; }
                     m.flags = (first ? kFirst : 0) | (win.last && st == nstages - 1 ? kLast : 0) |
                               (win.group ? kGroup : 0);
                     mbar_arrive_expect_tx(&full[stage],
@@ -796,19 +782,17 @@ __global__ void __launch_bounds__(32 * (NT + 1), 4) decode_mma_kernel(DecodePara
                 if (st == 0) {
                     // look one window ahead once this window's first stage is in flight:
                     // its block-table entries load while this window streams
-                    nxt = make_window<WIN>(p, blockIdx.x, a, end, q, pos + wtiles, rc);
+                    nxt = make_window(p, blockIdx.x, a, end, q, pos + wtiles, rc);
                     if (nxt.valid) {
                         const int32_t* trow = p.block_tables + (int64_t)nxt.s * p.max_blocks;
                         const int nj0 = nxt.t0 / B, nnb = (nxt.t1 + B - 1) / B - nj0;
-                        if constexpr (WIN) nspan = window_span(rc.ctx, p.window, p.sinks, p.log_block);
-                        n0 = lane < nnb ? trow[entry(nspan, nj0 + lane)] : 0;
-                        n1 = lane + 32 < nnb ? trow[entry(nspan, nj0 + lane + 32)] : 0;
+                        n0 = lane < nnb ? trow[nj0 + lane] : 0;
+                        n1 = lane + 32 < nnb ? trow[nj0 + lane + 32] : 0;
                     }
                 }
             }
             pos += wtiles;
             win = nxt;
-            if constexpr (WIN) span = nspan;
             e0 = n0;
             e1 = n1;
         }
@@ -897,22 +881,6 @@ __global__ void __launch_bounds__(32 * (NT + 1), 4) decode_mma_kernel(DecodePara
         const int r_lo = cw * MTC * 16;                  // this consumer's stage rows
         const int r_hi = r_lo + MTC * 16;
         const bool mine = nvalid > r_lo;                 // its m-tiles hold tokens
-        // under a window: hidden stage rows [hide_a, hide_b); every stage holds a row that is seen
-        const int hide_a = WIN ? meta.hide_lo - meta.ts : 0, hide_b = WIN ? meta.hide_hi - meta.ts : 0;
-        auto seen = [&](int r) { return r < nvalid && (!WIN || r < hide_a || r >= hide_b); };
-        if constexpr (WIN) {
-            const int za = max(hide_a, 0), zb = min(hide_b, nvalid);
-            if (za < zb) {                               // hidden rows may hold anything, as those past
-                for (int i = lane; i < (zb - za) * Cfg::HALVES * 8; i += 32) {
-                    const int r = za + i / (Cfg::HALVES * 8);
-                    const int h = (i / 8) % Cfg::HALVES, ch = i % 8;
-                    *reinterpret_cast<uint4*>(sbase + Cfg::KV_BYTES + h * Cfg::HALF_BYTES + r * 128 +
-                                              ch * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-        }
         if (mine && nvalid < r_hi) {
             // its rows past the context: stale or poisoned -> zero V (P is 0 there)
             const int zrows = r_hi - nvalid;
@@ -988,7 +956,7 @@ __global__ void __launch_bounds__(32 * (NT + 1), 4) decode_mma_kernel(DecodePara
 #pragma unroll
             for (int mi = 0; mi < MTC; ++mi) {
                 const int mt = cw * MTC + mi;
-                const bool va = seen(mt * 16 + g), vb = seen(mt * 16 + g + 8);
+                const bool va = mt * 16 + g < nvalid, vb = mt * 16 + g + 8 < nvalid;
                 x[mi][0] = va ? sa[mi][nt][0] * p.qk_scale_log2 : -INFINITY;
                 x[mi][1] = va ? sa[mi][nt][1] * p.qk_scale_log2 : -INFINITY;
                 x[mi][2] = vb ? sa[mi][nt][2] * p.qk_scale_log2 : -INFINITY;

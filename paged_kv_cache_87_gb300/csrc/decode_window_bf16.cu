@@ -1,5 +1,5 @@
 // decode_window_bf16.cu -- decode under a sliding window for bf16 queries (K/V in bf16 or FP8 e4m3).
-#include "decode_launch.cuh"
+#include "decode_window_kernel.cuh"
 
 namespace pkv {
 

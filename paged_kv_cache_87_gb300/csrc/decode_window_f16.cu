@@ -1,5 +1,5 @@
 // decode_window_f16.cu -- decode under a sliding window for f16 queries (K/V in f16 or FP8 e4m3).
-#include "decode_launch.cuh"
+#include "decode_window_kernel.cuh"
 
 namespace pkv {
 

@@ -1,5 +1,5 @@
 // decode_window_f32.cu -- decode under a sliding window for f32 queries (K/V in f32 or FP8 e4m3).
-#include "decode_launch.cuh"
+#include "decode_window_kernel.cuh"
 
 namespace pkv {
 

@@ -1,0 +1,439 @@
+// decode_window_kernel.cuh -- decode under a sliding window for 16-bit queries over 16-bit or FP8 caches,
+// in one launch: o = sum_t softmax_t(scale q.k_t) v_t over the tokens of the virtual context of
+// window_span.cuh (the sinks' blocks, then the window's).
+//
+// A window bounds every unit (sequence, kv head, eight query heads), so there is nothing to plan: a
+// cluster of 1, 2, 4 or 8 CTAs takes a unit, an equal run of its 64-token tiles each, and joins its
+// states through distributed shared memory.  A CTA is a producer warp, which fills a ring of tiles
+// (TMA boxes through the block table, 128-byte swizzle), and four consumer warps, 16 tokens of every
+// tile each (five warps spread over all four sub-partitions).  Products are mma.sync m16n8k16, as in
+// decode_mma.cuh: S^T = K Q^T, O^T += V^T P^T, FP8 widened exactly to f16 between ldmatrix and the
+// product, P kept in registers.  Tokens that are hidden or past the context are masked in S and their
+// rows of V zeroed in shared memory, by the warp that multiplies them.
+#pragma once
+
+#include "cluster.cuh"
+#include "decode_launch.cuh"
+#include "decode_mma.cuh"
+#include "tmap.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kWinTile = 64;                  // tokens of a stage
+constexpr int kWinWarps = 4;                  // consumers
+constexpr int kWinThreads = 32 * (kWinWarps + 1);
+
+template <typename QT, typename KT, int HD>
+struct WinCfg {
+    static constexpr bool FP8 = std::is_same<KT, E4M3>::value;
+    using MT = typename std::conditional<FP8, F16, KT>::type;
+    static constexpr int ROWB = HD * KT::bytes;
+    static constexpr int HALVES = ROWB / 128;
+    static constexpr int ELEMS = 128 / KT::bytes;                 // elements of a 128-byte slice
+    static constexpr int KSTEPS = HD / 16, MTILES = HD / 16;
+    static constexpr int HALF_BYTES = kWinTile * 128;
+    static constexpr int KV_BYTES = HALVES * HALF_BYTES;
+    static constexpr int STAGE_BYTES = 2 * KV_BYTES;
+    static constexpr int NSTAGE = STAGE_BYTES == 32768 ? 3 : 4;
+    static constexpr int OFF_BARS = NSTAGE * STAGE_BYTES;
+    static constexpr int OFF_MINE = OFF_BARS + 128;               // the CTA's state [8][HD], (m, l)[8]
+    static constexpr int SMEM = OFF_MINE + 8 * HD * 4 + 64 + 1024;
+    static constexpr int HS = HD + 4;                             // stride of a head's row where warps meet
+    static_assert(kWinWarps * 8 * (HS + 2) * 4 <= NSTAGE * STAGE_BYTES, "the ring holds the warps' states");
+    static_assert(ROWB >= 128, "rows of 128 bytes or more");
+};
+
+template <typename QT, typename KT, int HD>
+__global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
+    DecodeParams p, int log_cluster, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    using C = WinCfg<QT, KT, HD>;
+    using MT = typename C::MT;
+    extern __shared__ uint8_t smem_raw[];
+    // every CTA of a cluster places its state alike: the offset to the boundary is the same
+    uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+    uint64_t* empty = full + C::NSTAGE;
+    float* mine = reinterpret_cast<float*>(smem + C::OFF_MINE);
+    float* mine_ml = mine + 8 * HD;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NSTAGE; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kWinWarps);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    const int B = p.block_size, logB = p.log_block, upi = p.num_kv_heads * p.nsub;
+    const int unit = blockIdx.x >> log_cluster, rank = blockIdx.x & ((1 << log_cluster) - 1);
+    const int s = unit / upi, u = unit % upi, kvh = u / p.nsub, qsub = u % p.nsub;
+    const int h0 = kvh * p.group + qsub * 8, nh = min(8, p.group - qsub * 8);
+    const int64_t row0 = (int64_t)s * p.num_q_heads + h0;
+    int n = p.context_lens[s];
+    if (n < 0 || n > p.max_context_len) {
+        if (u == 0 && rank == 0 && threadIdx.x == 0) set_status(p.status, PKV_DEV_BAD_CONTEXT);
+        n = n < 0 ? 0 : p.max_context_len;
+    }
+    if (n == 0) {                                         // (the whole cluster leaves here)
+        if (rank == 0)
+            for (int i = threadIdx.x; i < nh * HD; i += kWinThreads) store_from_float<QT>(p.out, row0 * HD + i, 0.f);
+        return;
+    }
+    const WindowSpan span = window_span(n, p.window, p.sinks, logB);
+    const int tiles = (span.tokens - 1) / kWinTile + 1;
+    const int a = (int)((int64_t)tiles * rank >> log_cluster), end = (int)((int64_t)tiles * (rank + 1) >> log_cluster);
+
+    if (warp == kWinWarps) {
+        // ======================= producer warp =======================
+        const uint64_t policy = l2_evict_first_policy();
+        const int32_t* trow = p.block_tables + (int64_t)s * p.max_blocks;
+        const int log_per = 6 - logB, blocks = (span.tokens - 1) >> logB;       // entries a tile; the last block
+        // 32 table entries at a time, the next ones loading
+        int base = a << log_per;
+        auto entries = [&](int j) { return j <= blocks && j < end << log_per ? trow[window_entry(span, j)] : 0; };
+        int cur = entries(base + lane), nxt = entries(base + 32 + lane);
+        if (lane == 0) {
+            prefetch_tensormap(&tmK);
+            prefetch_tensormap(&tmV);
+        }
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int t = a; t < end; ++t) {
+            const int j0 = t << log_per, nblk = min(1 << log_per, blocks + 1 - j0);
+            if (j0 >= base + 32) {
+                base += 32;
+                cur = nxt;
+                nxt = entries(base + 32 + lane);
+            }
+            if (!mbar_wait(&empty[stage], phase ^ 1u)) {
+                set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
+                break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)(nblk << logB) * C::ROWB);
+            __syncwarp();
+            int phys = __shfl_sync(0xffffffffu, cur, (j0 - base + lane) & 31);
+            if (lane < nblk) {
+                if (phys < 0 || phys >= p.num_blocks) {
+                    set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
+                    phys = 0;
+                }
+                const int y = (phys * p.num_kv_heads + kvh) << logB;
+                uint8_t* to = smem + stage * C::STAGE_BYTES + (lane << logB) * 128;
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h) {
+                    tma_load_2d(to + h * C::HALF_BYTES, &tmK, h * C::ELEMS, y, &full[stage], policy);
+                    tma_load_2d(to + C::KV_BYTES + h * C::HALF_BYTES, &tmV, h * C::ELEMS, y, &full[stage], policy);
+                }
+            }
+            if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
+        }
+        if (log_cluster) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
+
+    // ========================= consumer warps =========================
+    const int g = lane >> 2, c = lane & 3;
+    uint32_t qf[C::KSTEPS][2];                   // Q^T fragments of head g
+    {
+        const uint32_t* qg = static_cast<const uint32_t*>(p.q);
+        const int64_t rowq = (row0 + g) * HD;
+        const bool live = g < nh;
+#pragma unroll
+        for (int t = 0; t < C::KSTEPS; ++t) {
+            const int d0 = C::FP8 ? 16 * t + 4 * c : 16 * t + 2 * c, d1 = C::FP8 ? d0 + 2 : d0 + 8;
+            qf[t][0] = live ? q_pair<QT, MT>(qg[(rowq + d0) >> 1]) : 0u;
+            qf[t][1] = live ? q_pair<QT, MT>(qg[(rowq + d1) >> 1]) : 0u;
+        }
+    }
+    float o[C::MTILES][4];
+#pragma unroll
+    for (int mt = 0; mt < C::MTILES; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;    // of heads 2c and 2c + 1
+    int stage = 0;
+    uint32_t phase = 0;
+    const int rl = (lane & 7) + ((lane >> 3) & 1) * 8 + 16 * warp;              // ldmatrix rows of K
+    const int mi = lane >> 3, rv = (lane & 7) + (mi >> 1) * 8 + 16 * warp;      // and of V
+    bool ok = true;
+    for (int t = a; t < end; ++t) {
+        if (!mbar_wait(&full[stage], phase)) {
+            set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
+            ok = false;
+            break;
+        }
+        uint8_t* sb = smem + stage * C::STAGE_BYTES;
+        const uint32_t sK = smem_addr(sb), sV = sK + C::KV_BYTES;
+        // this warp's rows: valid ones, hidden ones
+        const int t0 = t * kWinTile + 16 * warp;
+        const int nv = span.tokens - t0, ha = span.hide_lo - t0, hb = span.hide_hi - t0;
+        if (nv > 0) {
+            auto seen = [&](int r) { return r < nv && (r < ha || r >= hb); };
+            const bool part = nv < 16 || (ha < hb && ha < 16 && hb > 0);
+            if (part) {
+                // rows that are not seen may hold anything: V's become zeros
+                const int r = lane >> 1;
+                if (!seen(r))
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(sb + C::KV_BYTES + h * C::HALF_BYTES + (16 * warp + r) * 128 +
+                                                      ((lane & 1) * 4 + k) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();                        // before the ring's next copy
+                __syncwarp();
+            }
+            float sa[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (C::FP8) {
+#pragma unroll
+                for (int pr = 0; pr < C::KSTEPS / 2; ++pr) {
+                    uint32_t r[4];
+                    ldsm_x4(sK + swz(rl, 2 * pr + (lane >> 4)), r);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t f[4] = {e4m3x2_of<0>(r[2 * k]), e4m3x2_of<0>(r[2 * k + 1]),
+                                               e4m3x2_of<1>(r[2 * k]), e4m3x2_of<1>(r[2 * k + 1])};
+                        Mma<MT>::run(sa, f, qf[2 * pr + k][0], qf[2 * pr + k][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < C::KSTEPS; ++k) {
+                    uint32_t f[4];
+                    ldsm_x4(sK + (k >> 2) * C::HALF_BYTES + swz(rl, (k & 3) * 2 + (lane >> 4)), f);
+                    Mma<MT>::run(sa, f, qf[k][0], qf[k][1]);
+                }
+            }
+            // running softmax: elements 0, 1 are token g, 2, 3 token g + 8, of heads 2c and 2c + 1
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = sa[e] * p.qk_scale_log2;
+            if (part) {
+                if (!seen(g)) x[0] = x[1] = -INFINITY;
+                if (!seen(g + 8)) x[2] = x[3] = -INFINITY;
+            }
+            float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+            // a warp-wide maximum only where a lane's own passes the slack (rarely, after the first tiles)
+            if (__any_sync(0xffffffffu, mx0 > m0 + kRescaleSlack || mx1 > m1 + kRescaleSlack)) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+                }
+                const bool n0 = mx0 > m0 + kRescaleSlack, n1 = mx1 > m1 + kRescaleSlack;
+                const float r0 = n0 ? fast_exp2(m0 - mx0) : 1.f, r1 = n1 ? fast_exp2(m1 - mx1) : 1.f;
+                if (n0) m0 = mx0;
+                if (n1) m1 = mx1;
+                l0 *= r0;
+                l1 *= r1;
+#pragma unroll
+                for (int mt = 0; mt < C::MTILES; ++mt) {
+                    o[mt][0] *= r0;
+                    o[mt][2] *= r0;
+                    o[mt][1] *= r1;
+                    o[mt][3] *= r1;
+                }
+            }
+            // (a warp that has seen nothing yet has a maximum of -inf: its weights are zeros)
+            const float s0 = m0 == -INFINITY ? 0.f : m0, s1 = m1 == -INFINITY ? 0.f : m1;
+            float f0, f1, f2, f3;
+            const uint32_t p01 = Mma<MT>::pack(fast_exp2(x[0] - s0), fast_exp2(x[1] - s1), f0, f1);
+            const uint32_t p23 = Mma<MT>::pack(fast_exp2(x[2] - s0), fast_exp2(x[3] - s1), f2, f3);
+            l0 += f0 + f2;
+            l1 += f1 + f3;
+            const uint32_t b0 = movmatrix_trans(p01), b1 = movmatrix_trans(p23);
+            if constexpr (C::FP8) {
+#pragma unroll
+                for (int pr = 0; pr < C::MTILES / 2; ++pr) {
+                    uint32_t r[4], ev[4], od[4];
+                    ldsm_x4_trans(sV + swz(rv, 2 * pr + (mi & 1)), r);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w = __byte_perm(r[k], 0u, 0x3120);        // even dims' pair, odd dims'
+                        ev[k] = e4m3x2_of<0>(w);
+                        od[k] = e4m3x2_of<1>(w);
+                    }
+                    Mma<MT>::run(o[2 * pr], ev, b0, b1);
+                    Mma<MT>::run(o[2 * pr + 1], od, b0, b1);
+                }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < C::MTILES; ++mt) {
+                    uint32_t f[4];
+                    ldsm_x4_trans(sV + (mt >> 2) * C::HALF_BYTES + swz(rv, (mt & 3) * 2 + (mi & 1)), f);
+                    Mma<MT>::run(o[mt], f, b0, b1);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
+    }
+
+    // ---------------- the four warps' states meet, in the ring ----------------
+    named_bar_sync(1, kWinWarps * 32);                   // every tile has been read
+    float* xa = reinterpret_cast<float*>(smem);          // [warp][8][HS]
+    float* xml = xa + kWinWarps * 8 * C::HS;             // [warp][8] (m, l)
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    if (g == 0) {
+        float* to = xml + (warp * 8 + 2 * c) * 2;
+        to[0] = m0; to[1] = l0; to[2] = m1; to[3] = l1;
+    }
+    if (a < end) {
+#pragma unroll
+        for (int mt = 0; mt < C::MTILES; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dim = C::FP8 ? 32 * (mt >> 1) + 2 * g + (mt & 1) + 16 * (e >> 1) : 16 * mt + g + 8 * (e >> 1);
+                xa[(warp * 8 + 2 * c + (e & 1)) * C::HS + dim] = o[mt][e];
+            }
+    }
+    named_bar_sync(1, kWinWarps * 32);
+    constexpr int V = HD / 16;                           // 16 threads a head
+    const int h = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * V;
+    float M = -INFINITY, L = 0.f, A[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 0.f;
+    if (a < end && ok) {
+#pragma unroll
+        for (int w = 0; w < kWinWarps; ++w) M = fmaxf(M, xml[(w * 8 + h) * 2]);
+#pragma unroll
+        for (int w = 0; w < kWinWarps; ++w) {
+            const float mw = xml[(w * 8 + h) * 2], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+            L = fmaf(xml[(w * 8 + h) * 2 + 1], f, L);
+#pragma unroll
+            for (int i = 0; i < V; ++i) A[i] = fmaf(xa[(w * 8 + h) * C::HS + d0 + i], f, A[i]);
+        }
+    }
+    if (log_cluster == 0) {
+        const float inv = L > 0.f ? p.out_scale / L : 0.f;
+        if (h < nh)
+#pragma unroll
+            for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, (row0 + h) * HD + d0 + i, A[i] * inv);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[h * HD + d0 + i] = A[i];
+    if ((threadIdx.x & 15) == 0) {
+        mine_ml[2 * h] = M;
+        mine_ml[2 * h + 1] = L;
+    }
+    cluster_sync();
+    // a head a warp, HD / 32 dims a lane: heads `rank`, rank + cluster, ..
+    constexpr int W = HD / 32;
+    const int last = (1 << log_cluster) - 1;
+    for (int k = rank + (warp << log_cluster); k < nh; k += kWinWarps << log_cluster) {
+        float m[8], l[8], v[8][W], top = -INFINITY, sum = 0.f, acc[W] = {0.f};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {                    // every load in flight at once
+            load_from(mine_ml + 2 * k, min(r, last), m[r], l[r]);
+            load_from(mine + k * HD + W * lane, min(r, last), v[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) top = fmaxf(top, m[r]);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (r > last || m[r] == -INFINITY) continue;
+            const float f = fast_exp2(m[r] - top);
+            sum = fmaf(l[r], f, sum);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] = fmaf(v[r][i], f, acc[i]);
+        }
+        const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) store_from_float<QT>(p.out, (row0 + k) * HD + W * lane + i, acc[i] * inv);
+    }
+    __syncwarp();
+    cluster_sync();                                      // what the others read stays until they have
+}
+
+// CTAs of a cluster, by what a launch costs in rounds of tiles: rounds of resident CTAs, each of a
+// CTA's tiles and kWinStart for its start and its end (and as much again for a cluster's meeting).
+constexpr int kWinStart = 3;
+
+template <typename QT, typename KT, int HD>
+cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
+    using C = WinCfg<QT, KT, HD>;
+    static int resident[64] = {0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    auto kernel = decode_window_kernel<QT, KT, HD>;
+    if (resident[dev] == 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (err != cudaSuccess) return err;
+        int per_sm = 0, sms = 0;
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWinThreads, C::SMEM);
+        if (err != cudaSuccess) return err;
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (err != cudaSuccess) return err;
+        resident[dev] = (per_sm > 0 ? per_sm : 1) * sms;
+    }
+    CUtensorMap tk, tv;
+    const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
+    if (!encode_pool_map(&tk, p.k_cache, HD, KT::bytes, rows, p.block_size) ||
+        !encode_pool_map(&tv, p.v_cache, HD, KT::bytes, rows, p.block_size))
+        return cudaErrorInvalidValue;
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
+    const int64_t tiles = ((int64_t)p.max_seen + kWinTile - 1) / kWinTile;
+    int log_cluster = 0;
+    int64_t least = INT64_MAX;
+    for (int k = 0; k <= 3; ++k) {
+        if (k > 0 && tiles < 1 << k) break;
+        const int64_t rounds = ((units << k) + resident[dev] - 1) / resident[dev];
+        const int64_t cost = rounds * (((tiles + (1 << k) - 1) >> k) + kWinStart * (k ? 2 : 1));
+        if (cost < least) {
+            least = cost;
+            log_cluster = k;
+        }
+    }
+    if ((units << log_cluster) > INT32_MAX) return cudaErrorInvalidValue;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = 1 << log_cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units << log_cluster), 1, 1);
+    cfg.blockDim = dim3(kWinThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, log_cluster, tk, tv);
+}
+
+// fp32 queries and FP8 rows of 64 dims take the CUDA-core kernel of decode.cuh over virtual contexts.
+template <typename QT, typename KT, int HD>
+cudaError_t dispatch_window_hd(const DecodeParams& p, int hpi, cudaStream_t stream) {
+    constexpr bool kFp8 = std::is_same<KT, E4M3>::value;
+    if constexpr (!std::is_same<QT, F32>::value && !(kFp8 && HD == 64)) {
+        return launch_decode_window<QT, KT, HD>(p, stream);
+    } else {
+        if (hpi == 1) return launch_decode_simt<QT, KT, HD, 1, true>(p, stream);
+        if (hpi == 2) return launch_decode_simt<QT, KT, HD, 2, true>(p, stream);
+        return launch_decode_simt<QT, KT, HD, 4, true>(p, stream);
+    }
+}
+
+template <typename QT, typename KT>
+cudaError_t dispatch_window_kv(const DecodeParams& p, int hpi, cudaStream_t stream) {
+    return p.head_dim == 128 ? dispatch_window_hd<QT, KT, 128>(p, hpi, stream)
+                             : dispatch_window_hd<QT, KT, 64>(p, hpi, stream);
+}
+
+}  // namespace
+}  // namespace pkv

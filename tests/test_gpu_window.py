@@ -75,14 +75,18 @@ def test_empty_contexts_give_zeros(q_type, kv_type):
 
 @pytest.mark.parametrize("q_type,kv_type", TYPES)
 def test_a_window_over_everything_is_the_plain_decode(q_type, kv_type):
-    """The same bits, where the plain call takes the same kernel: nothing is hidden."""
+    """Nothing is hidden: the same bits where the plain call takes the same kernel (fp32 queries, 4 bits),
+    else the same within what either may be off."""
     rng = np.random.default_rng(5)
     c = Paged(rng, [1, 100, 513, 2000], [1] * 4, 8, 2, 128, 16, q_type, kv_type, None, 0)
     plain = binding.pkv_paged_decode_attention(c.q, *c.caches, c.gtable, c.glens, c.most, c.scale)
     for w, s in ((2000, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2000)):
         got = binding.pkv_paged_decode_attention_window(c.q, *c.caches, c.gtable, c.glens, c.most,
                                                         c.scale, w, s)
-        assert torch.equal(got, plain), (w, s)
+        if q_type == "f32" or kv_type == "fp4":
+            assert torch.equal(got, plain), (w, s)
+        c.check(got)
+    c.check(plain)
     assert binding.pkv_get_device_status() == 0
 
 
