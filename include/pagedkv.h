@@ -199,17 +199,26 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  *
  *   window     tokens, the query's own among them; at least 1 (INT_MAX: all)
  *   num_sinks  tokens, at least 0
- *   workspace  >= pkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned: of
- *              the size that contexts of the window and the sinks need, however
- *              long max_context_len is
- *   the other arguments, types and errors as in pkv_paged_decode_attention (16-bit
- *   queries over pools of 2^31 rows or more return PKV_ERR_UNSUPPORTED).
- * Launches and rounding are those of pkv_paged_decode_attention.
+ *   workspace  >= pkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned; where
+ *              that is 0 it may be NULL.  It is 0 for 16-bit queries over 16-bit caches,
+ *              over FP8 rows of 128 dims, and over 4 bits where the window and the sinks
+ *              hold about 2,048 tokens at most; else what contexts of the window and the
+ *              sinks need, however long max_context_len is
+ *   the other arguments, types and errors as in pkv_paged_decode_attention; where no
+ *   workspace is needed, pools of 2^31 rows or more (16 bits, FP8) and batches of 2^28
+ *   (sequence, kv head, eight query heads) units return PKV_ERR_UNSUPPORTED.
+ * Where no workspace is needed: one launch, a cluster of up to eight CTAs a unit; logits,
+ * maxima, sums and states are fp32, the weights enter the product with V in the operands'
+ * type (f16 over FP8 and 4 bits: taken 2^7 above the running maximum, 2^-32 of the largest
+ * is what is lost) and the denominator sums them unrounded; over 4 bits bf16 queries are
+ * scaled into f16 by a power of two per head.  The rest: launches and rounding of
+ * pkv_paged_decode_attention.
  */
 PKV_API size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                                  int head_dim, int block_size,
                                                  int max_context_len, int window,
-                                                 int num_sinks, pkv_dtype kv_dtype);
+                                                 int num_sinks, pkv_dtype q_dtype,
+                                                 pkv_dtype kv_dtype);
 
 PKV_API pkv_status pkv_paged_decode_attention_window(
     const void* query, const void* k_cache, const void* v_cache, const int32_t* block_tables,

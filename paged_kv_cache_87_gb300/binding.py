@@ -59,7 +59,7 @@ _SIGNATURES = {
                                                      ctypes.c_float, ctypes.c_void_p,
                                                      ctypes.c_size_t, ctypes.c_void_p,
                                                      ctypes.c_void_p]),
-    "pkv_decode_window_workspace_bytes": (ctypes.c_size_t, [_I] * 9),
+    "pkv_decode_window_workspace_bytes": (ctypes.c_size_t, [_I] * 10),
     "pkv_paged_decode_attention_window": (
         ctypes.c_int, [_P] * 5 + [_I] * 10 + [_F, _I, _I, _F, _P, ctypes.c_size_t, _P, _P]),
     "pkv_chunk_workspace_bytes": (ctypes.c_size_t, [_I] * 6),
@@ -279,10 +279,11 @@ def pkv_paged_decode_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cac
 
 def pkv_decode_window_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                                       head_dim: int, block_size: int, max_context_len: int,
-                                      window: int, sinks: int, kv_dtype) -> int:
+                                      window: int, sinks: int, q_dtype, kv_dtype) -> int:
+    """0 where the call needs none (most calls of 16-bit queries: include/pagedkv.h)."""
     return int(load().pkv_decode_window_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                                         block_size, max_context_len, window, sinks,
-                                                        dtype_code(kv_dtype)))
+                                                        dtype_code(q_dtype), dtype_code(kv_dtype)))
 
 
 def pkv_paged_decode_attention_window(query: torch.Tensor, k_cache: torch.Tensor,

@@ -135,6 +135,13 @@ pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4
     return PKV_OK;
 }
 
+// Whether the window decode's own kernel serves these types and virtual contexts of up to max_seen
+// tokens: it needs no workspace and no plan.
+bool window_kernel(pkv_dtype q, pkv_dtype kv, int head_dim, int max_seen) {
+    return (q == PKV_F16 || q == PKV_BF16) &&
+           (kv == q || (kv == PKV_FP4_E2M1 && max_seen <= kFp4WindowMost) || (kv == PKV_FP8_E4M3 && head_dim == 128));
+}
+
 // Workspace of the chunk attention.  Pieces: every item, and one more where a CTA's run ends inside
 // of one; partial states: two a CTA, of at most as many CTAs as the steps of the longest possible
 // launch keep busy.
@@ -324,8 +331,6 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     const bool mma = (q_dtype == PKV_F16 || q_dtype == PKV_BF16) &&
                      (kv_dtype == q_dtype || (kv_dtype == PKV_FP8_E4M3 && head_dim == 128)) &&
                      (int64_t)num_blocks * num_kv_heads * block_size <= 0x7fffffffLL;
-    if (window && !mma && q_dtype != PKV_F32 && !(kv_dtype == PKV_FP8_E4M3 && head_dim == 64))
-        return PKV_ERR_UNSUPPORTED;          // 2^31 rows or more
     const int hpi = mma ? kMmaHeadsPerItem : plan.hpi;
     p.nsub = (plan.group + hpi - 1) / hpi;   // never above plan.nsub: the workspace fits
     // CUDA-core path with every context within one chunk: no split, no merge, so the
@@ -333,10 +338,10 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     p.self_plan = !mma && max_seen <= plan.chunk_tokens;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (window)
+    if (window)                              // (other 16-bit queries do not come here)
         return cuda_status(q_dtype == PKV_F32   ? decode_window_f32(p, kv_dtype, hpi, s)
-                           : q_dtype == PKV_F16 ? decode_window_f16(p, kv_dtype, hpi, s)
-                                                : decode_window_bf16(p, kv_dtype, hpi, s));
+                           : q_dtype == PKV_F16 ? decode_window_f16(p, hpi, s)
+                                                : decode_window_bf16(p, hpi, s));
     switch (q_dtype) {
     case PKV_F32: err = decode_dispatch_f32(p, kv_dtype, hpi, s); break;
     case PKV_F16: err = decode_dispatch_f16(p, kv_dtype, hpi, s); break;
@@ -466,13 +471,14 @@ pkv_status pkv_paged_chunk_attention(
 
 size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                          int head_dim, int block_size, int max_context_len,
-                                         int window, int num_sinks, pkv_dtype kv_dtype) {
+                                         int window, int num_sinks, pkv_dtype q_dtype,
+                                         pkv_dtype kv_dtype) {
     if (window < 1 || num_sinks < 0 || max_context_len < 0 ||
         (block_size != 8 && block_size != 16 && block_size != 32))
         return 0;
-    return pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                                      window_most(max_context_len, window, num_sinks, block_size),
-                                      kv_dtype);
+    const int max_seen = window_most(max_context_len, window, num_sinks, block_size);
+    if (window_kernel(q_dtype, kv_dtype, head_dim, max_seen)) return 0;
+    return pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seen, kv_dtype);
 }
 
 pkv_status pkv_paged_decode_attention_window(
@@ -484,6 +490,53 @@ pkv_status pkv_paged_decode_attention_window(
     if (window < 1 || num_sinks < 0) return PKV_ERR_INVALID_ARG;
     if (block_size != 8 && block_size != 16 && block_size != 32)
         return block_size <= 0 ? PKV_ERR_INVALID_ARG : PKV_ERR_UNSUPPORTED;
+    const int max_seen = window_most(max_context_len, window, num_sinks, block_size);
+    if (window_kernel(q_dtype, kv_dtype, head_dim, max_seen)) {
+        if (num_seqs < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 || num_q_heads <= 0 ||
+            num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+            return PKV_ERR_INVALID_ARG;
+        if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+        if (!isfinite(scale) || !isfinite(kv_scale) || !(kv_scale > 0.f)) return PKV_ERR_INVALID_ARG;
+        if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PKV_ERR_INVALID_ARG;
+        const int group = num_q_heads / num_kv_heads, nsub = (group + 7) / 8;
+        // rows of a pool and CTAs of a launch are counted in 31 bits
+        if ((kv_dtype != PKV_FP4_E2M1 && (int64_t)num_blocks * num_kv_heads * block_size > INT32_MAX) ||
+            (int64_t)num_kv_heads * nsub > INT32_MAX / 8 || (int64_t)num_seqs * num_kv_heads * nsub > INT32_MAX / 8)
+            return PKV_ERR_UNSUPPORTED;
+        if (num_seqs == 0) return PKV_OK;
+        if (!query || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PKV_ERR_INVALID_ARG;
+        if (!aligned(query, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+            !aligned(block_tables, 4) || !aligned(context_lens, 4))
+            return PKV_ERR_INVALID_ARG;
+        DeviceInfo* dev = nullptr;
+        if (device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+        DecodeParams p{};
+        p.q = query;
+        p.k_cache = k_cache;
+        p.v_cache = v_cache;
+        p.block_tables = block_tables;
+        p.context_lens = context_lens;
+        p.out = out;
+        p.status = dev->status;
+        p.num_seqs = num_seqs;
+        p.num_q_heads = num_q_heads;
+        p.num_kv_heads = num_kv_heads;
+        p.group = group;
+        p.nsub = nsub;
+        p.head_dim = head_dim;
+        p.block_size = block_size;
+        p.num_blocks = num_blocks;
+        p.max_blocks = max_blocks_per_seq;
+        p.max_context_len = max_context_len;
+        p.window = window;
+        p.sinks = num_sinks;
+        p.max_seen = max_seen;
+        p.log_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
+        p.out_scale = quantised(kv_dtype) ? kv_scale : 1.f;
+        p.qk_scale_log2 = scale * 1.4426950408889634f * p.out_scale;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        return cuda_status(q_dtype == PKV_F16 ? window_kernel_f16(p, kv_dtype, s) : window_kernel_bf16(p, kv_dtype, s));
+    }
     return decode_impl(query, k_cache, v_cache, block_tables, context_lens, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                        max_blocks_per_seq, max_context_len, scale, q_dtype, kv_dtype, kv_scale,

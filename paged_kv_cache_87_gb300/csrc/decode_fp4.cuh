@@ -73,7 +73,12 @@ cudaError_t decode_fp4_f32(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_f16(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_bf16(const DecodeFp4Params& p, cudaStream_t s);
 
-// The same under a sliding window (decode_fp4_window_*.cu).
+// The same under a sliding window (decode_fp4_window_*.cu): fp32 queries, and wide windows.  16-bit
+// queries over virtual contexts of up to kFp4WindowMost tokens take decode_window_kernel.cuh.  Measured
+// (us, that kernel against this one), 32 / 8 heads, d 128: one sequence under a window of 1,024 5.3
+// against 8.2, 16 of them 10.1 against 13.3, 256 70.8 against 79.7; 8 under 32,000 (64 / 8 heads) 72.7
+// against 62.7, 64 under 4,096 (128 / 8) 125 against 102.
+constexpr int kFp4WindowMost = 2048;
 cudaError_t decode_fp4_window_f32(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_window_f16(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_window_bf16(const DecodeFp4Params& p, cudaStream_t s);

@@ -1,5 +1,4 @@
-// decode_window_kernel.cuh -- decode under a sliding window for 16-bit queries over 16-bit or FP8 caches,
-// in one launch: o = sum_t softmax_t(scale q.k_t) v_t over the tokens of the virtual context of
+// decode_window_kernel.cuh -- decode under a sliding window for 16-bit queries, in one launch: o = sum_t softmax_t(scale q.k_t) v_t over the tokens of the virtual context of
 // window_span.cuh (the sinks' blocks, then the window's).
 //
 // A window bounds every unit (sequence, kv head, eight query heads), so there is nothing to plan: a
@@ -7,18 +6,31 @@
 // states through distributed shared memory.  A CTA is a producer warp, which fills a ring of tiles
 // (TMA boxes through the block table, 128-byte swizzle), and four consumer warps, 16 tokens of every
 // tile each (five warps spread over all four sub-partitions).  Products are mma.sync m16n8k16, as in
-// decode_mma.cuh: S^T = K Q^T, O^T += V^T P^T, FP8 widened exactly to f16 between ldmatrix and the
-// product, P kept in registers.  Tokens that are hidden or past the context are masked in S and their
+// decode_mma.cuh: S^T = K Q^T, O^T += V^T P^T, FP8 and 4 bits widened exactly to f16 between ldmatrix and
+// the product (the 4-bit tiles as decode_fp4_kernel.cuh takes them: unswizzled, by bulk copies; bf16
+// queries then scaled into f16 by a power of two per head), P kept in registers.  Tokens that are hidden or past the context are masked in S and their
 // rows of V zeroed in shared memory, by the warp that multiplies them.
 #pragma once
 
 #include "cluster.cuh"
-#include "decode_launch.cuh"
 #include "decode_mma.cuh"
 #include "tmap.cuh"
 
 namespace pkv {
 namespace {
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The low (k = 0) or high half of an f16x2 in both halves (an operand modifier, not an operation).
+__device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 t = k ? __high2half2(h) : __low2half2(h);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
 
 constexpr int kWinTile = 64;                  // tokens of a stage
 constexpr int kWinWarps = 4;                  // consumers
@@ -26,27 +38,31 @@ constexpr int kWinThreads = 32 * (kWinWarps + 1);
 
 template <typename QT, typename KT, int HD>
 struct WinCfg {
-    static constexpr bool FP8 = std::is_same<KT, E4M3>::value;
-    using MT = typename std::conditional<FP8, F16, KT>::type;
-    static constexpr int ROWB = HD * KT::bytes;
-    static constexpr int HALVES = ROWB / 128;
-    static constexpr int ELEMS = 128 / KT::bytes;                 // elements of a 128-byte slice
+    static constexpr bool FP8 = std::is_same<KT, E4M3>::value, FP4 = std::is_same<KT, E2M1>::value;
+    using MT = typename std::conditional<FP8 || FP4, F16, QT>::type;
+    static constexpr int ELEM_BYTES = FP8 || FP4 ? 1 : 2;
+    static constexpr int ROWB = FP4 ? HD / 2 + HD / 16 : HD * ELEM_BYTES;
+    static constexpr int HALVES = FP4 ? 1 : ROWB / 128;
+    static constexpr int ELEMS = 128 / ELEM_BYTES;                // elements of a 128-byte slice
+    // f16 weights are taken 2^7 above the running maximum: 2^-32 of the largest still counts
+    static constexpr float LIFT = std::is_same<MT, F16>::value ? 7.f : 0.f;
     static constexpr int KSTEPS = HD / 16, MTILES = HD / 16;
     static constexpr int HALF_BYTES = kWinTile * 128;
-    static constexpr int KV_BYTES = HALVES * HALF_BYTES;
+    static constexpr int KV_BYTES = FP4 ? kWinTile * ROWB : HALVES * HALF_BYTES;
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
-    static constexpr int NSTAGE = STAGE_BYTES == 32768 ? 3 : 4;
+    static constexpr int NSTAGE = STAGE_BYTES == 32768 ? 3 : FP4 && HD == 64 ? 6 : 4;
     static constexpr int OFF_BARS = NSTAGE * STAGE_BYTES;
     static constexpr int OFF_MINE = OFF_BARS + 128;               // the CTA's state [8][HD], (m, l)[8]
     static constexpr int SMEM = OFF_MINE + 8 * HD * 4 + 64 + 1024;
     static constexpr int HS = HD + 4;                             // stride of a head's row where warps meet
     static_assert(kWinWarps * 8 * (HS + 2) * 4 <= NSTAGE * STAGE_BYTES, "the ring holds the warps' states");
-    static_assert(ROWB >= 128, "rows of 128 bytes or more");
+    static_assert(FP4 || ROWB >= 128, "rows of 128 bytes or more");
+    static constexpr int CTAS = STAGE_BYTES == 32768 ? 2 : FP4 ? (HD == 64 ? 7 : 4) : 3;   // resident, by registers and memory
 };
 
 template <typename QT, typename KT, int HD>
-__global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
-    DecodeParams p, int log_cluster, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+__global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decode_window_kernel(
+    DecodeParams p, int log_cluster, uint32_t even, uint32_t odd, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     using C = WinCfg<QT, KT, HD>;
     using MT = typename C::MT;
     extern __shared__ uint8_t smem_raw[];
@@ -95,7 +111,7 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
         int base = a << log_per;
         auto entries = [&](int j) { return j <= blocks && j < end << log_per ? trow[window_entry(span, j)] : 0; };
         int cur = entries(base + lane), nxt = entries(base + 32 + lane);
-        if (lane == 0) {
+        if (!C::FP4 && lane == 0) {
             prefetch_tensormap(&tmK);
             prefetch_tensormap(&tmV);
         }
@@ -120,12 +136,22 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
                     set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
                     phys = 0;
                 }
-                const int y = (phys * p.num_kv_heads + kvh) << logB;
-                uint8_t* to = smem + stage * C::STAGE_BYTES + (lane << logB) * 128;
+                uint8_t* to = smem + stage * C::STAGE_BYTES;
+                if constexpr (C::FP4) {
+                    const int bytes = C::ROWB << logB;
+                    const int64_t from = ((int64_t)phys * p.num_kv_heads + kvh) * bytes;
+                    to += lane * bytes;
+                    bulk_g2s_hint(to, static_cast<const uint8_t*>(p.k_cache) + from, bytes, &full[stage], policy);
+                    bulk_g2s_hint(to + C::KV_BYTES, static_cast<const uint8_t*>(p.v_cache) + from, bytes, &full[stage],
+                                  policy);
+                } else {
+                    const int y = (phys * p.num_kv_heads + kvh) << logB;
+                    to += (lane << logB) * 128;
 #pragma unroll
-                for (int h = 0; h < C::HALVES; ++h) {
-                    tma_load_2d(to + h * C::HALF_BYTES, &tmK, h * C::ELEMS, y, &full[stage], policy);
-                    tma_load_2d(to + C::KV_BYTES + h * C::HALF_BYTES, &tmV, h * C::ELEMS, y, &full[stage], policy);
+                    for (int h = 0; h < C::HALVES; ++h) {
+                        tma_load_2d(to + h * C::HALF_BYTES, &tmK, h * C::ELEMS, y, &full[stage], policy);
+                        tma_load_2d(to + C::KV_BYTES + h * C::HALF_BYTES, &tmV, h * C::ELEMS, y, &full[stage], policy);
+                    }
                 }
             }
             if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
@@ -141,7 +167,39 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
     // ========================= consumer warps =========================
     const int g = lane >> 2, c = lane & 3;
     uint32_t qf[C::KSTEPS][2];                   // Q^T fragments of head g
-    {
+    float qs0 = p.qk_scale_log2, qs1 = qs0;      // logit scales of heads 2c and 2c + 1
+    if constexpr (C::FP4) {
+        // dims 32 ch + 8c .. + 7 of chunk ch are the pairs of k-steps 2 ch and 2 ch + 1
+        const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + g) * HD);
+        uint32_t top = 0u;
+#pragma unroll
+        for (int ch = 0; ch < HD / 32; ++ch) {
+            const uint4 w = g < nh ? qg[4 * ch + c] : make_uint4(0u, 0u, 0u, 0u);
+            qf[2 * ch][0] = w.x; qf[2 * ch][1] = w.y; qf[2 * ch + 1][0] = w.z; qf[2 * ch + 1][1] = w.w;
+            top = __vmaxu2(__vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)),
+                           __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+        }
+        if constexpr (!std::is_same<QT, F16>::value) {
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the row's largest magnitude to [2^14, 2^15); 2^60 times at most, so that what undoes it in
+            // the logit scale stays a normal number
+            const int ex = (int)(max(top >> 16, top & 0xffffu) >> 7) - 127;
+            const int e = ex == 128 ? 0 : min(14 - ex, 60);
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            const float back = qs0 * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int t = 0; t < C::KSTEPS; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 x = __floats2half2_rn(__uint_as_float(qf[t][i] << 16) * up,
+                                                        __uint_as_float(qf[t][i] & 0xffff0000u) * up);
+                    qf[t][i] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+            qs0 = __shfl_sync(0xffffffffu, back, 8 * c);
+            qs1 = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+        }
+    } else {
         const uint32_t* qg = static_cast<const uint32_t*>(p.q);
         const int64_t rowq = (row0 + g) * HD;
         const bool live = g < nh;
@@ -162,6 +220,15 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
     uint32_t phase = 0;
     const int rl = (lane & 7) + ((lane >> 3) & 1) * 8 + 16 * warp;              // ldmatrix rows of K
     const int mi = lane >> 3, rv = (lane & 7) + (mi >> 1) * 8 + 16 * warp;      // and of V
+    // 4 bits: this lane's ldmatrix row (token 16 warp + 8 (mi & 1) + r of chunk mi >> 1), and the scales
+    // of tokens g (K) and 2c (V) of the warp's piece; 8 tokens on they are `eight` bytes on
+    const int tile_bytes = C::ROWB << logB;
+    auto place = [&](int tok, int bytes) { return (tok >> logB) * tile_bytes + (tok & (B - 1)) * bytes; };
+    const uint32_t ld_off = place(16 * warp + 8 * (mi & 1) + (lane & 7), 16) + (mi >> 1) * B * 16;
+    const uint32_t ks_at = B * (HD / 2) + place(16 * warp + g, HD / 16);
+    const uint32_t vs_at = B * (HD / 2) + place(16 * warp + 2 * c, HD / 16);
+    const int eight = B == 8 ? tile_bytes : 8 * (HD / 16);
+    const uint32_t ksel = (c >> 1) ? 0x7531u : 0x6420u, vsel = (g >> 2) ? 0x7351u : 0x6240u;
     bool ok = true;
     for (int t = a; t < end; ++t) {
         if (!mbar_wait(&full[stage], phase)) {
@@ -177,7 +244,7 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
         if (nv > 0) {
             auto seen = [&](int r) { return r < nv && (r < ha || r >= hb); };
             const bool part = nv < 16 || (ha < hb && ha < 16 && hb > 0);
-            if (part) {
+            if (!C::FP4 && part) {
                 // rows that are not seen may hold anything: V's become zeros
                 const int r = lane >> 1;
                 if (!seen(r))
@@ -191,7 +258,38 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
                 __syncwarp();
             }
             float sa[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (C::FP8) {
+            if constexpr (C::FP4) {
+                // a word of 8 codes of row g (g + 8) and its scale are two pairs of operands; the reduction
+                // index is permuted for K and q alike
+                uint32_t da, db;                         // this lane's scale byte of every chunk
+                if constexpr (HD == 128) {
+                    const uint2 ra = *reinterpret_cast<const uint2*>(sb + ks_at);
+                    const uint2 rb = *reinterpret_cast<const uint2*>(sb + ks_at + eight);
+                    da = __byte_perm(ra.x, ra.y, ksel);
+                    db = __byte_perm(rb.x, rb.y, ksel);
+                } else {
+                    da = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_at), 0u, ksel);
+                    db = __byte_perm(*reinterpret_cast<const uint32_t*>(sb + ks_at + eight), 0u, ksel);
+                }
+#pragma unroll
+                for (int cp = 0; cp < HD / 64; ++cp) {
+                    uint32_t r[4];
+                    ldsm_x4(sK + ld_off + cp * 2 * B * 16, r);
+                    const uint32_t pa = cp ? e4m3x2_of<1>(da) : e4m3x2_of<0>(da);
+                    const uint32_t pb = cp ? e4m3x2_of<1>(db) : e4m3x2_of<0>(db);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t wa = r[2 * k], wb = r[2 * k + 1], fa = half_twice(pa, k), fb = half_twice(pb, k);
+                        const uint32_t x[4] = {hmul2(e2m1x2_to_f16x2<0>(wa), fa), hmul2(e2m1x2_to_f16x2<0>(wb), fb),
+                                               hmul2(e2m1x2_to_f16x2<1>(wa), fa), hmul2(e2m1x2_to_f16x2<1>(wb), fb)};
+                        const uint32_t y[4] = {hmul2(e2m1x2_to_f16x2<2>(wa), fa), hmul2(e2m1x2_to_f16x2<2>(wb), fb),
+                                               hmul2(e2m1x2_to_f16x2<3>(wa), fa), hmul2(e2m1x2_to_f16x2<3>(wb), fb)};
+                        const int ch = 2 * cp + k;
+                        Mma<MT>::run(sa, x, qf[2 * ch][0], qf[2 * ch][1]);
+                        Mma<MT>::run(sa, y, qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
+                    }
+                }
+            } else if constexpr (C::FP8) {
 #pragma unroll
                 for (int pr = 0; pr < C::KSTEPS / 2; ++pr) {
                     uint32_t r[4];
@@ -214,7 +312,7 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
             // running softmax: elements 0, 1 are token g, 2, 3 token g + 8, of heads 2c and 2c + 1
             float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = sa[e] * p.qk_scale_log2;
+            for (int e = 0; e < 4; ++e) x[e] = sa[e] * (e & 1 ? qs1 : qs0);
             if (part) {
                 if (!seen(g)) x[0] = x[1] = -INFINITY;
                 if (!seen(g + 8)) x[2] = x[3] = -INFINITY;
@@ -242,14 +340,56 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
                 }
             }
             // (a warp that has seen nothing yet has a maximum of -inf: its weights are zeros)
-            const float s0 = m0 == -INFINITY ? 0.f : m0, s1 = m1 == -INFINITY ? 0.f : m1;
-            float f0, f1, f2, f3;
-            const uint32_t p01 = Mma<MT>::pack(fast_exp2(x[0] - s0), fast_exp2(x[1] - s1), f0, f1);
-            const uint32_t p23 = Mma<MT>::pack(fast_exp2(x[2] - s0), fast_exp2(x[3] - s1), f2, f3);
-            l0 += f0 + f2;
-            l1 += f1 + f3;
+            const float s0 = m0 == -INFINITY ? 0.f : m0 - C::LIFT, s1 = m1 == -INFINITY ? 0.f : m1 - C::LIFT;
+            const float w0 = fast_exp2(x[0] - s0), w1 = fast_exp2(x[1] - s1), w2 = fast_exp2(x[2] - s0),
+                        w3 = fast_exp2(x[3] - s1);
+            float unused;
+            const uint32_t p01 = Mma<MT>::pack(w0, w1, unused, unused), p23 = Mma<MT>::pack(w2, w3, unused, unused);
+            l0 += w0 + w2;
+            l1 += w1 + w3;
             const uint32_t b0 = movmatrix_trans(p01), b1 = movmatrix_trans(p23);
-            if constexpr (C::FP8) {
+            if constexpr (C::FP4) {
+                const uint8_t* sv = sb + C::KV_BYTES;
+                uint32_t va[4] = {0u, 0u, 0u, 0u}, vb[4] = {0u, 0u, 0u, 0u};   // scales of tokens 2c, 2c + 1; + 8
+                if constexpr (HD == 128) {
+                    const uint4 ra = *reinterpret_cast<const uint4*>(sv + vs_at);
+                    const uint4 rb = *reinterpret_cast<const uint4*>(sv + vs_at + eight);
+                    va[0] = ra.x; va[1] = ra.y; va[2] = ra.z; va[3] = ra.w;
+                    vb[0] = rb.x; vb[1] = rb.y; vb[2] = rb.z; vb[3] = rb.w;
+                } else {
+                    const uint2 ra = *reinterpret_cast<const uint2*>(sv + vs_at);
+                    const uint2 rb = *reinterpret_cast<const uint2*>(sv + vs_at + eight);
+                    va[0] = ra.x; va[2] = ra.y; vb[0] = rb.x; vb[2] = rb.y;
+                }
+                if (part) {      // rows that are not seen may hold anything: scale 0 (codes are finite)
+                    if (!seen(2 * c)) va[0] = va[1] = 0u;
+                    if (!seen(2 * c + 1)) va[2] = va[3] = 0u;
+                    if (!seen(2 * c + 8)) vb[0] = vb[1] = 0u;
+                    if (!seen(2 * c + 9)) vb[2] = vb[3] = 0u;
+                }
+#pragma unroll
+                for (int cp = 0; cp < HD / 64; ++cp) {
+                    uint32_t r[4];
+                    ldsm_x4_trans(sV + ld_off + cp * 2 * B * 16, r);
+                    const uint32_t ga = __byte_perm(va[cp], va[cp + 2], vsel), gb = __byte_perm(vb[cp], vb[cp + 2], vsel);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int ch = 2 * cp + k;
+                        const uint32_t wa = r[2 * k], wb = r[2 * k + 1];
+                        const uint32_t fa = k ? e4m3x2_of<1>(ga) : e4m3x2_of<0>(ga);
+                        const uint32_t fb = k ? e4m3x2_of<1>(gb) : e4m3x2_of<0>(gb);
+                        // nibble pairs (token 2c low, 2c + 1 high) in bytes 2 and 3, even dims and odd ones
+                        const uint32_t ea = (wa & 0x0f0f0f0fu) * even, eb = (wb & 0x0f0f0f0fu) * even;
+                        const uint32_t oa = (wa & 0xf0f0f0f0u) * odd, ob = (wb & 0xf0f0f0f0u) * odd;
+                        const uint32_t ev[4] = {hmul2(e2m1x2_to_f16x2<2>(ea), fa), hmul2(e2m1x2_to_f16x2<3>(ea), fa),
+                                                hmul2(e2m1x2_to_f16x2<2>(eb), fb), hmul2(e2m1x2_to_f16x2<3>(eb), fb)};
+                        const uint32_t od[4] = {hmul2(e2m1x2_to_f16x2<2>(oa), fa), hmul2(e2m1x2_to_f16x2<3>(oa), fa),
+                                                hmul2(e2m1x2_to_f16x2<2>(ob), fb), hmul2(e2m1x2_to_f16x2<3>(ob), fb)};
+                        Mma<MT>::run(o[2 * ch], ev, b0, b1);
+                        Mma<MT>::run(o[2 * ch + 1], od, b0, b1);
+                    }
+                }
+            } else if constexpr (C::FP8) {
 #pragma unroll
                 for (int pr = 0; pr < C::MTILES / 2; ++pr) {
                     uint32_t r[4], ev[4], od[4];
@@ -295,7 +435,9 @@ __global__ void __launch_bounds__(kWinThreads, 3) decode_window_kernel(
         for (int mt = 0; mt < C::MTILES; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int dim = C::FP8 ? 32 * (mt >> 1) + 2 * g + (mt & 1) + 16 * (e >> 1) : 16 * mt + g + 8 * (e >> 1);
+                const int dim = C::FP4   ? 32 * (mt >> 1) + 4 * g + (mt & 1) + 2 * (e >> 1)
+                                : C::FP8 ? 32 * (mt >> 1) + 2 * g + (mt & 1) + 16 * (e >> 1)
+                                         : 16 * mt + g + 8 * (e >> 1);
                 xa[(warp * 8 + 2 * c + (e & 1)) * C::HS + dim] = o[mt][e];
             }
     }
@@ -381,10 +523,10 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         resident[dev] = (per_sm > 0 ? per_sm : 1) * sms;
     }
-    CUtensorMap tk, tv;
+    CUtensorMap tk{}, tv{};
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
-    if (!encode_pool_map(&tk, p.k_cache, HD, KT::bytes, rows, p.block_size) ||
-        !encode_pool_map(&tv, p.v_cache, HD, KT::bytes, rows, p.block_size))
+    if (!C::FP4 && (!encode_pool_map(&tk, p.k_cache, HD, C::ELEM_BYTES, rows, p.block_size) ||
+                    !encode_pool_map(&tv, p.v_cache, HD, C::ELEM_BYTES, rows, p.block_size)))
         return cudaErrorInvalidValue;
     const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
     const int64_t tiles = ((int64_t)p.max_seen + kWinTile - 1) / kWinTile;
@@ -413,26 +555,7 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p, log_cluster, tk, tv);
-}
-
-// fp32 queries and FP8 rows of 64 dims take the CUDA-core kernel of decode.cuh over virtual contexts.
-template <typename QT, typename KT, int HD>
-cudaError_t dispatch_window_hd(const DecodeParams& p, int hpi, cudaStream_t stream) {
-    constexpr bool kFp8 = std::is_same<KT, E4M3>::value;
-    if constexpr (!std::is_same<QT, F32>::value && !(kFp8 && HD == 64)) {
-        return launch_decode_window<QT, KT, HD>(p, stream);
-    } else {
-        if (hpi == 1) return launch_decode_simt<QT, KT, HD, 1, true>(p, stream);
-        if (hpi == 2) return launch_decode_simt<QT, KT, HD, 2, true>(p, stream);
-        return launch_decode_simt<QT, KT, HD, 4, true>(p, stream);
-    }
-}
-
-template <typename QT, typename KT>
-cudaError_t dispatch_window_kv(const DecodeParams& p, int hpi, cudaStream_t stream) {
-    return p.head_dim == 128 ? dispatch_window_hd<QT, KT, 128>(p, hpi, stream)
-                             : dispatch_window_hd<QT, KT, 64>(p, hpi, stream);
+    return cudaLaunchKernelEx(&cfg, kernel, p, log_cluster, 0x10010u, 0x1001u, tk, tv);   // 2^4 + 2^16, 1 + 2^12
 }
 
 }  // namespace

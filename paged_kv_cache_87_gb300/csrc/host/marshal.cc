@@ -279,12 +279,13 @@ PyObject* decode_call(PyObject* const* a, bool windowed) {
         if (!ws.defined()) {
             const size_t bytes =
                 windowed ? pkv_decode_window_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, window,
-                                                             sinks, c.type)
+                                                             sinks, qt, c.type)
                          : pkv_decode_workspace_bytes(S, Hq, c.heads, c.d, c.block, max_ctx, c.type);
-            ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
+            if (bytes || !windowed)
+                ws = fresh({(int64_t)(bytes < 256 ? 256 : bytes)}, q.options().dtype(at::kByte), stream);
         }
         if (!out.defined()) out = fresh(q.sizes(), q.options(), stream);
-        ws_bytes = (size_t)ws.numel() * ws.element_size();
+        if (ws.defined()) ws_bytes = (size_t)ws.numel() * ws.element_size();
     };
     if (prepare) {
         take();
@@ -303,8 +304,8 @@ PyObject* decode_call(PyObject* const* a, bool windowed) {
             return pkv_paged_decode_attention_window(
                 q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const int32_t*>(bt.data_ptr()),
                 static_cast<const int32_t*>(cl.data_ptr()), S, Hq, c.heads, c.d, c.block, c.blocks, width,
-                max_ctx, window, sinks, scale, qt, c.type, kv_scale, ws.data_ptr(), ws_bytes,
-                out.data_ptr(), stream);
+                max_ctx, window, sinks, scale, qt, c.type, kv_scale, ws.defined() ? ws.data_ptr() : nullptr,
+                ws_bytes, out.data_ptr(), stream);
         });
         return THPVariable_Wrap(std::move(out));
     }

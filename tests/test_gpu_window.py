@@ -75,7 +75,7 @@ def test_empty_contexts_give_zeros(q_type, kv_type):
 
 @pytest.mark.parametrize("q_type,kv_type", TYPES)
 def test_a_window_over_everything_is_the_plain_decode(q_type, kv_type):
-    """Nothing is hidden: the same bits where the plain call takes the same kernel (fp32 queries, 4 bits),
+    """Nothing is hidden: the same bits where the plain call takes the same kernel (fp32 queries),
     else the same within what either may be off."""
     rng = np.random.default_rng(5)
     c = Paged(rng, [1, 100, 513, 2000], [1] * 4, 8, 2, 128, 16, q_type, kv_type, None, 0)
@@ -83,7 +83,7 @@ def test_a_window_over_everything_is_the_plain_decode(q_type, kv_type):
     for w, s in ((2000, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2000)):
         got = binding.pkv_paged_decode_attention_window(c.q, *c.caches, c.gtable, c.glens, c.most,
                                                         c.scale, w, s)
-        if q_type == "f32" or kv_type == "fp4":
+        if q_type == "f32":
             assert torch.equal(got, plain), (w, s)
         c.check(got)
     c.check(plain)
@@ -143,7 +143,7 @@ def test_a_step_of_a_windowed_model_captured_and_replayed():
     slot = torch.zeros(1, dtype=torch.int64, device="cuda")
     table = torch.full((1, 400 // B), -1, dtype=torch.int32, device="cuda")
     lens = torch.zeros(1, dtype=torch.int32, device="cuda")
-    ws = torch.empty(max(256, binding.pkv_decode_window_workspace_bytes(1, hq, h, d, B, 400, W, S, "bf16")),
+    ws = torch.empty(max(256, binding.pkv_decode_window_workspace_bytes(1, hq, h, d, B, 400, W, S, "bf16", "bf16")),
                      dtype=torch.uint8, device="cuda")
     out = torch.empty(1, hq, d, dtype=torch.bfloat16, device="cuda")
 
@@ -218,6 +218,8 @@ def test_refusals():
                dict(v_cache=c.caches[1].to(torch.bfloat16)), dict(query=c.q.transpose(0, 1))):
         with pytest.raises(ValueError):
             f(**kw)
-    with pytest.raises(binding.PagedKVError):
-        f(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     c.check(f(), scale=0.1)
+    wide = Paged(rng, [30], [1], 2, 1, 64, 16, "f32", "f32", 5, 1)
+    with pytest.raises(binding.PagedKVError):
+        decode(wide, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    wide.check(decode(wide))
