@@ -453,7 +453,16 @@ pkv_status pkv_paged_chunk_attention(
     p.part_rows = pl.part_rows;
     p.item_tokens = pl.item_tokens;
     p.max_pairs = (int)(pl.items / num_kv_heads);
-    p.max_cuts = (int)(pl.items < p.num_ctas ? pl.items : p.num_ctas);
+    // steps of an item, at most: of the tokens that it sees of the longest context
+    const int64_t most_seen = (int64_t)p.window + pl.item_tokens + p.sinks + 2 * block_size;
+    const int64_t most_steps =
+        ((most_seen < max_context_len ? most_seen : (int64_t)max_context_len) + kChunkTile - 1) / kChunkTile;
+    // few items: no planner in front of them.  (Two a CTA only where they have one row tile: a mixed step
+    // of 210 items of two took 24.5 us dealt round, 22.1 from the planner's counter, longest first.)
+    p.self_plan = num_seqs <= kChunkSelfSeqs && most_steps <= 1 << 16 &&
+                  pl.items <= (pl.item_tokens == p.qpt ? 2 : 1) * p.num_ctas;
+    // (items that are no longer than this, and one a CTA, are never cut)
+    p.may_split = pl.items > p.num_ctas || most_steps > kChunkMinRun + kChunkSplitCost;
     const float kv = quantised(kv_dtype) ? kv_scale : 1.f;
     p.qk_scale_log2 = scale * 1.4426950408889634f * kv;
     p.out_scale = kv;

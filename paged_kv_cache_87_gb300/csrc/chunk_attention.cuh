@@ -13,6 +13,10 @@ constexpr int kChunkMaxCtas = 160;    // persistent CTAs, at most (one an SM)
 constexpr int kChunkMinRun = 4;
 // What splitting costs, in steps of every CTA: two partial states written, the joining kernel.
 constexpr int kChunkSplitCost = 8;
+// Launches of few items plan for themselves, in every CTA's producer warp: a planner in front of them
+// costs 5 us (one token 12.9 us with it, 8.1 without; drafts over FP8 98 and 92).  Sequences are one a
+// lane.
+constexpr int kChunkSelfSeqs = 32;
 
 // A run of an item's steps, as the planner lists them: CTA c's first one is entry c, what else it
 // takes (`first`, or the counter) lies behind entry num_ctas - 1.
@@ -24,11 +28,11 @@ struct __align__(16) ChunkPiece {
     int pad[3];
 };
 
-// An item that several CTAs share: what the joining kernel needs.
+// The item that a CTA begins and another one ends: what the joining kernel needs.
 struct __align__(16) ChunkCut {
     int kvh, pair, q_begin, n;
-    int c0, c1;                       // the CTAs with its first and its last steps
-    int pad[2];
+    int last;                         // the CTA with its last steps; below 0: none is left unfinished
+    int pad[3];
 };
 
 // What the planner leaves besides.
@@ -37,8 +41,6 @@ struct __align__(16) ChunkHead {
     int end;                          // end of the list (whole items: of those behind the first ones)
     int split;                        // a CTA's other pieces are `first`'s, not the counter's
     int next;                         // the counter
-    int cuts;
-    int pad[3];
 };
 
 struct ChunkParams {
@@ -51,7 +53,7 @@ struct ChunkParams {
     void* out;                        // [total_q, Hq, d]
     int* pair_prefix;                 // workspace [S + 1]: pairs of row tiles before a sequence (many sequences)
     ChunkPiece* pieces;               // workspace [max_pieces]
-    ChunkCut* cuts;                   // workspace [kChunkMaxCtas]
+    ChunkCut* cuts;                   // workspace [num_ctas]
     int* first;                       // workspace [kChunkMaxCtas + 1]: a CTA's second piece (split)
     ChunkHead* head;                  // workspace
     float* part_acc;                  // workspace [slots][part_rows][d]
@@ -63,7 +65,8 @@ struct ChunkParams {
     int window, sinks;                // window >= max_context_len: none
     int max_pairs;                    // pairs of row tiles that the workspace has room for
     int num_ctas, part_rows;
-    int max_cuts;                     // items that can be cut, by the sizes
+    int self_plan;                    // no planner: every CTA finds its pieces
+    int may_split;                    // an item can be cut, by the sizes
     float qk_scale_log2;              // scale * log2(e) * kv_scale
     float out_scale;                  // kv_scale of FP8 and 4 bits, else 1
 };

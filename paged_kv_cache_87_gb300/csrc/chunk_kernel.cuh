@@ -201,6 +201,133 @@ struct ChunkBars {
     }
 };
 
+// ---- a launch that plans for itself: the producer warp of every CTA finds its CTA's pieces ----
+// As the planner (chunk_plan.cu) deals them, but for the order of the sequences, which is their own,
+// and whole items, which go round the CTAs.  Called by a whole warp; lane s holds sequence s.
+struct ChunkSelf {
+    int q0, n, ctx, incl;              // this lane's sequence; pairs up to and including it
+    int total, items, split, q;        // steps of all items; a run's
+    int pos, end;                      // split: the next step of this CTA's run, its end; else the next item
+    int g, base;                       // split: the pair that holds pos, its first step
+
+    // Of pair g_ (a lane's own): its sequence, its place there, its steps (0: no such pair).
+    __device__ __forceinline__ int steps_of(const ChunkParams& p, int g_, int& seq, int& pair) const {
+        int l = 0;
+#pragma unroll
+        for (int b = 16; b; b >>= 1)
+            if (__shfl_sync(0xffffffffu, incl, l + b - 1) <= g_) l += b;
+        seq = l = min(l, 31);
+        pair = __shfl_sync(0xffffffffu, incl, l) - 1 - g_;
+        const int rows = __shfl_sync(0xffffffffu, n, l), before = __shfl_sync(0xffffffffu, ctx, l) - rows;
+        if (pair < 0) return 0;
+        const int a = pair * p.item_tokens, b = min(rows, a + p.item_tokens);
+        return chunk_span(before + a, before + b, p.window, p.sinks, p.log_block).steps;
+    }
+
+    __device__ __forceinline__ void init(const ChunkParams& p) {
+        const int lane = threadIdx.x & 31, S = p.num_seqs;
+        const int64_t cap = min((int64_t)p.max_context_len, (int64_t)p.max_blocks * p.block_size);
+        int pairs = 0;
+        bool bad = false;
+        q0 = n = ctx = 0;
+        if (lane < S) {
+            q0 = p.query_start[lane];
+            const int q1 = p.query_start[lane + 1];
+            ctx = p.context_lens[lane];
+            const int64_t rows = (int64_t)q1 - q0;
+            if (rows >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= rows && ctx <= cap) {
+                n = (int)rows;
+                pairs = (n + p.item_tokens - 1) / p.item_tokens;
+            } else {
+                bad = true;
+            }
+            bad |= (lane == 0 && q0 != 0) || (lane == S - 1 && q1 != p.total_q);
+        }
+        incl = pairs;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        int all = __shfl_sync(0xffffffffu, incl, 31);
+        // (starts that run back and forth could list rows twice, and more pairs than there is room for)
+        if (all > p.max_pairs) {
+            bad = true;
+            all = 0;
+        }
+        if (bad && blockIdx.x == 0) set_status(p.status, PKV_DEV_BAD_CONTEXT);
+        int sum = 0, most = 0;
+        for (int g0 = 0; g0 < all; g0 += 32) {
+            int seq, pair;
+            const int st = steps_of(p, g0 + lane, seq, pair);
+            sum += st;
+            most = max(most, st);
+        }
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int N = p.num_ctas;
+        total = sum * p.num_kv_heads;
+        items = all * p.num_kv_heads;
+        q = max(kChunkMinRun, (total + N - 1) / N);
+        const int whole = items ? max(most, (items + N - 1) / N * total / items) : 0;
+        split = whole > q + kChunkSplitCost;
+        pos = split ? min((int)blockIdx.x * q, total) : (int)blockIdx.x;
+        end = split ? min(pos + q, total) : items;
+        g = base = 0;
+        if (split && pos < end) {
+            for (int g0 = 0;; g0 += 32) {
+                int seq, pair, mine = steps_of(p, g0 + lane, seq, pair) * p.num_kv_heads, x = mine;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, off);
+                    if (lane >= off) x += y;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, base + x > pos);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    g = g0 + l;
+                    base += __shfl_sync(0xffffffffu, x - mine, l);
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, x, 31);
+            }
+        }
+        if (lane == 0) p.cuts[blockIdx.x].last = -1;
+    }
+
+    __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPiece& x) {
+        if (pos >= end) return false;
+        const int c = blockIdx.x;
+        int c1 = c, st;
+        x.slot = -1;
+        x.j0 = 0;
+        if (split) {
+            while (pos >= base + (st = steps_of(p, g, x.s, x.pair)) * p.num_kv_heads) {
+                base += st * p.num_kv_heads;
+                ++g;
+            }
+            const int h = (pos - base) / st, a = base + h * st, c0 = a / q;
+            c1 = (a + st - 1) / q;
+            x.kvh = h;
+            x.j0 = pos - a;
+            x.j1 = min(st, x.j0 + end - pos);
+            if (c0 != c1) x.slot = 2 * c + (c == c0);
+            pos += x.j1 - x.j0;
+        } else {
+            g = pos / p.num_kv_heads;
+            x.kvh = pos - g * p.num_kv_heads;
+            x.j1 = steps_of(p, g, x.s, x.pair);
+            pos += p.num_ctas;
+        }
+        x.q_begin = __shfl_sync(0xffffffffu, q0, x.s);
+        x.n = __shfl_sync(0xffffffffu, n, x.s);
+        x.ctx = __shfl_sync(0xffffffffu, ctx, x.s);
+        if (x.slot == 2 * c + 1 && (threadIdx.x & 31) == 0)      // begun here, ended elsewhere
+            p.cuts[c] = ChunkCut{x.kvh, x.pair, x.q_begin, x.n, c1, {0, 0, 0}};
+        return true;
+    }
+};
+
 // ---- the producer warp: pieces; per step the entries K_j, V_j ----
 template <typename C, int HD, bool NARROW>
 __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUtensorMap* tmK,
@@ -218,11 +345,19 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
     const uint64_t policy = l2_evict_last_policy();      // other items read K/V again
     const uint64_t q_policy = l2_evict_first_policy();   // a query row is read once
     const int B = p.block_size, logB = p.log_block, per_tile = kT >> logB;
-    // one round of loads to the CTA's first piece
-    const ChunkPiece piece0 = p.pieces[blockIdx.x];
-    const ChunkHead head = *p.head;
-    int next = p.first[blockIdx.x];
-    const int end = head.split ? p.first[blockIdx.x + 1] : head.end;
+    ChunkSelf self;
+    ChunkPiece piece;
+    ChunkHead head{};
+    int next = 0, end = 0;
+    if (p.self_plan) {
+        self.init(p);
+    } else {
+        // one round of loads to the CTA's first piece
+        piece = p.pieces[blockIdx.x];
+        head = *p.head;
+        next = p.first[blockIdx.x];
+        end = head.split ? p.first[blockIdx.x + 1] : head.end;
+    }
     uint64_t* ring_full = C::WIDE ? b.raw_full : b.full;
     uint64_t* ring_empty = C::WIDE ? b.raw_empty : b.empty;
     constexpr int RING = C::WIDE ? C::RAWS : C::STAGES;
@@ -235,7 +370,9 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
                 set_status(p.status, PKV_DEV_WAIT_TIMEOUT);
                 *abort_flag = 1;
             } else if (!*abort_flag) {
-                if (k == 0) {
+                if (p.self_plan) {
+                    idx = 0;
+                } else if (k == 0) {
                     idx = blockIdx.x < head.begun ? (int)blockIdx.x : -1;
                 } else {
                     idx = head.split ? next++ : atomicAdd(&p.head->next, 1);
@@ -245,7 +382,14 @@ __device__ __forceinline__ void chunk_producer(const ChunkParams& p, const CUten
         }
         idx = __shfl_sync(0xffffffffu, idx, 0);
         ChunkItem it{};
-        if (idx >= 0) it = chunk_item<NARROW>(p, k == 0 ? piece0 : p.pieces[idx]);
+        if (idx >= 0) {
+            if (p.self_plan) {
+                if (!self.next(p, piece)) idx = -1;
+            } else if (k > 0) {
+                piece = p.pieces[idx];
+            }
+            if (idx >= 0) it = chunk_item<NARROW>(p, piece);
+        }
         if (lane == 0) {
             items[slot].it = it;
             items[slot].idx = idx;
@@ -949,16 +1093,16 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) ch
     named_bar_sync(1, C::THREADS);
 }
 
-// Joins the items that lie in several CTAs' runs, entry blockIdx.x of the planner's list: the states
-// of CTAs c0, c0 + 1, .. in that order, a warp a row, HD / 32 dims a lane, eight states' loads in flight.
+// Joins the items that lie in several CTAs' runs, here the one that CTA blockIdx.x began and left
+// unfinished, if it did: the states of CTAs c0 = blockIdx.x, c0 + 1, .. in that order, a warp a row, HD / 32 dims a lane, eight states' loads in flight.
 template <typename QT, int HD>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int V = HD / 32, FLY = 8;
     const ChunkCut cut = p.cuts[blockIdx.x];
-    if ((int)blockIdx.x >= p.head->cuts) return;
-    const int kvh = cut.kvh, c0 = cut.c0, c1 = cut.c1, q_begin = cut.q_begin, n = cut.n, q0 = cut.pair * p.item_tokens;
+    if (cut.last < 0) return;
+    const int kvh = cut.kvh, c0 = blockIdx.x, c1 = cut.last, q_begin = cut.q_begin, n = cut.n, q0 = cut.pair * p.item_tokens;
     const int lane = threadIdx.x & 31, warps = gridDim.y * 8;
     for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < p.part_rows; row += warps) {
         const int X = row >> 7, r = row & (kT - 1), tok = q0 + X * p.qpt + r / p.group;
@@ -1036,8 +1180,10 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
         if (!made) return cudaErrorInvalidValue;
     }
     if (!encode_chunk_q_map(&tq, p.q, p.total_q, p.num_q_heads, p.group, p.qpt, HD)) return cudaErrorInvalidValue;
-    err = launch_chunk_plan(p, stream);
-    if (err != cudaSuccess) return err;
+    if (!p.self_plan) {
+        err = launch_chunk_plan(p, stream);
+        if (err != cudaSuccess) return err;
+    }
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1049,10 +1195,9 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, kernel, p, tk, tv, tq);
-    if (err != cudaSuccess) return err;
-    // eight warps a CTA, a row each at a time; about 1,200 CTAs at most, as many as are resident
-    const int most = p.part_rows / 8, want = 1200 / p.max_cuts;
-    cfg.gridDim = dim3((unsigned)p.max_cuts, (unsigned)(want < 4 ? 4 : want < most ? want : most), 1);
+    if (err != cudaSuccess || !p.may_split) return err;
+    // eight warps a CTA, a row each at a time
+    cfg.gridDim = dim3((unsigned)p.num_ctas, (unsigned)(p.part_rows / 16), 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, chunk_join_kernel<QT, HD>, p);

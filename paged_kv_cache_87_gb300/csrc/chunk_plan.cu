@@ -57,15 +57,16 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     __shared__ int s_ctx[kSeqs];
     __shared__ Seq s_seq[kSeqs];
     __shared__ int s_prefix[kSeqs + 1];
-    __shared__ int s_most, s_cuts;
+    __shared__ int s_most;
     __shared__ unsigned long long s_total;
     const int tid = threadIdx.x, S = p.num_seqs;
     const bool small = S <= kSeqs;
     if (tid == 0) {
-        s_most = s_cuts = 0;
+        s_most = 0;
         s_total = 0;
     }
     pdl_wait();
+    for (int c = tid; c < p.num_ctas; c += kThreads) p.cuts[c].last = -1;
     const int64_t cap = min((int64_t)p.max_context_len, (int64_t)p.max_blocks * p.block_size);
     // pairs of a sequence; one that breaks the contract has none
     auto pairs_of = [&](int q0, int q1, int ctx) {
@@ -200,8 +201,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
                 p.pieces[c] = x;
                 p.first[c] = p.num_ctas + e;
             }
-            if (c0 != c1)                                    // (in any order: each is an item of its own)
-                p.cuts[atomicAdd(&s_cuts, 1)] = ChunkCut{h, r.pair, r.q.q0, r.q.n, (int)c0, (int)c1, {0, 0}};
+            if (c0 != c1) p.cuts[c0] = ChunkCut{h, r.pair, r.q.q0, r.q.n, (int)c1, {0, 0, 0}};
         }
         at_steps += all_steps;
         extras += all_extras;
@@ -209,9 +209,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     }
     for (int c = tid; c <= p.num_ctas; c += kThreads)        // where CTAs without work would begin
         if (c >= used) p.first[c] = p.num_ctas + extras;
-    __syncthreads();
-    if (tid == 0)
-        *p.head = ChunkHead{used, split ? p.num_ctas + extras : nitems, split, p.num_ctas, s_cuts, {0, 0, 0}};
+    if (tid == 0) *p.head = ChunkHead{used, split ? p.num_ctas + extras : nitems, split, p.num_ctas};
 }
 
 }  // namespace
