@@ -210,8 +210,8 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  * Where no workspace is needed: one launch, a cluster of up to eight CTAs a unit; logits,
  * maxima, sums and states are fp32, the weights enter the product with V in the operands'
  * type (f16 over FP8 and 4 bits: taken 2^7 above the running maximum, 2^-32 of the largest
- * is what is lost) and the denominator sums them unrounded; over 4 bits bf16 queries are
- * scaled into f16 by a power of two per head.  The rest: launches and rounding of
+ * is what is lost) and the denominator sums them unrounded; over FP8 and 4 bits bf16 queries
+ * are scaled into f16 by a power of two per head.  The rest: launches and rounding of
  * pkv_paged_decode_attention.
  */
 PKV_API size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,

@@ -7,8 +7,8 @@
 // (TMA boxes through the block table, 128-byte swizzle), and four consumer warps, 16 tokens of every
 // tile each (five warps spread over all four sub-partitions).  Products are mma.sync m16n8k16, as in
 // decode_mma.cuh: S^T = K Q^T, O^T += V^T P^T, FP8 and 4 bits widened exactly to f16 between ldmatrix and
-// the product (the 4-bit tiles as decode_fp4_kernel.cuh takes them: unswizzled, by bulk copies; bf16
-// queries then scaled into f16 by a power of two per head), P kept in registers.  Tokens that are hidden or past the context are masked in S and their
+// the product (the 4-bit tiles as decode_fp4_kernel.cuh takes them: unswizzled, by bulk copies), bf16
+// queries then scaled into f16 by a power of two per head, P kept in registers.  Tokens that are hidden or past the context are masked in S and their
 // rows of V zeroed in shared memory, by the warp that multiplies them.
 #pragma once
 
@@ -168,22 +168,33 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
     const int g = lane >> 2, c = lane & 3;
     uint32_t qf[C::KSTEPS][2];                   // Q^T fragments of head g
     float qs0 = p.qk_scale_log2, qs1 = qs0;      // logit scales of heads 2c and 2c + 1
-    if constexpr (C::FP4) {
-        // dims 32 ch + 8c .. + 7 of chunk ch are the pairs of k-steps 2 ch and 2 ch + 1
-        const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + g) * HD);
-        uint32_t top = 0u;
+    {
+        const uint16_t* qg = static_cast<const uint16_t*>(p.q) + (row0 + g) * HD;
+        const bool live = g < nh;
+        if constexpr (C::FP4) {
+            // dims 32 ch + 8c .. + 7 of chunk ch are the pairs of k-steps 2 ch and 2 ch + 1
 #pragma unroll
-        for (int ch = 0; ch < HD / 32; ++ch) {
-            const uint4 w = g < nh ? qg[4 * ch + c] : make_uint4(0u, 0u, 0u, 0u);
-            qf[2 * ch][0] = w.x; qf[2 * ch][1] = w.y; qf[2 * ch + 1][0] = w.z; qf[2 * ch + 1][1] = w.w;
-            top = __vmaxu2(__vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)),
-                           __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+            for (int ch = 0; ch < HD / 32; ++ch) {
+                const uint4 w = live ? reinterpret_cast<const uint4*>(qg)[4 * ch + c] : make_uint4(0u, 0u, 0u, 0u);
+                qf[2 * ch][0] = w.x; qf[2 * ch][1] = w.y; qf[2 * ch + 1][0] = w.z; qf[2 * ch + 1][1] = w.w;
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < C::KSTEPS; ++t) {
+                const int d0 = C::FP8 ? 16 * t + 4 * c : 16 * t + 2 * c, d1 = C::FP8 ? d0 + 2 : d0 + 8;
+                qf[t][0] = live ? *reinterpret_cast<const uint32_t*>(qg + d0) : 0u;
+                qf[t][1] = live ? *reinterpret_cast<const uint32_t*>(qg + d1) : 0u;
+            }
         }
-        if constexpr (!std::is_same<QT, F16>::value) {
+        if constexpr (!std::is_same<QT, MT>::value) {
+            // bf16 queries beside f16 operands: the row's largest magnitude to [2^14, 2^15), by 2^60 at
+            // most, so that what undoes it in the logit scale stays a normal number
+            uint32_t top = 0u;
+#pragma unroll
+            for (int t = 0; t < C::KSTEPS; ++t)
+                top = __vmaxu2(top, __vmaxu2(qf[t][0] & 0x7fff7fffu, qf[t][1] & 0x7fff7fffu));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the row's largest magnitude to [2^14, 2^15); 2^60 times at most, so that what undoes it in
-            // the logit scale stays a normal number
             const int ex = (int)(max(top >> 16, top & 0xffffu) >> 7) - 127;
             const int e = ex == 128 ? 0 : min(14 - ex, 60);
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
@@ -198,16 +209,6 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
                 }
             qs0 = __shfl_sync(0xffffffffu, back, 8 * c);
             qs1 = __shfl_sync(0xffffffffu, back, 8 * c + 4);
-        }
-    } else {
-        const uint32_t* qg = static_cast<const uint32_t*>(p.q);
-        const int64_t rowq = (row0 + g) * HD;
-        const bool live = g < nh;
-#pragma unroll
-        for (int t = 0; t < C::KSTEPS; ++t) {
-            const int d0 = C::FP8 ? 16 * t + 4 * c : 16 * t + 2 * c, d1 = C::FP8 ? d0 + 2 : d0 + 8;
-            qf[t][0] = live ? q_pair<QT, MT>(qg[(rowq + d0) >> 1]) : 0u;
-            qf[t][1] = live ? q_pair<QT, MT>(qg[(rowq + d1) >> 1]) : 0u;
         }
     }
     float o[C::MTILES][4];
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
         }
     }
     if (log_cluster == 0) {
-        const float inv = L > 0.f ? p.out_scale / L : 0.f;
+        const float inv = L != 0.f ? p.out_scale / L : 0.f;   // (a NaN stays one)
         if (h < nh)
 #pragma unroll
             for (int i = 0; i < V; ++i) store_from_float<QT>(p.out, (row0 + h) * HD + d0 + i, A[i] * inv);
@@ -486,13 +487,13 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
         for (int r = 0; r < 8; ++r) top = fmaxf(top, m[r]);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            if (r > last || m[r] == -INFINITY) continue;
-            const float f = fast_exp2(m[r] - top);
+            if (r > last || (m[r] == -INFINITY && l[r] == 0.f)) continue;     // no tiles there
+            const float f = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - top);
             sum = fmaf(l[r], f, sum);
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[i] = fmaf(v[r][i], f, acc[i]);
         }
-        const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+        const float inv = sum != 0.f ? p.out_scale / sum : 0.f;
 #pragma unroll
         for (int i = 0; i < W; ++i) store_from_float<QT>(p.out, (row0 + k) * HD + W * lane + i, acc[i] * inv);
     }

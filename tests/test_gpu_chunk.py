@@ -202,6 +202,24 @@ def test_queries_of_any_magnitude():
         big.check(out)
 
 
+def test_nan_in_what_is_seen_is_not_hidden():
+    rng = np.random.default_rng(15)
+    for q_type, kv_type in (("bf16", "bf16"), ("f16", "e4m3")):
+        for which in (0, 1):
+            for lens, new in (([100, 300], [60, 2]), ([3000], [40]), ([4000], [2])):
+                c = Paged(rng, lens, new, 4, 2, 128, 16, q_type, kv_type, 500, 2)
+                n, m = lens[0], new[0]
+                blk, at = int(c.table[0, (n - m) // 16]), (n - m) % 16
+                raw = c.caches[which]
+                if kv_type == "e4m3":
+                    raw.view(torch.uint8)[blk, 1, at] = 0x7F
+                else:
+                    raw[blk, 1, at] = float("nan")
+                out = chunk(c)
+                assert torch.isnan(out[:m, 2:]).all() and not torch.isnan(out[:m, :2]).any()
+                assert not torch.isnan(out[m:]).any()
+
+
 def test_outputs_that_are_16_byte_aligned():
     rng = np.random.default_rng(11)
     c = Paged(rng, [140], [140], 2, 1, 64, 16, "bf16", "bf16", None, 0)

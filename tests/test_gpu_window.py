@@ -223,3 +223,67 @@ def test_refusals():
     with pytest.raises(binding.PagedKVError):
         decode(wide, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     wide.check(decode(wide))
+
+
+def test_queries_of_any_magnitude():
+    """bf16 queries over quantised caches are scaled into f16: heads from 2^-30 to 2^30, zeros."""
+    rng = np.random.default_rng(11)
+    for kv_type in ("e4m3", "fp4"):
+        c = Paged(rng, [150, 90, 7], [1] * 3, 16, 2, 128, 16, "bf16", kv_type, 60, 3, kv_scale=2.0 ** -5)
+        mul = torch.tensor(2.0 ** rng.integers(-30, 4, (3, 16, 1)).astype(np.float64)).cuda()
+        c.q = (c.q.double() * mul).to(torch.bfloat16)
+        c.q[1, 3] = 0
+        c.check(decode(c))
+        big = Paged(rng, [40], [1], 4, 2, 128, 16, "bf16", kv_type, 30, 0, kv_scale=2.0 ** -100)
+        big.check(decode(big))
+    assert binding.pkv_get_device_status() == 0
+
+
+def test_nan_in_what_is_seen_is_not_hidden():
+    """A NaN key or value that is seen reaches the output of its heads, and of no others."""
+    rng = np.random.default_rng(12)
+    for q_type, kv_type in (("bf16", "bf16"), ("f16", "e4m3"), ("f32", "f32")):
+        for which in (0, 1):
+            if q_type == "f32" and which == 0:
+                continue                  # a sum of weights that is NaN gives zeros there, as in the plain decode
+            c = Paged(rng, [100, 100], [1, 1], 4, 2, 128, 16, q_type, kv_type, 50, 2)
+            blk = int(c.table[0, 99 // 16])
+            raw = c.caches[which]
+            if kv_type == "e4m3":
+                raw.view(torch.uint8)[blk, 1, 99 % 16] = 0x7F
+            else:
+                raw[blk, 1, 99 % 16] = float("nan")
+            out = decode(c)
+            assert torch.isnan(out[0, 2:]).all() and not torch.isnan(out[0, :2]).any()
+            assert not torch.isnan(out[1]).any()
+
+
+@pytest.mark.parametrize("q_type,kv_type", [("bf16", "bf16"), ("f16", "e4m3"), ("f16", "fp4"), ("f32", "fp4")])
+def test_caches_beyond_32_bits(q_type, kv_type):
+    """Pools of more than 2^32 bytes each, with the blocks that are used at their end; decode and chunk."""
+    from oracle import window as plain
+    from tests.window_cases import bound, f64, weight_step
+    h, B, d, hq, W, S = 8, 16, 128, 16, 70, 3
+    row = {"bf16": 256, "e4m3": 128, "fp4": 72}[kv_type]
+    nb = 2 ** 32 // (h * B * row) + 40
+    rng = np.random.default_rng(13)
+    small = Paged(rng, [200], [3], hq, h, d, B, q_type, kv_type, None, 0)
+    # the small case's blocks, moved to the end of a large pool
+    k, v = (torch.zeros((nb, *c.shape[1:]), dtype=torch.uint8 if kv_type == "fp4" else c.dtype, device="cuda")
+            if kv_type != "e4m3" else torch.zeros((nb, *c.shape[1:]), dtype=torch.uint8, device="cuda").view(c.dtype)
+            for c in small.caches)
+    n = small.caches[0].shape[0]
+    for big, c in ((k, small.caches[0]), (v, small.caches[1])):
+        big.view(torch.uint8)[nb - n:] = c.view(torch.uint8)
+    table = small.gtable + (nb - n)
+    kk, vv, _ = small.rows(0)
+    q = f64(small.q)
+    ep = weight_step(q_type, kv_type)
+    out = binding.pkv_paged_decode_attention_window(small.q[2:], k, v, table, small.glens, 200, small.scale, W, S)
+    ref = plain.attention(q[2:], kk, vv, small.scale, W, S)
+    assert (np.abs(f64(out) - ref) <= bound(q[2:], kk, vv, small.scale, ep, ref, q_type)).all()
+    if q_type != "f32":
+        out = binding.pkv_paged_chunk_attention(small.q, k, v, table, small.glens, small.gstart, 200, small.scale, W, S)
+        ref = plain.attention(q, kk, vv, small.scale, W, S)
+        assert (np.abs(f64(out) - ref) <= bound(q, kk, vv, small.scale, ep, ref, q_type)).all()
+    assert binding.pkv_get_device_status() == 0
