@@ -50,31 +50,35 @@ struct WinCfg {
     static constexpr int HALF_BYTES = kWinTile * 128;
     static constexpr int KV_BYTES = FP4 ? kWinTile * ROWB : HALVES * HALF_BYTES;
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
+    // stages of the ring: the most, and the fewest, with which a CTA more is resident (FP8)
     static constexpr int NSTAGE = STAGE_BYTES == 32768 ? 3 : FP4 && HD == 64 ? 6 : 4;
-    static constexpr int OFF_BARS = NSTAGE * STAGE_BYTES;
-    static constexpr int OFF_MINE = OFF_BARS + 128;               // the CTA's state [8][HD], (m, l)[8]
-    static constexpr int SMEM = OFF_MINE + 8 * HD * 4 + 64 + 1024;
+    static constexpr int FEWEST = FP8 ? 3 : NSTAGE;
+    // in front of the ring: the barriers, the CTA's state [8][HD], (m, l)[8]
+    static constexpr int OFF_MINE = 128;
+    static constexpr int OFF_RING = (OFF_MINE + 8 * HD * 4 + 64 + 1023) / 1024 * 1024;
+    static constexpr int smem(int stages) { return OFF_RING + stages * STAGE_BYTES + 1024; }
     static constexpr int HS = HD + 4;                             // stride of a head's row where warps meet
-    static_assert(kWinWarps * 8 * (HS + 2) * 4 <= NSTAGE * STAGE_BYTES, "the ring holds the warps' states");
+    static_assert(kWinWarps * 8 * (HS + 2) * 4 <= FEWEST * STAGE_BYTES, "the ring holds the warps' states");
     static_assert(FP4 || ROWB >= 128, "rows of 128 bytes or more");
-    static constexpr int CTAS = STAGE_BYTES == 32768 ? 2 : FP4 ? (HD == 64 ? 7 : 4) : 3;   // resident, by registers and memory
+    static constexpr int CTAS = STAGE_BYTES == 32768 ? 2 : FP4 ? (HD == 64 ? 7 : 4) : FP8 ? 4 : 3;   // resident, at most
 };
 
 template <typename QT, typename KT, int HD>
 __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decode_window_kernel(
-    DecodeParams p, int log_cluster, uint32_t even, uint32_t odd, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    DecodeParams p, int log_cluster, int stages, uint32_t even, uint32_t odd, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     using C = WinCfg<QT, KT, HD>;
     using MT = typename C::MT;
     extern __shared__ uint8_t smem_raw[];
     // every CTA of a cluster places its state alike: the offset to the boundary is the same
     uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + C::NSTAGE;
+    uint8_t* ring = smem + C::OFF_RING;
     float* mine = reinterpret_cast<float*>(smem + C::OFF_MINE);
     float* mine_ml = mine + 8 * HD;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NSTAGE; ++i) {
+        for (int i = 0; i < stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], kWinWarps);
         }
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
                     set_status(p.status, PKV_DEV_BAD_BLOCK_ID);
                     phys = 0;
                 }
-                uint8_t* to = smem + stage * C::STAGE_BYTES;
+                uint8_t* to = ring + stage * C::STAGE_BYTES;
                 if constexpr (C::FP4) {
                     const int bytes = C::ROWB << logB;
                     const int64_t from = ((int64_t)phys * p.num_kv_heads + kvh) * bytes;
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
                     }
                 }
             }
-            if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
         if (log_cluster) {
             __syncwarp();
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
             ok = false;
             break;
         }
-        uint8_t* sb = smem + stage * C::STAGE_BYTES;
+        uint8_t* sb = ring + stage * C::STAGE_BYTES;
         const uint32_t sK = smem_addr(sb), sV = sK + C::KV_BYTES;
         // this warp's rows: valid ones, hidden ones
         const int t0 = t * kWinTile + 16 * warp;
@@ -415,12 +419,12 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == C::NSTAGE) { stage = 0; phase ^= 1u; }
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
     }
 
     // ---------------- the four warps' states meet, in the ring ----------------
     named_bar_sync(1, kWinWarps * 32);                   // every tile has been read
-    float* xa = reinterpret_cast<float*>(smem);          // [warp][8][HS]
+    float* xa = reinterpret_cast<float*>(ring);          // [warp][8][HS]
     float* xml = xa + kWinWarps * 8 * C::HS;             // [warp][8] (m, l)
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -501,28 +505,36 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<QT, KT, HD>::CTAS)) decod
     cluster_sync();                                      // what the others read stays until they have
 }
 
-// CTAs of a cluster, by what a launch costs in rounds of tiles: rounds of resident CTAs, each of a
-// CTA's tiles and kWinStart for its start and its end (and as much again for a cluster's meeting).
+// CTAs of a cluster (and stages of the ring), by what a launch costs in rounds of tiles: rounds of
+// resident CTAs, each of a CTA's tiles and kWinStart for its start and its end (and as much again for a
+// cluster's meeting).  Measured (us): one sequence under 1,024 tokens 5.1 in clusters of eight; 80 units of
+// 4,096 27.6 in pairs, 35.5 in fours; 160 units of 4,096 49.6 alone, 60.2 in pairs; FP8, 512 units of 4,096
+// 94 in fours of four stages (three CTAs an SM), 85 alone of three (four an SM), 320 units of 1,024 15.0
+// and 18.6 alone of four and of three.
 constexpr int kWinStart = 3;
 
 template <typename QT, typename KT, int HD>
 cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     using C = WinCfg<QT, KT, HD>;
-    static int resident[64] = {0};
+    static int resident[2][64] = {{0}};                  // with all stages, with the fewest
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     auto kernel = decode_window_kernel<QT, KT, HD>;
-    if (resident[dev] == 0) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (resident[1][dev] == 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::NSTAGE));
         if (err != cudaSuccess) return err;
-        int per_sm = 0, sms = 0;
-        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWinThreads, C::SMEM);
-        if (err != cudaSuccess) return err;
+        int sms = 0;
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (err != cudaSuccess) return err;
-        resident[dev] = (per_sm > 0 ? per_sm : 1) * sms;
+        for (int i = 0; i < 2; ++i) {
+            int per_sm = 0;
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWinThreads,
+                                                                C::smem(i ? C::FEWEST : C::NSTAGE));
+            if (err != cudaSuccess) return err;
+            resident[i][dev] = (per_sm > 0 ? per_sm : 1) * sms;
+        }
     }
     CUtensorMap tk{}, tv{};
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
@@ -531,17 +543,18 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * p.nsub;
     const int64_t tiles = ((int64_t)p.max_seen + kWinTile - 1) / kWinTile;
-    int log_cluster = 0;
+    int log_cluster = 0, stages = C::NSTAGE;
     int64_t least = INT64_MAX;
-    for (int k = 0; k <= 3; ++k) {
-        if (k > 0 && tiles < 1 << k) break;
-        const int64_t rounds = ((units << k) + resident[dev] - 1) / resident[dev];
-        const int64_t cost = rounds * (((tiles + (1 << k) - 1) >> k) + kWinStart * (k ? 2 : 1));
-        if (cost < least) {
-            least = cost;
-            log_cluster = k;
+    for (int i = 0; i <= (C::FEWEST < C::NSTAGE); ++i)
+        for (int k = 0; k <= 3 && (k == 0 || tiles >= 1 << k); ++k) {
+            const int64_t rounds = ((units << k) + resident[i][dev] - 1) / resident[i][dev];
+            const int64_t cost = rounds * (((tiles + (1 << k) - 1) >> k) + kWinStart * (k ? 2 : 1));
+            if (cost < least) {
+                least = cost;
+                log_cluster = k;
+                stages = i ? C::FEWEST : C::NSTAGE;
+            }
         }
-    }
     if ((units << log_cluster) > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -552,11 +565,11 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units << log_cluster), 1, 1);
     cfg.blockDim = dim3(kWinThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = C::smem(stages);
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p, log_cluster, 0x10010u, 0x1001u, tk, tv);   // 2^4 + 2^16, 1 + 2^12
+    return cudaLaunchKernelEx(&cfg, kernel, p, log_cluster, stages, 0x10010u, 0x1001u, tk, tv);   // 2^4 + 2^16, 1 + 2^12
 }
 
 }  // namespace
