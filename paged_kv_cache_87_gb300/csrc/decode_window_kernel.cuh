@@ -52,7 +52,7 @@ struct WinCfg {
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
     // stages of the ring: the most, and the fewest, with which a CTA more is resident (FP8)
     static constexpr int NSTAGE = STAGE_BYTES == 32768 ? 3 : FP4 && HD == 64 ? 6 : 4;
-    static constexpr int FEWEST = FP8 ? 3 : NSTAGE;
+    static constexpr int FEWEST = FP8 ? 3 : STAGE_BYTES == 32768 ? 2 : NSTAGE;
     // in front of the ring: the barriers, the CTA's state [8][HD], (m, l)[8]
     static constexpr int OFF_MINE = 128;
     static constexpr int OFF_RING = (OFF_MINE + 8 * HD * 4 + 64 + 1023) / 1024 * 1024;
@@ -60,7 +60,7 @@ struct WinCfg {
     static constexpr int HS = HD + 4;                             // stride of a head's row where warps meet
     static_assert(kWinWarps * 8 * (HS + 2) * 4 <= FEWEST * STAGE_BYTES, "the ring holds the warps' states");
     static_assert(FP4 || ROWB >= 128, "rows of 128 bytes or more");
-    static constexpr int CTAS = STAGE_BYTES == 32768 ? 2 : FP4 ? (HD == 64 ? 7 : 4) : FP8 ? 4 : 3;   // resident, at most
+    static constexpr int CTAS = STAGE_BYTES == 32768 ? 3 : FP4 ? (HD == 64 ? 7 : 4) : FP8 ? 4 : 3;   // resident, at most
 };
 
 template <typename QT, typename KT, int HD>
