@@ -142,6 +142,14 @@ bool window_kernel(pkv_dtype q, pkv_dtype kv, int head_dim, int max_seen) {
            (kv == q || (kv == PKV_FP4_E2M1 && max_seen <= kFp4WindowMost) || (kv == PKV_FP8_E4M3 && head_dim == 128));
 }
 
+// Whether a call of the chunk attention has sequences of few rows on average, and as many (sequence, kv head)
+// units as the kernel of few rows needs to be the sooner one (measured in chunk_few_kernel.cuh).
+bool chunk_few(pkv_dtype kv, int head_dim, int64_t rows, int num_seqs, int64_t units, int num_sms) {
+    const bool has = kv == PKV_FP4_E2M1 || (kv == PKV_FP8_E4M3) == (head_dim == 128);
+    return has && rows <= (int64_t)num_seqs * kChunkFewRows && units >= (head_dim == 64 ? 4 : 5) * num_sms &&
+           units <= INT32_MAX;
+}
+
 // Workspace of the chunk attention.  Pieces: every item, and one more where a CTA's run ends inside
 // of one; partial states: two a CTA, of at most as many CTAs as the steps of the longest possible
 // launch keep busy.
@@ -468,6 +476,13 @@ pkv_status pkv_paged_chunk_attention(
     p.out_scale = kv;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = q_dtype == PKV_BF16;
+    // many sequences of few rows: those that have few go to a kernel of their own, in front of the others'
+    const int64_t rows = (int64_t)total_q * p.group;
+    if (chunk_few(kv_dtype, head_dim, rows, num_seqs, (int64_t)num_seqs * num_kv_heads, dev->num_sms)) {
+        const cudaError_t e = bf16 ? chunk_few_bf16(p, head_dim, kv_dtype, s) : chunk_few_f16(p, head_dim, kv_dtype, s);
+        if (e != cudaSuccess) return cuda_status(e);
+        p.few_rows = kChunkFewRows;
+    }
     switch (kv_dtype) {
     case PKV_FP8_E4M3:
         return cuda_status(bf16 ? chunk_bf16_fp8(p, head_dim, s) : chunk_f16_fp8(p, head_dim, s));

@@ -18,6 +18,10 @@ constexpr int kChunkSplitCost = 8;
 // lane.
 constexpr int kChunkSelfSeqs = 32;
 
+// (token, head) rows of a sequence and kv head, up to which it goes to the kernel of few rows where a call has
+// such sequences (chunk_few_kernel.cuh).
+constexpr int kChunkFewRows = 24;
+
 // A run of an item's steps, as the planner lists them: CTA c's first one is entry c, what else it
 // takes (`first`, or the counter) lies behind entry num_ctas - 1.
 struct __align__(16) ChunkPiece {
@@ -65,6 +69,7 @@ struct ChunkParams {
     int window, sinks;                // window >= max_context_len: none
     int max_pairs;                    // pairs of row tiles that the workspace has room for
     int num_ctas, part_rows;
+    int few_rows;                     // sequences with as many rows of a kv head are another kernel's
     int self_plan;                    // no planner: every CTA finds its pieces
     int may_split;                    // an item can be cut, by the sizes
     float qk_scale_log2;              // scale * log2(e) * kv_scale
@@ -104,6 +109,10 @@ __host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end
 
 // Defined in chunk_plan.cu.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
+
+// The kernel of few rows, in front of the others: FP8 of 128 dims, 4 bits, 16 bits of 64.
+cudaError_t chunk_few_f16(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s);
+cudaError_t chunk_few_bf16(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s);
 
 // Planner, attention and joining kernel; each defined in the .cu file of its name.
 cudaError_t chunk_f16_16(const ChunkParams& p, int head_dim, cudaStream_t s);

@@ -236,7 +236,7 @@ struct ChunkSelf {
             ctx = p.context_lens[lane];
             const int64_t rows = (int64_t)q1 - q0;
             if (rows >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= rows && ctx <= cap) {
-                n = (int)rows;
+                n = rows * p.group <= p.few_rows ? 0 : (int)rows;        // (few: another kernel's)
                 pairs = (n + p.item_tokens - 1) / p.item_tokens;
             } else {
                 bad = true;

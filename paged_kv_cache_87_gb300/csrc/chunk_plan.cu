@@ -68,11 +68,11 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     pdl_wait();
     for (int c = tid; c < p.num_ctas; c += kThreads) p.cuts[c].last = -1;
     const int64_t cap = min((int64_t)p.max_context_len, (int64_t)p.max_blocks * p.block_size);
-    // pairs of a sequence; one that breaks the contract has none
+    // pairs of a sequence; one that breaks the contract, or is another kernel's, has none
     auto pairs_of = [&](int q0, int q1, int ctx) {
         const int64_t n = (int64_t)q1 - q0;
         if (n >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= n && ctx <= cap)
-            return (int)(((uint32_t)n + p.item_tokens - 1) / (uint32_t)(p.item_tokens));
+            return n * p.group <= p.few_rows ? 0 : (int)(((uint32_t)n + p.item_tokens - 1) / (uint32_t)(p.item_tokens));
         set_status(p.status, PKV_DEV_BAD_CONTEXT);
         return 0;
     };
