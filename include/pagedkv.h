@@ -338,7 +338,8 @@ PKV_API pkv_status pkv_paged_tree_attention(
  * - n_s + i, and for each query head h
  *   out[row][h] = sum_t softmax_t(scale * q[row][h] . k_t) v_t
  * over the tokens t <= p with t > p - window or t < num_sinks.  Table entries of blocks that none
- * of a sequence's rows sees are never read, and cache rows that none sees may hold anything.
+ * of a sequence's rows sees are never read, and cache rows that none sees may hold anything.  A NaN
+ * or an infinity in a value that some of them see may reach the sequence's other rows.
  *
  *   query        [total_q][num_q_heads][head_dim], q_dtype, 16-byte aligned
  *   query_start  int32 [num_seqs + 1], query_start[0] = 0, non-decreasing,
