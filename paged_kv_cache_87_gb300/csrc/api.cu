@@ -143,11 +143,15 @@ bool window_kernel(pkv_dtype q, pkv_dtype kv, int head_dim, int max_seen) {
 }
 
 // Whether a call of the chunk attention has sequences of few rows on average, and as many (sequence, kv head)
-// units as the kernel of few rows needs to be the sooner one (measured in chunk_few_kernel.cuh).
-bool chunk_few(pkv_dtype kv, int head_dim, int64_t rows, int num_seqs, int64_t units, int num_sms) {
+// units as the kernel of few rows needs to be the sooner one, by the tokens that a row sees at most: it does not
+// cut contexts.  Measured (us, chunk kernel | few rows; 3 tokens, 32 / 8 heads, bf16 queries, 152 SMs): rows of
+// 1,028 tokens at most, 160 units: FP8 34.6 | 27.0, 4 bits 36.0 | 25.8, 16 bits of 64 dims 30.9 | 19.1; of 100 -
+// 1,000: 24.3 | 24.4, 24.9 | 22.9, 21.2 | 16.9; 64 units of 1,000, FP8: 17.8 | 25.7.  Of 1,000 - 8,000, 64 dims,
+// 160 units: 49.6 | 77.3, 256 80.8 | 76.7, 456 134 | 95; 128 dims: FP8 456 units 147 | 163, 800 275 | 228.
+bool chunk_few(pkv_dtype kv, int head_dim, int64_t rows, int num_seqs, int64_t units, int64_t seen, int num_sms) {
     const bool has = kv == PKV_FP4_E2M1 || (kv == PKV_FP8_E4M3) == (head_dim == 128);
-    return has && rows <= (int64_t)num_seqs * kChunkFewRows && units >= (head_dim == 64 ? 4 : 5) * num_sms &&
-           units <= INT32_MAX;
+    const int64_t least = seen <= kChunkFewShort ? num_sms : head_dim == 64 ? num_sms * 3 / 2 : num_sms * 5;
+    return has && rows <= (int64_t)num_seqs * kChunkFewRows && units >= least && units <= INT32_MAX;
 }
 
 // Workspace of the chunk attention.  Pieces: every item, and one more where a CTA's run ends inside
@@ -478,7 +482,8 @@ pkv_status pkv_paged_chunk_attention(
     const bool bf16 = q_dtype == PKV_BF16;
     // many sequences of few rows: those that have few go to a kernel of their own, in front of the others'
     const int64_t rows = (int64_t)total_q * p.group;
-    if (chunk_few(kv_dtype, head_dim, rows, num_seqs, (int64_t)num_seqs * num_kv_heads, dev->num_sms)) {
+    const int64_t seen = (int64_t)p.window + p.sinks < max_context_len ? p.window + p.sinks : max_context_len;
+    if (chunk_few(kv_dtype, head_dim, rows, num_seqs, (int64_t)num_seqs * num_kv_heads, seen, dev->num_sms)) {
         const cudaError_t e = bf16 ? chunk_few_bf16(p, head_dim, kv_dtype, s) : chunk_few_f16(p, head_dim, kv_dtype, s);
         if (e != cudaSuccess) return cuda_status(e);
         p.few_rows = kChunkFewRows;

@@ -21,6 +21,7 @@ constexpr int kChunkSelfSeqs = 32;
 // (token, head) rows of a sequence and kv head, up to which it goes to the kernel of few rows where a call has
 // such sequences (chunk_few_kernel.cuh).
 constexpr int kChunkFewRows = 24;
+constexpr int kChunkFewShort = 1088;  // tokens that a row sees, up to which one unit an SM is enough for it
 
 // A run of an item's steps, as the planner lists them: CTA c's first one is entry c, what else it
 // takes (`first`, or the counter) lies behind entry num_ctas - 1.

@@ -8,12 +8,12 @@
 // head): one launch, nothing planned, no workspace.  Sequences with more rows leave at once; the chunk kernel,
 // launched behind, takes those and leaves these.
 //
-// Contexts are not cut, so there have to be enough of them for the longest to end among the others: five units
-// an SM, four of 64 dims (chunk_few in api.cu).  Measured (us, the chunk kernel alone | with this one), 5 tokens
-// over 1,000 - 8,000, 32 / 8 heads, bf16 queries: FP8, d 128, 200 sequences 541 | 380, 100 275 | 228, 76 171 | 192;
-// 4 bits, d 128, 588 | 355, 290 | 210, 177 | 182; 16 bits, d 64, 412 | 254, 205 | 148, 155 | 120.  3 tokens under a
-// window of 1,024 + 4, 256 sequences: FP8 219 | 154, 16 bits of 64 dims 194 | 102.  16 bits of 128 dims, where the
-// chunk kernel widens nothing, 468 | 462, 236 | 262: not taken.
+// Contexts are not cut, so there have to be enough of them for the longest to end among the others (chunk_few in
+// api.cu, with what was measured on either side).  Large ones (us, the chunk kernel alone | with this one), 5 tokens
+// over 1,000 - 8,000, 32 / 8 heads, bf16 queries: FP8, d 128, 200 sequences 541 | 380, 100 275 | 228; 4 bits, d 128,
+// 588 | 355, 290 | 210; 16 bits, d 64, 412 | 254, 205 | 148.  3 tokens under a window of 1,024 + 4, 256 sequences:
+// FP8 219 | 154, 16 bits of 64 dims 194 | 102.  16 bits of 128 dims, where the chunk kernel widens nothing,
+// 468 | 462, 236 | 262: not taken.
 // What bounds it: 450 instructions and 48 products a warp and 16 tokens, with two CTAs' warps an SM (three of 64
 // dims) to hide their latencies (FP8: 0.36 of an instruction a clock and sub-partition, tensor pipe 35 %, HBM
 // 56 %); three sets' sums of O leave no registers for more.  Q^T comes from shared memory for the same reason:

@@ -47,6 +47,17 @@ def test_few_rows_under_a_window(q_type, kv_type, d, B, window, sinks):
 
 
 @pytest.mark.parametrize("q_type,kv_type,d", KINDS)
+@pytest.mark.parametrize("window,sinks", [(None, 0), (1000, 5)])
+def test_one_unit_an_sm(q_type, kv_type, d, window, sinks):
+    """As few units as the kernel takes: of 1,088 tokens, or a window of as many; fewer stay with the chunk kernel."""
+    rng = np.random.default_rng(d)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for S in (-(-sms // 8), (sms - 1) // 8, -(-3 * sms // 16), 5):
+        lens = rng.integers(5, 1089 if window is None else 1700, S).tolist()
+        run(rng, lens, [1 + i % 5 for i in range(S)], 32, 8, d, 16, q_type, kv_type, window, sinks)
+
+
+@pytest.mark.parametrize("q_type,kv_type,d", KINDS)
 def test_long_contexts(q_type, kv_type, d):
     rng = np.random.default_rng(3)
     lens, new = many(24, [20, 40, 33], [5, 1, 2])
