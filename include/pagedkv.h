@@ -200,10 +200,10 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  *   window     tokens, the query's own among them; at least 1 (INT_MAX: all)
  *   num_sinks  tokens, at least 0
  *   workspace  >= pkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned; where
- *              that is 0 it may be NULL.  It is 0 for 16-bit queries over 16-bit caches,
- *              over FP8 rows of 128 dims, and over 4 bits where the window and the sinks
- *              hold about 2,048 tokens at most; else what contexts of the window and the
- *              sinks need, however long max_context_len is
+ *              that is 0 it may be NULL.  It is 0 for 16-bit queries over 16-bit and FP8
+ *              caches, and over 4 bits where the window and the sinks hold about 2,048
+ *              tokens at most; else what contexts of the window and the sinks need,
+ *              however long max_context_len is
  *   the other arguments, types and errors as in pkv_paged_decode_attention; where no
  *   workspace is needed, pools of 2^31 rows or more (16 bits, FP8) and batches of 2^28
  *   (sequence, kv head, eight query heads) units return PKV_ERR_UNSUPPORTED.

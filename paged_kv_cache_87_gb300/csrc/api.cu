@@ -137,9 +137,9 @@ pkv_status make_fp4_plan(int S, int Hq, int Hkv, int HD, int B, int max_ctx, Fp4
 
 // Whether the window decode's own kernel serves these types and virtual contexts of up to max_seen
 // tokens: it needs no workspace and no plan.
-bool window_kernel(pkv_dtype q, pkv_dtype kv, int head_dim, int max_seen) {
+bool window_kernel(pkv_dtype q, pkv_dtype kv, int max_seen) {
     return (q == PKV_F16 || q == PKV_BF16) &&
-           (kv == q || (kv == PKV_FP4_E2M1 && max_seen <= kFp4WindowMost) || (kv == PKV_FP8_E4M3 && head_dim == 128));
+           (kv == q || kv == PKV_FP8_E4M3 || (kv == PKV_FP4_E2M1 && max_seen <= kFp4WindowMost));
 }
 
 // Whether a call of the chunk attention has sequences of few rows on average, and as many (sequence, kv head)
@@ -149,7 +149,7 @@ bool window_kernel(pkv_dtype q, pkv_dtype kv, int head_dim, int max_seen) {
 // 1,000: 24.3 | 24.4, 24.9 | 22.9, 21.2 | 16.9; 64 units of 1,000, FP8: 17.8 | 25.7.  Of 1,000 - 8,000, 64 dims,
 // 160 units: 49.6 | 77.3, 256 80.8 | 76.7, 456 134 | 95; 128 dims: FP8 456 units 147 | 163, 800 275 | 228.
 bool chunk_few(pkv_dtype kv, int head_dim, int64_t rows, int num_seqs, int64_t units, int64_t seen, int num_sms) {
-    const bool has = kv == PKV_FP4_E2M1 || (kv == PKV_FP8_E4M3) == (head_dim == 128);
+    const bool has = quantised(kv) || head_dim == 64;
     const int64_t least = seen <= kChunkFewShort ? num_sms : head_dim == 64 ? num_sms * 3 / 2 : num_sms * 5;
     return has && rows <= (int64_t)num_seqs * kChunkFewRows && units >= least && units <= INT32_MAX;
 }
@@ -350,10 +350,7 @@ pkv_status decode_impl(const void* query, const void* k_cache, const void* v_cac
     p.self_plan = !mma && max_seen <= plan.chunk_tokens;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (window)                              // (other 16-bit queries do not come here)
-        return cuda_status(q_dtype == PKV_F32   ? decode_window_f32(p, kv_dtype, hpi, s)
-                           : q_dtype == PKV_F16 ? decode_window_f16(p, hpi, s)
-                                                : decode_window_bf16(p, hpi, s));
+    if (window) return cuda_status(decode_window_f32(p, kv_dtype, hpi, s));     // (16-bit queries do not come here)
     switch (q_dtype) {
     case PKV_F32: err = decode_dispatch_f32(p, kv_dtype, hpi, s); break;
     case PKV_F16: err = decode_dispatch_f16(p, kv_dtype, hpi, s); break;
@@ -506,7 +503,7 @@ size_t pkv_decode_window_workspace_bytes(int num_seqs, int num_q_heads, int num_
         (block_size != 8 && block_size != 16 && block_size != 32))
         return 0;
     const int max_seen = window_most(max_context_len, window, num_sinks, block_size);
-    if (window_kernel(q_dtype, kv_dtype, head_dim, max_seen)) return 0;
+    if (window_kernel(q_dtype, kv_dtype, max_seen)) return 0;
     return pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seen, kv_dtype);
 }
 
@@ -520,7 +517,7 @@ pkv_status pkv_paged_decode_attention_window(
     if (block_size != 8 && block_size != 16 && block_size != 32)
         return block_size <= 0 ? PKV_ERR_INVALID_ARG : PKV_ERR_UNSUPPORTED;
     const int max_seen = window_most(max_context_len, window, num_sinks, block_size);
-    if (window_kernel(q_dtype, kv_dtype, head_dim, max_seen)) {
+    if (window_kernel(q_dtype, kv_dtype, max_seen)) {
         if (num_seqs < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 || num_q_heads <= 0 ||
             num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
             return PKV_ERR_INVALID_ARG;

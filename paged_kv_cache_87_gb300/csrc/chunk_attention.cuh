@@ -111,7 +111,7 @@ __host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end
 // Defined in chunk_plan.cu.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
 
-// The kernel of few rows, in front of the others: FP8 of 128 dims, 4 bits, 16 bits of 64.
+// The kernel of few rows, in front of the others: FP8, 4 bits, 16 bits of 64 dims.
 cudaError_t chunk_few_f16(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s);
 cudaError_t chunk_few_bf16(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s);
 

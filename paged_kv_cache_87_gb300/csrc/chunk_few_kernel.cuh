@@ -11,7 +11,7 @@
 // Contexts are not cut, so there have to be enough of them for the longest to end among the others (chunk_few in
 // api.cu, with what was measured on either side).  Large ones (us, the chunk kernel alone | with this one), 5 tokens
 // over 1,000 - 8,000, 32 / 8 heads, bf16 queries: FP8, d 128, 200 sequences 541 | 380, 100 275 | 228; 4 bits, d 128,
-// 588 | 355, 290 | 210; 16 bits, d 64, 412 | 254, 205 | 148.  3 tokens under a window of 1,024 + 4, 256 sequences:
+// 588 | 355, 290 | 210; d 64, 200 sequences: FP8 453 | 208, 4 bits 453 | 226, 16 bits 412 | 254.  3 tokens under a window of 1,024 + 4, 256 sequences:
 // FP8 219 | 154, 16 bits of 64 dims 194 | 102.  16 bits of 128 dims, where the chunk kernel widens nothing,
 // 468 | 462, 236 | 262: not taken.
 // What bounds it: 450 instructions and 48 products a warp and 16 tokens, with two CTAs' warps an SM (three of 64
@@ -180,7 +180,8 @@ cudaError_t launch_chunk_few(const ChunkParams& p, cudaStream_t stream) {
 
 template <typename QT>
 cudaError_t launch_chunk_few_q(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s) {
-    if (kv == PKV_FP8_E4M3) return launch_chunk_few<QT, E4M3, 128>(p, s);
+    if (kv == PKV_FP8_E4M3)
+        return head_dim == 128 ? launch_chunk_few<QT, E4M3, 128>(p, s) : launch_chunk_few<QT, E4M3, 64>(p, s);
     if (kv == PKV_FP4_E2M1)
         return head_dim == 128 ? launch_chunk_few<QT, E2M1, 128>(p, s) : launch_chunk_few<QT, E2M1, 64>(p, s);
     return launch_chunk_few<QT, QT, 64>(p, s);

@@ -164,8 +164,8 @@ cudaError_t dispatch_decode_kv(const DecodeParams& p, int hpi, cudaStream_t stre
     return launch_decode_simt<QT, KT, 64, 4>(p, stream);
 }
 
-// Under a sliding window (p.window) the CUDA-core kernel over virtual contexts serves fp32 queries, and
-// 16-bit ones over FP8 rows of 64 dims; the rest has a kernel of its own (decode_window_kernel.cuh).
+// Under a sliding window (p.window) the CUDA-core kernel over virtual contexts serves fp32 queries; 16-bit
+// ones have a kernel of their own (decode_window_kernel.cuh).
 template <typename QT, typename KT, int HD>
 cudaError_t dispatch_window(const DecodeParams& p, int hpi, cudaStream_t stream) {
     if (hpi == 1) return launch_decode_simt<QT, KT, HD, 1, true>(p, stream);
@@ -175,8 +175,6 @@ cudaError_t dispatch_window(const DecodeParams& p, int hpi, cudaStream_t stream)
 
 // Defined in decode_window_f32.cu / decode_window_f16.cu / decode_window_bf16.cu.
 cudaError_t decode_window_f32(const DecodeParams& p, pkv_dtype kv, int hpi, cudaStream_t s);
-cudaError_t decode_window_f16(const DecodeParams& p, int hpi, cudaStream_t s);
-cudaError_t decode_window_bf16(const DecodeParams& p, int hpi, cudaStream_t s);
 cudaError_t window_kernel_f16(const DecodeParams& p, pkv_dtype kv, cudaStream_t s);
 cudaError_t window_kernel_bf16(const DecodeParams& p, pkv_dtype kv, cudaStream_t s);
 

@@ -4,12 +4,9 @@
 
 namespace pkv {
 
-cudaError_t decode_window_f16(const DecodeParams& p, int hpi, cudaStream_t s) {
-    return dispatch_window<F16, E4M3, 64>(p, hpi, s);
-}
-
 cudaError_t window_kernel_f16(const DecodeParams& p, pkv_dtype kv, cudaStream_t s) {
-    if (kv == PKV_FP8_E4M3) return launch_decode_window<F16, E4M3, 128>(p, s);
+    if (kv == PKV_FP8_E4M3)
+        return p.head_dim == 128 ? launch_decode_window<F16, E4M3, 128>(p, s) : launch_decode_window<F16, E4M3, 64>(p, s);
     if (kv == PKV_FP4_E2M1)
         return p.head_dim == 128 ? launch_decode_window<F16, E2M1, 128>(p, s) : launch_decode_window<F16, E2M1, 64>(p, s);
     return p.head_dim == 128 ? launch_decode_window<F16, F16, 128>(p, s) : launch_decode_window<F16, F16, 64>(p, s);

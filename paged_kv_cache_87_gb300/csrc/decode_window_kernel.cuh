@@ -11,7 +11,8 @@
 // the context are masked in S and their rows of V zeroed in shared memory, by the warp that multiplies them.
 //
 // Measured (us; of the bytes' time at 6,792 GB/s): 256 sequences of 64 - 32k, 32 / 8 heads, d 128, bf16 under
-// 1,024 + 4: 115 (1.0); 64 of 4k - 131k, 64 / 8, FP8 under 4,096 + 16: 85 (0.94), both bound by HBM; over 4 bits
+// 1,024 + 4: 115 (1.0); 64 of 4k - 131k, 64 / 8, FP8 under 4,096 + 16: 85 (0.94), of 64 dims under 4,096: 45 (0.89),
+// all bound by HBM; over 4 bits
 // 256 under 1,024: 74 (0.6), bound by the widening's instructions (2.65 of 4 a clock); one sequence under
 // 1,024: 5.3 (0.11), bound by the latency of length, table, first tile and the cluster's meeting.
 #pragma once

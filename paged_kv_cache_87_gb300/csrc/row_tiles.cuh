@@ -39,19 +39,21 @@ struct TileCfg {
     using MT = typename std::conditional<FP8 || FP4, F16, QT>::type;
     static constexpr int ELEM_BYTES = FP8 || FP4 ? 1 : 2;
     static constexpr int ROWB = FP4 ? HD / 2 + HD / 16 : HD * ELEM_BYTES;
-    static constexpr int HALVES = FP4 ? 1 : ROWB / 128;
-    static constexpr int ELEMS = 128 / ELEM_BYTES;                // elements of a 128-byte slice
+    // rows lie in slices of 128 bytes (FP8 of 64 dims: 64), under the swizzle of that width
+    static constexpr int SLICE = !FP4 && ROWB == 64 ? 64 : 128;
+    static constexpr int HALVES = FP4 ? 1 : ROWB / SLICE;
+    static constexpr int ELEMS = SLICE / ELEM_BYTES;              // elements of a slice
     // f16 weights are taken 2^7 above the running maximum: 2^-32 of the largest still counts
     static constexpr float LIFT = std::is_same<MT, F16>::value ? 7.f : 0.f;
     static constexpr int KSTEPS = HD / 16, MTILES = HD / 16;
-    static constexpr int HALF_BYTES = kRowTile * 128;
+    static constexpr int HALF_BYTES = kRowTile * SLICE;
     static constexpr int KV_BYTES = FP4 ? kRowTile * ROWB : HALVES * HALF_BYTES;
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
     // stages of the ring: the most, and the fewest, with which a CTA more is resident (FP8, and 16 bits
     // of 128 dims)
-    static constexpr int NSTAGE = N > 1 ? (FP4 ? 8 : HD == 64 ? 4 : 6)
-                                        : STAGE_BYTES == 32768 ? 3 : FP4 && HD == 64 ? 6 : 4;
-    static constexpr int FEWEST = N > 1 ? NSTAGE : FP8 ? 3 : STAGE_BYTES == 32768 ? 2 : NSTAGE;
+    static constexpr int NSTAGE = N > 1 ? (FP4 || SLICE == 64 ? 8 : HD == 64 ? 4 : 6)
+                                        : STAGE_BYTES == 32768 ? 3 : HD == 64 && STAGE_BYTES <= 8192 ? 6 : 4;
+    static constexpr int FEWEST = N > 1 || SLICE == 64 ? NSTAGE : FP8 ? 3 : STAGE_BYTES == 32768 ? 2 : NSTAGE;
     // in front of the ring: the barriers; one set: the CTA's state [8][HD], (m, l)[8]; several: the fragments
     // of Q^T, and where the rows are (their place in q and out, 64 bits, their token's in the virtual context)
     static constexpr int OFF_MINE = 128, OFF_Q = 128;
@@ -60,10 +62,15 @@ struct TileCfg {
     static constexpr int smem(int stages) { return OFF_RING + stages * STAGE_BYTES + 1024; }
     static constexpr int HS = HD + 4;                             // stride of a head's row where warps meet
     static_assert(kRowWarps * 8 * N * (HS + 2) * 4 <= FEWEST * STAGE_BYTES, "the ring holds the warps' states");
-    static_assert(FP4 || ROWB >= 128, "rows of 128 bytes or more");
     // resident, at most
     static constexpr int CTAS = N > 1 ? (HD == 64 ? 3 : 2) : STAGE_BYTES == 32768 ? 3 : FP4 ? (HD == 64 ? 7 : 4) : FP8 ? 4 : 3;
 };
+
+// Byte offset of 16-byte chunk `chunk` of row r in a slice of a tile.
+template <typename C>
+__device__ __forceinline__ uint32_t tile_at(int r, int chunk) {
+    return C::SLICE == 64 ? (uint32_t)(r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4)) : swz(r, chunk);
+}
 
 // Where a lane's operands of a tile are.
 template <typename C, int HD>
@@ -144,7 +151,7 @@ __device__ __forceinline__ void tile_producer(const void* k_cache, const void* v
                               policy);
             } else {
                 const int y = (phys * num_kv_heads + kvh) << logB;
-                to += (lane << logB) * 128;
+                to += (lane << logB) * C::SLICE;
 #pragma unroll
                 for (int h = 0; h < C::HALVES; ++h) {
                     tma_load_2d(to + h * C::HALF_BYTES, tmK, h * C::ELEMS, y, &full[stage], policy);
@@ -210,9 +217,9 @@ __device__ __forceinline__ void tile_zero_rows(const TileLane<C, HD>& w, uint8_t
 #pragma unroll
         for (int h = 0; h < C::HALVES; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(sb + C::KV_BYTES + h * C::HALF_BYTES + (16 * w.warp + r) * 128 +
-                                          ((w.lane & 1) * 4 + k) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < C::SLICE / 32; ++k)
+                *reinterpret_cast<uint4*>(sb + C::KV_BYTES + h * C::HALF_BYTES + (16 * w.warp + r) * C::SLICE +
+                                          ((w.lane & 1) * (C::SLICE / 32) + k) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();                        // before the ring's next copy
     __syncwarp();
 }
@@ -265,7 +272,7 @@ __device__ __forceinline__ void tile_scores(const TileLane<C, HD>& w, const uint
 #pragma unroll ROLL
         for (int pr = 0; pr < C::KSTEPS / 2; ++pr) {
             uint32_t r[4];
-            ldsm_x4(sK + swz(w.rl, 2 * pr + (w.lane >> 4)), r);
+            ldsm_x4(sK + tile_at<C>(w.rl, 2 * pr + (w.lane >> 4)), r);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint32_t f[4] = {e4m3x2_of<0>(r[2 * k]), e4m3x2_of<0>(r[2 * k + 1]),
@@ -281,7 +288,7 @@ __device__ __forceinline__ void tile_scores(const TileLane<C, HD>& w, const uint
 #pragma unroll (N > 1 ? 2 : 8)
         for (int k = 0; k < C::KSTEPS; ++k) {
             uint32_t f[4];
-            ldsm_x4(sK + (k >> 2) * C::HALF_BYTES + swz(w.rl, (k & 3) * 2 + (w.lane >> 4)), f);
+            ldsm_x4(sK + (k >> 2) * C::HALF_BYTES + tile_at<C>(w.rl, (k & 3) * 2 + (w.lane >> 4)), f);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint2 b = q(i, k);
@@ -396,7 +403,7 @@ __device__ __forceinline__ void tile_weigh(const TileLane<C, HD>& w, const uint8
 #pragma unroll
         for (int pr = 0; pr < C::MTILES / 2; ++pr) {
             uint32_t r[4], ev[4], od[4];
-            ldsm_x4_trans(sV + swz(w.rv, 2 * pr + (w.mi & 1)), r);
+            ldsm_x4_trans(sV + tile_at<C>(w.rv, 2 * pr + (w.mi & 1)), r);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t pairs = __byte_perm(r[k], 0u, 0x3120);        // even dims' pair, odd dims'
@@ -413,7 +420,7 @@ __device__ __forceinline__ void tile_weigh(const TileLane<C, HD>& w, const uint8
 #pragma unroll
         for (int mt = 0; mt < C::MTILES; ++mt) {
             uint32_t f[4];
-            ldsm_x4_trans(sV + (mt >> 2) * C::HALF_BYTES + swz(w.rv, (mt & 3) * 2 + (w.mi & 1)), f);
+            ldsm_x4_trans(sV + (mt >> 2) * C::HALF_BYTES + tile_at<C>(w.rv, (mt & 3) * 2 + (w.mi & 1)), f);
 #pragma unroll
             for (int i = 0; i < N; ++i) Mma<MT>::run(o[i][mt], f, b[i][0], b[i][1]);
         }

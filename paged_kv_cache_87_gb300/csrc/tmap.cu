@@ -3,7 +3,8 @@
 // A pool [num_blocks][num_kv_heads][B][d] is viewed as a 2-D tensor of
 // num_blocks*num_kv_heads*B rows by d columns.  One box = 128 bytes of a row
 // (64 two-byte or 128 one-byte elements) x B rows, with the 128-byte swizzle,
-// so one (block, kv head) tile of a 128-byte-row half lands as B swizzled rows.
+// so one (block, kv head) tile of a 128-byte-row half lands as B swizzled rows.  FP8 rows of 64
+// elements are boxes of 64 bytes with the 64-byte swizzle.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -41,12 +42,14 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, int head_dim, int elem_
     if (!enc || rows <= 0 || rows > 0x7fffffffLL) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)head_dim * elem_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes), (cuuint32_t)box_rows};
+    const bool narrow = head_dim * elem_bytes == 64;
+    const cuuint32_t box[2] = {(cuuint32_t)((narrow ? 64 : 128) / elem_bytes), (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType dt =
         elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     return enc(map, dt, 2, const_cast<void*>(pool), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }

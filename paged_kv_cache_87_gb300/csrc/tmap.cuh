@@ -6,7 +6,7 @@
 namespace pkv {
 
 // 2-D map over `rows` rows of `head_dim` elements of `elem_bytes` bytes; box =
-// 128 bytes x `box_rows` rows, 128-byte swizzle.  False if it cannot be encoded.
+// 128 bytes x `box_rows` rows, 128-byte swizzle (rows of 64 bytes: the 64-byte one).  False if it cannot be encoded.
 bool encode_pool_map(CUtensorMap* map, const void* pool, int head_dim, int elem_bytes,
                      long long rows, int box_rows);
 

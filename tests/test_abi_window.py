@@ -42,11 +42,11 @@ def test_window_types_and_workspace(lib):
     assert _window(lib, NB=2 ** 24) == E.PKV_ERR_UNSUPPORTED       # 2^31 rows of a pool
     need = binding.pkv_decode_window_workspace_bytes
     # none for the one-launch kernel; else by what is seen, not by the context
-    for q, kv, d in (("bf16", "bf16", 64), ("f16", "e4m3", 128), ("bf16", "e2m1", 128)):
+    for q, kv, d in (("bf16", "bf16", 64), ("f16", "e4m3", 128), ("f16", "e4m3", 64), ("bf16", "e2m1", 128)):
         assert need(4, 8, 8, d, 16, 10 ** 6, 1000, 4, q, kv) == 0
     assert _window(lib, qt=0, kt=0) == E.PKV_ERR_WORKSPACE
-    assert _window(lib, qt=1, kt=3) == E.PKV_ERR_WORKSPACE         # FP8 rows of 64 dims
-    for q, kv, d in (("f32", "f32", 64), ("f16", "e4m3", 64), ("f32", "e2m1", 128), ("f16", "e2m1", 128)):
+    assert _window(lib, qt=0, kt=3) == E.PKV_ERR_WORKSPACE
+    for q, kv, d in (("f32", "f32", 64), ("f32", "e4m3", 64), ("f32", "e2m1", 128), ("f16", "e2m1", 128)):
         a, b = (need(4, 8, 8, d, 16, ctx, 5000, 4, q, kv) for ctx in (20000, 10 ** 6))
         assert a == b > 0
         assert (need(4, 8, 8, d, 16, 100, 5000, 4, q, kv) > 0) == ((q, kv) != ("f16", "e2m1"))

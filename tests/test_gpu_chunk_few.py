@@ -11,7 +11,7 @@ from tests.window_cases import Paged
 pytestmark = pytest.mark.gpu
 
 # what that kernel serves; other types and sizes stay with the chunk kernel
-KINDS = [("bf16", "e4m3", 128), ("f16", "e4m3", 128), ("bf16", "fp4", 128), ("f16", "fp4", 128), ("bf16", "fp4", 64),
+KINDS = [("bf16", "e4m3", 128), ("f16", "e4m3", 128), ("bf16", "e4m3", 64), ("f16", "e4m3", 64), ("bf16", "fp4", 128), ("f16", "fp4", 128), ("bf16", "fp4", 64),
          ("f16", "fp4", 64), ("bf16", "bf16", 64), ("f16", "f16", 64)]
 
 
