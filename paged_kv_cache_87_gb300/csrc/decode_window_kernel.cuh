@@ -12,9 +12,9 @@
 //
 // Measured (us; of the bytes' time at 6,792 GB/s): 256 sequences of 64 - 32k, 32 / 8 heads, d 128, bf16 under
 // 1,024 + 4: 115 (1.0); 64 of 4k - 131k, 64 / 8, FP8 under 4,096 + 16: 85 (0.94), of 64 dims under 4,096: 45 (0.89),
-// all bound by HBM; over 4 bits
-// 256 under 1,024: 74 (0.6), bound by the widening's instructions (2.65 of 4 a clock); one sequence under
-// 1,024: 5.3 (0.11), bound by the latency of length, table, first tile and the cluster's meeting.
+// all bound by HBM; over 4 bits 256 under 1,024: 74 (0.6), bound by the widening's instructions (2.65 of 4 a
+// clock); one sequence under 1,024: 5.3 (0.11), bound by the latency of length, table, first tile and the
+// cluster's meeting.
 #pragma once
 
 #include "row_tiles.cuh"
@@ -130,9 +130,8 @@ __global__ void __launch_bounds__(kRowThreads, (TileCfg<QT, KT, HD, 1>::CTAS)) d
 // resident CTAs, each of a CTA's tiles and kWinStart for its start and its end (and as much again for a
 // cluster's meeting).  Measured (us): one sequence under 1,024 tokens 5.1 in clusters of eight; 80 units of
 // 4,096 27.6 in pairs, 35.5 in fours; 160 units of 4,096 49.6 alone, 60.2 in pairs; 320 of 1,024 33.8 in three
-// stages, 27.4 in two; FP8, 512 units of 4,096
-// 94 in fours of four stages (three CTAs an SM), 85 alone of three (four an SM), 320 units of 1,024 15.0
-// and 18.6 alone of four and of three.
+// stages, 27.4 in two; FP8, 512 units of 4,096 94 in fours of four stages (three CTAs an SM), 85 alone of three
+// (four an SM), 320 units of 1,024 15.0 and 18.6 alone of four and of three.
 constexpr int kWinStart = 3;
 
 template <typename QT, typename KT, int HD>
