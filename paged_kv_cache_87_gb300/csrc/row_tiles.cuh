@@ -50,10 +50,11 @@ struct TileCfg {
     static constexpr int KV_BYTES = FP4 ? kRowTile * ROWB : HALVES * HALF_BYTES;
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
     // stages of the ring: the most, and the fewest, with which a CTA more is resident (FP8, and 16 bits
-    // of 128 dims)
+    // of 128 dims).  FP8 of 64 dims, 1,340 units of 514 tokens: 26.0 us with four CTAs of six stages alone, 20.0
+    // with five of five beside them, 20.9 with six of four, whose 64 registers cost 64 x 4,096 44.7 -> 47.0
     static constexpr int NSTAGE = N > 1 ? (FP4 || SLICE == 64 ? 8 : HD == 64 ? 4 : 6)
                                         : STAGE_BYTES == 32768 ? 3 : HD == 64 && STAGE_BYTES <= 8192 ? 6 : 4;
-    static constexpr int FEWEST = N > 1 || SLICE == 64 ? NSTAGE : FP8 ? 3 : STAGE_BYTES == 32768 ? 2 : NSTAGE;
+    static constexpr int FEWEST = N > 1 ? NSTAGE : SLICE == 64 ? 5 : FP8 ? 3 : STAGE_BYTES == 32768 ? 2 : NSTAGE;
     // in front of the ring: the barriers; one set: the CTA's state [8][HD], (m, l)[8]; several: the fragments
     // of Q^T, and where the rows are (their place in q and out, 64 bits, their token's in the virtual context)
     static constexpr int OFF_MINE = 128, OFF_Q = 128;
@@ -63,7 +64,11 @@ struct TileCfg {
     static constexpr int HS = HD + 4;                             // stride of a head's row where warps meet
     static_assert(kRowWarps * 8 * N * (HS + 2) * 4 <= FEWEST * STAGE_BYTES, "the ring holds the warps' states");
     // resident, at most
-    static constexpr int CTAS = N > 1 ? (HD == 64 ? 3 : 2) : STAGE_BYTES == 32768 ? 3 : FP4 ? (HD == 64 ? 7 : 4) : FP8 ? 4 : 3;
+    static constexpr int CTAS = N > 1                  ? (HD == 64 ? 3 : 2)
+                                : STAGE_BYTES == 32768 ? 3
+                                : FP4                  ? (HD == 64 ? 7 : 4)
+                                : FP8                  ? (HD == 64 ? 5 : 4)
+                                                       : 3;
 };
 
 // Byte offset of 16-byte chunk `chunk` of row r in a slice of a tile.
