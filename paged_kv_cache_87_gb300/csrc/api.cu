@@ -473,7 +473,8 @@ pkv_status pkv_paged_chunk_attention(
     // (items that are no longer than this, and one a CTA, are never cut)
     p.may_split = pl.items > p.num_ctas || most_steps > kChunkMinRun + kChunkSplitCost;
     const float kv = quantised(kv_dtype) ? kv_scale : 1.f;
-    p.qk_scale_log2 = scale * 1.4426950408889634f * kv;
+    const float qk = scale * 1.4426950408889634f * kv;
+    p.qk_scale_log2 = qk > 0.f ? qk : 0x1p-149f;       // (never 0: masked scores, -inf, are multiplied by it)
     p.out_scale = kv;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = q_dtype == PKV_BF16;

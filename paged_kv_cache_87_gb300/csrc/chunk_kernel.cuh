@@ -587,11 +587,11 @@ __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t to, int logB, 
     }
 }
 
-// Row r of a Q tile (bf16) at shared address `tile` to f16 in place, times 2^e; returns e (2^60 at
-// most, so that the logit scale that undoes it stays a normal number; rows below 2^-46 lose what is
-// 2^-24 under 2^-60).
+// Row r of a Q tile (bf16) at shared address `tile` to f16 in place, times 2^e; returns e: `most` at
+// most, so that the logit scale, times the 2^-e that undoes it, is never 0 (rows below 2^-46 lose what is 2^-24
+// under 2^-60).
 template <typename C, int HD>
-__device__ __forceinline__ int scale_q_row(uint32_t tile, int r) {
+__device__ __forceinline__ int scale_q_row(uint32_t tile, int r, int most) {
     const uint32_t row = tile + r * 128, x7 = (r & 7) << 4;
     auto at = [&](int c) { return row + (c >> 3) * C::HALF_BYTES + (((c & 7) << 4) ^ x7); };
     uint32_t top = 0u;                 // the largest magnitudes of even and of odd dims
@@ -609,7 +609,7 @@ __device__ __forceinline__ int scale_q_row(uint32_t tile, int r) {
         }
     }
     const int ex = (int)(max(top >> 16, top & 0xffffu) >> 7) - 127;    // floor(log2); 128: not finite
-    const int e = ex == 128 ? 0 : min(14 - ex, 60);
+    const int e = ex == 128 ? 0 : min(14 - ex, most);
     const float up = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll 1
     for (int c0 = 0; c0 < HD / 8; c0 += 2) {
@@ -636,6 +636,8 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
                                               const ChunkSlot* items, volatile int* abort_flag) {
     const int tid = threadIdx.x - 384, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
+    // 2^-most times the logit scale is a normal number (of a subnormal scale, more than it)
+    const int most_e = min(60, (int)(__float_as_uint(p.qk_scale_log2) >> 23) - 1);
     int st = 0, rs = 0;                                  // an entry's places, and their phases
     uint32_t st_phase = 0, rs_phase = 0;
     bool ok = true;
@@ -677,7 +679,8 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
                 int8_t* back = reinterpret_cast<int8_t*>(smem + C::OFF_BACK) + (k & 1) * 256;
 #pragma unroll 1
                 for (int X = 0; X < (it.qn_b > 0 ? 2 : 1); ++X)
-                    back[X * kT + tid] = (int8_t)scale_q_row<C, HD>(base + C::OFF_Q + X * C::TILE_BYTES, tid);
+                    back[X * kT + tid] =
+                        (int8_t)scale_q_row<C, HD>(base + C::OFF_Q + X * C::TILE_BYTES, tid, most_e);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.q_full[k & 1]);

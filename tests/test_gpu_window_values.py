@@ -1,0 +1,39 @@
+"""Windowed decode and chunks at the ends of what scales, logits and rounding allow."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_87_gb300 import binding
+from tests.test_gpu_chunk import chunk
+from tests.test_gpu_chunk_few import many
+from tests.test_gpu_window import decode
+from tests.window_cases import DT, HALF, Paged
+
+pytestmark = pytest.mark.gpu
+
+
+def everywhere(rng, hq, h, d, B, q_type, kv_type, window=None, sinks=0, **kw):
+    """A call of every kernel that serves these types: chunks of one and of two row tiles an item, the kernel of
+    few rows, the windowed decode of one CTA a unit and of several."""
+    for lens, new in (([150, 20], [90, 20]), ([300, 260], [300, 130]), many(h, [40, 21, 130], [2, 1, 3])):
+        yield chunk, Paged(rng, lens, new, hq, h, d, B, q_type, kv_type, window, sinks, **kw)
+    for lens in ([150, 20, 700], [30] * 400):
+        yield decode, Paged(rng, lens, [1] * len(lens), hq, h, d, B, q_type, kv_type, window, sinks, **kw)
+
+
+@pytest.mark.parametrize("kv_type", ["e4m3", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_zeros_under_tiny_scales_give_the_mean(kv_type, d):
+    """Logits are zeros, or far below what counts, however small scale and kv_scale get."""
+    rng = np.random.default_rng(d)
+    cases = [("bf16", 2.0 ** -100, None), ("bf16", 2.0 ** -126, None), ("bf16", 2.0 ** -100, 2.0 ** -100),
+             ("bf16", 2.0 ** -5, 2.0 ** -149), ("f16", 2.0 ** -5, 2.0 ** -149)]     # (f16 holds no smaller values)
+    for q_type, kv_scale, scale in cases:
+        for call, c in everywhere(rng, 4, 2, d, 16, q_type, kv_type, 60, 3, kv_scale=kv_scale):
+            if scale:
+                c.q = torch.from_numpy(rng.standard_normal(c.q.shape)).to(DT[q_type]).cuda()
+                c.scale = scale
+            c.q[2] = 0
+            c.q[:, 1] = 0
+            c.check(call(c))
+    assert binding.pkv_get_device_status() == 0
