@@ -588,8 +588,8 @@ __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t to, int logB, 
 }
 
 // Row r of a Q tile (bf16) at shared address `tile` to f16 in place, times 2^e; returns e: `most` at
-// most, so that the logit scale, times the 2^-e that undoes it, is never 0 (rows below 2^-46 lose what is 2^-24
-// under 2^-60).
+// most, so that the logit scale, times the 2^-e that undoes it, is never 0 (rows below 2^-112, or whose logits
+// are nothing, lose what is 2^-24 under 2^-most).
 template <typename C, int HD>
 __device__ __forceinline__ int scale_q_row(uint32_t tile, int r, int most) {
     const uint32_t row = tile + r * 128, x7 = (r & 7) << 4;
@@ -637,7 +637,7 @@ __device__ __forceinline__ void chunk_widener(const ChunkParams& p, uint8_t* sme
     const int tid = threadIdx.x - 384, lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
     // 2^-most times the logit scale is a normal number (of a subnormal scale, more than it)
-    const int most_e = min(60, (int)(__float_as_uint(p.qk_scale_log2) >> 23) - 1);
+    const int most_e = min(126, (int)(__float_as_uint(p.qk_scale_log2) >> 23) - 1);
     int st = 0, rs = 0;                                  // an entry's places, and their phases
     uint32_t st_phase = 0, rs_phase = 0;
     bool ok = true;

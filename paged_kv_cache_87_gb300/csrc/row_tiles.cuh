@@ -189,8 +189,8 @@ __device__ __forceinline__ void tile_query(const TileLane<C, HD>& w, const uint1
         }
     }
     if constexpr (!std::is_same<QT, MT>::value) {
-        // bf16 queries beside f16 operands: the row's largest magnitude to [2^14, 2^15), by 2^60 at
-        // most, so that what undoes it in the logit scale stays a normal number
+        // bf16 queries beside f16 operands: the row's largest magnitude to [2^14, 2^15), by 2^126 at
+        // most, so that what undoes it in the logit scale is a normal number
         uint32_t top = 0u;
 #pragma unroll
         for (int t = 0; t < C::KSTEPS; ++t)
@@ -198,7 +198,7 @@ __device__ __forceinline__ void tile_query(const TileLane<C, HD>& w, const uint1
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = (int)(max(top >> 16, top & 0xffffu) >> 7) - 127;
-        const int e = ex == 128 ? 0 : min(14 - ex, 60);
+        const int e = ex == 128 ? 0 : min(14 - ex, 126);
         const float up = __uint_as_float((uint32_t)(e + 127) << 23);
         const float back = qs0 * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll

@@ -37,3 +37,15 @@ def test_rows_of_zeros_under_tiny_scales_give_the_mean(kv_type, d):
             c.q[:, 1] = 0
             c.check(call(c))
     assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("kv_type", ["e4m3", "fp4"])
+@pytest.mark.parametrize("kv_scale", [2.0 ** 100, 2.0 ** 60, 2.0 ** -110])
+def test_bf16_rows_beside_caches_of_any_scale(kv_type, kv_scale):
+    """Logits of unit spread from queries near 1 / kv_scale: rows are scaled into f16 wherever they lie."""
+    rng = np.random.default_rng(1)
+    for call, c in everywhere(rng, 4, 2, 128, 16, "bf16", kv_type, 60, 3, kv_scale=kv_scale):
+        mul = torch.from_numpy(2.0 ** rng.integers(-12, 3, (len(c.q), 4, 1)).astype(np.float64)).cuda()
+        c.q = (c.q.double() * mul).to(torch.bfloat16)
+        c.check(call(c))
+    assert binding.pkv_get_device_status() == 0
