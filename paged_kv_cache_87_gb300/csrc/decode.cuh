@@ -219,6 +219,12 @@ __device__ __forceinline__ void merge_factor(float ma, float mb, float& fa, floa
     fb = mb == -INFINITY ? 0.f : fast_exp2(mb - M);
 }
 
+// Whether a sum of weights is divided by; else the output is zeros.  Under a window a sum that is NaN, from a NaN
+// key in sight, makes the output NaN; without one it gives zeros, here as in the other plain decodes.
+__device__ __forceinline__ bool has_weights(const DecodeParams& p, float sum) {
+    return p.window ? sum != 0.f : sum > 0.f;
+}
+
 // End of a work item, after every consumer warp has put its state in `scratch`
 // ([NCW][HPI][HD] acc, then [NCW][HPI] m, then [NCW][HPI] l; all relative to
 // the warp's own reference max, log2 domain).  Merges the warps by the
@@ -252,7 +258,7 @@ __device__ __forceinline__ void finish_item(const DecodeParams& p, const StageMe
         }
         const int64_t sh = (int64_t)meta.s * p.num_q_heads + hq0 + h;
         if (single) {
-            store_from_float<QT>(p.out, sh * HD + dim, L > 0.f ? A / L * p.out_scale : 0.f);
+            store_from_float<QT>(p.out, sh * HD + dim, has_weights(p, L) ? A / L * p.out_scale : 0.f);
         } else {
             const int64_t pi = sh * p.part_stride + meta.chunk;
             p.ws.pacc[pi * HD + dim] = A;
@@ -310,7 +316,7 @@ __device__ __forceinline__ void finish_item(const DecodeParams& p, const StageMe
                 A = fmaf(__ldcg(&p.ws.pacc[(sh * p.part_stride + c) * HD + dim]),
                          f_tab[h * kMaxMergeChunks + c], A);
             const float L = lsum[h];
-            store_from_float<QT>(p.out, sh * HD + dim, L > 0.f ? A / L * p.out_scale : 0.f);
+            store_from_float<QT>(p.out, sh * HD + dim, has_weights(p, L) ? A / L * p.out_scale : 0.f);
         }
     }
     named_bar_sync(1, NT);   // scratch and misc are reused by the next item

@@ -49,3 +49,22 @@ def test_bf16_rows_beside_caches_of_any_scale(kv_type, kv_scale):
         c.q = (c.q.double() * mul).to(torch.bfloat16)
         c.check(call(c))
     assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("kv_type", ["f32", "e4m3", "fp4"])
+@pytest.mark.parametrize("lens,window,at", [([100, 100], 50, 99), ([9000, 4000], 8000, 1500), ([3, 3], 1, 2)])
+def test_a_nan_key_that_is_seen_reaches_fp32_queries(kv_type, lens, window, at):
+    """... of its kv head and its sequence, and no others: alone, among pieces that are joined, and alone in sight."""
+    rng = np.random.default_rng(2)
+    c = Paged(rng, lens, [1] * 2, 4, 2, 128, 16, "f32", kv_type, window, 0, kv_scale=1.0 if kv_type == "f32" else 0.5)
+    blk, row = int(c.table[0, at // 16]), at % 16
+    if kv_type == "f32":
+        c.caches[0][blk, 1, row] = float("nan")
+    elif kv_type == "e4m3":
+        c.caches[0].view(torch.uint8)[blk, 1, row] = 0x7F
+    else:
+        c.caches[0].view(-1, 2, 16 * 72)[blk, 1, 16 * 64:].view(16, 8)[row] = 0x7F     # the row's scales
+    out = decode(c)
+    assert torch.isnan(out[0, 2:]).all() and not torch.isnan(out[0, :2]).any()
+    assert not torch.isnan(out[1]).any()
+    assert binding.pkv_get_device_status() == 0
