@@ -210,7 +210,7 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  * Where no workspace is needed: one launch, a cluster of up to eight CTAs a unit; logits,
  * maxima, sums and states are fp32, the weights enter the product with V in the operands'
  * type (f16 over FP8 and 4 bits: taken 2^7 above the running maximum, 2^-32 of the largest
- * is what is lost) and the denominator sums them unrounded; over FP8 and 4 bits bf16 queries
+ * is what is lost) and the denominator sums them as rounded; over FP8 and 4 bits bf16 queries
  * are scaled into f16 by a power of two per head.  The rest: launches and rounding of
  * pkv_paged_decode_attention.
  */
@@ -362,7 +362,7 @@ PKV_API pkv_status pkv_paged_tree_attention(
  * cache's 16-bit type; over FP8 and 4 bits they are f16, which the cached values are exactly, and
  * bf16 queries are scaled into f16 by a power of two per row (a value keeps its bits down to 2^-29
  * of the row's largest).  Softmax weights enter the product with V in the operands' type (f16:
- * 2^-32 of the largest is what is lost), the denominator sums them unrounded.
+ * 2^-32 of the largest is what is lost), the denominator sums them unrounded (sequences of few rows, below: as rounded).
  * Up to four launches: many sequences with up to 24 rows of a kv head (tokens times its query heads)
  * on average have these taken by a kernel of their own; then a planner (few sequences are planned by
  * the attention itself), the attention, and the joining of what was split over several SMs (few or

@@ -341,10 +341,10 @@ __device__ __forceinline__ void tile_softmax(const float (&x)[N][4], float (&m)[
     for (int i = 0; i < N; ++i) {
         // (a warp that has seen nothing yet has a maximum of -inf: its weights are zeros)
         const float s0 = m[i][0] == -INFINITY ? 0.f : m[i][0] - C::LIFT, s1 = m[i][1] == -INFINITY ? 0.f : m[i][1] - C::LIFT;
-        const float w0 = fast_exp2(x[i][0] - s0), w1 = fast_exp2(x[i][1] - s1), w2 = fast_exp2(x[i][2] - s0),
-                    w3 = fast_exp2(x[i][3] - s1);
-        float unused;
-        const uint32_t p01 = Mma<MT>::pack(w0, w1, unused, unused), p23 = Mma<MT>::pack(w2, w3, unused, unused);
+        // the sum is of the weights as they are multiplied, rounded to 16 bits
+        float w0, w1, w2, w3;
+        const uint32_t p01 = Mma<MT>::pack(fast_exp2(x[i][0] - s0), fast_exp2(x[i][1] - s1), w0, w1);
+        const uint32_t p23 = Mma<MT>::pack(fast_exp2(x[i][2] - s0), fast_exp2(x[i][3] - s1), w2, w3);
         l[i][0] += w0 + w2;
         l[i][1] += w1 + w3;
         b[i][0] = movmatrix_trans(p01);

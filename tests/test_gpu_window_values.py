@@ -68,3 +68,40 @@ def test_a_nan_key_that_is_seen_reaches_fp32_queries(kv_type, lens, window, at):
     assert torch.isnan(out[0, 2:]).all() and not torch.isnan(out[0, :2]).any()
     assert not torch.isnan(out[1]).any()
     assert binding.pkv_get_device_status() == 0
+
+
+def _agreeing(q_type, kv_type, d, lens, new, hq, h, window):
+    """Logits of 0 in every 16th token and x in the others, where 2^x is rounded down by nearly a whole half step of
+    q_type; values of 1.  Every 16 tokens hold both, so that whoever walks them has 0 as the largest."""
+    p = {"bf16": 8, "f16": 11}[q_type]
+    x = np.log2(1 + 2.0 ** -p - 2.0 ** (-p - 4)) - 1           # rounds to 1/2
+    c = Paged(np.random.default_rng(4), lens, new, hq, h, d, 16, q_type, kv_type, window, 0)
+    for i, raw in enumerate(c.caches):
+        raw = raw.view(torch.uint8) if kv_type == "e4m3" else raw
+        nan = (raw[..., :1] == 0x7F) if kv_type == "e4m3" else torch.isnan(raw[..., :1])
+        one = 0x38 if kv_type == "e4m3" else 1.0
+        raw.zero_()
+        if i == 0:
+            raw[:, :, 1:, 0] = one
+        else:
+            raw.fill_(one)
+        raw.masked_fill_(nan, 0x7F if kv_type == "e4m3" else float("nan"))
+    c.q.zero_()
+    c.q[:, :, 0] = -1
+    c.scale = float(-x * np.log(2))
+    return c
+
+
+@pytest.mark.parametrize("q_type,kv_type", [("bf16", "bf16"), ("f16", "f16"), ("f16", "e4m3")])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_and_their_sum_agree(q_type, kv_type, d):
+    """Rounded weights are summed as they are multiplied: the mean of equal values is that value, to the bit.  (Summed
+    before they are rounded, it is off by 0.83 of a half step of the weights: 1 becomes the number below it.)"""
+    for lens, window in (([160, 2000, 48], None), ([1600], 1024), ([512] * 200, 256)):
+        c = _agreeing(q_type, kv_type, d, lens, [1] * len(lens), 8, 2, window)
+        assert (decode(c) == 1).all(), (lens, window)
+    if d == 64 or kv_type == "e4m3":
+        lens, new = many(2, [160, 64, 320], [1, 1, 1])
+        c = _agreeing(q_type, kv_type, d, lens, new, 8, 2, None)
+        assert (chunk(c) == 1).all()
+    assert binding.pkv_get_device_status() == 0
