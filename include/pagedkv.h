@@ -358,7 +358,8 @@ PKV_API pkv_status pkv_paged_tree_attention(
  * Supported: head_dim in {64, 128}; block_size in {8, 16, 32}; up to 128 query heads a kv head;
  * max_context_len up to 2^30; pools of fewer than 2^31 rows (num_blocks * num_kv_heads *
  * block_size); others return PKV_ERR_UNSUPPORTED.
- * Rounding: logits, maxima, sums, accumulators and partial states are fp32.  Operands are the
+ * Rounding: logits, maxima, sums, accumulators and partial states are fp32; logits (scale q.k) stay
+ * below 2^26 in magnitude (rows with larger ones may come out as zeros or NaN).  Operands are the
  * cache's 16-bit type; over FP8 and 4 bits they are f16, which the cached values are exactly, and
  * bf16 queries are scaled into f16 by a power of two per row (a value keeps its bits down to 2^-29
  * of the row's largest).  Softmax weights enter the product with V in the operands' type (f16:

@@ -105,3 +105,57 @@ def test_weights_and_their_sum_agree(q_type, kv_type, d):
         c = _agreeing(q_type, kv_type, d, lens, new, 8, 2, None)
         assert (chunk(c) == 1).all()
     assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("q_type,kv_type", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3"), ("f16", "fp4"),
+                                            ("f32", "f32"), ("f32", "e4m3")])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_equal_logits_of_any_size_give_the_mean(q_type, kv_type, sign):
+    """Keys that are all one vector: the weights are equal, whatever their logits are, up to the type's ends (chunks:
+    up to 2^26, which is what the call allows)."""
+    rng = np.random.default_rng(5)
+    d = 64
+    for log_size in (8, 20, 22, 27, 40, 120):
+        # products of up to 2^log_size, 64 of them, times 1/8: from the largest queries and keys that give them
+        top = {"bf16": 2.0 ** 60, "f16": 2.0 ** 15, "f32": 2.0 ** 60}[q_type]
+        key = {"e4m3": 448.0, "fp4": 6.0}.get(kv_type, min(top, 2.0 ** (log_size // 2)))
+        for call, c in everywhere(rng, 4, 2, d, 16, q_type, kv_type, 70, 3):
+            if call is chunk and (q_type == "f32" or log_size > 22):
+                continue
+            raw = c.caches[0]
+            if kv_type == "fp4":
+                flat = raw.view(raw.shape[0], raw.shape[1], -1)
+                flat[..., :16 * d // 2] = 0x77                                       # 6 and 6
+                scales = flat[..., 16 * d // 2:]
+                scales.masked_fill_(scales != 0x7F, 0x38)                            # 1
+            elif kv_type == "e4m3":
+                raw.view(torch.uint8).masked_fill_(raw.view(torch.uint8) != 0x7F, 0x7E)   # 448
+            else:
+                raw.masked_fill_(~torch.isnan(raw), key)
+            c.q.fill_(sign * min(top, 2.0 ** log_size / key))
+            out = call(c).double().cpu().numpy()
+            for s, (n, m) in enumerate(zip(c.lens, c.new)):
+                _, v, t = c.rows(s)
+                for i in range(0, m, 7):
+                    p = n - m + i
+                    see = (t <= p) & ((t > p - 70) | (t < 3))
+                    ref = np.repeat(v[:, see].mean(1), 2, 0)
+                    step = 2.0 ** -22 if q_type == "f32" else HALF["bf16" if kv_type == "bf16" else "f16"]
+                    # equal weights, rounded alike, under a sum that may be of them as they were before; sums of
+                    # 73 values; one rounding
+                    tol = (step + 80 * 2.0 ** -24) * np.repeat(np.abs(v[:, see]).max(1), 2, 0) + HALF[q_type] * np.abs(ref) + 1e-30
+                    got = out[c.start[s] + i]
+                    assert (np.abs(got - ref) <= tol).all(), (call.__name__, log_size, s, i, got[0, :3], ref[0, :3])
+    assert binding.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("kv_type", ["e4m3", "fp4"])
+def test_rows_of_one_call_from_2_to_the_minus_30_to_30(kv_type):
+    """bf16 rows beside each other, each scaled by a power of two of its own; the largest have logits of unit spread."""
+    rng = np.random.default_rng(6)
+    for call, c in everywhere(rng, 4, 2, 128, 16, "bf16", kv_type, 60, 3, kv_scale=2.0 ** -5):
+        mul = torch.from_numpy(2.0 ** rng.integers(-30, 31, (len(c.q), 4, 1)).astype(np.float64)).cuda()
+        c.q = (c.q.double() * mul).to(torch.bfloat16)
+        c.scale = 2.0 ** -33
+        c.check(call(c))
+    assert binding.pkv_get_device_status() == 0
