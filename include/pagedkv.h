@@ -364,10 +364,10 @@ PKV_API pkv_status pkv_paged_tree_attention(
  * bf16 queries are scaled into f16 by a power of two per row (a value keeps its bits down to 2^-29
  * of the row's largest).  Softmax weights enter the product with V in the operands' type (f16:
  * 2^-32 of the largest is what is lost), the denominator sums them unrounded (sequences of few rows, below: as rounded).
- * Up to four launches: many sequences with up to 24 rows of a kv head (tokens times its query heads)
- * on average have these taken by a kernel of their own; then a planner (few sequences are planned by
- * the attention itself), the attention, and the joining of what was split over several SMs (few or
- * long items).  Results are the same bits on every call.
+ * Up to four launches: a planner (few sequences are planned by the attention itself); where many
+ * sequences have up to 24 rows of a kv head (tokens times its query heads) on average, a kernel of
+ * their own for these (but for contexts that are much longer than the rest); the attention; and the
+ * joining of what was split over several SMs (few or long items).  Results are the same bits on every call.
  */
 PKV_API size_t pkv_chunk_workspace_bytes(int num_seqs, int total_q, int num_q_heads,
                                          int num_kv_heads, int head_dim, int max_context_len);

@@ -481,10 +481,19 @@ pkv_status pkv_paged_chunk_attention(
     // many sequences of few rows: those that have few go to a kernel of their own, in front of the others'
     const int64_t rows = (int64_t)total_q * p.group;
     const int64_t seen = (int64_t)p.window + p.sinks < max_context_len ? p.window + p.sinks : max_context_len;
-    if (chunk_few(kv_dtype, head_dim, rows, num_seqs, (int64_t)num_seqs * num_kv_heads, seen, dev->num_sms)) {
+    const bool few = chunk_few(kv_dtype, head_dim, rows, num_seqs, (int64_t)num_seqs * num_kv_heads, seen, dev->num_sms);
+    if (few) {
+        p.few_rows = kChunkFewRows;
+        // (three CTAs an SM of 64 dims, two of 128)
+        p.few_ctas = seen <= kChunkFewShort ? 0 : (head_dim == 64 ? 3 : 2) * dev->num_sms;
+    }
+    if (!p.self_plan) {
+        const cudaError_t e = launch_chunk_plan(p, s);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    if (few) {
         const cudaError_t e = bf16 ? chunk_few_bf16(p, head_dim, kv_dtype, s) : chunk_few_f16(p, head_dim, kv_dtype, s);
         if (e != cudaSuccess) return cuda_status(e);
-        p.few_rows = kChunkFewRows;
     }
     switch (kv_dtype) {
     case PKV_FP8_E4M3:

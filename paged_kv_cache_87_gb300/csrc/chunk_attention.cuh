@@ -22,6 +22,10 @@ constexpr int kChunkSelfSeqs = 32;
 // such sequences (chunk_few_kernel.cuh).
 constexpr int kChunkFewRows = 24;
 constexpr int kChunkFewShort = 1088;  // tokens that a row sees, up to which one unit an SM is enough for it
+// A context that is much longer than the others' share would end long after them, since that kernel does not cut it:
+// sequences that walk more than kChunkFewShares times a CTA's share of the few-rows sequences' tokens, and
+// kChunkFewAlone more, go to the tile kernel, which cuts them.
+constexpr int kChunkFewShares = 3, kChunkFewAlone = 2048;
 
 // A run of an item's steps, as the planner lists them: CTA c's first one is entry c, what else it
 // takes (`first`, or the counter) lies behind entry num_ctas - 1.
@@ -46,6 +50,8 @@ struct __align__(16) ChunkHead {
     int end;                          // end of the list (whole items: of those behind the first ones)
     int split;                        // a CTA's other pieces are `first`'s, not the counter's
     int next;                         // the counter
+    int few_most;                     // tokens that a sequence of few rows walks, at most, to be the other kernel's
+    int pad[3];
 };
 
 struct ChunkParams {
@@ -70,7 +76,8 @@ struct ChunkParams {
     int window, sinks;                // window >= max_context_len: none
     int max_pairs;                    // pairs of row tiles that the workspace has room for
     int num_ctas, part_rows;
-    int few_rows;                     // sequences with as many rows of a kv head are another kernel's
+    int few_rows;                     // sequences with as many rows of a kv head are another kernel's (0: none)
+    int few_ctas;                     // its resident CTAs, where some may be too long for it; else 0
     int self_plan;                    // no planner: every CTA finds its pieces
     int may_split;                    // an item can be cut, by the sizes
     float qk_scale_log2;              // scale * log2(e) * kv_scale
@@ -108,14 +115,33 @@ __host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end
     return w;
 }
 
+// What a sequence of n rows, the last of ctx tokens, walks, if it has few rows (else 0).
+__device__ __forceinline__ int few_tokens(const ChunkParams& p, int64_t n, int ctx) {
+    if (n <= 0 || n * p.group > p.few_rows) return 0;
+    return chunk_span(ctx - (int)n, ctx, p.window, p.sinks, p.log_block).kv_end;
+}
+
+// Tokens that such a sequence walks at most, by what all of them walk.
+__device__ __forceinline__ int few_most(const ChunkParams& p, int64_t tokens) {
+    if (p.few_ctas == 0) return INT32_MAX;
+    return (int)min((int64_t)INT32_MAX, tokens * p.num_kv_heads / p.few_ctas * kChunkFewShares + kChunkFewAlone);
+}
+
+// The sum of a warp's lanes.
+__device__ __forceinline__ int64_t few_sum(int64_t tokens) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, off);
+    return tokens;
+}
+
 // Defined in chunk_plan.cu.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
 
-// The kernel of few rows, in front of the others: FP8, 4 bits, 16 bits of 64 dims.
+// The kernel of few rows, between the planner and the attention: FP8, 4 bits, 16 bits of 64 dims.
 cudaError_t chunk_few_f16(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s);
 cudaError_t chunk_few_bf16(const ChunkParams& p, int head_dim, pkv_dtype kv, cudaStream_t s);
 
-// Planner, attention and joining kernel; each defined in the .cu file of its name.
+// Attention and joining kernel; each defined in the .cu file of its name.
 cudaError_t chunk_f16_16(const ChunkParams& p, int head_dim, cudaStream_t s);
 cudaError_t chunk_f16_fp8(const ChunkParams& p, int head_dim, cudaStream_t s);
 cudaError_t chunk_f16_fp4(const ChunkParams& p, int head_dim, cudaStream_t s);

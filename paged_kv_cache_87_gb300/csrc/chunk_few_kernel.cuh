@@ -9,7 +9,7 @@
 // launched behind, takes those and leaves these.
 //
 // Contexts are not cut, so there have to be enough of them for the longest to end among the others (chunk_few in
-// api.cu, with what was measured on either side).  Large ones (us, the chunk kernel alone | with this one), 5 tokens
+// api.cu, with what was measured on either side), and single long ones are left to the chunk kernel (few_most).  Large ones (us, the chunk kernel alone | with this one), 5 tokens
 // over 1,000 - 8,000, 32 / 8 heads, bf16 queries: FP8, d 128, 200 sequences 541 | 380, 100 275 | 228; 4 bits, d 128,
 // 588 | 355, 290 | 210; d 64, 200 sequences: FP8 453 | 208, 4 bits 453 | 226, 16 bits 412 | 254.  3 tokens under a window of 1,024 + 4, 256 sequences:
 // FP8 219 | 154, 16 bits of 64 dims 194 | 102.  16 bits of 128 dims, where the chunk kernel widens nothing,
@@ -65,6 +65,21 @@ __global__ void __launch_bounds__(kRowThreads, (TileCfg<QT, KT, HD, kFewSets>::C
     const int n = (int)n64;
     const int rows = n * p.group, first = ctx - n;
     const ChunkSpan span = chunk_span(first, ctx, p.window, p.sinks, logB);
+    if (p.few_ctas && span.kv_end > kChunkFewAlone) {          // too long for this kernel?
+        int most;
+        if (p.self_plan) {                                     // up to 32 sequences, one a lane
+            int walked = 0;
+            if (lane < p.num_seqs) {
+                const int a = p.query_start[lane], c = p.context_lens[lane];
+                const int64_t r = (int64_t)p.query_start[lane + 1] - a;
+                if (r >= 0 && a >= 0 && a + r <= p.total_q && c >= r && c <= cap) walked = few_tokens(p, r, c);
+            }
+            most = few_most(p, few_sum(walked));
+        } else {
+            most = p.head->few_most;
+        }
+        if (span.kv_end > most) return;
+    }
     if (threadIdx.x < 8 * N) {
         const int r = min((int)threadIdx.x, rows - 1), token = r / p.group;
         place[threadIdx.x] = (((int64_t)q0 + token) * p.num_q_heads + kvh * p.group + (r - token * p.group)) * HD;

@@ -234,7 +234,7 @@ struct ChunkSelf {
     __device__ __forceinline__ void init(const ChunkParams& p) {
         const int lane = threadIdx.x & 31, S = p.num_seqs;
         const int64_t cap = min((int64_t)p.max_context_len, (int64_t)p.max_blocks * p.block_size);
-        int pairs = 0;
+        int walked = 0;
         bool bad = false;
         q0 = n = ctx = 0;
         if (lane < S) {
@@ -243,14 +243,17 @@ struct ChunkSelf {
             ctx = p.context_lens[lane];
             const int64_t rows = (int64_t)q1 - q0;
             if (rows >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= rows && ctx <= cap) {
-                n = rows * p.group <= p.few_rows ? 0 : (int)rows;        // (few: another kernel's)
-                pairs = (n + p.item_tokens - 1) / p.item_tokens;
+                n = (int)rows;
+                walked = few_tokens(p, rows, ctx);
             } else {
                 bad = true;
             }
             bad |= (lane == 0 && q0 != 0) || (lane == S - 1 && q1 != p.total_q);
         }
-        incl = pairs;
+        // sequences of few rows are another kernel's, but for those that are too long for it
+        const int few = few_most(p, few_sum(walked));
+        if ((int64_t)n * p.group <= p.few_rows && walked <= few) n = 0;
+        incl = (n + p.item_tokens - 1) / p.item_tokens;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, off);
@@ -1190,10 +1193,6 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
         if (!made) return cudaErrorInvalidValue;
     }
     if (!encode_chunk_q_map(&tq, p.q, p.total_q, p.num_q_heads, p.group, p.qpt, HD)) return cudaErrorInvalidValue;
-    if (!p.self_plan) {
-        err = launch_chunk_plan(p, stream);
-        if (err != cudaSuccess) return err;
-    }
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;

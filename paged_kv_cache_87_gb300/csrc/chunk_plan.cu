@@ -58,21 +58,41 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     __shared__ Seq s_seq[kSeqs];
     __shared__ int s_prefix[kSeqs + 1];
     __shared__ int s_most;
-    __shared__ unsigned long long s_total;
+    __shared__ unsigned long long s_total, s_few;
     const int tid = threadIdx.x, S = p.num_seqs;
     const bool small = S <= kSeqs;
     if (tid == 0) {
         s_most = 0;
         s_total = 0;
+        s_few = 0;
     }
     pdl_wait();
     for (int c = tid; c < p.num_ctas; c += kThreads) p.cuts[c].last = -1;
     const int64_t cap = min((int64_t)p.max_context_len, (int64_t)p.max_blocks * p.block_size);
+    auto good = [&](int q0, int q1, int ctx) {
+        const int64_t n = (int64_t)q1 - q0;
+        return n >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= n && ctx <= cap;
+    };
+    int few = INT32_MAX;
+    if (p.few_ctas) {                       // which sequences of few rows are too long for their kernel
+        unsigned long long tokens = 0;
+        for (int s = tid; s < S; s += kThreads) {
+            const int q0 = p.query_start[s], q1 = p.query_start[s + 1], ctx = p.context_lens[s];
+            if (good(q0, q1, ctx)) tokens += few_tokens(p, (int64_t)q1 - q0, ctx);
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, off);
+        __syncthreads();
+        if ((tid & 31) == 0 && tokens) atomicAdd(&s_few, tokens);
+        __syncthreads();
+        few = few_most(p, (int64_t)s_few);
+    }
     // pairs of a sequence; one that breaks the contract, or is another kernel's, has none
     auto pairs_of = [&](int q0, int q1, int ctx) {
         const int64_t n = (int64_t)q1 - q0;
-        if (n >= 0 && q0 >= 0 && q1 <= p.total_q && ctx >= n && ctx <= cap)
-            return n * p.group <= p.few_rows ? 0 : (int)(((uint32_t)n + p.item_tokens - 1) / (uint32_t)(p.item_tokens));
+        if (good(q0, q1, ctx))
+            return n * p.group <= p.few_rows && few_tokens(p, n, ctx) <= few
+                       ? 0 : (int)(((uint32_t)n + p.item_tokens - 1) / (uint32_t)(p.item_tokens));
         set_status(p.status, PKV_DEV_BAD_CONTEXT);
         return 0;
     };
@@ -209,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     }
     for (int c = tid; c <= p.num_ctas; c += kThreads)        // where CTAs without work would begin
         if (c >= used) p.first[c] = p.num_ctas + extras;
-    if (tid == 0) *p.head = ChunkHead{used, split ? p.num_ctas + extras : nitems, split, p.num_ctas};
+    if (tid == 0) *p.head = ChunkHead{used, split ? p.num_ctas + extras : nitems, split, p.num_ctas, few, {0, 0, 0}};
 }
 
 }  // namespace
