@@ -207,7 +207,7 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  *   the other arguments, types and errors as in pkv_paged_decode_attention; where no
  *   workspace is needed, pools of 2^31 rows or more (16 bits, FP8) and batches of 2^28
  *   (sequence, kv head, eight query heads) units return PKV_ERR_UNSUPPORTED.
- * Where no workspace is needed: one launch, a cluster of up to eight CTAs a unit; logits,
+ * Where no workspace is needed: one launch, a cluster of up to sixteen CTAs a unit; logits,
  * maxima, sums and states are fp32, the weights enter the product with V in the operands'
  * type (f16 over FP8 and 4 bits: taken 2^7 above the running maximum, 2^-32 of the largest
  * is what is lost) and the denominator sums them as rounded; over FP8 and 4 bits bf16 queries

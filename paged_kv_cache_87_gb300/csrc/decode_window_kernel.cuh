@@ -3,7 +3,7 @@
 // sinks' blocks, then the window's).
 //
 // A window bounds every unit (sequence, kv head, eight query heads), so there is nothing to plan: a
-// cluster of 1, 2, 4 or 8 CTAs takes a unit, an equal run of its 64-token tiles each, and joins its
+// cluster of 1, 2, 4, 8 or 16 CTAs takes a unit, an equal run of its 64-token tiles each, and joins its
 // states through distributed shared memory.  A CTA is a producer warp, which fills a ring of tiles
 // (TMA boxes through the block table, 128-byte swizzle; 4 bits: bulk copies, unswizzled, as
 // decode_fp4_kernel.cuh takes them), and four consumer warps, 16 tokens of every tile each (five warps
@@ -133,11 +133,17 @@ __global__ void __launch_bounds__(kRowThreads, (TileCfg<QT, KT, HD, 1>::CTAS)) d
 // stages, 27.4 in two; FP8, 512 units of 4,096 94 in fours of four stages (three CTAs an SM), 85 alone of three
 // (four an SM), 320 units of 1,024 15.0 and 18.6 alone of four and of three.
 constexpr int kWinStart = 3;
+// Sixteen CTAs a cluster are more than every device has to offer (and are asked for): units of 64 tiles or more take
+// them where all units' clusters are resident at once, which is fewer than their CTAs would be, since a cluster
+// lies within a GPC.  One sequence, 8 / 1 heads, bf16, in eights and sixteens: 1,024 tokens 4.8 and 4.9 us, 2,048 6.3
+// and 5.7 (16 units, FP8, 7.5 and 8.8), 4,096 9.0 and 7.1 (10.3 and 10.3), 131,072 177 and 92 (64 / 8 heads 185 and
+// 97; the plain decode of as many 138); where they take a second round, 16 units of 131,072, 185 and 188.
+constexpr int kWinWide = 64;
 
 template <typename QT, typename KT, int HD>
 cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     using C = TileCfg<QT, KT, HD, 1>;
-    static int resident[2][64] = {{0}};                  // with all stages, with the fewest
+    static int resident[2][64] = {{0}}, wide[2][64] = {{0}};     // with all stages, with the fewest: CTAs; clusters of 16
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -145,6 +151,8 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     auto kernel = decode_window_kernel<QT, KT, HD>;
     if (resident[1][dev] == 0) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::NSTAGE));
+        if (err != cudaSuccess) return err;
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);     // sixteen
         if (err != cudaSuccess) return err;
         int sms = 0;
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -154,6 +162,20 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
             err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kRowThreads,
                                                                 C::smem(i ? C::FEWEST : C::NSTAGE));
             if (err != cudaSuccess) return err;
+            cudaLaunchAttribute of16[1];
+            of16[0].id = cudaLaunchAttributeClusterDimension;
+            of16[0].val.clusterDim.x = 16;
+            of16[0].val.clusterDim.y = of16[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t at = {};
+            at.gridDim = dim3(16, 1, 1);
+            at.blockDim = dim3(kRowThreads, 1, 1);
+            at.dynamicSmemBytes = C::smem(i ? C::FEWEST : C::NSTAGE);
+            at.attrs = of16;
+            at.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&wide[i][dev], kernel, &at) != cudaSuccess) {
+                wide[i][dev] = 0;                        // (a device without them)
+                (void)cudaGetLastError();
+            }
             resident[i][dev] = (per_sm > 0 ? per_sm : 1) * sms;
         }
     }
@@ -167,7 +189,8 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     int log_cluster = 0, stages = C::NSTAGE;
     int64_t least = INT64_MAX;
     for (int i = 0; i <= (C::FEWEST < C::NSTAGE); ++i)
-        for (int k = 0; k <= 3 && (k == 0 || tiles >= 1 << k); ++k) {
+        for (int k = 0; k <= 4 && (k == 0 || tiles >= 1 << k); ++k) {
+            if (k == 4 && (tiles < kWinWide || units > wide[i][dev])) break;
             const int64_t rounds = ((units << k) + resident[i][dev] - 1) / resident[i][dev];
             const int64_t cost = rounds * (((tiles + (1 << k) - 1) >> k) + kWinStart * (k ? 2 : 1));
             if (cost < least) {

@@ -508,21 +508,30 @@ __device__ __forceinline__ void tile_finish(const TileLane<C, HD>& w, uint8_t* r
     constexpr int W = HD / 32;
     const int last = parts - 1;
     for (int k = rank + w.warp * parts; k < rows; k += kRowWarps * parts) {
-        float m8[8], l8[8], v[8][W], top = -INFINITY, sum = 0.f, acc[W] = {0.f};
+        float top = -INFINITY, sum = 0.f, acc[W] = {0.f};
+#pragma unroll 1
+        for (int r0 = 0; r0 < parts; r0 += 8) {
+            float m8[8], l8[8], v[8][W], high = top;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {                    // every load in flight at once
-            load_from(mine_ml + 2 * k, min(r, last), m8[r], l8[r]);
-            load_from(mine + k * HD + W * w.lane, min(r, last), v[r]);
-        }
+            for (int r = 0; r < 8; ++r) {                // eight states' loads in flight at once
+                load_from(mine_ml + 2 * k, min(r0 + r, last), m8[r], l8[r]);
+                load_from(mine + k * HD + W * w.lane, min(r0 + r, last), v[r]);
+            }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) top = fmaxf(top, m8[r]);
+            for (int r = 0; r < 8; ++r) high = fmaxf(high, m8[r]);
+            const float keep = top == -INFINITY ? 0.f : fast_exp2(top - high);
+            top = high;
+            sum *= keep;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if (r > last || (m8[r] == -INFINITY && l8[r] == 0.f)) continue;     // no tiles there
-            const float f = m8[r] == -INFINITY ? 0.f : fast_exp2(m8[r] - top);
-            sum = fmaf(l8[r], f, sum);
+            for (int i = 0; i < W; ++i) acc[i] *= keep;
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] = fmaf(v[r][i], f, acc[i]);
+            for (int r = 0; r < 8; ++r) {
+                if (r0 + r > last || (m8[r] == -INFINITY && l8[r] == 0.f)) continue;     // no tiles there
+                const float f = m8[r] == -INFINITY ? 0.f : fast_exp2(m8[r] - top);
+                sum = fmaf(l8[r], f, sum);
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc[i] = fmaf(v[r][i], f, acc[i]);
+            }
         }
         const float inv = sum != 0.f ? out_scale / sum : 0.f;
 #pragma unroll
