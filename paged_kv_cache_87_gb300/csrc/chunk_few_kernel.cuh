@@ -23,6 +23,8 @@
 // 92), or as its length asks, the rest of the cluster leaving (112; 155 against 69 where nothing is cut).
 #pragma once
 
+#include <atomic>
+
 #include "chunk_attention.cuh"
 #include "row_tiles.cuh"
 
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kRowThreads, (TileCfg<QT, KT, HD, kFewSets>::C
 template <typename QT, typename KT, int HD>
 cudaError_t launch_chunk_few(const ChunkParams& p, cudaStream_t stream) {
     using C = TileCfg<QT, KT, HD, kFewSets>;
-    static bool attr_set[64] = {};
+    static std::atomic<bool> attr_set[64];            // (several threads may be the first)
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;

@@ -34,6 +34,7 @@
 // cycles between items, 4,600 for an item's output.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "cache_row.cuh"
@@ -1172,7 +1173,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkParams p) {
 template <typename QT, typename KT, int HD, bool NARROW>
 cudaError_t launch_chunk_typed(const ChunkParams& p, cudaStream_t stream) {
     using C = ChunkCfg<QT, KT, HD, NARROW>;
-    static bool attr_set[64] = {};
+    static std::atomic<bool> attr_set[64];            // (several threads may be the first)
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;

@@ -17,6 +17,9 @@
 // cluster's meeting.
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "row_tiles.cuh"
 #include "window_span.cuh"
 
@@ -140,17 +143,22 @@ constexpr int kWinStart = 3;
 // 97; the plain decode of as many 138); where they take a second round, 16 units of 131,072, 185 and 188.
 constexpr int kWinWide = 64;
 
+// What a device holds at once, with all stages of the ring and with the fewest: CTAs, clusters of sixteen.
+struct WindowRoom {
+    int ctas[2], wide[2];
+};
+
+// Asked for once a device; several threads may be the first.
 template <typename QT, typename KT, int HD>
-cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
+cudaError_t window_room(int dev, WindowRoom* out) {
     using C = TileCfg<QT, KT, HD, 1>;
-    static int resident[2][64] = {{0}}, wide[2][64] = {{0}};     // with all stages, with the fewest: CTAs; clusters of 16
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = decode_window_kernel<QT, KT, HD>;
-    if (resident[1][dev] == 0) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::NSTAGE));
+    static std::mutex lock;
+    static std::atomic<bool> known[64];
+    static WindowRoom rooms[64];
+    if (!known[dev].load(std::memory_order_acquire)) {
+        const std::lock_guard<std::mutex> held(lock);
+        auto kernel = decode_window_kernel<QT, KT, HD>;
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::NSTAGE));
         if (err != cudaSuccess) return err;
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);     // sixteen
         if (err != cudaSuccess) return err;
@@ -172,13 +180,29 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
             at.dynamicSmemBytes = C::smem(i ? C::FEWEST : C::NSTAGE);
             at.attrs = of16;
             at.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&wide[i][dev], kernel, &at) != cudaSuccess) {
-                wide[i][dev] = 0;                        // (a device without them)
+            if (cudaOccupancyMaxActiveClusters(&rooms[dev].wide[i], kernel, &at) != cudaSuccess) {
+                rooms[dev].wide[i] = 0;                  // (a device without them)
                 (void)cudaGetLastError();
             }
-            resident[i][dev] = (per_sm > 0 ? per_sm : 1) * sms;
+            rooms[dev].ctas[i] = (per_sm > 0 ? per_sm : 1) * sms;
         }
+        known[dev].store(true, std::memory_order_release);
     }
+    *out = rooms[dev];
+    return cudaSuccess;
+}
+
+template <typename QT, typename KT, int HD>
+cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
+    using C = TileCfg<QT, KT, HD, 1>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    WindowRoom room;
+    err = window_room<QT, KT, HD>(dev, &room);
+    if (err != cudaSuccess) return err;
+    auto kernel = decode_window_kernel<QT, KT, HD>;
     CUtensorMap tk{}, tv{};
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
     if (!C::FP4 && (!encode_pool_map(&tk, p.k_cache, HD, C::ELEM_BYTES, rows, p.block_size) ||
@@ -190,8 +214,8 @@ cudaError_t launch_decode_window(const DecodeParams& p, cudaStream_t stream) {
     int64_t least = INT64_MAX;
     for (int i = 0; i <= (C::FEWEST < C::NSTAGE); ++i)
         for (int k = 0; k <= 4 && (k == 0 || tiles >= 1 << k); ++k) {
-            if (k == 4 && (tiles < kWinWide || units > wide[i][dev])) break;
-            const int64_t rounds = ((units << k) + resident[i][dev] - 1) / resident[i][dev];
+            if (k == 4 && (tiles < kWinWide || units > room.wide[i])) break;
+            const int64_t rounds = ((units << k) + room.ctas[i] - 1) / room.ctas[i];
             const int64_t cost = rounds * (((tiles + (1 << k) - 1) >> k) + kWinStart * (k ? 2 : 1));
             if (cost < least) {
                 least = cost;
