@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kRowThreads, (TileCfg<QT, KT, HD, kFewSets>::C
     }
     tile_finish<C, QT>(w, ring, nullptr, 0, 1, ok, rows, p.out_scale, p.out,
                        [&](int k) { return place[k]; }, m, l, o);
+    if (!ok) mbar_let_land(full, C::NSTAGE);
 }
 
 template <typename QT, typename KT, int HD>

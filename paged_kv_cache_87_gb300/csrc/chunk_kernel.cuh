@@ -24,7 +24,8 @@
 //
 // Rows of V that no row of the item sees (past the last token, before the window, behind the
 // sinks: stale, poisoned or never loaded) are zeroed in shared memory, since 0 * NaN would reach O;
-// rows of K may hold anything, their scores are masked.  Every wait is bounded (2 s).
+// rows of K may hold anything, their scores are masked.  Every wait is bounded (2 s), and a CTA in which one
+// ran out stays until its copies have landed.
 //
 // Measured (32 / 8 heads, d 128; us; of the products' time at 1,890 TFLOP/s): 2 x 1,024 over 15k - 31k, 4 bits 768
 // (0.68); 16 x 512 over 0 - 8k, FP8 197 (0.47); 4 prompts of 4k - 16k under 1,024 + 4, bf16 820 (0.53); 1 x 37 over
@@ -1105,6 +1106,16 @@ __global__ void __launch_bounds__((ChunkCfg<QT, KT, HD, NARROW>::THREADS), 1) ch
     }
     tc5::fence_before_sync();
     named_bar_sync(1, C::THREADS);
+    if (warp == 0 && *abort_flag) {
+        // somebody gave up: the CTA stays until its copies have landed (a barrier that none is on its way to takes
+        // the bound of a wait)
+        constexpr int RING = C::WIDE ? C::RAWS : C::STAGES, QS = C::SCALE_Q ? 1 : 2;
+        uint64_t* bar = lane < RING ? (C::WIDE ? b.raw_full : b.full) + lane
+                                    : (C::SCALE_Q ? b.q_raw : b.q_full) + lane - RING;
+        if (lane < RING + QS)
+#pragma unroll 1
+            for (uint32_t parity = 0; parity < 2; ++parity) (void)mbar_wait(bar, parity);
+    }
 }
 
 // Joins the items that lie in several CTAs' runs, here the one that CTA blockIdx.x began and left

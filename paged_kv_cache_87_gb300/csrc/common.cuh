@@ -103,6 +103,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// Where somebody gave up: a warp stays, and its CTA with it, until the copies that complete on n (up to 32) barriers
+// have landed, whatever phase they are in; a barrier that none is on its way to takes the bound of a wait.  (A
+// function of its own: what does not run should not lie among what does.)
+static __device__ __noinline__ void mbar_let_land(uint64_t* bars, int n) {
+    const int lane = threadIdx.x & 31;
+    if (lane < n)
+        for (uint32_t parity = 0; parity < 2; ++parity) (void)mbar_wait(bars + lane, parity);
+    __syncwarp();
+}
+
 // -------------------------------------------------------- bulk copies --
 
 // 1-D bulk copy global -> shared (this CTA), completing on `bar` with `bytes`

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kRowThreads, (TileCfg<QT, KT, HD, 1>::CTAS)) d
     }
     tile_finish<C, QT>(w, ring, mine, rank, 1 << log_cluster, a < end && ok, nh, p.out_scale, p.out,
                        [&](int k) { return (row0 + k) * HD; }, m, l, o);
+    if (!ok) mbar_let_land(full, stages);
 }
 
 // CTAs of a cluster (and stages of the ring), by what a launch costs in rounds of tiles: rounds of
