@@ -13,6 +13,8 @@ constexpr int kChunkMaxCtas = 160;    // persistent CTAs, at most (one an SM)
 constexpr int kChunkMinRun = 4;
 // What splitting costs, in steps of every CTA: two partial states written, the joining kernel.
 constexpr int kChunkSplitCost = 8;
+// What an item's end costs (its output, the next one's start: 6,000 - 8,000 cycles), in steps.
+constexpr int kChunkItemCost = 2;
 // Launches of few items plan for themselves, in every CTA's producer warp: a planner in front of them
 // costs 5 us (one token 12.9 us with it, 8.1 without; drafts over FP8 98 and 92).  Sequences are one a
 // lane.
@@ -113,6 +115,17 @@ __host__ __device__ __forceinline__ ChunkSpan chunk_span(int p_first, int kv_end
     w.kv_end = kv_end - w.skip;
     w.steps = (w.kv_end - 1) / kChunkTile + 1;
     return w;
+}
+
+// Whether items are cut into equal runs of q steps, a CTA each, or dealt whole: rounds of items of average length, or
+// the longest one, against a run, with as many items' ends as the shortest ones put into it.  (Runs are equal in
+// steps: over a prompt's first rows a run holds dozens of short items.  One prompt of 4,096 tokens, 32 / 8 heads, bf16:
+// 227 us in runs, 120 whole; 1 x 512 over 8,192 73 in runs, 117 whole.)
+__device__ __forceinline__ bool chunk_split(int64_t total, int items, int most, int least, int ctas, int64_t q) {
+    if (items == 0) return false;
+    const float rounds = (float)((items + ctas - 1) / ctas);
+    const float whole = fmaxf((float)most, rounds * ((float)total / (float)items + kChunkItemCost) - kChunkItemCost);
+    return whole > (float)q + kChunkSplitCost + (float)q / (float)least * kChunkItemCost;
 }
 
 // What a sequence of n rows, the last of ctx tokens, walks, if it has few rows (else 0).

@@ -268,21 +268,22 @@ struct ChunkSelf {
             all = 0;
         }
         if (bad && blockIdx.x == 0) set_status(p.status, PKV_DEV_BAD_CONTEXT);
-        int sum = 0, most = 0;
+        int sum = 0, most = 0, least = INT32_MAX;
         for (int g0 = 0; g0 < all; g0 += 32) {
             int seq, pair;
             const int st = steps_of(p, g0 + lane, seq, pair);
             sum += st;
             most = max(most, st);
+            if (st) least = min(least, st);
         }
         sum = __reduce_add_sync(0xffffffffu, sum);
         most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
         const int N = p.num_ctas;
         total = sum * p.num_kv_heads;
         items = all * p.num_kv_heads;
         q = max(kChunkMinRun, (total + N - 1) / N);
-        const int whole = items ? max(most, (items + N - 1) / N * total / items) : 0;
-        split = whole > q + kChunkSplitCost;
+        split = chunk_split(total, items, most, least, N, q);
         pos = split ? min((int)blockIdx.x * q, total) : (int)blockIdx.x;
         end = split ? min(pos + q, total) : items;
         g = base = 0;

@@ -6,7 +6,7 @@
 // equal runs, one a CTA, whatever item they belong to; an item that lies in several runs leaves a
 // partial state in each, and the joining kernel adds them up in order (no atomics: the same bits
 // on every call).  Splitting costs about kChunkSplitCost steps a CTA, whole items cost their last
-// round: the cheaper one is taken, by the exact counts.
+// round: the cheaper one is taken (chunk_split), by the exact counts.
 //
 // Its time is latency, in front of every call: lengths and starts are read once, and up to kSeqs
 // sequences everything after that is in shared memory.
@@ -57,12 +57,13 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
     __shared__ int s_ctx[kSeqs];
     __shared__ Seq s_seq[kSeqs];
     __shared__ int s_prefix[kSeqs + 1];
-    __shared__ int s_most;
+    __shared__ int s_most, s_least;
     __shared__ unsigned long long s_total, s_few;
     const int tid = threadIdx.x, S = p.num_seqs;
     const bool small = S <= kSeqs;
     if (tid == 0) {
         s_most = 0;
+        s_least = INT32_MAX;
         s_total = 0;
         s_few = 0;
     }
@@ -168,28 +169,29 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkParams p) {
         r.steps = chunk_span(before + a, before + b, p.window, p.sinks, p.log_block).steps;
         return r;
     };
-    // all steps, and the longest item's
+    // all steps, the longest item's and the shortest one's
     int64_t steps = 0;
-    int most = 0;
+    int most = 0, least = INT32_MAX;
     for (int g = tid; g < pairs; g += kThreads) {
         const int n = pair_at(g).steps;
         steps += n;
         most = max(most, n);
+        least = min(least, n);
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, off);
     most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
     if ((tid & 31) == 0 && most) {
         atomicAdd(&s_total, (unsigned long long)steps);
         atomicMax(&s_most, most);
+        atomicMin(&s_least, least);
     }
     __syncthreads();
     most = s_most;
     const int64_t total = (int64_t)s_total * p.num_kv_heads, items = (int64_t)pairs * p.num_kv_heads;
     const int64_t q64 = max((int64_t)kChunkMinRun, (total + p.num_ctas - 1) / p.num_ctas);
-    // rounds of items of average length, or the longest one
-    const int64_t whole = max((int64_t)most, (items + p.num_ctas - 1) / p.num_ctas * total / max(items, (int64_t)1));
-    const bool split = whole > q64 + kChunkSplitCost && total <= INT32_MAX - (1 << 20);
+    const bool split = chunk_split(total, (int)items, most, s_least, p.num_ctas, q64) && total <= INT32_MAX - (1 << 20);
     const uint32_t q = (uint32_t)q64;
     // the pieces, in the flattened order, an item a thread
     const int nitems = (int)items, used = split ? (int)((total + q - 1) / q) : min(nitems, p.num_ctas);
