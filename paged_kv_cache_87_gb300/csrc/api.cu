@@ -144,10 +144,12 @@ bool window_kernel(pkv_dtype q, pkv_dtype kv, int max_seen) {
 
 // Whether a call of the chunk attention has sequences of few rows on average, and as many (sequence, kv head)
 // units as the kernel of few rows needs to be the sooner one, by the tokens that a row sees at most: it does not
-// cut contexts.  Measured (us, chunk kernel | few rows; 3 tokens, 32 / 8 heads, bf16 queries, 152 SMs): rows of
-// 1,028 tokens at most, 160 units: FP8 34.6 | 27.0, 4 bits 36.0 | 25.8, 16 bits of 64 dims 30.9 | 19.1; of 100 -
-// 1,000: 24.3 | 24.4, 24.9 | 22.9, 21.2 | 16.9; 64 units of 1,000, FP8: 17.8 | 25.7.  Of 1,000 - 8,000, 64 dims,
-// 160 units: 49.6 | 77.3, 256 80.8 | 76.7, 456 134 | 95; 128 dims: FP8 456 units 147 | 163, 800 275 | 228.
+// cut contexts.  Measured (us, chunk kernel | few rows; 3 tokens, 32 / 8 heads, bf16 queries, 152 SMs; contexts of one
+// length, FP8 and 16 bits of 64 dims): 160 units of 1,000 33.0 | 27.3, 29.5 | 19.6; of 1,152 36.0 | 29.1, 31.8 | 20.9; of
+// 1,536 38.0 | 35.0, 29.3 | 24.4; of 2,048 43.6 | 42.1 (4 bits 44.1 | 41.1), 34.3 | 29.2; of 500 - 2,000 38.9 | 37.7,
+// 27.5 | 25.4; of 1,000 - 4,000 54.5 | 62.3, 40.8 | 42.2, 240 units of these 85.5 | 67.8, 84.1 | 47.6; 64 units of 1,000,
+// FP8: 17.8 | 25.7.  Of 1,000 - 8,000, 64 dims, 160 units: 49.6 | 77.3, 256 80.8 | 76.7, 456 134 | 95; 128 dims: FP8 456
+// units 147 | 163, 800 275 | 228.
 bool chunk_few(pkv_dtype kv, int head_dim, int64_t rows, int num_seqs, int64_t units, int64_t seen, int num_sms) {
     const bool has = quantised(kv) || head_dim == 64;
     const int64_t least = seen <= kChunkFewShort ? num_sms : head_dim == 64 ? num_sms * 3 / 2 : num_sms * 5;

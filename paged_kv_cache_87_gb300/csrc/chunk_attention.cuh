@@ -23,7 +23,7 @@ constexpr int kChunkSelfSeqs = 32;
 // (token, head) rows of a sequence and kv head, up to which it goes to the kernel of few rows where a call has
 // such sequences (chunk_few_kernel.cuh).
 constexpr int kChunkFewRows = 24;
-constexpr int kChunkFewShort = 1088;  // tokens that a row sees, up to which one unit an SM is enough for it
+constexpr int kChunkFewShort = 2048;  // tokens that a row sees, up to which one unit an SM is enough for it
 // A context that is much longer than the others' share would end long after them, since that kernel does not cut it:
 // sequences that walk more than kChunkFewShares times a CTA's share of the few-rows sequences' tokens, and
 // kChunkFewAlone more, go to the tile kernel, which cuts them.
