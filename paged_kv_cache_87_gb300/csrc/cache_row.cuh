@@ -67,6 +67,20 @@ __device__ __forceinline__ uint32_t e4m3x2_of(uint32_t w) {
     return r;
 }
 
+// Element-wise product of two f16x2.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The low (k = 0) or high half of an f16x2 in both halves (an operand modifier, not an operation).
+__device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 t = k ? __high2half2(h) : __low2half2(h);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
 // Eight fp32 values -> e2m1 codes (round to nearest even, saturate to +-6), the first in the
 // lowest nibble.
 __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&q)[8]) {

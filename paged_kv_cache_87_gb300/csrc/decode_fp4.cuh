@@ -75,9 +75,11 @@ cudaError_t decode_fp4_bf16(const DecodeFp4Params& p, cudaStream_t s);
 
 // The same under a sliding window (decode_fp4_window_*.cu): fp32 queries, and wide windows.  16-bit
 // queries over virtual contexts of up to kFp4WindowMost tokens take decode_window_kernel.cuh.  Measured
-// (us, that kernel against this one), 32 / 8 heads, d 128: one sequence under a window of 1,024 5.3
-// against 8.2, 16 of them 10.1 against 13.3, 256 70.8 against 79.7; 8 under 32,000 (64 / 8 heads) 72.7
-// against 62.7, 64 under 4,096 (128 / 8) 125 against 102.
+// (us, that kernel | this one), 32 / 8 heads, d 128: under a window of 1,024, 1, 16, 64 and 256 sequences 5.8 | 8.1,
+// 10.3 | 13.4, 22.1 | 27.1, 70.8 | 82.5; of 2,000 6.3 | 8.2, 14.3 | 16.7, 38.9 | 38.8, 126 | 124; of 2,500 6.9 | 8.9,
+// 16.5 | 18.3, 47.5 | 44.3, 155 | 147; of 8,192 10.6 | 12.5, 40.8 | 36.6, 148 | 118, 474 | 430.  Of 64 dims the two meet
+// earlier where there are many: 1,024 5.7 | 7.3, 12.0 | 9.8, 18.0 | 19.9, 51.8 | 48.2; 2,000 6.2 | 7.5, 14.6 | 11.7,
+// 28.9 | 27.1, 93.0 | 76.2.
 constexpr int kFp4WindowMost = 2048;
 cudaError_t decode_fp4_window_f32(const DecodeFp4Params& p, cudaStream_t s);
 cudaError_t decode_fp4_window_f16(const DecodeFp4Params& p, cudaStream_t s);

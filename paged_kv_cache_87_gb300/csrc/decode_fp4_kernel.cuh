@@ -101,22 +101,9 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The low (k = 0) or high half of an f16x2 in both halves (an operand modifier, not an operation).
-__device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
-    const __half2 h = *reinterpret_cast<const __half2*>(&x);
-    const __half2 t = k ? __high2half2(h) : __low2half2(h);
-    return *reinterpret_cast<const uint32_t*>(&t);
 }
 
 // What is left of (lo, hi) after pack_f16's rounding, as fp16 again.

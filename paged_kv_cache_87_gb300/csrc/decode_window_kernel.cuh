@@ -5,15 +5,15 @@
 // A window bounds every unit (sequence, kv head, eight query heads), so there is nothing to plan: a
 // cluster of 1, 2, 4, 8 or 16 CTAs takes a unit, an equal run of its 64-token tiles each, and joins its
 // states through distributed shared memory.  A CTA is a producer warp, which fills a ring of tiles
-// (TMA boxes through the block table, 128-byte swizzle; 4 bits: bulk copies, unswizzled, as
-// decode_fp4_kernel.cuh takes them), and four consumer warps, 16 tokens of every tile each (five warps
+// (TMA boxes through the block table, under the swizzle of a row's slices: 128 bytes, FP8 of 64 dims 64; 4 bits:
+// bulk copies, unswizzled, as decode_fp4_kernel.cuh takes them), and four consumer warps, 16 tokens of every tile each (five warps
 // spread over all four sub-partitions).  The products are row_tiles.cuh's.  Tokens that are hidden or past
 // the context are masked in S and their rows of V zeroed in shared memory, by the warp that multiplies them.
 //
 // Measured (us; of the bytes' time at 6,792 GB/s): 256 sequences of 64 - 32k, 32 / 8 heads, d 128, bf16 under
 // 1,024 + 4: 115 (1.0); 64 of 4k - 131k, 64 / 8, FP8 under 4,096 + 16: 85 (0.94), of 64 dims under 4,096: 45 (0.89),
-// all bound by HBM; over 4 bits 256 under 1,024: 74 (0.6), bound by the widening's instructions (2.65 of 4 a
-// clock); one sequence under 1,024: 5.3 (0.11), bound by the latency of length, table, first tile and the
+// all bound by HBM; over 4 bits 256 under 1,024: 71 (0.64), nothing full (2.65 of 4 instructions a clock, DRAM 53 %):
+// chains of dependent widening, products and softmax in four warps a CTA; one sequence under 1,024: 5.3 (0.11), bound by the latency of length, table, first tile and the
 // cluster's meeting.
 #pragma once
 

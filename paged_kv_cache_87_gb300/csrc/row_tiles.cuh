@@ -15,19 +15,6 @@
 namespace pkv {
 namespace {
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// The low (k = 0) or high half of an f16x2 in both halves (an operand modifier, not an operation).
-__device__ __forceinline__ uint32_t half_twice(uint32_t x, int k) {
-    const __half2 h = *reinterpret_cast<const __half2*>(&x);
-    const __half2 t = k ? __high2half2(h) : __low2half2(h);
-    return *reinterpret_cast<const uint32_t*>(&t);
-}
-
 constexpr int kRowTile = 64;                  // tokens of a stage
 constexpr int kRowWarps = 4;                  // consumers
 constexpr int kRowThreads = 32 * (kRowWarps + 1);
