@@ -194,8 +194,9 @@ PKV_API pkv_status pkv_paged_decode_attention(const void* query, const void* k_c
  * t >= low and to t < num_sinks:
  *     out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) * v_t  over those t.
  * Table entries of blocks that hold no such token are never read: a caller gives
- * those blocks back and leaves what it likes in the table.  Cache rows that are
- * not seen may hold anything (NaN), as may those past the context.
+ * those blocks back and leaves what it likes in the table (in a list of its own: pkv_bm_* frees
+ * whole sequences).  Cache rows that are not seen may hold anything (NaN), as may those past the
+ * context; a NaN in a key or a value that is seen reaches the outputs of its kv head.
  *
  *   window     tokens, the query's own among them; at least 1 (INT_MAX: all)
  *   num_sinks  tokens, at least 0
@@ -337,8 +338,10 @@ PKV_API pkv_status pkv_paged_tree_attention(
  * its context_lens[s] cached tokens.  Row i of them is the token at position p = context_lens[s]
  * - n_s + i, and for each query head h
  *   out[row][h] = sum_t softmax_t(scale * q[row][h] . k_t) v_t
- * over the tokens t <= p with t > p - window or t < num_sinks.  Table entries of blocks that none
- * of a sequence's rows sees are never read, and cache rows that none sees may hold anything.  A NaN
+ * over the tokens t <= p with t > p - window or t < num_sinks.  (Causal rows over 16 bits and head_dim
+ * 128 are pkv_paged_multi_query_attention's too, where the group divides 128: 2 to 9 % sooner where
+ * every sequence has hundreds of rows; it does not cut contexts, which is what few rows over long ones
+ * need.)  Table entries of blocks that none of a sequence's rows sees are never read, and cache rows that none sees may hold anything.  A NaN
  * or an infinity in a value that some of them see may reach the sequence's other rows.
  *
  *   query        [total_q][num_q_heads][head_dim], q_dtype, 16-byte aligned

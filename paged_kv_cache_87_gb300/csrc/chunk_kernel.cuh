@@ -27,8 +27,8 @@
 // rows of K may hold anything, their scores are masked.  Every wait is bounded (2 s), and a CTA in which one
 // ran out stays until its copies have landed.
 //
-// Measured (32 / 8 heads, d 128; us; of the products' time at 1,890 TFLOP/s): 2 x 1,024 over 15k - 31k, 4 bits 768
-// (0.68); 16 x 512 over 0 - 8k, FP8 197 (0.47); 4 prompts of 4k - 16k under 1,024 + 4, bf16 820 (0.53); 1 x 37 over
+// Measured (32 / 8 heads, d 128; us; of the products' time at 1,890 TFLOP/s): 2 x 1,024 over 15k - 31k, 4 bits 775
+// (0.67); 16 x 512 over 0 - 8k, FP8 196 (0.48); 4 prompts of 4k - 16k under 1,024 + 4, bf16 823 (0.53); 1 x 37 over
 // 30k, 4 bits 48 (0.20); 32 x 5 over 1k - 8k, FP8 92 (0.36 of the bytes' time).  The tile step bounds it: 3,260 cycles
 // in 16 bits, 3,300 - 4,000 widened, of which the four runs of products take 2,048; Q and K both come from shared
 // memory, whose 128 bytes a clock the products and the widening share.  Short items add their ends: 1,500 - 3,600
