@@ -338,11 +338,12 @@ PKV_API pkv_status pkv_paged_tree_attention(
  * its context_lens[s] cached tokens.  Row i of them is the token at position p = context_lens[s]
  * - n_s + i, and for each query head h
  *   out[row][h] = sum_t softmax_t(scale * q[row][h] . k_t) v_t
- * over the tokens t <= p with t > p - window or t < num_sinks.  (Causal rows over 16 bits and head_dim
- * 128 are pkv_paged_multi_query_attention's too, where the group divides 128: 2 to 9 % sooner where
- * every sequence has hundreds of rows; it does not cut contexts, which is what few rows over long ones
- * need.)  Table entries of blocks that none of a sequence's rows sees are never read, and cache rows that none sees may hold anything.  A NaN
+ * over the tokens t <= p with t > p - window or t < num_sinks.  Table entries of blocks that none
+ * of a sequence's rows sees are never read, and cache rows that none sees may hold anything.  A NaN
  * or an infinity in a value that some of them see may reach the sequence's other rows.
+ * (Causal rows over 16 bits and head_dim 128 are pkv_paged_multi_query_attention's too, where the
+ * group divides 128: 2 to 9 % sooner where every sequence has hundreds of rows; it does not cut
+ * contexts, which is what few rows over long ones need.)
  *
  *   query        [total_q][num_q_heads][head_dim], q_dtype, 16-byte aligned
  *   query_start  int32 [num_seqs + 1], query_start[0] = 0, non-decreasing,

@@ -47,3 +47,39 @@ print("all right")
 def test_first_calls_from_many_threads():
     r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "all right" in r.stdout, r.stdout + r.stderr
+
+
+CAPTURED = """
+import numpy as np
+import torch
+from paged_kv_cache_87_gb300 import binding
+from tests.test_gpu_chunk import chunk
+from tests.test_gpu_window import decode
+from tests.window_cases import Paged
+
+rng = np.random.default_rng(2)
+cases = [(decode, Paged(rng, [300, 5000], [1, 1], 8, 2, 128, 16, "bf16", "bf16", 4500, 2)),
+         (chunk, Paged(rng, [300, 2000], [40, 3], 8, 2, 128, 16, "bf16", "e4m3", 500, 2)),
+         (chunk, Paged(rng, [40] * 400, [2] * 400, 8, 2, 64, 16, "f16", "fp4", 30, 2))]
+binding.load()
+side = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=side):
+    outs = [call(c) for call, c in cases]
+for _ in range(2):
+    for out in outs:
+        out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    for (_, c), out in zip(cases, outs):
+        c.check(out)
+assert binding.pkv_get_device_status() == 0
+print("all right")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    r = subprocess.run([sys.executable, "-c", CAPTURED], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "all right" in r.stdout, r.stdout + r.stderr
